@@ -12,6 +12,20 @@
  *                        SiLU-and-mul + FP8 requant, w2 down GEMM.
  *   moe_topk_reduce      top-k weighted sum back to token order.
  *
+ * Around them stand the other operators of an MoE block, for serving and for
+ * training, in bf16, fp16 and fp32:
+ *
+ *   moe_route            router logits -> top-k ids and weights (and the
+ *                        gradient of the logits).
+ *   moe_sort_routes, moe_permute, moe_unpermute
+ *                        rows sorted by expert and back with the routing
+ *                        weights applied (and their gradients).
+ *   moe_block_norm       the RMS norm after a block with its gate, residual
+ *                        scale and residual sum, and the norm before the next
+ *                        block, in one pass (and its gradient).
+ *   moe_lora_linear      a projection shared by all tokens plus each token's
+ *                        own low-rank adapter.
+ *
  * Conventions shared by every call
  *   - All tensor pointers are DEVICE pointers unless stated otherwise; every
  *     output buffer is allocated by the caller; the library never allocates
@@ -52,6 +66,7 @@ typedef enum moe_status {
 #define MOE_DEV_CAPACITY 1u   /* an expert got more than max_tokens_per_expert routes */
 #define MOE_DEV_BAD_EXPERT 2u /* routed id >= num_experts / num_logical, or bad EPLB entry */
 #define MOE_DEV_TIMEOUT 4u    /* a bounded pipeline wait inside a GEMM expired */
+#define MOE_DEV_BAD_ADAPTER 8u /* an adapter id >= num_adapters (taken as no adapter) */
 
 typedef enum moe_sf_mode {
   MOE_SF_NONE = 0,         /* no quantisation: x receives a bf16 copy of hidden */
@@ -63,6 +78,14 @@ typedef enum moe_ids_dtype { MOE_IDS_INT32 = 0, MOE_IDS_INT64 = 1 } moe_ids_dtyp
 typedef enum moe_weights_dtype { MOE_WEIGHTS_FP32 = 0, MOE_WEIGHTS_BF16 = 1 } moe_weights_dtype_t;
 typedef enum moe_activation { MOE_ACT_SILU = 0 } moe_activation_t;
 typedef enum moe_shared_dtype { MOE_SHARED_BF16 = 0, MOE_SHARED_FP8 = 1 } moe_shared_dtype_t;
+typedef enum moe_dtype { MOE_DTYPE_FP32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_FP16 = 2 } moe_dtype_t;
+typedef enum moe_scoring { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_scoring_t;
+typedef enum moe_gate {
+  MOE_GATE_NONE = 0,
+  MOE_GATE_CHANNEL = 1, /* [K]: one factor per column */
+  MOE_GATE_TOKEN = 2,   /* [T]: one factor per token */
+  MOE_GATE_FULL = 3     /* [T, K] */
+} moe_gate_t;
 
 /* Stage mask of moe_batched_experts. */
 #define MOE_STAGE_W13 1
@@ -400,6 +423,252 @@ moe_status_t moe_topk_reduce(const void* expert_out, int64_t num_experts,
                              const int64_t* topk_idx, const int32_t* route_slot,
                              const float* topk_weights, int64_t num_tokens, int64_t top_k,
                              const int32_t* num_valid_tokens, void* out, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* moe_route                                                                 */
+/*                                                                           */
+/* Top-k ids and weights of router logits l[t, e], in fp32.                  */
+/*   key[t, e] = l                     without a bias (both scorings are      */
+/*                                     monotone in the logit);                */
+/*               l + bias[e]           softmax with a bias;                   */
+/*               1/(1+exp(-l)) + bias  sigmoid with a bias.                   */
+/* An expert whose key is NaN or -inf is not selectable (a masked expert).   */
+/* Groups (num_groups > 1; E % num_groups == 0): a group's value is its       */
+/* highest key, with a bias the sum of its two highest (a missing second     */
+/* counts 0); only experts of the top_groups best groups stay selectable.    */
+/* The k selectable experts of highest key are taken, in descending order;   */
+/* among equal keys (of experts or groups) the lowest index comes first.     */
+/*   softmax:  p_e = exp(l_e - m) / sum over all selectable-by-logit e'       */
+/*             (l not NaN) of exp(l_e' - m); renormalize: the sum over the    */
+/*             taken experts instead.                                        */
+/*   sigmoid:  p_e = 1/(1+exp(-l_e)); renormalize: divided by the taken       */
+/*             experts' sum + 1e-20.                                         */
+/*   topk_weights[t, j] = scale * p_(ids[t, j]).                              */
+/* Where fewer than k experts are selectable the rest of the row is id -1,   */
+/* weight 0; padding tokens (is_padding[t] != 0) are -1 and 0 throughout.    */
+/* topk_ids int32 or int64 [T, k], topk_weights fp32 [T, k], contiguous.     */
+/* Errors: k < 1, k > E, E % num_groups, top_groups outside [1, num_groups],  */
+/* k > top_groups * E / num_groups -> SHAPE; E > 1024, k > 32, num_groups >   */
+/* 32 -> UNSUPPORTED.                                                        */
+/*                                                                           */
+/* moe_route_backward: d_logits[t, :] (the type of logits, every value        */
+/* written) from d_weights fp32 [T, k] and the ids that moe_route gave: the   */
+/* gradient of the formulas above with the selection held fixed.  Entries    */
+/* with id < 0 (or >= E) contribute nothing.                                 */
+/* ------------------------------------------------------------------------ */
+typedef struct moe_route_args {
+  int64_t num_tokens, num_experts, top_k;
+  const void* logits; /* [T, E], inner stride 1 */
+  int32_t logits_dtype;
+  int64_t logits_stride0;
+  const float* bias;         /* nullable [E] */
+  const uint8_t* is_padding; /* nullable [T] */
+  int32_t scoring;           /* MOE_SCORE_* */
+  int32_t renormalize;
+  float scale;
+  int64_t num_groups, top_groups; /* 1, 1: no groups */
+  void* topk_ids;
+  int32_t topk_ids_dtype; /* MOE_IDS_* */
+  float* topk_weights;
+} moe_route_args_t;
+
+moe_status_t moe_route(const moe_route_args_t* args, void* stream);
+
+typedef struct moe_route_backward_args {
+  int64_t num_tokens, num_experts, top_k;
+  const void* logits;
+  int32_t logits_dtype;
+  int64_t logits_stride0;
+  int32_t scoring;
+  int32_t renormalize;
+  float scale;
+  const void* topk_ids; /* [T, k] contiguous, as moe_route wrote them */
+  int32_t topk_ids_dtype;
+  const float* d_weights; /* [T, k] contiguous */
+  void* d_logits;         /* [T, E], the type of logits */
+  int64_t d_logits_stride0;
+} moe_route_backward_args_t;
+
+moe_status_t moe_route_backward(const moe_route_backward_args_t* args, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* moe_sort_routes, moe_permute, moe_unpermute                               */
+/*                                                                           */
+/* Route (t, j) with id e = topk_ids[t, j] in [0, E) has row                  */
+/*   route_row[t, j] = #routes to experts < e + #earlier routes (t', j') to e, */
+/* earlier in (token, k) order; any other id gives -1 (an id >= E also sets   */
+/* MOE_DEV_BAD_EXPERT).  expert_offsets[e] = #routes to experts < e, e <= E;  */
+/* row_route[r] = t * k + j of row r, -1 for r >= expert_offsets[E].          */
+/* topk_ids int32 or int64 [T, k]; expert_offsets int32 [E + 1]; route_row    */
+/* and row_route int32 [T * k].  workspace: moe_sort_workspace_size() bytes,  */
+/* need not be cleared.  E > 1024 -> UNSUPPORTED.                             */
+/*                                                                           */
+/* With `rows` [num_rows, K] in the order of the experts:                     */
+/*   moe_permute             rows[route_row[t, j]] = x[t]; rows from           */
+/*                           expert_offsets[E] on are written as zeros;        */
+/*   moe_unpermute           out[t] = sum_j w[t, j] * rows[route_row[t, j]],    */
+/*                           in fp32 in ascending j, rounded once; with        */
+/*                           topk_weights = NULL every weight is 1, which is   */
+/*                           the gradient of moe_permute (d_rows -> d_x);      */
+/*   moe_unpermute_backward  d_rows[r(t, j)] = w[t, j] * d_out[t], rows from    */
+/*                           expert_offsets[E] on zeros;                       */
+/*                           d_weights[t, j] = <d_out[t], rows[r(t, j)]>, fp32. */
+/* Routes with route_row outside [0, num_rows) are left out (weight gradient  */
+/* 0); rows of `rows` that no route names are not read.  Tensors of one call  */
+/* have one dtype (MOE_DTYPE_*), inner stride 1 and a row stride of their own; */
+/* weights are fp32.  top_k > 32 -> UNSUPPORTED.                              */
+/* ------------------------------------------------------------------------ */
+size_t moe_sort_workspace_size(int64_t num_tokens, int64_t top_k, int64_t num_experts);
+
+moe_status_t moe_sort_routes(const void* topk_ids, int32_t topk_ids_dtype, int64_t num_tokens,
+                             int64_t top_k, int64_t num_experts, int32_t* expert_offsets,
+                             int32_t* route_row, int32_t* row_route, void* workspace,
+                             size_t workspace_bytes, uint32_t* device_status, void* stream);
+
+moe_status_t moe_permute(const void* x, int64_t x_stride0, int32_t dtype, int64_t num_tokens,
+                         int64_t hidden_size, int64_t top_k, const int32_t* route_row,
+                         const int32_t* expert_offsets, int64_t num_experts, void* rows,
+                         int64_t rows_stride0, int64_t num_rows, void* stream);
+
+moe_status_t moe_unpermute(const void* rows, int64_t rows_stride0, int64_t num_rows, int32_t dtype,
+                           const int32_t* route_row, const float* topk_weights,
+                           int64_t num_tokens, int64_t hidden_size, int64_t top_k, void* out,
+                           int64_t out_stride0, void* stream);
+
+moe_status_t moe_unpermute_backward(const void* d_out, int64_t d_out_stride0, const void* rows,
+                                    int64_t rows_stride0, int64_t num_rows, int32_t dtype,
+                                    const int32_t* route_row, const float* topk_weights,
+                                    const int32_t* expert_offsets, int64_t num_experts,
+                                    int64_t num_tokens, int64_t hidden_size, int64_t top_k,
+                                    void* d_rows, int64_t d_rows_stride0, float* d_weights,
+                                    void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* moe_block_norm                                                            */
+/*                                                                           */
+/* The seam between two blocks: the residual stream x, the output z of the    */
+/* block before and the input y of the block after.  In fp32, per token:      */
+/*   n = z * rstd_post * (post_weight + weight_offset),                       */
+/*       rstd_post = 1 / sqrt(mean(z^2) + eps)      (no post_weight: n = z)   */
+/*   x_out = x + scale * gate * n                   (no z: x_out is x)        */
+/*   y = x_out * rstd_pre * (pre_weight + weight_offset),                     */
+/*       rstd_pre = 1 / sqrt(mean(x_out^2) + eps)                             */
+/* x_out and y are rounded once each; y comes from the unrounded x_out.       */
+/* z NULL: no x_out, gate or post_weight; pre_weight NULL: no y or rstd_pre.  */
+/* x_out may be x itself (in place).  x, z, x_out, y and a full gate have     */
+/* one dtype, inner stride 1 and row strides of their own; weights and a      */
+/* channel gate are [K] of weight_dtype; a token gate is [T] of dtype.        */
+/* rstd_post and rstd_pre: nullable fp32 [T], kept for the gradient.          */
+/*                                                                           */
+/* moe_block_norm_backward: d_x, d_z, d_gate (the gate's shape and type),     */
+/* d_post_weight and d_pre_weight (weight_dtype) from d_x_out and d_y (either */
+/* may be NULL: zero) and the inputs, rstd_post and rstd_pre of the forward.  */
+/* Sums over tokens run in fp32 in a fixed order.  workspace:                 */
+/* moe_block_norm_workspace_size() bytes, need not be cleared.  Every output  */
+/* but d_x may be NULL.                                                       */
+/* Errors: K > 16384 -> UNSUPPORTED.                                          */
+/* ------------------------------------------------------------------------ */
+typedef struct moe_block_norm_args {
+  int64_t num_tokens, hidden_size;
+  int32_t dtype, weight_dtype; /* MOE_DTYPE_* */
+  const void* x;
+  int64_t x_stride0;
+  const void* z; /* nullable */
+  int64_t z_stride0;
+  const void* post_weight; /* nullable [K] */
+  const void* gate;
+  int32_t gate_kind; /* MOE_GATE_* */
+  int64_t gate_stride0; /* row stride of a full gate, element stride of a token gate */
+  float scale;
+  const void* pre_weight; /* nullable [K] */
+  float weight_offset, eps;
+  void* x_out; /* iff z */
+  int64_t x_out_stride0;
+  void* y; /* iff pre_weight */
+  int64_t y_stride0;
+  float* rstd_post; /* nullable [T] */
+  float* rstd_pre;  /* nullable [T] */
+} moe_block_norm_args_t;
+
+moe_status_t moe_block_norm(const moe_block_norm_args_t* args, void* stream);
+
+typedef struct moe_block_norm_backward_args {
+  int64_t num_tokens, hidden_size;
+  int32_t dtype, weight_dtype;
+  const void* x;
+  int64_t x_stride0;
+  const void* z; /* nullable */
+  int64_t z_stride0;
+  const void* post_weight; /* nullable */
+  const void* gate;
+  int32_t gate_kind;
+  int64_t gate_stride0;
+  float scale;
+  const void* pre_weight; /* nullable */
+  float weight_offset;
+  const float* rstd_post; /* iff post_weight */
+  const float* rstd_pre;  /* iff pre_weight */
+  const void* d_x_out;    /* nullable */
+  int64_t d_x_out_stride0;
+  const void* d_y; /* nullable; needs pre_weight */
+  int64_t d_y_stride0;
+  void* d_x;
+  int64_t d_x_stride0;
+  void* d_z; /* nullable */
+  int64_t d_z_stride0;
+  void* d_gate; /* nullable */
+  int64_t d_gate_stride0;
+  void* d_post_weight; /* nullable [K] */
+  void* d_pre_weight;  /* nullable [K] */
+  void* workspace;
+  size_t workspace_bytes;
+} moe_block_norm_backward_args_t;
+
+moe_status_t moe_block_norm_backward(const moe_block_norm_backward_args_t* args, void* stream);
+
+size_t moe_block_norm_workspace_size(int64_t num_tokens, int64_t hidden_size);
+
+/* ------------------------------------------------------------------------ */
+/* moe_lora_linear                                                           */
+/*                                                                           */
+/*   out[t, n] = sum_k x[t, k] * weight[n, k]                                 */
+/*             + lora_scale[a] * sum_r lora_b[a, n, r] * h[t, r],             */
+/*   h[t, r] = sum_k x[t, k] * lora_a[a, r, k],  a = adapter_ids[t];          */
+/* tokens with a < 0 (no adapter; a >= num_adapters also sets                 */
+/* MOE_DEV_BAD_ADAPTER) take the first sum alone.  Sums are in fp32; scale*h  */
+/* enters the second product as two values of the tensors' type (its rounding */
+/* and the remainder), out is rounded once.                                   */
+/* x [T, K] and out [T, N]: inner stride 1, row strides of their own; weight  */
+/* [N, K], lora_a [S, R, K], lora_b [S, N, R] contiguous; adapter_ids int32   */
+/* [T]; lora_scale fp32 [S]; bf16 or fp16.  An adapter of lower rank than R   */
+/* has zero rows in lora_a.  num_adapters == 0: the projection alone.         */
+/* workspace: moe_lora_workspace_size() bytes, need not be cleared.           */
+/* Errors: K % 8, R % 8, x_stride0 % 8 != 0, x, weight, lora_a, lora_b not    */
+/* 16-byte aligned -> ALIGNMENT; R > 128, num_adapters > 4096, fp32 ->        */
+/* UNSUPPORTED.  A GEMM wait that ran out sets MOE_DEV_TIMEOUT.               */
+/* ------------------------------------------------------------------------ */
+typedef struct moe_lora_args {
+  int64_t num_tokens, in_features, out_features; /* T, K, N */
+  int64_t num_adapters, rank;                    /* S, R */
+  int32_t dtype;                                 /* MOE_DTYPE_BF16 or MOE_DTYPE_FP16 */
+  const void* x;
+  int64_t x_stride0;
+  const void* weight;
+  const void* lora_a;
+  const void* lora_b;
+  const int32_t* adapter_ids;
+  const float* lora_scale;
+  void* out;
+  int64_t out_stride0;
+  void* workspace;
+  size_t workspace_bytes;
+  uint32_t* device_status;
+} moe_lora_args_t;
+
+moe_status_t moe_lora_linear(const moe_lora_args_t* args, void* stream);
+
+size_t moe_lora_workspace_size(int64_t num_tokens, int64_t in_features, int64_t out_features,
+                               int64_t num_adapters, int64_t rank);
 
 /* ------------------------------------------------------------------------ */
 /* Utilities                                                                 */

@@ -1,7 +1,8 @@
 """Thin ctypes binding of ``libmoe_prep.so`` (argument marshalling only).
 
 The functions keep the C names: ``moe_prepare_inputs``, ``moe_batched_experts``,
-``moe_topk_reduce``.  Tensors are PyTorch CUDA tensors; only their data
+``moe_topk_reduce``; around them ``moe_route``, ``moe_sort_routes``, ``moe_permute``,
+``moe_unpermute``, ``moe_block_norm``, ``moe_lora_linear`` and their gradients.  Tensors are PyTorch CUDA tensors; only their data
 pointers, shapes and strides cross the boundary.  Every step of the path runs
 in the library's kernels; if the library is missing this module raises.
 """
@@ -22,7 +23,10 @@ MOE_WEIGHTS_FP32, MOE_WEIGHTS_BF16 = 0, 1
 MOE_ACT_SILU = 0
 MOE_SHARED_BF16, MOE_SHARED_FP8 = 0, 1
 MOE_STAGE_W13, MOE_STAGE_W2, MOE_STAGE_ALL = 1, 2, 3
-MOE_DEV_CAPACITY, MOE_DEV_BAD_EXPERT, MOE_DEV_TIMEOUT = 1, 2, 4
+MOE_DTYPE_FP32, MOE_DTYPE_BF16, MOE_DTYPE_FP16 = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_FULL = 0, 1, 2, 3
+MOE_DEV_CAPACITY, MOE_DEV_BAD_EXPERT, MOE_DEV_TIMEOUT, MOE_DEV_BAD_ADAPTER = 1, 2, 4, 8
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARGUMENT", 2: "MOE_ERR_SHAPE",
                 3: "MOE_ERR_UNSUPPORTED", 4: "MOE_ERR_ALIGNMENT", 5: "MOE_ERR_WORKSPACE",
                 6: "MOE_ERR_CUDA"}
@@ -98,6 +102,64 @@ class ExpertsArgs(ctypes.Structure):
     ]
 
 
+_f32 = ctypes.c_float
+
+
+class RouteArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", _i64), ("num_experts", _i64), ("top_k", _i64),
+        ("logits", _vp), ("logits_dtype", _i32), ("logits_stride0", _i64),
+        ("bias", _vp), ("is_padding", _vp), ("scoring", _i32), ("renormalize", _i32),
+        ("scale", _f32), ("num_groups", _i64), ("top_groups", _i64),
+        ("topk_ids", _vp), ("topk_ids_dtype", _i32), ("topk_weights", _vp),
+    ]
+
+
+class RouteBackwardArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", _i64), ("num_experts", _i64), ("top_k", _i64),
+        ("logits", _vp), ("logits_dtype", _i32), ("logits_stride0", _i64),
+        ("scoring", _i32), ("renormalize", _i32), ("scale", _f32),
+        ("topk_ids", _vp), ("topk_ids_dtype", _i32), ("d_weights", _vp),
+        ("d_logits", _vp), ("d_logits_stride0", _i64),
+    ]
+
+
+class BlockNormArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", _i64), ("hidden_size", _i64), ("dtype", _i32), ("weight_dtype", _i32),
+        ("x", _vp), ("x_stride0", _i64), ("z", _vp), ("z_stride0", _i64),
+        ("post_weight", _vp), ("gate", _vp), ("gate_kind", _i32), ("gate_stride0", _i64),
+        ("scale", _f32), ("pre_weight", _vp), ("weight_offset", _f32), ("eps", _f32),
+        ("x_out", _vp), ("x_out_stride0", _i64), ("y", _vp), ("y_stride0", _i64),
+        ("rstd_post", _vp), ("rstd_pre", _vp),
+    ]
+
+
+class BlockNormBackwardArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", _i64), ("hidden_size", _i64), ("dtype", _i32), ("weight_dtype", _i32),
+        ("x", _vp), ("x_stride0", _i64), ("z", _vp), ("z_stride0", _i64),
+        ("post_weight", _vp), ("gate", _vp), ("gate_kind", _i32), ("gate_stride0", _i64),
+        ("scale", _f32), ("pre_weight", _vp), ("weight_offset", _f32),
+        ("rstd_post", _vp), ("rstd_pre", _vp),
+        ("d_x_out", _vp), ("d_x_out_stride0", _i64), ("d_y", _vp), ("d_y_stride0", _i64),
+        ("d_x", _vp), ("d_x_stride0", _i64), ("d_z", _vp), ("d_z_stride0", _i64),
+        ("d_gate", _vp), ("d_gate_stride0", _i64), ("d_post_weight", _vp), ("d_pre_weight", _vp),
+        ("workspace", _vp), ("workspace_bytes", _sz),
+    ]
+
+
+class LoraArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", _i64), ("in_features", _i64), ("out_features", _i64),
+        ("num_adapters", _i64), ("rank", _i64), ("dtype", _i32),
+        ("x", _vp), ("x_stride0", _i64), ("weight", _vp), ("lora_a", _vp), ("lora_b", _vp),
+        ("adapter_ids", _vp), ("lora_scale", _vp), ("out", _vp), ("out_stride0", _i64),
+        ("workspace", _vp), ("workspace_bytes", _sz), ("device_status", _vp),
+    ]
+
+
 _lib = None
 
 
@@ -131,6 +193,27 @@ def configure(lib):
     lib.moe_topk_reduce.restype = ctypes.c_int
     lib.moe_topk_reduce.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _vp,
                                     _vp]
+    for name, args in (("moe_route", RouteArgs), ("moe_route_backward", RouteBackwardArgs),
+                       ("moe_block_norm", BlockNormArgs),
+                       ("moe_block_norm_backward", BlockNormBackwardArgs),
+                       ("moe_lora_linear", LoraArgs)):
+        getattr(lib, name).restype = ctypes.c_int
+        getattr(lib, name).argtypes = [ctypes.POINTER(args), _vp]
+    for name, n in (("moe_sort_workspace_size", 3), ("moe_block_norm_workspace_size", 2),
+                    ("moe_lora_workspace_size", 5)):
+        getattr(lib, name).restype = _sz
+        getattr(lib, name).argtypes = [_i64] * n
+    lib.moe_sort_routes.restype = ctypes.c_int
+    lib.moe_sort_routes.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp,
+                                    _vp]
+    lib.moe_permute.restype = ctypes.c_int
+    lib.moe_permute.argtypes = [_vp, _i64, _i32, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _i64,
+                                _vp]
+    lib.moe_unpermute.restype = ctypes.c_int
+    lib.moe_unpermute.argtypes = [_vp, _i64, _i64, _i32, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp]
+    lib.moe_unpermute_backward.restype = ctypes.c_int
+    lib.moe_unpermute_backward.argtypes = [_vp, _i64, _vp, _i64, _i64, _i32, _vp, _vp, _vp, _i64,
+                                           _i64, _i64, _i64, _vp, _i64, _vp, _vp]
     return lib
 
 
@@ -398,6 +481,256 @@ def moe_topk_reduce(expert_out, topk_idx, route_slot, topk_weights, out, stream=
     _check("moe_topk_reduce", load().moe_topk_reduce(
         _ptr(expert_out), E, M_max, K, _ptr(topk_idx), _ptr(route_slot), _ptr(topk_weights), T, k,
         _ptr(num_valid_tokens), _ptr(out), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# The operators around the experts.  The library sees pointers, sizes and
+# strides; what only the tensors know (types, shapes, inner strides) is checked
+# here and raises ValueError.
+# ---------------------------------------------------------------------------
+_DTYPE = {torch.float32: MOE_DTYPE_FP32, torch.bfloat16: MOE_DTYPE_BF16,
+          torch.float16: MOE_DTYPE_FP16}
+_IDS = {torch.int32: MOE_IDS_INT32, torch.int64: MOE_IDS_INT64}
+
+
+def _raw_stream(stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rows(name, t, T, K, dtype):
+    """Row stride of a [T, K] tensor with inner stride 1 (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype != dtype or t.shape != (T, K):
+        raise ValueError(f"{name}: want {dtype} [{T}, {K}], got {t.dtype} {list(t.shape)}")
+    s0, s1 = t.stride()
+    if s1 != 1 and K > 1:
+        raise ValueError(f"{name}: inner stride must be 1, got {s1}")
+    return s0
+
+
+def _flat(name, t, shape, dtype):
+    """Checks a contiguous tensor (or None) and gives its address."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: want contiguous {dtype} {list(shape)}, got {t.dtype} "
+                         f"{list(t.shape)} with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _dtype_of(name, t, table=_DTYPE):
+    d = table.get(t.dtype)
+    if d is None:
+        raise ValueError(f"{name}: unsupported type {t.dtype}")
+    return d
+
+
+def moe_route(logits, topk_ids, topk_weights, bias=None, is_padding=None,
+              scoring=MOE_SCORE_SOFTMAX, renormalize=True, scale=1.0, num_groups=1, top_groups=1,
+              stream=None):
+    """Router: top-k ids (int32 or int64 [T, k]) and weights (fp32 [T, k]) of logits [T, E].
+
+    bias: fp32 [E], added for the selection alone; is_padding: uint8 [T]; num_groups,
+    top_groups: only the experts of the best groups are taken.  See include/moe_prep.h."""
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    if bias is not None:
+        _flat("bias", bias, (E,), torch.float32)
+    if is_padding is not None:
+        _flat("is_padding", is_padding, (T,), torch.uint8)
+    a = RouteArgs(T, E, k, logits.data_ptr(), _dtype_of("logits", logits),
+                  _rows("logits", logits, T, E, logits.dtype), _at(bias), _at(is_padding), scoring,
+                  1 if renormalize else 0, scale, num_groups, top_groups,
+                  _flat("topk_ids", topk_ids, (T, k), topk_ids.dtype),
+                  _dtype_of("topk_ids", topk_ids, _IDS),
+                  _flat("topk_weights", topk_weights, (T, k), torch.float32))
+    _check("moe_route", load().moe_route(a, _raw_stream(stream)))
+
+
+def moe_route_backward(logits, topk_ids, d_weights, d_logits, scoring=MOE_SCORE_SOFTMAX,
+                       renormalize=True, scale=1.0, stream=None):
+    """Gradient of the logits (every value written) from that of ``moe_route``'s weights; scoring,
+    renormalize and scale as in the forward call.  See include/moe_prep.h."""
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    a = RouteBackwardArgs(T, E, k, logits.data_ptr(), _dtype_of("logits", logits),
+                          _rows("logits", logits, T, E, logits.dtype), scoring,
+                          1 if renormalize else 0, scale,
+                          _flat("topk_ids", topk_ids, (T, k), topk_ids.dtype),
+                          _dtype_of("topk_ids", topk_ids, _IDS),
+                          _flat("d_weights", d_weights, (T, k), torch.float32),
+                          d_logits.data_ptr(), _rows("d_logits", d_logits, T, E, logits.dtype))
+    _check("moe_route_backward", load().moe_route_backward(a, _raw_stream(stream)))
+
+
+def sort_workspace_size(num_tokens, top_k, num_experts) -> int:
+    return int(load().moe_sort_workspace_size(num_tokens, top_k, num_experts))
+
+
+def moe_sort_routes(topk_ids, expert_offsets, route_row, row_route, workspace=None,
+                    device_status=None, stream=None):
+    """Rows of the routes in expert order.  topk_ids: int32 or int64 [T, k]; expert_offsets: int32
+    [E + 1]; route_row: int32 [T, k]; row_route: int32 [T * k]; workspace: uint8,
+    sort_workspace_size() bytes.  See include/moe_prep.h."""
+    T, k = topk_ids.shape
+    E = expert_offsets.shape[0] - 1
+    _check("moe_sort_routes", load().moe_sort_routes(
+        _flat("topk_ids", topk_ids, (T, k), topk_ids.dtype), _dtype_of("topk_ids", topk_ids, _IDS),
+        T, k, E, _flat("expert_offsets", expert_offsets, (E + 1,), torch.int32),
+        _flat("route_row", route_row, (T, k), torch.int32),
+        _flat("row_route", row_route, (T * k,), torch.int32), _at(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _at(device_status), _raw_stream(stream)))
+
+
+def moe_permute(x, route_row, expert_offsets, rows, stream=None):
+    """rows[route_row[t, j]] = x[t]; rows past the last routed one become zeros.  x: [T, K] and
+    rows: [num_rows, K] of one type (fp32, bf16, fp16).  See include/moe_prep.h."""
+    T, k = route_row.shape
+    K, n = rows.shape[1], rows.shape[0]
+    _check("moe_permute", load().moe_permute(
+        x.data_ptr(), _rows("x", x, T, K, rows.dtype), _dtype_of("rows", rows), T, K, k,
+        _flat("route_row", route_row, (T, k), torch.int32),
+        _flat("expert_offsets", expert_offsets, expert_offsets.shape[:1], torch.int32),
+        expert_offsets.shape[0] - 1, rows.data_ptr(), _rows("rows", rows, n, K, rows.dtype), n,
+        _raw_stream(stream)))
+
+
+def moe_unpermute(rows, route_row, topk_weights, out, stream=None):
+    """out[t] = sum_j topk_weights[t, j] * rows[route_row[t, j]], summed in fp32; topk_weights None:
+    every weight is 1.  See include/moe_prep.h."""
+    T, k = route_row.shape
+    n, K = rows.shape
+    _check("moe_unpermute", load().moe_unpermute(
+        rows.data_ptr(), _rows("rows", rows, n, K, rows.dtype), n, _dtype_of("rows", rows),
+        _flat("route_row", route_row, (T, k), torch.int32),
+        _flat("topk_weights", topk_weights, (T, k), torch.float32), T, K, k, out.data_ptr(),
+        _rows("out", out, T, K, rows.dtype), _raw_stream(stream)))
+
+
+def moe_permute_backward(d_rows, route_row, d_x, stream=None):
+    """d_x[t] = sum_j d_rows[route_row[t, j]]: the gradient of ``moe_permute``."""
+    moe_unpermute(d_rows, route_row, None, d_x, stream=stream)
+
+
+def moe_unpermute_backward(d_out, rows, route_row, topk_weights, expert_offsets, d_rows, d_weights,
+                           stream=None):
+    """Gradients of ``moe_unpermute``: d_rows [num_rows, K] (zeros past the last routed row) and
+    d_weights fp32 [T, k].  See include/moe_prep.h."""
+    T, k = route_row.shape
+    n, K = rows.shape
+    _check("moe_unpermute_backward", load().moe_unpermute_backward(
+        d_out.data_ptr(), _rows("d_out", d_out, T, K, rows.dtype), rows.data_ptr(),
+        _rows("rows", rows, n, K, rows.dtype), n, _dtype_of("rows", rows),
+        _flat("route_row", route_row, (T, k), torch.int32),
+        _flat("topk_weights", topk_weights, (T, k), torch.float32),
+        _flat("expert_offsets", expert_offsets, expert_offsets.shape[:1], torch.int32),
+        expert_offsets.shape[0] - 1, T, K, k, d_rows.data_ptr(),
+        _rows("d_rows", d_rows, n, K, rows.dtype),
+        _flat("d_weights", d_weights, (T, k), torch.float32), _raw_stream(stream)))
+
+
+def _gate(gate, name, x, wdtype):
+    """(kind, stride) of a gate, or of its gradient, by its shape: [K], [T] or [T, K] ([T, 1] is
+    [T]; a [K] gate with T == K is taken per channel)."""
+    T, K = x.shape
+    if gate is None:
+        return MOE_GATE_NONE, 0
+    if gate.dim() == 1 and gate.shape[0] == K and gate.dtype == wdtype:
+        _flat(name, gate, (K,), wdtype)
+        return MOE_GATE_CHANNEL, 0
+    if gate.dtype == x.dtype and (gate.shape == (T,) or (gate.shape == (T, 1) and K != 1)):
+        return MOE_GATE_TOKEN, gate.stride(0)
+    return MOE_GATE_FULL, _rows(name, gate, T, K, x.dtype)
+
+
+def moe_block_norm(x, z=None, post_weight=None, gate=None, scale=1.0, pre_weight=None,
+                   weight_offset=0.0, eps=1e-6, x_out=None, y=None, rstd_post=None, rstd_pre=None,
+                   stream=None):
+    """x_out = x + scale * gate * rmsnorm(z, post_weight) and y = rmsnorm(x_out, pre_weight).
+
+    x, z, x_out, y: [T, K] of one type; post_weight, pre_weight and a channel gate: [K] of one
+    type (fp32, bf16 or fp16); a token gate: [T] of x's type; a full gate: [T, K].  Without z only
+    y = rmsnorm(x) is written, without pre_weight only x_out.  rstd_post, rstd_pre: fp32 [T], kept
+    for the gradient.  See include/moe_prep.h."""
+    T, K = x.shape
+    w = pre_weight if pre_weight is not None else post_weight
+    wdtype = w.dtype if w is not None else (gate.dtype if gate is not None else x.dtype)
+    kind, gs = _gate(gate, "gate", x, wdtype)
+    dt = x.dtype
+    a = BlockNormArgs(T, K, _dtype_of("x", x), _DTYPE.get(wdtype, -1), x.data_ptr(),
+                      _rows("x", x, T, K, dt), _at(z), _rows("z", z, T, K, dt),
+                      _flat("post_weight", post_weight, (K,), wdtype), _at(gate), kind, gs, scale,
+                      _flat("pre_weight", pre_weight, (K,), wdtype), weight_offset, eps,
+                      _at(x_out), _rows("x_out", x_out, T, K, dt), _at(y),
+                      _rows("y", y, T, K, dt), _flat("rstd_post", rstd_post, (T,), torch.float32),
+                      _flat("rstd_pre", rstd_pre, (T,), torch.float32))
+    _check("moe_block_norm", load().moe_block_norm(a, _raw_stream(stream)))
+
+
+def block_norm_workspace_size(num_tokens, hidden_size) -> int:
+    return int(load().moe_block_norm_workspace_size(num_tokens, hidden_size))
+
+
+def moe_block_norm_backward(x, z=None, post_weight=None, gate=None, scale=1.0, pre_weight=None,
+                            weight_offset=0.0, rstd_post=None, rstd_pre=None, d_x_out=None,
+                            d_y=None, d_x=None, d_z=None, d_gate=None, d_post_weight=None,
+                            d_pre_weight=None, workspace=None, stream=None):
+    """Gradients of ``moe_block_norm`` from d_x_out and d_y (either may be None) and the forward's
+    inputs, rstd_post and rstd_pre.  d_x is always written, the others where given.  workspace:
+    uint8, block_norm_workspace_size() bytes.  See include/moe_prep.h."""
+    T, K = x.shape
+    w = pre_weight if pre_weight is not None else post_weight
+    wdtype = w.dtype if w is not None else (gate.dtype if gate is not None else x.dtype)
+    kind, gs = _gate(gate, "gate", x, wdtype)
+    dkind, dgs = _gate(d_gate, "d_gate", x, wdtype)
+    if d_gate is not None and (dkind != kind or d_gate.shape != gate.shape):
+        raise ValueError("d_gate must have the gate's shape and type")
+    dt, f32 = x.dtype, torch.float32
+    a = BlockNormBackwardArgs(
+        T, K, _dtype_of("x", x), _DTYPE.get(wdtype, -1), x.data_ptr(), _rows("x", x, T, K, dt),
+        _at(z), _rows("z", z, T, K, dt), _flat("post_weight", post_weight, (K,), wdtype),
+        _at(gate), kind, gs, scale, _flat("pre_weight", pre_weight, (K,), wdtype), weight_offset,
+        _flat("rstd_post", rstd_post, (T,), f32), _flat("rstd_pre", rstd_pre, (T,), f32),
+        _at(d_x_out), _rows("d_x_out", d_x_out, T, K, dt), _at(d_y), _rows("d_y", d_y, T, K, dt),
+        _at(d_x), _rows("d_x", d_x, T, K, dt), _at(d_z), _rows("d_z", d_z, T, K, dt), _at(d_gate),
+        dgs, _flat("d_post_weight", d_post_weight, (K,), wdtype),
+        _flat("d_pre_weight", d_pre_weight, (K,), wdtype), _at(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size())
+    _check("moe_block_norm_backward", load().moe_block_norm_backward(a, _raw_stream(stream)))
+
+
+def lora_workspace_size(num_tokens, in_features, out_features, num_adapters, rank) -> int:
+    return int(load().moe_lora_workspace_size(num_tokens, in_features, out_features, num_adapters,
+                                              rank))
+
+
+def moe_lora_linear(x, weight, lora_a, lora_b, adapter_ids, lora_scale, out, workspace,
+                    device_status=None, stream=None):
+    """out[t] = x[t] weight^T + lora_scale[a] * (x[t] lora_a[a]^T) lora_b[a]^T, a = adapter_ids[t]
+    (< 0: no adapter).  x [T, K], weight [N, K], lora_a [S, R, K], lora_b [S, N, R], out [T, N] of
+    one type (bf16 or fp16); adapter_ids int32 [T]; lora_scale fp32 [S].  lora_a None: the
+    projection alone.  workspace: uint8, lora_workspace_size() bytes.  See include/moe_prep.h."""
+    T, K = x.shape
+    N = weight.shape[0]
+    dt = x.dtype
+    S, R = (lora_a.shape[0], lora_a.shape[1]) if lora_a is not None else (0, 0)
+    a = LoraArgs(T, K, N, S, R, _dtype_of("x", x), x.data_ptr(), _rows("x", x, T, K, dt),
+                 _flat("weight", weight, (N, K), dt), _flat("lora_a", lora_a, (S, R, K), dt),
+                 _flat("lora_b", lora_b, (S, N, R), dt),
+                 _flat("adapter_ids", adapter_ids, (T,), torch.int32),
+                 _flat("lora_scale", lora_scale, (S,), torch.float32), out.data_ptr(),
+                 _rows("out", out, T, N, dt), _at(workspace),
+                 0 if workspace is None else workspace.numel() * workspace.element_size(),
+                 _at(device_status))
+    _check("moe_lora_linear", load().moe_lora_linear(a, _raw_stream(stream)))
 
 
 class MoeLayer:

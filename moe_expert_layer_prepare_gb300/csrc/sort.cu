@@ -1,0 +1,565 @@
+// Rows sorted by expert and back with the routing weights applied, and the
+// gradients of both.
+//
+// moe_sort_routes is a stable counting sort: a route's row is the number of
+// routes to lower experts plus that of earlier routes to its own.  Blocks take
+// consecutive routes and the warps of a block consecutive segments; in a warp
+// __match_any_sync gives the rank among 32 routes and a shared table of counts
+// per (warp, expert) the ranks across its segment.  Up to SORT_ONE_BLOCK routes
+// one block does it all; above, a first launch counts each block's routes per
+// expert and a second one places them, every block summing the counts of the
+// blocks before it.  No atomics on results, so rows are the same every time.
+//
+// The row kernels move each routed row once: moe_permute reads a token's row
+// once and writes it to its k rows, moe_unpermute reads k rows and writes one,
+// the gradient of the weights comes from the same reads that scale d_out.
+// All are bound by HBM.
+#include "block_common.cuh"
+
+namespace moe {
+
+constexpr int SORT_WARPS = 16;
+constexpr int SORT_THREADS = SORT_WARPS * 32;
+constexpr int SORT_MAX_EXPERTS = 1024;
+constexpr int SORT_MAX_BLOCKS = 128;
+
+struct SortParams {
+  const void* ids;
+  int ids64;
+  int32_t R, E, blocks, per_block;  // per_block: a multiple of SORT_THREADS
+  int32_t* offsets;
+  int32_t* route_row;
+  int32_t* row_route;
+  int32_t* hist;  // [blocks, E]
+  uint32_t* status;
+};
+
+// Expert of route r, or -1.
+__device__ __forceinline__ int route_expert(const SortParams& p, int r, bool* bad) {
+  const int64_t id = p.ids64 ? static_cast<const int64_t*>(p.ids)[r]
+                             : (int64_t)static_cast<const int32_t*>(p.ids)[r];
+  if (id >= p.E) *bad = true;
+  return id >= 0 && id < p.E ? (int)id : -1;
+}
+
+__global__ void __launch_bounds__(SORT_THREADS) sort_count_kernel(SortParams p) {
+  __shared__ int cnt[SORT_MAX_EXPERTS];
+  for (int e = threadIdx.x; e < p.E; e += SORT_THREADS) cnt[e] = 0;
+  __syncthreads();
+  pdl_wait();
+  pdl_launch_dependents();
+  const int r0 = blockIdx.x * p.per_block, r1 = min(p.R, r0 + p.per_block);
+  bool bad = false;
+  for (int r = r0 + threadIdx.x; r < r1; r += SORT_THREADS) {
+    const int e = route_expert(p, r, &bad);
+    if (e >= 0) atomicAdd(&cnt[e], 1);
+  }
+  if (bad) set_status(p.status, MOE_DEV_BAD_EXPERT);
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += SORT_THREADS) p.hist[blockIdx.x * p.E + e] = cnt[e];
+}
+
+__global__ void __launch_bounds__(SORT_THREADS) sort_place_kernel(SortParams p) {
+  // count of (warp, expert), then the warp's first rank in the block: at most
+  // per_block / SORT_WARPS < 65536
+  __shared__ uint16_t table[SORT_WARPS][SORT_MAX_EXPERTS];
+  __shared__ int base[SORT_MAX_EXPERTS];  // first row of this block's routes of an expert
+  __shared__ int warp_total[SORT_WARPS];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int i = tid; i < SORT_WARPS * p.E; i += SORT_THREADS) table[i / p.E][i % p.E] = 0;
+  __syncthreads();
+  pdl_wait();
+  pdl_launch_dependents();
+  const int per_warp = p.per_block / SORT_WARPS;
+  const int w0 = min((int64_t)p.R, (int64_t)blockIdx.x * p.per_block + (int64_t)warp * per_warp);
+  const int w1 = min((int64_t)p.R, (int64_t)w0 + per_warp);
+  bool bad = false;
+  for (int r0 = w0; r0 < w1; r0 += 32) {
+    const int r = r0 + lane;
+    const int e = r < w1 ? route_expert(p, r, &bad) : -1;
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+    if (e >= 0 && (same & lanemask_lt()) == 0) table[warp][e] += (uint16_t)__popc(same);
+    __syncwarp();
+  }
+  if (bad && p.blocks == 1) set_status(p.status, MOE_DEV_BAD_EXPERT);
+  __syncthreads();
+  // per expert: the counts become exclusive prefixes over the warps; the rows
+  // before this block's are those of all blocks to lower experts (scanned
+  // below) and of earlier blocks to the same expert
+  int carry = 0;
+  for (int e0 = 0; e0 < p.E; e0 += SORT_THREADS) {
+    const int e = e0 + tid;
+    int mine = 0, all = 0, before = 0;
+    if (e < p.E) {
+      for (int w = 0; w < SORT_WARPS; ++w) {
+        const int c = table[w][e];
+        table[w][e] = (uint16_t)mine;
+        mine += c;
+      }
+      if (p.blocks == 1) {
+        all = mine;
+      } else {
+        for (int b = 0; b < p.blocks; ++b) {
+          const int c = __ldg(p.hist + b * p.E + e);
+          all += c;
+          if (b < (int)blockIdx.x) before += c;
+        }
+      }
+    }
+    int incl = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_total[warp] = incl;
+    __syncthreads();
+    int below = carry;
+    for (int w = 0; w < SORT_WARPS; ++w) {
+      if (w < warp) below += warp_total[w];
+      carry += warp_total[w];
+    }
+    if (e < p.E) {
+      base[e] = below + incl - all + before;
+      if (blockIdx.x == 0) p.offsets[e] = below + incl - all;
+    }
+    __syncthreads();
+  }
+  if (blockIdx.x == 0 && tid == 0) p.offsets[p.E] = carry;
+  for (int r0 = w0; r0 < w1; r0 += 32) {
+    const int r = r0 + lane;
+    bool unused = false;
+    const int e = r < w1 ? route_expert(p, r, &unused) : -1;
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+    int row = -1;
+    if (e >= 0) {
+      row = base[e] + table[warp][e] + __popc(same & lanemask_lt());
+      p.row_route[row] = r;
+    }
+    if (r < w1) p.route_row[r] = row;
+    __syncwarp();
+    if (e >= 0 && (same & lanemask_lt()) == 0) table[warp][e] += (uint16_t)__popc(same);
+    __syncwarp();
+  }
+  for (int64_t r = (int64_t)carry + (int64_t)blockIdx.x * SORT_THREADS + tid; r < p.R;
+       r += (int64_t)gridDim.x * SORT_THREADS)
+    p.row_route[r] = -1;
+}
+
+struct RowParams {
+  int64_t T, K, num_rows;
+  int k;
+  const int32_t* route_row;
+  const float* w;         // nullable
+  const int32_t* offsets;  // [E + 1]
+  int64_t E;
+  const void* x;  // token rows read
+  int64_t x_stride;
+  const void* rows;  // expert rows read
+  int64_t rows_stride;
+  void* out;  // token rows written
+  int64_t out_stride;
+  void* out_rows;  // expert rows written
+  int64_t out_rows_stride;
+  float* d_w;
+};
+
+// Row of route (t, lane) for lane < k, or -1.
+__device__ __forceinline__ int lane_row(const RowParams& p, int64_t t, int lane) {
+  const int r = lane < p.k ? p.route_row[t * p.k + lane] : -1;
+  return r >= 0 && r < p.num_rows ? r : -1;
+}
+
+// One warp per (token, PERMUTE_VECS * 32 packs of the row): the packs are read
+// once and written to the k rows.  Tasks past the tokens clear the rows past
+// the last routed one.
+constexpr int PERMUTE_VECS = 4;
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) permute_kernel(RowParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t gwarp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
+  constexpr int64_t chunk = (int64_t)PERMUTE_VECS * 32 * VEC;
+  const int64_t chunks = (p.K + chunk - 1) / chunk;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t used = min(max((int64_t)p.offsets[p.E], (int64_t)0), p.num_rows);
+  const int64_t tasks = (p.T + p.num_rows - used) * chunks;
+  T* rows = static_cast<T*>(p.out_rows);
+  for (int64_t task = gwarp; task < tasks; task += nwarps) {
+    const int64_t t = task / chunks;
+    const int64_t c0 = (task - t * chunks) * chunk + lane * VEC;
+    Pack<T, VEC> v[PERMUTE_VECS];
+    if (t >= p.T) {
+      T* dst = rows + (used + t - p.T) * p.out_rows_stride;
+      const Pack<T, VEC> zero = zero_pack<T, VEC>();
+#pragma unroll
+      for (int i = 0; i < PERMUTE_VECS; ++i)
+        if (c0 + i * 32 * VEC < p.K) store_pack<T, VEC>(dst + c0 + i * 32 * VEC, zero);
+      continue;
+    }
+    const int my_row = lane_row(p, t, lane);
+    const T* src = static_cast<const T*>(p.x) + t * p.x_stride;
+#pragma unroll
+    for (int i = 0; i < PERMUTE_VECS; ++i)
+      if (c0 + i * 32 * VEC < p.K) v[i] = load_pack_stream<T, VEC>(src + c0 + i * 32 * VEC);
+    for (int j = 0; j < p.k; ++j) {
+      const int row = __shfl_sync(0xFFFFFFFFu, my_row, j);
+      if (row < 0) continue;
+      T* dst = rows + (int64_t)row * p.out_rows_stride;
+#pragma unroll
+      for (int i = 0; i < PERMUTE_VECS; ++i)
+        if (c0 + i * 32 * VEC < p.K) store_pack<T, VEC>(dst + c0 + i * 32 * VEC, v[i]);
+    }
+  }
+}
+
+// One warp per (token, 32 packs): the routed rows' packs are read eight at a
+// time, all in flight, and summed in fp32 in ascending j.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) unpermute_kernel(RowParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t gwarp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
+  const int64_t chunks = (p.K + 32 * VEC - 1) / (32 * VEC);
+  const int64_t tasks = p.T * chunks;
+  pdl_wait();
+  pdl_launch_dependents();
+  const T* rows = static_cast<const T*>(p.rows);
+  for (int64_t task = gwarp; task < tasks; task += nwarps) {
+    const int64_t t = task / chunks;
+    const int64_t c0 = (task - t * chunks) * 32 * VEC + lane * VEC;
+    const bool active = c0 < p.K;
+    const int my_row = lane_row(p, t, lane);
+    const float my_w = lane < p.k ? (p.w != nullptr ? p.w[t * p.k + lane] : 1.0f) : 0.0f;
+    float acc[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
+    for (int j0 = 0; j0 < p.k; j0 += 8) {
+      Pack<T, VEC> v[8];
+      int row[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        row[i] = __shfl_sync(0xFFFFFFFFu, my_row, (j0 + i) & 31);
+        if (j0 + i >= p.k) row[i] = -1;
+        if (row[i] >= 0 && active)
+          v[i] = load_pack_stream<T, VEC>(rows + (int64_t)row[i] * p.rows_stride + c0);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float w = __shfl_sync(0xFFFFFFFFu, my_w, (j0 + i) & 31);
+        if (row[i] < 0 || !active) continue;
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) acc[q] = fmaf(w, to_f32(v[i].v[q]), acc[q]);
+      }
+    }
+    if (active) {
+      Pack<T, VEC> o;
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) o.v[q] = from_f32<T>(acc[q]);
+      store_pack<T, VEC>(static_cast<T*>(p.out) + t * p.out_stride + c0, o);
+    }
+  }
+}
+
+// One block per token: each thread takes packs of d_out and, for eight routes
+// at a time, reads their rows' packs (for the weights' gradients) and writes
+// w * d_out in their place.  Tasks past the tokens clear the unused rows.
+constexpr int BACK_THREADS = 256;
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(BACK_THREADS) unpermute_backward_kernel(RowParams p) {
+  __shared__ float part[BACK_THREADS / 32][8];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t used = min(max((int64_t)p.offsets[p.E], (int64_t)0), p.num_rows);
+  const int64_t tasks = p.T + p.num_rows - used;
+  const T* rows = static_cast<const T*>(p.rows);
+  T* d_rows = static_cast<T*>(p.out_rows);
+  for (int64_t t = blockIdx.x; t < tasks; t += gridDim.x) {
+    if (t >= p.T) {
+      T* dst = d_rows + (used + t - p.T) * p.out_rows_stride;
+      for (int64_t c = (int64_t)tid * VEC; c < p.K; c += BACK_THREADS * VEC)
+        store_pack<T, VEC>(dst + c, zero_pack<T, VEC>());
+      continue;
+    }
+    const int my_row = lane_row(p, t, lane);
+    const float my_w = lane < p.k ? p.w[t * p.k + lane] : 0.0f;
+    const T* up = static_cast<const T*>(p.x) + t * p.x_stride;
+    for (int j0 = 0; j0 < p.k; j0 += 8) {
+      int row[8];
+      float w[8], dot[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        row[i] = __shfl_sync(0xFFFFFFFFu, my_row, (j0 + i) & 31);
+        if (j0 + i >= p.k) row[i] = -1;
+        w[i] = __shfl_sync(0xFFFFFFFFu, my_w, (j0 + i) & 31);
+        dot[i] = 0.0f;
+      }
+      for (int64_t c = (int64_t)tid * VEC; c < p.K; c += BACK_THREADS * VEC) {
+        const Pack<T, VEC> g = load_pack<T, VEC>(up + c);
+        Pack<T, VEC> v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (row[i] >= 0)
+            v[i] = load_pack_stream<T, VEC>(rows + (int64_t)row[i] * p.rows_stride + c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (row[i] < 0) continue;
+          Pack<T, VEC> o;
+#pragma unroll
+          for (int q = 0; q < VEC; ++q) {
+            const float gf = to_f32(g.v[q]);
+            dot[i] = fmaf(gf, to_f32(v[i].v[q]), dot[i]);
+            o.v[q] = from_f32<T>(w[i] * gf);
+          }
+          store_pack<T, VEC>(d_rows + (int64_t)row[i] * p.out_rows_stride + c, o);
+        }
+      }
+      __syncthreads();  // the sums of the routes before have been read
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        dot[i] = warp_sum(dot[i]);
+        if (lane == 0) part[warp][i] = dot[i];
+      }
+      __syncthreads();
+      if (tid < 8 && j0 + tid < p.k) {
+        float sum = 0.0f;
+        for (int v = 0; v < BACK_THREADS / 32; ++v) sum += part[v][tid];
+        p.d_w[t * p.k + j0 + tid] = sum;
+      }
+    }
+  }
+}
+
+}  // namespace moe
+
+namespace moe_host {
+
+using moe::RowParams;
+using moe::SortParams;
+
+// Up to this many routes one block sorts them in one launch.
+constexpr int64_t kSortOneBlock = 4096;
+
+static void sort_split(int64_t R, int32_t* blocks, int32_t* per_block) {
+  int64_t per = 1024;
+  if (R <= kSortOneBlock)
+    per = kSortOneBlock;
+  else if (R > per * moe::SORT_MAX_BLOCKS)
+    per = ((R + moe::SORT_MAX_BLOCKS - 1) / moe::SORT_MAX_BLOCKS + 511) / 512 * 512;
+  *per_block = (int32_t)per;
+  *blocks = (int32_t)((R + per - 1) / per);
+}
+
+template <typename K>
+static dim3 one_wave(K kernel, int64_t blocks, int threads) {
+  const int64_t cap =
+      (int64_t)num_sms() * resident_blocks(reinterpret_cast<const void*>(kernel), threads);
+  return dim3((unsigned)(blocks < 1 ? 1 : (blocks > cap ? cap : blocks)));
+}
+
+static moe_status_t check_rows(int64_t T, int64_t K, int64_t k, int64_t num_rows, int32_t dtype) {
+  if (T < 0 || K < 0 || k < 0 || num_rows < 0)
+    return set_error(MOE_ERR_INVALID_ARGUMENT, "negative size");
+  if (!dtype_ok(dtype)) return set_error(MOE_ERR_INVALID_ARGUMENT, "bad dtype %d", dtype);
+  if (k > 32) return set_error(MOE_ERR_UNSUPPORTED, "at most 32 routes a token");
+  if (num_rows >= ((int64_t)1 << 31))
+    return set_error(MOE_ERR_UNSUPPORTED, "num_rows must be below 2^31");
+  return MOE_OK;
+}
+
+// 16-byte packs where every row of every tensor of the call starts on a
+// 16-byte boundary and K fills whole packs, else element by element.
+static bool packs16(int64_t K, size_t elem) { return (K * (int64_t)elem) % 16 == 0; }
+
+}  // namespace moe_host
+
+using namespace moe_host;
+
+extern "C" {
+
+size_t moe_sort_workspace_size(int64_t num_tokens, int64_t top_k, int64_t num_experts) {
+  if (num_tokens <= 0 || top_k <= 0 || num_experts <= 0) return 0;
+  int32_t blocks, per;
+  sort_split(num_tokens * top_k, &blocks, &per);
+  return blocks == 1 ? 0 : (size_t)blocks * num_experts * 4;
+}
+
+moe_status_t moe_sort_routes(const void* topk_ids, int32_t topk_ids_dtype, int64_t num_tokens,
+                             int64_t top_k, int64_t num_experts, int32_t* expert_offsets,
+                             int32_t* route_row, int32_t* row_route, void* workspace,
+                             size_t workspace_bytes, uint32_t* device_status, void* stream) {
+  clear_error();
+  if (num_tokens < 0 || top_k < 0) return set_error(MOE_ERR_INVALID_ARGUMENT, "negative size");
+  if (topk_ids_dtype != MOE_IDS_INT32 && topk_ids_dtype != MOE_IDS_INT64)
+    return set_error(MOE_ERR_INVALID_ARGUMENT, "bad topk_ids_dtype");
+  if (num_experts < 1) return set_error(MOE_ERR_SHAPE, "num_experts must be >= 1");
+  if (num_experts > moe::SORT_MAX_EXPERTS)
+    return set_error(MOE_ERR_UNSUPPORTED, "at most %d experts", moe::SORT_MAX_EXPERTS);
+  if (top_k > 0 && num_tokens > ((int64_t)1 << 26) / top_k)
+    return set_error(MOE_ERR_UNSUPPORTED, "num_tokens * top_k must be at most 2^26");
+  const int64_t R = num_tokens * top_k;
+  if (!expert_offsets || (R > 0 && (!topk_ids || !route_row || !row_route)))
+    return set_error(MOE_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
+  SortParams p{};
+  p.ids = topk_ids;
+  p.ids64 = topk_ids_dtype == MOE_IDS_INT64;
+  p.R = (int32_t)R;
+  p.E = (int32_t)num_experts;
+  sort_split(R > 0 ? R : 1, &p.blocks, &p.per_block);
+  p.offsets = expert_offsets;
+  p.route_row = route_row;
+  p.row_route = row_route;
+  p.hist = static_cast<int32_t*>(workspace);
+  p.status = device_status;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (p.blocks > 1) {
+    const size_t need = (size_t)p.blocks * num_experts * 4;
+    if (workspace == nullptr || workspace_bytes < need)
+      return set_error(MOE_ERR_WORKSPACE, "sorting needs %zu bytes of workspace, got %zu", need,
+                       workspace_bytes);
+    if ((reinterpret_cast<uintptr_t>(workspace) & 3u) != 0)
+      return set_error(MOE_ERR_ALIGNMENT, "workspace must be 4-byte aligned");
+    moe_status_t st = launched(launch_pdl(moe::sort_count_kernel, dim3(p.blocks),
+                                          dim3(moe::SORT_THREADS), 0, s, p), "sort count");
+    if (st != MOE_OK) return st;
+  }
+  return launched(launch_pdl(moe::sort_place_kernel, dim3(p.blocks), dim3(moe::SORT_THREADS), 0,
+                             s, p), "sort place");
+}
+
+moe_status_t moe_permute(const void* x, int64_t x_stride0, int32_t dtype, int64_t num_tokens,
+                         int64_t hidden_size, int64_t top_k, const int32_t* route_row,
+                         const int32_t* expert_offsets, int64_t num_experts, void* rows,
+                         int64_t rows_stride0, int64_t num_rows, void* stream) {
+  clear_error();
+  moe_status_t st = check_rows(num_tokens, hidden_size, top_k, num_rows, dtype);
+  if (st != MOE_OK) return st;
+  if (num_experts < 0) return set_error(MOE_ERR_INVALID_ARGUMENT, "negative size");
+  if (num_rows == 0 || hidden_size == 0) return MOE_OK;
+  if (!rows || !expert_offsets || (num_tokens * top_k > 0 && (!x || !route_row)))
+    return set_error(MOE_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
+  if ((num_tokens > 1 && x_stride0 < hidden_size) || (num_rows > 1 && rows_stride0 < hidden_size))
+    return set_error(MOE_ERR_SHAPE, "row stride smaller than the row");
+  RowParams p{};
+  p.T = num_tokens;
+  p.K = hidden_size;
+  p.num_rows = num_rows;
+  p.k = (int)top_k;
+  p.route_row = route_row;
+  p.offsets = expert_offsets;
+  p.E = num_experts;
+  p.x = x;
+  p.x_stride = x_stride0;
+  p.out_rows = rows;
+  p.out_rows_stride = rows_stride0;
+  return with_dtype(dtype, [&](auto v) {
+    using T = decltype(v);
+    constexpr int V = 16 / sizeof(T);
+    const bool wide = packs16(hidden_size, sizeof(T)) &&
+                      rows_aligned16(x, x_stride0, sizeof(T), num_tokens) &&
+                      rows_aligned16(rows, rows_stride0, sizeof(T), num_rows);
+    auto go = [&](auto kernel, int vec) {
+      const int64_t chunk = (int64_t)moe::PERMUTE_VECS * 32 * vec;
+      const int64_t warps = (num_tokens + num_rows) * ((hidden_size + chunk - 1) / chunk);
+      return launched(launch_pdl(kernel, one_wave(kernel, (warps + 7) / 8, 256), dim3(256), 0,
+                                 static_cast<cudaStream_t>(stream), p), "permute");
+    };
+    return wide ? go(moe::permute_kernel<T, V>, V) : go(moe::permute_kernel<T, 1>, 1);
+  });
+}
+
+moe_status_t moe_unpermute(const void* rows, int64_t rows_stride0, int64_t num_rows, int32_t dtype,
+                           const int32_t* route_row, const float* topk_weights,
+                           int64_t num_tokens, int64_t hidden_size, int64_t top_k, void* out,
+                           int64_t out_stride0, void* stream) {
+  clear_error();
+  moe_status_t st = check_rows(num_tokens, hidden_size, top_k, num_rows, dtype);
+  if (st != MOE_OK) return st;
+  if (num_tokens == 0 || hidden_size == 0) return MOE_OK;
+  if (!out || (num_rows > 0 && !rows) || (top_k > 0 && !route_row))
+    return set_error(MOE_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
+  if ((num_tokens > 1 && out_stride0 < hidden_size) || (num_rows > 1 && rows_stride0 < hidden_size))
+    return set_error(MOE_ERR_SHAPE, "row stride smaller than the row");
+  RowParams p{};
+  p.T = num_tokens;
+  p.K = hidden_size;
+  p.num_rows = num_rows;
+  p.k = (int)top_k;
+  p.route_row = route_row;
+  p.w = topk_weights;
+  p.rows = rows;
+  p.rows_stride = rows_stride0;
+  p.out = out;
+  p.out_stride = out_stride0;
+  return with_dtype(dtype, [&](auto v) {
+    using T = decltype(v);
+    constexpr int V = 16 / sizeof(T);
+    const bool wide = packs16(hidden_size, sizeof(T)) &&
+                      rows_aligned16(rows, rows_stride0, sizeof(T), num_rows) &&
+                      rows_aligned16(out, out_stride0, sizeof(T), num_tokens);
+    auto go = [&](auto kernel, int vec) {
+      const int64_t warps = num_tokens * ((hidden_size + 32 * vec - 1) / (32 * vec));
+      return launched(launch_pdl(kernel, one_wave(kernel, (warps + 7) / 8, 256), dim3(256), 0,
+                                 static_cast<cudaStream_t>(stream), p), "unpermute");
+    };
+    return wide ? go(moe::unpermute_kernel<T, V>, V) : go(moe::unpermute_kernel<T, 1>, 1);
+  });
+}
+
+moe_status_t moe_unpermute_backward(const void* d_out, int64_t d_out_stride0, const void* rows,
+                                    int64_t rows_stride0, int64_t num_rows, int32_t dtype,
+                                    const int32_t* route_row, const float* topk_weights,
+                                    const int32_t* expert_offsets, int64_t num_experts,
+                                    int64_t num_tokens, int64_t hidden_size, int64_t top_k,
+                                    void* d_rows, int64_t d_rows_stride0, float* d_weights,
+                                    void* stream) {
+  clear_error();
+  moe_status_t st = check_rows(num_tokens, hidden_size, top_k, num_rows, dtype);
+  if (st != MOE_OK) return st;
+  if (num_experts < 0) return set_error(MOE_ERR_INVALID_ARGUMENT, "negative size");
+  if (num_tokens * top_k == 0 && num_rows == 0) return MOE_OK;
+  if ((num_rows > 0 && hidden_size > 0 && (!rows || !d_rows)) || !expert_offsets ||
+      (num_tokens * top_k > 0 &&
+       (!route_row || !topk_weights || !d_weights || (hidden_size > 0 && !d_out))))
+    return set_error(MOE_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
+  if ((num_tokens > 1 && d_out_stride0 < hidden_size) ||
+      (num_rows > 1 && (rows_stride0 < hidden_size || d_rows_stride0 < hidden_size)))
+    return set_error(MOE_ERR_SHAPE, "row stride smaller than the row");
+  RowParams p{};
+  p.T = num_tokens;
+  p.K = hidden_size;
+  p.num_rows = num_rows;
+  p.k = (int)top_k;
+  p.route_row = route_row;
+  p.w = topk_weights;
+  p.offsets = expert_offsets;
+  p.E = num_experts;
+  p.x = d_out;
+  p.x_stride = d_out_stride0;
+  p.rows = rows;
+  p.rows_stride = rows_stride0;
+  p.out_rows = d_rows;
+  p.out_rows_stride = d_rows_stride0;
+  p.d_w = d_weights;
+  return with_dtype(dtype, [&](auto v) {
+    using T = decltype(v);
+    constexpr int V = 16 / sizeof(T);
+    const bool wide = packs16(hidden_size, sizeof(T)) &&
+                      rows_aligned16(d_out, d_out_stride0, sizeof(T), num_tokens) &&
+                      rows_aligned16(rows, rows_stride0, sizeof(T), num_rows) &&
+                      rows_aligned16(d_rows, d_rows_stride0, sizeof(T), num_rows);
+    auto go = [&](auto kernel) {
+      return launched(launch_pdl(kernel, one_wave(kernel, num_tokens + num_rows, moe::BACK_THREADS),
+                                 dim3(moe::BACK_THREADS), 0, static_cast<cudaStream_t>(stream), p),
+                      "unpermute backward");
+    };
+    return wide ? go(moe::unpermute_backward_kernel<T, V>)
+                : go(moe::unpermute_backward_kernel<T, 1>);
+  });
+}
+
+}  // extern "C"

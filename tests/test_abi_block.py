@@ -1,0 +1,174 @@
+"""Host-side refusals of the operators around the experts (no GPU: every call below returns
+before its first CUDA call)."""
+import ctypes
+
+import pytest
+
+from moe_expert_layer_prepare_gb300 import binding as B
+
+FAKE = 0x10000  # never dereferenced
+OK, INVALID, SHAPE, UNSUPPORTED, ALIGNMENT, WORKSPACE = range(6)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from moe_expert_layer_prepare_gb300 import build
+    build.build()
+    return B.load()
+
+
+def fill(cls, **kw):
+    a = cls()
+    for n, t in cls._fields_:
+        if t is ctypes.c_void_p:
+            setattr(a, n, FAKE)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def route(lib, cls=B.RouteArgs, fn="moe_route", **kw):
+    base = dict(num_tokens=8, num_experts=16, top_k=2, logits_dtype=B.MOE_DTYPE_BF16,
+                logits_stride0=16, topk_ids_dtype=B.MOE_IDS_INT32)
+    base.update(dict(num_groups=1, top_groups=1) if cls is B.RouteArgs else
+                dict(d_logits_stride0=16))
+    base.update(kw)
+    return getattr(lib, fn)(fill(cls, **base), None)
+
+
+def test_route(lib):
+    assert lib.moe_route(None, None) == INVALID
+    assert route(lib, num_tokens=-1) == INVALID
+    assert route(lib, num_tokens=0) == OK
+    assert route(lib, top_k=0) == SHAPE
+    assert route(lib, top_k=17) == SHAPE
+    assert route(lib, num_experts=1025, logits_stride0=1025) == UNSUPPORTED
+    assert route(lib, num_experts=64, logits_stride0=64, top_k=33) == UNSUPPORTED
+    assert route(lib, logits_dtype=3) == INVALID
+    assert route(lib, scoring=2) == INVALID
+    assert route(lib, topk_ids_dtype=2) == INVALID
+    assert route(lib, num_groups=3) == SHAPE
+    assert route(lib, num_groups=0) == SHAPE
+    assert route(lib, num_groups=4, top_groups=5) == SHAPE
+    assert route(lib, num_groups=16, top_groups=1) == SHAPE  # two experts of one-expert groups
+    assert route(lib, num_experts=64, logits_stride0=64, num_groups=64, top_groups=8) == UNSUPPORTED
+    assert route(lib, logits_stride0=15) == SHAPE
+    assert route(lib, logits=None) == INVALID
+    assert route(lib, topk_weights=None) == INVALID
+    assert b"NULL" in lib.moe_last_error()
+    back = dict(cls=B.RouteBackwardArgs, fn="moe_route_backward")
+    assert route(lib, num_tokens=0, **back) == OK
+    assert lib.moe_last_error() == b""
+    assert route(lib, d_logits=None, **back) == INVALID
+    assert route(lib, d_logits_stride0=8, **back) == SHAPE
+    assert route(lib, top_k=33, num_experts=64, **back) == UNSUPPORTED
+
+
+def test_sort(lib):
+    def sort(ids=FAKE, dt=B.MOE_IDS_INT32, T=8, k=2, E=4, off=FAKE, rr=FAKE, ro=FAKE, ws=FAKE,
+             n=1 << 20):
+        return lib.moe_sort_routes(ids, dt, T, k, E, off, rr, ro, ws, n, None, None)
+    assert sort(T=-1) == INVALID
+    assert sort(dt=7) == INVALID
+    assert sort(E=0) == SHAPE
+    assert sort(E=1025) == UNSUPPORTED
+    assert sort(T=1 << 26, k=2) == UNSUPPORTED
+    assert sort(off=None) == INVALID
+    assert sort(ids=None) == INVALID
+    assert sort(T=100000, ws=None) == WORKSPACE
+    assert sort(T=100000, n=16) == WORKSPACE
+    assert sort(T=100000, ws=FAKE + 2) == ALIGNMENT
+    assert lib.moe_sort_workspace_size(64, 2, 8) == 0
+    assert lib.moe_sort_workspace_size(-1, 2, 8) == 0
+    assert lib.moe_sort_workspace_size(8192, 8, 256) > 0
+
+
+def test_rows(lib):
+    def permute(x=FAKE, xs=64, dt=B.MOE_DTYPE_BF16, T=4, K=64, k=2, rr=FAKE, off=FAKE, E=4,
+                rows=FAKE, rs=64, n=8):
+        return lib.moe_permute(x, xs, dt, T, K, k, rr, off, E, rows, rs, n, None)
+    assert permute(T=-1) == INVALID
+    assert permute(dt=9) == INVALID
+    assert permute(k=33) == UNSUPPORTED
+    assert permute(n=1 << 31) == UNSUPPORTED
+    assert permute(K=0) == OK and permute(n=0) == OK
+    assert permute(rows=None) == INVALID and permute(off=None) == INVALID
+    assert permute(x=None) == INVALID
+    assert permute(xs=63) == SHAPE and permute(rs=63) == SHAPE
+
+    def unpermute(rows=FAKE, rs=64, n=8, dt=0, rr=FAKE, w=FAKE, T=4, K=64, k=2, out=FAKE, os=64):
+        return lib.moe_unpermute(rows, rs, n, dt, rr, w, T, K, k, out, os, None)
+    assert unpermute(T=0) == OK
+    assert unpermute(out=None) == INVALID and unpermute(rr=None) == INVALID
+    assert unpermute(os=3) == SHAPE and unpermute(k=40) == UNSUPPORTED
+
+    def back(up=FAKE, us=64, rows=FAKE, rs=64, n=8, dt=0, rr=FAKE, w=FAKE, off=FAKE, E=4, T=4,
+             K=64, k=2, dr=FAKE, ds=64, dw=FAKE):
+        return lib.moe_unpermute_backward(up, us, rows, rs, n, dt, rr, w, off, E, T, K, k, dr, ds,
+                                          dw, None)
+    assert back(T=0, n=0) == OK
+    for name in ("up", "rows", "rr", "w", "off", "dr", "dw"):
+        assert back(**{name: None}) == INVALID
+    assert back(ds=1) == SHAPE and back(us=1) == SHAPE and back(dt=-1) == INVALID
+
+
+def norm(lib, cls=B.BlockNormArgs, fn="moe_block_norm", **kw):
+    base = dict(num_tokens=4, hidden_size=64, dtype=1, weight_dtype=1, gate_kind=1, gate_stride0=64)
+    base.update({n: 64 for n, _ in cls._fields_ if n.endswith("stride0")})
+    if cls is B.BlockNormBackwardArgs:
+        base["workspace_bytes"] = 1 << 20
+    base.update(kw)
+    return getattr(lib, fn)(fill(cls, **base), None)
+
+
+def test_block_norm(lib):
+    assert lib.moe_block_norm(None, None) == INVALID
+    assert norm(lib, num_tokens=0) == OK
+    assert norm(lib, hidden_size=-1) == INVALID
+    assert norm(lib, hidden_size=16385) == UNSUPPORTED
+    assert norm(lib, dtype=4) == INVALID and norm(lib, weight_dtype=-1) == INVALID
+    assert norm(lib, gate_kind=4) == INVALID
+    assert norm(lib, gate_kind=0) == INVALID and norm(lib, gate=None) == INVALID
+    assert norm(lib, x=None) == INVALID
+    assert norm(lib, z=None) == INVALID and norm(lib, x_out=None) == INVALID
+    assert norm(lib, y=None) == INVALID and norm(lib, pre_weight=None) == INVALID
+    assert norm(lib, y_stride0=8) == SHAPE and norm(lib, z_stride0=8) == SHAPE
+    back = dict(cls=B.BlockNormBackwardArgs, fn="moe_block_norm_backward")
+    assert norm(lib, hidden_size=0, **back) == OK
+    assert norm(lib, x=None, **back) == INVALID and norm(lib, d_x=None, **back) == INVALID
+    assert norm(lib, rstd_pre=None, **back) == INVALID
+    assert norm(lib, rstd_post=None, **back) == INVALID
+    assert norm(lib, z=None, **back) == INVALID
+    assert norm(lib, pre_weight=None, **back) == INVALID
+    assert norm(lib, gate=None, gate_kind=0, **back) == INVALID  # d_gate without a gate
+    assert norm(lib, d_z_stride0=1, **back) == SHAPE
+    assert norm(lib, workspace=None, **back) == WORKSPACE
+    assert norm(lib, workspace_bytes=64, **back) == WORKSPACE
+    assert norm(lib, workspace=FAKE + 4, **back) == ALIGNMENT
+    assert lib.moe_block_norm_workspace_size(0, 64) == 0
+    assert lib.moe_block_norm_workspace_size(4, 64) > 0
+
+
+def test_lora(lib):
+    def lora(**kw):
+        base = dict(num_tokens=4, in_features=64, out_features=32, num_adapters=2, rank=8,
+                    dtype=B.MOE_DTYPE_BF16, x_stride0=64, out_stride0=32, workspace_bytes=1 << 20)
+        base.update(kw)
+        return lib.moe_lora_linear(fill(B.LoraArgs, **base), None)
+    assert lib.moe_lora_linear(None, None) == INVALID
+    assert lora(num_tokens=0) == OK and lora(out_features=0) == OK
+    assert lora(rank=-8) == INVALID
+    assert lora(dtype=B.MOE_DTYPE_FP32) == UNSUPPORTED and lora(dtype=5) == INVALID
+    assert lora(in_features=0) == SHAPE and lora(rank=0) == SHAPE
+    assert lora(rank=136) == UNSUPPORTED and lora(num_adapters=4097) == UNSUPPORTED
+    for name in ("x", "weight", "out", "lora_a", "lora_b", "adapter_ids", "lora_scale"):
+        assert lora(**{name: None}) == INVALID
+    assert lora(x_stride0=63) == SHAPE and lora(out_stride0=31) == SHAPE
+    assert lora(in_features=60) == ALIGNMENT and lora(rank=12) == ALIGNMENT
+    assert lora(x=FAKE + 8) == ALIGNMENT and lora(lora_b=FAKE + 2) == ALIGNMENT
+    assert lora(x_stride0=68) == ALIGNMENT
+    assert lora(workspace=None) == WORKSPACE and lora(workspace_bytes=8) == WORKSPACE
+    assert lora(workspace=FAKE + 4) == ALIGNMENT
+    assert lora(out_features=1 << 30, out_stride0=1 << 30) == UNSUPPORTED
+    assert lib.moe_lora_workspace_size(4, 64, 32, 0, 8) == 0
+    assert lib.moe_lora_workspace_size(4, 64, 32, 2, 8) > 0

@@ -1,0 +1,186 @@
+"""moe_lora_linear against its formula in 64 bits."""
+import ctypes
+import time
+
+import pytest
+import torch
+
+from moe_expert_layer_prepare_gb300 import binding as B
+from tests._block_util import DTYPES, assert_within, rounded, strided
+from tests._util import need_cuda
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def cuda():
+    need_cuda()
+    from moe_expert_layer_prepare_gb300 import build
+    build.build()
+    B.load()
+
+
+def problem(T, K, N, S, R, dtype, seed=0, order="mixed", layout="plain"):
+    g = torch.Generator(device="cuda").manual_seed(seed + T + K + N)
+    dt = DTYPES[dtype]
+
+    def rnd(*shape, std=1.0):
+        return (torch.randn(shape, generator=g, device="cuda") * std).to(dt)
+
+    ids = torch.randint(-1, S, (T,), generator=g, device="cuda", dtype=torch.int32)
+    if order == "sorted":
+        ids = ids.sort().values
+    elif order == "none":
+        ids.fill_(-1)
+    x = rnd(T, K)
+    out = torch.full((T, N), float("nan"), dtype=dt, device="cuda")
+    if layout != "plain":
+        x = strided(x, 8)
+        out = strided(out, 3, 1)
+    a = rnd(S, R, K, std=K ** -0.5)
+    b = rnd(S, N, R, std=max(R, 1) ** -0.5)
+    return dict(x=x, weight=rnd(N, K, std=K ** -0.5), lora_a=a, lora_b=b, adapter_ids=ids,
+                lora_scale=torch.rand(S, generator=g, device="cuda") * 2, out=out)
+
+
+def run(p, status=None, stream=None):
+    T, K = p["x"].shape
+    S, R = p["lora_a"].shape[:2] if p["lora_a"] is not None else (0, 0)
+    ws = torch.full((max(16, B.lora_workspace_size(T, K, p["weight"].shape[0], S, R)),), 0xFF,
+                    dtype=torch.uint8, device="cuda")
+    B.moe_lora_linear(workspace=ws, device_status=status, stream=stream, **p)
+    return p["out"]
+
+
+def expect(p):
+    """(value, bound of the fp32 sums' error) in fp64, adapter by adapter."""
+    x, w = p["x"].cpu().double(), p["weight"].cpu().double()
+    ref, mag = x @ w.t(), x.abs() @ w.abs().t()
+    if p["lora_a"] is not None:
+        ids = p["adapter_ids"].cpu()
+        for s in range(p["lora_a"].shape[0]):
+            at = (ids == s).nonzero()[:, 0]
+            if not len(at):
+                continue
+            a, b = p["lora_a"][s].cpu().double(), p["lora_b"][s].cpu().double()
+            c = p["lora_scale"][s].item()
+            ref[at] += c * ((x[at] @ a.t()) @ b.t())
+            mag[at] += c * ((x[at].abs() @ a.abs().t()) @ b.abs().t())
+    # fp32 accumulation, and s h as a 16-bit value and its 16-bit remainder (2^-17 for bf16)
+    return ref, mag * 2.0 ** -16
+
+
+def check(p, **kw):
+    out = run(p, **kw)
+    ref, extra = expect(p)
+    assert_within(out, ref, rounded(ref, out.dtype, extra), "out")
+
+
+# token counts around every tile, features and K that fill no tile, ranks with one and two parts
+@pytest.mark.parametrize("T,K,N,S,R", [
+    (1, 8, 1, 1, 8), (1, 7168, 512, 8, 16), (2, 72, 100, 3, 24), (15, 64, 128, 3, 8),
+    (16, 1000, 257, 20, 16), (17, 512, 130, 5, 32), (33, 2048, 384, 40, 32),
+    (64, 256, 129, 70, 40), (65, 320, 300, 4, 64), (128, 4096, 256, 9, 72),
+    (129, 136, 64, 3, 128), (257, 264, 140, 6, 16), (300, 1032, 260, 30, 48),
+    (700, 512, 512, 2, 128), (1500, 192, 72, 100, 8)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("order", ["mixed", "sorted"])
+def test_against_the_formula(T, K, N, S, R, dtype, order):
+    check(problem(T, K, N, S, R, dtype, order=order))
+
+
+@pytest.mark.parametrize("T", [3, 40, 200])
+def test_strides_and_no_adapter(T):
+    check(problem(T, 520, 200, 4, 16, "bf16", layout="strided"))
+    check(problem(T, 520, 200, 4, 16, "bf16", order="none"))
+    p = problem(T, 520, 200, 4, 16, "fp16")
+    p.update(lora_a=None, lora_b=None, adapter_ids=None, lora_scale=None)
+    check(p)
+
+
+def test_every_token_its_own_adapter():
+    p = problem(64, 512, 256, 64, 16, "bf16")
+    p["adapter_ids"] = torch.randperm(64, device="cuda").to(torch.int32)
+    check(p)
+    p = problem(300, 128, 128, 300, 8, "bf16")
+    p["adapter_ids"] = torch.arange(300, device="cuda", dtype=torch.int32)
+    check(p)
+
+
+def test_ids_out_of_range_and_nan_in_unused_adapters():
+    p = problem(30, 256, 200, 5, 16, "bf16")
+    p["adapter_ids"][3] = 5
+    p["adapter_ids"][4] = 2 ** 31 - 1
+    p["adapter_ids"][p["adapter_ids"] == 2] = -7
+    p["lora_a"][2] = float("nan")
+    p["lora_b"][2] = float("nan")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = run(p, status=st)
+    q = dict(p, adapter_ids=torch.where(p["adapter_ids"] >= 5, -1, p["adapter_ids"]))
+    ref, extra = expect(q)
+    assert_within(out, ref, rounded(ref, out.dtype, extra), "out")
+    assert int(st.item()) == B.MOE_DEV_BAD_ADAPTER
+
+
+def test_stream_and_same_bits_twice():
+    p = problem(50, 1024, 512, 12, 32, "bf16")
+    first = run(p).clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    p["out"].zero_()
+    torch.cuda.synchronize()
+    run(p, stream=s)
+    s.synchronize()
+    assert torch.equal(first, p["out"])
+
+
+def test_back_to_back_calls_share_a_workspace():
+    ps = [problem(T, 512, 384, 6, 16, "bf16", seed=T) for T in (40, 33, 64, 7)]
+    ws = torch.empty(max(B.lora_workspace_size(p["x"].shape[0], 512, 384, 6, 16) for p in ps),
+                     dtype=torch.uint8, device="cuda")
+    for _ in range(5):
+        for p in ps:
+            B.moe_lora_linear(workspace=ws, **p)
+    torch.cuda.synchronize()
+    for p in ps:
+        ref, extra = expect(p)
+        assert_within(p["out"], ref, rounded(ref, p["out"].dtype, extra), "out")
+
+
+def test_refusals():
+    p = problem(4, 64, 32, 2, 8, "bf16")
+    with pytest.raises(ValueError):
+        run(dict(p, out=p["out"].float()))
+    with pytest.raises(ValueError):
+        run(dict(p, weight=p["weight"].t().contiguous().t()))
+    with pytest.raises(B.MoeError) as e:
+        B.moe_lora_linear(workspace=None, **p)
+    assert e.value.status == 5
+    q = {k: (v.float() if v.is_floating_point() else v) for k, v in p.items()}
+    with pytest.raises(B.MoeError) as e:
+        run(q)
+    assert e.value.status == 3
+    with pytest.raises(B.MoeError) as e:
+        run(problem(4, 60, 32, 2, 8, "bf16"))
+    assert e.value.status == 4
+
+
+def test_wait_timeout_sets_status_and_context_survives():
+    """The test build's CTA 0 issues no slab after its first, so the MMA warp's wait on it runs
+    out after 5 ms; the CTA drains what it issued and returns, alone and inside a cluster."""
+    from moe_expert_layer_prepare_gb300 import build
+    test_lib = B.configure(ctypes.CDLL(build.build_test_variant("timeout")))
+    regular = B.load()
+    for T, N in ((8, 256), (300, 20000)):  # eight CTAs share a tile's K; one each
+        p = problem(T, 2048, N, 3, 16, "bf16")
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        B._lib = test_lib
+        try:
+            t0 = time.perf_counter()
+            run(p, status=st)
+            torch.cuda.synchronize()
+            assert time.perf_counter() - t0 < 5.0
+        finally:
+            B._lib = regular
+        assert int(st.item()) & B.MOE_DEV_TIMEOUT
+        check(p)

@@ -1,0 +1,226 @@
+"""moe_route and moe_route_backward against their formulas in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+from moe_expert_layer_prepare_gb300 import binding as B
+from tests._block_util import DTYPES, HALF_ULP, assert_within, rounded
+from tests._util import need_cuda
+
+pytestmark = pytest.mark.gpu
+SCORING = {"softmax": B.MOE_SCORE_SOFTMAX, "sigmoid": B.MOE_SCORE_SIGMOID}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def cuda():
+    need_cuda()
+    from moe_expert_layer_prepare_gb300 import build
+    build.build()
+    B.load()
+
+
+def select(l, bias, scoring, k, groups, top_groups):
+    """ids of the definition, row by row (l: fp32 numpy [T, E])."""
+    T, E = l.shape
+    key = l.astype(np.float32)
+    if bias is not None:
+        if scoring == "sigmoid":
+            with np.errstate(over="ignore"):
+                key = (np.float32(1) / (np.float32(1) + np.exp(-key))).astype(np.float32)
+        key = (key + bias).astype(np.float32)
+    ids = np.full((T, k), -1, np.int64)
+    size = E // groups
+    for t in range(T):
+        ok = [e for e in range(E) if key[t, e] > -np.inf]
+        if groups > 1:
+            value = {}
+            for g in range(groups):
+                mine = sorted((key[t, e] for e in ok if e // size == g), reverse=True)
+                if mine:
+                    second = mine[1] if len(mine) > 1 else np.float32(0)
+                    value[g] = mine[0] if bias is None else np.float32(mine[0] + second)
+            best = sorted(value, key=lambda g: (-value[g], g))[:top_groups]
+            ok = [e for e in ok if e // size in best]
+        taken = sorted(ok, key=lambda e: (-key[t, e], e))[:k]
+        ids[t, :len(taken)] = taken
+    return ids
+
+
+def weights64(l, ids, scoring, renorm, scale):
+    """Weights in fp64 of logits l (fp64 tensor, may require grad) with the selection given."""
+    taken = ids >= 0
+    at = l.gather(1, ids.clamp_min(0))
+    if scoring == "sigmoid":
+        s = torch.where(taken, torch.sigmoid(at), torch.zeros_like(at))
+        w = s / (s.sum(dim=1, keepdim=True) + 1e-20) if renorm else s
+    else:
+        # exponentials relative to the largest logit in the sum; rows that take nothing give 0
+        if renorm:
+            pool, mine = at, taken
+        else:
+            pool, mine = l, l > -float("inf")
+        some = taken.any(dim=1, keepdim=True)
+        mine = mine & some
+        ninf = torch.full_like(pool, -float("inf"))
+        m = torch.where(mine, pool, ninf).amax(dim=1, keepdim=True).detach()
+        m = torch.where(some, m, torch.zeros_like(m))
+
+        def ex(v, use):
+            return torch.where(use, torch.exp(torch.where(use, v - m, torch.zeros_like(v))),
+                               torch.zeros_like(v))
+        total = ex(pool, mine).sum(dim=1, keepdim=True)
+        w = ex(at, taken) / torch.where(some, total, torch.ones_like(total))
+    return w * scale
+
+
+def route(l, k, scoring="softmax", renorm=True, scale=1.0, bias=None, pad=None, groups=1,
+          top_groups=1, ids_dtype=torch.int32):
+    T = l.shape[0]
+    ids = torch.full((T, k), 77, dtype=ids_dtype, device="cuda")
+    w = torch.full((T, k), 77.0, device="cuda")
+    B.moe_route(l, ids, w, bias=bias, is_padding=pad, scoring=SCORING[scoring],
+                renormalize=renorm, scale=scale, num_groups=groups, top_groups=top_groups)
+    return ids, w
+
+
+CASES = [(1, 1, 1), (3, 5, 5), (7, 8, 2), (9, 32, 32), (65, 33, 4), (40, 100, 8), (130, 256, 8),
+         (17, 300, 7), (5, 1000, 32)]
+
+
+@pytest.mark.parametrize("T,E,k", CASES)
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("scoring,renorm", [("softmax", True), ("softmax", False),
+                                            ("sigmoid", True), ("sigmoid", False)])
+def test_forward_and_gradient(T, E, k, dtype, scoring, renorm):
+    g = torch.Generator().manual_seed(T * 1000 + E)
+    l = (torch.randn(T, E, generator=g) * 2).to(DTYPES[dtype])  # 16-bit logits tie often
+    pad = (torch.rand(T, generator=g) < 0.2).to(torch.uint8)
+    ids, w = route(l.cuda(), k, scoring, renorm, 1.7, pad=pad.cuda())
+    want = select(l.float().numpy(), None, scoring, k, 1, 1)
+    want[pad.numpy() != 0] = -1
+    assert np.array_equal(ids.cpu().numpy(), want)
+    l64 = l.double().requires_grad_(True)
+    wid = torch.from_numpy(want)
+    ref = weights64(l64, wid, scoring, renorm, 1.7)
+    # exp and the quotient: a few units in the last place of fp32, the sum's E of them
+    assert_within(w, ref.detach(), ref.detach().abs() * (E + 16) * 2.0 ** -24 + 1e-30, "weights")
+
+    dw = torch.randn(T, k, generator=g)
+    dl = torch.full((T, E), 77.0, dtype=l.dtype, device="cuda")
+    B.moe_route_backward(l.cuda(), ids, dw.cuda(), dl, scoring=SCORING[scoring],
+                         renormalize=renorm, scale=1.7)
+    (ref * dw.double()).sum().backward()
+    mag = 1.7 * dw.abs().double().sum(dim=1, keepdim=True).expand(T, E)
+    assert_within(dl, l64.grad, rounded(l64.grad, l.dtype, mag * (E + 32) * 2.0 ** -24),
+                  "d_logits")
+    assert bool((dl[pad.cuda() != 0] == 0).all())
+
+
+@pytest.mark.parametrize("E,groups,top_groups,k", [(256, 8, 4, 8), (96, 4, 1, 5), (60, 3, 2, 6),
+                                                   (64, 32, 16, 8), (40, 5, 5, 8), (1024, 8, 3, 32)])
+@pytest.mark.parametrize("scoring,with_bias", [("sigmoid", True), ("softmax", True),
+                                               ("softmax", False), ("sigmoid", False)])
+def test_groups_and_bias(E, groups, top_groups, k, scoring, with_bias):
+    T = 50
+    g = torch.Generator().manual_seed(E + groups)
+    l = torch.randn(T, E, generator=g)
+    # a coarse grid: keys tie often, and no two differ by less than exp's rounding
+    l = torch.round(l * 4) / 4
+    bias = torch.round(torch.randn(E, generator=g) * 4) / 64 if with_bias else None
+    ids, w = route(l.cuda(), k, scoring, True, 2.5, groups=groups, top_groups=top_groups,
+                   bias=None if bias is None else bias.cuda(), ids_dtype=torch.int64)
+    got = ids.cpu().numpy()
+    if scoring == "sigmoid" and with_bias:
+        # the key's exp is the GPU's: take the keys from the same elementary operations there
+        key = (1.0 / (1.0 + torch.exp(-l.cuda())) + bias.cuda()).cpu().numpy()
+        want = select(key, None, "softmax", k, 1, 1) if groups == 1 else \
+            select(key, np.zeros(E, np.float32), "softmax", k, groups, top_groups)
+    else:
+        want = select(l.numpy(), None if bias is None else bias.numpy(), scoring, k, groups,
+                      top_groups)
+    assert np.array_equal(got, want)
+    ref = weights64(l.double(), torch.from_numpy(want), scoring, True, 2.5)
+    assert_within(w, ref, ref.abs() * (E + 16) * 2.0 ** -24 + 1e-30, "weights")
+
+
+@pytest.mark.parametrize("scoring,renorm", [("softmax", True), ("softmax", False),
+                                            ("sigmoid", True), ("sigmoid", False)])
+def test_masked_and_extreme_logits(scoring, renorm):
+    inf, nan = float("inf"), float("nan")
+    low = torch.finfo(torch.float32).min
+    rows = [[-inf] * 8, [nan] * 8, [-inf, 1.0, -inf, nan, 0.5, -inf, nan, -inf],
+            [low] * 8, [low, 0.0, low, 1.0, low, low, low, low], [0.0, -0.0, 0.0, -0.0] * 2,
+            [inf, 0.0, inf, 1.0, 2.0, -inf, nan, 3.0], [3e38, 3e38, 1.0, 0.0, 0.0, 0.0, 0.0, 0.0],
+            [-200.0, -300.0, -250.0, low, low, low, low, low]]
+    l = torch.tensor(rows)
+    ids, w = route(l.cuda(), 4, scoring, renorm)
+    want = select(l.numpy(), None, scoring, 4, 1, 1)
+    assert np.array_equal(ids.cpu().numpy(), want)
+    w = w.cpu()
+    assert bool(torch.isfinite(w).all())
+    assert bool((w[torch.from_numpy(want) < 0] == 0).all())
+    finite = [r for r in range(len(rows)) if r != 6]
+    ref = weights64(l[finite].double(), torch.from_numpy(want[finite]), scoring, renorm, 1.0)
+    assert_within(w[finite], ref, ref.abs() * 1e-5 + 1e-30, "weights")
+    if scoring == "softmax":  # infinite logits share the weight
+        assert w[6].tolist() == [0.5, 0.5, 0.0, 0.0]
+    dw = torch.ones(len(rows), 4)
+    dl = torch.full((len(rows), 8), 77.0, device="cuda")
+    B.moe_route_backward(l.cuda(), ids, dw.cuda(), dl, scoring=SCORING[scoring],
+                         renormalize=renorm)
+    assert bool(torch.isfinite(dl).all())
+    assert bool((dl[0] == 0).all()) and bool((dl[1] == 0).all())
+
+
+def test_strided_logits_other_stream_and_no_tokens():
+    g = torch.Generator(device="cuda").manual_seed(3)
+    wide = torch.randn(20, 70, generator=g, device="cuda")
+    part = wide[:, 3:67]
+    s = torch.cuda.Stream()
+    ids = torch.empty(20, 6, dtype=torch.int32, device="cuda")
+    w = torch.empty(20, 6, device="cuda")
+    s.wait_stream(torch.cuda.current_stream())
+    B.moe_route(part, ids, w, stream=s)
+    s.synchronize()
+    ids2, w2 = route(part.contiguous(), 6)
+    assert torch.equal(ids, ids2) and torch.equal(w, w2)
+    route(torch.empty(0, 8, device="cuda"), 2)
+
+
+def test_gradient_against_differences():
+    # logits 0.2 apart or more keep the selection under steps of 1e-2
+    g = torch.Generator().manual_seed(5)
+    T, E, k, h = 6, 12, 4, 1e-2
+    l = torch.stack([torch.randperm(E, generator=g).float() * 0.25 for _ in range(T)])
+    c = torch.randn(T, k, generator=g)
+    v = torch.randn(T, E, generator=g).clamp(-2, 2)
+    for scoring in SCORING:
+        for renorm in (True, False):
+            def loss(x):
+                return (route(x.cuda(), k, scoring, renorm)[1].cpu().double() * c).sum(dim=1)
+            num = (loss(l + h * v) - loss(l - h * v)) / (2 * h)
+            ids, _ = route(l.cuda(), k, scoring, renorm)
+            dl = torch.empty(T, E, device="cuda")
+            B.moe_route_backward(l.cuda(), ids, c.cuda(), dl, scoring=SCORING[scoring],
+                                 renormalize=renorm)
+            ana = (dl.cpu().double() * v).sum(dim=1)
+            # truncation h^2 |v|^3 |c| / 6 and the forward's rounding over h
+            size = c.abs().sum(dim=1).double()
+            bound = size * (h * h * 8 + 32 * HALF_ULP[torch.float32] / h)
+            assert_within(ana, num, bound, f"{scoring} {renorm}")
+
+
+def test_refusals():
+    l = torch.randn(4, 8, device="cuda")
+    ids = torch.empty(4, 2, dtype=torch.int32, device="cuda")
+    w = torch.empty(4, 2, device="cuda")
+    with pytest.raises(ValueError):
+        B.moe_route(l, ids, w.half())
+    with pytest.raises(ValueError):
+        B.moe_route(l, ids.float(), w)
+    with pytest.raises(ValueError):
+        B.moe_route(l.t(), torch.empty(8, 2, dtype=torch.int32, device="cuda"),
+                    torch.empty(8, 2, device="cuda"))
+    with pytest.raises(B.MoeError) as e:
+        B.moe_route(l, ids, w, num_groups=3)
+    assert e.value.status == 2
