@@ -250,14 +250,15 @@ __global__ void __launch_bounds__(256) unpermute_kernel(RowParams p) {
       for (int i = 0; i < 8; ++i) {
         const float w = __shfl_sync(0xFFFFFFFFu, my_w, (j0 + i) & 31);
         if (row[i] < 0 || !active) continue;
+        float f[VEC];
+        v[i].get(f);
 #pragma unroll
-        for (int q = 0; q < VEC; ++q) acc[q] = fmaf(w, to_f32(v[i].v[q]), acc[q]);
+        for (int q = 0; q < VEC; ++q) acc[q] = fmaf(w, f[q], acc[q]);
       }
     }
     if (active) {
       Pack<T, VEC> o;
-#pragma unroll
-      for (int q = 0; q < VEC; ++q) o.v[q] = from_f32<T>(acc[q]);
+      o.set(acc);
       store_pack<T, VEC>(static_cast<T*>(p.out) + t * p.out_stride + c0, o);
     }
   }
@@ -299,7 +300,8 @@ __global__ void __launch_bounds__(BACK_THREADS) unpermute_backward_kernel(RowPar
         dot[i] = 0.0f;
       }
       for (int64_t c = (int64_t)tid * VEC; c < p.K; c += BACK_THREADS * VEC) {
-        const Pack<T, VEC> g = load_pack<T, VEC>(up + c);
+        float g[VEC];
+        load_pack<T, VEC>(up + c).get(g);
         Pack<T, VEC> v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -308,13 +310,15 @@ __global__ void __launch_bounds__(BACK_THREADS) unpermute_backward_kernel(RowPar
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           if (row[i] < 0) continue;
-          Pack<T, VEC> o;
+          float f[VEC], wg[VEC];
+          v[i].get(f);
 #pragma unroll
           for (int q = 0; q < VEC; ++q) {
-            const float gf = to_f32(g.v[q]);
-            dot[i] = fmaf(gf, to_f32(v[i].v[q]), dot[i]);
-            o.v[q] = from_f32<T>(w[i] * gf);
+            dot[i] = fmaf(g[q], f[q], dot[i]);
+            wg[q] = w[i] * g[q];
           }
+          Pack<T, VEC> o;
+          o.set(wg);
           store_pack<T, VEC>(d_rows + (int64_t)row[i] * p.out_rows_stride + c, o);
         }
       }
