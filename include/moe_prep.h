@@ -636,15 +636,16 @@ size_t moe_block_norm_workspace_size(int64_t num_tokens, int64_t hidden_size);
 /*   h[t, r] = sum_k x[t, k] * lora_a[a, r, k],  a = adapter_ids[t];          */
 /* tokens with a < 0 (no adapter; a >= num_adapters also sets                 */
 /* MOE_DEV_BAD_ADAPTER) take the first sum alone.  Sums are in fp32; scale*h  */
-/* enters the second product as two values of the tensors' type (its rounding */
-/* and the remainder), out is rounded once.                                   */
+/* enters the second product in fp32, or for long batches as two values of    */
+/* the tensors' type (its rounding and the remainder); out is rounded once.   */
+/* An adapter's values, non-finite ones too, reach its own tokens alone.      */
 /* x [T, K] and out [T, N]: inner stride 1, row strides of their own; weight  */
 /* [N, K], lora_a [S, R, K], lora_b [S, N, R] contiguous; adapter_ids int32   */
 /* [T]; lora_scale fp32 [S]; bf16 or fp16.  An adapter of lower rank than R   */
 /* has zero rows in lora_a.  num_adapters == 0: the projection alone.         */
 /* workspace: moe_lora_workspace_size() bytes, need not be cleared.           */
 /* Errors: K % 8, R % 8, x_stride0 % 8 != 0, x, weight, lora_a, lora_b not    */
-/* 16-byte aligned -> ALIGNMENT; R > 128, num_adapters > 4096, fp32 ->        */
+/* 16-byte aligned -> ALIGNMENT; R > 128, num_adapters > 1023, fp32 ->        */
 /* UNSUPPORTED.  A GEMM wait that ran out sets MOE_DEV_TIMEOUT.               */
 /* ------------------------------------------------------------------------ */
 typedef struct moe_lora_args {

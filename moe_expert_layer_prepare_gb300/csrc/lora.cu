@@ -1,26 +1,35 @@
 // A projection shared by all tokens plus each token's own low-rank adapter:
 //   out = x W^T + s_a (x A_a^T) B_a^T.
 //
-// Two launches.  The first, lora_shrink_kernel, gives h = x A_a^T as fp32 sums
-// per share of K.  It reads A and the rows of x, a few flops a byte, so it
-// runs on mma.sync tiles fed by cp.async; blocks take (64 tokens, share of K,
-// share of the adapters among these tokens).
+// lora_shrink_kernel gives h = x A_a^T as fp32 sums per share of K.  It reads A
+// and the rows of x, a few flops a byte, so it runs on mma.sync tiles fed by
+// cp.async; blocks take (64 tokens, share of K, share of the adapters among them).
 //
-// The second, lora_gemm_kernel, is the projection on tcgen05, features by
-// tokens: the accumulator's 128 rows are features (the MMA's A operand is a
-// weight tile) and its columns a tile of tokens, so that a single token costs a
-// 16-column tile and a decode batch streams W once.  K slabs of 64 come by TMA
-// through a ring of shared-memory stages.  After them the adapters of the tile's
-// tokens enter the same accumulator, one K step of the MMA per 16 ranks: B_a's
-// rows by TMA as the A operand, and as the B operand a tile of s_a h with zeros
-// in the rows of tokens that have another adapter, which the warps that later
-// run the epilogue write during the main loop.  h is in fp32; as the MMA takes 16-bit operands
-// s_a h enters as its rounding and the rounded remainder, which keeps the
-// adapters' part as exact as the rest.
+// The projection is on tcgen05, features by tokens: the accumulator's rows are
+// features (the MMA's A operand is a weight tile) and its columns tokens, so that
+// a single token costs a 16-column tile.  K slabs of 64 come by TMA through a ring
+// of shared-memory stages.
 //
-// With few tiles (decode) the K slabs are dealt out to the CTAs of a cluster and
-// their sums joined through distributed shared memory in rank order.  The second
-// launch starts while the first still runs and waits for it only where h is read.
+//   Up to SPLIT_TOKENS tokens (lora_split_kernel): W is streamed once or a few
+//   times, so HBM bounds it.  With few tiles the K slabs are dealt out to the CTAs of
+//   a cluster and the sums joined through distributed shared memory in rank order.
+//   The adapters' second product, R products for each (token, feature), is done in
+//   fp32 by the threads that join, each reading its feature's row of B_a.
+//
+//   Above (lora_pair_kernel): the tensor cores bound it.  CTA pairs keep 256 x 256
+//   tiles and two accumulators, one in use while the other is written out.  Tokens
+//   are taken in the order of their adapters (a counting sort of the ids), every
+//   adapter from a multiple of RUN tokens on: rows that lie together in x are read
+//   there, others from a copy that the shrink writes in that order.  A tile's
+//   columns are then runs of one adapter each, and the second product enters the
+//   accumulator as further K steps on the columns of a run alone: B_a's rows as the A
+//   operand, s_a h as the B operand.  So an adapter's values reach its own tokens only
+//   (a non-finite weight stays with them).  As the MMA takes 16-bit operands, s_a h
+//   enters as its rounding and the rounded remainder, which keeps the adapters' part as
+//   exact as the rest.
+//
+// The projection's launch starts while the shrink still runs and waits for it only
+// where h is read.
 #include <mutex>
 
 #include "block_common.cuh"
@@ -31,14 +40,19 @@ namespace moe {
 using namespace tc;
 
 constexpr int LORA_MAX_RANK = 128;
-constexpr int LORA_MAX_ADAPTERS = 4096;
+constexpr int LORA_MAX_ADAPTERS = 1023;  // the counting sort's bins, less one
+constexpr int RUN = 32;  // an adapter's tokens begin at multiples of this: the pair MMA's N step
 
 struct LoraParams {
   int64_t T, N, K, S, R;
   const void* x;
   int64_t x_stride;
   const void* a;
+  const void* b;
   const int32_t* ids;
+  const int32_t* order;  // nullable: tokens in the order of their adapters, -1 between
+  const int32_t* places;  // of order, in use (device)
+  void* xs;               // x's rows in that order, where they do not lie together in x
   const float* scale;
   void* out;
   int64_t out_stride;
@@ -51,7 +65,7 @@ struct LoraParams {
 };
 
 __device__ __forceinline__ int adapter_of(const LoraParams& p, int64_t t, bool* bad) {
-  const int a = t < p.T ? p.ids[t] : -1;
+  const int a = t >= 0 && t < p.T ? p.ids[t] : -1;
   if (a >= p.S) *bad = true;
   return a >= 0 && a < p.S ? a : -1;
 }
@@ -118,16 +132,30 @@ __device__ __forceinline__ uint32_t tile_at(int row, int piece) {
   return (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4));
 }
 
+// Whether the RUN places of a group, one a lane (-1: no token), hold tokens that
+// follow one another, so that one copy fetches their rows.
+__device__ __forceinline__ bool group_together(int tok) {
+  const int first = __shfl_sync(0xFFFFFFFFu, tok, 0);
+  return __all_sync(0xFFFFFFFFu, tok < 0 || tok == first + (int)(threadIdx.x & 31));
+}
+
 template <typename T>
 __global__ void __launch_bounds__(SH_THREADS) lora_shrink_kernel(LoraParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int16_t s_id[SH_TOK], s_first[SH_TOK], s_list[SH_TOK];
+  __shared__ int32_t s_tok[SH_TOK];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   pdl_launch_dependents();
   const int64_t t0 = (int64_t)blockIdx.x * SH_TOK;
+  if (p.order != nullptr && t0 >= *p.places) return;
   bool bad = false;
-  if (tid < SH_TOK) s_id[tid] = (int16_t)adapter_of(p, t0 + tid, &bad);
+  if (tid < SH_TOK) {
+    int64_t t = t0 + tid;
+    if (p.order != nullptr) t = t < *p.places ? p.order[t] : -1;
+    s_tok[tid] = (int32_t)t;
+    s_id[tid] = (int16_t)adapter_of(p, t, &bad);
+  }
   if (bad) set_status(p.status, MOE_DEV_BAD_ADAPTER);
   __syncthreads();
   const int n_list = distinct_adapters(s_id, s_first, s_list, SH_TOK, tid, SH_THREADS,
@@ -141,23 +169,51 @@ __global__ void __launch_bounds__(SH_THREADS) lora_shrink_kernel(LoraParams p) {
   const T* x = static_cast<const T*>(p.x);
   const int m0 = (warp & 3) * 16, nh = warp >> 2;
 
+  if (p.order != nullptr && blockIdx.z == 0) {
+    // this share of the rows that the projection cannot fetch as they lie in x
+    T* xs = static_cast<T*>(p.xs);
+    for (int r = warp; r < SH_TOK; r += SH_THREADS / 32) {
+      const int tok = s_tok[r];
+      const bool apart = !group_together(s_tok[(r & ~(RUN - 1)) + lane]);
+      if (tok < 0 || !apart) continue;
+      const T* src = x + tok * p.x_stride;
+      T* dst = xs + (t0 + r) * p.K;
+      for (int64_t k = k0 + lane * 8; k < k1; k += 256)
+        store_pack<T, 8>(dst + k, load_pack<T, 8>(src + k));
+    }
+  }
+
+  // a thread's pieces: 16-byte piece c of rows row, row + 32, ...
+  const int row = tid >> 3, c = tid & 7;
+  const uint32_t at = base + tile_at(row, c);
   for (int d = blockIdx.z; d < n_list; d += gridDim.z) {
     const int a = s_list[d];
     const T* A = static_cast<const T*>(p.a) + (int64_t)a * R * p.K;
+    const T *xp[2], *ap[4];
+    uint32_t take = 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const bool t = s_id[row + 32 * j] == a;
+      xp[j] = t ? x + s_tok[row + 32 * j] * p.x_stride + k0 + c * 8 : x;
+      take |= (uint32_t)t << j;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool t = row + 32 * j < R;
+      ap[j] = t ? A + (int64_t)(row + 32 * j) * p.K + k0 + c * 8 : A;
+      take |= (uint32_t)t << (2 + j);
+    }
     auto load = [&](int slab) {
-      const uint32_t s = base + (slab % SH_STAGES) * stage_bytes;
-      const int64_t k = k0 + (int64_t)slab * 64;
-      for (int i = tid; i < SH_TOK * 8; i += SH_THREADS) {
-        const int r = i >> 3, c = i & 7;
-        const bool take = s_id[r] == a && k + c * 8 < k1;
-        cp_async16(s + tile_at(r, c), take ? x + (t0 + r) * p.x_stride + k + c * 8 : x, take);
-      }
-      for (int i = tid; i < r16 * 8; i += SH_THREADS) {
-        const int r = i >> 3, c = i & 7;
-        const bool take = r < R && k + c * 8 < k1;
-        cp_async16(s + SH_X_BYTES + tile_at(r, c), take ? A + (int64_t)r * p.K + k + c * 8 : A,
-                   take);
-      }
+      const uint32_t s = at + (uint32_t)(slab % SH_STAGES) * stage_bytes;
+      const uint32_t t = k0 + (int64_t)slab * 64 + c * 8 < k1 ? take : 0u;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        cp_async16(s + j * 4096, xp[j] + ((t >> j) & 1u ? slab * 64 : 0), (t >> j) & 1u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (row + 32 * j < r16)
+          cp_async16(s + SH_X_BYTES + j * 4096, ap[j] + ((t >> (2 + j)) & 1u ? slab * 64 : 0),
+                     (t >> (2 + j)) & 1u);
     };
     float acc[4][2][4];
 #pragma unroll
@@ -205,75 +261,139 @@ __global__ void __launch_bounds__(SH_THREADS) lora_shrink_kernel(LoraParams p) {
         for (int j = 0; j < 2; ++j) {
           const int n = (i * 2 + nh) * 16 + j * 8 + (lane & 3) * 2;
           if (n < R)
-            *reinterpret_cast<float2*>(h + (t0 + r) * R + n) =
+            *reinterpret_cast<float2*>(h + (int64_t)s_tok[r] * R + n) =
                 make_float2(acc[i][j][half * 2], acc[i][j][half * 2 + 1]);
         }
     }
   }
 }
 
-// -------------------------------------------------------------- projection
+// ------------------------------------------------- projection, few tokens
+constexpr int SPLIT_TOKENS = 256;
 constexpr int LG_M = 128;  // features of a tile
 constexpr int LG_A_BYTES = LG_M * 128;
 constexpr int LG_THREADS = 256;
-constexpr int LG_BUILDERS = 192;  // warps 2..7 write the tiles of s h
-constexpr int LG_MAX_STAGES = 6;
+constexpr int LG_SIDE = 192;  // warps 2..7 prepare the adapters' part
+constexpr int LG_MAX_STAGES = 5;
 
-// Stages of the ring and buffers of s h for a tile of NT tokens: two CTAs
-// share an SM up to NT = 64, one has it from NT = 128 on.
-constexpr int lg_stages(int nt) { return nt <= 32 ? 5 : (nt <= 64 ? 4 : (nt <= 128 ? 5 : 4)); }
-constexpr int lg_hbufs(int nt) { return nt <= 32 || nt == 128 ? 2 : 1; }
-constexpr int lg_smem(int nt) {
-  return 1024 + lg_stages(nt) * (LG_A_BYTES + nt * 128) + lg_hbufs(nt) * nt * 128 + 256 + nt * 6;
+// Stages of the ring for a tile of NT tokens: two CTAs share an SM up to NT = 64.
+constexpr int lg_stages(int nt) { return nt <= 32 ? 5 : 4; }
+constexpr int lg_ring(int nt) { return lg_stages(nt) * (LG_A_BYTES + nt * 128); }
+// Shared memory: ring, s h of this CTA's share of the tokens, barriers, ids, order.
+__host__ __device__ inline int lg_smem(int nt, int splits, int R) {
+  return 1024 + lg_ring(nt) + nt / splits * R * 4 + 256 + nt * 4;
+}
+
+// Sum of the cluster's partial sums at this shared address, in rank order.
+template <int SPLITS>
+__device__ __forceinline__ float join_sum(uint32_t at) {
+  float v[SPLITS];
+#pragma unroll
+  for (int r = 0; r < SPLITS; ++r) v[r] = ld_cluster(at, r);
+#pragma unroll
+  for (int r = 1; r < SPLITS; ++r) v[0] += v[r];
+  return v[0];
+}
+
+// Joins token positions [i0, i1) of this CTA's share for feature n, adds the
+// adapters' part and stores them.  G tokens are in flight, each with its feature's
+// row of B (RV 16-byte pieces), which tokens of one adapter, neighbours in the
+// order, share.
+template <typename T, int RV, int G>
+__device__ __forceinline__ void join_tokens(const LoraParams& p, const int16_t* id,
+                                            const int16_t* order, const float* hs, int64_t t0,
+                                            int pos0, int i0, int i1, int64_t n, uint32_t red) {
+  const int R = (int)p.R;
+  const T* B = static_cast<const T*>(p.b) + n * R;
+  const int64_t per_adapter = p.N * R;
+  Pack<T, 8> last[RV];
+  int last_a = -1;
+  for (int i = i0; i < i1; i += G) {
+    Pack<T, 8> row[G][RV];
+    int a[G], c[G];
+    float sum[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      c[g] = i + g < i1 ? order[pos0 + i + g] : 0;
+      a[g] = i + g < i1 ? id[c[g]] : -1;
+      if (a[g] >= 0 && a[g] == (g > 0 ? a[g - 1] : last_a)) {
+#pragma unroll
+        for (int v = 0; v < RV; ++v) row[g][v] = g > 0 ? row[g - 1][v] : last[v];
+      } else if (a[g] >= 0) {
+#pragma unroll
+        for (int v = 0; v < RV; ++v)
+          row[g][v] = v * 8 < R ? load_pack<T, 8>(B + a[g] * per_adapter + v * 8) : zero_pack<T, 8>();
+      }
+    }
+    last_a = a[G - 1];
+#pragma unroll
+    for (int v = 0; v < RV; ++v) last[v] = row[G - 1][v];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const uint32_t at = red + (uint32_t)c[g] * LG_M * 4;
+      sum[g] = p.splits == 1 ? join_sum<1>(at)
+                             : (p.splits == 2 ? join_sum<2>(at)
+                                              : (p.splits == 4 ? join_sum<4>(at) : join_sum<8>(at)));
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      if (i + g >= i1) break;
+      if (t0 + c[g] >= p.T) continue;
+      float2 acc = both(0.0f);
+      if (a[g] >= 0) {
+        const float4* h = reinterpret_cast<const float4*>(hs + (i + g) * R);
+#pragma unroll
+        for (int v = 0; v < RV; ++v) {
+          if (v * 8 >= R) break;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const float4 f = h[v * 2 + q];
+            acc = fma2(make_float2(f.x, f.y), row[g][v].get2(2 * q), acc);
+            acc = fma2(make_float2(f.z, f.w), row[g][v].get2(2 * q + 1), acc);
+          }
+        }
+      }
+      static_cast<T*>(p.out)[(t0 + c[g]) * p.out_stride + n] =
+          from_f32<T>(sum[g] + (acc.x + acc.y));
+    }
+  }
 }
 
 template <typename T, int NT>
-__global__ void __launch_bounds__(LG_THREADS)
-    lora_gemm_kernel(const __grid_constant__ LoraParams p, const __grid_constant__ CUtensorMap tmW,
-                     const __grid_constant__ CUtensorMap tmX,
-                     const __grid_constant__ CUtensorMap tmB) {
-  constexpr int STAGES = lg_stages(NT), HB = lg_hbufs(NT);
-  constexpr int H_BYTES = NT * 128, STAGE_BYTES = LG_A_BYTES + NT * 128;
+__global__ void __launch_bounds__(LG_THREADS, NT <= 64 ? 2 : 1)
+    lora_split_kernel(const __grid_constant__ LoraParams p, const __grid_constant__ CUtensorMap tmW,
+                      const __grid_constant__ CUtensorMap tmX) {
+  constexpr int STAGES = lg_stages(NT), STAGE_BYTES = LG_A_BYTES + NT * 128;
   constexpr uint32_t IDESC = f16_idesc(std::is_same<T, __nv_bfloat16>::value, LG_M, NT);
   constexpr uint32_t TMEM_COLS = NT < 32 ? 32 : NT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint8_t* hbuf = smem + STAGES * STAGE_BYTES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(hbuf + HB * H_BYTES);
-  // full[STAGES], empty[STAGES], hfull[HB], hempty[HB], list, done
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * LG_MAX_STAGES + 6);
+  const int share = NT / p.splits;
+  float* hs = reinterpret_cast<float*>(smem + STAGES * STAGE_BYTES);  // [share][R]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(hs + share * p.R);
+  // full[STAGES], empty[STAGES], done
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * LG_MAX_STAGES + 1);
   int* s_abort = reinterpret_cast<int*>(tmem_holder + 1);
-  int* s_count = s_abort + 1;
   int16_t* s_id = reinterpret_cast<int16_t*>(reinterpret_cast<uint8_t*>(bars) + 256);
-  int16_t* s_first = s_id + NT;
-  int16_t* s_list = s_first + NT;
+  int16_t* s_order = s_id + NT;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort_flag = s_abort;
   const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + LG_MAX_STAGES);
-  const uint32_t hfull0 = smem_u32(bars + 2 * LG_MAX_STAGES);
-  const uint32_t hempty0 = smem_u32(bars + 2 * LG_MAX_STAGES + 2);
-  const uint32_t list_bar = smem_u32(bars + 2 * LG_MAX_STAGES + 4);
-  const uint32_t done_bar = smem_u32(bars + 2 * LG_MAX_STAGES + 5);
+  const uint32_t done_bar = smem_u32(bars + 2 * LG_MAX_STAGES);
 
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
     }
-    for (int s = 0; s < HB; ++s) {
-      mbar_init(hfull0 + 8 * s, LG_BUILDERS);
-      mbar_init(hempty0 + 8 * s, 1);
-    }
-    mbar_init(list_bar, LG_BUILDERS);
     mbar_init(done_bar, 1);
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async_smem();
     prefetch_map(&tmW);
     prefetch_map(&tmX);
-    prefetch_map(&tmB);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -298,46 +418,28 @@ __global__ void __launch_bounds__(LG_THREADS)
   const int slabs = (int)((p.K + 63) / 64);
   const int per = (slabs + p.splits - 1) / p.splits;
   const int kb0 = rank * per, kb1 = min(slabs, kb0 + per);
-  const int r16 = (int)((p.R + 15) & ~15);
-  const int rchunks = (r16 + 63) / 64;
-  const bool one_part = 2 * r16 <= 64;  // rounding and remainder fit one tile
-  const bool adapters = p.S > 0;
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA
     int stage = 0;
     uint32_t phase = 0, issued = 0, issued_phase = 0;
-    auto next = [&](auto&& issue) {
-      if (!warp_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, p.status)) return false;
-      if (elect_one()) issue(full0 + 8 * stage, smem_u32(smem + stage * STAGE_BYTES));
+    for (int kb = kb0; kb < kb1; ++kb) {
+#ifdef MOE_TEST_WITHHOLD_STAGE
+      // Failure-detection test builds only: CTA 0 issues neither its second
+      // slab nor anything after it, and the MMA warp's wait runs out.
+      if (blockIdx.x == 0 && blockIdx.y == 0 && kb > kb0) break;
+#endif
+      if (!warp_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, p.status)) break;
+      if (elect_one()) {
+        const uint32_t bar = full0 + 8 * stage, s = smem_u32(smem + stage * STAGE_BYTES);
+        mbar_expect_tx(bar, STAGE_BYTES);
+        tma_load_2d(s, &tmW, kb * 64, (int)n0, bar);
+        tma_load_2d(s + LG_A_BYTES, &tmX, kb * 64, (int)t0, bar);
+      }
       __syncwarp();
       issued |= 1u << stage;
       issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
       if (++stage == STAGES) stage = 0, phase ^= 1u;
-      return true;
-    };
-    bool ok = true;
-    for (int kb = kb0; kb < kb1 && ok; ++kb)
-#ifdef MOE_TEST_WITHHOLD_STAGE
-      // Failure-detection test builds only: CTA 0 issues neither its second
-      // slab nor anything after it, and the MMA warp's wait runs out.
-      if (blockIdx.x == 0 && blockIdx.y == 0 && kb > kb0) {
-        ok = false;
-      } else
-#endif
-      ok = next([&](uint32_t bar, uint32_t s) {
-        mbar_expect_tx(bar, STAGE_BYTES);
-        tma_load_2d(s, &tmW, kb * 64, (int)n0, bar);
-        tma_load_2d(s + LG_A_BYTES, &tmX, kb * 64, (int)t0, bar);
-      });
-    if (adapters && ok) ok = warp_wait(list_bar, 0, abort_flag, p.status);
-    if (adapters && ok) {
-      const int n = *s_count * rchunks;
-      for (int q = rank; q < n && ok; q += p.splits)
-        ok = next([&](uint32_t bar, uint32_t s) {
-          mbar_expect_tx(bar, LG_A_BYTES);
-          tma_load_2d(s, &tmB, (q % rchunks) * 64, (int)(s_list[q / rchunks] * p.N + n0), bar);
-        });
     }
     for (int s = 0; s < STAGES; ++s)  // every copy has landed before exit
       if (issued & (1u << s)) {
@@ -347,12 +449,10 @@ __global__ void __launch_bounds__(LG_THREADS)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA
-    int stage = 0, slot = 0;
-    uint32_t phase = 0, hphase = 0, accumulate = 0;
-    bool ok = true;
+    int stage = 0;
+    uint32_t phase = 0, accumulate = 0;
     for (int kb = kb0; kb < kb1; ++kb) {
-      ok = warp_wait(full0 + 8 * stage, phase, abort_flag, p.status);
-      if (!ok) break;
+      if (!warp_wait(full0 + 8 * stage, phase, abort_flag, p.status)) break;
       fence_after();
       const uint32_t s = smem_u32(smem + stage * STAGE_BYTES);
       const uint64_t ad = sw128_desc(s), bd = sw128_desc(s + LG_A_BYTES);
@@ -365,34 +465,6 @@ __global__ void __launch_bounds__(LG_THREADS)
       accumulate = 1;
       if (++stage == STAGES) stage = 0, phase ^= 1u;
     }
-    if (adapters && ok) ok = warp_wait(list_bar, 0, abort_flag, p.status);
-    if (adapters && ok) {
-      const int n = *s_count * rchunks;
-      for (int q = rank; q < n && ok; q += p.splits) {
-        ok = warp_wait(full0 + 8 * stage, phase, abort_flag, p.status);
-        const uint64_t ad = sw128_desc(smem_u32(smem + stage * STAGE_BYTES));
-        const int steps = min(4, r16 / 16 - (q % rchunks) * 4);
-        for (int part = 0; part < (one_part ? 1 : 2) && ok; ++part) {
-          ok = warp_wait(hfull0 + 8 * slot, hphase, abort_flag, p.status);
-          if (!ok) break;
-          fence_after();
-          const uint64_t bd = sw128_desc(smem_u32(hbuf + slot * H_BYTES));
-          if (elect_one()) {
-            for (int k = 0; k < steps; ++k) {
-              mma_f16(tmem, ad + 2 * k, bd + 2 * k, IDESC, accumulate | (k > 0));
-              if (one_part) mma_f16(tmem, ad + 2 * k, bd + 2 * (steps + k), IDESC, 1);
-            }
-            mma_commit(hempty0 + 8 * slot);
-          }
-          __syncwarp();
-          accumulate = 1;
-          if (++slot == HB) slot = 0, hphase ^= 1u;
-        }
-        if (ok && elect_one()) mma_commit(empty0 + 8 * stage);
-        __syncwarp();
-        if (++stage == STAGES) stage = 0, phase ^= 1u;
-      }
-    }
     if (accumulate) {  // all MMAs complete before the sums are read or TMEM is freed
       if (elect_one()) mma_commit(done_bar);
       __syncwarp();
@@ -401,71 +473,51 @@ __global__ void __launch_bounds__(LG_THREADS)
       __syncwarp();
     }
   } else {
-    // ------------------------------------------------- tiles of s h, epilogue
-    const int bt = tid - 64;
-    auto builders_sync = [] { asm volatile("bar.sync 1, 192;" ::: "memory"); };
-    if (adapters) {
+    // -------------------------------------- tokens' order, s h; then the sums
+    const int st = tid - 64;
+    auto side_sync = [] { asm volatile("bar.sync 1, 192;" ::: "memory"); };
+    if (p.S > 0) {
       bool bad = false;
-      for (int i = bt; i < NT; i += LG_BUILDERS) s_id[i] = (int16_t)adapter_of(p, t0 + i, &bad);
-      builders_sync();
-      const int count =
-          distinct_adapters(s_id, s_first, s_list, NT, bt, LG_BUILDERS, builders_sync);
-      if (bt == 0) *s_count = count;
-      mbar_arrive(list_bar);
-      if (!p.wait_first) pdl_wait();
-      int slot = 0;
-      uint32_t hphase = 0;
-      bool ok = true;
-      const int R = (int)p.R, n = count * rchunks;
-      for (int q = rank; q < n && ok; q += p.splits) {
-        const int a = s_list[q / rchunks], rc = (q % rchunks) * 64;
-        const float scale = __ldg(p.scale + a);
-        for (int part = 0; part < (one_part ? 1 : 2) && ok; ++part) {
-          ok = warp_wait(hempty0 + 8 * slot, hphase ^ 1u, abort_flag, p.status);
-          if (!ok) break;
-          uint8_t* dst = hbuf + slot * H_BYTES;
-          for (int i = bt; i < NT * 8; i += LG_BUILDERS) {
-            const int t = i >> 3, c = i & 7;
-            // columns of the tile: the rounding, then (one_part) the remainder
-            const bool low = one_part ? c * 8 >= r16 : part == 1;
-            const int r = rc + (one_part && low ? c * 8 - r16 : c * 8);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (s_id[t] == a && r < R) {
-              float hv[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) hv[e] = 0.0f;
-              const float* src = p.h + (t0 + t) * R + r;
-              for (int s = 0; s < p.shares; ++s, src += p.T * R) {
-                const float4 u0 = __ldcg(reinterpret_cast<const float4*>(src));
-                const float4 u1 = __ldcg(reinterpret_cast<const float4*>(src) + 1);
-                hv[0] += u0.x, hv[1] += u0.y, hv[2] += u0.z, hv[3] += u0.w;
-                hv[4] += u1.x, hv[5] += u1.y, hv[6] += u1.z, hv[7] += u1.w;
-              }
-              T o[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float sh = scale * hv[e];
-                o[e] = from_f32<T>(sh);
-                if (low) o[e] = from_f32<T>(sh - to_f32(o[e]));
-              }
-              memcpy(&v, o, 16);
-            }
-            *reinterpret_cast<uint4*>(dst + tile_at(t, c)) = v;
-          }
-          fence_async_smem();
-          mbar_arrive(hfull0 + 8 * slot);
-          if (++slot == HB) slot = 0, hphase ^= 1u;
-        }
+      for (int i = st; i < NT; i += LG_SIDE) s_id[i] = (int16_t)adapter_of(p, t0 + i, &bad);
+      side_sync();
+      for (int i = st; i < NT; i += LG_SIDE) {
+        int before = 0;
+        for (int j = 0; j < NT; ++j)
+          before += s_id[j] < s_id[i] || (s_id[j] == s_id[i] && j < i);
+        s_order[before] = (int16_t)i;
       }
-    } else if (!p.wait_first) {
-      pdl_wait();
+      side_sync();
+      // the rows of B that the join will read start towards L2
+      const T* B = static_cast<const T*>(p.b);
+      for (int i = st; i < share; i += LG_SIDE) {
+        const int pos = rank * share + i, a = s_id[s_order[pos]];
+        if (a >= 0 && (i == 0 || s_id[s_order[pos - 1]] != a))
+          prefetch_l2(B + ((int64_t)a * p.N + n0) * p.R,
+                      (uint32_t)(min((int64_t)LG_M, p.N - n0) * p.R * 2));
+      }
+      if (!p.wait_first) pdl_wait();
+      const int q4 = (int)p.R / 4;
+      for (int i = st; i < share * q4; i += LG_SIDE) {
+        const int k = i / q4, c = s_order[rank * share + k], a = s_id[c];
+        if (a < 0) continue;
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const float* src = p.h + (t0 + c) * p.R + (i - k * q4) * 4;
+        for (int s = 0; s < p.shares; ++s, src += p.T * p.R) {
+          const float4 u = __ldcg(reinterpret_cast<const float4*>(src));
+          sum.x += u.x, sum.y += u.y, sum.z += u.z, sum.w += u.w;
+        }
+        const float scale = __ldg(p.scale + a);
+        reinterpret_cast<float4*>(hs)[i] =
+            make_float4(scale * sum.x, scale * sum.y, scale * sum.z, scale * sum.w);
+      }
+    } else {
+      for (int i = st; i < NT; i += LG_SIDE) s_id[i] = -1, s_order[i] = (int16_t)i;
     }
     // done is also signalled after a wait ran out; the sums are then not whole
     if (warp >= 4 && warp_wait(done_bar, 0, abort_flag, p.status) && *abort_flag == 0) {
       fence_after();
       const int nl = (warp & 3) * 32 + lane;
       const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-      T* out = static_cast<T*>(p.out) + n0 + nl;
       float* red = reinterpret_cast<float*>(smem);  // the ring is no longer in use
 #pragma unroll 1
       for (int c = 0; c < NT; c += 16) {
@@ -473,38 +525,438 @@ __global__ void __launch_bounds__(LG_THREADS)
         tmem_ld16(lanes + c, v);
         tmem_wait16(v);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          if (p.splits > 1)
-            red[(c + j) * LG_M + nl] = __uint_as_float(v[j]);
-          else if (t0 + c + j < p.T && n0 + nl < p.N)
-            out[(t0 + c + j) * p.out_stride] = from_f32<T>(__uint_as_float(v[j]));
-        }
+        for (int j = 0; j < 16; ++j) red[(c + j) * LG_M + nl] = __uint_as_float(v[j]);
       }
       fence_before();
     }
   }
   __syncwarp();
-  if (p.splits > 1) {
-    // each CTA joins its share of the tile's tokens, partial sums in rank order
+  if (p.splits > 1)
     cluster_sync();
-    const int share = NT / p.splits;
-    const uint32_t red0 = smem_u32(smem);
-    if (*abort_flag == 0) {
-      for (int i = tid; i < share * LG_M; i += LG_THREADS) {
-        const int c = rank * share + i / LG_M, nl = i % LG_M;
-        if (t0 + c >= p.T || n0 + nl >= p.N) continue;
-        float sum = 0.0f;
-        for (int r = 0; r < p.splits; ++r) sum += ld_cluster(red0 + (c * LG_M + nl) * 4, r);
-        static_cast<T*>(p.out)[(t0 + c) * p.out_stride + n0 + nl] = from_f32<T>(sum);
-      }
-    }
-    cluster_sync();  // no CTA leaves while its sums are read
+  else
+    __syncthreads();
+  // Each CTA finishes its share of the tile's tokens, partial sums in rank order.
+  const int nl = tid % LG_M;
+  if (*abort_flag == 0 && n0 + nl < p.N) {
+    const uint32_t red = smem_u32(smem) + (uint32_t)nl * 4;
+    const int half = share / 2, i0 = tid < LG_M ? 0 : half, i1 = tid < LG_M ? half : share;
+    const int pos0 = rank * share;
+    const int64_t n = n0 + nl;
+    if (p.R <= 16)
+      join_tokens<T, 2, 4>(p, s_id, s_order, hs, t0, pos0, i0, i1, n, red);
+    else if (p.R <= 32)
+      join_tokens<T, 4, 4>(p, s_id, s_order, hs, t0, pos0, i0, i1, n, red);
+    else if (p.R <= 64)
+      join_tokens<T, 8, 2>(p, s_id, s_order, hs, t0, pos0, i0, i1, n, red);
+    else
+      join_tokens<T, 16, 1>(p, s_id, s_order, hs, t0, pos0, i0, i1, n, red);
   }
+  __syncwarp();
+  if (p.splits > 1) cluster_sync();  // no CTA leaves while its sums are read
   fence_before();
   __syncthreads();
   if (warp == 1) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS)
+                 : "memory");
+  }
+}
+
+// ------------------------------------------------ projection, many tokens
+constexpr int LP_TILE = 256;    // features and tokens of a pair's tile
+constexpr int LP_HALF = 128;    // of them one CTA's
+constexpr int LP_STAGES = 6;
+constexpr int LP_STAGE_BYTES = 2 * LP_HALF * 128;  // a CTA's part: W rows, x rows
+constexpr int LP_H_BYTES = LP_HALF * 128;
+constexpr int LP_THREADS = 384;
+constexpr int LP_EPI_WARP0 = 8;                    // warps 8..11: epilogue
+constexpr int LP_BUILD_WARPS = 6;                  // warps 2..7: tiles of s h
+constexpr int LP_BUILDERS = LP_BUILD_WARPS * 32;
+constexpr int LP_SMEM = 1024 + LP_STAGES * LP_STAGE_BYTES + 2 * LP_H_BYTES + 256 + LP_HALF * 8;
+constexpr int LP_GROUPS = LP_TILE / RUN;
+
+// The runs of a tile, the same in every warp that asks: lane g < LP_GROUPS has
+// the adapter of columns [RUN g, RUN g + RUN), and bit g of `starts` is set where
+// a run of an adapter begins, of `ends` where a run or a gap ends.
+struct Runs {
+  int adapter;
+  uint32_t starts, ends;
+};
+__device__ __forceinline__ Runs tile_runs(const LoraParams& p, int64_t pos0, int64_t places,
+                                          int lane) {
+  Runs r;
+  const int64_t pos = pos0 + lane * RUN;
+  bool bad = false;
+  r.adapter = -1;
+  if (lane < LP_GROUPS && pos < places) r.adapter = adapter_of(p, p.order[pos], &bad);
+  const int before = __shfl_up_sync(0xFFFFFFFFu, r.adapter, 1);
+  const bool begins = lane < LP_GROUPS && (lane == 0 || before != r.adapter);
+  r.starts = __ballot_sync(0xFFFFFFFFu, begins && r.adapter >= 0);
+  r.ends = __ballot_sync(0xFFFFFFFFu, begins) >> 1 | 1u << (LP_GROUPS - 1);
+  return r;
+}
+// Last group of the run that begins at g.
+__device__ __forceinline__ int run_end(const Runs& r, int g) { return __ffs(r.ends >> g) - 1 + g; }
+
+// A persistent pair of CTAs; CTA r of the pair has features [128 r, 128 r + 128)
+// and tokens [128 r, ...) of a tile's operands, and those features' sums for all
+// 256 tokens.  The first CTA issues the MMAs of both; its full[] and hfull
+// barriers count both CTAs' copies and tiles, and each commit reaches both.
+template <typename T>
+__global__ void __launch_bounds__(LP_THREADS, 1)
+    lora_pair_kernel(const __grid_constant__ LoraParams p, const __grid_constant__ CUtensorMap tmW,
+                     const __grid_constant__ CUtensorMap tmX,
+                     const __grid_constant__ CUtensorMap tmXs,
+                     const __grid_constant__ CUtensorMap tmB) {
+  constexpr uint32_t IDESC = f16_idesc(std::is_same<T, __nv_bfloat16>::value, LP_TILE, LP_TILE);
+  constexpr uint32_t IDESC_RUN = f16_idesc(std::is_same<T, __nv_bfloat16>::value, LP_TILE, RUN);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* hbuf = smem + LP_STAGES * LP_STAGE_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(hbuf + 2 * LP_H_BYTES);
+  // full[STAGES], empty[STAGES], hfull[2], hempty[2], tfull[2], tempty[2]
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * LP_STAGES + 8);
+  int* s_abort = reinterpret_cast<int*>(tmem_holder + 1);
+  int* s_go = s_abort + 1;
+  int32_t* s_tok = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(bars) + 256);  // [128]
+  int32_t* s_row = s_tok + LP_HALF;  // adapter of a row of the tile of s h
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort_flag = s_abort;
+  const uint32_t rank = cluster_rank();
+  const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + LP_STAGES);
+  const uint32_t hfull0 = smem_u32(bars + 2 * LP_STAGES), hempty0 = hfull0 + 16;
+  const uint32_t tfull0 = hfull0 + 32, tempty0 = hfull0 + 48;
+
+  if (tid == 0) {
+    for (int s = 0; s < LP_STAGES; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(hfull0 + 8 * b, 2 * LP_BUILD_WARPS);
+      mbar_init(hempty0 + 8 * b, 1);
+      mbar_init(tfull0 + 8 * b, 1);
+      mbar_init(tempty0 + 8 * b, 2 * 4);
+    }
+    *s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_async_smem();
+    prefetch_map(&tmW);
+    prefetch_map(&tmX);
+    prefetch_map(&tmXs);
+    prefetch_map(&tmB);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_holder)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are set up
+  fence_after();
+  const uint32_t tmem = *tmem_holder;
+  if (p.wait_first) pdl_wait();  // else as in lora_split_kernel; order too is complete
+  pdl_launch_dependents();
+
+  const bool adapters = p.S > 0;
+  const int64_t places = adapters ? *p.places : p.T;
+  const int n_tiles = (int)((p.N + LP_TILE - 1) / LP_TILE);
+  const int units = n_tiles * (int)((places + LP_TILE - 1) / LP_TILE);
+  const int first = (int)(blockIdx.x >> 1), stride = (int)(gridDim.x >> 1);
+  const int slabs = (int)((p.K + 63) / 64);
+  const int r16 = (int)((p.R + 15) & ~15);
+  const int rchunks = (r16 + 63) / 64;
+  const bool one_part = 2 * r16 <= 64;  // rounding and remainder fit one tile
+  const int builds = adapters ? rchunks * (one_part ? 1 : 2) : 0;  // tiles of s h of a unit
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA
+    int stage = 0;
+    uint32_t phase = 0, issued = 0, issued_phase = 0;
+    auto advance = [&] {
+      issued |= 1u << stage;
+      issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+      if (++stage == LP_STAGES) stage = 0, phase ^= 1u;
+    };
+    bool ok = true;
+    for (int u = first; ok && u < units; u += stride) {
+      const int n0 = (u % n_tiles) * LP_TILE + (int)rank * LP_HALF;
+      const int64_t t0 = (int64_t)(u / n_tiles) * LP_TILE;
+      // this CTA's four groups: first row in x where their tokens follow one
+      // another, else ~place in the rows that the shrink has put in order
+      int from[LP_GROUPS / 2];
+      bool sorted_rows = false;
+#pragma unroll
+      for (int i = 0; i < LP_GROUPS / 2; ++i) {
+        const int64_t place = t0 + rank * LP_HALF + i * RUN;
+        from[i] = (int)place;
+        if (!adapters) continue;
+        const int tok = place + lane < places ? p.order[place + lane] : -1;
+        const bool together = group_together(tok);
+        const int row0 = __shfl_sync(0xFFFFFFFFu, tok, 0);
+        from[i] = place >= places ? 0 : (together ? row0 : ~(int)place);
+        sorted_rows = sorted_rows || from[i] < 0;
+      }
+      if (sorted_rows) pdl_wait();
+      for (int kb = 0; kb < slabs && ok; ++kb) {
+#ifdef MOE_TEST_WITHHOLD_STAGE
+        if (blockIdx.x < 2 && kb > 0) {  // as in lora_split_kernel: the first pair stops here
+          ok = false;
+          break;
+        }
+#endif
+        ok = warp_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, p.status);
+        if (!ok) break;
+        const uint32_t bar = cluster_address(full0 + 8 * stage, 0);
+        const uint32_t s = smem_u32(smem + stage * LP_STAGE_BYTES);
+        if (elect_one()) {
+          if (rank == 0) mbar_expect_tx(full0 + 8 * stage, 2 * LP_STAGE_BYTES);
+          tma_load_2d_pair(s, &tmW, kb * 64, n0, bar);
+#pragma unroll
+          for (int i = 0; i < LP_GROUPS / 2; ++i) {
+            const uint32_t dst = s + LP_HALF * 128 + i * RUN * 128;
+            if (from[i] >= 0)
+              tma_load_2d_pair(dst, &tmX, kb * 64, from[i], bar);
+            else
+              tma_load_2d_pair(dst, &tmXs, kb * 64, ~from[i], bar);
+          }
+        }
+        __syncwarp();
+        advance();
+      }
+      if (!adapters || !ok) continue;
+      const Runs runs = tile_runs(p, t0, places, lane);
+      for (int b = 0; b < builds && ok; ++b) {
+        const int rc = (one_part ? b : b >> 1) * 64;
+        for (uint32_t m = runs.starts; m != 0 && ok; m &= m - 1) {
+          const int a = __shfl_sync(0xFFFFFFFFu, runs.adapter, __ffs(m) - 1);
+          ok = warp_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, p.status);
+          if (!ok) break;
+          if (elect_one()) {
+            if (rank == 0) mbar_expect_tx(full0 + 8 * stage, 2 * LP_HALF * 128);
+            tma_load_2d_pair(smem_u32(smem + stage * LP_STAGE_BYTES), &tmB, rc,
+                             (int)(a * p.N + n0), cluster_address(full0 + 8 * stage, 0));
+          }
+          __syncwarp();
+          advance();
+        }
+      }
+    }
+    if (rank == 0)  // both CTAs' copies have landed before either leaves
+      for (int s = 0; s < LP_STAGES; ++s)
+        if (issued & (1u << s)) {
+          volatile int never = 0;
+          mbar_wait(full0 + 8 * s, (issued_phase >> s) & 1u, &never, p.status);
+        }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------- MMA (the first CTA's)
+    int stage = 0, ab = 0, hs = 0;
+    uint32_t phase = 0, hphase = 0, aphase = 0;
+    bool ok = rank == 0;
+    for (int u = first; ok && u < units; u += stride) {
+      ok = warp_wait(tempty0 + 8 * ab, aphase ^ 1u, abort_flag, p.status);
+      const uint32_t d = tmem + (uint32_t)(ab * LP_TILE);
+      for (int kb = 0; kb < slabs && ok; ++kb) {
+        ok = warp_wait(full0 + 8 * stage, phase, abort_flag, p.status);
+        if (!ok) break;
+        fence_after();
+        const uint32_t s = smem_u32(smem + stage * LP_STAGE_BYTES);
+        const uint64_t ad = sw128_desc(s), bd = sw128_desc(s + LP_HALF * 128);
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_f16_pair(d, ad + 2 * k, bd + 2 * k, IDESC, kb > 0 || k > 0);
+          mma_commit_pair(empty0 + 8 * stage);
+        }
+        __syncwarp();
+        if (++stage == LP_STAGES) stage = 0, phase ^= 1u;
+      }
+      Runs runs{};
+      if (adapters) runs = tile_runs(p, (int64_t)(u / n_tiles) * LP_TILE, places, lane);
+      if (runs.starts != 0) {
+        for (int b = 0; b < builds && ok; ++b) {
+          const int steps = min(4, r16 / 16 - (one_part ? b : b >> 1) * 4);
+          ok = warp_wait(hfull0 + 8 * hs, hphase, abort_flag, p.status);
+          const uint8_t* hb = hbuf + hs * LP_H_BYTES;
+          for (uint32_t m = runs.starts; m != 0 && ok; m &= m - 1) {
+            const int g = __ffs(m) - 1, len = run_end(runs, g) - g + 1;
+            ok = warp_wait(full0 + 8 * stage, phase, abort_flag, p.status);
+            if (!ok) break;
+            fence_after();
+            // the run's columns alone; each CTA has half of its tokens in hbuf
+            const uint32_t dr = d + (uint32_t)(g * RUN);
+            const uint32_t idesc = IDESC_RUN + ((uint32_t)((len - 1) * (RUN >> 3)) << 17);
+            const uint64_t ad = sw128_desc(smem_u32(smem + stage * LP_STAGE_BYTES));
+            const uint64_t bd = sw128_desc(smem_u32(hb + g * (RUN / 2) * 128));
+            if (elect_one()) {
+              for (int k = 0; k < steps; ++k) {
+                mma_f16_pair(dr, ad + 2 * k, bd + 2 * k, idesc, 1);
+                if (one_part) mma_f16_pair(dr, ad + 2 * k, bd + 2 * (steps + k), idesc, 1);
+              }
+              mma_commit_pair(empty0 + 8 * stage);
+            }
+            __syncwarp();
+            if (++stage == LP_STAGES) stage = 0, phase ^= 1u;
+          }
+          if (elect_one()) mma_commit_pair(hempty0 + 8 * hs);
+          __syncwarp();
+          hs ^= 1;
+          if (hs == 0) hphase ^= 1u;
+        }
+      }
+      if (elect_one()) mma_commit_pair(tfull0 + 8 * ab);
+      __syncwarp();
+      ab ^= 1;
+      if (ab == 0) aphase ^= 1u;
+    }
+  } else if (warp < LP_EPI_WARP0) {
+    // ---------------------------------------------------------- tiles of s h
+    const int bt = tid - 64;
+    auto build_sync = [] { asm volatile("bar.sync 1, 192;" ::: "memory"); };
+    int hs = 0;
+    uint32_t hphase = 0;
+    bool ok = true, waited = p.wait_first != 0;
+    const int R = (int)p.R;
+    for (int u = first; adapters && u < units; u += stride) {
+      // one warp decides for all whether to go on, so that the barriers match
+      if (bt == 0) *s_go = ok && *abort_flag == 0;
+      build_sync();
+      if (*s_go == 0) break;
+      const int64_t t0 = (int64_t)(u / n_tiles) * LP_TILE;
+      const Runs runs = tile_runs(p, t0, places, lane);
+      if (runs.starts == 0) {
+        build_sync();
+        continue;
+      }
+      // row j of this CTA's tile: of a run of `len` groups from g on, the first
+      // half of its tokens lies in the first CTA's rows, the second in the other's
+      if (warp < 6) {
+        const int j = bt, grp = j / (RUN / 2);
+        const int g = 31 - __clz(runs.starts & ((2u << grp) - 1u));  // -1: no run before
+        int tok = -1, a = -1;
+        const int end = g >= 0 ? run_end(runs, g) : -1;
+        if (g >= 0 && grp <= end) {
+          const int len = end - g + 1;
+          tok = p.order[t0 + g * RUN + (int)rank * len * (RUN / 2) + j - g * (RUN / 2)];
+        }
+        a = __shfl_sync(0xFFFFFFFFu, runs.adapter, g >= 0 ? g : 0);
+        s_tok[j] = tok;
+        s_row[j] = a;
+      }
+      build_sync();
+      if (!waited) pdl_wait();
+      waited = true;
+      // hi: the rounding of s h, low: the rounded remainder.  With one_part both
+      // go to one tile, side by side; else to two tiles, from one reading of h.
+      auto value = [&](int t, int r, Pack<T, 8>& hi, Pack<T, 8>& low) {
+        hi = low = zero_pack<T, 8>();
+        const int tok = s_tok[t];
+        if (tok < 0 || r >= R) return;
+        const float* src = p.h + (int64_t)tok * R + r;
+        const int64_t step = p.T * R;
+        float4 u0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u1 = u0;
+        for (int s0 = 0; s0 < p.shares; s0 += 4) {  // four shares' sums in flight
+          float4 v0[4], v1[4];
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            v0[s] = v1[s] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (s0 + s < p.shares) {
+              v0[s] = __ldcg(reinterpret_cast<const float4*>(src + (s0 + s) * step));
+              v1[s] = __ldcg(reinterpret_cast<const float4*>(src + (s0 + s) * step) + 1);
+            }
+          }
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            u0.x += v0[s].x, u0.y += v0[s].y, u0.z += v0[s].z, u0.w += v0[s].w;
+            u1.x += v1[s].x, u1.y += v1[s].y, u1.z += v1[s].z, u1.w += v1[s].w;
+          }
+        }
+        const float scale = __ldg(p.scale + s_row[t]);
+        const float2 f[4] = {make_float2(scale * u0.x, scale * u0.y),
+                             make_float2(scale * u0.z, scale * u0.w),
+                             make_float2(scale * u1.x, scale * u1.y),
+                             make_float2(scale * u1.z, scale * u1.w)};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          hi.set2(e, f[e]);
+          const float2 h = hi.get2(e);
+          low.set2(e, make_float2(f[e].x - h.x, f[e].y - h.y));
+        }
+      };
+      auto ready = [&] {
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(cluster_address(hfull0 + 8 * hs, 0));
+        hs ^= 1;
+        if (hs == 0) hphase ^= 1u;
+      };
+      for (int rc = 0; rc < r16 && ok; rc += 64) {
+        ok = warp_wait(hempty0 + 8 * hs, hphase ^ 1u, abort_flag, p.status);
+        if (!one_part) ok = ok && warp_wait(hempty0 + 8, hphase ^ 1u, abort_flag, p.status);
+        if (!ok) break;
+        uint8_t* to = hbuf + hs * LP_H_BYTES;
+        const int pieces = one_part ? r16 / 8 : 8;
+        for (int i = bt; i < LP_HALF * 8; i += LP_BUILDERS) {
+          const int t = i >> 3, c = i & 7;
+          if (c >= pieces) continue;
+          Pack<T, 8> hi, low;
+          value(t, rc + c * 8, hi, low);
+          *reinterpret_cast<uint4*>(to + tile_at(t, c)) = hi.w;
+          *reinterpret_cast<uint4*>(one_part ? to + tile_at(t, pieces + c)
+                                             : to + LP_H_BYTES + tile_at(t, c)) = low.w;
+        }
+        ready();
+        if (!one_part) ready();
+      }
+    }
+    if (!waited) pdl_wait();
+  } else {
+    // -------------------------------------------------------------- epilogue
+    const int nl = (warp & 3) * 32 + lane;
+    int ab = 0;
+    uint32_t aphase = 0;
+    for (int u = first; u < units; u += stride) {
+      if (!warp_wait(tfull0 + 8 * ab, aphase, abort_flag, p.status) || *abort_flag != 0) break;
+      fence_after();
+      const int64_t n = (int64_t)(u % n_tiles) * LP_TILE + rank * LP_HALF + nl;
+      const int64_t t0 = (int64_t)(u / n_tiles) * LP_TILE;
+      const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(ab * LP_TILE);
+      T* out = static_cast<T*>(p.out) + n;
+#pragma unroll 1
+      for (int c = 0; c < LP_TILE; c += 32) {
+        uint32_t v[2][16];
+        tmem_ld16(lanes + c, v[0]);
+        tmem_ld16(lanes + c + 16, v[1]);
+        // lane l holds the token of column c + l
+        const int64_t mine = t0 + c + lane;
+        const int tok = mine < places ? (adapters ? p.order[mine] : (int)mine) : -1;
+        tmem_wait16(v[0]);
+        tmem_wait16(v[1]);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const int t = __shfl_sync(0xFFFFFFFFu, tok, j);
+          if (t >= 0 && n < p.N)
+            out[t * p.out_stride] = from_f32<T>(__uint_as_float(v[j >> 4][j & 15]));
+        }
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_address(tempty0 + 8 * ab, 0));
+      ab ^= 1;
+      if (ab == 0) aphase ^= 1u;
+    }
+  }
+  __syncwarp();
+  fence_before();
+  cluster_sync();  // both CTAs' copies, MMAs and reads are done
+  if (warp == 1) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
                  : "memory");
   }
 }
@@ -515,31 +967,48 @@ namespace moe_host {
 
 using moe::LoraParams;
 
+size_t token_order_scratch(int64_t T, int64_t S);
+moe_status_t launch_token_order(const int32_t* adapter_ids, int64_t T, int64_t S, int align,
+                                int32_t* order, int64_t rows, int32_t* scratch, cudaStream_t s);
+
+// Sizes of one call; the same for the workspace query and the launch.
 struct LoraPlan {
-  int tiles, shares, share_k, zs;  // shrink
-  int nt, splits;                  // projection
+  bool pair;                        // lora_pair_kernel
+  int64_t places;                   // most places of the tokens' order (pair)
+  int64_t order_words;              // of the workspace: order and the sort's scratch
+  int64_t copy_words;               // of the workspace: x in that order
+  int tiles, shares, share_k, zs;   // shrink
+  int nt, splits;                   // lora_split_kernel
 };
 
 static LoraPlan lora_plan(int64_t T, int64_t K, int64_t N, int64_t S) {
   LoraPlan q{};
   const int64_t sms = num_sms();
-  // Shrink: shares of K until about two blocks an SM, at least 256 wide.
-  q.tiles = (int)((T + moe::SH_TOK - 1) / moe::SH_TOK);
+  q.pair = T > moe::SPLIT_TOKENS;
+  q.places = T;
+  if (q.pair && S > 0) {
+    q.places = (T + (moe::RUN - 1) * (S + 1) + 63) / 64 * 64;
+    q.order_words = (q.places + (int64_t)token_order_scratch(T, S) + 3) / 4 * 4;
+    q.copy_words = (q.places * K / 2 + 3) / 4 * 4;
+  }
+  // Shrink: one block for each adapter that 64 tokens may have, or for all of
+  // them where the order leaves two at most; shares of K, at least 256 wide, until
+  // about four blocks an SM.
+  q.tiles = (int)((q.places + moe::SH_TOK - 1) / moe::SH_TOK);
   int64_t z = S < moe::SH_TOK ? S : moe::SH_TOK;
   if (T < z) z = T;
-  if (z < 1) z = 1;
-  const int64_t most = q.tiles >= sms ? 1 : (2 * sms + q.tiles - 1) / q.tiles;
+  if (q.pair || z < 1) z = 1;
+  const int64_t most = q.tiles >= 4 * sms ? 1 : (4 * sms + q.tiles - 1) / q.tiles;
   q.zs = (int)(z < most ? z : most);
-  if (q.tiles >= 32) q.zs = 1;  // long batches: a tile's tokens share few adapters
-  int64_t shares = (2 * sms) / ((int64_t)q.tiles * q.zs);
+  int64_t shares = (4 * sms) / ((int64_t)q.tiles * q.zs);
   if (shares > (K + 255) / 256) shares = (K + 255) / 256;
   if (shares > 16) shares = 16;
   if (shares < 1) shares = 1;
   q.share_k = (int)(((K + shares - 1) / shares + 63) / 64 * 64);
   q.shares = (int)((K + q.share_k - 1) / q.share_k);
-  // Projection: the smallest tile that holds the batch, up to 256 tokens; a
+  // Split projection: the smallest tile that holds the batch, up to 128 tokens; a
   // cluster shares a tile's K while tiles leave CTA slots empty.
-  q.nt = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 ? 64 : (T <= 128 ? 128 : 256)));
+  q.nt = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 ? 64 : 128));
   const int64_t tiles = (N + moe::LG_M - 1) / moe::LG_M * ((T + q.nt - 1) / q.nt);
   const int64_t slots = q.nt <= 64 ? 2 * sms : sms;
   const int64_t slabs = (K + 63) / 64;
@@ -550,6 +1019,10 @@ static LoraPlan lora_plan(int64_t T, int64_t K, int64_t N, int64_t S) {
     q.splits *= 2;
   }
   return q;
+}
+
+static size_t lora_workspace(const LoraPlan& q, int64_t T, int64_t R) {
+  return (size_t)((q.order_words + q.copy_words + (int64_t)q.shares * T * R) * 4);
 }
 
 // Dynamic shared memory limit of a kernel, raised once per device.
@@ -569,30 +1042,53 @@ static moe_status_t allow_smem(int bytes) {
   return MOE_OK;
 }
 
-template <typename T, int NT>
-static moe_status_t launch_gemm(const LoraParams& p, const CUtensorMap& w, const CUtensorMap& x,
-                                const CUtensorMap& b, cudaStream_t s) {
-  auto kernel = moe::lora_gemm_kernel<T, NT>;
-  constexpr int smem = moe::lg_smem(NT);
-  static_assert(smem <= 232448, "shared memory of one CTA");
-  moe_status_t st = allow_smem<moe::lora_gemm_kernel<T, NT>>(smem);
-  if (st != MOE_OK) return st;
+template <typename... KArgs, typename... Args>
+static cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, int threads, int cluster,
+                                  size_t smem, cudaStream_t s, Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((p.N + moe::LG_M - 1) / moe::LG_M * p.splits),
-                     (unsigned)((p.T + NT - 1) / NT));
-  cfg.blockDim = dim3(moe::LG_THREADS);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = p.splits;
+  attr[1].val.clusterDim.x = cluster;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return launched(cudaLaunchKernelEx(&cfg, kernel, p, w, x, b), "projection");
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+constexpr int kMaxSmem = 232448;
+
+template <typename T, int NT>
+static moe_status_t launch_split(const LoraParams& p, const CUtensorMap& w, const CUtensorMap& x,
+                                 cudaStream_t s) {
+  const int smem = moe::lg_smem(NT, p.splits, (int)p.R);  // <= kMaxSmem for R <= 128
+  moe_status_t st = allow_smem<moe::lora_split_kernel<T, NT>>(kMaxSmem);
+  if (st != MOE_OK) return st;
+  const dim3 grid((unsigned)((p.N + moe::LG_M - 1) / moe::LG_M * p.splits),
+                  (unsigned)((p.T + NT - 1) / NT));
+  return launched(launch_cluster(moe::lora_split_kernel<T, NT>, grid, moe::LG_THREADS, p.splits,
+                                 smem, s, p, w, x), "projection");
+}
+
+template <typename T>
+static moe_status_t launch_pair(const LoraParams& p, int64_t places, const CUtensorMap& w,
+                                const CUtensorMap& x, const CUtensorMap& xs, const CUtensorMap& b,
+                                cudaStream_t s) {
+  static_assert(moe::LP_SMEM <= kMaxSmem, "shared memory of one CTA");
+  moe_status_t st = allow_smem<moe::lora_pair_kernel<T>>(moe::LP_SMEM);
+  if (st != MOE_OK) return st;
+  const int64_t units = (p.N + moe::LP_TILE - 1) / moe::LP_TILE *
+                        ((places + moe::LP_TILE - 1) / moe::LP_TILE);
+  const int64_t pairs = num_sms() / 2;
+  const dim3 grid((unsigned)(2 * (units < pairs ? units : pairs)));
+  return launched(launch_cluster(moe::lora_pair_kernel<T>, grid, moe::LP_THREADS, 2, moe::LP_SMEM,
+                                 s, p, w, x, xs, b), "projection");
 }
 
 template <typename T>
@@ -601,32 +1097,43 @@ static moe_status_t launch_lora(const moe_lora_args_t* a, const LoraPlan& q, Lor
   const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
   const bool adapters = p.S > 0;
   p.wait_first = !adapters;
-  CUtensorMap w, x, b;
+  CUtensorMap w, x, xs, b;
   const int64_t x_stride = p.T > 1 ? p.x_stride : p.K;
   if (!make_map16(&w, bf16, a->weight, p.N, p.K, p.K, moe::LG_M) ||
-      !make_map16(&x, bf16, a->x, p.T, p.K, x_stride, q.nt))
+      !make_map16(&x, bf16, a->x, p.T, p.K, x_stride, q.pair ? moe::RUN : q.nt))
     return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the projection");
-  b = w;
+  b = xs = x;
   if (adapters) {
-    if (!make_map16(&b, bf16, a->lora_b, p.S * p.N, p.R, p.R, moe::LG_M))
-      return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for lora_b");
-    auto kernel = moe::lora_shrink_kernel<T>;
-    const int r16 = (int)((p.R + 15) & ~15);
-    const size_t smem = (size_t)moe::SH_STAGES * (moe::SH_X_BYTES + r16 * 128);
+    if (q.pair) {
+      p.xs = static_cast<int32_t*>(a->workspace) + q.order_words;
+      if (!make_map16(&b, bf16, a->lora_b, p.S * p.N, p.R, p.R, moe::LP_HALF) ||
+          !make_map16(&xs, bf16, p.xs, q.places, p.K, p.K, moe::RUN))
+        return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the adapters");
+      int32_t* order = static_cast<int32_t*>(a->workspace);
+      int32_t* scratch = order + q.places;
+      moe_status_t st =
+          launch_token_order(p.ids, p.T, p.S, moe::RUN, order, q.places, scratch, s);
+      if (st != MOE_OK) return st;
+      p.order = order;
+      p.places = scratch + p.S + 1;
+    }
     moe_status_t st = allow_smem<moe::lora_shrink_kernel<T>>(
         moe::SH_STAGES * (moe::SH_X_BYTES + moe::LORA_MAX_RANK * 128));
     if (st != MOE_OK) return st;
-    st = launched(
-        launch_pdl(kernel, dim3((unsigned)q.tiles, (unsigned)q.shares, (unsigned)q.zs),
-                   dim3(moe::SH_THREADS), smem, s, p), "adapter");
+    const int r16 = (int)((p.R + 15) & ~15);
+    st = launched(launch_pdl(moe::lora_shrink_kernel<T>,
+                             dim3((unsigned)q.tiles, (unsigned)q.shares, (unsigned)q.zs),
+                             dim3(moe::SH_THREADS),
+                             (size_t)moe::SH_STAGES * (moe::SH_X_BYTES + r16 * 128), s, p),
+                  "adapter");
     if (st != MOE_OK) return st;
   }
+  if (q.pair) return launch_pair<T>(p, q.places, w, x, xs, b, s);
   switch (q.nt) {
-    case 16: return launch_gemm<T, 16>(p, w, x, b, s);
-    case 32: return launch_gemm<T, 32>(p, w, x, b, s);
-    case 64: return launch_gemm<T, 64>(p, w, x, b, s);
-    case 128: return launch_gemm<T, 128>(p, w, x, b, s);
-    default: return launch_gemm<T, 256>(p, w, x, b, s);
+    case 16: return launch_split<T, 16>(p, w, x, s);
+    case 32: return launch_split<T, 32>(p, w, x, s);
+    case 64: return launch_split<T, 64>(p, w, x, s);
+    default: return launch_split<T, 128>(p, w, x, s);
   }
 }
 
@@ -640,8 +1147,8 @@ size_t moe_lora_workspace_size(int64_t num_tokens, int64_t in_features, int64_t 
                                int64_t num_adapters, int64_t rank) {
   if (num_tokens <= 0 || in_features <= 0 || out_features <= 0 || num_adapters <= 0 || rank <= 0)
     return 0;
-  const LoraPlan q = lora_plan(num_tokens, in_features, out_features, num_adapters);
-  return (size_t)q.shares * num_tokens * rank * 4;
+  return lora_workspace(lora_plan(num_tokens, in_features, out_features, num_adapters), num_tokens,
+                        rank);
 }
 
 moe_status_t moe_lora_linear(const moe_lora_args_t* a, void* stream) {
@@ -674,7 +1181,7 @@ moe_status_t moe_lora_linear(const moe_lora_args_t* a, void* stream) {
     return set_error(MOE_ERR_UNSUPPORTED, "problem too large for 32-bit tile coordinates");
   const LoraPlan q = lora_plan(T, K, N, S);
   if (S > 0) {
-    const size_t need = (size_t)q.shares * T * R * 4;
+    const size_t need = lora_workspace(q, T, R);
     if (a->workspace == nullptr || a->workspace_bytes < need)
       return set_error(MOE_ERR_WORKSPACE, "the adapters need %zu bytes of workspace, got %zu", need,
                        a->workspace_bytes);
@@ -690,11 +1197,12 @@ moe_status_t moe_lora_linear(const moe_lora_args_t* a, void* stream) {
   p.x = a->x;
   p.x_stride = a->x_stride0;
   p.a = a->lora_a;
+  p.b = a->lora_b;
   p.ids = a->adapter_ids;
   p.scale = a->lora_scale;
   p.out = a->out;
   p.out_stride = a->out_stride0;
-  p.h = static_cast<float*>(a->workspace);
+  p.h = static_cast<float*>(a->workspace) + q.order_words + q.copy_words;
   p.shares = q.shares;
   p.share_k = q.share_k;
   p.splits = q.splits;

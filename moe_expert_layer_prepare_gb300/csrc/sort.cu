@@ -26,7 +26,10 @@ constexpr int SORT_MAX_BLOCKS = 128;
 struct SortParams {
   const void* ids;
   int ids64;
+  int none_last;  // ids outside [0, E - 1) count as E - 1 (adapters: tokens without one)
+  int align;       // experts begin at multiples of this, the rows between are -1
   int32_t R, E, blocks, per_block;  // per_block: a multiple of SORT_THREADS
+  int32_t rows;    // length of row_route
   int32_t* offsets;
   int32_t* route_row;
   int32_t* row_route;
@@ -38,6 +41,7 @@ struct SortParams {
 __device__ __forceinline__ int route_expert(const SortParams& p, int r, bool* bad) {
   const int64_t id = p.ids64 ? static_cast<const int64_t*>(p.ids)[r]
                              : (int64_t)static_cast<const int32_t*>(p.ids)[r];
+  if (p.none_last) return id >= 0 && id < p.E ? (int)id : p.E - 1;
   if (id >= p.E) *bad = true;
   return id >= 0 && id < p.E ? (int)id : -1;
 }
@@ -106,7 +110,8 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_place_kernel(SortParams p) 
         }
       }
     }
-    int incl = all;
+    const int room = (all + p.align - 1) / p.align * p.align;
+    int incl = room;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
@@ -120,8 +125,12 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_place_kernel(SortParams p) 
       carry += warp_total[w];
     }
     if (e < p.E) {
-      base[e] = below + incl - all + before;
-      if (blockIdx.x == 0) p.offsets[e] = below + incl - all;
+      const int start = below + incl - room;
+      base[e] = start + before;
+      if (blockIdx.x == 0) {
+        p.offsets[e] = start;
+        for (int r = start + all; r < start + room; ++r) p.row_route[r] = -1;
+      }
     }
     __syncthreads();
   }
@@ -141,7 +150,7 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_place_kernel(SortParams p) 
     if (e >= 0 && (same & lanemask_lt()) == 0) table[warp][e] += (uint16_t)__popc(same);
     __syncwarp();
   }
-  for (int64_t r = (int64_t)carry + (int64_t)blockIdx.x * SORT_THREADS + tid; r < p.R;
+  for (int64_t r = (int64_t)carry + (int64_t)blockIdx.x * SORT_THREADS + tid; r < p.rows;
        r += (int64_t)gridDim.x * SORT_THREADS)
     p.row_route[r] = -1;
 }
@@ -358,6 +367,43 @@ static void sort_split(int64_t R, int32_t* blocks, int32_t* per_block) {
   *blocks = (int32_t)((R + per - 1) / per);
 }
 
+static moe_status_t launch_sort(const SortParams& p, cudaStream_t s) {
+  if (p.blocks > 1) {
+    moe_status_t st = launched(launch_pdl(moe::sort_count_kernel, dim3(p.blocks),
+                                          dim3(moe::SORT_THREADS), 0, s, p), "sort count");
+    if (st != MOE_OK) return st;
+  }
+  return launched(launch_pdl(moe::sort_place_kernel, dim3(p.blocks), dim3(moe::SORT_THREADS), 0,
+                             s, p), "sort place");
+}
+
+// Tokens in the order of their adapters, those without one last: order[rows],
+// each adapter from a multiple of `align` on, -1 in between and at the end;
+// rows >= T + (align - 1) (S + 1).  Scratch: token_order_scratch() words, of which
+// scratch[S + 1] is then the number of places taken.
+size_t token_order_scratch(int64_t T, int64_t S) {
+  int32_t blocks, per;
+  sort_split(T, &blocks, &per);
+  return (size_t)((blocks > 1 ? blocks * (S + 1) : 0) + (S + 2) + T);
+}
+
+moe_status_t launch_token_order(const int32_t* adapter_ids, int64_t T, int64_t S, int align,
+                                int32_t* order, int64_t rows, int32_t* scratch, cudaStream_t s) {
+  SortParams p{};
+  p.ids = adapter_ids;
+  p.none_last = 1;
+  p.align = align;
+  p.R = (int32_t)T;
+  p.E = (int32_t)S + 1;
+  p.rows = (int32_t)rows;
+  sort_split(T, &p.blocks, &p.per_block);
+  p.offsets = scratch;
+  p.route_row = scratch + S + 2;
+  p.row_route = order;
+  p.hist = scratch + S + 2 + T;
+  return launch_sort(p, s);
+}
+
 template <typename K>
 static dim3 one_wave(K kernel, int64_t blocks, int threads) {
   const int64_t cap =
@@ -411,7 +457,8 @@ moe_status_t moe_sort_routes(const void* topk_ids, int32_t topk_ids_dtype, int64
   SortParams p{};
   p.ids = topk_ids;
   p.ids64 = topk_ids_dtype == MOE_IDS_INT64;
-  p.R = (int32_t)R;
+  p.align = 1;
+  p.R = p.rows = (int32_t)R;
   p.E = (int32_t)num_experts;
   sort_split(R > 0 ? R : 1, &p.blocks, &p.per_block);
   p.offsets = expert_offsets;
@@ -427,12 +474,8 @@ moe_status_t moe_sort_routes(const void* topk_ids, int32_t topk_ids_dtype, int64
                        workspace_bytes);
     if ((reinterpret_cast<uintptr_t>(workspace) & 3u) != 0)
       return set_error(MOE_ERR_ALIGNMENT, "workspace must be 4-byte aligned");
-    moe_status_t st = launched(launch_pdl(moe::sort_count_kernel, dim3(p.blocks),
-                                          dim3(moe::SORT_THREADS), 0, s, p), "sort count");
-    if (st != MOE_OK) return st;
   }
-  return launched(launch_pdl(moe::sort_place_kernel, dim3(p.blocks), dim3(moe::SORT_THREADS), 0,
-                             s, p), "sort place");
+  return launch_sort(p, s);
 }
 
 moe_status_t moe_permute(const void* x, int64_t x_stride0, int32_t dtype, int64_t num_tokens,

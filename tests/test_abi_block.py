@@ -160,7 +160,7 @@ def test_lora(lib):
     assert lora(rank=-8) == INVALID
     assert lora(dtype=B.MOE_DTYPE_FP32) == UNSUPPORTED and lora(dtype=5) == INVALID
     assert lora(in_features=0) == SHAPE and lora(rank=0) == SHAPE
-    assert lora(rank=136) == UNSUPPORTED and lora(num_adapters=4097) == UNSUPPORTED
+    assert lora(rank=136) == UNSUPPORTED and lora(num_adapters=1024) == UNSUPPORTED
     for name in ("x", "weight", "out", "lora_a", "lora_b", "adapter_ids", "lora_scale"):
         assert lora(**{name: None}) == INVALID
     assert lora(x_stride0=63) == SHAPE and lora(out_stride0=31) == SHAPE

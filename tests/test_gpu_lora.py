@@ -82,7 +82,8 @@ def check(p, **kw):
     (16, 1000, 257, 20, 16), (17, 512, 130, 5, 32), (33, 2048, 384, 40, 32),
     (64, 256, 129, 70, 40), (65, 320, 300, 4, 64), (128, 4096, 256, 9, 72),
     (129, 136, 64, 3, 128), (257, 264, 140, 6, 16), (300, 1032, 260, 30, 48),
-    (700, 512, 512, 2, 128), (1500, 192, 72, 100, 8)])
+    (512, 192, 264, 11, 64), (513, 72, 513, 5, 8), (700, 512, 512, 2, 128), (1500, 192, 72, 100, 8),
+    (2100, 136, 300, 24, 48)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("order", ["mixed", "sorted"])
 def test_against_the_formula(T, K, N, S, R, dtype, order):
@@ -107,8 +108,22 @@ def test_every_token_its_own_adapter():
     check(p)
 
 
-def test_ids_out_of_range_and_nan_in_unused_adapters():
-    p = problem(30, 256, 200, 5, 16, "bf16")
+@pytest.mark.parametrize("T", [9, 100, 900])
+def test_a_broken_adapter_stays_with_its_tokens(T):
+    p = problem(T, 256, 200, 5, 40, "bf16")
+    q = dict(p, adapter_ids=torch.where(p["adapter_ids"] == 3, -1, p["adapter_ids"]))
+    p["lora_a"][3, 1] = float("inf")
+    p["lora_b"][3] = float("nan")
+    out = run(p)
+    others = (p["adapter_ids"] != 3).cpu()
+    ref, extra = expect(q)
+    assert_within(out[others], ref[others], rounded(ref, out.dtype, extra)[others], "others")
+    assert bool(torch.isnan(out.cpu()[~others]).all())
+
+
+@pytest.mark.parametrize("T", [30, 120, 800])
+def test_ids_out_of_range_and_nan_in_unused_adapters(T):
+    p = problem(T, 256, 200, 5, 16, "bf16")
     p["adapter_ids"][3] = 5
     p["adapter_ids"][4] = 2 ** 31 - 1
     p["adapter_ids"][p["adapter_ids"] == 2] = -7
@@ -171,7 +186,8 @@ def test_wait_timeout_sets_status_and_context_survives():
     from moe_expert_layer_prepare_gb300 import build
     test_lib = B.configure(ctypes.CDLL(build.build_test_variant("timeout")))
     regular = B.load()
-    for T, N in ((8, 256), (300, 20000)):  # eight CTAs share a tile's K; one each
+    # eight CTAs share a tile's K; one each; a pair of CTAs a tile
+    for T, N in ((8, 256), (300, 20000), (600, 512)):
         p = problem(T, 2048, N, 3, 16, "bf16")
         st = torch.zeros(1, dtype=torch.int32, device="cuda")
         B._lib = test_lib
