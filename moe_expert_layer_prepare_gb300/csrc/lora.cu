@@ -3,7 +3,8 @@
 //
 // lora_shrink_kernel gives h = x A_a^T as fp32 sums per share of K.  It reads A
 // and the rows of x, a few flops a byte, so it runs on mma.sync tiles fed by
-// cp.async; blocks take (64 tokens, share of K, share of the adapters among them).
+// cp.async; blocks take (64 or 128 tokens, share of K, share of the adapters among
+// them).
 //
 // The projection is on tcgen05, features by tokens: the accumulator's rows are
 // features (the MMA's A operand is a weight tile) and its columns tokens, so that
@@ -94,10 +95,12 @@ __device__ __forceinline__ int distinct_adapters(const int16_t* id, int16_t* fir
 }
 
 // ------------------------------------------------------------------ shrink
-constexpr int SH_TOK = 64;
 constexpr int SH_THREADS = 256;
 constexpr int SH_STAGES = 4;
-constexpr int SH_X_BYTES = SH_TOK * 128;
+constexpr int SH_MAX_TOK = 128;
+
+// Shared memory of a block of `tok` tokens.
+__host__ __device__ constexpr int sh_smem(int tok, int r16) { return SH_STAGES * (tok + r16) * 128; }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -139,18 +142,23 @@ __device__ __forceinline__ bool group_together(int tok) {
   return __all_sync(0xFFFFFFFFu, tok < 0 || tok == first + (int)(threadIdx.x & 31));
 }
 
-template <typename T>
-__global__ void __launch_bounds__(SH_THREADS) lora_shrink_kernel(LoraParams p) {
+// TOK tokens a block: eight warps as TOK / 16 rows of 16 tokens by 128 / TOK
+// shares of the ranks, each warp up to NT16 times 16 of them.
+template <typename T, int TOK, int NT16>
+__global__ void __launch_bounds__(SH_THREADS, 2) lora_shrink_kernel(LoraParams p) {
+  constexpr int XP = TOK / 32;                           // a thread's pieces of x
+  constexpr int NSPLIT = 128 / TOK;                      // shares of the ranks
+  constexpr int AP = (NT16 * NSPLIT * 16 + 31) / 32;     // a thread's pieces of A
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int16_t s_id[SH_TOK], s_first[SH_TOK], s_list[SH_TOK];
-  __shared__ int32_t s_tok[SH_TOK];
+  __shared__ int16_t s_id[TOK], s_first[TOK], s_list[TOK];
+  __shared__ int32_t s_tok[TOK];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t t0 = (int64_t)blockIdx.x * SH_TOK;
+  const int64_t t0 = (int64_t)blockIdx.x * TOK;
   if (p.order != nullptr && t0 >= *p.places) return;
   bool bad = false;
-  if (tid < SH_TOK) {
+  if (tid < TOK) {
     int64_t t = t0 + tid;
     if (p.order != nullptr) t = t < *p.places ? p.order[t] : -1;
     s_tok[tid] = (int32_t)t;
@@ -158,95 +166,134 @@ __global__ void __launch_bounds__(SH_THREADS) lora_shrink_kernel(LoraParams p) {
   }
   if (bad) set_status(p.status, MOE_DEV_BAD_ADAPTER);
   __syncthreads();
-  const int n_list = distinct_adapters(s_id, s_first, s_list, SH_TOK, tid, SH_THREADS,
-                                       [] { __syncthreads(); });
+  // Block z has the adapters z, z + gridDim.z, ... of these tokens; in the tokens'
+  // order that of group z, unless an earlier group has it.
+  int n_list;
+  if (p.order == nullptr) {
+    n_list = distinct_adapters(s_id, s_first, s_list, TOK, tid, SH_THREADS, [] { __syncthreads(); });
+  } else {
+    const int z = blockIdx.z;
+    bool mine = s_id[z * RUN] >= 0;
+    for (int g = 0; g < z; ++g) mine = mine && s_id[g * RUN] != s_id[z * RUN];
+    if (tid == 0) s_list[z] = s_id[z * RUN];
+    n_list = mine ? z + 1 : 0;
+    __syncthreads();
+  }
   const int64_t k0 = (int64_t)blockIdx.y * p.share_k;
   const int64_t k1 = min(p.K, k0 + p.share_k);
   const int slabs = k1 > k0 ? (int)((k1 - k0 + 63) / 64) : 0;
   const int R = (int)p.R, r16 = (R + 15) & ~15;
   const uint32_t base = smem_u32(smem);
-  const uint32_t stage_bytes = SH_X_BYTES + r16 * 128;
+  const uint32_t stage_bytes = (TOK + r16) * 128;
   const T* x = static_cast<const T*>(p.x);
-  const int m0 = (warp & 3) * 16, nh = warp >> 2;
+  const int m0 = (warp % (TOK / 16)) * 16, nh = warp / (TOK / 16);
 
-  if (p.order != nullptr && blockIdx.z == 0) {
-    // this share of the rows that the projection cannot fetch as they lie in x
-    T* xs = static_cast<T*>(p.xs);
-    for (int r = warp; r < SH_TOK; r += SH_THREADS / 32) {
-      const int tok = s_tok[r];
-      const bool apart = !group_together(s_tok[(r & ~(RUN - 1)) + lane]);
-      if (tok < 0 || !apart) continue;
-      const T* src = x + tok * p.x_stride;
-      T* dst = xs + (t0 + r) * p.K;
-      for (int64_t k = k0 + lane * 8; k < k1; k += 256)
-        store_pack<T, 8>(dst + k, load_pack<T, 8>(src + k));
+  if (p.order != nullptr) {
+    // of group z's rows, where the projection cannot fetch them as they lie in x,
+    // this share of K: 16-byte pieces, four in flight a thread
+    const int g0 = blockIdx.z * RUN;
+    if (!group_together(s_tok[g0 + lane])) {
+      T* xs = static_cast<T*>(p.xs);
+      const int pieces = (int)((k1 - k0) / 8);
+      for (int i0 = tid; i0 < RUN * pieces; i0 += 4 * SH_THREADS) {
+        Pack<T, 8> v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = i0 + u * SH_THREADS, r = i / pieces;
+          if (i < RUN * pieces && s_tok[g0 + r] >= 0)
+            v[u] = load_pack<T, 8>(x + s_tok[g0 + r] * p.x_stride + k0 + (i - r * pieces) * 8);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = i0 + u * SH_THREADS, r = i / pieces;
+          if (i < RUN * pieces && s_tok[g0 + r] >= 0)
+            store_pack<T, 8>(xs + (t0 + g0 + r) * p.K + k0 + (i - r * pieces) * 8, v[u]);
+        }
+      }
     }
   }
 
   // a thread's pieces: 16-byte piece c of rows row, row + 32, ...
   const int row = tid >> 3, c = tid & 7;
   const uint32_t at = base + tile_at(row, c);
+  // a lane's addresses for ldmatrix: row of the tile, and the permuted piece of
+  // each 16-wide K step (rows eight apart have the same permutation)
+  const uint32_t xrow = (uint32_t)(m0 + (lane & 15)) * 128;
+  const uint32_t arow = (uint32_t)(TOK + nh * 16 + (lane & 7) + ((lane >> 4) << 3)) * 128;
+  uint32_t xk[4], ak[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    xk[k] = xrow + (((uint32_t)(k * 2 + (lane >> 4)) ^ (lane & 7)) << 4);
+    ak[k] = arow + (((uint32_t)(k * 2 + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
+  }
   for (int d = blockIdx.z; d < n_list; d += gridDim.z) {
     const int a = s_list[d];
     const T* A = static_cast<const T*>(p.a) + (int64_t)a * R * p.K;
-    const T *xp[2], *ap[4];
+    const T *xp[XP], *ap[AP];
     uint32_t take = 0;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < XP; ++j) {
       const bool t = s_id[row + 32 * j] == a;
       xp[j] = t ? x + s_tok[row + 32 * j] * p.x_stride + k0 + c * 8 : x;
       take |= (uint32_t)t << j;
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < AP; ++j) {
       const bool t = row + 32 * j < R;
       ap[j] = t ? A + (int64_t)(row + 32 * j) * p.K + k0 + c * 8 : A;
-      take |= (uint32_t)t << (2 + j);
+      take |= (uint32_t)t << (XP + j);
     }
-    auto load = [&](int slab) {
-      const uint32_t s = at + (uint32_t)(slab % SH_STAGES) * stage_bytes;
-      const uint32_t t = k0 + (int64_t)slab * 64 + c * 8 < k1 ? take : 0u;
+    int fill = 0;  // stage of the next load
+    int64_t left = k1 - k0 - c * 8;  // this thread's columns from the next load on
+    auto load = [&] {
+      const uint32_t s = at + (uint32_t)fill * stage_bytes;
+      const uint32_t t = left > 0 ? take : 0u;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        cp_async16(s + j * 4096, xp[j] + ((t >> j) & 1u ? slab * 64 : 0), (t >> j) & 1u);
+      for (int j = 0; j < XP; ++j) {
+        cp_async16(s + j * 4096, xp[j], (t >> j) & 1u);
+        xp[j] += (t >> j) & 1u ? 64 : 0;
+      }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (row + 32 * j < r16)
-          cp_async16(s + SH_X_BYTES + j * 4096, ap[j] + ((t >> (2 + j)) & 1u ? slab * 64 : 0),
-                     (t >> (2 + j)) & 1u);
+      for (int j = 0; j < AP; ++j)
+        if (row + 32 * j < r16) {
+          cp_async16(s + TOK * 128 + j * 4096, ap[j], (t >> (XP + j)) & 1u);
+          ap[j] += (t >> (XP + j)) & 1u ? 64 : 0;
+        }
+      left -= 64;
+      if (++fill == SH_STAGES) fill = 0;
     };
-    float acc[4][2][4];
+    float acc[NT16][2][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < NT16; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q) acc[i][j][q] = 0.0f;
     for (int s = 0; s < SH_STAGES - 1; ++s) {
-      if (s < slabs) load(s);
+      if (s < slabs) load();
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
+    uint32_t st = base;
     for (int s = 0; s < slabs; ++s) {
       asm volatile("cp.async.wait_group %0;" ::"n"(SH_STAGES - 2) : "memory");
       __syncthreads();
-      if (s + SH_STAGES - 1 < slabs) load(s + SH_STAGES - 1);
+      if (s + SH_STAGES - 1 < slabs) load();
       asm volatile("cp.async.commit_group;" ::: "memory");
-      const uint32_t xs = base + (s % SH_STAGES) * stage_bytes, as = xs + SH_X_BYTES;
 #pragma unroll
-      for (int k16 = 0; k16 < 4; ++k16) {
+      for (int k = 0; k < 4; ++k) {
         uint32_t av[4];
-        ldmatrix4(av, xs + tile_at(m0 + (lane & 15), k16 * 2 + (lane >> 4)));
+        ldmatrix4(av, st + xk[k]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int n0 = (i * 2 + nh) * 16;
-          if (n0 >= r16) break;
+        for (int i = 0; i < NT16; ++i) {
+          if ((i * NSPLIT + nh) * 16 >= r16) break;
           uint32_t bv[4];
-          ldmatrix4(bv, as + tile_at(n0 + (lane & 7) + ((lane >> 4) << 3),
-                                     k16 * 2 + ((lane >> 3) & 1)));
+          ldmatrix4(bv, st + ak[k] + i * NSPLIT * 2048);
           mma_16816<T>(acc[i][0], av, bv[0], bv[1]);
           mma_16816<T>(acc[i][1], av, bv[2], bv[3]);
         }
       }
+      st += stage_bytes;
+      if (st == base + SH_STAGES * stage_bytes) st = base;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();  // the stages are free for the next adapter
@@ -256,10 +303,10 @@ __global__ void __launch_bounds__(SH_THREADS) lora_shrink_kernel(LoraParams p) {
       const int r = m0 + (lane >> 2) + half * 8;
       if (s_id[r] != a) continue;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < NT16; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int n = (i * 2 + nh) * 16 + j * 8 + (lane & 3) * 2;
+          const int n = (i * NSPLIT + nh) * 16 + j * 8 + (lane & 3) * 2;
           if (n < R)
             *reinterpret_cast<float2*>(h + (int64_t)s_tok[r] * R + n) =
                 make_float2(acc[i][j][half * 2], acc[i][j][half * 2 + 1]);
@@ -977,7 +1024,7 @@ struct LoraPlan {
   int64_t places;                   // most places of the tokens' order (pair)
   int64_t order_words;              // of the workspace: order and the sort's scratch
   int64_t copy_words;               // of the workspace: x in that order
-  int tiles, shares, share_k, zs;   // shrink
+  int tok, tiles, shares, share_k, zs;  // shrink: tokens a block
   int nt, splits;                   // lora_split_kernel
 };
 
@@ -987,20 +1034,22 @@ static LoraPlan lora_plan(int64_t T, int64_t K, int64_t N, int64_t S) {
   q.pair = T > moe::SPLIT_TOKENS;
   q.places = T;
   if (q.pair && S > 0) {
-    q.places = (T + (moe::RUN - 1) * (S + 1) + 63) / 64 * 64;
+    q.places = (T + (moe::RUN - 1) * (S + 1) + 127) / 128 * 128;
     q.order_words = (q.places + (int64_t)token_order_scratch(T, S) + 3) / 4 * 4;
     q.copy_words = (q.places * K / 2 + 3) / 4 * 4;
   }
-  // Shrink: one block for each adapter that 64 tokens may have, or for all of
-  // them where the order leaves two at most; shares of K, at least 256 wide, until
-  // about four blocks an SM.
-  q.tiles = (int)((q.places + moe::SH_TOK - 1) / moe::SH_TOK);
-  int64_t z = S < moe::SH_TOK ? S : moe::SH_TOK;
-  if (T < z) z = T;
-  if (q.pair || z < 1) z = 1;
-  const int64_t most = q.tiles >= 4 * sms ? 1 : (4 * sms + q.tiles - 1) / q.tiles;
-  q.zs = (int)(z < most ? z : most);
-  int64_t shares = (4 * sms) / ((int64_t)q.tiles * q.zs);
+  // Shrink: 64 tokens as they come, or 128 in their order, and a block for each
+  // adapter that these may have (in the order a group of RUN has one).  A block
+  // whose tokens have fewer ends at once, so K is dealt out, in shares at least 256
+  // wide, by the number of adapters that they have on average.
+  q.tok = q.pair ? 128 : 64;
+  q.tiles = (int)((q.places + q.tok - 1) / q.tok);
+  const int64_t groups = q.pair ? q.tok / moe::RUN : (T < q.tok ? T : q.tok);
+  q.zs = (int)(S < groups ? (S < 1 ? 1 : S) : groups);
+  if (q.pair) q.zs = (int)groups;  // block z copies group z's rows too
+  double live = q.pair ? 1.0 + (double)S * q.tok / (double)T : q.zs;
+  if (live > q.zs) live = q.zs;
+  int64_t shares = (int64_t)(2.0 * sms / (q.tiles * live));
   if (shares > (K + 255) / 256) shares = (K + 255) / 256;
   if (shares > 16) shares = 16;
   if (shares < 1) shares = 1;
@@ -1064,6 +1113,17 @@ static cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, int threa
 
 constexpr int kMaxSmem = 232448;
 
+template <typename T, int TOK, int NT16>
+static moe_status_t launch_shrink(const LoraPlan& q, const LoraParams& p, cudaStream_t s) {
+  constexpr auto kernel = moe::lora_shrink_kernel<T, TOK, NT16>;
+  moe_status_t st = allow_smem<kernel>(moe::sh_smem(TOK, moe::LORA_MAX_RANK));
+  if (st != MOE_OK) return st;
+  const int r16 = (int)((p.R + 15) & ~15);
+  return launched(launch_pdl(kernel, dim3((unsigned)q.tiles, (unsigned)q.shares, (unsigned)q.zs),
+                             dim3(moe::SH_THREADS), (size_t)moe::sh_smem(TOK, r16), s, p),
+                  "adapter");
+}
+
 template <typename T, int NT>
 static moe_status_t launch_split(const LoraParams& p, const CUtensorMap& w, const CUtensorMap& x,
                                  cudaStream_t s) {
@@ -1117,15 +1177,15 @@ static moe_status_t launch_lora(const moe_lora_args_t* a, const LoraPlan& q, Lor
       p.order = order;
       p.places = scratch + p.S + 1;
     }
-    moe_status_t st = allow_smem<moe::lora_shrink_kernel<T>>(
-        moe::SH_STAGES * (moe::SH_X_BYTES + moe::LORA_MAX_RANK * 128));
-    if (st != MOE_OK) return st;
-    const int r16 = (int)((p.R + 15) & ~15);
-    st = launched(launch_pdl(moe::lora_shrink_kernel<T>,
-                             dim3((unsigned)q.tiles, (unsigned)q.shares, (unsigned)q.zs),
-                             dim3(moe::SH_THREADS),
-                             (size_t)moe::SH_STAGES * (moe::SH_X_BYTES + r16 * 128), s, p),
-                  "adapter");
+    const int t16 = (int)((p.R + 15) / 16);
+    moe_status_t st;
+    if (q.tok == 64)
+      st = t16 <= 2 ? launch_shrink<T, 64, 1>(q, p, s)
+                    : (t16 <= 4 ? launch_shrink<T, 64, 2>(q, p, s) : launch_shrink<T, 64, 4>(q, p, s));
+    else
+      st = t16 <= 2 ? launch_shrink<T, 128, 2>(q, p, s)
+                    : (t16 <= 4 ? launch_shrink<T, 128, 4>(q, p, s)
+                                : launch_shrink<T, 128, 8>(q, p, s));
     if (st != MOE_OK) return st;
   }
   if (q.pair) return launch_pair<T>(p, q.places, w, x, xs, b, s);
