@@ -636,8 +636,8 @@ size_t moe_block_norm_workspace_size(int64_t num_tokens, int64_t hidden_size);
 /*   h[t, r] = sum_k x[t, k] * lora_a[a, r, k],  a = adapter_ids[t];          */
 /* tokens with a < 0 (no adapter; a >= num_adapters also sets                 */
 /* MOE_DEV_BAD_ADAPTER) take the first sum alone.  Sums are in fp32; scale*h  */
-/* enters the second product in fp32, or for long batches as two values of    */
-/* the tensors' type (its rounding and the remainder); out is rounded once.   */
+/* enters the second product as two values of the tensors' type, its rounding */
+/* and the remainder; out is rounded once.                                    */
 /* An adapter's values, non-finite ones too, reach its own tokens alone.      */
 /* x [T, K] and out [T, N]: inner stride 1, row strides of their own; weight  */
 /* [N, K], lora_a [S, R, K], lora_b [S, N, R] contiguous; adapter_ids int32   */

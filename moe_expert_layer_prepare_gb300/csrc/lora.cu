@@ -14,8 +14,8 @@
 //   Up to SPLIT_TOKENS tokens (lora_split_kernel): W is streamed once or a few
 //   times, so HBM bounds it.  With few tiles the K slabs are dealt out to the CTAs of
 //   a cluster and the sums joined through distributed shared memory in rank order.
-//   The adapters' second product, R products for each (token, feature), is done in
-//   fp32 by the threads that join, each reading its feature's row of B_a.
+//   The adapters' second product is done meanwhile by warps that have no part in the
+//   main loop, on mma.sync tiles of 16 features by 8 tokens of one adapter.
 //
 //   Above (lora_pair_kernel): the tensor cores bound it.  CTA pairs keep 256 x 256
 //   tiles and two accumulators, one in use while the other is written out.  Tokens
@@ -24,10 +24,11 @@
 //   there, others from a copy that the shrink writes in that order.  A tile's
 //   columns are then runs of one adapter each, and the second product enters the
 //   accumulator as further K steps on the columns of a run alone: B_a's rows as the A
-//   operand, s_a h as the B operand.  So an adapter's values reach its own tokens only
-//   (a non-finite weight stays with them).  As the MMA takes 16-bit operands, s_a h
-//   enters as its rounding and the rounded remainder, which keeps the adapters' part as
-//   exact as the rest.
+//   operand, s_a h as the B operand.
+//
+// In both an adapter's values reach its own tokens only (a non-finite weight stays
+// with them), and as the MMA takes 16-bit operands, s_a h enters as its rounding and
+// the rounded remainder, which keeps the adapters' part as exact as the rest.
 //
 // The projection's launch starts while the shrink still runs and waits for it only
 // where h is read.
@@ -71,27 +72,28 @@ __device__ __forceinline__ int adapter_of(const LoraParams& p, int64_t t, bool* 
   return a >= 0 && a < p.S ? a : -1;
 }
 
-// Distinct values >= 0 of id[0, n) in order of first appearance: list and its
-// length.  All `threads` threads call it, n <= threads or strided; sync() is
-// their barrier.
-template <typename Sync>
-__device__ __forceinline__ int distinct_adapters(const int16_t* id, int16_t* first, int16_t* list,
-                                                 int n, int tid, int threads, Sync sync) {
-  for (int i = tid; i < n; i += threads) {
-    bool is = id[i] >= 0;
-    for (int j = 0; j < i && is; ++j) is = id[j] != id[i];
-    first[i] = is;
+// The distinct ids >= 0 among id[0, n), n <= blockDim.x, in ascending order, by a
+// bitmap; list and its length.  All threads of the block call it.
+__device__ __forceinline__ int distinct_adapters(const int16_t* id, int16_t* list, uint32_t* bits,
+                                                 int* count, int n) {
+  const int tid = threadIdx.x;
+  if (tid < 32) bits[tid] = 0;
+  __syncthreads();
+  if (tid < n && id[tid] >= 0) atomicOr(&bits[id[tid] >> 5], 1u << (id[tid] & 31));
+  __syncthreads();
+  if (tid < 32) {
+    uint32_t w = bits[tid];
+    int incl = __popc(w);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (tid >= o) incl += v;
+    }
+    if (tid == 31) *count = incl;
+    for (int at = incl - __popc(w); w != 0; w &= w - 1) list[at++] = (int16_t)(tid * 32 + __ffs(w) - 1);
   }
-  sync();
-  int count = 0;
-  for (int i = tid; i < n; i += threads) {
-    int rank = 0;
-    for (int j = 0; j < i; ++j) rank += first[j];
-    if (first[i]) list[rank] = id[i];
-  }
-  for (int j = 0; j < n; ++j) count += first[j];
-  sync();
-  return count;
+  __syncthreads();
+  return *count;
 }
 
 // ------------------------------------------------------------------ shrink
@@ -150,8 +152,10 @@ __global__ void __launch_bounds__(SH_THREADS, 2) lora_shrink_kernel(LoraParams p
   constexpr int NSPLIT = 128 / TOK;                      // shares of the ranks
   constexpr int AP = (NT16 * NSPLIT * 16 + 31) / 32;     // a thread's pieces of A
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int16_t s_id[TOK], s_first[TOK], s_list[TOK];
+  __shared__ int16_t s_id[TOK], s_list[TOK];
   __shared__ int32_t s_tok[TOK];
+  __shared__ uint32_t s_bits[32];
+  __shared__ int s_n;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   pdl_launch_dependents();
@@ -170,7 +174,7 @@ __global__ void __launch_bounds__(SH_THREADS, 2) lora_shrink_kernel(LoraParams p
   // order that of group z, unless an earlier group has it.
   int n_list;
   if (p.order == nullptr) {
-    n_list = distinct_adapters(s_id, s_first, s_list, TOK, tid, SH_THREADS, [] { __syncthreads(); });
+    n_list = distinct_adapters(s_id, s_list, s_bits, &s_n, TOK);
   } else {
     const int z = blockIdx.z;
     bool mine = s_id[z * RUN] >= 0;
@@ -326,82 +330,111 @@ constexpr int LG_MAX_STAGES = 5;
 // Stages of the ring for a tile of NT tokens: two CTAs share an SM up to NT = 64.
 constexpr int lg_stages(int nt) { return nt <= 32 ? 5 : 4; }
 constexpr int lg_ring(int nt) { return lg_stages(nt) * (LG_A_BYTES + nt * 128); }
-// Shared memory: ring, s h of this CTA's share of the tokens, barriers, ids, order.
+// Shared memory: ring; of this CTA's share of the tokens s h (rounding, remainder)
+// and the adapters' part; barriers, ids, order, chunks.
 __host__ __device__ inline int lg_smem(int nt, int splits, int R) {
-  return 1024 + lg_ring(nt) + nt / splits * R * 4 + 256 + nt * 4;
+  return 1024 + lg_ring(nt) + (R > 0 ? nt / splits * (R + LG_M) * 4 : 0) + 256 + nt * 12;
 }
 
-// Sum of the cluster's partial sums at this shared address, in rank order.
-template <int SPLITS>
-__device__ __forceinline__ float join_sum(uint32_t at) {
-  float v[SPLITS];
-#pragma unroll
-  for (int r = 0; r < SPLITS; ++r) v[r] = ld_cluster(at, r);
-#pragma unroll
-  for (int r = 1; r < SPLITS; ++r) v[0] += v[r];
-  return v[0];
-}
+// Tokens of one adapter, neighbours in the order, at most 8: one MMA tile.
+struct Chunk {
+  int16_t pos, count, adapter, unused;
+};
 
-// Joins token positions [i0, i1) of this CTA's share for feature n, adds the
-// adapters' part and stores them.  G tokens are in flight, each with its feature's
-// row of B (RV 16-byte pieces), which tokens of one adapter, neighbours in the
-// order, share.
-template <typename T, int RV, int G>
-__device__ __forceinline__ void join_tokens(const LoraParams& p, const int16_t* id,
-                                            const int16_t* order, const float* hs, int64_t t0,
-                                            int pos0, int i0, int i1, int64_t n, uint32_t red) {
+// The adapters' part of a share of the tokens, add[token][LG_M features], with
+// mma.sync: 16 features by 8 tokens a task, dealt out to the warps, U tasks in
+// flight.  Any order of the ranks serves as long as both operands have the same:
+// lane q of four takes ranks 8 q .. 8 q + 7 of every 32 for two K steps, so a
+// feature's row of B comes in 16-byte loads, end to end over the four lanes.
+// hs: s h of the share, [token][R] its rounding, then the same of the remainder.
+template <typename T, int RS, int U>  // RS: K of the tasks, 32 ranks each
+__device__ __forceinline__ void expand_tokens(const LoraParams& p, const Chunk* chunks, int n,
+                                              const T* hs, int share, float* add, int64_t n0,
+                                              int warp, int warps) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int R = (int)p.R;
-  const T* B = static_cast<const T*>(p.b) + n * R;
-  const int64_t per_adapter = p.N * R;
-  Pack<T, 8> last[RV];
-  int last_a = -1;
-  for (int i = i0; i < i1; i += G) {
-    Pack<T, 8> row[G][RV];
-    int a[G], c[G];
-    float sum[G];
+  const T* B = static_cast<const T*>(p.b) + n0 * R;
+  const T* low = hs + share * R;
+  const int tasks = n * (LG_M / 16);
+  for (int k0 = warp * U; k0 < tasks; k0 += warps * U) {
+    uint4 b[U][RS][2];  // rows g and g + 8
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      c[g] = i + g < i1 ? order[pos0 + i + g] : 0;
-      a[g] = i + g < i1 ? id[c[g]] : -1;
-      if (a[g] >= 0 && a[g] == (g > 0 ? a[g - 1] : last_a)) {
+    for (int u = 0; u < U; ++u) {
+      const int k = min(k0 + u, tasks - 1), f = (k % (LG_M / 16)) * 16 + g;
+      const int a = chunks[k / (LG_M / 16)].adapter;
 #pragma unroll
-        for (int v = 0; v < RV; ++v) row[g][v] = g > 0 ? row[g - 1][v] : last[v];
-      } else if (a[g] >= 0) {
+      for (int s = 0; s < RS; ++s)
 #pragma unroll
-        for (int v = 0; v < RV; ++v)
-          row[g][v] = v * 8 < R ? load_pack<T, 8>(B + a[g] * per_adapter + v * 8) : zero_pack<T, 8>();
-      }
-    }
-    last_a = a[G - 1];
-#pragma unroll
-    for (int v = 0; v < RV; ++v) last[v] = row[G - 1][v];
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const uint32_t at = red + (uint32_t)c[g] * LG_M * 4;
-      sum[g] = p.splits == 1 ? join_sum<1>(at)
-                             : (p.splits == 2 ? join_sum<2>(at)
-                                              : (p.splits == 4 ? join_sum<4>(at) : join_sum<8>(at)));
+        for (int e = 0; e < 2; ++e) {
+          const int r = s * 32 + q * 8;
+          b[u][s][e] = make_uint4(0, 0, 0, 0);
+          if (a >= 0 && r < R && n0 + f + e * 8 < p.N)
+            b[u][s][e] = __ldg(reinterpret_cast<const uint4*>(
+                B + ((int64_t)a * p.N + f + e * 8) * R + r));
+        }
     }
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      if (i + g >= i1) break;
-      if (t0 + c[g] >= p.T) continue;
-      float2 acc = both(0.0f);
-      if (a[g] >= 0) {
-        const float4* h = reinterpret_cast<const float4*>(hs + (i + g) * R);
+    for (int u = 0; u < U; ++u) {
+      if (k0 + u >= tasks) break;
+      const Chunk c = chunks[(k0 + u) / (LG_M / 16)];
+      const int f = ((k0 + u) % (LG_M / 16)) * 16 + g;
+      float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int v = 0; v < RV; ++v) {
-          if (v * 8 >= R) break;
+      for (int s = 0; s < RS; ++s) {
+        const int r = s * 32 + q * 8;
+        uint4 h[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        if (c.adapter >= 0 && g < c.count && r < R) {  // token g of the chunk
+          h[0] = *reinterpret_cast<const uint4*>(hs + (c.pos + g) * R + r);
+          h[1] = *reinterpret_cast<const uint4*>(low + (c.pos + g) * R + r);
+        }
+        const uint4 b0 = b[u][s][0], b1 = b[u][s][1];
+        const uint32_t a0[4] = {b0.x, b1.x, b0.y, b1.y}, a1[4] = {b0.z, b1.z, b0.w, b1.w};
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const float4 f = h[v * 2 + q];
-            acc = fma2(make_float2(f.x, f.y), row[g][v].get2(2 * q), acc);
-            acc = fma2(make_float2(f.z, f.w), row[g][v].get2(2 * q + 1), acc);
-          }
+        for (int part = 0; part < 2; ++part) {
+          mma_16816<T>(acc, a0, h[part].x, h[part].y);
+          mma_16816<T>(acc, a1, h[part].z, h[part].w);
         }
       }
-      static_cast<T*>(p.out)[(t0 + c[g]) * p.out_stride + n] =
-          from_f32<T>(sum[g] + (acc.x + acc.y));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {  // feature f (+ 8), token 2 q (+ 1)
+        const int t = q * 2 + (e & 1);
+        if (t < c.count) add[(c.pos + t) * LG_M + f + (e >> 1) * 8] = acc[e];
+      }
+    }
+  }
+}
+
+// Stores the share's tokens: the cluster's sums in rank order and the adapters' part.
+template <typename T, int SPLITS>
+__device__ __forceinline__ void join_tokens(const LoraParams& p, const float* sums,
+                                            const float* add, const int16_t* order, int64_t t0,
+                                            int64_t n0, int pos0, int share) {
+  const uint32_t at0 = smem_u32(sums);
+  const bool pairs = (p.out_stride % 2 == 0) && (reinterpret_cast<uintptr_t>(p.out) & 3u) == 0;
+  for (int i = threadIdx.x; i < share * (LG_M / 4); i += LG_THREADS) {
+    const int k = i / (LG_M / 4), c = order[pos0 + k], f = (i % (LG_M / 4)) * 4;
+    if (t0 + c >= p.T) continue;
+    float4 v[SPLITS];
+#pragma unroll
+    for (int r = 0; r < SPLITS; ++r)
+      v[r] = SPLITS == 1 ? *reinterpret_cast<const float4*>(sums + c * LG_M + f)
+                         : ld_cluster4(at0 + (uint32_t)(c * LG_M + f) * 4, r);
+#pragma unroll
+    for (int r = 1; r < SPLITS; ++r)
+      v[0].x += v[r].x, v[0].y += v[r].y, v[0].z += v[r].z, v[0].w += v[r].w;
+    if (add != nullptr) {
+      const float4 u = *reinterpret_cast<const float4*>(add + k * LG_M + f);
+      v[0].x += u.x, v[0].y += u.y, v[0].z += u.z, v[0].w += u.w;
+    }
+    T* out = static_cast<T*>(p.out) + (t0 + c) * p.out_stride + n0 + f;
+    if (pairs && n0 + f + 4 <= p.N) {
+      reinterpret_cast<uint32_t*>(out)[0] = pack2<T>(make_float2(v[0].x, v[0].y));
+      reinterpret_cast<uint32_t*>(out)[1] = pack2<T>(make_float2(v[0].z, v[0].w));
+    } else {
+      const float w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n0 + f + e < p.N) out[e] = from_f32<T>(w[e]);
     }
   }
 }
@@ -417,12 +450,15 @@ __global__ void __launch_bounds__(LG_THREADS, NT <= 64 ? 2 : 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const int share = NT / p.splits;
-  float* hs = reinterpret_cast<float*>(smem + STAGES * STAGE_BYTES);  // [share][R]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(hs + share * p.R);
+  T* hs = reinterpret_cast<T*>(smem + STAGES * STAGE_BYTES);  // [2][share][R]
+  float* add = reinterpret_cast<float*>(hs + 2 * share * p.R);  // [share][LG_M]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(add + (p.S > 0 ? share * LG_M : 0));
   // full[STAGES], empty[STAGES], done
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * LG_MAX_STAGES + 1);
   int* s_abort = reinterpret_cast<int*>(tmem_holder + 1);
-  int16_t* s_id = reinterpret_cast<int16_t*>(reinterpret_cast<uint8_t*>(bars) + 256);
+  int* s_chunks = s_abort + 1;
+  Chunk* chunks = reinterpret_cast<Chunk*>(reinterpret_cast<uint8_t*>(bars) + 256);  // [NT]
+  int16_t* s_id = reinterpret_cast<int16_t*>(chunks + NT);
   int16_t* s_order = s_id + NT;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -534,29 +570,65 @@ __global__ void __launch_bounds__(LG_THREADS, NT <= 64 ? 2 : 1)
         s_order[before] = (int16_t)i;
       }
       side_sync();
-      // the rows of B that the join will read start towards L2
-      const T* B = static_cast<const T*>(p.b);
+      // chunks of the share: runs of an adapter, cut every 8 tokens; the rows of B
+      // that they will read start towards L2
+      const int pos0 = rank * share;
+      auto adapter = [&](int i) { return (int)s_id[s_order[pos0 + i]]; };
+      auto run_begin = [&](int i) {
+        int j = i;
+        while (j > 0 && adapter(j - 1) == adapter(i)) --j;
+        return j;
+      };
+      if (st == 0) *s_chunks = 0;
+      side_sync();
       for (int i = st; i < share; i += LG_SIDE) {
-        const int pos = rank * share + i, a = s_id[s_order[pos]];
-        if (a >= 0 && (i == 0 || s_id[s_order[pos - 1]] != a))
-          prefetch_l2(B + ((int64_t)a * p.N + n0) * p.R,
+        const int a = adapter(i), begin = run_begin(i);
+        if ((i - begin) % 8 != 0) continue;
+        int count = 1;
+        while (count < 8 && i + count < share && adapter(i + count) == a) ++count;
+        chunks[atomicAdd(s_chunks, 1)] = Chunk{(int16_t)i, (int16_t)count, (int16_t)a, 0};
+        if (a >= 0 && i == begin)
+          prefetch_l2(static_cast<const T*>(p.b) + ((int64_t)a * p.N + n0) * p.R,
                       (uint32_t)(min((int64_t)LG_M, p.N - n0) * p.R * 2));
       }
       if (!p.wait_first) pdl_wait();
       const int q4 = (int)p.R / 4;
       for (int i = st; i < share * q4; i += LG_SIDE) {
-        const int k = i / q4, c = s_order[rank * share + k], a = s_id[c];
+        const int k = i / q4, c = s_order[pos0 + k], a = s_id[c];
         if (a < 0) continue;
         float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         const float* src = p.h + (t0 + c) * p.R + (i - k * q4) * 4;
-        for (int s = 0; s < p.shares; ++s, src += p.T * p.R) {
-          const float4 u = __ldcg(reinterpret_cast<const float4*>(src));
-          sum.x += u.x, sum.y += u.y, sum.z += u.z, sum.w += u.w;
+        for (int s0 = 0; s0 < p.shares; s0 += 8) {  // eight shares' sums in flight
+          float4 u[8];
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+            u[s] = s0 + s < p.shares
+                       ? __ldcg(reinterpret_cast<const float4*>(src + (s0 + s) * p.T * p.R))
+                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+            sum.x += u[s].x, sum.y += u[s].y, sum.z += u[s].z, sum.w += u[s].w;
         }
         const float scale = __ldg(p.scale + a);
-        reinterpret_cast<float4*>(hs)[i] =
-            make_float4(scale * sum.x, scale * sum.y, scale * sum.z, scale * sum.w);
+        const float2 f[2] = {make_float2(scale * sum.x, scale * sum.y),
+                             make_float2(scale * sum.z, scale * sum.w)};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t hi = pack2<T>(f[e]);
+          const float2 h = unpack2<T>(hi);
+          reinterpret_cast<uint32_t*>(hs)[2 * i + e] = hi;
+          reinterpret_cast<uint32_t*>(hs + share * p.R)[2 * i + e] =
+              pack2<T>(make_float2(f[e].x - h.x, f[e].y - h.y));
+        }
       }
+      side_sync();
+      const int n = *s_chunks, w = warp - 2;
+      if (p.R <= 32)
+        expand_tokens<T, 1, 4>(p, chunks, n, hs, share, add, n0, w, LG_SIDE / 32);
+      else if (p.R <= 64)
+        expand_tokens<T, 2, 2>(p, chunks, n, hs, share, add, n0, w, LG_SIDE / 32);
+      else
+        expand_tokens<T, 4, 1>(p, chunks, n, hs, share, add, n0, w, LG_SIDE / 32);
     } else {
       for (int i = st; i < NT; i += LG_SIDE) s_id[i] = -1, s_order[i] = (int16_t)i;
     }
@@ -582,21 +654,19 @@ __global__ void __launch_bounds__(LG_THREADS, NT <= 64 ? 2 : 1)
     cluster_sync();
   else
     __syncthreads();
-  // Each CTA finishes its share of the tile's tokens, partial sums in rank order.
-  const int nl = tid % LG_M;
-  if (*abort_flag == 0 && n0 + nl < p.N) {
-    const uint32_t red = smem_u32(smem) + (uint32_t)nl * 4;
-    const int half = share / 2, i0 = tid < LG_M ? 0 : half, i1 = tid < LG_M ? half : share;
+  // Each CTA finishes its share of the tile's tokens.
+  if (*abort_flag == 0) {
+    const float* sums = reinterpret_cast<const float*>(smem);
+    const float* part = p.S > 0 ? add : nullptr;
     const int pos0 = rank * share;
-    const int64_t n = n0 + nl;
-    if (p.R <= 16)
-      join_tokens<T, 2, 4>(p, s_id, s_order, hs, t0, pos0, i0, i1, n, red);
-    else if (p.R <= 32)
-      join_tokens<T, 4, 4>(p, s_id, s_order, hs, t0, pos0, i0, i1, n, red);
-    else if (p.R <= 64)
-      join_tokens<T, 8, 2>(p, s_id, s_order, hs, t0, pos0, i0, i1, n, red);
+    if (p.splits == 1)
+      join_tokens<T, 1>(p, sums, part, s_order, t0, n0, pos0, share);
+    else if (p.splits == 2)
+      join_tokens<T, 2>(p, sums, part, s_order, t0, n0, pos0, share);
+    else if (p.splits == 4)
+      join_tokens<T, 4>(p, sums, part, s_order, t0, n0, pos0, share);
     else
-      join_tokens<T, 16, 1>(p, s_id, s_order, hs, t0, pos0, i0, i1, n, red);
+      join_tokens<T, 8>(p, sums, part, s_order, t0, n0, pos0, share);
   }
   __syncwarp();
   if (p.splits > 1) cluster_sync();  // no CTA leaves while its sums are read
@@ -900,39 +970,50 @@ __global__ void __launch_bounds__(LP_THREADS, 1)
       waited = true;
       // hi: the rounding of s h, low: the rounded remainder.  With one_part both
       // go to one tile, side by side; else to two tiles, from one reading of h.
-      auto value = [&](int t, int r, Pack<T, 8>& hi, Pack<T, 8>& low) {
-        hi = low = zero_pack<T, 8>();
-        const int tok = s_tok[t];
-        if (tok < 0 || r >= R) return;
-        const float* src = p.h + (int64_t)tok * R + r;
+      constexpr int U = 2, SH = 4;  // pieces and shares' sums in flight
+      auto values = [&](const int (&t)[U], const int (&r)[U], Pack<T, 8> (&hi)[U],
+                        Pack<T, 8> (&low)[U]) {
+        float4 u0[U], u1[U];
         const int64_t step = p.T * R;
-        float4 u0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u1 = u0;
-        for (int s0 = 0; s0 < p.shares; s0 += 4) {  // four shares' sums in flight
-          float4 v0[4], v1[4];
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            v0[s] = v1[s] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (s0 + s < p.shares) {
-              v0[s] = __ldcg(reinterpret_cast<const float4*>(src + (s0 + s) * step));
-              v1[s] = __ldcg(reinterpret_cast<const float4*>(src + (s0 + s) * step) + 1);
+        for (int k = 0; k < U; ++k) u0[k] = u1[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int s0 = 0; s0 < p.shares; s0 += SH) {
+          float4 v0[U][SH], v1[U][SH];
+#pragma unroll
+          for (int k = 0; k < U; ++k)
+#pragma unroll
+            for (int s = 0; s < SH; ++s) {
+              v0[k][s] = v1[k][s] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if (t[k] >= 0 && s_tok[t[k]] >= 0 && r[k] < R && s0 + s < p.shares) {
+                const float4* src = reinterpret_cast<const float4*>(
+                    p.h + (int64_t)s_tok[t[k]] * R + r[k] + (s0 + s) * step);
+                v0[k][s] = __ldcg(src);
+                v1[k][s] = __ldcg(src + 1);
+              }
             }
-          }
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            u0.x += v0[s].x, u0.y += v0[s].y, u0.z += v0[s].z, u0.w += v0[s].w;
-            u1.x += v1[s].x, u1.y += v1[s].y, u1.z += v1[s].z, u1.w += v1[s].w;
-          }
+          for (int k = 0; k < U; ++k)
+#pragma unroll
+            for (int s = 0; s < SH; ++s) {
+              u0[k].x += v0[k][s].x, u0[k].y += v0[k][s].y;
+              u0[k].z += v0[k][s].z, u0[k].w += v0[k][s].w;
+              u1[k].x += v1[k][s].x, u1[k].y += v1[k][s].y;
+              u1[k].z += v1[k][s].z, u1[k].w += v1[k][s].w;
+            }
         }
-        const float scale = __ldg(p.scale + s_row[t]);
-        const float2 f[4] = {make_float2(scale * u0.x, scale * u0.y),
-                             make_float2(scale * u0.z, scale * u0.w),
-                             make_float2(scale * u1.x, scale * u1.y),
-                             make_float2(scale * u1.z, scale * u1.w)};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          hi.set2(e, f[e]);
-          const float2 h = hi.get2(e);
-          low.set2(e, make_float2(f[e].x - h.x, f[e].y - h.y));
+        for (int k = 0; k < U; ++k) {
+          const float scale = t[k] >= 0 && s_row[t[k]] >= 0 ? __ldg(p.scale + s_row[t[k]]) : 0.0f;
+          const float2 f[4] = {make_float2(scale * u0[k].x, scale * u0[k].y),
+                               make_float2(scale * u0[k].z, scale * u0[k].w),
+                               make_float2(scale * u1[k].x, scale * u1[k].y),
+                               make_float2(scale * u1[k].z, scale * u1[k].w)};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            hi[k].set2(e, f[e]);
+            const float2 h = hi[k].get2(e);
+            low[k].set2(e, make_float2(f[e].x - h.x, f[e].y - h.y));
+          }
         }
       };
       auto ready = [&] {
@@ -947,15 +1028,25 @@ __global__ void __launch_bounds__(LP_THREADS, 1)
         if (!one_part) ok = ok && warp_wait(hempty0 + 8, hphase ^ 1u, abort_flag, p.status);
         if (!ok) break;
         uint8_t* to = hbuf + hs * LP_H_BYTES;
-        const int pieces = one_part ? r16 / 8 : 8;
-        for (int i = bt; i < LP_HALF * 8; i += LP_BUILDERS) {
-          const int t = i >> 3, c = i & 7;
-          if (c >= pieces) continue;
-          Pack<T, 8> hi, low;
-          value(t, rc + c * 8, hi, low);
-          *reinterpret_cast<uint4*>(to + tile_at(t, c)) = hi.w;
-          *reinterpret_cast<uint4*>(one_part ? to + tile_at(t, pieces + c)
-                                             : to + LP_H_BYTES + tile_at(t, c)) = low.w;
+        const int pieces = min(8, (r16 - rc) / 8);  // of a row, those that the MMAs read
+        for (int i = bt; i < LP_HALF * pieces; i += U * LP_BUILDERS) {
+          int t[U], r[U];
+          Pack<T, 8> hi[U], low[U];
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            const int j = i + k * LP_BUILDERS;
+            t[k] = j < LP_HALF * pieces ? j / pieces : -1;
+            r[k] = rc + (j % pieces) * 8;
+          }
+          values(t, r, hi, low);
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            if (t[k] < 0) continue;
+            const int c = (r[k] - rc) / 8;
+            *reinterpret_cast<uint4*>(to + tile_at(t[k], c)) = hi[k].w;
+            *reinterpret_cast<uint4*>(one_part ? to + tile_at(t[k], pieces + c)
+                                               : to + LP_H_BYTES + tile_at(t[k], c)) = low[k].w;
+          }
         }
         ready();
         if (!one_part) ready();
@@ -1028,7 +1119,7 @@ struct LoraPlan {
   int nt, splits;                   // lora_split_kernel
 };
 
-static LoraPlan lora_plan(int64_t T, int64_t K, int64_t N, int64_t S) {
+static LoraPlan lora_plan(int64_t T, int64_t K, int64_t N, int64_t S, int64_t R) {
   LoraPlan q{};
   const int64_t sms = num_sms();
   q.pair = T > moe::SPLIT_TOKENS;
@@ -1057,7 +1148,8 @@ static LoraPlan lora_plan(int64_t T, int64_t K, int64_t N, int64_t S) {
   q.shares = (int)((K + q.share_k - 1) / q.share_k);
   // Split projection: the smallest tile that holds the batch, up to 128 tokens; a
   // cluster shares a tile's K while tiles leave CTA slots empty.
-  q.nt = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 ? 64 : 128));
+  // (Shared memory holds the adapters' part of 128 tokens up to rank 64.)
+  q.nt = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 || R > 64 ? 64 : 128));
   const int64_t tiles = (N + moe::LG_M - 1) / moe::LG_M * ((T + q.nt - 1) / q.nt);
   const int64_t slots = q.nt <= 64 ? 2 * sms : sms;
   const int64_t slabs = (K + 63) / 64;
@@ -1127,7 +1219,7 @@ static moe_status_t launch_shrink(const LoraPlan& q, const LoraParams& p, cudaSt
 template <typename T, int NT>
 static moe_status_t launch_split(const LoraParams& p, const CUtensorMap& w, const CUtensorMap& x,
                                  cudaStream_t s) {
-  const int smem = moe::lg_smem(NT, p.splits, (int)p.R);  // <= kMaxSmem for R <= 128
+  const int smem = moe::lg_smem(NT, p.splits, (int)p.R);  // <= kMaxSmem
   moe_status_t st = allow_smem<moe::lora_split_kernel<T, NT>>(kMaxSmem);
   if (st != MOE_OK) return st;
   const dim3 grid((unsigned)((p.N + moe::LG_M - 1) / moe::LG_M * p.splits),
@@ -1207,8 +1299,8 @@ size_t moe_lora_workspace_size(int64_t num_tokens, int64_t in_features, int64_t 
                                int64_t num_adapters, int64_t rank) {
   if (num_tokens <= 0 || in_features <= 0 || out_features <= 0 || num_adapters <= 0 || rank <= 0)
     return 0;
-  return lora_workspace(lora_plan(num_tokens, in_features, out_features, num_adapters), num_tokens,
-                        rank);
+  return lora_workspace(lora_plan(num_tokens, in_features, out_features, num_adapters, rank),
+                        num_tokens, rank);
 }
 
 moe_status_t moe_lora_linear(const moe_lora_args_t* a, void* stream) {
@@ -1239,7 +1331,7 @@ moe_status_t moe_lora_linear(const moe_lora_args_t* a, void* stream) {
   if (T >= ((int64_t)1 << 22) || K >= ((int64_t)1 << 31) || N >= ((int64_t)1 << 28) ||
       S * N >= ((int64_t)1 << 31))
     return set_error(MOE_ERR_UNSUPPORTED, "problem too large for 32-bit tile coordinates");
-  const LoraPlan q = lora_plan(T, K, N, S);
+  const LoraPlan q = lora_plan(T, K, N, S, R);
   if (S > 0) {
     const size_t need = lora_workspace(q, T, R);
     if (a->workspace == nullptr || a->workspace_bytes < need)

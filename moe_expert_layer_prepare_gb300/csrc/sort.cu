@@ -355,7 +355,7 @@ using moe::RowParams;
 using moe::SortParams;
 
 // Up to this many routes one block sorts them in one launch.
-constexpr int64_t kSortOneBlock = 4096;
+constexpr int64_t kSortOneBlock = 2048;
 
 static void sort_split(int64_t R, int32_t* blocks, int32_t* per_block) {
   int64_t per = 1024;

@@ -196,13 +196,16 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// A float of the shared memory of the cluster's CTA `rank` at this CTA's address.
-__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
-  float v;
-  asm volatile("{ .reg .b32 a; mapa.shared::cluster.u32 a, %1, %2; ld.shared::cluster.f32 %0, [a]; }"
-               : "=f"(v)
-               : "r"(addr), "r"(rank)
-               : "memory");
+// Four floats of the shared memory of the cluster's CTA `rank` at this CTA's
+// address.
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr, uint32_t rank) {
+  float4 v;
+  asm volatile(
+      "{ .reg .b32 a; mapa.shared::cluster.u32 a, %4, %5;"
+      " ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a]; }"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(addr), "r"(rank)
+      : "memory");
   return v;
 }
 
