@@ -501,7 +501,7 @@ moe_status_t moe_route_backward(const moe_route_backward_args_t* args, void* str
 /* row_route[r] = t * k + j of row r, -1 for r >= expert_offsets[E].          */
 /* topk_ids int32 or int64 [T, k]; expert_offsets int32 [E + 1]; route_row    */
 /* and row_route int32 [T * k].  workspace: moe_sort_workspace_size() bytes,  */
-/* need not be cleared.  E > 1024 -> UNSUPPORTED.                             */
+/* 16-byte aligned, need not be cleared.  E > 1024 -> UNSUPPORTED.                             */
 /*                                                                           */
 /* With `rows` [num_rows, K] in the order of the experts:                     */
 /*   moe_permute             rows[route_row[t, j]] = x[t]; rows from           */

@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(SH_THREADS, 2) lora_shrink_kernel(LoraParams p
 }
 
 // ------------------------------------------------- projection, few tokens
-constexpr int SPLIT_TOKENS = 256;
+constexpr int SPLIT_TOKENS = 512;
 constexpr int LG_M = 128;  // features of a tile
 constexpr int LG_A_BYTES = LG_M * 128;
 constexpr int LG_THREADS = 256;

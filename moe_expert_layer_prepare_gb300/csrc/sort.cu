@@ -33,7 +33,8 @@ struct SortParams {
   int32_t* offsets;
   int32_t* route_row;
   int32_t* row_route;
-  int32_t* hist;  // [blocks, E]
+  int32_t* hist;  // [E, hist_row]: an expert's counts by block
+  int hist_row;   // blocks, up to a multiple of four
   uint32_t* status;
 };
 
@@ -60,7 +61,7 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_count_kernel(SortParams p) 
   }
   if (bad) set_status(p.status, MOE_DEV_BAD_EXPERT);
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += SORT_THREADS) p.hist[blockIdx.x * p.E + e] = cnt[e];
+  for (int e = threadIdx.x; e < p.E; e += SORT_THREADS) p.hist[e * p.hist_row + blockIdx.x] = cnt[e];
 }
 
 __global__ void __launch_bounds__(SORT_THREADS) sort_place_kernel(SortParams p) {
@@ -70,7 +71,7 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_place_kernel(SortParams p) 
   __shared__ int base[SORT_MAX_EXPERTS];  // first row of this block's routes of an expert
   __shared__ int warp_total[SORT_WARPS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int i = tid; i < SORT_WARPS * p.E; i += SORT_THREADS) table[i / p.E][i % p.E] = 0;
+  for (int e = lane; e < p.E; e += 32) table[warp][e] = 0;  // each warp its own row
   __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
@@ -103,10 +104,23 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_place_kernel(SortParams p) 
       if (p.blocks == 1) {
         all = mine;
       } else {
-        for (int b = 0; b < p.blocks; ++b) {
-          const int c = __ldg(p.hist + b * p.E + e);
-          all += c;
-          if (b < (int)blockIdx.x) before += c;
+        // sixteen blocks' counts in flight; what lies past the last block is not used
+        const int4* row = reinterpret_cast<const int4*>(p.hist + e * p.hist_row);
+        for (int b0 = 0; b0 < p.blocks; b0 += 16) {
+          int4 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            v[i] = b0 + 4 * i < p.hist_row ? __ldcg(row + b0 / 4 + i) : make_int4(0, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int b = b0 + 4 * i + j;
+              if (b < p.blocks) all += c[j];
+              if (b < (int)blockIdx.x) before += c[j];
+            }
+          }
         }
       }
     }
@@ -173,6 +187,19 @@ struct RowParams {
   float* d_w;
 };
 
+// A warp's way over (token, chunk) tasks, nwarps apart, without a division each.
+struct Walk {
+  int64_t t, dt;
+  int c, dc, chunks;
+  __device__ __forceinline__ Walk(int64_t first, int64_t step, int n)
+      : t(first / n), dt(step / n), c((int)(first % n)), dc((int)(step % n)), chunks(n) {}
+  __device__ __forceinline__ void next() {
+    t += dt;
+    c += dc;
+    if (c >= chunks) c -= chunks, ++t;
+  }
+};
+
 // Row of route (t, lane) for lane < k, or -1.
 __device__ __forceinline__ int lane_row(const RowParams& p, int64_t t, int lane) {
   const int r = lane < p.k ? p.route_row[t * p.k + lane] : -1;
@@ -189,16 +216,15 @@ __global__ void __launch_bounds__(256) permute_kernel(RowParams p) {
   const int lane = threadIdx.x & 31;
   const int64_t gwarp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-  constexpr int64_t chunk = (int64_t)PERMUTE_VECS * 32 * VEC;
-  const int64_t chunks = (p.K + chunk - 1) / chunk;
+  constexpr int chunk = PERMUTE_VECS * 32 * VEC;
   pdl_wait();
   pdl_launch_dependents();
   const int64_t used = min(max((int64_t)p.offsets[p.E], (int64_t)0), p.num_rows);
-  const int64_t tasks = (p.T + p.num_rows - used) * chunks;
+  const int64_t rows_and_rest = p.T + p.num_rows - used;
   T* rows = static_cast<T*>(p.out_rows);
-  for (int64_t task = gwarp; task < tasks; task += nwarps) {
-    const int64_t t = task / chunks;
-    const int64_t c0 = (task - t * chunks) * chunk + lane * VEC;
+  for (Walk w(gwarp, nwarps, (int)((p.K + chunk - 1) / chunk)); w.t < rows_and_rest; w.next()) {
+    const int64_t t = w.t;
+    const int64_t c0 = (int64_t)w.c * chunk + lane * VEC;
     Pack<T, VEC> v[PERMUTE_VECS];
     if (t >= p.T) {
       T* dst = rows + (used + t - p.T) * p.out_rows_stride;
@@ -224,51 +250,59 @@ __global__ void __launch_bounds__(256) permute_kernel(RowParams p) {
   }
 }
 
-// One warp per (token, 32 packs): the routed rows' packs are read eight at a
-// time, all in flight, and summed in fp32 in ascending j.
-template <typename T, int VEC>
+// One warp per (token, CH times 32 packs): KB routes' packs are read at a time, KB
+// CH = 8 of them in flight a lane, and summed in fp32 in ascending j.
+template <typename T, int VEC, int KB>
 __global__ void __launch_bounds__(256) unpermute_kernel(RowParams p) {
+  constexpr int CH = 8 / KB, chunk = CH * 32 * VEC;
   const int lane = threadIdx.x & 31;
   const int64_t gwarp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-  const int64_t chunks = (p.K + 32 * VEC - 1) / (32 * VEC);
-  const int64_t tasks = p.T * chunks;
   pdl_wait();
   pdl_launch_dependents();
   const T* rows = static_cast<const T*>(p.rows);
-  for (int64_t task = gwarp; task < tasks; task += nwarps) {
-    const int64_t t = task / chunks;
-    const int64_t c0 = (task - t * chunks) * 32 * VEC + lane * VEC;
-    const bool active = c0 < p.K;
+  for (Walk w(gwarp, nwarps, (int)((p.K + chunk - 1) / chunk)); w.t < p.T; w.next()) {
+    const int64_t t = w.t;
+    const int64_t c0 = (int64_t)w.c * chunk + lane * VEC;
     const int my_row = lane_row(p, t, lane);
-    const float my_w = lane < p.k ? (p.w != nullptr ? p.w[t * p.k + lane] : 1.0f) : 0.0f;
-    float acc[VEC];
+    const float my_w = my_row >= 0 ? (p.w != nullptr ? p.w[t * p.k + lane] : 1.0f) : 0.0f;
+    float acc[CH][VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
-    for (int j0 = 0; j0 < p.k; j0 += 8) {
-      Pack<T, VEC> v[8];
-      int row[8];
+    for (int h = 0; h < CH; ++h)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        row[i] = __shfl_sync(0xFFFFFFFFu, my_row, (j0 + i) & 31);
-        if (j0 + i >= p.k) row[i] = -1;
-        if (row[i] >= 0 && active)
-          v[i] = load_pack_stream<T, VEC>(rows + (int64_t)row[i] * p.rows_stride + c0);
+      for (int q = 0; q < VEC; ++q) acc[h][q] = 0.0f;
+    for (int j0 = 0; j0 < p.k; j0 += KB) {
+      Pack<T, VEC> v[KB][CH];
+#pragma unroll
+      for (int i = 0; i < KB; ++i) {
+        // routes past the last read as absent: lanes >= k hold none
+        const int row = j0 + i < 32 ? __shfl_sync(0xFFFFFFFFu, my_row, j0 + i) : -1;
+#pragma unroll
+        for (int h = 0; h < CH; ++h)
+          v[i][h] = row >= 0 && c0 + h * 32 * VEC < p.K
+                        ? load_pack_stream<T, VEC>(rows + (int64_t)row * p.rows_stride + c0 +
+                                                   h * 32 * VEC)
+                        : zero_pack<T, VEC>();
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float w = __shfl_sync(0xFFFFFFFFu, my_w, (j0 + i) & 31);
-        if (row[i] < 0 || !active) continue;
-        float f[VEC];
-        v[i].get(f);
+      for (int i = 0; i < KB; ++i) {
+        const float wt = __shfl_sync(0xFFFFFFFFu, my_w, (j0 + i) & 31);
+        if (j0 + i >= p.k) break;
 #pragma unroll
-        for (int q = 0; q < VEC; ++q) acc[q] = fmaf(w, f[q], acc[q]);
+        for (int h = 0; h < CH; ++h) {
+          float f[VEC];
+          v[i][h].get(f);
+#pragma unroll
+          for (int q = 0; q < VEC; ++q) acc[h][q] = fmaf(wt, f[q], acc[h][q]);
+        }
       }
     }
-    if (active) {
+#pragma unroll
+    for (int h = 0; h < CH; ++h) {
+      if (c0 + h * 32 * VEC >= p.K) break;
       Pack<T, VEC> o;
-      o.set(acc);
-      store_pack<T, VEC>(static_cast<T*>(p.out) + t * p.out_stride + c0, o);
+      o.set(acc[h]);
+      store_pack<T, VEC>(static_cast<T*>(p.out) + t * p.out_stride + c0 + h * 32 * VEC, o);
     }
   }
 }
@@ -367,6 +401,8 @@ static void sort_split(int64_t R, int32_t* blocks, int32_t* per_block) {
   *blocks = (int32_t)((R + per - 1) / per);
 }
 
+static int32_t hist_row(int32_t blocks) { return (blocks + 3) / 4 * 4; }
+
 static moe_status_t launch_sort(const SortParams& p, cudaStream_t s) {
   if (p.blocks > 1) {
     moe_status_t st = launched(launch_pdl(moe::sort_count_kernel, dim3(p.blocks),
@@ -384,7 +420,7 @@ static moe_status_t launch_sort(const SortParams& p, cudaStream_t s) {
 size_t token_order_scratch(int64_t T, int64_t S) {
   int32_t blocks, per;
   sort_split(T, &blocks, &per);
-  return (size_t)((blocks > 1 ? blocks * (S + 1) : 0) + (S + 2) + T);
+  return (size_t)((blocks > 1 ? hist_row(blocks) * (S + 1) + 3 : 0) + (S + 2) + T);
 }
 
 moe_status_t launch_token_order(const int32_t* adapter_ids, int64_t T, int64_t S, int align,
@@ -400,7 +436,8 @@ moe_status_t launch_token_order(const int32_t* adapter_ids, int64_t T, int64_t S
   p.offsets = scratch;
   p.route_row = scratch + S + 2;
   p.row_route = order;
-  p.hist = scratch + S + 2 + T;
+  p.hist = scratch + (S + 2 + T + 3) / 4 * 4;  // scratch is 16-byte aligned
+  p.hist_row = hist_row(p.blocks);
   return launch_sort(p, s);
 }
 
@@ -435,7 +472,7 @@ size_t moe_sort_workspace_size(int64_t num_tokens, int64_t top_k, int64_t num_ex
   if (num_tokens <= 0 || top_k <= 0 || num_experts <= 0) return 0;
   int32_t blocks, per;
   sort_split(num_tokens * top_k, &blocks, &per);
-  return blocks == 1 ? 0 : (size_t)blocks * num_experts * 4;
+  return blocks == 1 ? 0 : (size_t)hist_row(blocks) * num_experts * 4;
 }
 
 moe_status_t moe_sort_routes(const void* topk_ids, int32_t topk_ids_dtype, int64_t num_tokens,
@@ -465,15 +502,16 @@ moe_status_t moe_sort_routes(const void* topk_ids, int32_t topk_ids_dtype, int64
   p.route_row = route_row;
   p.row_route = row_route;
   p.hist = static_cast<int32_t*>(workspace);
+  p.hist_row = hist_row(p.blocks);
   p.status = device_status;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (p.blocks > 1) {
-    const size_t need = (size_t)p.blocks * num_experts * 4;
+    const size_t need = (size_t)p.hist_row * num_experts * 4;
     if (workspace == nullptr || workspace_bytes < need)
       return set_error(MOE_ERR_WORKSPACE, "sorting needs %zu bytes of workspace, got %zu", need,
                        workspace_bytes);
-    if ((reinterpret_cast<uintptr_t>(workspace) & 3u) != 0)
-      return set_error(MOE_ERR_ALIGNMENT, "workspace must be 4-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(workspace) & 15u) != 0)
+      return set_error(MOE_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
   }
   return launch_sort(p, s);
 }
@@ -548,12 +586,19 @@ moe_status_t moe_unpermute(const void* rows, int64_t rows_stride0, int64_t num_r
     const bool wide = packs16(hidden_size, sizeof(T)) &&
                       rows_aligned16(rows, rows_stride0, sizeof(T), num_rows) &&
                       rows_aligned16(out, out_stride0, sizeof(T), num_tokens);
-    auto go = [&](auto kernel, int vec) {
-      const int64_t warps = num_tokens * ((hidden_size + 32 * vec - 1) / (32 * vec));
+    auto go = [&](auto kernel, int vec, int kb) {
+      const int64_t chunk = (int64_t)(8 / kb) * 32 * vec;
+      const int64_t warps = num_tokens * ((hidden_size + chunk - 1) / chunk);
       return launched(launch_pdl(kernel, one_wave(kernel, (warps + 7) / 8, 256), dim3(256), 0,
                                  static_cast<cudaStream_t>(stream), p), "unpermute");
     };
-    return wide ? go(moe::unpermute_kernel<T, V>, V) : go(moe::unpermute_kernel<T, 1>, 1);
+    if (wide)
+      return top_k > 4   ? go(moe::unpermute_kernel<T, V, 8>, V, 8)
+             : top_k > 2 ? go(moe::unpermute_kernel<T, V, 4>, V, 4)
+                         : go(moe::unpermute_kernel<T, V, 2>, V, 2);
+    return top_k > 4   ? go(moe::unpermute_kernel<T, 1, 8>, 1, 8)
+           : top_k > 2 ? go(moe::unpermute_kernel<T, 1, 4>, 1, 4)
+                       : go(moe::unpermute_kernel<T, 1, 2>, 1, 2);
   });
 }
 

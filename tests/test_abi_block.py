@@ -77,7 +77,7 @@ def test_sort(lib):
     assert sort(ids=None) == INVALID
     assert sort(T=100000, ws=None) == WORKSPACE
     assert sort(T=100000, n=16) == WORKSPACE
-    assert sort(T=100000, ws=FAKE + 2) == ALIGNMENT
+    assert sort(T=100000, ws=FAKE + 4) == ALIGNMENT
     assert lib.moe_sort_workspace_size(64, 2, 8) == 0
     assert lib.moe_sort_workspace_size(-1, 2, 8) == 0
     assert lib.moe_sort_workspace_size(8192, 8, 256) > 0
