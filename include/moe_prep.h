@@ -520,28 +520,62 @@ moe_status_t moe_route_backward(const moe_route_backward_args_t* args, void* str
 /* ------------------------------------------------------------------------ */
 size_t moe_sort_workspace_size(int64_t num_tokens, int64_t top_k, int64_t num_experts);
 
-moe_status_t moe_sort_routes(const void* topk_ids, int32_t topk_ids_dtype, int64_t num_tokens,
-                             int64_t top_k, int64_t num_experts, int32_t* expert_offsets,
-                             int32_t* route_row, int32_t* row_route, void* workspace,
-                             size_t workspace_bytes, uint32_t* device_status, void* stream);
+typedef struct moe_sort_args {
+  int64_t num_tokens, top_k, num_experts;
+  const void* topk_ids; /* [T, k] contiguous */
+  int32_t topk_ids_dtype;
+  int32_t* expert_offsets; /* [E + 1] */
+  int32_t* route_row;      /* [T, k] */
+  int32_t* row_route;      /* [T * k] */
+  void* workspace;
+  size_t workspace_bytes;
+  uint32_t* device_status;
+} moe_sort_args_t;
 
-moe_status_t moe_permute(const void* x, int64_t x_stride0, int32_t dtype, int64_t num_tokens,
-                         int64_t hidden_size, int64_t top_k, const int32_t* route_row,
-                         const int32_t* expert_offsets, int64_t num_experts, void* rows,
-                         int64_t rows_stride0, int64_t num_rows, void* stream);
+moe_status_t moe_sort_routes(const moe_sort_args_t* args, void* stream);
 
-moe_status_t moe_unpermute(const void* rows, int64_t rows_stride0, int64_t num_rows, int32_t dtype,
-                           const int32_t* route_row, const float* topk_weights,
-                           int64_t num_tokens, int64_t hidden_size, int64_t top_k, void* out,
-                           int64_t out_stride0, void* stream);
+typedef struct moe_permute_args {
+  int64_t num_tokens, hidden_size, top_k, num_experts, num_rows;
+  int32_t dtype;
+  const void* x; /* [T, K] */
+  int64_t x_stride0;
+  const int32_t* route_row;      /* [T, k] */
+  const int32_t* expert_offsets; /* [E + 1] */
+  void* rows;                    /* [num_rows, K] */
+  int64_t rows_stride0;
+} moe_permute_args_t;
 
-moe_status_t moe_unpermute_backward(const void* d_out, int64_t d_out_stride0, const void* rows,
-                                    int64_t rows_stride0, int64_t num_rows, int32_t dtype,
-                                    const int32_t* route_row, const float* topk_weights,
-                                    const int32_t* expert_offsets, int64_t num_experts,
-                                    int64_t num_tokens, int64_t hidden_size, int64_t top_k,
-                                    void* d_rows, int64_t d_rows_stride0, float* d_weights,
-                                    void* stream);
+moe_status_t moe_permute(const moe_permute_args_t* args, void* stream);
+
+typedef struct moe_unpermute_args {
+  int64_t num_tokens, hidden_size, top_k, num_rows;
+  int32_t dtype;
+  const void* rows; /* [num_rows, K] */
+  int64_t rows_stride0;
+  const int32_t* route_row;  /* [T, k] */
+  const float* topk_weights; /* nullable [T, k] */
+  void* out;                 /* [T, K] */
+  int64_t out_stride0;
+} moe_unpermute_args_t;
+
+moe_status_t moe_unpermute(const moe_unpermute_args_t* args, void* stream);
+
+typedef struct moe_unpermute_backward_args {
+  int64_t num_tokens, hidden_size, top_k, num_experts, num_rows;
+  int32_t dtype;
+  const void* d_out; /* [T, K] */
+  int64_t d_out_stride0;
+  const void* rows; /* [num_rows, K] */
+  int64_t rows_stride0;
+  const int32_t* route_row;
+  const float* topk_weights;
+  const int32_t* expert_offsets;
+  void* d_rows; /* [num_rows, K] */
+  int64_t d_rows_stride0;
+  float* d_weights; /* [T, k] */
+} moe_unpermute_backward_args_t;
+
+moe_status_t moe_unpermute_backward(const moe_unpermute_backward_args_t* args, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* moe_block_norm                                                            */

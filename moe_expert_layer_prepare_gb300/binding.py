@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -105,6 +106,19 @@ class ExpertsArgs(ctypes.Structure):
 _f32 = ctypes.c_float
 
 
+# Argument structs of the operators around the experts.  A call fills one with
+# ``pack`` (the struct's bytes from its values in order, None not allowed: a NULL
+# pointer is 0), a quarter of the time that filling the ctypes object takes, which
+# counts where a call's kernel runs for two microseconds.
+_FORMAT = {_i64: "q", _i32: "i", _vp: "P", _sz: "N", _f32: "f"}
+
+
+def _packer(cls):
+    cls.pack = staticmethod(struct.Struct("@" + "".join(_FORMAT[t] for _, t in cls._fields_)).pack)
+    return cls
+
+
+@_packer
 class RouteArgs(ctypes.Structure):
     _fields_ = [
         ("num_tokens", _i64), ("num_experts", _i64), ("top_k", _i64),
@@ -115,6 +129,7 @@ class RouteArgs(ctypes.Structure):
     ]
 
 
+@_packer
 class RouteBackwardArgs(ctypes.Structure):
     _fields_ = [
         ("num_tokens", _i64), ("num_experts", _i64), ("top_k", _i64),
@@ -125,6 +140,44 @@ class RouteBackwardArgs(ctypes.Structure):
     ]
 
 
+@_packer
+class SortArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", _i64), ("top_k", _i64), ("num_experts", _i64), ("topk_ids", _vp),
+        ("topk_ids_dtype", _i32), ("expert_offsets", _vp), ("route_row", _vp),
+        ("row_route", _vp), ("workspace", _vp), ("workspace_bytes", _sz), ("device_status", _vp),
+    ]
+
+
+@_packer
+class PermuteArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", _i64), ("hidden_size", _i64), ("top_k", _i64), ("num_experts", _i64),
+        ("num_rows", _i64), ("dtype", _i32), ("x", _vp), ("x_stride0", _i64), ("route_row", _vp),
+        ("expert_offsets", _vp), ("rows", _vp), ("rows_stride0", _i64),
+    ]
+
+
+@_packer
+class UnpermuteArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", _i64), ("hidden_size", _i64), ("top_k", _i64), ("num_rows", _i64),
+        ("dtype", _i32), ("rows", _vp), ("rows_stride0", _i64), ("route_row", _vp),
+        ("topk_weights", _vp), ("out", _vp), ("out_stride0", _i64),
+    ]
+
+
+@_packer
+class UnpermuteBackwardArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", _i64), ("hidden_size", _i64), ("top_k", _i64), ("num_experts", _i64),
+        ("num_rows", _i64), ("dtype", _i32), ("d_out", _vp), ("d_out_stride0", _i64),
+        ("rows", _vp), ("rows_stride0", _i64), ("route_row", _vp), ("topk_weights", _vp),
+        ("expert_offsets", _vp), ("d_rows", _vp), ("d_rows_stride0", _i64), ("d_weights", _vp),
+    ]
+
+
+@_packer
 class BlockNormArgs(ctypes.Structure):
     _fields_ = [
         ("num_tokens", _i64), ("hidden_size", _i64), ("dtype", _i32), ("weight_dtype", _i32),
@@ -136,6 +189,7 @@ class BlockNormArgs(ctypes.Structure):
     ]
 
 
+@_packer
 class BlockNormBackwardArgs(ctypes.Structure):
     _fields_ = [
         ("num_tokens", _i64), ("hidden_size", _i64), ("dtype", _i32), ("weight_dtype", _i32),
@@ -150,6 +204,7 @@ class BlockNormBackwardArgs(ctypes.Structure):
     ]
 
 
+@_packer
 class LoraArgs(ctypes.Structure):
     _fields_ = [
         ("num_tokens", _i64), ("in_features", _i64), ("out_features", _i64),
@@ -193,27 +248,15 @@ def configure(lib):
     lib.moe_topk_reduce.restype = ctypes.c_int
     lib.moe_topk_reduce.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _vp,
                                     _vp]
-    for name, args in (("moe_route", RouteArgs), ("moe_route_backward", RouteBackwardArgs),
-                       ("moe_block_norm", BlockNormArgs),
-                       ("moe_block_norm_backward", BlockNormBackwardArgs),
-                       ("moe_lora_linear", LoraArgs)):
+    for name in ("moe_route", "moe_route_backward", "moe_sort_routes", "moe_permute",
+                 "moe_unpermute", "moe_unpermute_backward", "moe_block_norm",
+                 "moe_block_norm_backward", "moe_lora_linear"):
         getattr(lib, name).restype = ctypes.c_int
-        getattr(lib, name).argtypes = [ctypes.POINTER(args), _vp]
+        getattr(lib, name).argtypes = [_vp, _vp]  # the packed struct's bytes, the stream
     for name, n in (("moe_sort_workspace_size", 3), ("moe_block_norm_workspace_size", 2),
                     ("moe_lora_workspace_size", 5)):
         getattr(lib, name).restype = _sz
         getattr(lib, name).argtypes = [_i64] * n
-    lib.moe_sort_routes.restype = ctypes.c_int
-    lib.moe_sort_routes.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp,
-                                    _vp]
-    lib.moe_permute.restype = ctypes.c_int
-    lib.moe_permute.argtypes = [_vp, _i64, _i32, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _i64,
-                                _vp]
-    lib.moe_unpermute.restype = ctypes.c_int
-    lib.moe_unpermute.argtypes = [_vp, _i64, _i64, _i32, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp]
-    lib.moe_unpermute_backward.restype = ctypes.c_int
-    lib.moe_unpermute_backward.argtypes = [_vp, _i64, _vp, _i64, _i64, _i32, _vp, _vp, _vp, _i64,
-                                           _i64, _i64, _i64, _vp, _i64, _vp, _vp]
     return lib
 
 
@@ -488,47 +531,57 @@ def moe_topk_reduce(expert_out, topk_idx, route_slot, topk_weights, out, stream=
 # strides; what only the tensors know (types, shapes, inner strides) is checked
 # here and raises ValueError.
 # ---------------------------------------------------------------------------
-_DTYPE = {torch.float32: MOE_DTYPE_FP32, torch.bfloat16: MOE_DTYPE_BF16,
-          torch.float16: MOE_DTYPE_FP16}
-_IDS = {torch.int32: MOE_IDS_INT32, torch.int64: MOE_IDS_INT64}
+_BF16, _FP16, _FP32, _INT32 = torch.bfloat16, torch.float16, torch.float32, torch.int32
+_DTYPE = {_FP32: MOE_DTYPE_FP32, _BF16: MOE_DTYPE_BF16, _FP16: MOE_DTYPE_FP16}
+_IDS = {_INT32: MOE_IDS_INT32, torch.int64: MOE_IDS_INT64}
+_current_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def _raw_stream(stream):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _current_stream(_current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _call(name, args, stream):
+    st = getattr(_lib or load(), name)(args, _raw_stream(stream))
+    if st != MOE_OK:
+        _check(name, st)
+
+
 def _at(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
-def _rows(name, t, T, K, dtype):
-    """Row stride of a [T, K] tensor with inner stride 1 (0 for None)."""
+def _bytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _rows(name, t, shape, dtype):
+    """Row stride of a tensor of this shape with inner stride 1 (0 for None)."""
     if t is None:
         return 0
-    if t.dtype != dtype or t.shape != (T, K):
-        raise ValueError(f"{name}: want {dtype} [{T}, {K}], got {t.dtype} {list(t.shape)}")
-    s0, s1 = t.stride()
-    if s1 != 1 and K > 1:
-        raise ValueError(f"{name}: inner stride must be 1, got {s1}")
+    s0, s1 = t.stride() if t.dim() == 2 else (0, 0)
+    if t.dtype is not dtype or t.shape != shape or (s1 != 1 and shape[1] > 1):
+        raise ValueError(f"{name}: want {dtype} {list(shape)} with inner stride 1, got {t.dtype} "
+                         f"{list(t.shape)} with strides {t.stride()}")
     return s0
 
 
 def _flat(name, t, shape, dtype):
-    """Checks a contiguous tensor (or None) and gives its address."""
+    """Address of a contiguous tensor of this shape and type (0 for None)."""
     if t is None:
-        return None
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        return 0
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: want contiguous {dtype} {list(shape)}, got {t.dtype} "
                          f"{list(t.shape)} with strides {t.stride()}")
     return t.data_ptr()
 
 
-def _dtype_of(name, t, table=_DTYPE):
-    d = table.get(t.dtype)
+def _code(name, dtype, table=_DTYPE):
+    d = table.get(dtype)
     if d is None:
-        raise ValueError(f"{name}: unsupported type {t.dtype}")
+        raise ValueError(f"{name}: unsupported type {dtype}")
     return d
 
 
@@ -541,33 +594,27 @@ def moe_route(logits, topk_ids, topk_weights, bias=None, is_padding=None,
     top_groups: only the experts of the best groups are taken.  See include/moe_prep.h."""
     T, E = logits.shape
     k = topk_ids.shape[1]
-    if bias is not None:
-        _flat("bias", bias, (E,), torch.float32)
-    if is_padding is not None:
-        _flat("is_padding", is_padding, (T,), torch.uint8)
-    a = RouteArgs(T, E, k, logits.data_ptr(), _dtype_of("logits", logits),
-                  _rows("logits", logits, T, E, logits.dtype), _at(bias), _at(is_padding), scoring,
-                  1 if renormalize else 0, scale, num_groups, top_groups,
-                  _flat("topk_ids", topk_ids, (T, k), topk_ids.dtype),
-                  _dtype_of("topk_ids", topk_ids, _IDS),
-                  _flat("topk_weights", topk_weights, (T, k), torch.float32))
-    _check("moe_route", load().moe_route(a, _raw_stream(stream)))
+    dt, idt, tk = logits.dtype, topk_ids.dtype, (T, k)
+    _call("moe_route", RouteArgs.pack(
+        T, E, k, logits.data_ptr(), _code("logits", dt), _rows("logits", logits, (T, E), dt),
+        _flat("bias", bias, (E,), _FP32), _flat("is_padding", is_padding, (T,), torch.uint8),
+        scoring, 1 if renormalize else 0, scale, num_groups, top_groups,
+        _flat("topk_ids", topk_ids, tk, idt), _code("topk_ids", idt, _IDS),
+        _flat("topk_weights", topk_weights, tk, _FP32)), stream)
 
 
 def moe_route_backward(logits, topk_ids, d_weights, d_logits, scoring=MOE_SCORE_SOFTMAX,
                        renormalize=True, scale=1.0, stream=None):
     """Gradient of the logits (every value written) from that of ``moe_route``'s weights; scoring,
     renormalize and scale as in the forward call.  See include/moe_prep.h."""
-    T, E = logits.shape
+    T, E = shape = logits.shape
     k = topk_ids.shape[1]
-    a = RouteBackwardArgs(T, E, k, logits.data_ptr(), _dtype_of("logits", logits),
-                          _rows("logits", logits, T, E, logits.dtype), scoring,
-                          1 if renormalize else 0, scale,
-                          _flat("topk_ids", topk_ids, (T, k), topk_ids.dtype),
-                          _dtype_of("topk_ids", topk_ids, _IDS),
-                          _flat("d_weights", d_weights, (T, k), torch.float32),
-                          d_logits.data_ptr(), _rows("d_logits", d_logits, T, E, logits.dtype))
-    _check("moe_route_backward", load().moe_route_backward(a, _raw_stream(stream)))
+    dt, idt, tk = logits.dtype, topk_ids.dtype, (T, k)
+    _call("moe_route_backward", RouteBackwardArgs.pack(
+        T, E, k, logits.data_ptr(), _code("logits", dt), _rows("logits", logits, shape, dt),
+        scoring, 1 if renormalize else 0, scale, _flat("topk_ids", topk_ids, tk, idt),
+        _code("topk_ids", idt, _IDS), _flat("d_weights", d_weights, tk, _FP32),
+        d_logits.data_ptr(), _rows("d_logits", d_logits, shape, dt)), stream)
 
 
 def sort_workspace_size(num_tokens, top_k, num_experts) -> int:
@@ -579,40 +626,39 @@ def moe_sort_routes(topk_ids, expert_offsets, route_row, row_route, workspace=No
     """Rows of the routes in expert order.  topk_ids: int32 or int64 [T, k]; expert_offsets: int32
     [E + 1]; route_row: int32 [T, k]; row_route: int32 [T * k]; workspace: uint8,
     sort_workspace_size() bytes.  See include/moe_prep.h."""
-    T, k = topk_ids.shape
-    E = expert_offsets.shape[0] - 1
-    _check("moe_sort_routes", load().moe_sort_routes(
-        _flat("topk_ids", topk_ids, (T, k), topk_ids.dtype), _dtype_of("topk_ids", topk_ids, _IDS),
-        T, k, E, _flat("expert_offsets", expert_offsets, (E + 1,), torch.int32),
-        _flat("route_row", route_row, (T, k), torch.int32),
-        _flat("row_route", row_route, (T * k,), torch.int32), _at(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(),
-        _at(device_status), _raw_stream(stream)))
+    T, k = tk = topk_ids.shape
+    n, idt = expert_offsets.shape[0], topk_ids.dtype
+    _call("moe_sort_routes", SortArgs.pack(
+        T, k, n - 1, _flat("topk_ids", topk_ids, tk, idt), _code("topk_ids", idt, _IDS),
+        _flat("expert_offsets", expert_offsets, (n,), _INT32),
+        _flat("route_row", route_row, tk, _INT32), _flat("row_route", row_route, (T * k,), _INT32),
+        _at(workspace), _bytes(workspace), _at(device_status)), stream)
 
 
 def moe_permute(x, route_row, expert_offsets, rows, stream=None):
     """rows[route_row[t, j]] = x[t]; rows past the last routed one become zeros.  x: [T, K] and
     rows: [num_rows, K] of one type (fp32, bf16, fp16).  See include/moe_prep.h."""
-    T, k = route_row.shape
-    K, n = rows.shape[1], rows.shape[0]
-    _check("moe_permute", load().moe_permute(
-        x.data_ptr(), _rows("x", x, T, K, rows.dtype), _dtype_of("rows", rows), T, K, k,
-        _flat("route_row", route_row, (T, k), torch.int32),
-        _flat("expert_offsets", expert_offsets, expert_offsets.shape[:1], torch.int32),
-        expert_offsets.shape[0] - 1, rows.data_ptr(), _rows("rows", rows, n, K, rows.dtype), n,
-        _raw_stream(stream)))
+    T, k = tk = route_row.shape
+    R, K = shape = rows.shape
+    n, dt = expert_offsets.shape[0], rows.dtype
+    _call("moe_permute", PermuteArgs.pack(
+        T, K, k, n - 1, R, _code("rows", dt), x.data_ptr(), _rows("x", x, (T, K), dt),
+        _flat("route_row", route_row, tk, _INT32),
+        _flat("expert_offsets", expert_offsets, (n,), _INT32), rows.data_ptr(),
+        _rows("rows", rows, shape, dt)), stream)
 
 
 def moe_unpermute(rows, route_row, topk_weights, out, stream=None):
     """out[t] = sum_j topk_weights[t, j] * rows[route_row[t, j]], summed in fp32; topk_weights None:
     every weight is 1.  See include/moe_prep.h."""
-    T, k = route_row.shape
-    n, K = rows.shape
-    _check("moe_unpermute", load().moe_unpermute(
-        rows.data_ptr(), _rows("rows", rows, n, K, rows.dtype), n, _dtype_of("rows", rows),
-        _flat("route_row", route_row, (T, k), torch.int32),
-        _flat("topk_weights", topk_weights, (T, k), torch.float32), T, K, k, out.data_ptr(),
-        _rows("out", out, T, K, rows.dtype), _raw_stream(stream)))
+    T, k = tk = route_row.shape
+    R, K = shape = rows.shape
+    dt = rows.dtype
+    _call("moe_unpermute", UnpermuteArgs.pack(
+        T, K, k, R, _code("rows", dt), rows.data_ptr(), _rows("rows", rows, shape, dt),
+        _flat("route_row", route_row, tk, _INT32),
+        _flat("topk_weights", topk_weights, tk, _FP32), out.data_ptr(),
+        _rows("out", out, (T, K), dt)), stream)
 
 
 def moe_permute_backward(d_rows, route_row, d_x, stream=None):
@@ -624,31 +670,37 @@ def moe_unpermute_backward(d_out, rows, route_row, topk_weights, expert_offsets,
                            stream=None):
     """Gradients of ``moe_unpermute``: d_rows [num_rows, K] (zeros past the last routed row) and
     d_weights fp32 [T, k].  See include/moe_prep.h."""
-    T, k = route_row.shape
-    n, K = rows.shape
-    _check("moe_unpermute_backward", load().moe_unpermute_backward(
-        d_out.data_ptr(), _rows("d_out", d_out, T, K, rows.dtype), rows.data_ptr(),
-        _rows("rows", rows, n, K, rows.dtype), n, _dtype_of("rows", rows),
-        _flat("route_row", route_row, (T, k), torch.int32),
-        _flat("topk_weights", topk_weights, (T, k), torch.float32),
-        _flat("expert_offsets", expert_offsets, expert_offsets.shape[:1], torch.int32),
-        expert_offsets.shape[0] - 1, T, K, k, d_rows.data_ptr(),
-        _rows("d_rows", d_rows, n, K, rows.dtype),
-        _flat("d_weights", d_weights, (T, k), torch.float32), _raw_stream(stream)))
+    T, k = tk = route_row.shape
+    R, K = shape = rows.shape
+    n, dt = expert_offsets.shape[0], rows.dtype
+    _call("moe_unpermute_backward", UnpermuteBackwardArgs.pack(
+        T, K, k, n - 1, R, _code("rows", dt), d_out.data_ptr(), _rows("d_out", d_out, (T, K), dt),
+        rows.data_ptr(), _rows("rows", rows, shape, dt),
+        _flat("route_row", route_row, tk, _INT32), _flat("topk_weights", topk_weights, tk, _FP32),
+        _flat("expert_offsets", expert_offsets, (n,), _INT32), d_rows.data_ptr(),
+        _rows("d_rows", d_rows, shape, dt), _flat("d_weights", d_weights, tk, _FP32)), stream)
 
 
-def _gate(gate, name, x, wdtype):
+def _gate(gate, name, shape, dtype, wdtype):
     """(kind, stride) of a gate, or of its gradient, by its shape: [K], [T] or [T, K] ([T, 1] is
     [T]; a [K] gate with T == K is taken per channel)."""
-    T, K = x.shape
     if gate is None:
         return MOE_GATE_NONE, 0
-    if gate.dim() == 1 and gate.shape[0] == K and gate.dtype == wdtype:
+    T, K = shape
+    gs = gate.shape
+    if gs == (K,) and gate.dtype is wdtype:
         _flat(name, gate, (K,), wdtype)
         return MOE_GATE_CHANNEL, 0
-    if gate.dtype == x.dtype and (gate.shape == (T,) or (gate.shape == (T, 1) and K != 1)):
+    if gate.dtype is dtype and (gs == (T,) or (gs == (T, 1) and K != 1)):
         return MOE_GATE_TOKEN, gate.stride(0)
-    return MOE_GATE_FULL, _rows(name, gate, T, K, x.dtype)
+    return MOE_GATE_FULL, _rows(name, gate, shape, dtype)
+
+
+def _weight_type(x, pre_weight, post_weight, gate):
+    for t in (pre_weight, post_weight, gate):
+        if t is not None:
+            return t.dtype
+    return x.dtype
 
 
 def moe_block_norm(x, z=None, post_weight=None, gate=None, scale=1.0, pre_weight=None,
@@ -660,19 +712,16 @@ def moe_block_norm(x, z=None, post_weight=None, gate=None, scale=1.0, pre_weight
     type (fp32, bf16 or fp16); a token gate: [T] of x's type; a full gate: [T, K].  Without z only
     y = rmsnorm(x) is written, without pre_weight only x_out.  rstd_post, rstd_pre: fp32 [T], kept
     for the gradient.  See include/moe_prep.h."""
-    T, K = x.shape
-    w = pre_weight if pre_weight is not None else post_weight
-    wdtype = w.dtype if w is not None else (gate.dtype if gate is not None else x.dtype)
-    kind, gs = _gate(gate, "gate", x, wdtype)
-    dt = x.dtype
-    a = BlockNormArgs(T, K, _dtype_of("x", x), _DTYPE.get(wdtype, -1), x.data_ptr(),
-                      _rows("x", x, T, K, dt), _at(z), _rows("z", z, T, K, dt),
-                      _flat("post_weight", post_weight, (K,), wdtype), _at(gate), kind, gs, scale,
-                      _flat("pre_weight", pre_weight, (K,), wdtype), weight_offset, eps,
-                      _at(x_out), _rows("x_out", x_out, T, K, dt), _at(y),
-                      _rows("y", y, T, K, dt), _flat("rstd_post", rstd_post, (T,), torch.float32),
-                      _flat("rstd_pre", rstd_pre, (T,), torch.float32))
-    _check("moe_block_norm", load().moe_block_norm(a, _raw_stream(stream)))
+    T, K = shape = x.shape
+    dt, wdt = x.dtype, _weight_type(x, pre_weight, post_weight, gate)
+    kind, gs = _gate(gate, "gate", shape, dt, wdt)
+    _call("moe_block_norm", BlockNormArgs.pack(
+        T, K, _code("x", dt), _code("weights", wdt), x.data_ptr(), _rows("x", x, shape, dt),
+        _at(z), _rows("z", z, shape, dt), _flat("post_weight", post_weight, (K,), wdt), _at(gate),
+        kind, gs, scale, _flat("pre_weight", pre_weight, (K,), wdt), weight_offset, eps,
+        _at(x_out), _rows("x_out", x_out, shape, dt), _at(y), _rows("y", y, shape, dt),
+        _flat("rstd_post", rstd_post, (T,), _FP32), _flat("rstd_pre", rstd_pre, (T,), _FP32)),
+        stream)
 
 
 def block_norm_workspace_size(num_tokens, hidden_size) -> int:
@@ -686,25 +735,23 @@ def moe_block_norm_backward(x, z=None, post_weight=None, gate=None, scale=1.0, p
     """Gradients of ``moe_block_norm`` from d_x_out and d_y (either may be None) and the forward's
     inputs, rstd_post and rstd_pre.  d_x is always written, the others where given.  workspace:
     uint8, block_norm_workspace_size() bytes.  See include/moe_prep.h."""
-    T, K = x.shape
-    w = pre_weight if pre_weight is not None else post_weight
-    wdtype = w.dtype if w is not None else (gate.dtype if gate is not None else x.dtype)
-    kind, gs = _gate(gate, "gate", x, wdtype)
-    dkind, dgs = _gate(d_gate, "d_gate", x, wdtype)
+    T, K = shape = x.shape
+    dt, wdt = x.dtype, _weight_type(x, pre_weight, post_weight, gate)
+    kind, gs = _gate(gate, "gate", shape, dt, wdt)
+    dkind, dgs = _gate(d_gate, "d_gate", shape, dt, wdt)
     if d_gate is not None and (dkind != kind or d_gate.shape != gate.shape):
         raise ValueError("d_gate must have the gate's shape and type")
-    dt, f32 = x.dtype, torch.float32
-    a = BlockNormBackwardArgs(
-        T, K, _dtype_of("x", x), _DTYPE.get(wdtype, -1), x.data_ptr(), _rows("x", x, T, K, dt),
-        _at(z), _rows("z", z, T, K, dt), _flat("post_weight", post_weight, (K,), wdtype),
-        _at(gate), kind, gs, scale, _flat("pre_weight", pre_weight, (K,), wdtype), weight_offset,
-        _flat("rstd_post", rstd_post, (T,), f32), _flat("rstd_pre", rstd_pre, (T,), f32),
-        _at(d_x_out), _rows("d_x_out", d_x_out, T, K, dt), _at(d_y), _rows("d_y", d_y, T, K, dt),
-        _at(d_x), _rows("d_x", d_x, T, K, dt), _at(d_z), _rows("d_z", d_z, T, K, dt), _at(d_gate),
-        dgs, _flat("d_post_weight", d_post_weight, (K,), wdtype),
-        _flat("d_pre_weight", d_pre_weight, (K,), wdtype), _at(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size())
-    _check("moe_block_norm_backward", load().moe_block_norm_backward(a, _raw_stream(stream)))
+    _call("moe_block_norm_backward", BlockNormBackwardArgs.pack(
+        T, K, _code("x", dt), _code("weights", wdt), x.data_ptr(), _rows("x", x, shape, dt),
+        _at(z), _rows("z", z, shape, dt), _flat("post_weight", post_weight, (K,), wdt), _at(gate),
+        kind, gs, scale, _flat("pre_weight", pre_weight, (K,), wdt), weight_offset,
+        _flat("rstd_post", rstd_post, (T,), _FP32), _flat("rstd_pre", rstd_pre, (T,), _FP32),
+        _at(d_x_out), _rows("d_x_out", d_x_out, shape, dt), _at(d_y),
+        _rows("d_y", d_y, shape, dt), _at(d_x), _rows("d_x", d_x, shape, dt), _at(d_z),
+        _rows("d_z", d_z, shape, dt), _at(d_gate), dgs,
+        _flat("d_post_weight", d_post_weight, (K,), wdt),
+        _flat("d_pre_weight", d_pre_weight, (K,), wdt), _at(workspace), _bytes(workspace)),
+        stream)
 
 
 def lora_workspace_size(num_tokens, in_features, out_features, num_adapters, rank) -> int:
@@ -718,19 +765,16 @@ def moe_lora_linear(x, weight, lora_a, lora_b, adapter_ids, lora_scale, out, wor
     (< 0: no adapter).  x [T, K], weight [N, K], lora_a [S, R, K], lora_b [S, N, R], out [T, N] of
     one type (bf16 or fp16); adapter_ids int32 [T]; lora_scale fp32 [S].  lora_a None: the
     projection alone.  workspace: uint8, lora_workspace_size() bytes.  See include/moe_prep.h."""
-    T, K = x.shape
-    N = weight.shape[0]
-    dt = x.dtype
-    S, R = (lora_a.shape[0], lora_a.shape[1]) if lora_a is not None else (0, 0)
-    a = LoraArgs(T, K, N, S, R, _dtype_of("x", x), x.data_ptr(), _rows("x", x, T, K, dt),
-                 _flat("weight", weight, (N, K), dt), _flat("lora_a", lora_a, (S, R, K), dt),
-                 _flat("lora_b", lora_b, (S, N, R), dt),
-                 _flat("adapter_ids", adapter_ids, (T,), torch.int32),
-                 _flat("lora_scale", lora_scale, (S,), torch.float32), out.data_ptr(),
-                 _rows("out", out, T, N, dt), _at(workspace),
-                 0 if workspace is None else workspace.numel() * workspace.element_size(),
-                 _at(device_status))
-    _check("moe_lora_linear", load().moe_lora_linear(a, _raw_stream(stream)))
+    T, K = shape = x.shape
+    N, dt = weight.shape[0], x.dtype
+    S, R = lora_a.shape[:2] if lora_a is not None else (0, 0)
+    _call("moe_lora_linear", LoraArgs.pack(
+        T, K, N, S, R, _code("x", dt), x.data_ptr(), _rows("x", x, shape, dt),
+        _flat("weight", weight, (N, K), dt), _flat("lora_a", lora_a, (S, R, K), dt),
+        _flat("lora_b", lora_b, (S, N, R), dt), _flat("adapter_ids", adapter_ids, (T,), _INT32),
+        _flat("lora_scale", lora_scale, (S,), _FP32), out.data_ptr(),
+        _rows("out", out, (T, N), dt), _at(workspace), _bytes(workspace), _at(device_status)),
+        stream)
 
 
 class MoeLayer:

@@ -2,12 +2,17 @@
 //
 // One warp per token; lane i holds logits i, i + 32, i + 64, ... in registers,
 // so a row is read once and coalesced.  Selection compares order-preserving
-// 32-bit integers of the keys: k rounds, each a warp maximum of the lanes' best
-// keys (redux.sync) and a warp minimum of the index among equal ones.  Without
-// a bias the key is the logit itself (softmax and sigmoid are monotone), so the
-// choice does not depend on how exp rounds.  With a sigmoid and a bias the key
-// is 1/(1+expf(-l)) + bias with IEEE division and no contraction, the value that
-// elementary fp32 tensor operations give.
+// 32-bit integers of the keys.  Without a bias the key is the logit itself (softmax
+// and sigmoid are monotone), so the choice does not depend on how exp rounds.  With a
+// sigmoid and a bias the key is 1/(1+expf(-l)) + bias with IEEE division and no
+// contraction, the value that elementary fp32 tensor operations give.
+//
+// Issue slots bound it, not memory.  Up to 256 experts each lane sorts its keys,
+// cut to make room for the expert's index in the low bits, and k rounds take the
+// largest head (one redux.sync) and pop it.  The cut keys decide unless two of the
+// taken ones, or the last taken and the next, are equal in what is left; then, and
+// above 256 experts, k rounds over the whole keys take the warp's maximum and the
+// lowest index among equal ones.
 #include "block_common.cuh"
 
 namespace moe {
@@ -49,23 +54,88 @@ __device__ __forceinline__ float exp_rel(float l, float m) {
   return l == m ? 1.0f : (l < m ? expf(l - m) : 0.0f);
 }
 
+// l becomes exp(l - m) for the warp's largest logit m; NaN and -inf give 0.
+template <int VPL>
+__device__ __forceinline__ void exp_row(float (&l)[VPL], float m) {
+  if (fabsf(m) < INFINITY) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) l[i] = expf((l[i] > -INFINITY ? l[i] : -INFINITY) - m);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) l[i] = l[i] > -INFINITY ? exp_rel(l[i], m) : 0.0f;
+  }
+}
+
 __device__ __forceinline__ int64_t load_id(const void* ids, int ids64, int64_t i) {
   return ids64 ? static_cast<const int64_t*>(ids)[i] : (int64_t)static_cast<const int32_t*>(ids)[i];
 }
 
-// Clears the keys of experts outside the best top_groups groups.  The keys go
-// through shared memory; lanes_per_group lanes share a group, each starting at
-// an offset of its own so that the groups' lanes fall into different banks.
+// Largest key of the warp, as the logit that it stands for.
+__device__ __forceinline__ float warp_max_key(uint32_t k) {
+  return key_value(__reduce_max_sync(0xFFFFFFFFu, k));
+}
+
+// A group's value from its two highest keys (0: none).
+__device__ __forceinline__ uint32_t group_key(const RouteParams& p, uint32_t k1, uint32_t k2) {
+  if (p.bias == nullptr || k1 == 0) return k1;
+  return order_key(__fadd_rn(key_value(k1), k2 ? key_value(k2) : 0.0f));
+}
+
+// Whether group g, whose value lane g << shift has in gk, is among the best
+// top_groups: fewer than these come before it.  Bit g << shift of the answer.
+__device__ __forceinline__ uint32_t best_groups(const RouteParams& p, uint32_t gk, int g,
+                                                int shift) {
+  int before = 0;
+  for (int o = 0; o < p.groups; ++o) {
+    const uint32_t v = __shfl_sync(0xFFFFFFFFu, gk, o << shift);
+    before += (v > gk || (v == gk && o < g)) ? 1 : 0;
+  }
+  return __ballot_sync(0xFFFFFFFFu, g < p.groups && gk != 0 && before < p.top_groups);
+}
+
+// Clears the keys of experts outside the best top_groups groups.  Where groups
+// are whole multiples of 32 experts, a register of the warp belongs to one group.
+// Otherwise the keys go through shared memory; lpg lanes share a group, each
+// starting at an offset of its own so that the groups' lanes fall into different
+// banks.
 template <int VPL>
 __device__ __forceinline__ void limit_groups(const RouteParams& p, uint32_t (&key)[VPL],
                                              uint32_t* sk, int lane) {
+  const int size = p.E / p.groups;
+  if (size % 32 == 0) {
+    const int regs = size / 32;
+    uint32_t gk = 0, k1 = 0, k2 = 0;
+    int g = 0, in = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      if (i * 32 >= p.E) break;
+      k2 = max(k2, min(k1, key[i]));
+      k1 = max(k1, key[i]);
+      if (++in < regs) continue;
+      const uint32_t m1 = __reduce_max_sync(0xFFFFFFFFu, k1);
+      const uint32_t who = __ballot_sync(0xFFFFFFFFu, k1 == m1);
+      const uint32_t m2 =
+          __reduce_max_sync(0xFFFFFFFFu, lane == __ffs(who) - 1 ? k2 : k1);
+      if (lane == g) gk = group_key(p, m1, m2);
+      k1 = k2 = 0;
+      in = 0;
+      ++g;
+    }
+    const uint32_t kept = best_groups(p, gk, lane, 0);
+    g = in = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      if (!((kept >> g) & 1u)) key[i] = 0;
+      if (++in == regs) in = 0, ++g;
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int e = i * 32 + lane;
     if (e < p.E) sk[e] = key[i];
   }
   __syncwarp();
-  const int size = p.E / p.groups;
   int lpg = 1, shift = 0;  // lanes per group, a power of two
   while (lpg * 2 * p.groups <= 32) lpg *= 2, ++shift;
   const int g = lane >> shift, sub = lane & (lpg - 1);
@@ -85,22 +155,95 @@ __device__ __forceinline__ void limit_groups(const RouteParams& p, uint32_t (&ke
     k2 = max(max(k2, b), min(k1, a));
     k1 = max(k1, a);
   }
-  uint32_t gk = k1;
-  if (p.bias != nullptr && k1 != 0) gk = order_key(key_value(k1) + (k2 ? key_value(k2) : 0.0f));
-  if (g >= p.groups) gk = 0;
-  // a group stays when fewer than top_groups others come before it
-  int before = 0;
-  for (int o = 0; o < p.groups; ++o) {
-    const uint32_t v = __shfl_sync(0xFFFFFFFFu, gk, o << shift);
-    before += (v > gk || (v == gk && o < g)) ? 1 : 0;
-  }
-  const bool stays = g < p.groups && gk != 0 && before < p.top_groups;
-  const uint32_t kept = __ballot_sync(0xFFFFFFFFu, stays);  // bit g << shift
+  const uint32_t kept = best_groups(p, g < p.groups ? group_key(p, k1, k2) : 0, g, shift);
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int e = i * 32 + lane;
     if (e < p.E && !((kept >> ((e / size) << shift)) & 1u)) key[i] = 0;
   }
+}
+
+__device__ __forceinline__ void order2(uint32_t& a, uint32_t& b) {  // a >= b
+  const uint32_t hi = max(a, b);
+  b = min(a, b);
+  a = hi;
+}
+// Descending, by a sorting network.
+template <int VPL>
+__device__ __forceinline__ void sort_keys(uint32_t (&c)[VPL]) {
+  if constexpr (VPL == 2) order2(c[0], c[1]);
+  if constexpr (VPL == 4 || VPL == 8) {
+#pragma unroll
+    for (int h = 0; h < VPL; h += 4) {
+      order2(c[h], c[h + 1]), order2(c[h + 2], c[h + 3]);
+      order2(c[h], c[h + 2]), order2(c[h + 1], c[h + 3]);
+      order2(c[h + 1], c[h + 2]);
+    }
+  }
+  if constexpr (VPL == 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) order2(c[i], c[i + 4]);
+    order2(c[2], c[4]), order2(c[3], c[5]);
+    order2(c[1], c[2]), order2(c[3], c[4]), order2(c[5], c[6]);
+  }
+}
+
+// The k experts of highest key, lane j the j-th (-1: none left).  Uses keys up.
+template <int VPL>
+__device__ __forceinline__ int take_exact(uint32_t (&key)[VPL], int k, int lane) {
+  uint32_t bk = 0;
+  int bi = 0, my_id = -1;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    if (key[i] > bk) bk = key[i], bi = i;
+  for (int j = 0; j < k; ++j) {
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, bk);
+    if (m == 0) break;
+    const uint32_t win =
+        __reduce_min_sync(0xFFFFFFFFu, bk == m ? (uint32_t)(bi * 32 + lane) : 0x7FFFFFFFu);
+    if (lane == j) my_id = (int)win;
+    if ((int)(win & 31u) == lane) {
+      const int wi = (int)(win >> 5);
+      bk = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        if (i == wi) key[i] = 0;
+        if (key[i] > bk) bk = key[i], bi = i;
+      }
+    }
+  }
+  return my_id;
+}
+
+// The same by cut keys; `whole`: the cut bits of every key are zero.  False when the
+// cut keys do not decide (the same for the whole warp).
+template <int VPL>
+__device__ __forceinline__ bool take_cut(const uint32_t (&key)[VPL], int k, int lane, bool whole,
+                                         int* id) {
+  constexpr uint32_t mask = VPL * 32 - 1;
+  uint32_t c[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    c[i] = key[i] ? (key[i] & ~mask) | (mask - (uint32_t)(i * 32 + lane)) : 0u;
+  sort_keys<VPL>(c);
+  uint32_t mine = 0;
+  for (int j = 0; j < k; ++j) {
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, c[0]);
+    if (lane == j) mine = m;
+    if (c[0] == m) {
+#pragma unroll
+      for (int i = 0; i + 1 < VPL; ++i) c[i] = c[i + 1];
+      c[VPL - 1] = 0;
+    }
+  }
+  // lane j against the one taken after it, the last against the largest left
+  const uint32_t left = __reduce_max_sync(0xFFFFFFFFu, c[0]);
+  const uint32_t after = __shfl_down_sync(0xFFFFFFFFu, mine, 1);
+  const uint32_t next = lane == k - 1 ? left : after;
+  const bool tie =
+      __any_sync(0xFFFFFFFFu, lane < k && next != 0 && ((mine ^ next) & ~mask) == 0);
+  *id = mine != 0 ? (int)(mask - (mine & mask)) : -1;
+  return whole || !tie;
 }
 
 template <typename T, int VPL>
@@ -119,15 +262,6 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(RouteParams p) 
     const int e = i * 32 + lane;
     l[i] = e < p.E ? to_f32(row[e]) : -INFINITY;
   }
-  float m_all = -INFINITY, z_all = 0.0f;
-  if (!p.sigmoid && !p.renorm) {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) m_all = fmaxf(m_all, l[i]);
-    m_all = warp_max(m_all);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) z_all += l[i] > -INFINITY ? exp_rel(l[i], m_all) : 0.0f;
-    z_all = warp_sum(z_all);
-  }
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int e = i * 32 + lane;
@@ -135,29 +269,25 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(RouteParams p) 
     if (p.bias != nullptr && e < p.E) v = __fadd_rn(p.sigmoid ? sigmoid(v) : v, __ldg(p.bias + e));
     key[i] = e < p.E ? order_key(v) : 0u;
   }
+  float m_all = -INFINITY, z_all = 0.0f;
+  if (!p.sigmoid && !p.renorm) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) top = max(top, p.bias == nullptr ? key[i] : order_key(l[i]));
+    m_all = warp_max_key(top);
+    exp_row<VPL>(l, m_all);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) z_all += l[i];
+    z_all = warp_sum(z_all);
+  }
   if (p.groups > 1) limit_groups<VPL>(p, key, smem_keys + warp * p.E, lane);
   const bool padding = p.is_padding != nullptr && p.is_padding[t] != 0;
-
-  uint32_t bk = 0;
-  int bi = 0;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i)
-    if (key[i] > bk) bk = key[i], bi = i;
   int my_id = -1;
-  for (int j = 0; j < p.k && !padding; ++j) {
-    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, bk);
-    if (m == 0) break;
-    const uint32_t win = __reduce_min_sync(0xFFFFFFFFu, bk == m ? (uint32_t)(bi * 32 + lane) : 0x7FFFFFFFu);
-    if (lane == j) my_id = (int)win;
-    if ((int)(win & 31u) == lane) {
-      const int wi = (int)(win >> 5);
-      bk = 0;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        if (i == wi) key[i] = 0;
-        if (key[i] > bk) bk = key[i], bi = i;
-      }
-    }
+  if (!padding) {
+    bool decided = false;
+    if constexpr (VPL <= 8)
+      decided = take_cut<VPL>(key, p.k, lane, sizeof(T) == 2 && p.bias == nullptr, &my_id);
+    if (!decided) my_id = take_exact<VPL>(key, p.k, lane);
   }
   // lane j holds the j-th expert
   const float lv = my_id >= 0 ? to_f32(row[my_id]) : -INFINITY;
@@ -211,27 +341,28 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_backward_kernel(RouteP
   }
   float d = 0.0f;
   if (!p.sigmoid && !p.renorm) {
-    float l[VPL], m = -INFINITY, z = 0.0f;
+    float l[VPL], z = 0.0f;
+    uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const int e = i * 32 + lane;
       l[i] = e < p.E ? to_f32(row[e]) : -INFINITY;
-      m = fmaxf(m, l[i]);
+      top = max(top, order_key(l[i]));
     }
-    m = warp_max(m);
+    const float m = warp_max_key(top);
+    exp_row<VPL>(l, m);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      l[i] = l[i] > -INFINITY ? exp_rel(l[i], m) : 0.0f;
-      z += l[i];
-    }
+    for (int i = 0; i < VPL; ++i) z += l[i];
     z = warp_sum(z);
-    const float w = id >= 0 ? exp_rel(lv, m) / z : 0.0f;
+    const float inv = z > 0.0f ? 1.0f / z : 0.0f;
+    const float w = id >= 0 ? exp_rel(lv, m) * inv : 0.0f;
     const float mean = warp_sum(dw * w);
     d = w * (dw - mean);
+    const float base = -(inv * mean);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const int e = i * 32 + lane;
-      if (e < p.E) drow[e] = from_f32<T>(z > 0.0f ? -(l[i] / z) * mean : 0.0f);
+      if (e < p.E) drow[e] = from_f32<T>(l[i] * base);
     }
   } else {
 #pragma unroll

@@ -475,13 +475,12 @@ size_t moe_sort_workspace_size(int64_t num_tokens, int64_t top_k, int64_t num_ex
   return blocks == 1 ? 0 : (size_t)hist_row(blocks) * num_experts * 4;
 }
 
-moe_status_t moe_sort_routes(const void* topk_ids, int32_t topk_ids_dtype, int64_t num_tokens,
-                             int64_t top_k, int64_t num_experts, int32_t* expert_offsets,
-                             int32_t* route_row, int32_t* row_route, void* workspace,
-                             size_t workspace_bytes, uint32_t* device_status, void* stream) {
+moe_status_t moe_sort_routes(const moe_sort_args_t* a, void* stream) {
   clear_error();
+  if (a == nullptr) return set_error(MOE_ERR_INVALID_ARGUMENT, "args is NULL");
+  const int64_t num_tokens = a->num_tokens, top_k = a->top_k, num_experts = a->num_experts;
   if (num_tokens < 0 || top_k < 0) return set_error(MOE_ERR_INVALID_ARGUMENT, "negative size");
-  if (topk_ids_dtype != MOE_IDS_INT32 && topk_ids_dtype != MOE_IDS_INT64)
+  if (a->topk_ids_dtype != MOE_IDS_INT32 && a->topk_ids_dtype != MOE_IDS_INT64)
     return set_error(MOE_ERR_INVALID_ARGUMENT, "bad topk_ids_dtype");
   if (num_experts < 1) return set_error(MOE_ERR_SHAPE, "num_experts must be >= 1");
   if (num_experts > moe::SORT_MAX_EXPERTS)
@@ -489,64 +488,65 @@ moe_status_t moe_sort_routes(const void* topk_ids, int32_t topk_ids_dtype, int64
   if (top_k > 0 && num_tokens > ((int64_t)1 << 26) / top_k)
     return set_error(MOE_ERR_UNSUPPORTED, "num_tokens * top_k must be at most 2^26");
   const int64_t R = num_tokens * top_k;
-  if (!expert_offsets || (R > 0 && (!topk_ids || !route_row || !row_route)))
+  if (!a->expert_offsets || (R > 0 && (!a->topk_ids || !a->route_row || !a->row_route)))
     return set_error(MOE_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
   SortParams p{};
-  p.ids = topk_ids;
-  p.ids64 = topk_ids_dtype == MOE_IDS_INT64;
+  p.ids = a->topk_ids;
+  p.ids64 = a->topk_ids_dtype == MOE_IDS_INT64;
   p.align = 1;
   p.R = p.rows = (int32_t)R;
   p.E = (int32_t)num_experts;
   sort_split(R > 0 ? R : 1, &p.blocks, &p.per_block);
-  p.offsets = expert_offsets;
-  p.route_row = route_row;
-  p.row_route = row_route;
-  p.hist = static_cast<int32_t*>(workspace);
+  p.offsets = a->expert_offsets;
+  p.route_row = a->route_row;
+  p.row_route = a->row_route;
+  p.hist = static_cast<int32_t*>(a->workspace);
   p.hist_row = hist_row(p.blocks);
-  p.status = device_status;
+  p.status = a->device_status;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (p.blocks > 1) {
     const size_t need = (size_t)p.hist_row * num_experts * 4;
-    if (workspace == nullptr || workspace_bytes < need)
+    if (a->workspace == nullptr || a->workspace_bytes < need)
       return set_error(MOE_ERR_WORKSPACE, "sorting needs %zu bytes of workspace, got %zu", need,
-                       workspace_bytes);
-    if ((reinterpret_cast<uintptr_t>(workspace) & 15u) != 0)
+                       a->workspace_bytes);
+    if ((reinterpret_cast<uintptr_t>(a->workspace) & 15u) != 0)
       return set_error(MOE_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
   }
   return launch_sort(p, s);
 }
 
-moe_status_t moe_permute(const void* x, int64_t x_stride0, int32_t dtype, int64_t num_tokens,
-                         int64_t hidden_size, int64_t top_k, const int32_t* route_row,
-                         const int32_t* expert_offsets, int64_t num_experts, void* rows,
-                         int64_t rows_stride0, int64_t num_rows, void* stream) {
+moe_status_t moe_permute(const moe_permute_args_t* a, void* stream) {
   clear_error();
-  moe_status_t st = check_rows(num_tokens, hidden_size, top_k, num_rows, dtype);
+  if (a == nullptr) return set_error(MOE_ERR_INVALID_ARGUMENT, "args is NULL");
+  const int64_t num_tokens = a->num_tokens, hidden_size = a->hidden_size;
+  const int64_t top_k = a->top_k, num_rows = a->num_rows;
+  moe_status_t st = check_rows(num_tokens, hidden_size, top_k, num_rows, a->dtype);
   if (st != MOE_OK) return st;
-  if (num_experts < 0) return set_error(MOE_ERR_INVALID_ARGUMENT, "negative size");
+  if (a->num_experts < 0) return set_error(MOE_ERR_INVALID_ARGUMENT, "negative size");
   if (num_rows == 0 || hidden_size == 0) return MOE_OK;
-  if (!rows || !expert_offsets || (num_tokens * top_k > 0 && (!x || !route_row)))
+  if (!a->rows || !a->expert_offsets || (num_tokens * top_k > 0 && (!a->x || !a->route_row)))
     return set_error(MOE_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
-  if ((num_tokens > 1 && x_stride0 < hidden_size) || (num_rows > 1 && rows_stride0 < hidden_size))
+  if ((num_tokens > 1 && a->x_stride0 < hidden_size) ||
+      (num_rows > 1 && a->rows_stride0 < hidden_size))
     return set_error(MOE_ERR_SHAPE, "row stride smaller than the row");
   RowParams p{};
   p.T = num_tokens;
   p.K = hidden_size;
   p.num_rows = num_rows;
   p.k = (int)top_k;
-  p.route_row = route_row;
-  p.offsets = expert_offsets;
-  p.E = num_experts;
-  p.x = x;
-  p.x_stride = x_stride0;
-  p.out_rows = rows;
-  p.out_rows_stride = rows_stride0;
-  return with_dtype(dtype, [&](auto v) {
+  p.route_row = a->route_row;
+  p.offsets = a->expert_offsets;
+  p.E = a->num_experts;
+  p.x = a->x;
+  p.x_stride = a->x_stride0;
+  p.out_rows = a->rows;
+  p.out_rows_stride = a->rows_stride0;
+  return with_dtype(a->dtype, [&](auto v) {
     using T = decltype(v);
     constexpr int V = 16 / sizeof(T);
     const bool wide = packs16(hidden_size, sizeof(T)) &&
-                      rows_aligned16(x, x_stride0, sizeof(T), num_tokens) &&
-                      rows_aligned16(rows, rows_stride0, sizeof(T), num_rows);
+                      rows_aligned16(a->x, a->x_stride0, sizeof(T), num_tokens) &&
+                      rows_aligned16(a->rows, a->rows_stride0, sizeof(T), num_rows);
     auto go = [&](auto kernel, int vec) {
       const int64_t chunk = (int64_t)moe::PERMUTE_VECS * 32 * vec;
       const int64_t warps = (num_tokens + num_rows) * ((hidden_size + chunk - 1) / chunk);
@@ -557,35 +557,36 @@ moe_status_t moe_permute(const void* x, int64_t x_stride0, int32_t dtype, int64_
   });
 }
 
-moe_status_t moe_unpermute(const void* rows, int64_t rows_stride0, int64_t num_rows, int32_t dtype,
-                           const int32_t* route_row, const float* topk_weights,
-                           int64_t num_tokens, int64_t hidden_size, int64_t top_k, void* out,
-                           int64_t out_stride0, void* stream) {
+moe_status_t moe_unpermute(const moe_unpermute_args_t* a, void* stream) {
   clear_error();
-  moe_status_t st = check_rows(num_tokens, hidden_size, top_k, num_rows, dtype);
+  if (a == nullptr) return set_error(MOE_ERR_INVALID_ARGUMENT, "args is NULL");
+  const int64_t num_tokens = a->num_tokens, hidden_size = a->hidden_size;
+  const int64_t top_k = a->top_k, num_rows = a->num_rows;
+  moe_status_t st = check_rows(num_tokens, hidden_size, top_k, num_rows, a->dtype);
   if (st != MOE_OK) return st;
   if (num_tokens == 0 || hidden_size == 0) return MOE_OK;
-  if (!out || (num_rows > 0 && !rows) || (top_k > 0 && !route_row))
+  if (!a->out || (num_rows > 0 && !a->rows) || (top_k > 0 && !a->route_row))
     return set_error(MOE_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
-  if ((num_tokens > 1 && out_stride0 < hidden_size) || (num_rows > 1 && rows_stride0 < hidden_size))
+  if ((num_tokens > 1 && a->out_stride0 < hidden_size) ||
+      (num_rows > 1 && a->rows_stride0 < hidden_size))
     return set_error(MOE_ERR_SHAPE, "row stride smaller than the row");
   RowParams p{};
   p.T = num_tokens;
   p.K = hidden_size;
   p.num_rows = num_rows;
   p.k = (int)top_k;
-  p.route_row = route_row;
-  p.w = topk_weights;
-  p.rows = rows;
-  p.rows_stride = rows_stride0;
-  p.out = out;
-  p.out_stride = out_stride0;
-  return with_dtype(dtype, [&](auto v) {
+  p.route_row = a->route_row;
+  p.w = a->topk_weights;
+  p.rows = a->rows;
+  p.rows_stride = a->rows_stride0;
+  p.out = a->out;
+  p.out_stride = a->out_stride0;
+  return with_dtype(a->dtype, [&](auto v) {
     using T = decltype(v);
     constexpr int V = 16 / sizeof(T);
     const bool wide = packs16(hidden_size, sizeof(T)) &&
-                      rows_aligned16(rows, rows_stride0, sizeof(T), num_rows) &&
-                      rows_aligned16(out, out_stride0, sizeof(T), num_tokens);
+                      rows_aligned16(a->rows, a->rows_stride0, sizeof(T), num_rows) &&
+                      rows_aligned16(a->out, a->out_stride0, sizeof(T), num_tokens);
     auto go = [&](auto kernel, int vec, int kb) {
       const int64_t chunk = (int64_t)(8 / kb) * 32 * vec;
       const int64_t warps = num_tokens * ((hidden_size + chunk - 1) / chunk);
@@ -602,48 +603,45 @@ moe_status_t moe_unpermute(const void* rows, int64_t rows_stride0, int64_t num_r
   });
 }
 
-moe_status_t moe_unpermute_backward(const void* d_out, int64_t d_out_stride0, const void* rows,
-                                    int64_t rows_stride0, int64_t num_rows, int32_t dtype,
-                                    const int32_t* route_row, const float* topk_weights,
-                                    const int32_t* expert_offsets, int64_t num_experts,
-                                    int64_t num_tokens, int64_t hidden_size, int64_t top_k,
-                                    void* d_rows, int64_t d_rows_stride0, float* d_weights,
-                                    void* stream) {
+moe_status_t moe_unpermute_backward(const moe_unpermute_backward_args_t* a, void* stream) {
   clear_error();
-  moe_status_t st = check_rows(num_tokens, hidden_size, top_k, num_rows, dtype);
+  if (a == nullptr) return set_error(MOE_ERR_INVALID_ARGUMENT, "args is NULL");
+  const int64_t num_tokens = a->num_tokens, hidden_size = a->hidden_size;
+  const int64_t top_k = a->top_k, num_rows = a->num_rows;
+  moe_status_t st = check_rows(num_tokens, hidden_size, top_k, num_rows, a->dtype);
   if (st != MOE_OK) return st;
-  if (num_experts < 0) return set_error(MOE_ERR_INVALID_ARGUMENT, "negative size");
+  if (a->num_experts < 0) return set_error(MOE_ERR_INVALID_ARGUMENT, "negative size");
   if (num_tokens * top_k == 0 && num_rows == 0) return MOE_OK;
-  if ((num_rows > 0 && hidden_size > 0 && (!rows || !d_rows)) || !expert_offsets ||
+  if ((num_rows > 0 && hidden_size > 0 && (!a->rows || !a->d_rows)) || !a->expert_offsets ||
       (num_tokens * top_k > 0 &&
-       (!route_row || !topk_weights || !d_weights || (hidden_size > 0 && !d_out))))
+       (!a->route_row || !a->topk_weights || !a->d_weights || (hidden_size > 0 && !a->d_out))))
     return set_error(MOE_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
-  if ((num_tokens > 1 && d_out_stride0 < hidden_size) ||
-      (num_rows > 1 && (rows_stride0 < hidden_size || d_rows_stride0 < hidden_size)))
+  if ((num_tokens > 1 && a->d_out_stride0 < hidden_size) ||
+      (num_rows > 1 && (a->rows_stride0 < hidden_size || a->d_rows_stride0 < hidden_size)))
     return set_error(MOE_ERR_SHAPE, "row stride smaller than the row");
   RowParams p{};
   p.T = num_tokens;
   p.K = hidden_size;
   p.num_rows = num_rows;
   p.k = (int)top_k;
-  p.route_row = route_row;
-  p.w = topk_weights;
-  p.offsets = expert_offsets;
-  p.E = num_experts;
-  p.x = d_out;
-  p.x_stride = d_out_stride0;
-  p.rows = rows;
-  p.rows_stride = rows_stride0;
-  p.out_rows = d_rows;
-  p.out_rows_stride = d_rows_stride0;
-  p.d_w = d_weights;
-  return with_dtype(dtype, [&](auto v) {
+  p.route_row = a->route_row;
+  p.w = a->topk_weights;
+  p.offsets = a->expert_offsets;
+  p.E = a->num_experts;
+  p.x = a->d_out;
+  p.x_stride = a->d_out_stride0;
+  p.rows = a->rows;
+  p.rows_stride = a->rows_stride0;
+  p.out_rows = a->d_rows;
+  p.out_rows_stride = a->d_rows_stride0;
+  p.d_w = a->d_weights;
+  return with_dtype(a->dtype, [&](auto v) {
     using T = decltype(v);
     constexpr int V = 16 / sizeof(T);
     const bool wide = packs16(hidden_size, sizeof(T)) &&
-                      rows_aligned16(d_out, d_out_stride0, sizeof(T), num_tokens) &&
-                      rows_aligned16(rows, rows_stride0, sizeof(T), num_rows) &&
-                      rows_aligned16(d_rows, d_rows_stride0, sizeof(T), num_rows);
+                      rows_aligned16(a->d_out, a->d_out_stride0, sizeof(T), num_tokens) &&
+                      rows_aligned16(a->rows, a->rows_stride0, sizeof(T), num_rows) &&
+                      rows_aligned16(a->d_rows, a->d_rows_stride0, sizeof(T), num_rows);
     auto go = [&](auto kernel) {
       return launched(launch_pdl(kernel, one_wave(kernel, num_tokens + num_rows, moe::BACK_THREADS),
                                  dim3(moe::BACK_THREADS), 0, static_cast<cudaStream_t>(stream), p),

@@ -33,7 +33,7 @@ def route(lib, cls=B.RouteArgs, fn="moe_route", **kw):
     base.update(dict(num_groups=1, top_groups=1) if cls is B.RouteArgs else
                 dict(d_logits_stride0=16))
     base.update(kw)
-    return getattr(lib, fn)(fill(cls, **base), None)
+    return getattr(lib, fn)(ctypes.byref(fill(cls, **base)), None)
 
 
 def test_route(lib):
@@ -64,52 +64,69 @@ def test_route(lib):
     assert route(lib, top_k=33, num_experts=64, **back) == UNSUPPORTED
 
 
+def test_packed_structs_have_the_c_layout():
+    for cls in (B.RouteArgs, B.RouteBackwardArgs, B.SortArgs, B.PermuteArgs, B.UnpermuteArgs,
+                B.UnpermuteBackwardArgs, B.BlockNormArgs, B.BlockNormBackwardArgs, B.LoraArgs):
+        values = [float(i) if t is ctypes.c_float else i + 1
+                  for i, (_, t) in enumerate(cls._fields_)]
+        raw = cls.pack(*values)
+        a = cls(*values)
+        assert bytes(a)[:len(raw)] == raw and len(raw) > ctypes.sizeof(cls) - 8
+
+
 def test_sort(lib):
-    def sort(ids=FAKE, dt=B.MOE_IDS_INT32, T=8, k=2, E=4, off=FAKE, rr=FAKE, ro=FAKE, ws=FAKE,
-             n=1 << 20):
-        return lib.moe_sort_routes(ids, dt, T, k, E, off, rr, ro, ws, n, None, None)
-    assert sort(T=-1) == INVALID
-    assert sort(dt=7) == INVALID
-    assert sort(E=0) == SHAPE
-    assert sort(E=1025) == UNSUPPORTED
-    assert sort(T=1 << 26, k=2) == UNSUPPORTED
-    assert sort(off=None) == INVALID
-    assert sort(ids=None) == INVALID
-    assert sort(T=100000, ws=None) == WORKSPACE
-    assert sort(T=100000, n=16) == WORKSPACE
-    assert sort(T=100000, ws=FAKE + 4) == ALIGNMENT
+    def sort(**kw):
+        base = dict(num_tokens=8, top_k=2, num_experts=4, workspace_bytes=1 << 20)
+        base.update(kw)
+        return lib.moe_sort_routes(ctypes.byref(fill(B.SortArgs, **base)), None)
+    assert lib.moe_sort_routes(None, None) == INVALID
+    assert sort(num_tokens=-1) == INVALID
+    assert sort(topk_ids_dtype=7) == INVALID
+    assert sort(num_experts=0) == SHAPE
+    assert sort(num_experts=1025) == UNSUPPORTED
+    assert sort(num_tokens=1 << 26) == UNSUPPORTED
+    for name in ("expert_offsets", "topk_ids", "route_row", "row_route"):
+        assert sort(**{name: None}) == INVALID
+    assert sort(num_tokens=100000, workspace=None) == WORKSPACE
+    assert sort(num_tokens=100000, workspace_bytes=16) == WORKSPACE
+    assert sort(num_tokens=100000, workspace=FAKE + 4) == ALIGNMENT
     assert lib.moe_sort_workspace_size(64, 2, 8) == 0
     assert lib.moe_sort_workspace_size(-1, 2, 8) == 0
     assert lib.moe_sort_workspace_size(8192, 8, 256) > 0
 
 
 def test_rows(lib):
-    def permute(x=FAKE, xs=64, dt=B.MOE_DTYPE_BF16, T=4, K=64, k=2, rr=FAKE, off=FAKE, E=4,
-                rows=FAKE, rs=64, n=8):
-        return lib.moe_permute(x, xs, dt, T, K, k, rr, off, E, rows, rs, n, None)
-    assert permute(T=-1) == INVALID
-    assert permute(dt=9) == INVALID
-    assert permute(k=33) == UNSUPPORTED
-    assert permute(n=1 << 31) == UNSUPPORTED
-    assert permute(K=0) == OK and permute(n=0) == OK
-    assert permute(rows=None) == INVALID and permute(off=None) == INVALID
-    assert permute(x=None) == INVALID
-    assert permute(xs=63) == SHAPE and permute(rs=63) == SHAPE
+    def call(fn, cls, **kw):
+        base = dict(num_tokens=4, hidden_size=64, top_k=2, num_rows=8, dtype=B.MOE_DTYPE_BF16)
+        if cls is not B.UnpermuteArgs:
+            base["num_experts"] = 4
+        base.update({n: 64 for n, _ in cls._fields_ if n.endswith("stride0")})
+        base.update(kw)
+        return getattr(lib, fn)(ctypes.byref(fill(cls, **base)), None)
 
-    def unpermute(rows=FAKE, rs=64, n=8, dt=0, rr=FAKE, w=FAKE, T=4, K=64, k=2, out=FAKE, os=64):
-        return lib.moe_unpermute(rows, rs, n, dt, rr, w, T, K, k, out, os, None)
-    assert unpermute(T=0) == OK
-    assert unpermute(out=None) == INVALID and unpermute(rr=None) == INVALID
-    assert unpermute(os=3) == SHAPE and unpermute(k=40) == UNSUPPORTED
+    def permute(**kw):
+        return call("moe_permute", B.PermuteArgs, **kw)
 
-    def back(up=FAKE, us=64, rows=FAKE, rs=64, n=8, dt=0, rr=FAKE, w=FAKE, off=FAKE, E=4, T=4,
-             K=64, k=2, dr=FAKE, ds=64, dw=FAKE):
-        return lib.moe_unpermute_backward(up, us, rows, rs, n, dt, rr, w, off, E, T, K, k, dr, ds,
-                                          dw, None)
-    assert back(T=0, n=0) == OK
-    for name in ("up", "rows", "rr", "w", "off", "dr", "dw"):
+    def unpermute(**kw):
+        return call("moe_unpermute", B.UnpermuteArgs, **kw)
+
+    def back(**kw):
+        return call("moe_unpermute_backward", B.UnpermuteBackwardArgs, **kw)
+
+    for f in (permute, unpermute, back):
+        assert f(num_tokens=-1) == INVALID and f(dtype=9) == INVALID
+        assert f(top_k=33) == UNSUPPORTED and f(num_rows=1 << 31) == UNSUPPORTED
+        assert f(rows=None) == INVALID and f(route_row=None) == INVALID
+        assert f(rows_stride0=63) == SHAPE
+    assert permute(hidden_size=0) == OK and permute(num_rows=0) == OK
+    assert permute(x=None) == INVALID and permute(expert_offsets=None) == INVALID
+    assert permute(x_stride0=63) == SHAPE and permute(num_experts=-1) == INVALID
+    assert unpermute(num_tokens=0) == OK
+    assert unpermute(out=None) == INVALID and unpermute(out_stride0=3) == SHAPE
+    assert back(num_tokens=0, num_rows=0) == OK
+    for name in ("d_out", "topk_weights", "expert_offsets", "d_rows", "d_weights"):
         assert back(**{name: None}) == INVALID
-    assert back(ds=1) == SHAPE and back(us=1) == SHAPE and back(dt=-1) == INVALID
+    assert back(d_rows_stride0=1) == SHAPE and back(d_out_stride0=1) == SHAPE
 
 
 def norm(lib, cls=B.BlockNormArgs, fn="moe_block_norm", **kw):
@@ -118,7 +135,7 @@ def norm(lib, cls=B.BlockNormArgs, fn="moe_block_norm", **kw):
     if cls is B.BlockNormBackwardArgs:
         base["workspace_bytes"] = 1 << 20
     base.update(kw)
-    return getattr(lib, fn)(fill(cls, **base), None)
+    return getattr(lib, fn)(ctypes.byref(fill(cls, **base)), None)
 
 
 def test_block_norm(lib):
@@ -154,7 +171,7 @@ def test_lora(lib):
         base = dict(num_tokens=4, in_features=64, out_features=32, num_adapters=2, rank=8,
                     dtype=B.MOE_DTYPE_BF16, x_stride0=64, out_stride0=32, workspace_bytes=1 << 20)
         base.update(kw)
-        return lib.moe_lora_linear(fill(B.LoraArgs, **base), None)
+        return lib.moe_lora_linear(ctypes.byref(fill(B.LoraArgs, **base)), None)
     assert lib.moe_lora_linear(None, None) == INVALID
     assert lora(num_tokens=0) == OK and lora(out_features=0) == OK
     assert lora(rank=-8) == INVALID
