@@ -58,6 +58,8 @@ struct LoraParams {
   const float* scale;
   void* out;
   int64_t out_stride;
+  float* partials;  // pair, nullable: pieces of tiles, [pairs][2][LP_TILE tokens][LP_HALF]
+  int pairs;        // of CTAs
   float* h;        // [shares][T][R]
   int shares;      // of K in the shrink
   int share_k;     // K of one share, a multiple of 64
@@ -715,6 +717,33 @@ __device__ __forceinline__ Runs tile_runs(const LoraParams& p, int64_t pos0, int
 // Last group of the run that begins at g.
 __device__ __forceinline__ int run_end(const Runs& r, int g) { return __ffs(r.ends >> g) - 1 + g; }
 
+// The work of the pairs: whole tiles dealt out in rounds, and the tiles of a last
+// round that would leave pairs idle cut along K, so that each pair has a piece.
+constexpr int LP_MIN_SLABS = 8;  // of a piece
+constexpr int64_t LP_PIECE = 2 * LP_TILE * LP_HALF;  // its sums
+struct Work {
+  int units, pairs, full, parts, items, per, slabs;
+  __device__ __forceinline__ Work(int n_units, int n_pairs, int n_slabs, bool cut)
+      : units(n_units), pairs(n_pairs), slabs(n_slabs) {
+    const int rest = n_units % n_pairs;
+    parts = cut && rest > 0 ? min(n_pairs / rest, n_slabs / LP_MIN_SLABS) : 1;
+    if (parts < 2) parts = 1;
+    per = (n_slabs + parts - 1) / parts;
+    parts = (n_slabs + per - 1) / per;  // every piece has slabs
+    full = parts > 1 ? n_units - rest : n_units;
+    items = full + (n_units - full) * parts;
+  }
+};
+struct Item {
+  int unit, kb0, kb1, piece;  // piece: -1, a whole tile; else its place among the pieces
+  bool adapters;              // the adapters' part goes with the first piece
+};
+__device__ __forceinline__ Item work_item(const Work& w, int i) {
+  if (i < w.full) return Item{i, 0, w.slabs, -1, true};
+  const int j = i - w.full, part = j % w.parts;
+  return Item{w.full + j / w.parts, part * w.per, min(w.slabs, (part + 1) * w.per), j, part == 0};
+}
+
 // A persistent pair of CTAs; CTA r of the pair has features [128 r, 128 r + 128)
 // and tokens [128 r, ...) of a tile's operands, and those features' sums for all
 // 256 tokens.  The first CTA issues the MMAs of both; its full[] and hfull
@@ -785,7 +814,7 @@ __global__ void __launch_bounds__(LP_THREADS, 1)
   const int n_tiles = (int)((p.N + LP_TILE - 1) / LP_TILE);
   const int units = n_tiles * (int)((places + LP_TILE - 1) / LP_TILE);
   const int first = (int)(blockIdx.x >> 1), stride = (int)(gridDim.x >> 1);
-  const int slabs = (int)((p.K + 63) / 64);
+  const Work work(units, stride, (int)((p.K + 63) / 64), p.partials != nullptr);
   const int r16 = (int)((p.R + 15) & ~15);
   const int rchunks = (r16 + 63) / 64;
   const bool one_part = 2 * r16 <= 64;  // rounding and remainder fit one tile
@@ -801,7 +830,9 @@ __global__ void __launch_bounds__(LP_THREADS, 1)
       if (++stage == LP_STAGES) stage = 0, phase ^= 1u;
     };
     bool ok = true;
-    for (int u = first; ok && u < units; u += stride) {
+    for (int i = first; ok && i < work.items; i += stride) {
+      const Item item = work_item(work, i);
+      const int u = item.unit;
       const int n0 = (u % n_tiles) * LP_TILE + (int)rank * LP_HALF;
       const int64_t t0 = (int64_t)(u / n_tiles) * LP_TILE;
       // this CTA's four groups: first row in x where their tokens follow one
@@ -820,9 +851,9 @@ __global__ void __launch_bounds__(LP_THREADS, 1)
         sorted_rows = sorted_rows || from[i] < 0;
       }
       if (sorted_rows) pdl_wait();
-      for (int kb = 0; kb < slabs && ok; ++kb) {
+      for (int kb = item.kb0; kb < item.kb1 && ok; ++kb) {
 #ifdef MOE_TEST_WITHHOLD_STAGE
-        if (blockIdx.x < 2 && kb > 0) {  // as in lora_split_kernel: the first pair stops here
+        if (blockIdx.x < 2 && kb > item.kb0) {  // as in lora_split_kernel: the first pair stops here
           ok = false;
           break;
         }
@@ -846,7 +877,7 @@ __global__ void __launch_bounds__(LP_THREADS, 1)
         __syncwarp();
         advance();
       }
-      if (!adapters || !ok) continue;
+      if (!adapters || !item.adapters || !ok) continue;
       const Runs runs = tile_runs(p, t0, places, lane);
       for (int b = 0; b < builds && ok; ++b) {
         const int rc = (one_part ? b : b >> 1) * 64;
@@ -876,10 +907,12 @@ __global__ void __launch_bounds__(LP_THREADS, 1)
     int stage = 0, ab = 0, hs = 0;
     uint32_t phase = 0, hphase = 0, aphase = 0;
     bool ok = rank == 0;
-    for (int u = first; ok && u < units; u += stride) {
+    for (int i = first; ok && i < work.items; i += stride) {
+      const Item item = work_item(work, i);
+      const int u = item.unit;
       ok = warp_wait(tempty0 + 8 * ab, aphase ^ 1u, abort_flag, p.status);
       const uint32_t d = tmem + (uint32_t)(ab * LP_TILE);
-      for (int kb = 0; kb < slabs && ok; ++kb) {
+      for (int kb = item.kb0; kb < item.kb1 && ok; ++kb) {
         ok = warp_wait(full0 + 8 * stage, phase, abort_flag, p.status);
         if (!ok) break;
         fence_after();
@@ -887,14 +920,16 @@ __global__ void __launch_bounds__(LP_THREADS, 1)
         const uint64_t ad = sw128_desc(s), bd = sw128_desc(s + LP_HALF * 128);
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_f16_pair(d, ad + 2 * k, bd + 2 * k, IDESC, kb > 0 || k > 0);
+          for (int k = 0; k < 4; ++k) mma_f16_pair(d, ad + 2 * k, bd + 2 * k, IDESC,
+                         kb > item.kb0 || k > 0);
           mma_commit_pair(empty0 + 8 * stage);
         }
         __syncwarp();
         if (++stage == LP_STAGES) stage = 0, phase ^= 1u;
       }
       Runs runs{};
-      if (adapters) runs = tile_runs(p, (int64_t)(u / n_tiles) * LP_TILE, places, lane);
+      if (adapters && item.adapters)
+        runs = tile_runs(p, (int64_t)(u / n_tiles) * LP_TILE, places, lane);
       if (runs.starts != 0) {
         for (int b = 0; b < builds && ok; ++b) {
           const int steps = min(4, r16 / 16 - (one_part ? b : b >> 1) * 4);
@@ -939,7 +974,10 @@ __global__ void __launch_bounds__(LP_THREADS, 1)
     uint32_t hphase = 0;
     bool ok = true, waited = p.wait_first != 0;
     const int R = (int)p.R;
-    for (int u = first; adapters && u < units; u += stride) {
+    for (int i = first; adapters && i < work.items; i += stride) {
+      const Item item = work_item(work, i);
+      if (!item.adapters) continue;
+      const int u = item.unit;
       // one warp decides for all whether to go on, so that the barriers match
       if (bt == 0) *s_go = ok && *abort_flag == 0;
       build_sync();
@@ -1029,12 +1067,12 @@ __global__ void __launch_bounds__(LP_THREADS, 1)
         if (!ok) break;
         uint8_t* to = hbuf + hs * LP_H_BYTES;
         const int pieces = min(8, (r16 - rc) / 8);  // of a row, those that the MMAs read
-        for (int i = bt; i < LP_HALF * pieces; i += U * LP_BUILDERS) {
+        for (int e = bt; e < LP_HALF * pieces; e += U * LP_BUILDERS) {
           int t[U], r[U];
           Pack<T, 8> hi[U], low[U];
 #pragma unroll
           for (int k = 0; k < U; ++k) {
-            const int j = i + k * LP_BUILDERS;
+            const int j = e + k * LP_BUILDERS;
             t[k] = j < LP_HALF * pieces ? j / pieces : -1;
             r[k] = rc + (j % pieces) * 8;
           }
@@ -1058,13 +1096,16 @@ __global__ void __launch_bounds__(LP_THREADS, 1)
     const int nl = (warp & 3) * 32 + lane;
     int ab = 0;
     uint32_t aphase = 0;
-    for (int u = first; u < units; u += stride) {
+    for (int i = first; i < work.items; i += stride) {
       if (!warp_wait(tfull0 + 8 * ab, aphase, abort_flag, p.status) || *abort_flag != 0) break;
       fence_after();
+      const Item item = work_item(work, i);
+      const int u = item.unit;
       const int64_t n = (int64_t)(u % n_tiles) * LP_TILE + rank * LP_HALF + nl;
       const int64_t t0 = (int64_t)(u / n_tiles) * LP_TILE;
       const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(ab * LP_TILE);
       T* out = static_cast<T*>(p.out) + n;
+      float* part = p.partials + item.piece * LP_PIECE + rank * (LP_TILE * LP_HALF) + nl;
 #pragma unroll 1
       for (int c = 0; c < LP_TILE; c += 32) {
         uint32_t v[2][16];
@@ -1075,6 +1116,12 @@ __global__ void __launch_bounds__(LP_THREADS, 1)
         const int tok = mine < places ? (adapters ? p.order[mine] : (int)mine) : -1;
         tmem_wait16(v[0]);
         tmem_wait16(v[1]);
+        if (item.piece >= 0) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            part[(c + j) * LP_HALF] = __uint_as_float(v[j >> 4][j & 15]);
+          continue;
+        }
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
           const int t = __shfl_sync(0xFFFFFFFFu, tok, j);
@@ -1099,6 +1146,49 @@ __global__ void __launch_bounds__(LP_THREADS, 1)
   }
 }
 
+// Sums the pieces of the tiles that were cut, in their order, and stores them: a
+// block eight tokens of a tile, a thread four features of two of them.
+constexpr int JOIN_TOKENS = 8;
+
+template <typename T>
+__global__ void __launch_bounds__(256) lora_join_kernel(LoraParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t places = *p.places;
+  const int n_tiles = (int)((p.N + LP_TILE - 1) / LP_TILE);
+  const Work work(n_tiles * (int)((places + LP_TILE - 1) / LP_TILE), p.pairs,
+                  (int)((p.K + 63) / 64), true);
+  const int u = work.full + blockIdx.y;
+  if (u >= work.units) return;
+  const int f = (threadIdx.x & 63) * 4;  // feature of the tile
+  const int64_t n = (int64_t)(u % n_tiles) * LP_TILE + f;
+  const float* from = p.partials + (int64_t)blockIdx.y * work.parts * LP_PIECE +
+                      (f / LP_HALF) * (LP_TILE * LP_HALF) + f % LP_HALF;
+  for (int c = blockIdx.x * JOIN_TOKENS + (threadIdx.x >> 6); c < (blockIdx.x + 1) * JOIN_TOKENS;
+       c += 4) {
+    const int64_t place = (int64_t)(u / n_tiles) * LP_TILE + c;
+    const int t = place < places ? p.order[place] : -1;
+    if (t < 0) continue;
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int q0 = 0; q0 < work.parts; q0 += 4) {
+      float4 v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        v[q] = q0 + q < work.parts
+                   ? __ldcg(reinterpret_cast<const float4*>(from + (q0 + q) * LP_PIECE + c * LP_HALF))
+                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        sum.x += v[q].x, sum.y += v[q].y, sum.z += v[q].z, sum.w += v[q].w;
+    }
+    const float w[4] = {sum.x, sum.y, sum.z, sum.w};
+    T* out = static_cast<T*>(p.out) + t * p.out_stride + n;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < p.N) out[e] = from_f32<T>(w[e]);
+  }
+}
+
 }  // namespace moe
 
 namespace moe_host {
@@ -1115,6 +1205,7 @@ struct LoraPlan {
   int64_t places;                   // most places of the tokens' order (pair)
   int64_t order_words;              // of the workspace: order and the sort's scratch
   int64_t copy_words;               // of the workspace: x in that order
+  int64_t part_words;               // of the workspace: pieces of tiles (pair)
   int tok, tiles, shares, share_k, zs;  // shrink: tokens a block
   int nt, splits;                   // lora_split_kernel
 };
@@ -1128,6 +1219,7 @@ static LoraPlan lora_plan(int64_t T, int64_t K, int64_t N, int64_t S, int64_t R)
     q.places = (T + (moe::RUN - 1) * (S + 1) + 127) / 128 * 128;
     q.order_words = (q.places + (int64_t)token_order_scratch(T, S) + 3) / 4 * 4;
     q.copy_words = (q.places * K / 2 + 3) / 4 * 4;
+    q.part_words = sms / 2 * moe::LP_PIECE;
   }
   // Shrink: 64 tokens as they come, or 128 in their order, and a block for each
   // adapter that these may have (in the order a group of RUN has one).  A block
@@ -1163,7 +1255,7 @@ static LoraPlan lora_plan(int64_t T, int64_t K, int64_t N, int64_t S, int64_t R)
 }
 
 static size_t lora_workspace(const LoraPlan& q, int64_t T, int64_t R) {
-  return (size_t)((q.order_words + q.copy_words + (int64_t)q.shares * T * R) * 4);
+  return (size_t)((q.order_words + q.copy_words + q.part_words + (int64_t)q.shares * T * R) * 4);
 }
 
 // Dynamic shared memory limit of a kernel, raised once per device.
@@ -1237,10 +1329,14 @@ static moe_status_t launch_pair(const LoraParams& p, int64_t places, const CUten
   if (st != MOE_OK) return st;
   const int64_t units = (p.N + moe::LP_TILE - 1) / moe::LP_TILE *
                         ((places + moe::LP_TILE - 1) / moe::LP_TILE);
-  const int64_t pairs = num_sms() / 2;
-  const dim3 grid((unsigned)(2 * (units < pairs ? units : pairs)));
-  return launched(launch_cluster(moe::lora_pair_kernel<T>, grid, moe::LP_THREADS, 2, moe::LP_SMEM,
-                                 s, p, w, x, xs, b), "projection");
+  const int64_t pairs = num_sms() / 2;  // with adapters few tiles are cut to give all a piece
+  const dim3 grid((unsigned)(2 * (units < pairs && p.partials == nullptr ? units : pairs)));
+  st = launched(launch_cluster(moe::lora_pair_kernel<T>, grid, moe::LP_THREADS, 2, moe::LP_SMEM,
+                               s, p, w, x, xs, b), "projection");
+  if (st != MOE_OK || p.partials == nullptr) return st;
+  return launched(launch_pdl(moe::lora_join_kernel<T>,
+                             dim3(moe::LP_TILE / moe::JOIN_TOKENS, (unsigned)(pairs / 2)), dim3(256),
+                             0, s, p), "projection join");
 }
 
 template <typename T>
@@ -1258,6 +1354,8 @@ static moe_status_t launch_lora(const moe_lora_args_t* a, const LoraPlan& q, Lor
   if (adapters) {
     if (q.pair) {
       p.xs = static_cast<int32_t*>(a->workspace) + q.order_words;
+      p.partials = static_cast<float*>(a->workspace) + q.order_words + q.copy_words;
+      p.pairs = num_sms() / 2;
       if (!make_map16(&b, bf16, a->lora_b, p.S * p.N, p.R, p.R, moe::LP_HALF) ||
           !make_map16(&xs, bf16, p.xs, q.places, p.K, p.K, moe::RUN))
         return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the adapters");
@@ -1354,7 +1452,7 @@ moe_status_t moe_lora_linear(const moe_lora_args_t* a, void* stream) {
   p.scale = a->lora_scale;
   p.out = a->out;
   p.out_stride = a->out_stride0;
-  p.h = static_cast<float*>(a->workspace) + q.order_words + q.copy_words;
+  p.h = static_cast<float*>(a->workspace) + q.order_words + q.copy_words + q.part_words;
   p.shares = q.shares;
   p.share_k = q.share_k;
   p.splits = q.splits;
