@@ -501,7 +501,8 @@ moe_status_t moe_route_backward(const moe_route_backward_args_t* args, void* str
 /* row_route[r] = t * k + j of row r, -1 for r >= expert_offsets[E].          */
 /* topk_ids int32 or int64 [T, k]; expert_offsets int32 [E + 1]; route_row    */
 /* and row_route int32 [T * k].  workspace: moe_sort_workspace_size() bytes,  */
-/* 16-byte aligned, need not be cleared.  E > 1024 -> UNSUPPORTED.                             */
+/* 16-byte aligned, need not be cleared; it serves fewer routes as well.      */
+/* E > 1024 -> UNSUPPORTED.                                                   */
 /*                                                                           */
 /* With `rows` [num_rows, K] in the order of the experts:                     */
 /*   moe_permute             rows[route_row[t, j]] = x[t]; rows from           */
@@ -598,8 +599,8 @@ moe_status_t moe_unpermute_backward(const moe_unpermute_backward_args_t* args, v
 /* d_post_weight and d_pre_weight (weight_dtype) from d_x_out and d_y (either */
 /* may be NULL: zero) and the inputs, rstd_post and rstd_pre of the forward.  */
 /* Sums over tokens run in fp32 in a fixed order.  workspace:                 */
-/* moe_block_norm_workspace_size() bytes, need not be cleared.  Every output  */
-/* but d_x may be NULL.                                                       */
+/* moe_block_norm_workspace_size() bytes, need not be cleared; it serves      */
+/* fewer tokens as well.  Every output but d_x may be NULL.                   */
 /* Errors: K > 16384 -> UNSUPPORTED.                                          */
 /* ------------------------------------------------------------------------ */
 typedef struct moe_block_norm_args {
@@ -677,7 +678,8 @@ size_t moe_block_norm_workspace_size(int64_t num_tokens, int64_t hidden_size);
 /* [N, K], lora_a [S, R, K], lora_b [S, N, R] contiguous; adapter_ids int32   */
 /* [T]; lora_scale fp32 [S]; bf16 or fp16.  An adapter of lower rank than R   */
 /* has zero rows in lora_a.  num_adapters == 0: the projection alone.         */
-/* workspace: moe_lora_workspace_size() bytes, need not be cleared.           */
+/* workspace: moe_lora_workspace_size() bytes, need not be cleared; it serves */
+/* every call with fewer tokens as well.                                      */
 /* Errors: K % 8, R % 8, x_stride0 % 8 != 0, x, weight, lora_a, lora_b not    */
 /* 16-byte aligned -> ALIGNMENT; R > 128, num_adapters > 1023, fp32 ->        */
 /* UNSUPPORTED.  A GEMM wait that ran out sets MOE_DEV_TIMEOUT.               */

@@ -1254,8 +1254,14 @@ static LoraPlan lora_plan(int64_t T, int64_t K, int64_t N, int64_t S, int64_t R)
   return q;
 }
 
+// The sums of the shrink come last: shares * T <= 16 T, and as tiles * shares is at
+// most two blocks an SM, shares * T <= 2 SMs * (tokens of a tile) unless shares is 1.
+// Bounded so, the size grows with T: a workspace serves every shorter batch too.
 static size_t lora_workspace(const LoraPlan& q, int64_t T, int64_t R) {
-  return (size_t)((q.order_words + q.copy_words + q.part_words + (int64_t)q.shares * T * R) * 4);
+  int64_t rows = 2 * (int64_t)num_sms() * q.tok;
+  if (rows > 16 * T) rows = 16 * T;
+  if (rows < T) rows = T;
+  return (size_t)((q.order_words + q.copy_words + q.part_words + rows * R) * 4);
 }
 
 // Dynamic shared memory limit of a kernel, raised once per device.

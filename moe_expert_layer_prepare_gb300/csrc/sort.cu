@@ -403,6 +403,14 @@ static void sort_split(int64_t R, int32_t* blocks, int32_t* per_block) {
 
 static int32_t hist_row(int32_t blocks) { return (blocks + 3) / 4 * 4; }
 
+// Grows with R, so that a workspace serves fewer routes too.
+static size_t sort_workspace(int64_t R, int64_t E) {
+  if (R <= kSortOneBlock) return 0;
+  const int64_t blocks = (R + 1023) / 1024;
+  return (size_t)hist_row((int32_t)(blocks < moe::SORT_MAX_BLOCKS ? blocks : moe::SORT_MAX_BLOCKS)) *
+         E * 4;
+}
+
 static moe_status_t launch_sort(const SortParams& p, cudaStream_t s) {
   if (p.blocks > 1) {
     moe_status_t st = launched(launch_pdl(moe::sort_count_kernel, dim3(p.blocks),
@@ -470,9 +478,7 @@ extern "C" {
 
 size_t moe_sort_workspace_size(int64_t num_tokens, int64_t top_k, int64_t num_experts) {
   if (num_tokens <= 0 || top_k <= 0 || num_experts <= 0) return 0;
-  int32_t blocks, per;
-  sort_split(num_tokens * top_k, &blocks, &per);
-  return blocks == 1 ? 0 : (size_t)hist_row(blocks) * num_experts * 4;
+  return sort_workspace(num_tokens * top_k, num_experts);
 }
 
 moe_status_t moe_sort_routes(const moe_sort_args_t* a, void* stream) {
@@ -505,7 +511,7 @@ moe_status_t moe_sort_routes(const moe_sort_args_t* a, void* stream) {
   p.status = a->device_status;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (p.blocks > 1) {
-    const size_t need = (size_t)p.hist_row * num_experts * 4;
+    const size_t need = sort_workspace(R, num_experts);
     if (a->workspace == nullptr || a->workspace_bytes < need)
       return set_error(MOE_ERR_WORKSPACE, "sorting needs %zu bytes of workspace, got %zu", need,
                        a->workspace_bytes);

@@ -166,6 +166,19 @@ def test_block_norm(lib):
     assert lib.moe_block_norm_workspace_size(4, 64) > 0
 
 
+def test_workspaces_serve_shorter_calls(lib):
+    ts = [1, 2, 7, 31, 63, 64, 65, 100, 127, 128, 129, 300, 511, 512, 513, 700, 1024, 1500, 2048,
+          2049, 3500, 5000, 8192, 16385, 16500, 40000, 131073, 300000]
+    for k, n, s, r in ((64, 64, 1, 8), (7168, 4096, 16, 64), (2048, 7168, 1000, 128)):
+        sizes = [lib.moe_lora_workspace_size(t, k, n, s, r) for t in ts]
+        assert sizes == sorted(sizes)
+    for f in (lambda t: lib.moe_sort_workspace_size(t, 1, 256),
+              lambda t: lib.moe_sort_workspace_size(t, 8, 1000),
+              lambda t: lib.moe_block_norm_workspace_size(t, 4096)):
+        sizes = [f(t) for t in ts]
+        assert sizes == sorted(sizes)
+
+
 def test_lora(lib):
     def lora(**kw):
         base = dict(num_tokens=4, in_features=64, out_features=32, num_adapters=2, rank=8,
