@@ -10,14 +10,15 @@
 
 namespace moe {
 
-// VEC weights of a pack as they lie in shared memory, in their own type.
+// VEC weights of a pack as they lie in shared memory, in their own type; fp32 ones
+// four a plane, so that neighbouring threads read neighbouring 16 bytes.
 template <int VEC>
-__device__ __forceinline__ void read_weights(const uint8_t* s, int dtype, int c,
+__device__ __forceinline__ void read_weights(const uint8_t* s, int dtype, int c, int packs,
                                              float2 (&w)[VEC / 2]) {
   if (dtype == MOE_DTYPE_FP32) {
 #pragma unroll
     for (int i = 0; i < VEC / 4; ++i) {
-      const float4 v = *reinterpret_cast<const float4*>(s + (size_t)c * VEC * 4 + i * 16);
+      const float4 v = *reinterpret_cast<const float4*>(s + ((size_t)i * packs + c) * 16);
       w[2 * i] = make_float2(v.x, v.y), w[2 * i + 1] = make_float2(v.z, v.w);
     }
     return;
@@ -55,8 +56,8 @@ __device__ __forceinline__ void fetch_weights(uint8_t* dst, const void* src, int
                    "l"(g)
                    : "memory");
     } else {
-      copy16(dst + o, g);
-      if (bytes == 32) copy16(dst + o + 16, g + 16);
+      copy16(dst + (size_t)c * 16, g);
+      if (bytes == 32) copy16(dst + (size_t)(packs + c) * 16, g + 16);
     }
   }
 }
@@ -145,13 +146,13 @@ __global__ void __launch_bounds__(512, NV <= 2 ? 2 : 1) block_norm_rows_kernel(N
         for (int q = 0; q < H; ++q) v[q] = z.get2(q);
         if (p.post_w != nullptr) {
           float2 w[H];
-          read_weights<VEC>(s_post, w_dtype, c, w);
+          read_weights<VEC>(s_post, w_dtype, c, packs, w);
 #pragma unroll
           for (int q = 0; q < H; ++q) v[q] = mul2(mul2(v[q], both(rz)), add2(w[q], offset));
         }
         if (p.gate_kind == MOE_GATE_CHANNEL) {
           float2 g[H];
-          read_weights<VEC>(s_gate, w_dtype, c, g);
+          read_weights<VEC>(s_gate, w_dtype, c, packs, g);
 #pragma unroll
           for (int q = 0; q < H; ++q) v[q] = mul2(v[q], g[q]);
         } else if (p.gate_kind == MOE_GATE_FULL) {
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(512, NV <= 2 ? 2 : 1) block_norm_rows_kernel(N
       const int c = tid + i * threads;
       if (c >= packs) break;
       float2 w[H];
-      read_weights<VEC>(s_pre, w_dtype, c, w);
+      read_weights<VEC>(s_pre, w_dtype, c, packs, w);
       P o;
 #pragma unroll
       for (int q = 0; q < H; ++q) o.set2(q, mul2(mul2(xo[i][q], both(rx)), add2(w[q], offset)));

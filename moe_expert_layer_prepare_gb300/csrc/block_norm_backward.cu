@@ -12,8 +12,9 @@ namespace moe {
 // Rows of 16-byte packs that fit shared memory twice: everything from one
 // reading.  A block takes every gridDim.x-th row, the next one's tensors on their
 // way to shared memory; the row's three sums cost one barrier, then the packs
-// are read again from shared memory for the gradients.  The [K] tensors lie there
-// in fp32, offset added.  Each thread keeps the column sums of its packs in
+// (kept in registers, or with two a thread read again) give the gradients.  The [K] tensors lie there
+// in fp32, offset added, a pack's first four values in one plane and the rest in the
+// next, so that neighbouring threads read neighbouring 16 bytes.  Each thread keeps the column sums of its packs in
 // registers over all rows of the block.
 template <typename T, int NV, int GATE>  // GATE: channel, full, or none for the others
 __global__ void __launch_bounds__(512) block_norm_backward_kernel(NormParams p, int stages) {
@@ -67,7 +68,9 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(NormParams p, 
       float v[VEC];
       load_weights<VEC>(w, p.w_dtype, (int64_t)c * VEC, offset, v);
 #pragma unroll
-      for (int q = 0; q < H; ++q) to[c * H + q] = make_float2(v[2 * q], v[2 * q + 1]);
+      for (int q = 0; q < H; q += 2)
+        *reinterpret_cast<float4*>(to + (q / 2 * packs + c) * 2) =
+            make_float4(v[2 * q], v[2 * q + 1], v[2 * q + 2], v[2 * q + 3]);
     };
     if (post) keep(s_post, p.post_w, p.offset);
     if (pre) keep(s_pre, p.pre_w, p.offset);
@@ -84,7 +87,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(NormParams p, 
   auto read = [&](const float2* s, int c, float2 (&w)[H]) {
 #pragma unroll
     for (int q = 0; q < H; q += 2) {
-      const float4 v = *reinterpret_cast<const float4*>(s + c * H + q);
+      const float4 v = *reinterpret_cast<const float4*>(s + (q / 2 * packs + c) * 2);
       w[q] = make_float2(v.x, v.y), w[q + 1] = make_float2(v.z, v.w);
     }
   };
@@ -177,11 +180,12 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(NormParams p, 
       return both(0.0f);
     };
     float2 t0 = both(0.0f), t1 = t0, t2 = t0;
+    float2 zh[H], gw[H], xh[H], dy[H], e[H];  // with one pack a thread kept to the end
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = tid + i * threads;
       if (c >= packs) break;
-      float2 zh[H], gw[H], a[H], xh[H], dy[H], e[H];
+      float2 a[H];
       t0 = add2(t0, columns(c, zh, gw, a, xh, dy, e));
 #pragma unroll
       for (int q = 0; q < H; ++q) {
@@ -206,8 +210,10 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(NormParams p, 
     for (int i = 0; i < NV; ++i) {
       const int c = tid + i * threads;
       if (c >= packs) break;
-      float2 zh[H], gw[H], a[H], xh[H], dy[H], e[H];
-      columns(c, zh, gw, a, xh, dy, e);
+      if (NV > 1) {
+        float2 a[H];
+        columns(c, zh, gw, a, xh, dy, e);
+      }
       P ox, oz;
 #pragma unroll
       for (int q = 0; q < H; ++q) {
