@@ -4,8 +4,12 @@
 //   n = z rz wp,  x' = x + s g n,  y = x' rx wq      (rz, rx: inverse RMS)
 //
 // A block of threads per row, so x and z are read once and x' and y written
-// once; two sums over the row, one after the other, since x' needs rz.  Bound by
-// HBM, so the next row is copied to shared memory during a row's sums.
+// once; two sums over the row, one after the other, since x' needs rz (one pass
+// with the square of x + s g n multiplied out would cancel).  Bound by HBM, as
+// long as enough rows are at work to cover the two sums' barriers: the next row is
+// copied to shared memory meanwhile, and up to three blocks share an SM.
+// Measured: 8192 x 7168 bf16, token gate: 73 us, 6.4 TB/s; 8192 x 4096 with a full
+// gate 52 us, 6.4 TB/s; one row of 7168: 3.6 us.
 #include "block_norm.cuh"
 
 namespace moe {
@@ -62,13 +66,14 @@ __device__ __forceinline__ void fetch_weights(uint8_t* dst, const void* src, int
   }
 }
 
-constexpr int FWD_STAGES = 2;
-
 // Rows of 16-byte packs: a block takes every gridDim.x-th row and has the next
 // one's x, z and full gate on their way to shared memory while it works; the
-// [K] tensors come there once.
-template <typename T, int NV>
-__global__ void __launch_bounds__(512, NV <= 2 ? 2 : 1) block_norm_rows_kernel(NormParams p) {
+// [K] tensors come there once.  With one STAGE the next row is copied over this
+// one as soon as x' is in registers (each thread reads only packs that it copied),
+// with two from the row's start.
+template <typename T, int NV, int STAGES>
+__global__ void __launch_bounds__(512, NV <= 2 ? (STAGES == 1 ? 3 : 2) : 1)
+    block_norm_rows_kernel(NormParams p) {
   constexpr int VEC = 16 / sizeof(T), H = VEC / 2;
   using P = Pack<T, VEC>;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -80,7 +85,7 @@ __global__ void __launch_bounds__(512, NV <= 2 ? 2 : 1) block_norm_rows_kernel(N
   const int stage_packs = arrays * packs;
   const int w_dtype = p.w_dtype;
   const size_t w_bytes = (size_t)p.K * (w_dtype == MOE_DTYPE_FP32 ? 4 : 2);
-  uint8_t* s_post = smem + (size_t)FWD_STAGES * stage_packs * 16;
+  uint8_t* s_post = smem + (size_t)STAGES * stage_packs * 16;
   uint8_t* s_pre = s_post + (p.post_w != nullptr ? w_bytes : 0);
   uint8_t* s_gate = s_pre + (p.pre_w != nullptr ? w_bytes : 0);
   pdl_wait();
@@ -112,12 +117,14 @@ __global__ void __launch_bounds__(512, NV <= 2 ? 2 : 1) block_norm_rows_kernel(N
   float ahead = factor(blockIdx.x);
   int it = 0;
   for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, it ^= 1) {
-    fetch(t + gridDim.x, it ^ 1);
-    copies_commit();
+    if (STAGES == 2) {
+      fetch(t + gridDim.x, it ^ 1);
+      copies_commit();
+    }
     const float2 branch = both(ahead);
     ahead = factor(t + gridDim.x);
-    copies_wait<FWD_STAGES - 1>();
-    const P* st = stage0 + it * stage_packs;
+    copies_wait<STAGES - 1>();
+    const P* st = STAGES == 2 ? stage0 + it * stage_packs : stage0;
     float rz = 1.0f;
     if (p.post_w != nullptr) {
       float2 ss = both(0.0f);
@@ -173,6 +180,10 @@ __global__ void __launch_bounds__(512, NV <= 2 ? 2 : 1) block_norm_rows_kernel(N
       }
 #pragma unroll
       for (int q = 0; q < H; ++q) ss = fma2(v[q], v[q], ss);
+    }
+    if (STAGES == 1) {
+      fetch(t + gridDim.x, 0);
+      copies_commit();
     }
     if (p.pre_w == nullptr) continue;
     const float rx = rsqrtf(fmaf(block_sum(ss.x + ss.y, part[it][1]), inv_k, p.eps));
@@ -273,21 +284,23 @@ namespace moe_host {
 
 using moe::NormParams;
 
+constexpr size_t kThirdBlockSmem = 75 * 1024;  // dynamic, of a block with two more beside it
+
 // Shared memory of a row block: the stages and the [K] tensors.
-static size_t rows_smem(const NormParams& p, size_t elem) {
+static size_t rows_smem(const NormParams& p, size_t elem, int stages) {
   const int arrays = 1 + (p.z != nullptr) + (p.gate_kind == MOE_GATE_FULL);
   const int weights = (p.post_w != nullptr) + (p.pre_w != nullptr) +
                       (p.gate_kind == MOE_GATE_CHANNEL);
-  return (size_t)p.K * (moe::FWD_STAGES * arrays * elem + weights * dtype_size(p.w_dtype));
+  return (size_t)p.K * (stages * arrays * elem + weights * dtype_size(p.w_dtype));
 }
 
-template <typename T, int NV>
+template <typename T, int NV, int STAGES = 2>
 static moe_status_t launch_rows(const NormParams& p, int threads, cudaStream_t s) {
-  const size_t smem = rows_smem(p, sizeof(T));
+  const size_t smem = rows_smem(p, sizeof(T), STAGES);
   const int64_t cap =
-      (int64_t)num_sms() * resident_with<moe::block_norm_rows_kernel<T, NV>>(threads, smem);
+      (int64_t)num_sms() * resident_with<moe::block_norm_rows_kernel<T, NV, STAGES>>(threads, smem);
   if (cap == 0) return set_error(MOE_ERR_CUDA, "block norm: no resident block");
-  return launched(launch_pdl(moe::block_norm_rows_kernel<T, NV>,
+  return launched(launch_pdl(moe::block_norm_rows_kernel<T, NV, STAGES>,
                              dim3((unsigned)(p.T < cap ? p.T : cap)), dim3(threads), smem, s, p),
                   "block norm");
 }
@@ -366,8 +379,15 @@ moe_status_t moe_block_norm(const moe_block_norm_args_t* a, void* stream) {
     w.weights(p.pre_w);
     const int64_t packs = w.ok ? K / V : K;
     auto threads = [&](int nv) { return (int)(((packs + nv - 1) / nv + 31) / 32 * 32); };
-    if (w.ok && rows_smem(p, sizeof(E)) <= kMaxBlockSmem) {
-      if (packs <= 256) return launch_rows<E, 1>(p, threads(1), s);
+    // One pack a thread up to 512, in two stages (8192 x 4096 full gate: 52 us; two
+    // packs a thread: 56; one stage and a third block: 55).  Above, two packs and, where
+    // three blocks fit, one stage: 8192 x 7168 73 us against 90 with two stages and two
+    // blocks, 8192 x 8192 88 against 91.  Longer rows: two stages (1000 x 16384: 24 us, one
+    // stage: 46), the sums' barriers being rarer there.
+    if (w.ok && rows_smem(p, sizeof(E), 2) <= kMaxBlockSmem) {
+      if (packs <= 512) return launch_rows<E, 1>(p, threads(1), s);
+      if (packs <= 1024 && rows_smem(p, sizeof(E), 1) <= kThirdBlockSmem)
+        return launch_rows<E, 2, 1>(p, threads(2), s);
       if (packs <= 1024) return launch_rows<E, 2>(p, threads(2), s);
       if (packs <= 2048) return launch_rows<E, 4>(p, threads(4), s);
       return launch_rows<E, 8>(p, threads(8), s);
