@@ -174,6 +174,14 @@ def test_weight_offset_and_many_rows():
     check(5003, 72, "bf16", "fp32", "full", offset=1.0)
 
 
+@pytest.mark.parametrize("T,K,dtype,wdtype", [(701, 4096, "bf16", "bf16"), (1003, 5120, "bf16", "bf16"),
+                                              (1003, 7168, "fp16", "fp16"), (701, 8192, "bf16", "fp32"),
+                                              (401, 7168, "fp32", "fp32"), (333, 16384, "bf16", "bf16")])
+@pytest.mark.parametrize("gate", ["token", "full"])
+def test_several_long_rows_a_block(T, K, dtype, wdtype, gate):
+    check(T, K, dtype, wdtype, gate)
+
+
 def test_in_place_zero_rows_and_infinite_values():
     s = tensors(8, 512, "bf16", "bf16", "none", "plain")
     x, z, post, pre = s["x"], s["z"], s["post"], s["pre"]
