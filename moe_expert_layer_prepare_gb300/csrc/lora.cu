@@ -1210,6 +1210,10 @@ struct LoraPlan {
   int nt, splits;                   // lora_split_kernel
 };
 
+// Blocks of the shrink that an SM is given: four of 64 tokens by 32 ranks (62
+// registers a thread; 64 tokens of 36 adapters: 20.3 us against 22.5 with two), else two.
+static int shrink_fill(int tok, int64_t R) { return tok == 64 && R <= 32 ? 4 : 2; }
+
 static LoraPlan lora_plan(int64_t T, int64_t K, int64_t N, int64_t S, int64_t R) {
   LoraPlan q{};
   const int64_t sms = num_sms();
@@ -1221,32 +1225,35 @@ static LoraPlan lora_plan(int64_t T, int64_t K, int64_t N, int64_t S, int64_t R)
     q.copy_words = (q.places * K / 2 + 3) / 4 * 4;
     q.part_words = sms / 2 * moe::LP_PIECE;
   }
-  // Shrink: 64 tokens as they come, or 128 in their order, and a block for each
-  // adapter that these may have (in the order a group of RUN has one).  A block
-  // whose tokens have fewer ends at once, so K is dealt out, in shares at least 256
-  // wide, by the number of adapters that they have on average.
-  q.tok = q.pair ? 128 : 64;
+  // Shrink: 64 tokens, from 129 on 128 (they read A_a once for twice the tokens: 512
+  // tokens 65 us against 72, 200 of rank 16 37 against 35), as they come or in their
+  // order, and a block for each adapter that these may have (in the order a group of
+  // RUN has one).  A block whose tokens have fewer ends at once, so K is dealt out, in
+  // shares at least 128 wide, by the number of adapters that they have on average.
+  q.tok = T > 128 ? 128 : 64;
   q.tiles = (int)((q.places + q.tok - 1) / q.tok);
   const int64_t groups = q.pair ? q.tok / moe::RUN : (T < q.tok ? T : q.tok);
   q.zs = (int)(S < groups ? (S < 1 ? 1 : S) : groups);
   if (q.pair) q.zs = (int)groups;  // block z copies group z's rows too
   double live = q.pair ? 1.0 + (double)S * q.tok / (double)T : q.zs;
   if (live > q.zs) live = q.zs;
-  int64_t shares = (int64_t)(2.0 * sms / (q.tiles * live));
-  if (shares > (K + 255) / 256) shares = (K + 255) / 256;
+  int64_t shares = (int64_t)(shrink_fill(q.tok, R) * sms / (q.tiles * live));
+  if (shares > (K + 127) / 128) shares = (K + 127) / 128;
   if (shares > 16) shares = 16;
   if (shares < 1) shares = 1;
   q.share_k = (int)(((K + shares - 1) / shares + 63) / 64 * 64);
   q.shares = (int)((K + q.share_k - 1) / q.share_k);
   // Split projection: the smallest tile that holds the batch, up to 128 tokens; a
-  // cluster shares a tile's K while tiles leave CTA slots empty.
+  // cluster shares a tile's K while tiles leave CTA slots empty; eight CTAs for the
+  // smallest tiles only where each has an SM, joining eight sums being most of their
+  // work otherwise (16 tokens, 4096 x 7168: 15.1 us against 16.7).
   // (Shared memory holds the adapters' part of 128 tokens up to rank 64.)
   q.nt = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 || R > 64 ? 64 : 128));
   const int64_t tiles = (N + moe::LG_M - 1) / moe::LG_M * ((T + q.nt - 1) / q.nt);
   const int64_t slots = q.nt <= 64 ? 2 * sms : sms;
   const int64_t slabs = (K + 63) / 64;
   q.splits = 1;
-  while (q.splits < 8 && tiles * q.splits * 2 <= slots) {
+  while (q.splits < 8 && tiles * q.splits * 2 <= (q.splits < 4 || q.nt > 16 ? slots : sms)) {
     const int64_t per = (slabs + 2 * q.splits - 1) / (2 * q.splits);
     if (per < 4 || per * (2 * q.splits - 1) >= slabs) break;  // every share has slabs
     q.splits *= 2;
@@ -1255,10 +1262,11 @@ static LoraPlan lora_plan(int64_t T, int64_t K, int64_t N, int64_t S, int64_t R)
 }
 
 // The sums of the shrink come last: shares * T <= 16 T, and as tiles * shares is at
-// most two blocks an SM, shares * T <= 2 SMs * (tokens of a tile) unless shares is 1.
+// most shrink_fill blocks an SM, shares * T <= that * SMs * (tokens of a tile) unless
+// shares is 1.
 // Bounded so, the size grows with T: a workspace serves every shorter batch too.
 static size_t lora_workspace(const LoraPlan& q, int64_t T, int64_t R) {
-  int64_t rows = 2 * (int64_t)num_sms() * q.tok;
+  int64_t rows = shrink_fill(q.tok, R) * (int64_t)num_sms() * q.tok;
   if (rows > 16 * T) rows = 16 * T;
   if (rows < T) rows = T;
   return (size_t)((q.order_words + q.copy_words + q.part_words + rows * R) * 4);
