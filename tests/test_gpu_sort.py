@@ -57,6 +57,18 @@ def test_sort(T, k, E, dtype):
         assert np.array_equal(got.cpu().numpy(), want)
 
 
+def test_sort_more_routes_of_an_expert_than_16_bits_count():
+    T = 9_000_001
+    ids = torch.zeros((T, 1), dtype=torch.int32, device="cuda")
+    ids[5::1000] = 1
+    off, rr, ro = sort_routes(ids, 2)
+    order = torch.sort(ids[:, 0], stable=True).indices.int()
+    n = int((ids == 0).sum())
+    assert off.tolist() == [0, n, T]
+    assert torch.equal(ro, order)
+    assert torch.equal(rr[:, 0][order.long()], torch.arange(T, dtype=torch.int32, device="cuda"))
+
+
 def test_sort_ids_out_of_range():
     ids = np.array([[0, 9], [3, -5], [2 ** 31 - 1, 1]])
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
