@@ -9,15 +9,20 @@
 
 namespace moe {
 
-// Rows of 16-byte packs that fit shared memory twice: everything from one
+// Rows of 16-byte packs, at most 1024, that fit shared memory twice: everything from one
 // reading.  A block takes every gridDim.x-th row, the next one's tensors on their
-// way to shared memory; the row's three sums cost one barrier, then the packs
-// (kept in registers, or with two a thread read again) give the gradients.  The [K] tensors lie there
-// in fp32, offset added, a pack's first four values in one plane and the rest in the
-// next, so that neighbouring threads read neighbouring 16 bytes.  Each thread keeps the column sums of its packs in
-// registers over all rows of the block.
+// way to shared memory (a third stage changes nothing: 103 us either way at 4099 x 4096,
+// forward and gradient); the row's three sums cost one barrier, then the packs
+// (kept in registers, or with two a thread read again) give the gradients.  The [K]
+// tensors lie there in fp32, offset added, a pack's first four values in one plane and
+// the rest in the next, so that neighbouring threads read neighbouring 16 bytes.  Each
+// thread keeps the column sums of its packs in registers over all rows of the block.
+//
+// Issue slots and the barrier bound it, at 16 warps an SM (the column sums leave room for
+// no more): 4099 x 4096 with a full gate 66 us (268 MB, 4.1 TB/s), 8192 x 7168 with a
+// token gate 165 us (705 MB, 4.3 TB/s).
 template <typename T, int NV, int GATE>  // GATE: channel, full, or none for the others
-__global__ void __launch_bounds__(512) block_norm_backward_kernel(NormParams p, int stages) {
+__global__ void __launch_bounds__(512) block_norm_backward_kernel(NormParams p) {
   constexpr int VEC = 16 / sizeof(T), H = VEC / 2;
   constexpr bool channel = GATE == MOE_GATE_CHANNEL, full = GATE == MOE_GATE_FULL;
   using P = Pack<T, VEC>;
@@ -31,7 +36,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(NormParams p, 
   const int at_z = packs, at_dx = at_z + (has_z ? packs : 0), at_dy = at_dx + (has_dx ? packs : 0);
   const int at_g = at_dy + (has_dy ? packs : 0), stage_packs = at_g + (full ? packs : 0);
   P* stage0 = reinterpret_cast<P*>(smem);
-  float2* s_post = reinterpret_cast<float2*>(smem + (size_t)stages * stage_packs * 16);
+  float2* s_post = reinterpret_cast<float2*>(smem + (size_t)2 * stage_packs * 16);
   float2* s_pre = s_post + (post ? p.K / 2 : 0);
   float2* s_gate = s_pre + (pre ? p.K / 2 : 0);
   pdl_wait();
@@ -56,10 +61,8 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(NormParams p, 
       }
     }
   };
-  for (int s = 0; s < stages - 1; ++s) {
-    fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
-    copies_commit();
-  }
+  fetch(blockIdx.x, 0);
+  copies_commit();
 #pragma unroll
   for (int i = 0; i < NV; ++i) {  // each thread its own packs
     const int c = tid + i * threads;
@@ -106,21 +109,16 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(NormParams p, 
   };
   Scalars ahead = scalars(blockIdx.x);
   const float inv_k = 1.0f / (float)p.K;
-  int it = 0, slot = 0, fill = stages - 1;
+  int it = 0;
   for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, it ^= 1) {
-    fetch(t + (int64_t)(stages - 1) * gridDim.x, fill);
+    fetch(t + gridDim.x, it ^ 1);
     copies_commit();
-    if (++fill == stages) fill = 0;
     const float rx = ahead.rx, branch = ahead.branch;
     const float2 rz2 = both(ahead.rz), rx2 = both(rx), branch2 = both(branch);
     const float rz = ahead.rz;
     ahead = scalars(t + gridDim.x);
-    if (stages == 3)
-      copies_wait<2>();
-    else
-      copies_wait<1>();
-    const P* st = stage0 + slot * stage_packs;
-    if (++slot == stages) slot = 0;
+    copies_wait<1>();
+    const P* st = stage0 + it * stage_packs;
 
     // Of a pack: zh, the gate times wp (gw), a = gate n, xh, dy and e.
     auto columns = [&](int c, float2 (&zh)[H], float2 (&gw)[H], float2 (&a)[H], float2 (&xh)[H],
@@ -322,8 +320,10 @@ __device__ __forceinline__ void back_columns(const NormParams& p, int64_t t, int
   }
 }
 
-// Any other rows, in two launches.  The first: the row's sums.  row_sums[t] = (mean(u xh), sum a e,
-// sum a xh, 0) with a = g n over channel or full gates.
+// Any other rows, in two launches that each read everything (2048 x 7168 fp32: 126 us of
+// gradient, where one reading would need twice the shared memory that there is).  The
+// first: the row's sums.  row_sums[t] = (mean(u xh), sum a e, sum a xh, 0) with a = g n
+// over channel or full gates.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) block_norm_sums_kernel(NormParams p) {
   __shared__ float part[3][32];
@@ -467,20 +467,15 @@ static bool launch_gated(NormParams& p, int threads, cudaStream_t s, moe_status_
                      (GATE == MOE_GATE_FULL);
   const int kept = (p.post_w != nullptr) + (p.pre_w != nullptr) + (GATE == MOE_GATE_CHANNEL);
   const size_t row = (size_t)arrays * p.K * sizeof(T), weights = (size_t)kept * p.K * 4;
-  // three stages where that costs no resident block, else two
-  int stages = 2;
-  if (2 * row + weights > kMaxBlockSmem) return false;
-  int64_t blocks = resident_with<kernel>(threads, 2 * row + weights);
-  if (3 * row + weights <= kMaxBlockSmem &&
-      resident_with<kernel>(threads, 3 * row + weights) == blocks)
-    stages = 3;
+  const size_t smem = 2 * row + weights;
+  if (smem > kMaxBlockSmem) return false;
+  int64_t blocks = resident_with<kernel>(threads, smem);
   if (blocks == 0) return false;
   blocks *= num_sms();
   if (blocks > kMaxRowBlocks) blocks = kMaxRowBlocks;
   if (blocks > p.T) blocks = p.T;
   p.row_blocks = (int)blocks;
-  *st = launched(launch_pdl(kernel, dim3((unsigned)blocks), dim3(threads),
-                            stages * row + weights, s, p, stages),
+  *st = launched(launch_pdl(kernel, dim3((unsigned)blocks), dim3(threads), smem, s, p),
                  "block norm gradient");
   return true;
 }
@@ -597,6 +592,8 @@ moe_status_t moe_block_norm_backward(const moe_block_norm_backward_args_t* a, vo
         moe_status_t r = MOE_OK;
         const int threads = (int)((packs + 31) / 32 * 32);
         const int half = (threads / 2 + 31) / 32 * 32;
+        // one pack a thread kept to the end: 4099 x 4096 with a channel gate 92 us with the
+        // forward, two a thread read again 101
         if (packs <= 512 && launch_backward<E, 1>(p, threads, s, &r)) return r;
         if (packs > 512 && packs <= 1024 && launch_backward<E, 2>(p, half, s, &r)) return r;
       }

@@ -1,10 +1,11 @@
 // A projection shared by all tokens plus each token's own low-rank adapter:
 //   out = x W^T + s_a (x A_a^T) B_a^T.
 //
-// lora_shrink_kernel gives h = x A_a^T as fp32 sums per share of K.  It reads A
-// and the rows of x, a few flops a byte, so it runs on mma.sync tiles fed by
-// cp.async; blocks take (64 or 128 tokens, share of K, share of the adapters among
-// them).
+// The shrink gives h = x A_a^T as fp32 sums per share of K.  It reads A and the rows of
+// x, a few flops a byte; blocks take (64 or 128 tokens, share of K, share of the adapters
+// among them) and copy only the rows of an adapter's own tokens, so the copies are
+// cp.async.  Up to 128 tokens (lora_shrink_kernel) on mma.sync, above
+// (lora_shrink_long_kernel) on tcgen05.
 //
 // The projection is on tcgen05, features by tokens: the accumulator's rows are
 // features (the MMA's A operand is a weight tile) and its columns tokens, so that
@@ -32,6 +33,11 @@
 //
 // The projection's launch starts while the shrink still runs and waits for it only
 // where h is read.
+//
+// Measured, 7168 -> 4096 bf16: one token of rank 16 14.2 us (59 MB, 4.2 TB/s); 512 tokens,
+// 16 adapters of rank 64, 56 us; 8192 tokens in order 313 us (1.58 PFLOP/s, the pairs alone
+// 1.8), without adapters 250 us (1.92 PFLOP/s).  2048 -> 7168 fp16, 64 tokens that name 36
+// adapters of rank 32: 20.3 us (59 MB).
 #include <mutex>
 
 #include "block_common.cuh"
@@ -101,10 +107,12 @@ __device__ __forceinline__ int distinct_adapters(const int16_t* id, int16_t* lis
 // ------------------------------------------------------------------ shrink
 constexpr int SH_THREADS = 256;
 constexpr int SH_STAGES = 4;
-constexpr int SH_MAX_TOK = 128;
+constexpr int SH_TOK = 64, SH_LONG = 128;  // tokens of a block
 
 // Shared memory of a block of `tok` tokens.
-__host__ __device__ constexpr int sh_smem(int tok, int r16) { return SH_STAGES * (tok + r16) * 128; }
+__host__ __device__ constexpr int sh_smem(int tok, int r16) {
+  return SH_STAGES * (tok + r16) * 128 + (tok == SH_LONG ? 1024 : 0);  // 1024: alignment
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -146,78 +154,35 @@ __device__ __forceinline__ bool group_together(int tok) {
   return __all_sync(0xFFFFFFFFu, tok < 0 || tok == first + (int)(threadIdx.x & 31));
 }
 
-// TOK tokens a block: eight warps as TOK / 16 rows of 16 tokens by 128 / TOK
-// shares of the ranks, each warp up to NT16 times 16 of them.
-template <typename T, int TOK, int NT16>
+// Up to 128 tokens in all, SH_TOK a block as they come, on mma.sync: eight warps as
+// four rows of 16 tokens by two shares of the ranks, each warp up to NT16 times 16 of
+// them.  Block z has the adapters z, z + gridDim.z, ... of its tokens.
+template <typename T, int NT16>
 __global__ void __launch_bounds__(SH_THREADS, 2) lora_shrink_kernel(LoraParams p) {
-  constexpr int XP = TOK / 32;                           // a thread's pieces of x
-  constexpr int NSPLIT = 128 / TOK;                      // shares of the ranks
+  constexpr int XP = SH_TOK / 32;                        // a thread's pieces of x
+  constexpr int NSPLIT = 2;                              // shares of the ranks
   constexpr int AP = (NT16 * NSPLIT * 16 + 31) / 32;     // a thread's pieces of A
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int16_t s_id[TOK], s_list[TOK];
-  __shared__ int32_t s_tok[TOK];
+  __shared__ int16_t s_id[SH_TOK], s_list[SH_TOK];
   __shared__ uint32_t s_bits[32];
   __shared__ int s_n;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t t0 = (int64_t)blockIdx.x * TOK;
-  if (p.order != nullptr && t0 >= *p.places) return;
+  const int64_t t0 = (int64_t)blockIdx.x * SH_TOK;
   bool bad = false;
-  if (tid < TOK) {
-    int64_t t = t0 + tid;
-    if (p.order != nullptr) t = t < *p.places ? p.order[t] : -1;
-    s_tok[tid] = (int32_t)t;
-    s_id[tid] = (int16_t)adapter_of(p, t, &bad);
-  }
+  if (tid < SH_TOK) s_id[tid] = (int16_t)adapter_of(p, t0 + tid, &bad);
   if (bad) set_status(p.status, MOE_DEV_BAD_ADAPTER);
   __syncthreads();
-  // Block z has the adapters z, z + gridDim.z, ... of these tokens; in the tokens'
-  // order that of group z, unless an earlier group has it.
-  int n_list;
-  if (p.order == nullptr) {
-    n_list = distinct_adapters(s_id, s_list, s_bits, &s_n, TOK);
-  } else {
-    const int z = blockIdx.z;
-    bool mine = s_id[z * RUN] >= 0;
-    for (int g = 0; g < z; ++g) mine = mine && s_id[g * RUN] != s_id[z * RUN];
-    if (tid == 0) s_list[z] = s_id[z * RUN];
-    n_list = mine ? z + 1 : 0;
-    __syncthreads();
-  }
+  const int n_list = distinct_adapters(s_id, s_list, s_bits, &s_n, SH_TOK);
   const int64_t k0 = (int64_t)blockIdx.y * p.share_k;
   const int64_t k1 = min(p.K, k0 + p.share_k);
   const int slabs = k1 > k0 ? (int)((k1 - k0 + 63) / 64) : 0;
   const int R = (int)p.R, r16 = (R + 15) & ~15;
   const uint32_t base = smem_u32(smem);
-  const uint32_t stage_bytes = (TOK + r16) * 128;
+  const uint32_t stage_bytes = (SH_TOK + r16) * 128;
   const T* x = static_cast<const T*>(p.x);
-  const int m0 = (warp % (TOK / 16)) * 16, nh = warp / (TOK / 16);
-
-  if (p.order != nullptr) {
-    // of group z's rows, where the projection cannot fetch them as they lie in x,
-    // this share of K: 16-byte pieces, four in flight a thread
-    const int g0 = blockIdx.z * RUN;
-    if (!group_together(s_tok[g0 + lane])) {
-      T* xs = static_cast<T*>(p.xs);
-      const int pieces = (int)((k1 - k0) / 8);
-      for (int i0 = tid; i0 < RUN * pieces; i0 += 4 * SH_THREADS) {
-        Pack<T, 8> v[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int i = i0 + u * SH_THREADS, r = i / pieces;
-          if (i < RUN * pieces && s_tok[g0 + r] >= 0)
-            v[u] = load_pack<T, 8>(x + s_tok[g0 + r] * p.x_stride + k0 + (i - r * pieces) * 8);
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int i = i0 + u * SH_THREADS, r = i / pieces;
-          if (i < RUN * pieces && s_tok[g0 + r] >= 0)
-            store_pack<T, 8>(xs + (t0 + g0 + r) * p.K + k0 + (i - r * pieces) * 8, v[u]);
-        }
-      }
-    }
-  }
+  const int m0 = (warp % 4) * 16, nh = warp / 4;
 
   // a thread's pieces: 16-byte piece c of rows row, row + 32, ...
   const int row = tid >> 3, c = tid & 7;
@@ -225,7 +190,7 @@ __global__ void __launch_bounds__(SH_THREADS, 2) lora_shrink_kernel(LoraParams p
   // a lane's addresses for ldmatrix: row of the tile, and the permuted piece of
   // each 16-wide K step (rows eight apart have the same permutation)
   const uint32_t xrow = (uint32_t)(m0 + (lane & 15)) * 128;
-  const uint32_t arow = (uint32_t)(TOK + nh * 16 + (lane & 7) + ((lane >> 4) << 3)) * 128;
+  const uint32_t arow = (uint32_t)(SH_TOK + nh * 16 + (lane & 7) + ((lane >> 4) << 3)) * 128;
   uint32_t xk[4], ak[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -240,7 +205,7 @@ __global__ void __launch_bounds__(SH_THREADS, 2) lora_shrink_kernel(LoraParams p
 #pragma unroll
     for (int j = 0; j < XP; ++j) {
       const bool t = s_id[row + 32 * j] == a;
-      xp[j] = t ? x + s_tok[row + 32 * j] * p.x_stride + k0 + c * 8 : x;
+      xp[j] = t ? x + (t0 + row + 32 * j) * p.x_stride + k0 + c * 8 : x;
       take |= (uint32_t)t << j;
     }
 #pragma unroll
@@ -262,7 +227,7 @@ __global__ void __launch_bounds__(SH_THREADS, 2) lora_shrink_kernel(LoraParams p
 #pragma unroll
       for (int j = 0; j < AP; ++j)
         if (row + 32 * j < r16) {
-          cp_async16(s + TOK * 128 + j * 4096, ap[j], (t >> (XP + j)) & 1u);
+          cp_async16(s + SH_TOK * 128 + j * 4096, ap[j], (t >> (XP + j)) & 1u);
           ap[j] += (t >> (XP + j)) & 1u ? 64 : 0;
         }
       left -= 64;
@@ -314,14 +279,218 @@ __global__ void __launch_bounds__(SH_THREADS, 2) lora_shrink_kernel(LoraParams p
         for (int j = 0; j < 2; ++j) {
           const int n = (i * NSPLIT + nh) * 16 + j * 8 + (lane & 3) * 2;
           if (n < R)
-            *reinterpret_cast<float2*>(h + (int64_t)s_tok[r] * R + n) =
+            *reinterpret_cast<float2*>(h + (t0 + r) * R + n) =
                 make_float2(acc[i][j][half * 2], acc[i][j][half * 2 + 1]);
         }
     }
   }
 }
 
+// More tokens, SH_LONG a block as they come or in their order, on tcgen05: a tile of the
+// accumulator has a token a lane and a rank a column, and the cp.async stages have the
+// 128-byte swizzle that the MMA reads.  In the tokens' order block z has the adapter of
+// group z, unless an earlier group has it, and copies the rows of that group that do
+// not lie together.
+template <typename T>
+__global__ void __launch_bounds__(SH_THREADS, 2) lora_shrink_long_kernel(LoraParams p) {
+  constexpr int XP = SH_LONG / 32, AP = LORA_MAX_RANK / 32;  // a thread's pieces of x and A
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int16_t s_id[SH_LONG], s_list[SH_LONG];
+  __shared__ int32_t s_tok[SH_LONG];
+  __shared__ uint32_t s_bits[32];
+  __shared__ int s_n, s_abort;
+  __shared__ uint32_t s_tmem;
+  __shared__ __align__(8) uint64_t s_bars[SH_STAGES];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t t0 = (int64_t)blockIdx.x * SH_LONG;
+  if (p.order != nullptr && t0 >= *p.places) return;
+  bool bad = false;
+  if (tid < SH_LONG) {
+    int64_t t = t0 + tid;
+    if (p.order != nullptr) t = t < *p.places ? p.order[t] : -1;
+    s_tok[tid] = (int32_t)t;
+    s_id[tid] = (int16_t)adapter_of(p, t, &bad);
+  }
+  if (bad) set_status(p.status, MOE_DEV_BAD_ADAPTER);
+  __syncthreads();
+  int n_list;
+  if (p.order == nullptr) {
+    n_list = distinct_adapters(s_id, s_list, s_bits, &s_n, SH_LONG);
+  } else {
+    const int z = blockIdx.z;
+    bool mine = s_id[z * RUN] >= 0;
+    for (int g = 0; g < z; ++g) mine = mine && s_id[g * RUN] != s_id[z * RUN];
+    if (tid == 0) s_list[z] = s_id[z * RUN];
+    n_list = mine ? z + 1 : 0;
+    __syncthreads();
+  }
+  const int64_t k0 = (int64_t)blockIdx.y * p.share_k;
+  const int64_t k1 = min(p.K, k0 + p.share_k);
+  const int slabs = (int)((k1 - k0 + 63) / 64);  // every share has some
+  const int R = (int)p.R, r16 = (R + 15) & ~15;
+  const T* x = static_cast<const T*>(p.x);
+
+  if (p.order != nullptr) {
+    // of group z's rows, where the projection cannot fetch them as they lie in x,
+    // this share of K: 16-byte pieces, four in flight a thread
+    const int g0 = blockIdx.z * RUN;
+    if (!group_together(s_tok[g0 + lane])) {
+      T* xs = static_cast<T*>(p.xs);
+      const int pieces = (int)((k1 - k0) / 8);
+      for (int i0 = tid; i0 < RUN * pieces; i0 += 4 * SH_THREADS) {
+        Pack<T, 8> v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = i0 + u * SH_THREADS, r = i / pieces;
+          if (i < RUN * pieces && s_tok[g0 + r] >= 0)
+            v[u] = load_pack<T, 8>(x + s_tok[g0 + r] * p.x_stride + k0 + (i - r * pieces) * 8);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = i0 + u * SH_THREADS, r = i / pieces;
+          if (i < RUN * pieces && s_tok[g0 + r] >= 0)
+            store_pack<T, 8>(xs + (t0 + g0 + r) * p.K + k0 + (i - r * pieces) * 8, v[u]);
+        }
+      }
+    }
+  }
+
+  if ((int)blockIdx.z >= n_list) return;
+  const uint32_t cols = r16 <= 32 ? 32 : (r16 <= 64 ? 64 : 128);
+  const uint32_t bars = smem_u32(s_bars);
+  volatile int* abort_flag = &s_abort;
+  if (tid == 0) {
+    for (int s = 0; s < SH_STAGES; ++s) mbar_init(bars + 8 * s, 1);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_async_smem();
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&s_tmem)),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = s_tmem;
+  const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
+  const uint32_t stage_bytes = (SH_LONG + r16) * 128;
+  const uint32_t idesc = f16_idesc(std::is_same<T, __nv_bfloat16>::value, SH_LONG, r16);
+  // a thread's pieces: 16-byte piece c of rows row, row + 32, ...
+  const int row = tid >> 3, c = tid & 7;
+  const uint32_t at = base + tile_at(row, c);
+  uint32_t seq = 0;  // slabs of all adapters so far; slab i has stage i % SH_STAGES
+  bool ok = true;
+  for (int d = blockIdx.z; d < n_list; d += gridDim.z) {
+    const int a = s_list[d];
+    const T* A = static_cast<const T*>(p.a) + (int64_t)a * R * p.K;
+    const T *xp[XP], *ap[AP];
+    uint32_t take = 0;
+#pragma unroll
+    for (int j = 0; j < XP; ++j) {
+      const bool t = s_id[row + 32 * j] == a;
+      xp[j] = t ? x + s_tok[row + 32 * j] * p.x_stride + k0 + c * 8 : x;
+      take |= (uint32_t)t << j;
+    }
+#pragma unroll
+    for (int j = 0; j < AP; ++j) {
+      const bool t = row + 32 * j < R;
+      ap[j] = t ? A + (int64_t)(row + 32 * j) * p.K + k0 + c * 8 : A;
+      take |= (uint32_t)t << (XP + j);
+    }
+    uint32_t fill = seq % SH_STAGES;  // stage of the next load
+    int64_t left = k1 - k0 - c * 8;   // this thread's columns from the next load on
+    auto load = [&] {
+      const uint32_t s = at + fill * stage_bytes;
+      const uint32_t t = left > 0 ? take : 0u;
+#pragma unroll
+      for (int j = 0; j < XP; ++j) {
+        cp_async16(s + j * 4096, xp[j], (t >> j) & 1u);
+        xp[j] += (t >> j) & 1u ? 64 : 0;
+      }
+#pragma unroll
+      for (int j = 0; j < AP; ++j)
+        if (row + 32 * j < r16) {
+          cp_async16(s + SH_LONG * 128 + j * 4096, ap[j], (t >> (XP + j)) & 1u);
+          ap[j] += (t >> (XP + j)) & 1u ? 64 : 0;
+        }
+      left -= 64;
+      if (++fill == SH_STAGES) fill = 0;
+    };
+    for (int s = 0; s < SH_STAGES - 1; ++s) {
+      if (s < slabs) load();
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    bool failed = false;
+    for (int s = 0; s < slabs; ++s, ++seq) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(SH_STAGES - 2) : "memory");
+      fence_async_smem();  // each thread's own copies, before the MMA reads them
+      failed = __syncthreads_or(!ok);
+      if (failed) break;
+      const uint32_t stage = seq % SH_STAGES;
+      if (warp == 0) {
+        const uint32_t st = base + stage * stage_bytes;
+        const uint64_t ad = sw128_desc(st), bd = sw128_desc(st + SH_LONG * 128);
+        if (elect_one()) {
+          fence_after();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f16(tmem, ad + 2 * k, bd + 2 * k, idesc, (s > 0 || k > 0) ? 1u : 0u);
+          mma_commit(bars + 8 * stage);
+        }
+        __syncwarp();
+      }
+      if (s + SH_STAGES - 1 < slabs) {  // over the stage of the slab before
+        if (s > 0) ok = mbar_wait(bars + 8 * ((seq - 1) % SH_STAGES),
+                                  ((seq - 1) / SH_STAGES) & 1u, abort_flag, p.status);
+        if (ok) load();
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (seq > 0) {  // the last MMAs issued; those before them are done too
+      volatile int never = 0;
+      ok = mbar_wait(bars + 8 * ((seq - 1) % SH_STAGES), ((seq - 1) / SH_STAGES) & 1u, &never,
+                     p.status) && ok;
+    }
+    if (__syncthreads_or(!ok || failed)) break;
+    fence_after();
+    const int r = (warp & 3) * 32 + lane;  // lane of the sums, its token
+    const bool mine = s_id[r] == a;
+    float* h = p.h + ((int64_t)blockIdx.y * p.T + (mine ? s_tok[r] : 0)) * R;
+    for (int n = (warp >> 2) * 16; n < r16; n += 32) {
+      uint32_t v[16];
+      tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + n, v);
+      tmem_wait16(v);
+#pragma unroll
+      for (int q = 0; q < 16; q += 4)
+        if (mine && n + q < R)
+          *reinterpret_cast<float4*>(h + n + q) =
+              make_float4(__uint_as_float(v[q]), __uint_as_float(v[q + 1]),
+                          __uint_as_float(v[q + 2]), __uint_as_float(v[q + 3]));
+      __syncwarp();
+    }
+    fence_before();
+    __syncthreads();  // stages and sums are free for the next adapter
+    fence_after();
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols)
+                 : "memory");
+  }
+}
+
 // ------------------------------------------------- projection, few tokens
+// At 512 tokens this path takes 56 us and the pairs 81 (two more launches for the order);
+// at 1024 the pairs take 113 us, and W would pass eight times here.
 constexpr int SPLIT_TOKENS = 512;
 constexpr int LG_M = 128;  // features of a tile
 constexpr int LG_A_BYTES = LG_M * 128;
@@ -718,7 +887,8 @@ __device__ __forceinline__ Runs tile_runs(const LoraParams& p, int64_t pos0, int
 __device__ __forceinline__ int run_end(const Runs& r, int g) { return __ffs(r.ends >> g) - 1 + g; }
 
 // The work of the pairs: whole tiles dealt out in rounds, and the tiles of a last
-// round that would leave pairs idle cut along K, so that each pair has a piece.
+// round that would leave pairs idle cut along K, so that each pair has a piece (1024
+// tokens 113 us, uncut 132; 8192 324 against 328).
 constexpr int LP_MIN_SLABS = 8;  // of a piece
 constexpr int64_t LP_PIECE = 2 * LP_TILE * LP_HALF;  // its sums
 struct Work {
@@ -1212,7 +1382,7 @@ struct LoraPlan {
 
 // Blocks of the shrink that an SM is given: four of 64 tokens by 32 ranks (62
 // registers a thread; 64 tokens of 36 adapters: 20.3 us against 22.5 with two), else two.
-static int shrink_fill(int tok, int64_t R) { return tok == 64 && R <= 32 ? 4 : 2; }
+static int shrink_fill(int tok, int64_t R) { return tok == moe::SH_TOK && R <= 32 ? 4 : 2; }
 
 static LoraPlan lora_plan(int64_t T, int64_t K, int64_t N, int64_t S, int64_t R) {
   LoraPlan q{};
@@ -1225,12 +1395,12 @@ static LoraPlan lora_plan(int64_t T, int64_t K, int64_t N, int64_t S, int64_t R)
     q.copy_words = (q.places * K / 2 + 3) / 4 * 4;
     q.part_words = sms / 2 * moe::LP_PIECE;
   }
-  // Shrink: 64 tokens, from 129 on 128 (they read A_a once for twice the tokens: 512
-  // tokens 65 us against 72, 200 of rank 16 37 against 35), as they come or in their
-  // order, and a block for each adapter that these may have (in the order a group of
+  // Shrink: 64 tokens, from 129 on 128 (they read A_a once for twice the tokens, and
+  // fill the tcgen05 tile: 512 tokens 56 us against 72, 256 37 against 43), as they come
+  // or in their order, and a block for each adapter that these may have (in the order a group of
   // RUN has one).  A block whose tokens have fewer ends at once, so K is dealt out, in
   // shares at least 128 wide, by the number of adapters that they have on average.
-  q.tok = T > 128 ? 128 : 64;
+  q.tok = T > 128 ? moe::SH_LONG : moe::SH_TOK;
   q.tiles = (int)((q.places + q.tok - 1) / q.tok);
   const int64_t groups = q.pair ? q.tok / moe::RUN : (T < q.tok ? T : q.tok);
   q.zs = (int)(S < groups ? (S < 1 ? 1 : S) : groups);
@@ -1311,14 +1481,13 @@ static cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, int threa
 
 constexpr int kMaxSmem = 232448;
 
-template <typename T, int TOK, int NT16>
+template <auto Kernel>
 static moe_status_t launch_shrink(const LoraPlan& q, const LoraParams& p, cudaStream_t s) {
-  constexpr auto kernel = moe::lora_shrink_kernel<T, TOK, NT16>;
-  moe_status_t st = allow_smem<kernel>(moe::sh_smem(TOK, moe::LORA_MAX_RANK));
+  moe_status_t st = allow_smem<Kernel>(moe::sh_smem(q.tok, moe::LORA_MAX_RANK));
   if (st != MOE_OK) return st;
   const int r16 = (int)((p.R + 15) & ~15);
-  return launched(launch_pdl(kernel, dim3((unsigned)q.tiles, (unsigned)q.shares, (unsigned)q.zs),
-                             dim3(moe::SH_THREADS), (size_t)moe::sh_smem(TOK, r16), s, p),
+  return launched(launch_pdl(Kernel, dim3((unsigned)q.tiles, (unsigned)q.shares, (unsigned)q.zs),
+                             dim3(moe::SH_THREADS), (size_t)moe::sh_smem(q.tok, r16), s, p),
                   "adapter");
 }
 
@@ -1381,15 +1550,15 @@ static moe_status_t launch_lora(const moe_lora_args_t* a, const LoraPlan& q, Lor
       p.order = order;
       p.places = scratch + p.S + 1;
     }
-    const int t16 = (int)((p.R + 15) / 16);
     moe_status_t st;
-    if (q.tok == 64)
-      st = t16 <= 2 ? launch_shrink<T, 64, 1>(q, p, s)
-                    : (t16 <= 4 ? launch_shrink<T, 64, 2>(q, p, s) : launch_shrink<T, 64, 4>(q, p, s));
+    if (q.tok == moe::SH_LONG)
+      st = launch_shrink<moe::lora_shrink_long_kernel<T>>(q, p, s);
+    else if (p.R <= 32)
+      st = launch_shrink<moe::lora_shrink_kernel<T, 1>>(q, p, s);
+    else if (p.R <= 64)
+      st = launch_shrink<moe::lora_shrink_kernel<T, 2>>(q, p, s);
     else
-      st = t16 <= 2 ? launch_shrink<T, 128, 2>(q, p, s)
-                    : (t16 <= 4 ? launch_shrink<T, 128, 4>(q, p, s)
-                                : launch_shrink<T, 128, 8>(q, p, s));
+      st = launch_shrink<moe::lora_shrink_kernel<T, 4>>(q, p, s);
     if (st != MOE_OK) return st;
   }
   if (q.pair) return launch_pair<T>(p, q.places, w, x, xs, b, s);
