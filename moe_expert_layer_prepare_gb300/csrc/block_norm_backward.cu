@@ -320,9 +320,9 @@ __device__ __forceinline__ void back_columns(const NormParams& p, int64_t t, int
   }
 }
 
-// Any other rows, in two launches that each read everything (2048 x 7168 fp32: 126 us of
-// gradient, where one reading would need twice the shared memory that there is).  The
-// first: the row's sums.  row_sums[t] = (mean(u xh), sum a e, sum a xh, 0) with a = g n
+// Any other rows, in two launches that each read everything (2048 x 7168 fp32: 112 us,
+// where one reading would need twice the shared memory that there is; 4099 x 4095 bf16,
+// element by element: 200 us).  The first: the row's sums.  row_sums[t] = (mean(u xh), sum a e, sum a xh, 0) with a = g n
 // over channel or full gates.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) block_norm_sums_kernel(NormParams p) {
@@ -564,9 +564,6 @@ moe_status_t moe_block_norm_backward(const moe_block_norm_backward_args_t* a, vo
   p.d_pre_w = a->d_pre_weight;
   p.row_sums = static_cast<float4*>(a->workspace);
   p.partials = reinterpret_cast<float*>(p.row_sums + T);
-  const int64_t blocks = norm_row_blocks(T);
-  p.rows_per_block = (int)((T + blocks - 1) / blocks);
-  p.row_blocks = p.rows_per_block > 0 ? (int)((T + p.rows_per_block - 1) / p.rows_per_block) : 0;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (T > 0) {
     st = with_dtype(a->dtype, [&](auto v) {
@@ -604,9 +601,17 @@ moe_status_t moe_block_norm_backward(const moe_block_norm_backward_args_t* a, vo
             launch_pdl(sums, dim3((unsigned)(T < cap ? T : cap)), dim3(256), 0, s, p),
             "block norm sums");
         if (r != MOE_OK) return r;
-        const int64_t cols = (K + vec - 1) / vec;
-        return launched(launch_pdl(apply, dim3((unsigned)((cols + 255) / 256), (unsigned)p.row_blocks),
-                                   dim3(256), 0, s, p), "block norm gradient");
+        // blocks of rows for one full round of the SMs, as each writes column sums (2048 x
+        // 7168 fp32: 112 us of gradient, with 512 blocks of rows 126)
+        const int64_t across = (K + 256 * vec - 1) / (256 * vec);
+        int64_t blocks = (int64_t)num_sms() *
+                         resident_blocks(reinterpret_cast<const void*>(apply), 256) / across;
+        if (blocks < 1) blocks = 1;
+        if (blocks > norm_row_blocks(T)) blocks = norm_row_blocks(T);
+        p.rows_per_block = (int)((T + blocks - 1) / blocks);
+        p.row_blocks = (int)((T + p.rows_per_block - 1) / p.rows_per_block);
+        return launched(launch_pdl(apply, dim3((unsigned)across, (unsigned)p.row_blocks), dim3(256),
+                                   0, s, p), "block norm gradient");
       };
       return w.ok ? go(moe::block_norm_sums_kernel<E, V>, moe::block_norm_apply_kernel<E, V>, V)
                   : go(moe::block_norm_sums_kernel<E, 1>, moe::block_norm_apply_kernel<E, 1>, 1);
