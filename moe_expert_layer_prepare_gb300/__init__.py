@@ -5,4 +5,4 @@ The compute path lives in the CUDA library ``libmoe_prep.so`` (built from
 package does not load the library; the first call through ``binding`` does, and
 raises if the library has not been built.
 """
-__all__ = ["binding", "synthetic"]
+__all__ = ["binding", "block", "synthetic"]

@@ -11,8 +11,8 @@ namespace moe {
 
 // Rows of 16-byte packs, at most 1024, that fit shared memory twice: everything from one
 // reading.  A block takes every gridDim.x-th row, the next one's tensors on their
-// way to shared memory (a third stage changes nothing: 103 us either way at 4099 x 4096,
-// forward and gradient); the row's three sums cost one barrier, then the packs
+// way to shared memory (a third stage changes little: 4099 x 4096 with a full gate 102
+// us with the forward, 103 with it); the row's three sums cost one barrier, then the packs
 // (kept in registers, or with two a thread read again) give the gradients.  The [K]
 // tensors lie there in fp32, offset added, a pack's first four values in one plane and
 // the rest in the next, so that neighbouring threads read neighbouring 16 bytes.  Each
@@ -322,8 +322,8 @@ __device__ __forceinline__ void back_columns(const NormParams& p, int64_t t, int
 
 // Any other rows, in two launches that each read everything (2048 x 7168 fp32: 112 us,
 // where one reading would need twice the shared memory that there is; 4099 x 4095 bf16,
-// element by element: 200 us).  The first: the row's sums.  row_sums[t] = (mean(u xh), sum a e, sum a xh, 0) with a = g n
-// over channel or full gates.
+// element by element: 196 us).  The first: the row's sums,
+// row_sums[t] = (mean(u xh), sum a e, sum a xh, 0) with a = g n over channel or full gates.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) block_norm_sums_kernel(NormParams p) {
   __shared__ float part[3][32];
@@ -589,8 +589,8 @@ moe_status_t moe_block_norm_backward(const moe_block_norm_backward_args_t* a, vo
         moe_status_t r = MOE_OK;
         const int threads = (int)((packs + 31) / 32 * 32);
         const int half = (threads / 2 + 31) / 32 * 32;
-        // one pack a thread kept to the end: 4099 x 4096 with a channel gate 92 us with the
-        // forward, two a thread read again 101
+        // one pack a thread kept to the end: 4099 x 4096 with a full gate 102 us with the
+        // forward, two a thread read again 107
         if (packs <= 512 && launch_backward<E, 1>(p, threads, s, &r)) return r;
         if (packs > 512 && packs <= 1024 && launch_backward<E, 2>(p, half, s, &r)) return r;
       }
