@@ -681,19 +681,33 @@ def moe_unpermute_backward(d_out, rows, route_row, topk_weights, expert_offsets,
         _rows("d_rows", d_rows, shape, dt), _flat("d_weights", d_weights, tk, _FP32)), stream)
 
 
-def _gate(gate, name, shape, dtype, wdtype):
-    """(kind, stride) of a gate, or of its gradient, by its shape: [K], [T] or [T, K] ([T, 1] is
-    [T]; a [K] gate with T == K is taken per channel)."""
+def _gate(gate, name, shape, dtype, wdtype, kind=None):
+    """(kind, stride) of a gate, or of its gradient: the given kind, else by its shape and type,
+    [K] of wdtype, [T] or [T, 1] of dtype, or [T, K] of dtype.  A 1-D gate that T == K lets be
+    either of two kinds is refused without one (T == K == 1: both are the same)."""
     if gate is None:
+        if kind not in (None, MOE_GATE_NONE):
+            raise ValueError(f"{name}: gate_kind {kind} without a gate")
         return MOE_GATE_NONE, 0
     T, K = shape
     gs = gate.shape
-    if gs == (K,) and gate.dtype is wdtype:
+    if kind is None:
+        channel = gs == (K,) and gate.dtype is wdtype
+        token = gate.dtype is dtype and (gs == (T,) or (gs == (T, 1) and K != 1))
+        if channel and token and K != 1:
+            raise ValueError(f"{name}: {list(gs)} with {T} tokens of {K} values is a channel gate "
+                             "or a token gate: give gate_kind (or a token gate as [T, 1])")
+        kind = MOE_GATE_CHANNEL if channel else MOE_GATE_TOKEN if token else MOE_GATE_FULL
+    if kind == MOE_GATE_CHANNEL:
         _flat(name, gate, (K,), wdtype)
-        return MOE_GATE_CHANNEL, 0
-    if gate.dtype is dtype and (gs == (T,) or (gs == (T, 1) and K != 1)):
-        return MOE_GATE_TOKEN, gate.stride(0)
-    return MOE_GATE_FULL, _rows(name, gate, shape, dtype)
+        return kind, 0
+    if kind == MOE_GATE_TOKEN:
+        if gate.dtype is not dtype or gs not in ((T,), (T, 1)):
+            raise ValueError(f"{name}: want {dtype} [{T}] or [{T}, 1], got {gate.dtype} {list(gs)}")
+        return kind, gate.stride(0)
+    if kind != MOE_GATE_FULL:
+        raise ValueError(f"{name}: gate_kind {kind} with a gate")
+    return kind, _rows(name, gate, shape, dtype)
 
 
 def _weight_type(x, pre_weight, post_weight, gate):
@@ -705,16 +719,18 @@ def _weight_type(x, pre_weight, post_weight, gate):
 
 def moe_block_norm(x, z=None, post_weight=None, gate=None, scale=1.0, pre_weight=None,
                    weight_offset=0.0, eps=1e-6, x_out=None, y=None, rstd_post=None, rstd_pre=None,
-                   stream=None):
+                   stream=None, gate_kind=None):
     """x_out = x + scale * gate * rmsnorm(z, post_weight) and y = rmsnorm(x_out, pre_weight).
 
     x, z, x_out, y: [T, K] of one type; post_weight, pre_weight and a channel gate: [K] of one
-    type (fp32, bf16 or fp16); a token gate: [T] of x's type; a full gate: [T, K].  Without z only
-    y = rmsnorm(x) is written, without pre_weight only x_out.  rstd_post, rstd_pre: fp32 [T], kept
-    for the gradient.  See include/moe_prep.h."""
+    type (fp32, bf16 or fp16); a token gate: [T] or [T, 1] of x's type; a full gate: [T, K].
+    gate_kind: MOE_GATE_CHANNEL, MOE_GATE_TOKEN or MOE_GATE_FULL; without it the gate's shape and
+    type tell, and a 1-D gate that could be a channel's or a token's, as T == K, raises ValueError.
+    Without z only y = rmsnorm(x) is written, without pre_weight only x_out.  rstd_post, rstd_pre:
+    fp32 [T], kept for the gradient.  See include/moe_prep.h."""
     T, K = shape = x.shape
     dt, wdt = x.dtype, _weight_type(x, pre_weight, post_weight, gate)
-    kind, gs = _gate(gate, "gate", shape, dt, wdt)
+    kind, gs = _gate(gate, "gate", shape, dt, wdt, gate_kind)
     _call("moe_block_norm", BlockNormArgs.pack(
         T, K, _code("x", dt), _code("weights", wdt), x.data_ptr(), _rows("x", x, shape, dt),
         _at(z), _rows("z", z, shape, dt), _flat("post_weight", post_weight, (K,), wdt), _at(gate),
@@ -731,16 +747,18 @@ def block_norm_workspace_size(num_tokens, hidden_size) -> int:
 def moe_block_norm_backward(x, z=None, post_weight=None, gate=None, scale=1.0, pre_weight=None,
                             weight_offset=0.0, rstd_post=None, rstd_pre=None, d_x_out=None,
                             d_y=None, d_x=None, d_z=None, d_gate=None, d_post_weight=None,
-                            d_pre_weight=None, workspace=None, stream=None):
+                            d_pre_weight=None, workspace=None, stream=None, gate_kind=None):
     """Gradients of ``moe_block_norm`` from d_x_out and d_y (either may be None) and the forward's
-    inputs, rstd_post and rstd_pre.  d_x is always written, the others where given.  workspace:
-    uint8, block_norm_workspace_size() bytes.  See include/moe_prep.h."""
+    inputs, rstd_post and rstd_pre; gate_kind as there.  d_x is always written, the others where
+    given.  workspace: uint8, block_norm_workspace_size() bytes.  See include/moe_prep.h."""
     T, K = shape = x.shape
     dt, wdt = x.dtype, _weight_type(x, pre_weight, post_weight, gate)
-    kind, gs = _gate(gate, "gate", shape, dt, wdt)
-    dkind, dgs = _gate(d_gate, "d_gate", shape, dt, wdt)
-    if d_gate is not None and (dkind != kind or d_gate.shape != gate.shape):
-        raise ValueError("d_gate must have the gate's shape and type")
+    kind, gs = _gate(gate, "gate", shape, dt, wdt, gate_kind)
+    dgs = 0
+    if d_gate is not None:
+        if gate is None or d_gate.shape != gate.shape:
+            raise ValueError("d_gate must have the gate's shape and type")
+        dgs = _gate(d_gate, "d_gate", shape, dt, wdt, kind)[1]
     _call("moe_block_norm_backward", BlockNormBackwardArgs.pack(
         T, K, _code("x", dt), _code("weights", wdt), x.data_ptr(), _rows("x", x, shape, dt),
         _at(z), _rows("z", z, shape, dt), _flat("post_weight", post_weight, (K,), wdt), _at(gate),

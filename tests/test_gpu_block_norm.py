@@ -263,3 +263,61 @@ def test_stream_same_bits_twice_and_refusals():
     with pytest.raises(B.MoeError) as e:
         B.moe_block_norm_backward(s["x"], rstd_post=rz, rstd_pre=rx, d_y=y, d_x=xo, **kw)
     assert e.value.status == 5  # no workspace
+
+
+@pytest.mark.parametrize("T", [2, 48, 520])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("kind", ["channel", "token"])
+def test_as_many_tokens_as_columns(T, dtype, kind):
+    # [T] and [K] are one shape: the caller says which
+    K, dt, token = T, DTYPES[dtype], kind == "token"
+    s = tensors(T, K, dtype, dtype, kind, "plain")
+    code = B.MOE_GATE_TOKEN if token else B.MOE_GATE_CHANNEL
+    kw = dict(z=s["z"], post_weight=s["post"], gate=s["gate"], scale=0.6, pre_weight=s["pre"])
+    xo, y, dxo, dy, dx, dz = (s["rnd"](T, K) for _ in range(6))
+    rz, rx = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    with pytest.raises(ValueError, match="gate_kind"):
+        B.moe_block_norm(s["x"], eps=EPS, x_out=xo, y=y, rstd_post=rz, rstd_pre=rx, **kw)
+    B.moe_block_norm(s["x"], eps=EPS, x_out=xo, y=y, rstd_post=rz, rstd_pre=rx, gate_kind=code, **kw)
+    dg, dp, dq = (torch.empty(K, dtype=dt, device="cuda") for _ in range(3))
+    ws = torch.empty(B.block_norm_workspace_size(T, K), dtype=torch.uint8, device="cuda")
+    back = dict(rstd_post=rz, rstd_pre=rx, d_x_out=dxo, d_y=dy, d_x=dx, d_z=dz, d_gate=dg,
+                d_post_weight=dp, d_pre_weight=dq, workspace=ws)
+    with pytest.raises(ValueError, match="gate_kind"):
+        B.moe_block_norm_backward(s["x"], **kw, **back)
+    B.moe_block_norm_backward(s["x"], gate_kind=code, **kw, **back)
+
+    leaf = {n: s[n].cpu().double().requires_grad_(True) for n in ("x", "z", "post", "gate", "pre")}
+    g = leaf["gate"][:, None] if token else leaf["gate"][None, :]
+    rxo, ry = forward64(leaf["x"], leaf["z"], leaf["post"], g, 0.6, leaf["pre"], 0.0)
+    torch.autograd.backward([rxo, ry], [dxo.cpu().double(), dy.cpu().double()])
+    # one rounding of each value, and fp32 sums that may cancel to a hundredth
+    tol = HALF_ULP[dt] + 6400 * U
+    for name, got, ref in (("x_out", xo, rxo), ("y", y, ry), ("d_x", dx, leaf["x"].grad),
+                           ("d_z", dz, leaf["z"].grad), ("d_gate", dg, leaf["gate"].grad),
+                           ("d_post", dp, leaf["post"].grad), ("d_pre", dq, leaf["pre"].grad)):
+        off = ((got.cpu().double() - ref).norm() / ref.norm()).item()
+        assert off <= tol, (name, off)
+
+
+def test_gate_kinds_that_shape_and_type_settle_and_refusals():
+    T = K = 32
+    s = tensors(T, K, "bf16", "fp32", "token", "plain")
+    kw = dict(z=s["z"], post_weight=s["post"], pre_weight=s["pre"])
+
+    def run(gate, **more):
+        xo, y = s["rnd"](T, K), s["rnd"](T, K)
+        B.moe_block_norm(s["x"], gate=gate, x_out=xo, y=y, **kw, **more)
+        return torch.cat([xo, y])
+
+    token, channel = s["gate"], s["rnd"](K, dtype=torch.float32)
+    assert torch.equal(run(token), run(token[:, None]))  # bf16, where channel gates are fp32
+    assert torch.equal(run(token), run(token, gate_kind=B.MOE_GATE_TOKEN))
+    assert torch.equal(run(channel), run(channel, gate_kind=B.MOE_GATE_CHANNEL))
+    full = token[:, None].expand(T, K).contiguous()
+    assert torch.equal(run(full), run(full, gate_kind=B.MOE_GATE_FULL))
+    for gate, kind in ((token, B.MOE_GATE_CHANNEL), (channel, B.MOE_GATE_TOKEN),
+                       (token, B.MOE_GATE_FULL), (full, B.MOE_GATE_TOKEN), (token, 7),
+                       (full, B.MOE_GATE_NONE), (None, B.MOE_GATE_TOKEN)):
+        with pytest.raises(ValueError):
+            run(gate, gate_kind=kind)
