@@ -80,10 +80,12 @@ __device__ __forceinline__ float warp_max_key(uint32_t k) {
   return key_value(__reduce_max_sync(0xFFFFFFFFu, k));
 }
 
-// A group's value from its two highest keys (0: none).
+// A group's value from its two highest keys (0: none).  Two keys near the lowest float
+// (masked experts) add up to -inf; such a group comes after all others and before those
+// that have no expert to take, so its value is 1.
 __device__ __forceinline__ uint32_t group_key(const RouteParams& p, uint32_t k1, uint32_t k2) {
   if (p.bias == nullptr || k1 == 0) return k1;
-  return order_key(__fadd_rn(key_value(k1), k2 ? key_value(k2) : 0.0f));
+  return max(order_key(__fadd_rn(key_value(k1), k2 ? key_value(k2) : 0.0f)), 1u);
 }
 
 // Whether group g, whose value lane g << shift has in gk, is among the best

@@ -224,3 +224,28 @@ def test_refusals():
     with pytest.raises(B.MoeError) as e:
         B.moe_route(l, ids, w, num_groups=3)
     assert e.value.status == 2
+
+
+@pytest.mark.parametrize("E,groups", [(64, 2), (128, 2), (12, 3), (60, 3)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_groups_whose_best_two_keys_add_up_to_minus_infinity(E, groups, scoring):
+    # masked by the type's lowest value, through the logits or the bias: such a group is the
+    # last to be taken, but it has experts, and comes before a group that has none
+    low, size = torch.finfo(torch.float32).min, E // groups
+    l, bias = torch.zeros(4, E), torch.zeros(E)
+    if scoring == "softmax":
+        l.fill_(low)
+    else:
+        bias.fill_(low)
+        bias[1] = 0.25
+    l[:, 1] = 1.0
+    l[1] = torch.arange(E) % 7
+    l[2, :size] = -float("inf") if scoring == "softmax" else float("nan")
+    l[3] = float("nan")
+    l[3, -2:] = low if scoring == "softmax" else 0.0
+    ids, w = route(l.cuda(), 6, scoring, True, bias=bias.cuda(), groups=groups, top_groups=2)
+    key = l if scoring == "softmax" else 1.0 / (1.0 + torch.exp(-l))
+    with np.errstate(over="ignore", invalid="ignore"):
+        want = select(key.numpy(), bias.numpy(), "softmax", 6, groups, 2)
+    assert np.array_equal(ids.cpu().numpy(), want)
+    assert bool(torch.isfinite(w).all())
