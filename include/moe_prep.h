@@ -600,7 +600,9 @@ moe_status_t moe_unpermute_backward(const moe_unpermute_backward_args_t* args, v
 /* may be NULL: zero) and the inputs, rstd_post and rstd_pre of the forward.  */
 /* Sums over tokens run in fp32 in a fixed order.  workspace:                 */
 /* moe_block_norm_workspace_size() bytes, need not be cleared; it serves      */
-/* fewer tokens as well.  Every output but d_x may be NULL.                   */
+/* fewer tokens as well.  Every output but d_x may be NULL.  Without tokens    */
+/* the [K] gradients are zeros; tensors with a row a token and the workspace  */
+/* may then be NULL.                                                          */
 /* Errors: K > 16384 -> UNSUPPORTED.                                          */
 /* ------------------------------------------------------------------------ */
 typedef struct moe_block_norm_args {

@@ -339,6 +339,7 @@ moe_status_t moe_block_norm(const moe_block_norm_args_t* a, void* stream) {
   const int64_t T = a->num_tokens, K = a->hidden_size;
   moe_status_t st = check_norm(T, K, a->dtype, a->weight_dtype, a->gate_kind);
   if (st != MOE_OK) return st;
+  if (T == 0 || K == 0) return MOE_OK;  // before the pointers: empty tensors have no address
   if ((a->z != nullptr) != (a->x_out != nullptr))
     return set_error(MOE_ERR_INVALID_ARGUMENT, "x_out must be given iff z is");
   if ((a->pre_weight != nullptr) != (a->y != nullptr))
@@ -347,7 +348,6 @@ moe_status_t moe_block_norm(const moe_block_norm_args_t* a, void* stream) {
     return set_error(MOE_ERR_INVALID_ARGUMENT, "gate must be given iff gate_kind is not NONE");
   if (a->z == nullptr && (a->gate != nullptr || a->post_weight != nullptr))
     return set_error(MOE_ERR_INVALID_ARGUMENT, "a gate or post_weight needs z");
-  if (T == 0 || K == 0) return MOE_OK;
   if (a->x == nullptr || (a->z == nullptr && a->y == nullptr))
     return set_error(MOE_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
   if (T > 1 && (a->x_stride0 < K || (a->z && (a->z_stride0 < K || a->x_out_stride0 < K)) ||

@@ -455,7 +455,9 @@ static int64_t norm_row_blocks(int64_t T) {
   return T < 1 ? 1 : (T < kMaxRowBlocks ? T : kMaxRowBlocks);
 }
 
+// Without tokens the columns' sums, all zero, come from no block of rows.
 static size_t norm_workspace(int64_t T, int64_t K) {
+  if (T <= 0 || K <= 0) return 0;
   return (size_t)(T * 16 + norm_row_blocks(T) * 3 * K * 4);
 }
 
@@ -495,7 +497,6 @@ using namespace moe_host;
 extern "C" {
 
 size_t moe_block_norm_workspace_size(int64_t num_tokens, int64_t hidden_size) {
-  if (num_tokens <= 0 || hidden_size <= 0) return 0;
   return norm_workspace(num_tokens, hidden_size);
 }
 
@@ -505,9 +506,12 @@ moe_status_t moe_block_norm_backward(const moe_block_norm_backward_args_t* a, vo
   const int64_t T = a->num_tokens, K = a->hidden_size;
   moe_status_t st = check_norm(T, K, a->dtype, a->weight_dtype, a->gate_kind);
   if (st != MOE_OK) return st;
-  if ((a->gate != nullptr) != (a->gate_kind != MOE_GATE_NONE))
+  if (K == 0) return MOE_OK;
+  // (without tokens their tensors have no address)
+  if (T > 0 && (a->gate != nullptr) != (a->gate_kind != MOE_GATE_NONE))
     return set_error(MOE_ERR_INVALID_ARGUMENT, "gate must be given iff gate_kind is not NONE");
-  if (a->z == nullptr && (a->gate != nullptr || a->post_weight != nullptr || a->d_z != nullptr))
+  if (T > 0 && a->z == nullptr &&
+      (a->gate != nullptr || a->post_weight != nullptr || a->d_z != nullptr))
     return set_error(MOE_ERR_INVALID_ARGUMENT, "a gate, post_weight or d_z needs z");
   if ((a->d_gate != nullptr && a->gate == nullptr) ||
       (a->d_post_weight != nullptr && a->post_weight == nullptr) ||
@@ -515,8 +519,8 @@ moe_status_t moe_block_norm_backward(const moe_block_norm_backward_args_t* a, vo
     return set_error(MOE_ERR_INVALID_ARGUMENT, "a gradient of an input that is not given");
   if (a->d_y != nullptr && a->pre_weight == nullptr)
     return set_error(MOE_ERR_INVALID_ARGUMENT, "d_y needs pre_weight");
-  if (K == 0 || (T == 0 && !a->d_post_weight && !a->d_pre_weight &&
-                 !(a->d_gate && a->gate_kind == MOE_GATE_CHANNEL)))
+  if (T == 0 && !a->d_post_weight && !a->d_pre_weight &&
+      !(a->d_gate && a->gate_kind == MOE_GATE_CHANNEL))
     return MOE_OK;
   if (T > 0 && (!a->x || !a->d_x || (a->post_weight && !a->rstd_post) ||
                 (a->pre_weight && !a->rstd_pre)))
@@ -528,7 +532,7 @@ moe_status_t moe_block_norm_backward(const moe_block_norm_backward_args_t* a, vo
                  (a->gate_stride0 < K || (a->d_gate && a->d_gate_stride0 < K)))))
     return set_error(MOE_ERR_SHAPE, "row stride smaller than the row");
   const size_t need = norm_workspace(T, K);
-  if (a->workspace == nullptr || a->workspace_bytes < need)
+  if (need > 0 && (a->workspace == nullptr || a->workspace_bytes < need))
     return set_error(MOE_ERR_WORKSPACE, "the gradient needs %zu bytes of workspace, got %zu", need,
                      a->workspace_bytes);
   if ((reinterpret_cast<uintptr_t>(a->workspace) & 15u) != 0)

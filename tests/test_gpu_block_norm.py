@@ -321,3 +321,31 @@ def test_gate_kinds_that_shape_and_type_settle_and_refusals():
                        (full, B.MOE_GATE_NONE), (None, B.MOE_GATE_TOKEN)):
         with pytest.raises(ValueError):
             run(gate, gate_kind=kind)
+
+
+@pytest.mark.parametrize("gate", ["none", "channel", "token", "full"])
+def test_no_tokens(gate):
+    K = 72
+    s = tensors(0, K, "bf16", "fp32", gate, "plain")
+    kw = dict(z=s["z"], post_weight=s["post"], gate=s["gate"], pre_weight=s["pre"])
+    e, r = s["rnd"](0, K), torch.empty(0, device="cuda")
+    B.moe_block_norm(s["x"], x_out=e, y=e.clone(), rstd_post=r, rstd_pre=r.clone(), **kw)
+    B.moe_block_norm(s["x"], pre_weight=s["pre"], y=e)
+    dp, dq = torch.full((K,), 7.0, device="cuda"), torch.full((K,), 7.0, device="cuda")
+    dg = None if s["gate"] is None else torch.full_like(s["gate"], 7.0)
+    n = B.block_norm_workspace_size(0, K)
+    B.moe_block_norm_backward(s["x"], rstd_post=r, rstd_pre=r, d_x_out=e, d_y=e, d_x=e, d_z=e,
+                              d_gate=dg, d_post_weight=dp, d_pre_weight=dq,
+                              workspace=torch.empty(n, dtype=torch.uint8, device="cuda"), **kw)
+    assert not dp.any() and not dq.any() and (dg is None or not dg.any())
+    dq.fill_(7.0)
+    B.moe_block_norm_backward(s["x"], pre_weight=s["pre"], rstd_pre=r, d_y=e, d_x=e,
+                              d_pre_weight=dq)
+    assert not dq.any()
+
+
+def test_no_columns():
+    x, w = torch.empty(5, 0, device="cuda"), torch.empty(0, device="cuda")
+    B.moe_block_norm(x, z=x, post_weight=w, pre_weight=w, x_out=x, y=x)
+    B.moe_block_norm_backward(x, z=x, post_weight=w, pre_weight=w, d_x=x, d_z=x, d_y=x,
+                              d_post_weight=w, d_pre_weight=w)
