@@ -532,13 +532,14 @@ moe_status_t moe_sort_routes(const moe_sort_args_t* a, void* stream) {
 moe_status_t moe_permute(const moe_permute_args_t* a, void* stream) {
   clear_error();
   if (a == nullptr) return set_error(MOE_ERR_INVALID_ARGUMENT, "args is NULL");
-  const int64_t num_tokens = a->num_tokens, hidden_size = a->hidden_size;
-  const int64_t top_k = a->top_k, num_rows = a->num_rows;
-  moe_status_t st = check_rows(num_tokens, hidden_size, top_k, num_rows, a->dtype);
+  const int64_t hidden_size = a->hidden_size, top_k = a->top_k, num_rows = a->num_rows;
+  moe_status_t st = check_rows(a->num_tokens, hidden_size, top_k, num_rows, a->dtype);
   if (st != MOE_OK) return st;
+  // tokens without routes have nothing to copy and their x, which may be NULL, is not read
+  const int64_t num_tokens = top_k > 0 ? a->num_tokens : 0;
   if (a->num_experts < 0) return set_error(MOE_ERR_INVALID_ARGUMENT, "negative size");
   if (num_rows == 0 || hidden_size == 0) return MOE_OK;
-  if (!a->rows || !a->expert_offsets || (num_tokens * top_k > 0 && (!a->x || !a->route_row)))
+  if (!a->rows || !a->expert_offsets || (num_tokens > 0 && (!a->x || !a->route_row)))
     return set_error(MOE_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
   if ((num_tokens > 1 && a->x_stride0 < hidden_size) ||
       (num_rows > 1 && a->rows_stride0 < hidden_size))

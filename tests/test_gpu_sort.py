@@ -221,3 +221,37 @@ def test_stream_and_refusals():
                           torch.empty(5000, 1, dtype=torch.int32, device="cuda"),
                           torch.empty(5000, dtype=torch.int32, device="cuda"))
     assert e.value.status == 5  # above one block's routes a workspace is needed
+
+
+def test_tokens_without_routes():
+    # top_k 0: nothing of x is read (the address may be NULL), every row is cleared
+    T, K, R = 70, 520, 9
+    off = torch.zeros(5, dtype=torch.int32, device="cuda")
+    rr = torch.empty(T, 0, dtype=torch.int32, device="cuda")
+    x = torch.full((T, K), float("nan"), dtype=torch.bfloat16, device="cuda")
+    for null in (False, True):
+        rows = torch.full((R, K), 7.0, dtype=torch.bfloat16, device="cuda")
+        if null:
+            st = B.load().moe_permute(B.PermuteArgs.pack(
+                T, K, 0, 4, R, B.MOE_DTYPE_BF16, 0, K, 0, off.data_ptr(), rows.data_ptr(), K),
+                torch.cuda.current_stream().cuda_stream)
+            assert st == B.MOE_OK
+        else:
+            B.moe_permute(x, rr, off, rows)
+        assert not rows.any()
+    out = torch.full((T, K), 7.0, dtype=torch.bfloat16, device="cuda")
+    B.moe_unpermute(rows, rr, None, out)
+    assert not out.any()
+
+
+def test_no_tokens():
+    off = torch.zeros(5, dtype=torch.int32, device="cuda")
+    rr = torch.empty(0, 2, dtype=torch.int32, device="cuda")
+    w, e = torch.empty(0, 2, device="cuda"), torch.empty(0, 64, device="cuda")
+    for R in (0, 3):
+        rows, d_rows = torch.full((R, 64), 7.0, device="cuda"), torch.full((R, 64), 7.0, device="cuda")
+        B.moe_permute(e, rr, off, rows)
+        B.moe_unpermute(rows, rr, w, e)
+        B.moe_unpermute_backward(e, rows, rr, w, off, d_rows, w)
+        B.moe_permute_backward(rows, rr, e)
+        assert not rows.any() and not d_rows.any()
