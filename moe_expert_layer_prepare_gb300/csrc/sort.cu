@@ -410,13 +410,18 @@ static void sort_split(int64_t R, int32_t* blocks, int32_t* per_block) {
 
 static int32_t hist_row(int32_t blocks) { return (blocks + 3) / 4 * 4; }
 
-// Grows with R, so that a workspace serves fewer routes too.
-static size_t sort_workspace(int64_t R, int64_t E) {
-  if (R <= kSortOneBlock) return 0;
+// Most blocks that R routes or fewer are split among: grows with R, unlike sort_split's
+// (128 at 131,072 routes, 86 at one more), so that a workspace serves fewer routes too.
+static int32_t most_blocks(int64_t R) {
+  if (R <= kSortOneBlock) return 1;
   int64_t blocks = (R + 1023) / 1024;
   if (blocks > moe::SORT_BLOCKS) blocks = moe::SORT_BLOCKS;
-  const int64_t most = (R + moe::SORT_MAX_PER_BLOCK - 1) / moe::SORT_MAX_PER_BLOCK;
-  return (size_t)hist_row((int32_t)(blocks > most ? blocks : most)) * E * 4;
+  const int64_t full = (R + moe::SORT_MAX_PER_BLOCK - 1) / moe::SORT_MAX_PER_BLOCK;
+  return (int32_t)(blocks > full ? blocks : full);
+}
+
+static size_t sort_workspace(int64_t R, int64_t E) {
+  return R <= kSortOneBlock ? 0 : (size_t)hist_row(most_blocks(R)) * E * 4;
 }
 
 static moe_status_t launch_sort(const SortParams& p, cudaStream_t s) {
@@ -434,8 +439,7 @@ static moe_status_t launch_sort(const SortParams& p, cudaStream_t s) {
 // rows >= T + (align - 1) (S + 1).  Scratch: token_order_scratch() words, of which
 // scratch[S + 1] is then the number of places taken.
 size_t token_order_scratch(int64_t T, int64_t S) {
-  int32_t blocks, per;
-  sort_split(T, &blocks, &per);
+  const int32_t blocks = most_blocks(T);
   return (size_t)((blocks > 1 ? hist_row(blocks) * (S + 1) + 3 : 0) + (S + 2) + T);
 }
 

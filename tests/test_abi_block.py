@@ -202,3 +202,18 @@ def test_lora(lib):
     assert lora(out_features=1 << 30, out_stride0=1 << 30) == UNSUPPORTED
     assert lib.moe_lora_workspace_size(4, 64, 32, 0, 8) == 0
     assert lib.moe_lora_workspace_size(4, 64, 32, 2, 8) > 0
+
+
+def test_workspaces_grow_with_the_tokens(lib):
+    # every step, at the counts where a plan changes: one block or many of the sort, its blocks'
+    # share, the projection's path and the shrink's tokens a block
+    steps = sorted({t + d for t in (16, 32, 64, 128, 256, 512, 1024, 2048, 4096, 32768, 65536,
+                                    131072, 132096, 196608, 262144, 1048576, 4063232)
+                    for d in (-1025, -129, -2, -1, 0, 1, 2, 97, 129, 1025) if t + d > 0})
+    for k, n, s, r in ((4096, 4096, 256, 16), (64, 64, 1023, 8), (7168, 4096, 16, 64),
+                       (2048, 7168, 48, 32), (512, 512, 1, 128)):
+        sizes = [lib.moe_lora_workspace_size(t, k, n, s, r) for t in steps]
+        assert sizes == sorted(sizes), (k, n, s, r)
+    for e in (1, 8, 1024):
+        sizes = [lib.moe_sort_workspace_size(t, 1, e) for t in steps]
+        assert sizes == sorted(sizes), e
