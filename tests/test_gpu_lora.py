@@ -200,3 +200,91 @@ def test_wait_timeout_sets_status_and_context_survives():
             B._lib = regular
         assert int(st.item()) & B.MOE_DEV_TIMEOUT
         check(p)
+
+
+@pytest.mark.parametrize("T", [130, 200, 400, 512])
+def test_a_broken_adapter_and_bad_ids_in_batches_of_two_to_four_tiles(T):
+    # tokens as they come through the tcgen05 shrink, then tiles of 64 or 128 tokens
+    for R in (16, 72):
+        p = problem(T, 264, 200, 6, R, "bf16")
+        p["adapter_ids"][3], p["adapter_ids"][T - 1] = 6, 2 ** 31 - 1
+        p["adapter_ids"][p["adapter_ids"] == 2] = -7
+        p["lora_a"][2] = float("nan")
+        p["lora_b"][2] = float("nan")
+        good = torch.where((p["adapter_ids"] == 3) | (p["adapter_ids"] >= 6), -1, p["adapter_ids"])
+        q = dict(p, adapter_ids=good)
+        p["lora_a"][3, 1] = float("inf")
+        p["lora_b"][3] = float("nan")
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = run(p, status=st)
+        others = (p["adapter_ids"] != 3).cpu()
+        ref, extra = expect(q)
+        assert_within(out[others], ref[others], rounded(ref, out.dtype, extra)[others], "others")
+        assert bool(torch.isnan(out.cpu()[~others]).all())
+        assert int(st.item()) == B.MOE_DEV_BAD_ADAPTER
+
+
+def test_batches_of_every_path_share_a_workspace_back_to_back():
+    # order, copied rows, pieces of tiles and sums of one call right behind those of another
+    sizes = (700, 300, 2100, 40, 1500, 513, 512, 1, 900)
+    ps = [problem(T, 520, 776, 9, 40, "bf16", seed=T) for T in sizes]
+    need = max(B.lora_workspace_size(T, 520, 776, 9, 40) for T in sizes)
+    assert need == B.lora_workspace_size(max(sizes), 520, 776, 9, 40)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    for _ in range(4):
+        for p in ps:
+            p["out"].fill_(float("nan"))
+        for p in ps:
+            B.moe_lora_linear(workspace=ws, **p)
+    torch.cuda.synchronize()
+    for p in ps:
+        ref, extra = expect(p)
+        assert_within(p["out"], ref, rounded(ref, p["out"].dtype, extra), "out")
+
+
+@pytest.mark.parametrize("T,dtype,order", [(600, "bf16", "mixed"), (1024, "fp16", "mixed"),
+                                           (2000, "bf16", "mixed"), (2000, "bf16", "sorted")])
+def test_mixed_batches_of_real_width(T, dtype, order):
+    p = problem(T, 2048, 7168, 16, 64, dtype, order=order)
+    check(p)
+    first = p["out"].clone()
+    for _ in range(10):  # the same bits each time
+        p["out"].fill_(0.0)
+        assert torch.equal(run(p), first)
+
+
+def test_norm_router_and_projection_behind_one_another():
+    # the chain of a block without a synchronisation, against the same calls one at a time
+    T, K, N, E = 1500, 2048, 1024, 64
+    p = problem(T, K, N, 8, 16, "bf16")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, z = (torch.randn(T, K, generator=g, device="cuda").bfloat16() for _ in range(2))
+    ones = torch.ones(K, dtype=torch.bfloat16, device="cuda")
+    router = (torch.randn(E, K, generator=g, device="cuda") * K ** -0.5).bfloat16()
+    ws = torch.empty(B.lora_workspace_size(T, K, N, 8, 16), dtype=torch.uint8, device="cuda")
+
+    def chain(pause):
+        bufs = dict(xo=torch.zeros_like(x), h=torch.zeros_like(x),
+                    logits=torch.zeros(T, E, dtype=torch.bfloat16, device="cuda"),
+                    ids=torch.zeros(T, 4, dtype=torch.int32, device="cuda"),
+                    w=torch.zeros(T, 4, device="cuda"), out=torch.zeros_like(p["out"]))
+        torch.cuda.synchronize()
+        steps = [
+            lambda: B.moe_block_norm(x, z=z, post_weight=ones, pre_weight=ones, x_out=bufs["xo"],
+                                     y=bufs["h"]),
+            lambda: B.moe_lora_linear(bufs["h"], router, None, None, None, None, bufs["logits"],
+                                      None),
+            lambda: B.moe_route(bufs["logits"], bufs["ids"], bufs["w"]),
+            lambda: B.moe_lora_linear(bufs["h"], p["weight"], p["lora_a"], p["lora_b"],
+                                      p["adapter_ids"], p["lora_scale"], bufs["out"], ws)]
+        for _ in range(3):
+            for step in steps:
+                step()
+                if pause:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return bufs
+
+    a, b = chain(True), chain(False)
+    for name in a:
+        assert torch.equal(a[name], b[name]), name

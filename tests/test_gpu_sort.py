@@ -255,3 +255,14 @@ def test_no_tokens():
         B.moe_unpermute_backward(e, rows, rr, w, off, d_rows, w)
         B.moe_permute_backward(rows, rr, e)
         assert not rows.any() and not d_rows.any()
+
+
+# 2048 routes are the most that one block sorts, 131,072 the most of blocks of 1024 routes each
+@pytest.mark.parametrize("R", [2047, 2048, 2049, 3072, 131071, 131073])
+@pytest.mark.parametrize("E", [1, 256, 1024])
+def test_sort_at_the_steps_of_the_split(R, E):
+    rng = np.random.default_rng(R + E)
+    ids = rng.integers(-1, E, size=(R, 1))
+    off, rr, ro = sort_routes(torch.from_numpy(ids).to("cuda", torch.int32), E)
+    for got, want in zip((off, rr, ro), plan(ids, E)):
+        assert np.array_equal(got.cpu().numpy(), want)
