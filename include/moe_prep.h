@@ -674,7 +674,10 @@ size_t moe_block_norm_workspace_size(int64_t num_tokens, int64_t hidden_size);
 /* tokens with a < 0 (no adapter; a >= num_adapters also sets                 */
 /* MOE_DEV_BAD_ADAPTER) take the first sum alone.  Sums are in fp32; scale*h  */
 /* enters the second product as two values of the tensors' type, its rounding */
-/* and the remainder; out is rounded once.                                    */
+/* and the remainder (16 bits of bf16; of fp16 22, in steps of 2^-24 at the    */
+/* smallest); of fp16, four or eight neighbouring ranks of a token with a      */
+/* value above 65504, or all below 2^-14, are multiplied in fp32.  out is      */
+/* rounded once.                                                              */
 /* An adapter's values, non-finite ones too, reach its own tokens alone.      */
 /* x [T, K] and out [T, N]: inner stride 1, row strides of their own; weight  */
 /* [N, K], lora_a [S, R, K], lora_b [S, N, R] contiguous; adapter_ids int32   */

@@ -29,7 +29,8 @@
 //
 // In both an adapter's values reach its own tokens only (a non-finite weight stays
 // with them), and as the MMA takes 16-bit operands, s_a h enters as its rounding and
-// the rounded remainder, which keeps the adapters' part as exact as the rest.
+// the rounded remainder: 16 bits of its significand in bf16, 22 in fp16, where the output
+// keeps 8 and 11.  What fp16's exponents do not hold is added in fp32 (wide_piece).
 //
 // The projection's launch starts while the shrink still runs and waits for it only
 // where h is read.
@@ -67,6 +68,7 @@ struct LoraParams {
   float* partials;  // pair, nullable: pieces of tiles, [pairs][2][LP_TILE tokens][LP_HALF]
   int pairs;        // of CTAs
   float* h;        // [shares][T][R]
+  uint32_t* wide;  // pair, fp16: whether any piece of s h is wide, then from word 4 on which
   int shares;      // of K in the shrink
   int share_k;     // K of one share, a multiple of 64
   int splits;      // cluster size of the projection
@@ -139,6 +141,34 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Whether a piece of a token's s h (N neighbouring ranks: four in short batches, eight in
+// long ones) is wide: beyond fp16's exponents, with a value above 65504 or not finite, or
+// all of them below its normal range, where the remainder's step of 2^-24 would show in
+// the output's 11 bits.  It goes into the MMA as zeros and is added in fp32: 2048 -> 7168,
+// 64 tokens of rank 32 20 us, all pieces wide 44; 7168 -> 4096, 1024 tokens of rank 64 112
+// and 434.
+template <typename T, int N>
+__device__ __forceinline__ bool wide_piece(const float (&f)[N]) {
+  if constexpr (!std::is_same<T, __half>::value) return false;
+  float m = 0.0f;
+  bool fits = true;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    fits = fits && fabsf(f[e]) <= 65504.0f;
+    m = fmaxf(m, fabsf(f[e]));
+  }
+  return !fits || (m > 0.0f && m < 0x1p-14f);
+}
+
+// Two values of s h as their roundings and rounded remainders; an infinity has none.
+template <typename T>
+__device__ __forceinline__ void split_pair(float2 f, uint32_t& hi, uint32_t& low) {
+  hi = pack2<T>(f);
+  const float2 h = unpack2<T>(hi);
+  low = pack2<T>(make_float2(fabsf(h.x) < INFINITY ? f.x - h.x : 0.0f,
+                             fabsf(h.y) < INFINITY ? f.y - h.y : 0.0f));
 }
 
 // Byte offset of 16-byte piece `piece` of row `row` in a tile of 128-byte rows,
@@ -305,6 +335,7 @@ __global__ void __launch_bounds__(SH_THREADS, 2) lora_shrink_long_kernel(LoraPar
   pdl_wait();
   pdl_launch_dependents();
   const int64_t t0 = (int64_t)blockIdx.x * SH_LONG;
+  if (p.wide != nullptr && blockIdx.x + blockIdx.y + blockIdx.z == 0 && tid == 0) *p.wide = 0;
   if (p.order != nullptr && t0 >= *p.places) return;
   bool bad = false;
   if (tid < SH_LONG) {
@@ -502,9 +533,9 @@ constexpr int LG_MAX_STAGES = 5;
 constexpr int lg_stages(int nt) { return nt <= 32 ? 5 : 4; }
 constexpr int lg_ring(int nt) { return lg_stages(nt) * (LG_A_BYTES + nt * 128); }
 // Shared memory: ring; of this CTA's share of the tokens s h (rounding, remainder)
-// and the adapters' part; barriers, ids, order, chunks.
+// and the adapters' part; barriers, ids, order, chunks, wide pieces.
 __host__ __device__ inline int lg_smem(int nt, int splits, int R) {
-  return 1024 + lg_ring(nt) + (R > 0 ? nt / splits * (R + LG_M) * 4 : 0) + 256 + nt * 12;
+  return 1024 + lg_ring(nt) + (R > 0 ? nt / splits * (R + LG_M) * 4 : 0) + 512 + nt * 12;
 }
 
 // Tokens of one adapter, neighbours in the order, at most 8: one MMA tile.
@@ -575,6 +606,43 @@ __device__ __forceinline__ void expand_tokens(const LoraParams& p, const Chunk* 
   }
 }
 
+// The wide pieces, in fp32: feature f a thread, piece after piece, bit i of `wide` ranks
+// 4 i, ... of the share's s h.  Where a piece's rounding and remainder were, hs has its
+// four floats by now.
+template <typename T>
+__device__ __forceinline__ void add_wide_tokens(const LoraParams& p, const uint32_t* wide,
+                                                const T* hs, const int16_t* id,
+                                                const int16_t* order, int share, float* add,
+                                                int64_t n0, int f) {
+  const int R = (int)p.R, q4 = R / 4;
+  for (int w = 0; w * 32 < share * q4; ++w)
+    for (uint32_t m = wide[w]; m != 0;) {
+      constexpr int U = 4;  // rows of B in flight
+      int piece[U];
+      uint2 b[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = m != 0 ? w * 32 + __ffs(m) - 1 : -1, k = i / q4;
+        m &= m - 1;
+        piece[u] = i;
+        b[u] = make_uint2(0, 0);
+        if (i >= 0 && n0 + f < p.N)
+          b[u] = __ldg(reinterpret_cast<const uint2*>(
+              static_cast<const T*>(p.b) +
+              ((int64_t)id[order[k]] * p.N + n0 + f) * R + (i - k * q4) * 4));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (piece[u] < 0) break;
+        const float2 b0 = unpack2<T>(b[u].x), b1 = unpack2<T>(b[u].y);
+        const float2 h0 = reinterpret_cast<const float2*>(hs)[piece[u]];
+        const float2 h1 = reinterpret_cast<const float2*>(hs + share * R)[piece[u]];
+        float& sum = add[piece[u] / q4 * LG_M + f];
+        sum = fmaf(b0.x, h0.x, fmaf(b0.y, h0.y, fmaf(b1.x, h1.x, fmaf(b1.y, h1.y, sum))));
+      }
+    }
+}
+
 // Stores the share's tokens: the cluster's sums in rank order and the adapters' part.
 template <typename T, int SPLITS>
 __device__ __forceinline__ void join_tokens(const LoraParams& p, const float* sums,
@@ -628,9 +696,13 @@ __global__ void __launch_bounds__(LG_THREADS, NT <= 64 ? 2 : 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * LG_MAX_STAGES + 1);
   int* s_abort = reinterpret_cast<int*>(tmem_holder + 1);
   int* s_chunks = s_abort + 1;
+  int* s_any_wide = s_chunks + 1;
   Chunk* chunks = reinterpret_cast<Chunk*>(reinterpret_cast<uint8_t*>(bars) + 256);  // [NT]
   int16_t* s_id = reinterpret_cast<int16_t*>(chunks + NT);
   int16_t* s_order = s_id + NT;
+  uint32_t* s_wide = reinterpret_cast<uint32_t*>(s_order + NT);  // [64]: NT R / 4 bits, R <= 64
+                                                                 // above 64 tokens
+  constexpr bool half = std::is_same<T, __half>::value;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort_flag = s_abort;
@@ -750,7 +822,8 @@ __global__ void __launch_bounds__(LG_THREADS, NT <= 64 ? 2 : 1)
         while (j > 0 && adapter(j - 1) == adapter(i)) --j;
         return j;
       };
-      if (st == 0) *s_chunks = 0;
+      if (st == 0) *s_chunks = *s_any_wide = 0;
+      for (int i = st; half && i < 64; i += LG_SIDE) s_wide[i] = 0;
       side_sync();
       for (int i = st; i < share; i += LG_SIDE) {
         const int a = adapter(i), begin = run_begin(i);
@@ -763,36 +836,47 @@ __global__ void __launch_bounds__(LG_THREADS, NT <= 64 ? 2 : 1)
                       (uint32_t)(min((int64_t)LG_M, p.N - n0) * p.R * 2));
       }
       if (!p.wait_first) pdl_wait();
-      const int q4 = (int)p.R / 4;
-      for (int i = st; i < share * q4; i += LG_SIDE) {
-        const int k = i / q4, c = s_order[pos0 + k], a = s_id[c];
-        if (a < 0) continue;
-        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const float* src = p.h + (t0 + c) * p.R + (i - k * q4) * 4;
-        for (int s0 = 0; s0 < p.shares; s0 += 8) {  // eight shares' sums in flight
-          float4 u[8];
+      // s h of the share, four ranks a thread: their roundings and remainders, or, where
+      // `floats` and the piece is wide, the values themselves
+      auto gather = [&](bool floats) {
+        const int q4 = (int)p.R / 4;
+        for (int i = st; i < share * q4; i += LG_SIDE) {
+          const int k = i / q4, c = s_order[pos0 + k], a = s_id[c];
+          if (a < 0) continue;
+          float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          const float* src = p.h + (t0 + c) * p.R + (i - k * q4) * 4;
+          for (int s0 = 0; s0 < p.shares; s0 += 8) {  // eight shares' sums in flight
+            float4 u[8];
 #pragma unroll
-          for (int s = 0; s < 8; ++s)
-            u[s] = s0 + s < p.shares
-                       ? __ldcg(reinterpret_cast<const float4*>(src + (s0 + s) * p.T * p.R))
-                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int s = 0; s < 8; ++s)
+              u[s] = s0 + s < p.shares
+                         ? __ldcg(reinterpret_cast<const float4*>(src + (s0 + s) * p.T * p.R))
+                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-          for (int s = 0; s < 8; ++s)
-            sum.x += u[s].x, sum.y += u[s].y, sum.z += u[s].z, sum.w += u[s].w;
+            for (int s = 0; s < 8; ++s)
+              sum.x += u[s].x, sum.y += u[s].y, sum.z += u[s].z, sum.w += u[s].w;
+          }
+          const float scale = __ldg(p.scale + a);
+          const float f[4] = {scale * sum.x, scale * sum.y, scale * sum.z, scale * sum.w};
+          uint2 hi, low;
+          if (half && wide_piece<T>(f)) {
+            atomicOr(s_wide + i / 32, 1u << (i & 31));
+            *s_any_wide = 1;
+            hi = low = make_uint2(0, 0);
+            if (floats) {
+              hi = make_uint2(__float_as_uint(f[0]), __float_as_uint(f[1]));
+              low = make_uint2(__float_as_uint(f[2]), __float_as_uint(f[3]));
+            }
+          } else {
+            split_pair<T>(make_float2(f[0], f[1]), hi.x, low.x);
+            split_pair<T>(make_float2(f[2], f[3]), hi.y, low.y);
+          }
+          reinterpret_cast<uint2*>(hs)[i] = hi;
+          reinterpret_cast<uint2*>(hs + share * p.R)[i] = low;
         }
-        const float scale = __ldg(p.scale + a);
-        const float2 f[2] = {make_float2(scale * sum.x, scale * sum.y),
-                             make_float2(scale * sum.z, scale * sum.w)};
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t hi = pack2<T>(f[e]);
-          const float2 h = unpack2<T>(hi);
-          reinterpret_cast<uint32_t*>(hs)[2 * i + e] = hi;
-          reinterpret_cast<uint32_t*>(hs + share * p.R)[2 * i + e] =
-              pack2<T>(make_float2(f[e].x - h.x, f[e].y - h.y));
-        }
-      }
-      side_sync();
+        side_sync();
+      };
+      gather(false);
       const int n = *s_chunks, w = warp - 2;
       if (p.R <= 32)
         expand_tokens<T, 1, 4>(p, chunks, n, hs, share, add, n0, w, LG_SIDE / 32);
@@ -800,6 +884,12 @@ __global__ void __launch_bounds__(LG_THREADS, NT <= 64 ? 2 : 1)
         expand_tokens<T, 2, 2>(p, chunks, n, hs, share, add, n0, w, LG_SIDE / 32);
       else
         expand_tokens<T, 4, 1>(p, chunks, n, hs, share, add, n0, w, LG_SIDE / 32);
+      if (half && *s_any_wide != 0) {
+        side_sync();  // the MMAs' part is there, and hs free
+        gather(true);
+        if (st < LG_M)
+          add_wide_tokens<T>(p, s_wide, hs, s_id, s_order + pos0, share, add, n0, st);
+      }
     } else {
       for (int i = st; i < NT; i += LG_SIDE) s_id[i] = -1, s_order[i] = (int16_t)i;
     }
@@ -912,6 +1002,45 @@ __device__ __forceinline__ Item work_item(const Work& w, int i) {
   if (i < w.full) return Item{i, 0, w.slabs, -1, true};
   const int j = i - w.full, part = j % w.parts;
   return Item{w.full + j / w.parts, part * w.per, min(w.slabs, (part + 1) * w.per), j, part == 0};
+}
+
+// Adds the wide pieces of a group's tokens, lane l's tok (-1: none), all of adapter a, to
+// this lane's sums, v[j >> 4][j & 15] of token j and feature n.
+template <typename T>
+__device__ __forceinline__ void add_wide(const LoraParams& p, int a, int tok, int64_t n,
+                                         uint32_t (&v)[2][16]) {
+  const int R = (int)p.R;
+  uint4 flags = make_uint4(0, 0, 0, 0);  // of pieces, a byte each
+  if (tok >= 0) flags = __ldcg(reinterpret_cast<const uint4*>(p.wide + 4) + tok);
+  for (int r = 0; r < R; r += 8) {
+    const uint32_t word = r < 32 ? flags.x : (r < 64 ? flags.y : (r < 96 ? flags.z : flags.w));
+    const bool mine = tok >= 0 && ((word >> (r & 31)) & 0xFFu) != 0;
+    const uint32_t which = __ballot_sync(0xFFFFFFFFu, mine);
+    if (which == 0) continue;
+    float f[8] = {};
+    if (mine) {
+      for (int s = 0; s < p.shares; ++s) {
+        const float4* src = reinterpret_cast<const float4*>(p.h + (s * p.T + tok) * R + r);
+        const float4 u0 = __ldcg(src), u1 = __ldcg(src + 1);
+        f[0] += u0.x, f[1] += u0.y, f[2] += u0.z, f[3] += u0.w;
+        f[4] += u1.x, f[5] += u1.y, f[6] += u1.z, f[7] += u1.w;
+      }
+      const float scale = __ldg(p.scale + a);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] *= scale;
+    }
+    float b[8] = {};
+    if (n < p.N)
+      load_pack<T, 8>(static_cast<const T*>(p.b) + (a * p.N + n) * R + r).get(b);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {  // no branch a token: their chains overlap
+      const float before = __uint_as_float(v[j >> 4][j & 15]);
+      float sum = before;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = fmaf(b[e], __shfl_sync(0xFFFFFFFFu, f[e], j), sum);
+      v[j >> 4][j & 15] = __float_as_uint((which >> j) & 1u ? sum : before);
+    }
+  }
 }
 
 // A persistent pair of CTAs; CTA r of the pair has features [128 r, 128 r + 128)
@@ -1212,15 +1341,22 @@ __global__ void __launch_bounds__(LP_THREADS, 1)
 #pragma unroll
         for (int k = 0; k < U; ++k) {
           const float scale = t[k] >= 0 && s_row[t[k]] >= 0 ? __ldg(p.scale + s_row[t[k]]) : 0.0f;
-          const float2 f[4] = {make_float2(scale * u0[k].x, scale * u0[k].y),
-                               make_float2(scale * u0[k].z, scale * u0[k].w),
-                               make_float2(scale * u1[k].x, scale * u1[k].y),
-                               make_float2(scale * u1[k].z, scale * u1[k].w)};
+          float f[8] = {scale * u0[k].x, scale * u0[k].y, scale * u0[k].z, scale * u0[k].w,
+                        scale * u1[k].x, scale * u1[k].y, scale * u1[k].z, scale * u1[k].w};
+          if constexpr (std::is_same<T, __half>::value) {
+            const bool wide = wide_piece<T>(f);
+            if (t[k] >= 0 && s_tok[t[k]] >= 0 && r[k] < R) {
+              reinterpret_cast<uint8_t*>(p.wide + 4)[(int64_t)s_tok[t[k]] * 16 + r[k] / 8] = wide;
+              if (wide) *p.wide = 1;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = wide ? 0.0f : f[e];
+          }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            hi[k].set2(e, f[e]);
-            const float2 h = hi[k].get2(e);
-            low[k].set2(e, make_float2(f[e].x - h.x, f[e].y - h.y));
+            uint32_t h, l;
+            split_pair<T>(make_float2(f[2 * e], f[2 * e + 1]), h, l);
+            hi[k].set_word(e, h), low[k].set_word(e, l);
           }
         }
       };
@@ -1263,16 +1399,21 @@ __global__ void __launch_bounds__(LP_THREADS, 1)
     if (!waited) pdl_wait();
   } else {
     // -------------------------------------------------------------- epilogue
+    constexpr bool half = std::is_same<T, __half>::value;
     const int nl = (warp & 3) * 32 + lane;
     int ab = 0;
     uint32_t aphase = 0;
     for (int i = first; i < work.items; i += stride) {
-      if (!warp_wait(tfull0 + 8 * ab, aphase, abort_flag, p.status) || *abort_flag != 0) break;
-      fence_after();
       const Item item = work_item(work, i);
       const int u = item.unit;
       const int64_t n = (int64_t)(u % n_tiles) * LP_TILE + rank * LP_HALF + nl;
       const int64_t t0 = (int64_t)(u / n_tiles) * LP_TILE;
+      Runs runs{};
+      if (half && adapters && item.adapters) runs = tile_runs(p, t0, places, lane);
+      if (!warp_wait(tfull0 + 8 * ab, aphase, abort_flag, p.status) || *abort_flag != 0) break;
+      fence_after();
+      // the builders of both CTAs have set the flag before their tiles went into the MMAs
+      const bool wide = half && runs.starts != 0 && __ldcg(p.wide) != 0;
       const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(ab * LP_TILE);
       T* out = static_cast<T*>(p.out) + n;
       float* part = p.partials + item.piece * LP_PIECE + rank * (LP_TILE * LP_HALF) + nl;
@@ -1286,6 +1427,10 @@ __global__ void __launch_bounds__(LP_THREADS, 1)
         const int tok = mine < places ? (adapters ? p.order[mine] : (int)mine) : -1;
         tmem_wait16(v[0]);
         tmem_wait16(v[1]);
+        if constexpr (half) {
+          const int a = __shfl_sync(0xFFFFFFFFu, runs.adapter, c / RUN);
+          if (wide && a >= 0) add_wide<T>(p, a, tok, n, v);
+        }
         if (item.piece >= 0) {
 #pragma unroll
           for (int j = 0; j < 32; ++j)
@@ -1376,6 +1521,7 @@ struct LoraPlan {
   int64_t order_words;              // of the workspace: order and the sort's scratch
   int64_t copy_words;               // of the workspace: x in that order
   int64_t part_words;               // of the workspace: pieces of tiles (pair)
+  int64_t wide_words;               // of the workspace: which pieces of s h are wide (pair)
   int tok, tiles, shares, share_k, zs;  // shrink: tokens a block
   int nt, splits;                   // lora_split_kernel
 };
@@ -1394,6 +1540,7 @@ static LoraPlan lora_plan(int64_t T, int64_t K, int64_t N, int64_t S, int64_t R)
     q.order_words = (q.places + (int64_t)token_order_scratch(T, S) + 3) / 4 * 4;
     q.copy_words = (q.places * K / 2 + 3) / 4 * 4;
     q.part_words = sms / 2 * moe::LP_PIECE;
+    q.wide_words = 4 + 4 * T;
   }
   // Shrink: 64 tokens, from 129 on 128 (they read A_a once for twice the tokens, and
   // fill the tcgen05 tile: 512 tokens 56 us against 72, 256 37 against 43), as they come
@@ -1439,7 +1586,7 @@ static size_t lora_workspace(const LoraPlan& q, int64_t T, int64_t R) {
   int64_t rows = shrink_fill(q.tok, R) * (int64_t)num_sms() * q.tok;
   if (rows > 16 * T) rows = 16 * T;
   if (rows < T) rows = T;
-  return (size_t)((q.order_words + q.copy_words + q.part_words + rows * R) * 4);
+  return (size_t)((q.order_words + q.copy_words + q.part_words + q.wide_words + rows * R) * 4);
 }
 
 // Dynamic shared memory limit of a kernel, raised once per device.
@@ -1539,6 +1686,7 @@ static moe_status_t launch_lora(const moe_lora_args_t* a, const LoraPlan& q, Lor
       p.xs = static_cast<int32_t*>(a->workspace) + q.order_words;
       p.partials = static_cast<float*>(a->workspace) + q.order_words + q.copy_words;
       p.pairs = num_sms() / 2;
+      if (!bf16) p.wide = reinterpret_cast<uint32_t*>(p.partials + q.part_words);
       if (!make_map16(&b, bf16, a->lora_b, p.S * p.N, p.R, p.R, moe::LP_HALF) ||
           !make_map16(&xs, bf16, p.xs, q.places, p.K, p.K, moe::RUN))
         return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the adapters");
@@ -1635,7 +1783,8 @@ moe_status_t moe_lora_linear(const moe_lora_args_t* a, void* stream) {
   p.scale = a->lora_scale;
   p.out = a->out;
   p.out_stride = a->out_stride0;
-  p.h = static_cast<float*>(a->workspace) + q.order_words + q.copy_words + q.part_words;
+  p.h = static_cast<float*>(a->workspace) + q.order_words + q.copy_words + q.part_words +
+        q.wide_words;
   p.shares = q.shares;
   p.share_k = q.share_k;
   p.splits = q.splits;

@@ -288,3 +288,61 @@ def test_norm_router_and_projection_behind_one_another():
     a, b = chain(True), chain(False)
     for name in a:
         assert torch.equal(a[name], b[name]), name
+
+
+@pytest.mark.parametrize("T", [1, 3, 16, 40, 100, 200, 512, 700, 1500])
+@pytest.mark.parametrize("R", [8, 24, 72, 128])
+@pytest.mark.parametrize("how", ["large", "small", "all"])
+def test_fp16_products_beyond_its_range(T, R, how):
+    # s h about 2^17 with rows of B about 2^-10, about 2^-20 with B about 2^10, and both beside
+    # ordinary ones and zeros: the sums are ordinary numbers, their middle factor is not
+    p = problem(T, 512, 264, 5, R, "fp16")
+    up = torch.ones(5, device="cuda")
+    if how != "small":
+        up[[0, 3]] = 2.0 ** 17
+    if how != "large":
+        up[[1, 4]] = 2.0 ** -20
+    if how == "large":
+        up.fill_(2.0 ** 17)
+    p["lora_scale"] = p["lora_scale"] * up
+    # B back by 2^-10 or 2^10 (its own range); what is left is up to 2^7 or 2^-10
+    back = torch.where(up > 1, 2.0 ** -10, torch.where(up < 1, 2.0 ** 10, 1.0))
+    p["lora_b"] = (p["lora_b"].float() * back[:, None, None]).half()
+    if how == "small":
+        p["weight"] *= 2.0 ** -9  # so that the adapters' part is the larger one
+    if T > 2:
+        p["x"][T // 2] = 0.0
+    out = run(p)
+    ref, extra = expect(p)
+    assert_within(out, ref, rounded(ref, out.dtype, extra), "out")
+
+
+@pytest.mark.parametrize("T", [5, 200, 1100])
+def test_fp16_rows_with_pieces_of_every_size(T):
+    # ranks 0..7 overflow, 8..15 vanish, 16..23 are ordinary, 24..31 zero, within each row
+    p = problem(T, 512, 300, 3, 32, "fp16")
+    size = torch.tensor([2.0 ** 13, 2.0 ** -16, 1.0, 0.0], device="cuda").repeat_interleave(8)
+    p["lora_a"] = (p["lora_a"].float() * size[:, None]).half()
+    p["lora_b"] = (p["lora_b"].float() / size.clamp_min(2.0 ** -16) / 16).half()
+    p["lora_scale"] = p["lora_scale"] * 16
+    out = run(p)
+    ref, extra = expect(p)
+    assert_within(out, ref, rounded(ref, out.dtype, extra), "out")
+
+
+@pytest.mark.parametrize("T", [2, 70, 300, 1000])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_an_infinite_sum_stays_one(T, dtype):
+    # h infinite: out is that infinity with the sign of B's value, not NaN
+    p = problem(T, 256, 200, 3, 24, dtype)
+    p["adapter_ids"][0] = 1
+    p["x"][:, 7] = 0.5
+    p["lora_a"][1, 2, 7] = float("inf")
+    p["lora_b"][1, :, 2] = torch.where(p["lora_b"][1, :, 2] > 0, 1.0, -1.0).to(p["x"].dtype)
+    out = run(p)
+    mine = (p["adapter_ids"] == 1).cpu()
+    want = torch.where(p["lora_b"][1, :, 2] > 0, float("inf"), -float("inf")).cpu()
+    assert bool((out.cpu()[mine].float() == want).all())
+    q = dict(p, adapter_ids=torch.where(p["adapter_ids"] == 1, -1, p["adapter_ids"]))
+    ref, extra = expect(q)
+    assert_within(out[~mine.cuda()], ref[~mine], rounded(ref, out.dtype, extra)[~mine], "others")
