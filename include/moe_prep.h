@@ -79,7 +79,13 @@ typedef enum moe_weights_dtype { MOE_WEIGHTS_FP32 = 0, MOE_WEIGHTS_BF16 = 1 } mo
 typedef enum moe_activation { MOE_ACT_SILU = 0 } moe_activation_t;
 typedef enum moe_shared_dtype { MOE_SHARED_BF16 = 0, MOE_SHARED_FP8 = 1 } moe_shared_dtype_t;
 typedef enum moe_dtype { MOE_DTYPE_FP32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_FP16 = 2 } moe_dtype_t;
-typedef enum moe_scoring { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_scoring_t;
+typedef enum moe_scoring {
+  MOE_SCORE_SOFTMAX = 0,
+  MOE_SCORE_SIGMOID = 1,
+  /* OR-ed to SOFTMAX: moe_route's bias is added to the score, not to the logit (SIGMOID's always
+   * is).  Without a bias, and to the gradient, it says nothing. */
+  MOE_SCORE_BIAS_ON_SCORE = 4
+} moe_scoring_t;
 typedef enum moe_gate {
   MOE_GATE_NONE = 0,
   MOE_GATE_CHANNEL = 1, /* [K]: one factor per column */
@@ -430,9 +436,15 @@ moe_status_t moe_topk_reduce(const void* expert_out, int64_t num_experts,
 /* Top-k ids and weights of router logits l[t, e], in fp32.                  */
 /*   key[t, e] = l                     without a bias (both scorings are      */
 /*                                     monotone in the logit);                */
-/*               l + bias[e]           softmax with a bias;                   */
+/*               l + bias[e]           softmax with a bias (on the logit: a    */
+/*                                     bias trained for scores goes with the  */
+/*                                     next form);                            */
+/*               exp(l - m)/z + bias   SOFTMAX | BIAS_ON_SCORE with a bias, the */
+/*                                     sum z over all experts as below;        */
 /*               1/(1+exp(-l)) + bias  sigmoid with a bias.                   */
-/* An expert whose key is NaN or -inf is not selectable (a masked expert).   */
+/* An expert whose key is NaN or -inf is not selectable (a masked expert),    */
+/* with BIAS_ON_SCORE neither one whose logit is.  (A sigmoid's score of a    */
+/* logit of -inf is 0: with a bias such an expert is masked by the bias.)     */
 /* Groups (num_groups > 1; E % num_groups == 0): a group's value is its       */
 /* highest key, with a bias the sum of its two highest (a missing second     */
 /* counts 0); only experts of the top_groups best groups stay selectable.    */

@@ -25,7 +25,7 @@ MOE_ACT_SILU = 0
 MOE_SHARED_BF16, MOE_SHARED_FP8 = 0, 1
 MOE_STAGE_W13, MOE_STAGE_W2, MOE_STAGE_ALL = 1, 2, 3
 MOE_DTYPE_FP32, MOE_DTYPE_BF16, MOE_DTYPE_FP16 = 0, 1, 2
-MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID, MOE_SCORE_BIAS_ON_SCORE = 0, 1, 4
 MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_FULL = 0, 1, 2, 3
 MOE_DEV_CAPACITY, MOE_DEV_BAD_EXPERT, MOE_DEV_TIMEOUT, MOE_DEV_BAD_ADAPTER = 1, 2, 4, 8
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARGUMENT", 2: "MOE_ERR_SHAPE",
@@ -590,8 +590,10 @@ def moe_route(logits, topk_ids, topk_weights, bias=None, is_padding=None,
               stream=None):
     """Router: top-k ids (int32 or int64 [T, k]) and weights (fp32 [T, k]) of logits [T, E].
 
-    bias: fp32 [E], added for the selection alone; is_padding: uint8 [T]; num_groups,
-    top_groups: only the experts of the best groups are taken.  See include/moe_prep.h."""
+    bias: fp32 [E], added for the selection alone: to the score of MOE_SCORE_SIGMOID and of
+    MOE_SCORE_SOFTMAX | MOE_SCORE_BIAS_ON_SCORE, to the logit of MOE_SCORE_SOFTMAX by itself.
+    is_padding: uint8 [T]; num_groups, top_groups: only the experts of the best groups are taken.
+    See include/moe_prep.h."""
     T, E = logits.shape
     k = topk_ids.shape[1]
     dt, idt, tk = logits.dtype, topk_ids.dtype, (T, k)

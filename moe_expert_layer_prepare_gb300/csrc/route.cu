@@ -5,7 +5,8 @@
 // 32-bit integers of the keys.  Without a bias the key is the logit itself (softmax
 // and sigmoid are monotone), so the choice does not depend on how exp rounds.  With a
 // sigmoid and a bias the key is 1/(1+expf(-l)) + bias with IEEE division and no
-// contraction, the value that elementary fp32 tensor operations give.
+// contraction, the value that elementary fp32 tensor operations give.  With a softmax the
+// bias is on the logit, or, where the caller says so, on the score like the sigmoid's.
 //
 // Issue slots bound it, not memory.  Up to 256 experts each lane sorts its keys,
 // cut to make room for the expert's index in the low bits, and k rounds take the
@@ -32,6 +33,7 @@ struct RouteParams {
   const float* bias;
   const uint8_t* is_padding;
   int sigmoid, renorm;
+  int score_key;  // softmax with a bias: it is added to the score
   float scale;
   int groups, top_groups;
   void* ids;
@@ -253,7 +255,9 @@ __device__ __forceinline__ bool take_cut(const uint32_t (&key)[VPL], int k, int 
   return whole || !tie;
 }
 
-template <typename T, int VPL>
+// SCORE_KEY: softmax with the bias on the score, exp(l - m) / z + bias; an expert whose logit
+// is NaN or -inf is not selectable then, whatever its bias.
+template <typename T, int VPL, bool SCORE_KEY>
 __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(RouteParams p) {
   extern __shared__ uint32_t smem_keys[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -269,23 +273,43 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(RouteParams p) 
     const int e = i * 32 + lane;
     l[i] = e < p.E ? to_f32(row[e]) : -INFINITY;
   }
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = i * 32 + lane;
-    float v = l[i];
-    if (p.bias != nullptr && e < p.E) v = __fadd_rn(p.sigmoid ? sigmoid(v) : v, __ldg(p.bias + e));
-    key[i] = e < p.E ? order_key(v) : 0u;
-  }
   float m_all = -INFINITY, z_all = 0.0f;
-  if (!p.sigmoid && !p.renorm) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) top = max(top, p.bias == nullptr ? key[i] : order_key(l[i]));
+  // l becomes exp(l - m), m and z the row's
+  auto row_softmax = [&](uint32_t top) {
     m_all = warp_max_key(top);
     exp_row<VPL>(l, m_all);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) z_all += l[i];
     z_all = warp_sum(z_all);
+  };
+  if constexpr (SCORE_KEY) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      key[i] = order_key(l[i]);
+      top = max(top, key[i]);
+    }
+    row_softmax(top);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = i * 32 + lane;
+      if (key[i] != 0) key[i] = order_key(__fadd_rn(__fdiv_rn(l[i], z_all), __ldg(p.bias + e)));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = i * 32 + lane;
+      float v = l[i];
+      if (p.bias != nullptr && e < p.E)
+        v = __fadd_rn(p.sigmoid ? sigmoid(v) : v, __ldg(p.bias + e));
+      key[i] = e < p.E ? order_key(v) : 0u;
+    }
+    if (!p.sigmoid && !p.renorm) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) top = max(top, p.bias == nullptr ? key[i] : order_key(l[i]));
+      row_softmax(top);
+    }
   }
   if (p.groups > 1) limit_groups<VPL>(p, key, smem_keys + warp * p.E, lane);
   const bool padding = p.is_padding != nullptr && p.is_padding[t] != 0;
@@ -410,7 +434,9 @@ static moe_status_t launch_one(const RouteParams& p, bool backward, cudaStream_t
     return launched(launch_pdl(moe::route_backward_kernel<T, VPL>, grid, block, 0, s, p),
                     "route backward");
   const size_t smem = p.groups > 1 ? (size_t)moe::ROUTE_WARPS * p.E * 4 : 0;  // <= 32 KB
-  return launched(launch_pdl(moe::route_kernel<T, VPL>, grid, block, smem, s, p), "route");
+  if (p.score_key)
+    return launched(launch_pdl(moe::route_kernel<T, VPL, true>, grid, block, smem, s, p), "route");
+  return launched(launch_pdl(moe::route_kernel<T, VPL, false>, grid, block, smem, s, p), "route");
 }
 
 static moe_status_t launch_any(const RouteParams& p, int32_t dtype, bool backward,
@@ -436,7 +462,8 @@ static moe_status_t check_route(int64_t T, int64_t E, int64_t k, int32_t dtype, 
                                 int32_t ids_dtype) {
   if (T < 0 || E < 0 || k < 0) return set_error(MOE_ERR_INVALID_ARGUMENT, "negative size");
   if (!dtype_ok(dtype)) return set_error(MOE_ERR_INVALID_ARGUMENT, "bad logits_dtype %d", dtype);
-  if (scoring != MOE_SCORE_SOFTMAX && scoring != MOE_SCORE_SIGMOID)
+  const int32_t form = scoring & ~MOE_SCORE_BIAS_ON_SCORE;
+  if (form != MOE_SCORE_SOFTMAX && form != MOE_SCORE_SIGMOID)
     return set_error(MOE_ERR_INVALID_ARGUMENT, "bad scoring %d", scoring);
   if (ids_dtype != MOE_IDS_INT32 && ids_dtype != MOE_IDS_INT64)
     return set_error(MOE_ERR_INVALID_ARGUMENT, "bad topk_ids_dtype");
@@ -477,8 +504,9 @@ moe_status_t moe_route(const moe_route_args_t* a, void* stream) {
   p.stride0 = a->logits_stride0;
   p.bias = a->bias;
   p.is_padding = a->is_padding;
-  p.sigmoid = a->scoring == MOE_SCORE_SIGMOID;
+  p.sigmoid = (a->scoring & ~MOE_SCORE_BIAS_ON_SCORE) == MOE_SCORE_SIGMOID;
   p.renorm = a->renormalize != 0;
+  p.score_key = !p.sigmoid && p.bias != nullptr && (a->scoring & MOE_SCORE_BIAS_ON_SCORE) != 0;
   p.scale = a->scale;
   p.groups = (int)a->num_groups;
   p.top_groups = (int)a->top_groups;
@@ -506,7 +534,7 @@ moe_status_t moe_route_backward(const moe_route_backward_args_t* a, void* stream
   p.k = (int)a->top_k;
   p.logits = a->logits;
   p.stride0 = a->logits_stride0;
-  p.sigmoid = a->scoring == MOE_SCORE_SIGMOID;
+  p.sigmoid = (a->scoring & ~MOE_SCORE_BIAS_ON_SCORE) == MOE_SCORE_SIGMOID;
   p.renorm = a->renormalize != 0;
   p.scale = a->scale;
   p.groups = p.top_groups = 1;

@@ -249,3 +249,89 @@ def test_groups_whose_best_two_keys_add_up_to_minus_infinity(E, groups, scoring)
         want = select(key.numpy(), bias.numpy(), "softmax", 6, groups, 2)
     assert np.array_equal(ids.cpu().numpy(), want)
     assert bool(torch.isfinite(w).all())
+
+
+def chosen64(l, bias, k, groups, top_groups, apart):
+    """Experts by softmax(l) + bias in 64 bits, and the rows where no two keys (or groups' values)
+    that decide are closer than `apart` times the row's largest score or key."""
+    l, bias = l.double().numpy(), bias.double().numpy()
+    T, E = l.shape
+    ids, clear = np.full((T, k), -1, np.int64), np.ones(T, bool)
+    for t in range(T):
+        ok = [e for e in range(E) if l[t, e] > -np.inf]
+        if not ok:
+            continue
+        ex = {e: np.exp(l[t, e] - max(l[t, i] for i in ok)) for e in ok}
+        z = sum(ex.values())
+        key = {e: ex[e] / z + bias[e] for e in ok if bias[e] > -np.inf}
+        least = apart * max([1 / z] + [abs(v) for v in key.values()])
+        if groups > 1:
+            value = {}
+            for e, v in key.items():
+                value.setdefault(e * groups // E, []).append(v)
+            value = {g: sum(sorted(v)[-2:]) for g, v in value.items()}
+            rank = sorted(value, key=lambda g: (-value[g], g))
+            if len(rank) > top_groups:
+                clear[t] &= value[rank[top_groups - 1]] - value[rank[top_groups]] > least
+            key = {e: v for e, v in key.items() if e * groups // E in rank[:top_groups]}
+        rank = sorted(key, key=lambda e: (-key[e], e))
+        ids[t, :min(k, len(rank))] = rank[:k]
+        clear[t] &= all(key[a] - key[b] > least for a, b in zip(rank[:k], rank[1:k + 1]))
+    return ids, clear
+
+
+@pytest.mark.parametrize("E,groups,top_groups,k", [(1, 1, 1, 1), (8, 1, 1, 2), (40, 5, 2, 8),
+                                                   (256, 1, 1, 8), (256, 8, 4, 8), (60, 3, 2, 6),
+                                                   (1000, 1, 1, 32)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_softmax_with_a_bias_on_the_score(E, groups, top_groups, k, dtype, renorm):
+    T = 60
+    g = torch.Generator().manual_seed(E + groups)
+    l = (torch.randn(T, E, generator=g) * 2).to(DTYPES[dtype])
+    bias = torch.randn(E, generator=g) * 0.03
+    if E > 8:
+        l[:, 3] = -float("inf")
+        l[1::7, 5] = float("nan")
+        l[2, :] = -float("inf")
+        l[3, 8:] = -float("inf")
+        bias[3] = 5.0  # a masked expert stays masked
+        bias[7] = -float("inf")
+    ids = torch.full((T, k), 77, dtype=torch.int32, device="cuda")
+    w = torch.full((T, k), 77.0, device="cuda")
+    scoring = B.MOE_SCORE_SOFTMAX | B.MOE_SCORE_BIAS_ON_SCORE
+    B.moe_route(l.cuda(), ids, w, bias=bias.cuda(), scoring=scoring, renormalize=renorm, scale=1.5,
+                num_groups=groups, top_groups=top_groups)
+    # a score's fp32 error: E / 32 + 5 sums after one another, exp, quotient, sum with the bias
+    # (twice for a group), in units of 2^-24; two keys are compared
+    want, clear = chosen64(l.float(), bias, k, groups, top_groups, 4 * (E / 32 + 16) * 2.0 ** -24)
+    assert clear.sum() > T // 2
+    assert np.array_equal(ids.cpu().numpy()[clear], want[clear])
+    l64 = l.double()
+    l64 = torch.where(torch.isnan(l64), torch.full_like(l64, -float("inf")), l64)
+    at = ids.cpu().long()
+    ref = weights64(l64, at, "softmax", renorm, 1.5)
+    assert_within(w, ref, ref.abs() * (E + 16) * 2.0 ** -24 + 1e-30, "weights")
+    # the gradient is the softmax's
+    dw = torch.randn(T, k, generator=g).cuda()
+    a, b = (torch.empty(T, E, dtype=l.dtype, device="cuda") for _ in range(2))
+    B.moe_route_backward(l.cuda(), ids, dw, a, scoring=scoring, renormalize=renorm)
+    B.moe_route_backward(l.cuda(), ids, dw, b, scoring=B.MOE_SCORE_SOFTMAX, renormalize=renorm)
+    assert torch.equal(a, b)
+
+
+def test_bias_on_the_score_where_it_says_nothing():
+    g = torch.Generator().manual_seed(2)
+    l, bias = torch.randn(30, 64, generator=g).cuda(), torch.randn(64, generator=g).cuda()
+    for form, b in ((B.MOE_SCORE_SOFTMAX, None), (B.MOE_SCORE_SIGMOID, None),
+                    (B.MOE_SCORE_SIGMOID, bias)):
+        got = []
+        for scoring in (form, form | B.MOE_SCORE_BIAS_ON_SCORE):
+            ids = torch.empty(30, 4, dtype=torch.int32, device="cuda")
+            w = torch.empty(30, 4, device="cuda")
+            B.moe_route(l, ids, w, bias=b, scoring=scoring)
+            got.append((ids, w))
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    for scoring in (2, 3, 6, 7, 8, -1):
+        with pytest.raises(B.MoeError):
+            B.moe_route(l, ids, w, scoring=scoring)
