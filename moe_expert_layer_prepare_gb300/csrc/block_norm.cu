@@ -295,8 +295,6 @@ namespace moe_host {
 
 using moe::NormParams;
 
-constexpr size_t kThirdBlockSmem = 75 * 1024;  // dynamic, of a block with two more beside it
-
 // Shared memory of a row block: the stages and the [K] tensors.
 static size_t rows_smem(const NormParams& p, size_t elem, int stages) {
   const int arrays = 1 + (p.z != nullptr) + (p.gate_kind == MOE_GATE_FULL);
@@ -305,11 +303,16 @@ static size_t rows_smem(const NormParams& p, size_t elem, int stages) {
   return (size_t)p.K * (stages * arrays * elem + weights * dtype_size(p.w_dtype));
 }
 
+template <typename T, int NV, int STAGES>
+static int rows_resident(const NormParams& p, int threads) {
+  return resident_with<moe::block_norm_rows_kernel<T, NV, STAGES>>(threads,
+                                                                   rows_smem(p, sizeof(T), STAGES));
+}
+
 template <typename T, int NV, int STAGES = 2>
 static moe_status_t launch_rows(const NormParams& p, int threads, cudaStream_t s) {
   const size_t smem = rows_smem(p, sizeof(T), STAGES);
-  const int64_t cap =
-      (int64_t)num_sms() * resident_with<moe::block_norm_rows_kernel<T, NV, STAGES>>(threads, smem);
+  const int64_t cap = (int64_t)num_sms() * rows_resident<T, NV, STAGES>(p, threads);
   if (cap == 0) return set_error(MOE_ERR_CUDA, "block norm: no resident block");
   return launched(launch_pdl(moe::block_norm_rows_kernel<T, NV, STAGES>,
                              dim3((unsigned)(p.T < cap ? p.T : cap)), dim3(threads), smem, s, p),
@@ -395,13 +398,21 @@ moe_status_t moe_block_norm(const moe_block_norm_args_t* a, void* stream) {
     // One pack a thread up to 512, in two stages (8192 x 4096 full gate: 52 us; two
     // packs a thread: 56; one stage and a third block: 55).  Above, two packs and, where
     // three blocks fit, one stage: 8192 x 7168 73 us against 90 with two stages and two
-    // blocks, 8192 x 8192 88 against 91.  Longer rows: two stages (1000 x 16384: 24 us, one
-    // stage: 46), the sums' barriers being rarer there.
+    // blocks, 8192 x 8192 88 against 91.  Where one stage fits twice and two stages do not,
+    // one with 16-bit weights (full gate, 8192 x 7680: 97 us, two: 102; x 7672: 105 and
+    // 116), two with fp32 ones (channel gate, 8192 x 6144: 88 us, one: 99; full gate, 1000 x
+    // 8192: 20 and 23).  Where both fit twice, two (channel gate, 8192 x 7680: 78 us, one:
+    // 93).  Longer rows: two stages (1000 x 16384: 24 us, one stage: 46), the sums' barriers
+    // being rarer there.
     if (w.ok && rows_smem(p, sizeof(E), 2) <= kMaxBlockSmem) {
       if (packs <= 512) return launch_rows<E, 1>(p, threads(1), s);
-      if (packs <= 1024 && rows_smem(p, sizeof(E), 1) <= kThirdBlockSmem)
-        return launch_rows<E, 2, 1>(p, threads(2), s);
-      if (packs <= 1024) return launch_rows<E, 2>(p, threads(2), s);
+      if (packs <= 1024) {
+        const int one = rows_resident<E, 2, 1>(p, threads(2));
+        if (one >= 3 ||
+            (one > rows_resident<E, 2, 2>(p, threads(2)) && p.w_dtype != MOE_DTYPE_FP32))
+          return launch_rows<E, 2, 1>(p, threads(2), s);
+        return launch_rows<E, 2>(p, threads(2), s);
+      }
       if (packs <= 2048) return launch_rows<E, 4>(p, threads(4), s);
       return launch_rows<E, 8>(p, threads(8), s);
     }

@@ -349,3 +349,11 @@ def test_no_columns():
     B.moe_block_norm(x, z=x, post_weight=w, pre_weight=w, x_out=x, y=x)
     B.moe_block_norm_backward(x, z=x, post_weight=w, pre_weight=w, d_x=x, d_z=x, d_y=x,
                               d_post_weight=w, d_pre_weight=w)
+
+
+# rows of two packs a thread, in each case of how many blocks one or two stages leave an SM
+@pytest.mark.parametrize("K,wdtype", [(6144, "fp32"), (7168, "bf16"), (7672, "bf16"),
+                                      (7680, "bf16"), (8192, "bf16"), (8192, "fp32")])
+@pytest.mark.parametrize("gate", ["none", "channel", "full"])
+def test_stages_of_long_rows(K, wdtype, gate):
+    check(503, K, "bf16", wdtype, gate)
