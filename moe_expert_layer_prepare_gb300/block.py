@@ -20,7 +20,9 @@ class MoeBlock:
          shared_gate_up [2 Ns, K], shared_down [K, Ns]
          adapters: dict(gate_up_a [S, R, K], gate_up_b [S, 2 Ns, R], down_a [S, R, Ns],
                         down_b [S, K, R], scale fp32 [S]), or None
-    T is the most tokens of a call."""
+    T is the most tokens of a call.  The logits are the router's projection in bf16, as the
+    projection rounds its output, and the experts are taken by them; moe_route takes fp32 logits
+    too, from a caller who computes them."""
 
     def __init__(self, T, K, N, E, top_k, M_max, weights, num_groups=1, top_groups=1,
                  scoring=B.MOE_SCORE_SIGMOID, route_scale=1.0, eps=1e-6, device="cuda"):

@@ -93,3 +93,73 @@ def test_example_runs_and_learns(ex, capsys):
     ex.serve()
     losses = ex.train()
     assert losses[-1] < 0.2 * losses[0]
+
+
+def test_served_block_in_a_cuda_graph(ex):
+    K, S = 512, 5
+    b = ex.make_block(700, K, 256, 16, 4, 384, S, 16, seed=7)
+    for T in (1, 64, 600):
+        g = torch.Generator(device="cuda").manual_seed(T)
+
+        def inputs():
+            return (torch.randn(T, K, generator=g, device="cuda").bfloat16(),
+                    torch.randn(T, K, generator=g, device="cuda").bfloat16(),
+                    torch.randint(-1, S, (T,), generator=g, device="cuda", dtype=torch.int32))
+
+        x, z, ids = inputs()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):  # the first call on a stream, before the capture
+            b.forward(x, z, adapter_ids=ids)
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            res, out = b.forward(x, z, adapter_ids=ids)
+        for _ in range(2):
+            for t, new in zip((x, z, ids), inputs()):
+                t.copy_(new)
+            graph.replay()
+            got = res.clone(), out.clone()
+            want = b.forward(x, z, adapter_ids=ids)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert int(b.status.item()) == 0 and int(b.experts.status.item()) == 0
+
+
+def test_training_calls_in_a_cuda_graph(ex):
+    T, K, E, k = 300, 256, 8, 2
+    g = torch.Generator(device="cuda").manual_seed(1)
+
+    def rnd(*shape):
+        return torch.randn(shape, generator=g, device="cuda")
+
+    logits, x, rows, d_out, pre = rnd(T, E), rnd(T, K), rnd(T * k, K), rnd(T, K), rnd(K)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ids, w = torch.empty(T, k, **i32), rnd(T, k)
+    off, rr, ro = torch.empty(E + 1, **i32), torch.empty(T, k, **i32), torch.empty(T * k, **i32)
+    sorted_rows, out, d_rows, d_w = rnd(T * k, K), rnd(T, K), rnd(T * k, K), rnd(T, k)
+    y, rx, d_x, d_pre, d_logits = rnd(T, K), rnd(T), rnd(T, K), rnd(K), rnd(T, E)
+    ws = torch.empty(B.block_norm_workspace_size(T, K), dtype=torch.uint8, device="cuda")
+
+    def step():
+        B.moe_block_norm(x, pre_weight=pre, y=y, rstd_pre=rx)
+        B.moe_route(logits, ids, w)
+        B.moe_sort_routes(ids, off, rr, ro)
+        B.moe_permute(y, rr, off, sorted_rows)
+        B.moe_unpermute(rows, rr, w, out)
+        B.moe_unpermute_backward(d_out, rows, rr, w, off, d_rows, d_w)
+        B.moe_route_backward(logits, ids, d_w, d_logits)
+        B.moe_permute_backward(d_rows, rr, d_x)
+        B.moe_block_norm_backward(x, pre_weight=pre, rstd_pre=rx, d_y=d_out, d_x=d_x,
+                                  d_pre_weight=d_pre, workspace=ws)
+        return [t.clone() for t in (ids, w, rr, sorted_rows, out, d_rows, d_w, d_logits, d_x, d_pre)]
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for t in (logits, x, rows, d_out):
+        t.copy_(rnd(*t.shape))
+    graph.replay()
+    for a, b in zip(got, step()):
+        assert torch.equal(a, b)
