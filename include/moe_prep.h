@@ -50,6 +50,8 @@
 extern "C" {
 #endif
 
+/* Changes with an existing signature, structure or result; entry points that are added keep it
+ * and are found by their names. */
 #define MOE_PREP_ABI_VERSION 3
 
 typedef enum moe_status {
