@@ -346,3 +346,30 @@ def test_an_infinite_sum_stays_one(T, dtype):
     q = dict(p, adapter_ids=torch.where(p["adapter_ids"] == 1, -1, p["adapter_ids"]))
     ref, extra = expect(q)
     assert_within(out[~mine.cuda()], ref[~mine], rounded(ref, out.dtype, extra)[~mine], "others")
+
+
+@pytest.mark.parametrize("T,K,N,R", [(600, 64, 2000, 8), (2100, 128, 1100, 64), (1500, 2048, 512, 128)])
+def test_fp16_wide_and_ordinary_batches_in_turn(T, K, N, R):
+    # one workspace, calls right behind one another: what one batch found wide is not the next one's
+    ps = []
+    for seed, up in ((1, 1.0), (2, 2.0 ** 17), (3, 1.0), (4, 2.0 ** -18)):
+        p = problem(T, K, N, 7, R, "fp16", seed=seed)
+        p["lora_scale"][::2] *= up
+        p["lora_b"][::2] = (p["lora_b"][::2].float() / up ** 0.5).half()
+        ps.append(p)
+    ws = torch.empty(B.lora_workspace_size(T, K, N, 7, R), dtype=torch.uint8, device="cuda")
+    first = []
+    for p in ps:
+        ws.fill_(0xFF)
+        B.moe_lora_linear(workspace=ws, **p)
+        ref, extra = expect(p)
+        assert_within(p["out"], ref, rounded(ref, p["out"].dtype, extra), "out")
+        first.append(p["out"].clone())
+    differs = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(60):
+        for p in ps:
+            B.moe_lora_linear(workspace=ws, **p)
+        for p, f in zip(ps, first):
+            differs += (p["out"] != f).sum()
+            p["out"].zero_()
+    assert differs.item() == 0
