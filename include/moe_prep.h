@@ -23,6 +23,8 @@
  *   moe_block_norm       the RMS norm after a block with its gate, residual
  *                        scale and residual sum, and the norm before the next
  *                        block, in one pass (and its gradient).
+ *   moe_norm_quant       the norm before a block with its output in 8 bits, as
+ *                        the experts take it.
  *   moe_lora_linear      a projection shared by all tokens plus each token's
  *                        own low-rank adapter.
  *
@@ -78,7 +80,11 @@ typedef enum moe_sf_mode {
 
 typedef enum moe_ids_dtype { MOE_IDS_INT32 = 0, MOE_IDS_INT64 = 1 } moe_ids_dtype_t;
 typedef enum moe_weights_dtype { MOE_WEIGHTS_FP32 = 0, MOE_WEIGHTS_BF16 = 1 } moe_weights_dtype_t;
-typedef enum moe_activation { MOE_ACT_SILU = 0 } moe_activation_t;
+typedef enum moe_activation {
+  MOE_ACT_SILU = 0,
+  MOE_ACT_GELU_TANH = 1, /* 0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) */
+  MOE_ACT_NONE = 2       /* moe_w4_linear: no gate */
+} moe_activation_t;
 typedef enum moe_shared_dtype { MOE_SHARED_BF16 = 0, MOE_SHARED_FP8 = 1 } moe_shared_dtype_t;
 typedef enum moe_dtype { MOE_DTYPE_FP32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_FP16 = 2 } moe_dtype_t;
 typedef enum moe_scoring {
@@ -725,6 +731,50 @@ moe_status_t moe_lora_linear(const moe_lora_args_t* args, void* stream);
 
 size_t moe_lora_workspace_size(int64_t num_tokens, int64_t in_features, int64_t out_features,
                                int64_t num_adapters, int64_t rank);
+
+/* ------------------------------------------------------------------------ */
+/* moe_norm_quant                                                            */
+/*                                                                           */
+/* The norm before a block with its output in 8 bits.  In fp32, per token:    */
+/*   x_out = x + z                                (no z: x_out is x)          */
+/*   y = x_out * rstd * (weight + weight_offset),                             */
+/*       rstd = 1 / sqrt(mean(x_out^2) + eps)                                 */
+/*   q = e4m3_rn_satfinite(y * (1 / qs)), qs of each 1x128 group of y by the   */
+/*       recipe of moe_prepare_inputs (sf_mode UE8M0_PACKED or FP32).         */
+/* x_out and y (nullable) are rounded once each; y comes from the unrounded   */
+/* x_out and q from the unrounded y.  A last group of K % 128 columns has a    */
+/* scale of its own; of packed exponents the last word is filled up with      */
+/* zero bytes.  q [T, K] and q_sf (int32 [T, ceil(G/4)] or fp32 [T, G], G =    */
+/* ceil(K/128)) are what moe_batched_experts takes as hidden and a_scale.     */
+/* x_out may be x or z itself.  x, z, x_out and y have one dtype; rows have   */
+/* inner stride 1 and a stride of their own; weight is [K] of weight_dtype.   */
+/* rstd: nullable fp32 [T].  The gradient, with the rounding to 8 bits passed  */
+/* straight through, is moe_block_norm_backward's (scale 1, no gate, no       */
+/* post_weight, this weight as pre_weight, rstd as rstd_pre).                 */
+/* Errors: K > 16384 -> UNSUPPORTED.                                          */
+/* ------------------------------------------------------------------------ */
+typedef struct moe_norm_quant_args {
+  int64_t num_tokens, hidden_size;
+  int32_t dtype, weight_dtype; /* MOE_DTYPE_* */
+  const void* x;
+  int64_t x_stride0;
+  const void* z; /* nullable */
+  int64_t z_stride0;
+  const void* weight; /* [K] */
+  float weight_offset, eps;
+  void* x_out; /* iff z */
+  int64_t x_out_stride0;
+  void* y; /* nullable */
+  int64_t y_stride0;
+  void* q; /* fp8 [T, K] */
+  int64_t q_stride0;
+  void* q_sf;
+  int32_t sf_mode; /* MOE_SF_UE8M0_PACKED or MOE_SF_FP32 */
+  int64_t q_sf_stride0;
+  float* rstd; /* nullable [T] */
+} moe_norm_quant_args_t;
+
+moe_status_t moe_norm_quant(const moe_norm_quant_args_t* args, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Utilities                                                                 */

@@ -21,7 +21,7 @@ MOE_OK = 0
 MOE_SF_NONE, MOE_SF_UE8M0_PACKED, MOE_SF_FP32 = 0, 1, 2
 MOE_IDS_INT32, MOE_IDS_INT64 = 0, 1
 MOE_WEIGHTS_FP32, MOE_WEIGHTS_BF16 = 0, 1
-MOE_ACT_SILU = 0
+MOE_ACT_SILU, MOE_ACT_GELU_TANH, MOE_ACT_NONE = 0, 1, 2
 MOE_SHARED_BF16, MOE_SHARED_FP8 = 0, 1
 MOE_STAGE_W13, MOE_STAGE_W2, MOE_STAGE_ALL = 1, 2, 3
 MOE_DTYPE_FP32, MOE_DTYPE_BF16, MOE_DTYPE_FP16 = 0, 1, 2
@@ -215,6 +215,17 @@ class LoraArgs(ctypes.Structure):
     ]
 
 
+@_packer
+class NormQuantArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", _i64), ("hidden_size", _i64), ("dtype", _i32), ("weight_dtype", _i32),
+        ("x", _vp), ("x_stride0", _i64), ("z", _vp), ("z_stride0", _i64), ("weight", _vp),
+        ("weight_offset", _f32), ("eps", _f32), ("x_out", _vp), ("x_out_stride0", _i64),
+        ("y", _vp), ("y_stride0", _i64), ("q", _vp), ("q_stride0", _i64), ("q_sf", _vp),
+        ("sf_mode", _i32), ("q_sf_stride0", _i64), ("rstd", _vp),
+    ]
+
+
 _lib = None
 
 
@@ -250,7 +261,7 @@ def configure(lib):
                                     _vp]
     for name in ("moe_route", "moe_route_backward", "moe_sort_routes", "moe_permute",
                  "moe_unpermute", "moe_unpermute_backward", "moe_block_norm",
-                 "moe_block_norm_backward", "moe_lora_linear"):
+                 "moe_block_norm_backward", "moe_lora_linear", "moe_norm_quant"):
         getattr(lib, name).restype = ctypes.c_int
         getattr(lib, name).argtypes = [_vp, _vp]  # the packed struct's bytes, the stream
     for name, n in (("moe_sort_workspace_size", 3), ("moe_block_norm_workspace_size", 2),
@@ -578,6 +589,14 @@ def _flat(name, t, shape, dtype):
     return t.data_ptr()
 
 
+def _here(**tensors):
+    """Every tensor on the current device, whose stream a call goes to."""
+    dev = _current_device()
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name}: on {t.device}, and the current device is cuda:{dev}")
+
+
 def _code(name, dtype, table=_DTYPE):
     d = table.get(dtype)
     if d is None:
@@ -795,6 +814,30 @@ def moe_lora_linear(x, weight, lora_a, lora_b, adapter_ids, lora_scale, out, wor
         _flat("lora_scale", lora_scale, (S,), _FP32), out.data_ptr(),
         _rows("out", out, (T, N), dt), _at(workspace), _bytes(workspace), _at(device_status)),
         stream)
+
+
+def moe_norm_quant(x, weight, q, q_sf, z=None, x_out=None, y=None, rstd=None, weight_offset=0.0,
+                   eps=1e-6, stream=None):
+    """x_out = x + z and rmsnorm(x_out, weight) in 8 bits, its 1x128 groups scaled as by
+    ``moe_prepare_inputs``.
+
+    x, z, x_out, y: [T, K] of one type (fp32, bf16 or fp16); weight: [K] (any of them); q: uint8
+    [T, K]; q_sf: packed UE8M0 exponents, int32 [T, ceil(G / 4)], or scales, fp32 [T, G], of the
+    G = ceil(K / 128) groups; y: the norm's output in x's type as well; rstd: fp32 [T], what
+    ``moe_block_norm_backward`` takes as rstd_pre.  See include/moe_prep.h."""
+    T, K = shape = x.shape
+    dt, wdt, sdt = x.dtype, weight.dtype, q_sf.dtype
+    G = (K + 127) // 128
+    mode = MOE_SF_FP32 if sdt is _FP32 else MOE_SF_UE8M0_PACKED
+    _here(x=x, weight=weight, q=q, q_sf=q_sf, z=z, x_out=x_out, y=y, rstd=rstd)
+    _call("moe_norm_quant", NormQuantArgs.pack(
+        T, K, _code("x", dt), _code("weight", wdt), x.data_ptr(), _rows("x", x, shape, dt),
+        _at(z), _rows("z", z, shape, dt), _flat("weight", weight, (K,), wdt), weight_offset, eps,
+        _at(x_out), _rows("x_out", x_out, shape, dt), _at(y), _rows("y", y, shape, dt),
+        q.data_ptr(), _rows("q", q, shape, torch.uint8), q_sf.data_ptr(), mode,
+        _rows("q_sf", q_sf, (T, G), _FP32) if mode == MOE_SF_FP32 else
+        _rows("q_sf", q_sf, (T, (G + 3) // 4), _INT32),
+        _flat("rstd", rstd, (T,), _FP32)), stream)
 
 
 class MoeLayer:
