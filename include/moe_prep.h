@@ -27,6 +27,8 @@
  *                        the experts take it.
  *   moe_lora_linear      a projection shared by all tokens plus each token's
  *                        own low-rank adapter.
+ *   moe_gated_linear     gate and up projections with the activation and the
+ *                        product in one kernel (and its gradients).
  *
  * Conventions shared by every call
  *   - All tensor pointers are DEVICE pointers unless stated otherwise; every
@@ -775,6 +777,72 @@ typedef struct moe_norm_quant_args {
 } moe_norm_quant_args_t;
 
 moe_status_t moe_norm_quant(const moe_norm_quant_args_t* args, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* moe_gated_linear                                                          */
+/*                                                                           */
+/* The first half of a gated feed-forward block (a shared expert's):          */
+/*   g = x Wg^T, u = x Wu^T, out = act(g) * u,                                 */
+/* with Wg rows [0, N) and Wu rows [N, 2N) of weight.  Sums, g, u and the      */
+/* product are in fp32; out is rounded once.  gate_up (nullable) gets g in     */
+/* columns [0, N) and u in [N, 2N), rounded once each, for the gradient.       */
+/* x [T, K], out [T, N] and gate_up [T, 2N]: inner stride 1, row strides of     */
+/* their own; weight [2N, K] contiguous; bf16 or fp16.  activation:            */
+/* MOE_ACT_SILU or MOE_ACT_GELU_TANH.                                         */
+/*                                                                           */
+/* moe_gated_linear_backward: from d_out [T, N], the forward's x and weight and */
+/* the gate_up that it wrote,                                                */
+/*   d_g = d_out * u * act'(g), d_u = d_out * act(g),                          */
+/*   d_x = d_g Wg + d_u Wu, d_weight = [d_g d_u]^T x  (either may be NULL);     */
+/* d_g and d_u enter the products rounded to the tensors' type, sums are in    */
+/* fp32 in a fixed order, results rounded once.  d_x [T, K] has a row stride   */
+/* of its own, d_weight [2N, K] is contiguous.  Without tokens d_weight is     */
+/* zeros; tensors with a row a token may then be NULL.  workspace:             */
+/* moe_gated_linear_workspace_size() bytes, 16-byte aligned, need not be        */
+/* cleared; it serves fewer tokens as well.                                   */
+/* Errors: K % 8, x_stride0 % 8 != 0, x or weight not 16-byte aligned ->       */
+/* ALIGNMENT; fp32, MOE_ACT_NONE -> UNSUPPORTED.  A GEMM wait that ran out      */
+/* sets MOE_DEV_TIMEOUT.                                                      */
+/* ------------------------------------------------------------------------ */
+typedef struct moe_gated_linear_args {
+  int64_t num_tokens, in_features, out_features; /* T, K, N */
+  int32_t dtype;                                 /* MOE_DTYPE_BF16 or MOE_DTYPE_FP16 */
+  int32_t activation;                            /* MOE_ACT_* */
+  const void* x;
+  int64_t x_stride0;
+  const void* weight; /* [2N, K] */
+  void* out;
+  int64_t out_stride0;
+  void* gate_up; /* nullable */
+  int64_t gate_up_stride0;
+  uint32_t* device_status;
+} moe_gated_linear_args_t;
+
+moe_status_t moe_gated_linear(const moe_gated_linear_args_t* args, void* stream);
+
+typedef struct moe_gated_linear_backward_args {
+  int64_t num_tokens, in_features, out_features;
+  int32_t dtype;
+  int32_t activation;
+  const void* d_out;
+  int64_t d_out_stride0;
+  const void* x;
+  int64_t x_stride0;
+  const void* weight;
+  const void* gate_up;
+  int64_t gate_up_stride0;
+  void* d_x; /* nullable */
+  int64_t d_x_stride0;
+  void* d_weight; /* nullable [2N, K] */
+  void* workspace;
+  size_t workspace_bytes;
+  uint32_t* device_status;
+} moe_gated_linear_backward_args_t;
+
+moe_status_t moe_gated_linear_backward(const moe_gated_linear_backward_args_t* args, void* stream);
+
+size_t moe_gated_linear_workspace_size(int64_t num_tokens, int64_t in_features,
+                                       int64_t out_features);
 
 /* ------------------------------------------------------------------------ */
 /* Utilities                                                                 */

@@ -226,6 +226,27 @@ class NormQuantArgs(ctypes.Structure):
     ]
 
 
+@_packer
+class GatedLinearArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", _i64), ("in_features", _i64), ("out_features", _i64), ("dtype", _i32),
+        ("activation", _i32), ("x", _vp), ("x_stride0", _i64), ("weight", _vp), ("out", _vp),
+        ("out_stride0", _i64), ("gate_up", _vp), ("gate_up_stride0", _i64),
+        ("device_status", _vp),
+    ]
+
+
+@_packer
+class GatedLinearBackwardArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", _i64), ("in_features", _i64), ("out_features", _i64), ("dtype", _i32),
+        ("activation", _i32), ("d_out", _vp), ("d_out_stride0", _i64), ("x", _vp),
+        ("x_stride0", _i64), ("weight", _vp), ("gate_up", _vp), ("gate_up_stride0", _i64),
+        ("d_x", _vp), ("d_x_stride0", _i64), ("d_weight", _vp), ("workspace", _vp),
+        ("workspace_bytes", _sz), ("device_status", _vp),
+    ]
+
+
 _lib = None
 
 
@@ -261,11 +282,12 @@ def configure(lib):
                                     _vp]
     for name in ("moe_route", "moe_route_backward", "moe_sort_routes", "moe_permute",
                  "moe_unpermute", "moe_unpermute_backward", "moe_block_norm",
-                 "moe_block_norm_backward", "moe_lora_linear", "moe_norm_quant"):
+                 "moe_block_norm_backward", "moe_lora_linear", "moe_norm_quant",
+                 "moe_gated_linear", "moe_gated_linear_backward"):
         getattr(lib, name).restype = ctypes.c_int
         getattr(lib, name).argtypes = [_vp, _vp]  # the packed struct's bytes, the stream
     for name, n in (("moe_sort_workspace_size", 3), ("moe_block_norm_workspace_size", 2),
-                    ("moe_lora_workspace_size", 5)):
+                    ("moe_lora_workspace_size", 5), ("moe_gated_linear_workspace_size", 3)):
         getattr(lib, name).restype = _sz
         getattr(lib, name).argtypes = [_i64] * n
     return lib
@@ -838,6 +860,51 @@ def moe_norm_quant(x, weight, q, q_sf, z=None, x_out=None, y=None, rstd=None, we
         _rows("q_sf", q_sf, (T, G), _FP32) if mode == MOE_SF_FP32 else
         _rows("q_sf", q_sf, (T, (G + 3) // 4), _INT32),
         _flat("rstd", rstd, (T,), _FP32)), stream)
+
+
+def moe_gated_linear(x, weight, out, activation=MOE_ACT_SILU, gate_up=None, device_status=None,
+                     stream=None):
+    """out = act(x Wg^T) * (x Wu^T), Wg and Wu the first and the second half of weight's rows.
+
+    x [T, K], weight [2 N, K], out [T, N] of one type (bf16 or fp16); activation: MOE_ACT_SILU or
+    MOE_ACT_GELU_TANH; gate_up [T, 2 N]: both projections, kept for the gradient.  See
+    include/moe_prep.h."""
+    T, K = shape = x.shape
+    rows, dt = weight.shape[0], x.dtype
+    if rows % 2:
+        raise ValueError(f"weight: {rows} rows are not as many gate rows as up rows")
+    N = rows // 2
+    _here(x=x, weight=weight, out=out, gate_up=gate_up, device_status=device_status)
+    _call("moe_gated_linear", GatedLinearArgs.pack(
+        T, K, N, _code("x", dt), activation, x.data_ptr(), _rows("x", x, shape, dt),
+        _flat("weight", weight, (rows, K), dt), out.data_ptr(), _rows("out", out, (T, N), dt),
+        _at(gate_up), _rows("gate_up", gate_up, (T, rows), dt), _at(device_status)), stream)
+
+
+def gated_linear_workspace_size(num_tokens, in_features, out_features) -> int:
+    """Bytes of ``moe_gated_linear_backward``'s workspace."""
+    return int(load().moe_gated_linear_workspace_size(num_tokens, in_features, out_features))
+
+
+def moe_gated_linear_backward(d_out, x, weight, gate_up, d_x=None, d_weight=None,
+                              activation=MOE_ACT_SILU, workspace=None, device_status=None,
+                              stream=None):
+    """Gradients of ``moe_gated_linear``: d_x [T, K] and d_weight [2 N, K], each where given, from
+    d_out [T, N], the forward's x and weight and the gate_up that it wrote.  workspace: uint8,
+    gated_linear_workspace_size() bytes.  See include/moe_prep.h."""
+    T, K = shape = x.shape
+    rows, dt = weight.shape[0], x.dtype
+    if rows % 2:
+        raise ValueError(f"weight: {rows} rows are not as many gate rows as up rows")
+    N = rows // 2
+    _here(d_out=d_out, x=x, weight=weight, gate_up=gate_up, d_x=d_x, d_weight=d_weight,
+          workspace=workspace, device_status=device_status)
+    _call("moe_gated_linear_backward", GatedLinearBackwardArgs.pack(
+        T, K, N, _code("x", dt), activation, d_out.data_ptr(), _rows("d_out", d_out, (T, N), dt),
+        x.data_ptr(), _rows("x", x, shape, dt), _flat("weight", weight, (rows, K), dt),
+        gate_up.data_ptr(), _rows("gate_up", gate_up, (T, rows), dt), _at(d_x),
+        _rows("d_x", d_x, shape, dt), _flat("d_weight", d_weight, (rows, K), dt), _at(workspace),
+        _bytes(workspace), _at(device_status)), stream)
 
 
 class MoeLayer:

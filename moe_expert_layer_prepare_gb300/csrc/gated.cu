@@ -1,0 +1,855 @@
+// The gated projection of a feed-forward block and its gradients:
+//   g = x Wg^T, u = x Wu^T, out = act(g) u;
+//   d_g = d_out u act'(g), d_u = d_out act(g), d_x = [d_g d_u] W, d_W = [d_g d_u]^T x.
+//
+// Three products on tcgen05 of one shape, D[m, n] = sum_k A[m, k] B[n, k]:
+//   forward   m tokens, n features, k the columns of x;
+//   d_x       m tokens, n the columns of x, k the rows of W;
+//   d_W       m the rows of W, n the columns of x, k tokens.
+// An operand that has k along its rows of memory is read as it lies (the MMA takes either
+// order), so nothing is transposed.  The forward's tile takes as many gate rows as up rows
+// of W, so that one thread has both values of an output and the activation costs no pass.
+//
+//   Few tokens (gated_split_kernel): W is streamed, so HBM bounds it.  Features are the
+//   rows of the accumulator (64 gate, 64 up), tokens its columns, and with few tiles the
+//   K slabs are dealt out to the CTAs of a cluster.
+//   Many (gated_pair_kernel): the tensor cores bound it.  CTA pairs keep 256 x 256 tiles
+//   and two accumulators, one in use while the other is written out.
+#include <mutex>
+#include <type_traits>
+
+#include "activation.cuh"
+#include "block_common.cuh"
+#include "tc_common.cuh"
+
+namespace moe {
+namespace gated {
+
+using namespace tc;
+
+enum Mode { FORWARD = 0, D_X = 1, D_W = 2 };
+
+struct Params {
+  int64_t T, K, N;
+  int act;
+  void* out;  // out, d_x or d_weight
+  int64_t out_stride;
+  void* gate_up;  // nullable
+  int64_t gate_up_stride;
+  bool out_wide, gate_up_wide;  // rows that start on 16 bytes
+  float* partials;              // pieces of tiles; nullptr: no tile is cut
+  int pairs, splits;
+  uint32_t* status;
+};
+
+// 16 values to neighbouring columns of a row, of which `left` exist.
+template <typename T>
+__device__ __forceinline__ void store16(T* p, const float (&v)[16], int64_t left, bool wide) {
+  if (wide && left >= 16) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack2<T>(make_float2(v[2 * i], v[2 * i + 1]));
+    st_v4(p, make_uint4(w[0], w[1], w[2], w[3]));
+    st_v4(p + 8, make_uint4(w[4], w[5], w[6], w[7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < left) p[i] = from_f32<T>(v[i]);
+  }
+}
+
+// ------------------------------------------------------------- few tokens
+constexpr int SPLIT_TOKENS = 512;
+constexpr int SM_ROWS = 128;     // of a tile: 64 gate rows of W, 64 up rows
+constexpr int SM_FEATURES = 64;  // outputs of a tile
+constexpr int SM_A_BYTES = SM_ROWS * 128;
+constexpr int SM_THREADS = 256;
+constexpr int SM_MAX_STAGES = 5;
+constexpr int sm_stages(int nt) { return nt <= 32 ? 5 : 4; }
+constexpr int sm_smem(int nt) { return 1024 + sm_stages(nt) * (SM_A_BYTES + nt * 128) + 256; }
+
+// Stores the CTA's share of the tile's tokens from the cluster's sums in rank order.
+template <typename T, int SPLITS>
+__device__ __forceinline__ void join_tokens(const Params& p, const float* sums, int64_t t0,
+                                            int64_t n0, int c0, int share) {
+  const uint32_t at0 = smem_u32(sums);
+  for (int i = threadIdx.x; i < share * (SM_FEATURES / 4); i += SM_THREADS) {
+    const int c = c0 + i / (SM_FEATURES / 4), f = (i % (SM_FEATURES / 4)) * 4;
+    const int64_t t = t0 + c, n = n0 + f;
+    if (t >= p.T || n >= p.N) continue;
+    float4 g[SPLITS], u[SPLITS];
+#pragma unroll
+    for (int r = 0; r < SPLITS; ++r) {
+      const float* s = sums + c * SM_ROWS + f;
+      g[r] = SPLITS == 1 ? *reinterpret_cast<const float4*>(s)
+                         : ld_cluster4(at0 + (uint32_t)(c * SM_ROWS + f) * 4, r);
+      u[r] = SPLITS == 1 ? *reinterpret_cast<const float4*>(s + SM_FEATURES)
+                         : ld_cluster4(at0 + (uint32_t)(c * SM_ROWS + SM_FEATURES + f) * 4, r);
+    }
+#pragma unroll
+    for (int r = 1; r < SPLITS; ++r) {
+      g[0].x += g[r].x, g[0].y += g[r].y, g[0].z += g[r].z, g[0].w += g[r].w;
+      u[0].x += u[r].x, u[0].y += u[r].y, u[0].z += u[r].z, u[0].w += u[r].w;
+    }
+    const float gv[4] = {g[0].x, g[0].y, g[0].z, g[0].w};
+    const float uv[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+    T* out = static_cast<T*>(p.out) + t * p.out_stride + n;
+    T* gu = static_cast<T*>(p.gate_up) + t * p.gate_up_stride + n;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (n + e >= p.N) break;
+      out[e] = from_f32<T>(act_value(p.act, gv[e]) * uv[e]);
+      if (p.gate_up != nullptr) gu[e] = from_f32<T>(gv[e]), gu[p.N + e] = from_f32<T>(uv[e]);
+    }
+  }
+}
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(SM_THREADS, NT <= 64 ? 2 : 1)
+    gated_split_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tmG,
+                       const __grid_constant__ CUtensorMap tmU,
+                       const __grid_constant__ CUtensorMap tmX) {
+  constexpr int STAGES = sm_stages(NT), STAGE_BYTES = SM_A_BYTES + NT * 128;
+  constexpr uint32_t IDESC = f16_idesc(std::is_same<T, __nv_bfloat16>::value, SM_ROWS, NT);
+  constexpr uint32_t TMEM_COLS = NT < 32 ? 32 : NT;
+  static_assert(NT * SM_ROWS * 4 <= STAGES * STAGE_BYTES, "the sums fit the ring");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES);
+  // full[STAGES], empty[STAGES], done
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * SM_MAX_STAGES + 1);
+  int* s_abort = reinterpret_cast<int*>(tmem_holder + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort_flag = s_abort;
+  const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + SM_MAX_STAGES);
+  const uint32_t done_bar = smem_u32(bars + 2 * SM_MAX_STAGES);
+
+  if (tid == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    mbar_init(done_bar, 1);
+    *s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_async_smem();
+    prefetch_map(&tmG);
+    prefetch_map(&tmU);
+    prefetch_map(&tmX);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_holder)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_holder;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  const int rank = p.splits > 1 ? (int)(blockIdx.x % (unsigned)p.splits) : 0;
+  const int64_t n0 = (int64_t)(blockIdx.x / (unsigned)p.splits) * SM_FEATURES;
+  const int64_t t0 = (int64_t)blockIdx.y * NT;
+  const int slabs = (int)((p.K + 63) / 64);
+  const int per = (slabs + p.splits - 1) / p.splits;
+  const int kb0 = rank * per, kb1 = min(slabs, kb0 + per);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA
+    int stage = 0;
+    uint32_t phase = 0, issued = 0, issued_phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+#ifdef MOE_TEST_WITHHOLD_STAGE
+      // Failure-detection test builds only: CTA 0 issues neither its second
+      // slab nor anything after it, and the MMA warp's wait runs out.
+      if (blockIdx.x == 0 && blockIdx.y == 0 && kb > kb0) break;
+#endif
+      if (!warp_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, p.status)) break;
+      if (elect_one()) {
+        const uint32_t bar = full0 + 8 * stage, s = smem_u32(smem + stage * STAGE_BYTES);
+        mbar_expect_tx(bar, STAGE_BYTES);
+        tma_load_2d(s, &tmG, kb * 64, (int)n0, bar);
+        tma_load_2d(s + SM_A_BYTES / 2, &tmU, kb * 64, (int)n0, bar);
+        tma_load_2d(s + SM_A_BYTES, &tmX, kb * 64, (int)t0, bar);
+      }
+      __syncwarp();
+      issued |= 1u << stage;
+      issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+      if (++stage == STAGES) stage = 0, phase ^= 1u;
+    }
+    for (int s = 0; s < STAGES; ++s)  // every copy has landed before exit
+      if (issued & (1u << s)) {
+        volatile int never = 0;
+        mbar_wait(full0 + 8 * s, (issued_phase >> s) & 1u, &never, p.status);
+      }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA
+    int stage = 0;
+    uint32_t phase = 0, accumulate = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!warp_wait(full0 + 8 * stage, phase, abort_flag, p.status)) break;
+      fence_after();
+      const uint32_t s = smem_u32(smem + stage * STAGE_BYTES);
+      const uint64_t ad = sw128_desc(s), bd = sw128_desc(s + SM_A_BYTES);
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_f16(tmem, ad + 2 * k, bd + 2 * k, IDESC, accumulate | (k > 0));
+        mma_commit(empty0 + 8 * stage);
+      }
+      __syncwarp();
+      accumulate = 1;
+      if (++stage == STAGES) stage = 0, phase ^= 1u;
+    }
+    if (accumulate) {  // all MMAs complete before the sums are read or TMEM is freed
+      if (elect_one()) mma_commit(done_bar);
+      __syncwarp();
+      volatile int never = 0;
+      mbar_wait(done_bar, 0, &never, p.status);
+      __syncwarp();
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------------ sums
+    // done is also signalled after a wait ran out; the sums are then not whole
+    if (warp_wait(done_bar, 0, abort_flag, p.status) && *abort_flag == 0) {
+      fence_after();
+      const int nl = (warp & 3) * 32 + lane;
+      const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+      float* red = reinterpret_cast<float*>(smem);  // the ring is no longer in use
+#pragma unroll 1
+      for (int c = 0; c < NT; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(lanes + c, v);
+        tmem_wait16(v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) red[(c + j) * SM_ROWS + nl] = __uint_as_float(v[j]);
+      }
+      fence_before();
+    }
+  }
+  __syncwarp();
+  if (p.splits > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  // Each CTA finishes its share of the tile's tokens.
+  if (*abort_flag == 0) {
+    const float* sums = reinterpret_cast<const float*>(smem);
+    const int share = NT / p.splits, c0 = rank * share;
+    if (p.splits == 1)
+      join_tokens<T, 1>(p, sums, t0, n0, c0, share);
+    else if (p.splits == 2)
+      join_tokens<T, 2>(p, sums, t0, n0, c0, share);
+    else if (p.splits == 4)
+      join_tokens<T, 4>(p, sums, t0, n0, c0, share);
+    else
+      join_tokens<T, 8>(p, sums, t0, n0, c0, share);
+  }
+  __syncwarp();
+  if (p.splits > 1) cluster_sync();  // no CTA leaves while its sums are read
+  fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS)
+                 : "memory");
+  }
+}
+
+// ------------------------------------------------------------ many tokens
+constexpr int TILE = 256;  // rows and columns of a pair's accumulator
+constexpr int HALF = 128;  // of them one CTA's operands
+constexpr int STAGES = 6;
+constexpr int OPERAND = HALF * 128;  // bytes of one CTA's A or B in a stage
+constexpr int STAGE_BYTES = 2 * OPERAND;
+constexpr int THREADS = 192;
+constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + 256;
+constexpr int MIN_SLABS = 8;                    // of a piece of a tile
+constexpr int64_t PIECE = (int64_t)TILE * TILE;  // its sums
+
+// The work of the pairs: whole tiles dealt out in rounds, and the tiles of a last round
+// that would leave pairs idle cut along k, so that each pair has a piece.
+struct Work {
+  int m_tiles, n_tiles, units, slabs, full, parts, items, per;
+  __host__ __device__ Work(Mode mode, int64_t T, int64_t K, int64_t N, int pairs, bool cut) {
+    const int64_t m = mode == D_W ? 2 * N : T, n = mode == FORWARD ? 2 * N : K;
+    const int64_t k = mode == FORWARD ? K : (mode == D_X ? 2 * N : T);
+    m_tiles = (int)((m + TILE - 1) / TILE);
+    // a tile of the forward has HALF gate rows and as many up rows
+    n_tiles = mode == FORWARD ? (int)((N + HALF - 1) / HALF) : (int)((n + TILE - 1) / TILE);
+    units = m_tiles * n_tiles;
+    slabs = (int)((k + 63) / 64);
+    const int rest = units % pairs;
+    parts = 1;
+    if (cut && rest > 0) {
+      parts = pairs / rest < slabs / MIN_SLABS ? pairs / rest : slabs / MIN_SLABS;
+      if (parts < 2) parts = 1;
+    }
+    per = (slabs + parts - 1) / parts;
+    parts = (slabs + per - 1) / per;  // every piece has slabs
+    full = parts > 1 ? units - rest : units;
+    items = full + (units - full) * parts;
+  }
+};
+struct Item {
+  int unit, kb0, kb1, piece;  // piece: -1, a whole tile; else its place among the pieces
+};
+__device__ __forceinline__ Item work_item(const Work& w, int i) {
+  if (i < w.full) return Item{i, 0, w.slabs, -1};
+  const int j = i - w.full, part = j % w.parts;
+  return Item{w.full + j / w.parts, part * w.per, min(w.slabs, (part + 1) * w.per), j};
+}
+
+// A persistent pair of CTAs; CTA r has rows [128 r, 128 r + 128) of a tile's A and B and
+// those rows of its sums.  The first CTA issues the MMAs of both; its full[] barriers count
+// both CTAs' copies, and each commit reaches both.
+template <typename T, Mode MODE>
+__global__ void __launch_bounds__(THREADS, 1)
+    gated_pair_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tmA,
+                      const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmB2) {
+  constexpr bool A_MN = MODE == D_W, B_MN = MODE != FORWARD;
+  constexpr uint32_t IDESC = f16_idesc(std::is_same<T, __nv_bfloat16>::value, TILE, TILE) |
+                             (A_MN ? IDESC_A_MN : 0u) | (B_MN ? IDESC_B_MN : 0u);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES);
+  // full[STAGES], empty[STAGES], tfull[2], tempty[2]
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 4);
+  int* s_abort = reinterpret_cast<int*>(tmem_holder + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort_flag = s_abort;
+  const uint32_t rank = cluster_rank();
+  const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + STAGES);
+  const uint32_t tfull0 = smem_u32(bars + 2 * STAGES), tempty0 = tfull0 + 16;
+
+  if (tid == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull0 + 8 * b, 1);
+      mbar_init(tempty0 + 8 * b, 2 * 4);
+    }
+    *s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_async_smem();
+    prefetch_map(&tmA);
+    prefetch_map(&tmB);
+    prefetch_map(&tmB2);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_holder)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are set up
+  fence_after();
+  const uint32_t tmem = *tmem_holder;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  const Work work(MODE, p.T, p.K, p.N, p.pairs, p.partials != nullptr);
+  const int first = (int)(blockIdx.x >> 1), stride = (int)(gridDim.x >> 1);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA
+    int stage = 0;
+    uint32_t phase = 0, issued = 0, issued_phase = 0;
+    bool ok = true;
+    for (int i = first; ok && i < work.items; i += stride) {
+      const Item item = work_item(work, i);
+      const int m0 = item.unit / work.n_tiles * TILE + (int)rank * HALF;
+      const int n0 = item.unit % work.n_tiles * (MODE == FORWARD ? HALF : TILE) +
+                     (MODE == FORWARD ? 0 : (int)rank * HALF);
+      for (int kb = item.kb0; kb < item.kb1; ++kb) {
+#ifdef MOE_TEST_WITHHOLD_STAGE
+        if (blockIdx.x < 2 && kb > item.kb0) {  // as above: the first pair stops here
+          ok = false;
+          break;
+        }
+#endif
+        ok = warp_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, p.status);
+        if (!ok) break;
+        const uint32_t bar = cluster_address(full0 + 8 * stage, 0);
+        const uint32_t s = smem_u32(smem + stage * STAGE_BYTES);
+        if (elect_one()) {
+          if (rank == 0) mbar_expect_tx(full0 + 8 * stage, 2 * STAGE_BYTES);
+          if (A_MN) {
+            tma_load_2d_pair(s, &tmA, m0, kb * 64, bar);
+            tma_load_2d_pair(s + MN_BOX, &tmA, m0 + 64, kb * 64, bar);
+          } else {
+            tma_load_2d_pair(s, &tmA, kb * 64, m0, bar);
+          }
+          if (B_MN) {
+            tma_load_2d_pair(s + OPERAND, &tmB, n0, kb * 64, bar);
+            tma_load_2d_pair(s + OPERAND + MN_BOX, &tmB, n0 + 64, kb * 64, bar);
+          } else {
+            tma_load_2d_pair(s + OPERAND, rank == 0 ? &tmB : &tmB2, kb * 64, n0, bar);
+          }
+        }
+        __syncwarp();
+        issued |= 1u << stage;
+        issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+        if (++stage == STAGES) stage = 0, phase ^= 1u;
+      }
+    }
+    if (rank == 0)  // both CTAs' copies have landed before either leaves
+      for (int s = 0; s < STAGES; ++s)
+        if (issued & (1u << s)) {
+          volatile int never = 0;
+          mbar_wait(full0 + 8 * s, (issued_phase >> s) & 1u, &never, p.status);
+        }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------- MMA (the first CTA's)
+    constexpr uint32_t A_STEP = A_MN ? 128 : 2, B_STEP = B_MN ? 128 : 2;  // 16 of k, in 16 bytes
+    int stage = 0, ab = 0;
+    uint32_t phase = 0, aphase = 0;
+    bool ok = rank == 0;
+    for (int i = first; ok && i < work.items; i += stride) {
+      const Item item = work_item(work, i);
+      ok = warp_wait(tempty0 + 8 * ab, aphase ^ 1u, abort_flag, p.status);
+      const uint32_t d = tmem + (uint32_t)(ab * TILE);
+      for (int kb = item.kb0; kb < item.kb1 && ok; ++kb) {
+        ok = warp_wait(full0 + 8 * stage, phase, abort_flag, p.status);
+        if (!ok) break;
+        fence_after();
+        const uint32_t s = smem_u32(smem + stage * STAGE_BYTES);
+        const uint64_t ad = A_MN ? sw128_mn_desc(s) : sw128_desc(s);
+        const uint64_t bd = B_MN ? sw128_mn_desc(s + OPERAND) : sw128_desc(s + OPERAND);
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f16_pair(d, ad + A_STEP * k, bd + B_STEP * k, IDESC, kb > item.kb0 || k > 0);
+          mma_commit_pair(empty0 + 8 * stage);
+        }
+        __syncwarp();
+        if (++stage == STAGES) stage = 0, phase ^= 1u;
+      }
+      if (elect_one()) mma_commit_pair(tfull0 + 8 * ab);
+      __syncwarp();
+      ab ^= 1;
+      if (ab == 0) aphase ^= 1u;
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue
+    const int row = (int)rank * HALF + (warp & 3) * 32 + lane;  // of the tile
+    const int64_t rows = MODE == D_W ? 2 * p.N : p.T;
+    int ab = 0;
+    uint32_t aphase = 0;
+    for (int i = first; i < work.items; i += stride) {
+      const Item item = work_item(work, i);
+      const int64_t m = (int64_t)(item.unit / work.n_tiles) * TILE + row;
+      if (!warp_wait(tfull0 + 8 * ab, aphase, abort_flag, p.status) || *abort_flag != 0) break;
+      fence_after();
+      const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(ab * TILE);
+      if constexpr (MODE == FORWARD) {
+        const int64_t n0 = (int64_t)(item.unit % work.n_tiles) * HALF;
+        T* out = static_cast<T*>(p.out) + m * p.out_stride + n0;
+        T* gu = static_cast<T*>(p.gate_up) + m * p.gate_up_stride + n0;
+#pragma unroll 1
+        for (int c = 0; c < HALF; c += 16) {
+          uint32_t vg[16], vu[16];
+          tmem_ld16(lanes + c, vg);
+          tmem_ld16(lanes + HALF + c, vu);
+          tmem_wait16(vg);
+          tmem_wait16(vu);
+          float o[16], g[16], u[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            g[j] = __uint_as_float(vg[j]), u[j] = __uint_as_float(vu[j]);
+            o[j] = act_value(p.act, g[j]) * u[j];
+          }
+          if (m >= rows) continue;
+          const int64_t left = p.N - n0 - c;
+          store16<T>(out + c, o, left, p.out_wide);
+          if (p.gate_up != nullptr) {
+            store16<T>(gu + c, g, left, p.gate_up_wide);
+            store16<T>(gu + p.N + c, u, left, p.gate_up_wide);
+          }
+        }
+      } else {
+        const int64_t n0 = (int64_t)(item.unit % work.n_tiles) * TILE;
+        T* out = static_cast<T*>(p.out) + m * p.out_stride + n0;
+        float* part = p.partials + item.piece * PIECE + row * TILE;
+#pragma unroll 1
+        for (int c = 0; c < TILE; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(lanes + c, v);
+          tmem_wait16(v);
+          if (item.piece >= 0) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 4)
+              st_v4(part + c + j, make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]));
+            continue;
+          }
+          float f[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]);
+          if (m < rows) store16<T>(out + c, f, p.K - n0 - c, p.out_wide);
+        }
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_address(tempty0 + 8 * ab, 0));
+      ab ^= 1;
+      if (ab == 0) aphase ^= 1u;
+    }
+  }
+  __syncwarp();
+  fence_before();
+  cluster_sync();  // both CTAs' copies, MMAs and reads are done
+  if (warp == 1) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                 : "memory");
+  }
+}
+
+// Sums the pieces of the tiles that were cut, in their order, and stores them: a block
+// JOIN_ROWS rows of a tile, a thread four columns of two of them.
+constexpr int JOIN_ROWS = 8;
+
+template <typename T, Mode MODE>
+__global__ void __launch_bounds__(256) gated_join_kernel(Params p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const Work work(MODE, p.T, p.K, p.N, p.pairs, true);
+  const int u = work.full + blockIdx.y;
+  const int64_t rows = MODE == D_W ? 2 * p.N : p.T;
+  const int f = (threadIdx.x & 63) * 4;
+  const int64_t n = (int64_t)(u % work.n_tiles) * TILE + f;
+  const float* from = p.partials + (int64_t)blockIdx.y * work.parts * PIECE + f;
+  for (int r = blockIdx.x * JOIN_ROWS + (threadIdx.x >> 6); r < (blockIdx.x + 1) * JOIN_ROWS; r += 4) {
+    const int64_t m = (int64_t)(u / work.n_tiles) * TILE + r;
+    if (m >= rows) continue;
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int q0 = 0; q0 < work.parts; q0 += 4) {
+      float4 v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        v[q] = q0 + q < work.parts
+                   ? __ldcg(reinterpret_cast<const float4*>(from + (q0 + q) * PIECE + r * TILE))
+                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        sum.x += v[q].x, sum.y += v[q].y, sum.z += v[q].z, sum.w += v[q].w;
+    }
+    const float w[4] = {sum.x, sum.y, sum.z, sum.w};
+    T* out = static_cast<T*>(p.out) + m * p.out_stride + n;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < p.K) out[e] = from_f32<T>(w[e]);
+  }
+}
+
+// ------------------------------------------------- gradients of gate and up
+// [d_g d_u] of VEC neighbouring columns a thread, rounded to the tensors' type, as which
+// they enter both products.
+struct SlopeParams {
+  int64_t T, N;
+  int act;
+  const void *d_out, *gate_up;
+  int64_t d_out_stride, gate_up_stride, d_stride;
+  void* d_gate_up;
+};
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) gated_slope_kernel(SlopeParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t packs = (p.N + VEC - 1) / VEC, total = packs * p.T;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+    const int64_t t = i / packs, n = (i - t * packs) * VEC;
+    const T* gu = static_cast<const T*>(p.gate_up) + t * p.gate_up_stride + n;
+    float g[VEC], u[VEC], d[VEC];
+    load_pack<T, VEC>(gu).get(g);
+    load_pack<T, VEC>(gu + p.N).get(u);
+    load_pack<T, VEC>(static_cast<const T*>(p.d_out) + t * p.d_out_stride + n).get(d);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float2 a = act_slope(p.act, g[e]);
+      g[e] = d[e] * u[e] * a.y;
+      u[e] = d[e] * a.x;
+    }
+    T* dst = static_cast<T*>(p.d_gate_up) + t * p.d_stride + n;
+    Pack<T, VEC> o;
+    o.set(g);
+    store_pack<T, VEC>(dst, o);
+    o.set(u);
+    store_pack<T, VEC>(dst + p.N, o);
+  }
+}
+
+}  // namespace gated
+}  // namespace moe
+
+namespace moe_host {
+
+namespace gated = moe::gated;
+
+// Smallest tile that holds the batch; a cluster shares a tile's K while tiles leave CTA
+// slots empty.
+struct SplitPlan {
+  int nt, splits;
+};
+static SplitPlan split_plan(int64_t T, int64_t K, int64_t N) {
+  SplitPlan q{};
+  const int64_t sms = num_sms();
+  q.nt = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 ? 64 : 128));
+  const int64_t tiles =
+      (N + gated::SM_FEATURES - 1) / gated::SM_FEATURES * ((T + q.nt - 1) / q.nt);
+  const int64_t slots = q.nt <= 64 ? 2 * sms : sms;
+  const int64_t slabs = (K + 63) / 64;
+  q.splits = 1;
+  while (q.splits < 8 && tiles * q.splits * 2 <= slots) {
+    const int64_t per = (slabs + 2 * q.splits - 1) / (2 * q.splits);
+    if (per < 4 || per * (2 * q.splits - 1) >= slabs) break;  // every share has slabs
+    q.splits *= 2;
+  }
+  return q;
+}
+
+template <typename T, int NT>
+static moe_status_t launch_gated_split(const gated::Params& p, const CUtensorMap& g,
+                                       const CUtensorMap& u, const CUtensorMap& x, cudaStream_t s) {
+  constexpr auto kernel = gated::gated_split_kernel<T, NT>;
+  static_assert(gated::sm_smem(NT) <= kMaxSmem, "shared memory of one CTA");
+  moe_status_t st = allow_smem<kernel>(gated::sm_smem(NT));
+  if (st != MOE_OK) return st;
+  const dim3 grid((unsigned)((p.N + gated::SM_FEATURES - 1) / gated::SM_FEATURES * p.splits),
+                  (unsigned)((p.T + NT - 1) / NT));
+  return launched(launch_cluster(kernel, grid, gated::SM_THREADS, p.splits,
+                                 (size_t)gated::sm_smem(NT), s, p, g, u, x),
+                  "gated projection");
+}
+
+template <typename T, gated::Mode MODE>
+static moe_status_t launch_gated_pair(const gated::Params& p, const CUtensorMap& a,
+                                      const CUtensorMap& b, const CUtensorMap& b2, cudaStream_t s) {
+  constexpr auto kernel = gated::gated_pair_kernel<T, MODE>;
+  static_assert(gated::SMEM <= kMaxSmem, "shared memory of one CTA");
+  moe_status_t st = allow_smem<kernel>(gated::SMEM);
+  if (st != MOE_OK) return st;
+  const gated::Work work(MODE, p.T, p.K, p.N, p.pairs, p.partials != nullptr);
+  const int pairs = work.items < p.pairs ? work.items : p.pairs;
+  st = launched(launch_cluster(kernel, dim3((unsigned)(2 * pairs)), gated::THREADS, 2,
+                               (size_t)gated::SMEM, s, p, a, b, b2),
+                "gated projection");
+  if (st != MOE_OK || work.full == work.units) return st;
+  if constexpr (MODE != gated::FORWARD)
+    st = launched(launch_pdl(gated::gated_join_kernel<T, MODE>,
+                             dim3(gated::TILE / gated::JOIN_ROWS, (unsigned)(work.units - work.full)),
+                             dim3(256), 0, s, p),
+                  "gated projection join");
+  return st;
+}
+
+template <typename T>
+static moe_status_t launch_gated(const moe_gated_linear_args_t* a, gated::Params p, cudaStream_t s) {
+  const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+  const int64_t x_stride = p.T > 1 ? a->x_stride0 : p.K;
+  const T* up = static_cast<const T*>(a->weight) + p.N * p.K;
+  const bool split = p.T <= gated::SPLIT_TOKENS;
+  const SplitPlan q = split_plan(p.T, p.K, p.N);
+  const int rows = split ? gated::SM_FEATURES : gated::HALF;
+  CUtensorMap g, u, x;
+  if (!make_map16(&g, bf16, a->weight, p.N, p.K, p.K, rows) ||
+      !make_map16(&u, bf16, up, p.N, p.K, p.K, rows) ||
+      !make_map16(&x, bf16, a->x, p.T, p.K, x_stride, split ? q.nt : gated::HALF))
+    return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the gated projection");
+  if (!split) return launch_gated_pair<T, gated::FORWARD>(p, x, g, u, s);
+  p.splits = q.splits;
+  switch (q.nt) {
+    case 16: return launch_gated_split<T, 16>(p, g, u, x, s);
+    case 32: return launch_gated_split<T, 32>(p, g, u, x, s);
+    case 64: return launch_gated_split<T, 64>(p, g, u, x, s);
+    default: return launch_gated_split<T, 128>(p, g, u, x, s);
+  }
+}
+
+// Workspace of the gradient: [T][d_stride] gradients of gate and up, then pieces of tiles.
+static int64_t d_gate_up_stride(int64_t N) { return (2 * N + 7) / 8 * 8; }
+static int64_t d_gate_up_bytes(int64_t T, int64_t N) {
+  return (T * d_gate_up_stride(N) * 2 + 255) / 256 * 256;
+}
+
+template <typename T>
+static moe_status_t launch_gated_backward(const moe_gated_linear_backward_args_t* a,
+                                          gated::Params p, cudaStream_t s) {
+  const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+  const int64_t ds = d_gate_up_stride(p.N);
+  gated::SlopeParams sp{};
+  sp.T = p.T;
+  sp.N = p.N;
+  sp.act = p.act;
+  sp.d_out = a->d_out;
+  sp.d_out_stride = a->d_out_stride0;
+  sp.gate_up = a->gate_up;
+  sp.gate_up_stride = a->gate_up_stride0;
+  sp.d_gate_up = a->workspace;
+  sp.d_stride = ds;
+  const bool wide = p.N % 8 == 0 && rows_aligned16(a->d_out, a->d_out_stride0, 2, p.T) &&
+                    rows_aligned16(a->gate_up, a->gate_up_stride0, 2, p.T);
+  const int64_t blocks = (p.T * ((p.N + (wide ? 7 : 0)) / (wide ? 8 : 1)) + 255) / 256;
+  const int64_t cap = 8 * (int64_t)num_sms();
+  const dim3 grid((unsigned)(blocks < cap ? blocks : cap));
+  moe_status_t st = launched(wide ? launch_pdl(gated::gated_slope_kernel<T, 8>, grid, dim3(256), 0, s, sp)
+                                  : launch_pdl(gated::gated_slope_kernel<T, 1>, grid, dim3(256), 0, s, sp),
+                             "gated slope");
+  if (st != MOE_OK) return st;
+  p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + d_gate_up_bytes(p.T, p.N));
+  CUtensorMap ma, mb;
+  if (a->d_x != nullptr) {
+    if (!make_map16(&ma, bf16, a->workspace, p.T, 2 * p.N, ds, gated::HALF) ||
+        !make_map16(&mb, bf16, a->weight, 2 * p.N, p.K, p.K, 64))
+      return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for d_x");
+    p.out = a->d_x;
+    p.out_stride = a->d_x_stride0;
+    p.out_wide = rows_aligned16(a->d_x, a->d_x_stride0, 2, p.T);
+    st = launch_gated_pair<T, gated::D_X>(p, ma, mb, mb, s);
+    if (st != MOE_OK) return st;
+  }
+  if (a->d_weight != nullptr) {
+    const int64_t x_stride = p.T > 1 ? a->x_stride0 : p.K;
+    if (!make_map16(&ma, bf16, a->workspace, p.T, 2 * p.N, ds, 64) ||
+        !make_map16(&mb, bf16, a->x, p.T, p.K, x_stride, 64))
+      return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for d_weight");
+    p.out = a->d_weight;
+    p.out_stride = p.K;
+    p.out_wide = rows_aligned16(a->d_weight, p.K, 2, 2 * p.N);
+    st = launch_gated_pair<T, gated::D_W>(p, ma, mb, mb, s);
+  }
+  return st;
+}
+
+static moe_status_t check_gated(int64_t T, int64_t K, int64_t N, int32_t dtype, int32_t act) {
+  if (T < 0 || K < 0 || N < 0) return set_error(MOE_ERR_INVALID_ARGUMENT, "negative size");
+  if (!dtype_ok(dtype)) return set_error(MOE_ERR_INVALID_ARGUMENT, "bad dtype %d", dtype);
+  if (act < MOE_ACT_SILU || act > MOE_ACT_NONE)
+    return set_error(MOE_ERR_INVALID_ARGUMENT, "bad activation %d", act);
+  if (act == MOE_ACT_NONE)
+    return set_error(MOE_ERR_UNSUPPORTED, "a gated projection has an activation");
+  if (dtype == MOE_DTYPE_FP32)
+    return set_error(MOE_ERR_UNSUPPORTED, "the projection takes bf16 or fp16");
+  if (T >= ((int64_t)1 << 22) || K >= ((int64_t)1 << 28) || N >= ((int64_t)1 << 28))
+    return set_error(MOE_ERR_UNSUPPORTED, "problem too large for 32-bit tile coordinates");
+  return MOE_OK;
+}
+
+// x and weight as TMA reads them.
+static moe_status_t check_gated_operands(const void* x, int64_t x_stride, const void* weight,
+                                         int64_t T, int64_t K) {
+  if (K % 8 != 0 || !rows_aligned16(x, x_stride, 2, T) || !rows_aligned16(weight, K, 2, 2))
+    return set_error(MOE_ERR_ALIGNMENT, "rows of x and weight must start on 16-byte boundaries");
+  return MOE_OK;
+}
+
+}  // namespace moe_host
+
+using namespace moe_host;
+
+extern "C" {
+
+moe_status_t moe_gated_linear(const moe_gated_linear_args_t* a, void* stream) {
+  clear_error();
+  if (a == nullptr) return set_error(MOE_ERR_INVALID_ARGUMENT, "args is NULL");
+  const int64_t T = a->num_tokens, K = a->in_features, N = a->out_features;
+  moe_status_t st = check_gated(T, K, N, a->dtype, a->activation);
+  if (st != MOE_OK) return st;
+  if (T == 0 || N == 0) return MOE_OK;
+  if (K < 1) return set_error(MOE_ERR_SHAPE, "in_features must be >= 1");
+  if (!a->x || !a->weight || !a->out)
+    return set_error(MOE_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
+  if (T > 1 && (a->x_stride0 < K || a->out_stride0 < N ||
+                (a->gate_up != nullptr && a->gate_up_stride0 < 2 * N)))
+    return set_error(MOE_ERR_SHAPE, "row stride smaller than the row");
+  st = check_gated_operands(a->x, a->x_stride0, a->weight, T, K);
+  if (st != MOE_OK) return st;
+  gated::Params p{};
+  p.T = T;
+  p.K = K;
+  p.N = N;
+  p.act = a->activation;
+  p.out = a->out;
+  p.out_stride = a->out_stride0;
+  p.out_wide = rows_aligned16(a->out, a->out_stride0, 2, T);
+  p.gate_up = a->gate_up;
+  p.gate_up_stride = a->gate_up_stride0;
+  p.gate_up_wide = N % 8 == 0 && rows_aligned16(a->gate_up, a->gate_up_stride0, 2, T);
+  p.pairs = num_sms() / 2;
+  p.splits = 1;
+  p.status = a->device_status;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return a->dtype == MOE_DTYPE_BF16 ? launch_gated<__nv_bfloat16>(a, p, s)
+                                    : launch_gated<__half>(a, p, s);
+}
+
+size_t moe_gated_linear_workspace_size(int64_t num_tokens, int64_t in_features,
+                                       int64_t out_features) {
+  if (num_tokens <= 0 || in_features <= 0 || out_features <= 0) return 0;
+  return (size_t)(d_gate_up_bytes(num_tokens, out_features) +
+                  (int64_t)(num_sms() / 2) * gated::PIECE * 4);
+}
+
+moe_status_t moe_gated_linear_backward(const moe_gated_linear_backward_args_t* a, void* stream) {
+  clear_error();
+  if (a == nullptr) return set_error(MOE_ERR_INVALID_ARGUMENT, "args is NULL");
+  const int64_t T = a->num_tokens, K = a->in_features, N = a->out_features;
+  moe_status_t st = check_gated(T, K, N, a->dtype, a->activation);
+  if (st != MOE_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (K == 0) return MOE_OK;
+  if (T == 0 || N == 0) {  // sums of nothing
+    cudaError_t e = cudaSuccess;
+    if (T == 0 && N > 0 && a->d_weight != nullptr)
+      e = cudaMemsetAsync(a->d_weight, 0, (size_t)(2 * N * K) * 2, s);
+    if (N == 0 && T > 0 && a->d_x != nullptr) {
+      if (T > 1 && a->d_x_stride0 < K)
+        return set_error(MOE_ERR_SHAPE, "row stride smaller than the row");
+      e = cudaMemset2DAsync(a->d_x, (size_t)(T > 1 ? a->d_x_stride0 : K) * 2, 0, (size_t)K * 2,
+                            (size_t)T, s);
+    }
+    if (e != cudaSuccess) return set_error(MOE_ERR_CUDA, "memset: %s", cudaGetErrorString(e));
+    return MOE_OK;
+  }
+  if (!a->d_out || !a->x || !a->weight || !a->gate_up)
+    return set_error(MOE_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
+  if (T > 1 && (a->x_stride0 < K || a->d_out_stride0 < N || a->gate_up_stride0 < 2 * N ||
+                (a->d_x != nullptr && a->d_x_stride0 < K)))
+    return set_error(MOE_ERR_SHAPE, "row stride smaller than the row");
+  st = check_gated_operands(a->x, a->x_stride0, a->weight, T, K);
+  if (st != MOE_OK) return st;
+  if (a->d_x == nullptr && a->d_weight == nullptr) return MOE_OK;
+  const size_t need = moe_gated_linear_workspace_size(T, K, N);
+  if (a->workspace == nullptr || a->workspace_bytes < need)
+    return set_error(MOE_ERR_WORKSPACE, "the gradients need %zu bytes of workspace, got %zu", need,
+                     a->workspace_bytes);
+  if ((reinterpret_cast<uintptr_t>(a->workspace) & 15u) != 0)
+    return set_error(MOE_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  gated::Params p{};
+  p.T = T;
+  p.K = K;
+  p.N = N;
+  p.act = a->activation;
+  p.pairs = num_sms() / 2;
+  p.splits = 1;
+  p.status = a->device_status;
+  return a->dtype == MOE_DTYPE_BF16 ? launch_gated_backward<__nv_bfloat16>(a, p, s)
+                                    : launch_gated_backward<__half>(a, p, s);
+}
+
+}  // extern "C"

@@ -1589,45 +1589,6 @@ static size_t lora_workspace(const LoraPlan& q, int64_t T, int64_t R) {
   return (size_t)((q.order_words + q.copy_words + q.part_words + q.wide_words + rows * R) * 4);
 }
 
-// Dynamic shared memory limit of a kernel, raised once per device.
-template <auto Kernel>
-static moe_status_t allow_smem(int bytes) {
-  static std::mutex mu;
-  static bool done[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
-    return set_error(MOE_ERR_CUDA, "no current device");
-  std::lock_guard<std::mutex> lock(mu);
-  if (done[dev]) return MOE_OK;
-  cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess)
-    return set_error(MOE_ERR_CUDA, "shared memory attribute: %s", cudaGetErrorString(e));
-  done[dev] = true;
-  return MOE_OK;
-}
-
-template <typename... KArgs, typename... Args>
-static cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, int threads, int cluster,
-                                  size_t smem, cudaStream_t s, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-constexpr int kMaxSmem = 232448;
-
 template <auto Kernel>
 static moe_status_t launch_shrink(const LoraPlan& q, const LoraParams& p, cudaStream_t s) {
   moe_status_t st = allow_smem<Kernel>(moe::sh_smem(q.tok, moe::LORA_MAX_RANK));

@@ -1,8 +1,10 @@
-// mbarrier, TMA and 16-bit tcgen05 helpers of the adapter projection.
+// mbarrier, TMA and 16-bit tcgen05 helpers of the projections.
 #pragma once
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
+
+#include <mutex>
 
 #include "common.cuh"
 
@@ -104,8 +106,17 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
+// The same for an operand whose M or N lies along the rows of 128 bytes: boxes of 64
+// columns by 64 K rows, one behind the other; 8 rows of K are 1024 bytes.
+constexpr int MN_BOX = 64 * 128;
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(MN_BOX >> 4) << 16 |
+         (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
 // Instruction descriptor of kind::f16: fp32 accumulator, A and B of one type,
-// both K-major.
+// both K-major; the two bits for operands that are not.
+constexpr uint32_t IDESC_A_MN = 1u << 15, IDESC_B_MN = 1u << 16;
 __host__ __device__ constexpr uint32_t f16_idesc(bool bf16, int m, int n) {
   return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(m >> 4) << 24);
@@ -242,5 +253,44 @@ inline bool make_map16(CUtensorMap* m, bool bf16, const void* base, int64_t rows
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+// Dynamic shared memory limit of a kernel, raised once per device.
+template <auto Kernel>
+moe_status_t allow_smem(int bytes) {
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+    return set_error(MOE_ERR_CUDA, "no current device");
+  std::lock_guard<std::mutex> lock(mu);
+  if (done[dev]) return MOE_OK;
+  cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess)
+    return set_error(MOE_ERR_CUDA, "shared memory attribute: %s", cudaGetErrorString(e));
+  done[dev] = true;
+  return MOE_OK;
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, int threads, int cluster,
+                                  size_t smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+constexpr int kMaxSmem = 232448;
 
 }  // namespace moe_host

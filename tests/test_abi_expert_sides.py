@@ -41,3 +41,54 @@ def test_norm_quant(lib):  # noqa: F811
         assert call(**{name: 255}) == SHAPE
     assert call(q_sf_stride0=1) == SHAPE
     assert call(q_sf_stride0=0, sf_mode=B.MOE_SF_UE8M0_PACKED) == SHAPE
+
+
+def test_gated_linear(lib):  # noqa: F811
+    packed_layout(B.GatedLinearArgs)
+    packed_layout(B.GatedLinearBackwardArgs)
+    sizes = dict(num_tokens=8, in_features=64, out_features=24, dtype=B.MOE_DTYPE_BF16,
+                 activation=B.MOE_ACT_SILU, x_stride0=64, gate_up_stride0=48)
+
+    def forward(**kw):
+        return lib.moe_gated_linear(
+            ctypes.byref(fill(B.GatedLinearArgs, **{**sizes, **dict(out_stride0=24), **kw})), None)
+
+    def backward(**kw):
+        base = {**sizes, **dict(d_out_stride0=24, d_x_stride0=64, workspace_bytes=1 << 40)}
+        return lib.moe_gated_linear_backward(
+            ctypes.byref(fill(B.GatedLinearBackwardArgs, **{**base, **kw})), None)
+
+    assert lib.moe_gated_linear(None, None) == INVALID
+    assert lib.moe_gated_linear_backward(None, None) == INVALID
+    for call in (forward, backward):
+        for name in ("num_tokens", "in_features", "out_features"):
+            assert call(**{name: -1}) == INVALID
+        assert call(dtype=5) == INVALID
+        assert call(activation=3) == INVALID
+        assert call(activation=B.MOE_ACT_NONE) == UNSUPPORTED
+        assert call(dtype=B.MOE_DTYPE_FP32) == UNSUPPORTED
+        assert call(num_tokens=1 << 22) == UNSUPPORTED
+        assert call(out_features=1 << 28) == UNSUPPORTED
+        assert call(x=None) == INVALID
+        assert call(weight=None) == INVALID
+        assert call(x_stride0=56) == SHAPE
+        assert call(gate_up_stride0=47) == SHAPE
+        assert call(in_features=60) == ALIGNMENT
+        assert call(x_stride0=68) == ALIGNMENT
+        assert call(x=FAKE + 8) == ALIGNMENT
+        assert call(weight=FAKE + 2) == ALIGNMENT
+    assert forward(num_tokens=0, x=None, out=None) == OK
+    assert forward(in_features=0) == SHAPE
+    assert forward(out=None) == INVALID
+    assert forward(out_stride0=23) == SHAPE
+    assert backward(in_features=0) == OK
+    assert backward(num_tokens=0, d_weight=None, x=None) == OK
+    assert backward(d_x=None, d_weight=None) == OK
+    assert backward(d_out=None) == INVALID
+    assert backward(gate_up=None) == INVALID
+    assert backward(d_out_stride0=23) == SHAPE
+    assert backward(d_x_stride0=63) == SHAPE
+    assert backward(workspace=None) == WORKSPACE
+    assert backward(workspace_bytes=1 << 10) == WORKSPACE
+    assert backward(workspace=FAKE + 4) == ALIGNMENT
+    assert lib.moe_gated_linear_workspace_size(0, 64, 24) == 0
