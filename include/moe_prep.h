@@ -29,6 +29,8 @@
  *                        own low-rank adapter.
  *   moe_gated_linear     gate and up projections with the activation and the
  *                        product in one kernel (and its gradients).
+ *   moe_w4_linear        products of few rows with 4-bit weights and group
+ *                        scales, of one matrix or of each row's expert.
  *
  * Conventions shared by every call
  *   - All tensor pointers are DEVICE pointers unless stated otherwise; every
@@ -89,6 +91,10 @@ typedef enum moe_activation {
 } moe_activation_t;
 typedef enum moe_shared_dtype { MOE_SHARED_BF16 = 0, MOE_SHARED_FP8 = 1 } moe_shared_dtype_t;
 typedef enum moe_dtype { MOE_DTYPE_FP32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_FP16 = 2 } moe_dtype_t;
+typedef enum moe_w4_format {
+  MOE_W4_INT4 = 0, /* q - zero point (8 without one), scales of the tensors' type */
+  MOE_W4_E2M1 = 1  /* sign, two bits of exponent, one of mantissa; scales 2^(byte - 127) */
+} moe_w4_format_t;
 typedef enum moe_scoring {
   MOE_SCORE_SOFTMAX = 0,
   MOE_SCORE_SIGMOID = 1,
@@ -843,6 +849,53 @@ moe_status_t moe_gated_linear_backward(const moe_gated_linear_backward_args_t* a
 
 size_t moe_gated_linear_workspace_size(int64_t num_tokens, int64_t in_features,
                                        int64_t out_features);
+
+/* ------------------------------------------------------------------------ */
+/* moe_w4_linear                                                             */
+/*                                                                           */
+/* Products of few rows with 4-bit weights and group scales.  A matrix is      */
+/*   W[n, k] = scales[n, k/G] * (q[n, k] - zeros[n, k/G])      INT4 (no zeros: */
+/*             q - 8), scales of dtype, zeros uint8 (their lower four bits);   */
+/*   W[n, k] = 2^(scales[n, k/G] - 127) * e2m1(q[n, k])        E2M1, scales    */
+/*             uint8 (255: not a number).                                    */
+/* q[n, k] is the low (k even) or high (k odd) half of byte k/2 of row n.      */
+/*   topk_ids NULL:  out[t] = x[t] W^T, one matrix [N, K];                      */
+/*   topk_ids [T, k]: out[t * k + j] = x[t] W_e^T of matrix e = topk_ids[t, j]  */
+/*                   of [E, N, K]; other ids give a row of zeros (id >= E also  */
+/*                   sets MOE_DEV_BAD_EXPERT).  With top_k 1 every row of x has */
+/*                   an expert of its own, as the second product of a layer     */
+/*                   needs it.                                               */
+/* activation MOE_ACT_NONE: out has N columns.  Else rows [0, N/2) are a gate,  */
+/* rows [N/2, N) up, and out = act(gate) * up has N/2 columns.                 */
+/* A group's sum is in fp32, of exact products; the scale multiplies it there;  */
+/* out is rounded once.  A row of x, non-finite values too, reaches its own     */
+/* rows of out alone.  x [T, K] and out: inner stride 1, row strides of their   */
+/* own; weight, scales and zeros contiguous; bf16 or fp16.                     */
+/* Errors: K % G, an odd N with an activation -> SHAPE; G other than 32, 64,    */
+/* 128 (E2M1: 32), zeros with E2M1, more than 1024 rows of out (routes), E >    */
+/* 1024, fp32 -> UNSUPPORTED; x, weight or x's rows not on 16-byte boundaries    */
+/* -> ALIGNMENT.                                                              */
+/* ------------------------------------------------------------------------ */
+typedef struct moe_w4_linear_args {
+  int64_t num_tokens, in_features, matrix_rows; /* T, K, N */
+  int64_t num_experts, top_k;                   /* with topk_ids */
+  int64_t group_size;                           /* G */
+  int32_t dtype;                                /* MOE_DTYPE_BF16 or MOE_DTYPE_FP16 */
+  int32_t format;                               /* MOE_W4_* */
+  int32_t activation;                           /* MOE_ACT_* */
+  const void* x;
+  int64_t x_stride0;
+  const void* weight; /* [E, N, K/2] bytes */
+  const void* scales; /* [E, N, K/G] */
+  const void* zeros;  /* nullable [E, N, K/G] */
+  const void* topk_ids;
+  int32_t topk_ids_dtype; /* MOE_IDS_* */
+  void* out;
+  int64_t out_stride0;
+  uint32_t* device_status;
+} moe_w4_linear_args_t;
+
+moe_status_t moe_w4_linear(const moe_w4_linear_args_t* args, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Utilities                                                                 */

@@ -22,6 +22,7 @@ MOE_SF_NONE, MOE_SF_UE8M0_PACKED, MOE_SF_FP32 = 0, 1, 2
 MOE_IDS_INT32, MOE_IDS_INT64 = 0, 1
 MOE_WEIGHTS_FP32, MOE_WEIGHTS_BF16 = 0, 1
 MOE_ACT_SILU, MOE_ACT_GELU_TANH, MOE_ACT_NONE = 0, 1, 2
+MOE_W4_INT4, MOE_W4_E2M1 = 0, 1
 MOE_SHARED_BF16, MOE_SHARED_FP8 = 0, 1
 MOE_STAGE_W13, MOE_STAGE_W2, MOE_STAGE_ALL = 1, 2, 3
 MOE_DTYPE_FP32, MOE_DTYPE_BF16, MOE_DTYPE_FP16 = 0, 1, 2
@@ -247,6 +248,17 @@ class GatedLinearBackwardArgs(ctypes.Structure):
     ]
 
 
+@_packer
+class W4LinearArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", _i64), ("in_features", _i64), ("matrix_rows", _i64),
+        ("num_experts", _i64), ("top_k", _i64), ("group_size", _i64), ("dtype", _i32),
+        ("format", _i32), ("activation", _i32), ("x", _vp), ("x_stride0", _i64), ("weight", _vp),
+        ("scales", _vp), ("zeros", _vp), ("topk_ids", _vp), ("topk_ids_dtype", _i32),
+        ("out", _vp), ("out_stride0", _i64), ("device_status", _vp),
+    ]
+
+
 _lib = None
 
 
@@ -283,7 +295,7 @@ def configure(lib):
     for name in ("moe_route", "moe_route_backward", "moe_sort_routes", "moe_permute",
                  "moe_unpermute", "moe_unpermute_backward", "moe_block_norm",
                  "moe_block_norm_backward", "moe_lora_linear", "moe_norm_quant",
-                 "moe_gated_linear", "moe_gated_linear_backward"):
+                 "moe_gated_linear", "moe_gated_linear_backward", "moe_w4_linear"):
         getattr(lib, name).restype = ctypes.c_int
         getattr(lib, name).argtypes = [_vp, _vp]  # the packed struct's bytes, the stream
     for name, n in (("moe_sort_workspace_size", 3), ("moe_block_norm_workspace_size", 2),
@@ -905,6 +917,45 @@ def moe_gated_linear_backward(d_out, x, weight, gate_up, d_x=None, d_weight=None
         gate_up.data_ptr(), _rows("gate_up", gate_up, (T, rows), dt), _at(d_x),
         _rows("d_x", d_x, shape, dt), _flat("d_weight", d_weight, (rows, K), dt), _at(workspace),
         _bytes(workspace), _at(device_status)), stream)
+
+
+def moe_w4_linear(x, weight, scales, out, zeros=None, topk_ids=None, activation=MOE_ACT_NONE,
+                  device_status=None, stream=None):
+    """Products of few rows with 4-bit weights and group scales.
+
+    x: [T, K] bf16 or fp16; weight: uint8 [N, K / 2], two codes a byte, the lower half first, or
+    with topk_ids [E, N, K / 2]; scales: [(E,) N, K / G], of x's type for integer codes
+    (scale * (q - 8), or with zeros, uint8 of the same shape, scale * (q - zero)), uint8 exponents
+    for e2m1 codes (2^(s - 127), G = 32); G is 32, 64 or 128.
+    topk_ids: int32 or int64 [T, k]; out: [T, N], with topk_ids [T * k, N], a row a route (zeros
+    where the id is none of an expert).  With an activation the first half of a matrix's rows is a
+    gate, the second up, and out has N / 2 columns, act(gate) * up.  See include/moe_prep.h."""
+    T, K = shape = x.shape
+    dt, ws, sdt = x.dtype, weight.shape, scales.dtype
+    E, k, idt = 0, 0, _INT32
+    if topk_ids is not None:
+        if len(ws) != 3:
+            raise ValueError(f"weight: want [E, N, K / 2] with topk_ids, got {list(ws)}")
+        E, k, idt = ws[0], topk_ids.shape[1], topk_ids.dtype
+    elif len(ws) != 2:
+        raise ValueError(f"weight: want [N, K / 2] without topk_ids, got {list(ws)}")
+    N, groups = ws[-2], scales.shape[-1]
+    if K % 2 or groups == 0 or K % groups:
+        raise ValueError(f"scales: {groups} groups of {K} values")
+    if sdt is not torch.uint8 and sdt is not dt:
+        raise ValueError(f"scales: want {dt} or torch.uint8 exponents, got {sdt}")
+    lead, rows = tuple(ws[:-1]), T * k if E else T
+    _here(x=x, weight=weight, scales=scales, out=out, zeros=zeros, topk_ids=topk_ids,
+          device_status=device_status)
+    n_out = N if activation == MOE_ACT_NONE else N // 2
+    _call("moe_w4_linear", W4LinearArgs.pack(
+        T, K, N, E, k, K // groups, _code("x", dt),
+        MOE_W4_E2M1 if sdt is torch.uint8 else MOE_W4_INT4, activation, x.data_ptr(),
+        _rows("x", x, shape, dt), _flat("weight", weight, (*lead, K // 2), torch.uint8),
+        _flat("scales", scales, (*lead, groups), sdt),
+        _flat("zeros", zeros, (*lead, groups), torch.uint8),
+        _flat("topk_ids", topk_ids, (T, k), idt), _code("topk_ids", idt, _IDS), out.data_ptr(),
+        _rows("out", out, (rows, n_out), dt), _at(device_status)), stream)
 
 
 class MoeLayer:

@@ -92,3 +92,45 @@ def test_gated_linear(lib):  # noqa: F811
     assert backward(workspace_bytes=1 << 10) == WORKSPACE
     assert backward(workspace=FAKE + 4) == ALIGNMENT
     assert lib.moe_gated_linear_workspace_size(0, 64, 24) == 0
+
+
+def test_w4_linear(lib):  # noqa: F811
+    packed_layout(B.W4LinearArgs)
+
+    def call(**kw):
+        base = dict(num_tokens=8, in_features=256, matrix_rows=32, num_experts=4, top_k=2,
+                    group_size=64, dtype=B.MOE_DTYPE_BF16, format=B.MOE_W4_INT4,
+                    activation=B.MOE_ACT_NONE, x_stride0=256, topk_ids_dtype=B.MOE_IDS_INT32,
+                    out_stride0=32)
+        return lib.moe_w4_linear(ctypes.byref(fill(B.W4LinearArgs, **{**base, **kw})), None)
+
+    assert lib.moe_w4_linear(None, None) == INVALID
+    for name in ("num_tokens", "in_features", "matrix_rows", "num_experts", "top_k"):
+        assert call(**{name: -1}) == INVALID
+    assert call(dtype=7) == INVALID
+    assert call(format=2) == INVALID
+    assert call(activation=3) == INVALID
+    assert call(activation=-1) == INVALID
+    assert call(topk_ids_dtype=2) == INVALID
+    assert call(dtype=B.MOE_DTYPE_FP32) == UNSUPPORTED
+    assert call(group_size=16) == UNSUPPORTED
+    assert call(group_size=0) == UNSUPPORTED
+    assert call(group_size=64, format=B.MOE_W4_E2M1, zeros=None) == UNSUPPORTED
+    assert call(group_size=32, format=B.MOE_W4_E2M1) == UNSUPPORTED  # zeros
+    assert call(matrix_rows=33, activation=B.MOE_ACT_SILU) == SHAPE
+    assert call(num_tokens=0) == OK
+    assert call(top_k=0) == OK
+    assert call(matrix_rows=0) == OK
+    assert call(in_features=0) == SHAPE
+    assert call(in_features=224) == SHAPE
+    assert call(num_experts=0) == SHAPE
+    assert call(num_tokens=513) == UNSUPPORTED
+    assert call(num_experts=1025) == UNSUPPORTED
+    assert call(num_tokens=1025, topk_ids=None) == UNSUPPORTED
+    for name in ("x", "weight", "scales", "out"):
+        assert call(**{name: None}) == INVALID
+    assert call(x_stride0=248) == SHAPE
+    assert call(out_stride0=31) == SHAPE
+    assert call(x_stride0=257) == ALIGNMENT
+    assert call(x=FAKE + 2) == ALIGNMENT
+    assert call(weight=FAKE + 8) == ALIGNMENT
