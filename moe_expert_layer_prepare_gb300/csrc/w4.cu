@@ -4,33 +4,39 @@
 // of the rows n is a gate and y = act(gate) up.
 //
 // The codes are the bytes that count, each read once for up to 8 NT rows, so HBM is the
-// bound and the work around a code has to stay under some three instructions.  Codes
-// become 16-bit numbers without rounding (an integer by its bits behind a power of two
-// that holds all sixteen, then minus that power and the zero point; e2m1 by its bits as
-// sign, exponent and mantissa of a number 2^126 or 2^14 times too small), the products of
-// a group are summed by mma.sync tiles in fp32, and the scale multiplies the group's sum.
+// bound as long as a code costs few instructions: an SM does 64 integer operations a
+// clock and HBM gives it 46 codes.  Codes become fp16 numbers without rounding: an integer
+// by a mask alone, its bits being those of a subnormal number, q 2^-24 or q 2^-20, less the
+// zero point's; e2m1 by the conversion instruction.  So x is brought to fp16 too, each row
+// times a power of two that puts its largest value in [2^14, 2^15): a bf16 value keeps all
+// its bits down to 2^-31 of that, an fp16 value to 2^-28, and what is smaller an error of
+// 2^-40 (2^-36) of it, far below that of the fp32 sums.  The products of a group are summed
+// by mma.sync tiles in fp32; its scale times the row's power multiplies the group's sum.
 //
-// A unit is 16 rows of a matrix (gated: 8 gate rows and their 8 up rows, so that both
-// values of an output meet in one thread's reach) by all of K for up to 8 NT rows of x.
-// Its K blocks of 256 codes are dealt out to the eight warps of a block, each with a ring
-// of cp.async stages of its own that runs ahead across units; the warps' sums are joined
-// in their order.  The k of a tile may come in any order that both operands share: lane c
-// of four takes the codes 8 c .. 8 c + 7 of 32, one word, and the same of x.
+// A unit is 16 rows of a matrix (gated: 8 gate rows and their 8 up rows, so that one lane
+// has both values of an output) by all of K for up to 8 NT rows of x, which a block keeps
+// in shared memory in the order of the codes.  The unit's K blocks of 256 codes are dealt
+// out to the warps of a team, each with a ring of cp.async stages of its own that runs
+// ahead across units; a team's sums are joined in the order of its warps.  The k of a tile
+// may come in any order that both operands share: lane c of four takes the codes 8 c ..
+// 8 c + 7 of 32, one word, and the same of x.
 #include <mutex>
 #include <type_traits>
 
 #include "activation.cuh"
 #include "block_common.cuh"
+#include "tc_common.cuh"
 
 namespace moe {
 namespace w4 {
 
-constexpr int WARPS = 8, THREADS = WARPS * 32;
 constexpr int ROWS = 16;           // of a unit
 constexpr int BLOCK_K = 256;       // codes of a row in a stage: 128 bytes
 constexpr int STAGE = ROWS * 128;  // bytes
-constexpr int STAGES = 5;
 constexpr int MAX_ROUTES = 1024, MAX_EXPERTS = 1024;
+// Columns take registers and x shared memory: fewer warps with more stages each.
+constexpr int warps_of(int nt) { return nt == 1 ? 16 : 8; }
+constexpr int stages_of(int nt) { return nt == 1 ? 3 : 4; }
 
 struct Params {
   int64_t T, K, N;  // N: rows of a matrix
@@ -44,6 +50,8 @@ struct Params {
   const void* ids;       // nullable: one matrix for all rows
   int ids64;
   int act;
+  int most;          // rows of a chunk
+  int team;          // warps that share a unit
   bool wide_scales;  // a block's scales of a row may be read at once
   void* out;
   int64_t out_stride;
@@ -54,145 +62,138 @@ struct Chunk {  // rows of x that share a matrix
   int16_t expert, first, count;
 };
 
-template <typename T, bool E2M1>
-struct Codes;
-// Pair i of a word: codes i and i + 4 as two 16-bit numbers, the lower first.
-template <typename T>
-struct Codes<T, false> {
-  static constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
-  static constexpr uint32_t BASE = BF16 ? 0x43004300u : 0x64006400u;  // 128 or 1024 in both halves
-  // what the numbers have too much: the base and the zero point
-  static __device__ __forceinline__ uint32_t offset(uint32_t zero) { return BASE + zero * 0x10001u; }
-  static __device__ __forceinline__ uint32_t pair(uint32_t w, int i, uint32_t off) {
-    const uint32_t v = ((w >> (4 * i)) & 0x000F000Fu) | BASE;
-    if constexpr (BF16) {
-      const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
-                                       *reinterpret_cast<const __nv_bfloat162*>(&off));
-      return *reinterpret_cast<const uint32_t*>(&d);
-    } else {
-      const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v),
-                                *reinterpret_cast<const __half2*>(&off));
-      return *reinterpret_cast<const uint32_t*>(&d);
+enum Format { INT4 = 0, INT4_ZEROS = 1, E2M1 = 2 };
+
+// The eight codes of a word as fp16 numbers in pairs.
+template <Format F>
+struct Codes {
+  // What a pair has too much, of codes at bits 0 and 16, and of those at 4 and 20: the zero
+  // point, a subnormal number too.
+  static __device__ __forceinline__ uint2 offset(uint32_t zero) {
+    return make_uint2(zero * 0x00010001u, zero * 0x00100010u);
+  }
+  // pair i: codes i and i + 4, times 2^-24 (i even) or 2^-20
+  static __device__ __forceinline__ void pairs(uint32_t w, uint2 off, uint32_t (&d)[4]) {
+    const uint32_t v[4] = {w & 0x000F000Fu, w & 0x00F000F0u, (w >> 8) & 0x000F000Fu,
+                           (w >> 8) & 0x00F000F0u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t o = i % 2 == 0 ? off.x : off.y;
+      const __half2 n = __hsub2(*reinterpret_cast<const __half2*>(&v[i]),
+                                *reinterpret_cast<const __half2*>(&o));
+      d[i] = *reinterpret_cast<const uint32_t*>(&n);
     }
   }
+  // what makes up for the 2^-24: half of it with a row's power, which goes up to 2^113, and
+  // half at the end
+  static constexpr float UNIT = 0x1p12f;
+  // x's eight values in the same order; those that meet codes times 2^-20 are 2^-4 as large
+  static __device__ __forceinline__ uint4 order(const float (&f)[8]) {
+    return make_uint4(pack2<__half>(make_float2(f[0], f[4])),
+                      pack2<__half>(make_float2(f[1] * 0.0625f, f[5] * 0.0625f)),
+                      pack2<__half>(make_float2(f[2], f[6])),
+                      pack2<__half>(make_float2(f[3] * 0.0625f, f[7] * 0.0625f)));
+  }
 };
-template <typename T>
-struct Codes<T, true> {
-  static constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
-  static constexpr int UP = BF16 ? 6 : 9;  // place of the mantissa's bit
-  static __device__ __forceinline__ uint32_t offset(uint32_t) { return 0; }
-  static __device__ __forceinline__ uint32_t pair(uint32_t w, int i, uint32_t) {
-    const int up = UP - 4 * i;
-    const uint32_t v = ((up >= 0 ? w << (up & 31) : w >> (-up & 31)) & (0x00070007u << UP)) |
-                       ((w << (12 - 4 * i)) & 0x80008000u);
-    if constexpr (BF16) {
-      const uint32_t f = 0x7E807E80u;  // 2^126
-      const __nv_bfloat162 d = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v),
-                                       *reinterpret_cast<const __nv_bfloat162*>(&f));
-      return *reinterpret_cast<const uint32_t*>(&d);
-    } else {
-      const uint32_t f = 0x74007400u;  // 2^14
-      const __half2 d =
-          __hmul2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&f));
-      return *reinterpret_cast<const uint32_t*>(&d);
-    }
+// e2m1: neighbouring codes a pair.
+template <>
+struct Codes<E2M1> {
+  static __device__ __forceinline__ uint2 offset(uint32_t) { return make_uint2(0, 0); }
+  static __device__ __forceinline__ void pairs(uint32_t w, uint2, uint32_t (&d)[4]) {
+    asm("{ .reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %4;"
+        " cvt.rn.f16x2.e2m1x2 %0, a; cvt.rn.f16x2.e2m1x2 %1, b;"
+        " cvt.rn.f16x2.e2m1x2 %2, c; cvt.rn.f16x2.e2m1x2 %3, d; }"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+        : "r"(w));
+  }
+  static constexpr float UNIT = 1.0f;
+  static __device__ __forceinline__ uint4 order(const float (&f)[8]) {
+    return make_uint4(pack2<__half>(make_float2(f[0], f[1])), pack2<__half>(make_float2(f[2], f[3])),
+                      pack2<__half>(make_float2(f[4], f[5])), pack2<__half>(make_float2(f[6], f[7])));
   }
 };
 
 // 16 rows by 16 of k times 16 of k by 8 columns, added to d.
-template <typename T>
 __device__ __forceinline__ void mma_tile(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
-  if constexpr (std::is_same<T, __nv_bfloat16>::value)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The scales of a K block of two rows (a lane's): 8 / SPG a row, of T or as exponents.
-template <typename T, bool E2M1, int SPG>
+// The scales of a K block of a row: 8 / SPG of T, or exponents; and zero points.
+template <typename T, Format F, int SPG>
 struct Scales {
   static constexpr int COUNT = 8 / SPG;
-  static constexpr int BYTES = COUNT * (E2M1 ? 1 : 2);
-  static constexpr int WORDS = (BYTES + 3) / 4;
-  uint32_t s[2][WORDS], z[2][2];
+  static constexpr int ITEM = F == E2M1 ? 1 : 2;
+  static constexpr int WORDS = (COUNT * ITEM + 3) / 4;
+  static constexpr int ZWORDS = F == INT4_ZEROS ? (COUNT + 3) / 4 : 1;
+  uint32_t s[WORDS], z[ZWORDS];
 
-  __device__ __forceinline__ float scale(int row, int j) const {
-    if constexpr (E2M1) {
-      const uint32_t e = (s[row][j / 4] >> (8 * (j % 4))) & 0xFFu;
-      // 2^-127 is subnormal; the largest byte is not a number
-      return e == 0 ? __uint_as_float(0x00400000u)
-                    : __uint_as_float(e == 255u ? 0x7FC00000u : e << 23);
-    } else {
-      const float2 v = unpack2<T>(s[row][j / 2]);
-      return j % 2 == 0 ? v.x : v.y;
-    }
+  __device__ __forceinline__ float scale(int j) const {
+    if constexpr (F == E2M1)  // byte 0 is 2^-127, a subnormal number
+      return __uint_as_float(max(((s[j / 4] >> (8 * (j % 4))) & 0xFFu) << 23, 0x00400000u));
+    const float2 v = unpack2<T>(s[j / 2]);
+    return j % 2 == 0 ? v.x : v.y;
   }
-  __device__ __forceinline__ uint32_t zero(int row, int j) const {
-    return (z[row][j / 4] >> (8 * (j % 4))) & 15u;
+  __device__ __forceinline__ uint32_t zero(int j) const {
+    return F == INT4_ZEROS ? (z[j / 4] >> (8 * (j % 4))) & 15u : 8u;
   }
-
-  // of block kb of the rows at `at` (in groups; < 0: no such row)
-  __device__ __forceinline__ void load(const Params& p, const int64_t (&at)[2], int kb) {
-    const int groups = (int)(p.K / (32 * SPG)), g0 = kb * COUNT;
+  // Whether an exponent is 255, which is not a number.
+  __device__ __forceinline__ bool broken() const {
+    uint32_t hit = 0;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-#pragma unroll
-      for (int i = 0; i < WORDS; ++i) s[r][i] = 0;
-      z[r][0] = z[r][1] = 0x08080808u;
-      if (at[r] < 0) continue;
-      const uint8_t* src = static_cast<const uint8_t*>(p.scales) + (at[r] + g0) * (E2M1 ? 1 : 2);
-      const uint8_t* zsrc = p.zeros + (at[r] + g0);
-      if (p.wide_scales) {
-        if constexpr (BYTES == 16) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
-          s[r][0] = v.x, s[r][1] = v.y, s[r][2] = v.z, s[r][3] = v.w;
-        } else if constexpr (BYTES == 8) {
-          const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
-          s[r][0] = v.x, s[r][1] = v.y;
-        } else {
-          s[r][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
-        }
-        if (!E2M1 && p.zeros != nullptr) {
-          if constexpr (COUNT == 8) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(zsrc));
-            z[r][0] = v.x, z[r][1] = v.y;
-          } else if constexpr (COUNT == 4) {
-            z[r][0] = __ldg(reinterpret_cast<const uint32_t*>(zsrc));
-          } else {
-            z[r][0] = __ldg(reinterpret_cast<const uint16_t*>(zsrc));
-          }
-        }
+    for (int i = 0; i < WORDS; ++i)
+      hit |= ((s[i] & 0x7F7F7F7Fu) + 0x01010101u) & s[i] & 0x80808080u;
+    return hit != 0;
+  }
+  // `left` groups of the row exist from here on
+  __device__ __forceinline__ void load(const uint8_t* src, const uint8_t* zsrc, int left, bool wide) {
+    if (wide) {
+      if constexpr (COUNT * ITEM == 16) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
+        s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
+      } else if constexpr (COUNT * ITEM == 8) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+        s[0] = v.x, s[1] = v.y;
       } else {
-#pragma unroll
-        for (int j = 0; j < COUNT; ++j) {
-          if (g0 + j >= groups) break;
-          if constexpr (E2M1)
-            s[r][j / 4] |= (uint32_t)__ldg(src + j) << (8 * (j % 4));
-          else
-            s[r][j / 2] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(src) + j) << (16 * (j % 2));
-          if (!E2M1 && p.zeros != nullptr)
-            z[r][j / 4] = (z[r][j / 4] & ~(0xFFu << (8 * (j % 4)))) |
-                          (uint32_t)__ldg(zsrc + j) << (8 * (j % 4));
+        s[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+      }
+      if constexpr (F == INT4_ZEROS) {
+        if constexpr (COUNT == 8) {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(zsrc));
+          z[0] = v.x, z[1] = v.y;
+        } else if constexpr (COUNT == 4) {
+          z[0] = __ldg(reinterpret_cast<const uint32_t*>(zsrc));
+        } else {
+          z[0] = __ldg(reinterpret_cast<const uint16_t*>(zsrc));
         }
       }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) s[i] = 0;
+#pragma unroll
+    for (int i = 0; i < ZWORDS; ++i) z[i] = 0;
+#pragma unroll
+    for (int j = 0; j < COUNT; ++j) {
+      if (j >= left) break;
+      if constexpr (F == E2M1)
+        s[j / 4] |= (uint32_t)__ldg(src + j) << (8 * (j % 4));
+      else
+        s[j / 2] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(src) + j) << (16 * (j % 2));
+      if constexpr (F == INT4_ZEROS) z[j / 4] |= (uint32_t)__ldg(zsrc + j) << (8 * (j % 4));
     }
   }
 };
 
 // Routes by expert: s_route in the order of the experts, chunks of at most `most`.  Routes
 // without an expert get zeros in out.  All threads of the block call it.
-template <typename T>
+template <typename T, int WARPS>
 __device__ __forceinline__ int sort_routes(const Params& p, int most, int* s_count, int* s_first,
                                            uint16_t* s_route, Chunk* s_chunk, int* s_part) {
+  constexpr int THREADS = WARPS * 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto id_of = [&](int r) {
     return p.ids64 ? static_cast<const int64_t*>(p.ids)[r]
@@ -214,7 +215,7 @@ __device__ __forceinline__ int sort_routes(const Params& p, int most, int* s_cou
     for (int64_t n = tid; n < p.n_out; n += THREADS) out[n] = from_f32<T>(0.0f);
   }
   __syncthreads();
-  // routes and chunks before each expert: four experts a thread, packed into one sum
+  // routes and chunks before each expert, packed into one sum
   constexpr int PER = MAX_EXPERTS / THREADS;
   int mine[PER], total = 0;
 #pragma unroll
@@ -270,217 +271,334 @@ __device__ __forceinline__ int sort_routes(const Params& p, int most, int* s_cou
   return chunks;
 }
 
-__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(there ? 16 : 0)
-               : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-constexpr int red_bytes(int nt) { return 2 * WARPS * ROWS * 8 * nt * 4; }
-constexpr int smem_bytes(int nt, bool experts) {
-  return WARPS * STAGES * STAGE + red_bytes(nt) +
-         (experts ? 2 * MAX_EXPERTS * 4 + MAX_ROUTES * (2 + 6) + 64 : 0);
+// Bytes of a row of x in shared memory: zeros up to a whole block, and 64 bytes so that two
+// rows' neighbouring 64 bytes lie in different banks.
+__host__ __device__ constexpr int64_t x_pitch(int64_t K) {
+  return (K + BLOCK_K - 1) / BLOCK_K * (BLOCK_K * 2) + 64;
 }
 
-template <typename T, bool E2M1, int SPG, int NT, bool EXPERTS>
-__global__ void __launch_bounds__(THREADS, 2) w4_kernel(Params p) {
-  using C = Codes<T, E2M1>;
+constexpr int ring_bytes(int nt) { return warps_of(nt) * stages_of(nt) * STAGE; }
+constexpr int red_bytes(int nt) { return 2 * warps_of(nt) * 32 * 16 * nt; }
+constexpr int route_bytes(bool experts) {
+  return experts ? 2 * MAX_EXPERTS * 4 + MAX_ROUTES * (2 + 6) + 64 : 0;
+}
+constexpr int fixed_bytes(int nt, bool experts) {
+  return ring_bytes(nt) + red_bytes(nt) + route_bytes(experts) + 8 * nt * 4 + warps_of(nt) * 4;
+}
+
+template <typename T, Format F, int SPG, int NT, bool EXPERTS>
+__global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
+  using C = Codes<F>;
+  using S = Scales<T, F, SPG>;
+  constexpr int WARPS = warps_of(NT), STAGES = stages_of(NT), COLS = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
-  float* red = reinterpret_cast<float*>(smem + WARPS * STAGES * STAGE);
+  float4* red = reinterpret_cast<float4*>(smem + ring_bytes(NT));
+  uint8_t* routing = smem + ring_bytes(NT) + red_bytes(NT);
+  float* s_power = reinterpret_cast<float*>(routing + route_bytes(EXPERTS));  // [COLS]
+  uint32_t* s_amax = reinterpret_cast<uint32_t*>(s_power + COLS);             // [WARPS]
+  uint8_t* s_x = reinterpret_cast<uint8_t*>(s_amax + WARPS);
   pdl_wait();
   pdl_launch_dependents();
 
-  constexpr int COLS = 8 * NT;
   Chunk* s_chunk = nullptr;
   uint16_t* s_route = nullptr;
-  int chunks = (int)((p.T + COLS - 1) / COLS);
+  int chunks = (int)((p.T + p.most - 1) / p.most);
   if constexpr (EXPERTS) {
-    int* s_count = reinterpret_cast<int*>(smem + WARPS * STAGES * STAGE + red_bytes(NT));
+    int* s_count = reinterpret_cast<int*>(routing);
     int* s_first = s_count + MAX_EXPERTS;
     int* s_part = s_first + MAX_EXPERTS;
     s_route = reinterpret_cast<uint16_t*>(s_part + 16);
     s_chunk = reinterpret_cast<Chunk*>(s_route + MAX_ROUTES);
-    chunks = sort_routes<T>(p, COLS, s_count, s_first, s_route, s_chunk, s_part);
+    chunks = sort_routes<T, WARPS>(p, p.most, s_count, s_first, s_route, s_chunk, s_part);
   }
   const bool gated = p.act != MOE_ACT_NONE;
   const int tile_out = gated ? ROWS / 2 : ROWS;
   const int tiles = (int)((p.n_out + tile_out - 1) / tile_out);
   const int64_t units = (int64_t)chunks * tiles;
+  const int blocks = (int)((p.K + BLOCK_K - 1) / BLOCK_K);
+  const int pitch = (int)(p.K / 2);  // bytes of a row
+  const int xp = (int)x_pitch(p.K);
   const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
   if (u0 == u1) return;
-  const int blocks = (int)((p.K + BLOCK_K - 1) / BLOCK_K);
-  const int64_t pitch = p.K / 2;  // bytes of a row
 
-  // Row r of unit u as a row of all matrices, -1 where there is none.
-  auto row_of = [&](int64_t u, int r) -> int64_t {
-    const int chunk = (int)(u / tiles);
-    const int64_t n0 = (u - (int64_t)chunk * tiles) * tile_out;
-    const int64_t base = EXPERTS ? (int64_t)s_chunk[chunk].expert * p.N : 0;
-    if (!gated) return n0 + r < p.N ? base + n0 + r : -1;
-    if (n0 + (r & 7) >= p.n_out) return -1;
-    return base + n0 + (r & 7) + (r >= 8 ? p.n_out : 0);
-  };
-
-  // This warp's blocks: every WARPS-th of the sequence (unit, block) of the CTA's units.
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * STAGES * STAGE;
+  // The CTA's units lie in one or a few chunks, one after another.  A chunk's are dealt out
+  // to teams of p.team warps, a unit's blocks to the team's warps.
+  const int teams = WARPS / p.team, team = warp / p.team, member = warp % p.team;
+  const int chunk0 = (int)(u0 / tiles), chunk1 = (int)((u1 - 1) / tiles);
+  auto tile_begin = [&](int chunk) { return chunk == chunk0 ? (int)(u0 - (int64_t)chunk * tiles) : 0; };
+  auto tile_end = [&](int chunk) { return chunk == chunk1 ? (int)(u1 - (int64_t)chunk * tiles) : tiles; };
   struct Place {
-    int64_t u;
-    int kb;
+    int chunk, tile;
   };
-  auto next = [&](Place& q) {
-    q.kb += WARPS;
-    while (q.kb >= blocks) q.kb -= blocks, ++q.u;
+  auto settle = [&](Place& q) {  // on to the next chunk that has a unit for this team
+    while (q.chunk <= chunk1 && q.tile >= tile_end(q.chunk)) {
+      ++q.chunk;
+      q.tile = team;
+      if (q.chunk <= chunk1) q.tile += tile_begin(q.chunk);
+    }
   };
-  Place ahead{u0, warp};
-  while (ahead.kb >= blocks) ahead.kb -= blocks, ++ahead.u;
-  Place at = ahead;
-  auto fetch = [&](int stage) {
-    if (ahead.u < u1) {
+  auto next_unit = [&](Place& q) {
+    q.tile += teams;
+    settle(q);
+  };
+  Place unit{chunk0, tile_begin(chunk0) + team};
+  settle(unit);
+  // Row r of a unit as a row of all matrices; past the last one the last, whose results are
+  // computed again and not stored.
+  auto row_of = [&](const Place& q, int r) -> int64_t {
+    const int64_t base = EXPERTS ? (int64_t)s_chunk[q.chunk].expert * p.N : 0;
+    const int64_t n = (int64_t)q.tile * tile_out + (gated ? r & 7 : r);
+    return base + min(n, p.n_out - 1) + (gated && r >= 8 ? p.n_out : 0);
+  };
+
+  // Copies run STAGES - 1 blocks ahead, scales one.
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * STAGES * STAGE;
+  Place ahead = unit;
+  int ahead_kb = member;
+  const uint8_t* from[4];  // this lane's 16 bytes of four rows
+  auto aim = [&] {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = i * 4 + (lane >> 3), j = lane & 7;
-        const int64_t row = row_of(ahead.u, r);
-        const int64_t byte = (int64_t)ahead.kb * 128 + j * 16;
-        const bool there = row >= 0 && byte < pitch;
-        copy16_or_zero(ring + stage * STAGE + r * 128 + ((j ^ (r & 7)) << 4),
-                       there ? p.w + row * pitch + byte : p.w, there);
+    for (int i = 0; i < 4; ++i)
+      from[i] = p.w + row_of(ahead, i * 4 + (lane >> 3)) * pitch + (lane & 7) * 16;
+  };
+  const uint32_t to = ring + (lane >> 3) * 128;
+  uint32_t at_piece[2];  // rows r and r + 4 differ in the permutation
+#pragma unroll
+  for (int i = 0; i < 2; ++i) at_piece[i] = ((lane & 7) ^ (((lane >> 3) + 4 * i) & 7)) << 4;
+  auto fetch = [&](int stage) {
+    if (ahead.chunk <= chunk1) {
+      const int byte = ahead_kb * 128;
+      if (byte + (lane & 7) * 16 < pitch) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          copy16(to + stage * STAGE + i * 512 + at_piece[i & 1], from[i] + byte);
       }
-      next(ahead);
+      ahead_kb += p.team;
+      if (ahead_kb >= blocks) {
+        ahead_kb = member;
+        next_unit(ahead);
+        if (ahead.chunk <= chunk1) aim();
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  if (ahead.chunk <= chunk1) aim();
 #pragma unroll
   for (int s = 0; s < STAGES - 1; ++s) fetch(s);
 
   const int groups = (int)(p.K / (32 * SPG));
-  auto scale_rows = [&](const Place& q, int64_t (&rows)[2]) {
+  S sc[2], sc_next[2];
+  int64_t scales_at[2];  // this lane's rows of the unit, in groups
+  auto aim_scales = [&](const Place& q) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int64_t row = q.u < u1 ? row_of(q.u, g + 8 * r) : -1;
-      rows[r] = row < 0 ? -1 : row * groups;
-    }
+    for (int r = 0; r < 2; ++r) scales_at[r] = row_of(q, g + 8 * r) * groups;
   };
-  Scales<T, E2M1, SPG> sc;
-  {
-    int64_t rows[2];
-    scale_rows(at, rows);
-    sc.load(p, rows, at.kb);
+  auto fetch_scales = [&](int kb) {
+    const int j = kb * S::COUNT;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      sc_next[r].load(static_cast<const uint8_t*>(p.scales) + (scales_at[r] + j) * S::ITEM,
+                      p.zeros + (scales_at[r] + j), groups - j, p.wide_scales);
+  };
+  if (unit.chunk <= chunk1) {
+    aim_scales(unit);
+    fetch_scales(member);
   }
 
-  int stage = 0, buf = 0;
-  for (int64_t u = u0; u < u1; ++u, buf ^= 1) {
-    const int chunk = (int)(u / tiles);
-    int first = chunk * COLS, count = (int)min((int64_t)COLS, p.T - first);
+  // a lane's row of two 32-code pieces for ldmatrix
+  const uint32_t lane_row = (lane & 15) * 128, lane_piece = ((lane >> 4) ^ (lane & 7)) << 4;
+  int stage = 0, buf = 0, turn = 0;
+  for (int chunk = chunk0; chunk <= chunk1; ++chunk) {
+    int first = chunk * p.most, count = (int)min((int64_t)p.most, p.T - first);
     if constexpr (EXPERTS) first = s_chunk[chunk].first, count = s_chunk[chunk].count;
-    const T* xr[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int col = t * 8 + g;
-      xr[t] = nullptr;
-      if (col < count) {
-        int row = first + col;
-        if constexpr (EXPERTS) row = s_route[row] / p.top_k;
-        xr[t] = static_cast<const T*>(p.x) + row * p.x_stride + c * 8;
-      }
-    }
-    float acc[NT][4];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[t][e] = 0.0f;
+    auto row_of_x = [&](int col) {
+      int row = first + col;
+      if constexpr (EXPERTS) row = s_route[row] / p.top_k;
+      return static_cast<const T*>(p.x) + row * p.x_stride;
+    };
 
-    while (at.u == u) {
-      const int kb = at.kb;
-      next(at);
-      Scales<T, E2M1, SPG> sc_next;
-      {
-        int64_t rows[2];
-        scale_rows(at, rows);
-        sc_next.load(p, rows, at.kb);
-      }
-      fetch((stage + STAGES - 1) % STAGES);
-      asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
-      __syncwarp();
-      const uint32_t base = ring + stage * STAGE;
-      const int steps = min(8, (int)((p.K - (int64_t)kb * BLOCK_K) / 32));
-      float part[NT][4];
+    // The chunk's rows of x: copied as they are, then brought to fp16 in place, each piece
+    // by the thread that copied it.  A row has as many warps as there are for each.
+    __syncthreads();  // the last chunk's are no longer read
+    int per = WARPS;
+    while (per > 1 && per * count > WARPS) per >>= 1;
+    const int pieces = blocks * (BLOCK_K / 8), real = (int)(p.K / 8);
+    for (int col0 = 0; col0 < count; col0 += WARPS / per) {
+      const int col = col0 + warp / per, lane0 = (warp % per) * 32 + lane;
+      uint32_t most = 0;
+      if (col < count) {
+        const uint4* src = reinterpret_cast<const uint4*>(row_of_x(col));
+        uint4* dst = reinterpret_cast<uint4*>(s_x + col * xp);
+        for (int i = lane0; i < pieces; i += per * 32) {
+          const uint4 v = i < real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+          dst[i] = v;
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        if (s >= steps) break;
-        const int j = s / SPG;
-        if (s % SPG == 0) {
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) part[t][e] = 0.0f;
-        }
-        // words of rows g and g + 8
-        uint32_t w0, w1;
-        {
-          const int r = lane & 15;
-          const uint32_t addr = base + r * 128 + ((s ^ (r & 7)) << 4);
-          asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];"
-                       : "=r"(w0), "=r"(w1)
-                       : "r"(addr)
-                       : "memory");
-        }
-        const uint32_t o0 = C::offset(sc.zero(0, j)), o1 = C::offset(sc.zero(1, j));
-        const uint32_t a0[4] = {C::pair(w0, 0, o0), C::pair(w1, 0, o1), C::pair(w0, 1, o0),
-                                C::pair(w1, 1, o1)};
-        const uint32_t a1[4] = {C::pair(w0, 2, o0), C::pair(w1, 2, o1), C::pair(w0, 3, o0),
-                                C::pair(w1, 3, o1)};
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (xr[t] != nullptr)
-            v = __ldg(reinterpret_cast<const uint4*>(xr[t] + kb * BLOCK_K + s * 32));
-          mma_tile<T>(part[t], a0, __byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632));
-          mma_tile<T>(part[t], a1, __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
-        }
-        if (s % SPG == SPG - 1) {
-          const float s0 = sc.scale(0, j), s1 = sc.scale(1, j);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            acc[t][0] = fmaf(s0, part[t][0], acc[t][0]);
-            acc[t][1] = fmaf(s0, part[t][1], acc[t][1]);
-            acc[t][2] = fmaf(s1, part[t][2], acc[t][2]);
-            acc[t][3] = fmaf(s1, part[t][3], acc[t][3]);
+          for (int e = 0; e < 8; ++e) {  // the largest finite value, by its bits
+            const uint32_t m = (u[e / 2] >> (16 * (e & 1))) & 0x7FFFu;
+            constexpr uint32_t INF = std::is_same<T, __nv_bfloat16>::value ? 0x7F80u : 0x7C00u;
+            most = max(most, m < INF ? m : 0u);
           }
         }
       }
-      sc = sc_next;
-      __syncwarp();  // the stage is free
-      if (++stage == STAGES) stage = 0;
+      most = __reduce_max_sync(0xFFFFFFFFu, most);
+      if (lane == 0) s_amax[warp] = most;
+      __syncthreads();
+      if (col < count) {
+        for (int w = warp / per * per; w < (warp / per + 1) * per; ++w) most = max(most, s_amax[w]);
+        const T big = *reinterpret_cast<const T*>(&most);
+        // 2^(14 - e) of a largest value in [2^e, 2^(e + 1)); of the smallest ones 2^100
+        const int e = max((int)(__float_as_uint(to_f32(big)) >> 23) - 127, -86);
+        const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+        uint4* dst = reinterpret_cast<uint4*>(s_x + col * xp);
+        for (int i = lane0; i < pieces; i += per * 32) {
+          const uint4 v = dst[i];
+          const float2 f0 = unpack2<T>(v.x), f1 = unpack2<T>(v.y), f2 = unpack2<T>(v.z),
+                       f3 = unpack2<T>(v.w);
+          const float f[8] = {f0.x * up, f0.y * up, f1.x * up, f1.y * up,
+                              f2.x * up, f2.y * up, f3.x * up, f3.y * up};
+          dst[i] = C::order(f);
+        }
+        if (lane0 == 0) s_power[col] = __uint_as_float((uint32_t)(127 - 14 + e) << 23) * C::UNIT;
+      }
+      __syncthreads();
     }
-
-    // sums of the warps, [warp][column][row]
-    float* mine = red + (buf * WARPS + warp) * (ROWS * COLS);
+    const uint8_t* xr[NT];
+    float power[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int col = t * 8 + 2 * c;
-      mine[col * ROWS + g] = acc[t][0];
-      mine[(col + 1) * ROWS + g] = acc[t][1];
-      mine[col * ROWS + g + 8] = acc[t][2];
-      mine[(col + 1) * ROWS + g + 8] = acc[t][3];
-    }
-    __syncthreads();
-    const float* all = red + buf * WARPS * (ROWS * COLS);
-    const int64_t n0 = (u - (int64_t)chunk * tiles) * tile_out;
-    for (int i = tid; i < tile_out * count; i += THREADS) {
-      const int col = i / tile_out, r = i % tile_out;
-      float v = 0.0f, up = 0.0f;
+      // columns without a row take the first one's; they are not stored
+      const int col = t * 8 + g;
+      xr[t] = s_x + (col < count ? col : 0) * xp + c * 16;
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        v += all[(w * COLS + col) * ROWS + r];
-        if (gated) up += all[(w * COLS + col) * ROWS + r + 8];
+      for (int e = 0; e < 2; ++e) {
+        const int of = t * 8 + 2 * c + e;
+        power[t][e] = s_power[of < count ? of : 0];
       }
-      if (gated) v = act_value(p.act, v) * up;
-      int row = first + col;
-      if constexpr (EXPERTS) row = s_route[row];
-      if (n0 + r < p.n_out)
-        (static_cast<T*>(p.out) + row * p.out_stride)[n0 + r] = from_f32<T>(v);
+    }
+
+    for (; unit.chunk == chunk; next_unit(unit), buf ^= 1) {
+      float acc[NT][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[t][e] = 0.0f;
+
+      for (int kb = member; kb < blocks; kb += p.team) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) sc[r] = sc_next[r];
+        if (kb + p.team < blocks) {
+          fetch_scales(kb + p.team);
+        } else {
+          Place q = unit;
+          next_unit(q);
+          if (q.chunk <= chunk1) {
+            aim_scales(q);
+            fetch_scales(member);
+          }
+        }
+        fetch(stage == 0 ? STAGES - 1 : stage - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+        __syncwarp();
+        const uint32_t base = ring + stage * STAGE + lane_row;
+        float part[NT][4];
+#pragma unroll
+        for (int s = 0; s < 8; s += 2) {
+          uint32_t w[4];  // words of rows g and g + 8 of 32 codes, then of the next 32
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                       : "r"(base + (lane_piece ^ (s << 4))));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int j = (s + i) / SPG;
+            if ((s + i) % SPG == 0) {
+#pragma unroll
+              for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) part[t][e] = 0.0f;
+            }
+            uint32_t d0[4], d1[4];
+            C::pairs(w[2 * i], C::offset(sc[0].zero(j)), d0);
+            C::pairs(w[2 * i + 1], C::offset(sc[1].zero(j)), d1);
+            const uint32_t a0[4] = {d0[0], d1[0], d0[1], d1[1]};
+            const uint32_t a1[4] = {d0[2], d1[2], d0[3], d1[3]};
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const uint4 v = *reinterpret_cast<const uint4*>(xr[t] + kb * (BLOCK_K * 2) + (s + i) * 64);
+              mma_tile(part[t], a0, v.x, v.y);
+              mma_tile(part[t], a1, v.z, v.w);
+            }
+            if ((s + i) % SPG == SPG - 1) {
+              const float s0 = sc[0].scale(j), s1 = sc[1].scale(j);
+#pragma unroll
+              for (int t = 0; t < NT; ++t) {
+                acc[t][0] = fmaf(s0 * power[t][0], part[t][0], acc[t][0]);
+                acc[t][1] = fmaf(s0 * power[t][1], part[t][1], acc[t][1]);
+                acc[t][2] = fmaf(s1 * power[t][0], part[t][2], acc[t][2]);
+                acc[t][3] = fmaf(s1 * power[t][1], part[t][3], acc[t][3]);
+              }
+            }
+          }
+        }
+        if constexpr (F == E2M1) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            if (sc[r].broken()) {
+#pragma unroll
+              for (int t = 0; t < NT; ++t)
+                acc[t][2 * r] = acc[t][2 * r + 1] = __uint_as_float(0x7FC00000u);
+            }
+        }
+        __syncwarp();  // the stage is free
+        if (++stage == STAGES) stage = 0;
+      }
+
+      if (p.team > 1) {  // join the team's sums in one of its warps, in turn
+        float4* sums = red + (buf * WARPS + team * p.team) * (32 * NT) + lane;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          sums[(member * NT + t) * 32] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+        asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(p.team * 32) : "memory");
+        const bool mine = turn == member;
+        if (++turn == p.team) turn = 0;
+        if (!mine) continue;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float4 v = sums[t * 32];
+          for (int m = 1; m < p.team; ++m) {
+            const float4 o = sums[(m * NT + t) * 32];
+            v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+          }
+          acc[t][0] = v.x, acc[t][1] = v.y, acc[t][2] = v.z, acc[t][3] = v.w;
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[t][e] *= C::UNIT;
+      const int64_t n0 = (int64_t)unit.tile * tile_out;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int col = t * 8 + 2 * c + e;
+          if (col >= count) continue;
+          int row = first + col;
+          if constexpr (EXPERTS) row = s_route[row];
+          T* out = static_cast<T*>(p.out) + row * p.out_stride + n0 + g;
+          if (gated) {
+            if (n0 + g < p.n_out) *out = from_f32<T>(act_value(p.act, acc[t][e]) * acc[t][2 + e]);
+          } else {
+            if (n0 + g < p.n_out) out[0] = from_f32<T>(acc[t][e]);
+            if (n0 + g + 8 < p.n_out) out[8] = from_f32<T>(acc[t][2 + e]);
+          }
+        }
     }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -493,54 +611,66 @@ namespace moe_host {
 
 namespace w4 = moe::w4;
 
-template <typename T, bool E2M1, int SPG, int NT, bool EXPERTS>
-static moe_status_t launch_w4(const w4::Params& p, cudaStream_t s) {
-  constexpr auto kernel = w4::w4_kernel<T, E2M1, SPG, NT, EXPERTS>;
-  constexpr int smem = w4::smem_bytes(NT, EXPERTS);
-  static std::mutex mu;
-  static int resident[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
-    return set_error(MOE_ERR_CUDA, "no current device");
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (resident[dev] == 0) {
-      int n = 0;
-      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      if (e == cudaSuccess)
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, w4::THREADS, smem);
-      if (e != cudaSuccess || n < 1)
-        return set_error(MOE_ERR_CUDA, "4-bit products: %s", cudaGetErrorString(e));
-      resident[dev] = n;
-    }
-  }
+constexpr int kW4Smem = 232448 - 1024;
+
+// Rows of x that a block has room for.
+static int w4_room(int nt, bool experts, int64_t K) {
+  const int64_t n = (kW4Smem - w4::fixed_bytes(nt, experts)) / w4::x_pitch(K);
+  return (int)(n < 8 * nt ? n : 8 * nt);
+}
+
+template <typename T, w4::Format F, int SPG, int NT, bool EXPERTS>
+static moe_status_t launch_w4(w4::Params p, cudaStream_t s) {
+  constexpr auto kernel = w4::w4_kernel<T, F, SPG, NT, EXPERTS>;
+  moe_status_t st = allow_smem<kernel>(kW4Smem);
+  if (st != MOE_OK) return st;
+  const int room = w4_room(NT, EXPERTS, p.K);
+  // with experts a chunk has no more rows than there are; the likely number of chunks is one
+  // an expert of a short batch
+  const int64_t rows = EXPERTS ? p.routes : p.T;
+  const int64_t passes = (rows + room - 1) / room;
+  p.most = EXPERTS ? (int)(rows < room ? rows : room) : (int)((rows + passes - 1) / passes);
   const int tile = p.act == MOE_ACT_NONE ? w4::ROWS : w4::ROWS / 2;
   const int64_t tiles = (p.n_out + tile - 1) / tile;
-  const int64_t cap = (int64_t)num_sms() * resident[dev];
-  // with experts at most a chunk a route
-  int64_t units = tiles * (EXPERTS ? p.routes : (p.T + 8 * NT - 1) / (8 * NT));
-  const unsigned grid = (unsigned)(units < cap ? units : cap);
-  return launched(launch_pdl(kernel, dim3(grid), dim3(w4::THREADS), (size_t)smem, s, p),
+  const int64_t chunks = EXPERTS ? p.routes : passes;
+  const int64_t likely = EXPERTS && p.E < chunks ? p.E : chunks;
+  const int64_t ctas = num_sms(), blocks = (p.K + w4::BLOCK_K - 1) / w4::BLOCK_K;
+  // Two blocks a warp at least, one where a CTA has but one unit.
+  constexpr int WARPS = w4::warps_of(NT);
+  const int64_t share = tiles * likely <= ctas ? 1 : 2;
+  p.team = 1;
+  while (p.team < WARPS && p.team * 2 * share <= blocks) p.team *= 2;
+  const int64_t units = tiles * chunks;
+  const size_t smem = (size_t)w4::fixed_bytes(NT, EXPERTS) + (size_t)(p.most * w4::x_pitch(p.K));
+  return launched(launch_pdl(kernel, dim3((unsigned)(units < ctas ? units : ctas)), dim3(WARPS * 32),
+                             smem, s, p),
                   "4-bit products");
 }
 
-template <typename T, bool E2M1, int SPG>
+template <typename T, w4::Format F, int SPG>
 static moe_status_t run_w4(const w4::Params& p, cudaStream_t s) {
   if (p.ids != nullptr) {
     // most experts of a short batch have one or two of its routes
-    if (p.routes <= 8 * p.E) return launch_w4<T, E2M1, SPG, 1, true>(p, s);
-    return launch_w4<T, E2M1, SPG, 2, true>(p, s);
+    if (p.routes <= 8 * p.E) return launch_w4<T, F, SPG, 1, true>(p, s);
+    return launch_w4<T, F, SPG, 2, true>(p, s);
   }
-  if (p.T <= 8) return launch_w4<T, E2M1, SPG, 1, false>(p, s);
-  return launch_w4<T, E2M1, SPG, 2, false>(p, s);
+  // as few passes over the matrix as there can be, and then as few columns of zeros
+  const int64_t one = w4_room(1, false, p.K), two = w4_room(2, false, p.K);
+  if ((p.T + one - 1) / one <= (p.T + two - 1) / two) return launch_w4<T, F, SPG, 1, false>(p, s);
+  return launch_w4<T, F, SPG, 2, false>(p, s);
 }
 
 template <typename T>
 static moe_status_t run_w4_format(const w4::Params& p, int format, int64_t group, cudaStream_t s) {
-  if (format == MOE_W4_E2M1) return run_w4<T, true, 1>(p, s);
-  if (group == 32) return run_w4<T, false, 1>(p, s);
-  if (group == 64) return run_w4<T, false, 2>(p, s);
-  return run_w4<T, false, 4>(p, s);
+  if (format == MOE_W4_E2M1) return run_w4<T, w4::E2M1, 1>(p, s);
+  if (p.zeros != nullptr) {
+    if (group == 32) return run_w4<T, w4::INT4_ZEROS, 1>(p, s);
+    if (group == 64) return run_w4<T, w4::INT4_ZEROS, 2>(p, s);
+    return run_w4<T, w4::INT4_ZEROS, 4>(p, s);
+  }
+  if (group == 32) return run_w4<T, w4::INT4, 1>(p, s);
+  if (group == 64) return run_w4<T, w4::INT4, 2>(p, s);
+  return run_w4<T, w4::INT4, 4>(p, s);
 }
 
 }  // namespace moe_host
@@ -582,8 +712,8 @@ moe_status_t moe_w4_linear(const moe_w4_linear_args_t* a, void* stream) {
                      w4::MAX_EXPERTS);
   if (!experts && T > w4::MAX_ROUTES)
     return set_error(MOE_ERR_UNSUPPORTED, "at most %d rows", w4::MAX_ROUTES);
-  if (K >= ((int64_t)1 << 28) || N >= ((int64_t)1 << 28))
-    return set_error(MOE_ERR_UNSUPPORTED, "matrix too large");
+  if (K > 32768 || N >= ((int64_t)1 << 28))
+    return set_error(MOE_ERR_UNSUPPORTED, "in_features above 32768 or too many rows of a matrix");
   if (!a->x || !a->weight || !a->scales || !a->out)
     return set_error(MOE_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
   if ((T > 1 && a->x_stride0 < K) || (rows > 1 && a->out_stride0 < n_out))
