@@ -874,7 +874,7 @@ size_t moe_gated_linear_workspace_size(int64_t num_tokens, int64_t in_features,
 /* own; weight, scales and zeros contiguous; bf16 or fp16.                     */
 /* Errors: K % G, an odd N with an activation -> SHAPE; G other than 32, 64,    */
 /* 128 (E2M1: 32), zeros with E2M1, more than 1024 rows of out (routes), E >    */
-/* 1024, K > 32768, fp32 -> UNSUPPORTED; x, weight or x's rows not on 16-byte boundaries    */
+/* 1024, K > 32768, N >= 2^20, fp32 -> UNSUPPORTED; x, weight or x's rows    */
 /* -> ALIGNMENT.                                                              */
 /* ------------------------------------------------------------------------ */
 typedef struct moe_w4_linear_args {

@@ -14,12 +14,13 @@
 // by mma.sync tiles in fp32; its scale times the row's power multiplies the group's sum.
 //
 // A unit is 16 rows of a matrix (gated: 8 gate rows and their 8 up rows, so that one lane
-// has both values of an output) by all of K for up to 8 NT rows of x, which a block keeps
-// in shared memory in the order of the codes.  The unit's K blocks of 256 codes are dealt
-// out to the warps of a team, each with a ring of cp.async stages of its own that runs
-// ahead across units; a team's sums are joined in the order of its warps.  The k of a tile
-// may come in any order that both operands share: lane c of four takes the codes 8 c ..
-// 8 c + 7 of 32, one word, and the same of x.
+// has both values of an output) by all of K for up to 8 NT rows of x, which a CTA keeps
+// in shared memory in the order of the codes.  The K blocks of 256 codes of the CTA's units
+// are one sequence, cut into a run for each warp, equal to one block; a warp stores the
+// units that are all its own, and those cut between warps are joined in the warps' order.
+// So no warp waits for another on the way, each with a ring of cp.async stages of its own.
+// The k of a tile may come in any order that both operands share: lane c of four takes the
+// codes 8 c .. 8 c + 7 of 32, one word, and the same of x.
 #include <mutex>
 #include <type_traits>
 
@@ -34,9 +35,10 @@ constexpr int ROWS = 16;           // of a unit
 constexpr int BLOCK_K = 256;       // codes of a row in a stage: 128 bytes
 constexpr int STAGE = ROWS * 128;  // bytes
 constexpr int MAX_ROUTES = 1024, MAX_EXPERTS = 1024;
-// Columns take registers and x shared memory: fewer warps with more stages each.
+// Columns take registers: fewer warps.
 constexpr int warps_of(int nt) { return nt == 1 ? 16 : 8; }
-constexpr int stages_of(int nt) { return nt == 1 ? 3 : 4; }
+// Stages of a warp's ring, as x leaves room.
+constexpr int MIN_STAGES = 3;
 
 struct Params {
   int64_t T, K, N;  // N: rows of a matrix
@@ -51,7 +53,7 @@ struct Params {
   int ids64;
   int act;
   int most;          // rows of a chunk
-  int team;          // warps that share a unit
+  int stages;        // of a warp's ring: 3, 4 or 6
   bool wide_scales;  // a block's scales of a row may be read at once
   void* out;
   int64_t out_stride;
@@ -113,13 +115,19 @@ struct Codes<E2M1> {
   }
 };
 
-// 16 rows by 16 of k times 16 of k by 8 columns, added to d.
+// 16 rows by 16 of k times 16 of k by 8 columns, added to d, or the first of a sum.
 __device__ __forceinline__ void mma_tile(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                                         uint32_t b1, bool first) {
+  if (first)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // The scales of a K block of a row: 8 / SPG of T, or exponents; and zero points.
@@ -131,22 +139,20 @@ struct Scales {
   static constexpr int ZWORDS = F == INT4_ZEROS ? (COUNT + 3) / 4 : 1;
   uint32_t s[WORDS], z[ZWORDS];
 
-  __device__ __forceinline__ float scale(int j) const {
-    if constexpr (F == E2M1)  // byte 0 is 2^-127, a subnormal number
-      return __uint_as_float(max(((s[j / 4] >> (8 * (j % 4))) & 0xFFu) << 23, 0x00400000u));
-    const float2 v = unpack2<T>(s[j / 2]);
-    return j % 2 == 0 ? v.x : v.y;
+  // scales 2 i and 2 i + 1
+  __device__ __forceinline__ float2 scales(int i) const {
+    if constexpr (F == E2M1) {
+      uint32_t d;  // exponents are bf16 numbers too, 2^-127 a subnormal one and 255 none
+      if (i % 2 == 0)
+        asm("{ .reg .b16 a, b; mov.b32 {a, b}, %1; cvt.rn.bf16x2.ue8m0x2 %0, a; }" : "=r"(d) : "r"(s[i / 2]));
+      else
+        asm("{ .reg .b16 a, b; mov.b32 {a, b}, %1; cvt.rn.bf16x2.ue8m0x2 %0, b; }" : "=r"(d) : "r"(s[i / 2]));
+      return unpack2<__nv_bfloat16>(d);
+    }
+    return unpack2<T>(s[i]);
   }
   __device__ __forceinline__ uint32_t zero(int j) const {
     return F == INT4_ZEROS ? (z[j / 4] >> (8 * (j % 4))) & 15u : 8u;
-  }
-  // Whether an exponent is 255, which is not a number.
-  __device__ __forceinline__ bool broken() const {
-    uint32_t hit = 0;
-#pragma unroll
-    for (int i = 0; i < WORDS; ++i)
-      hit |= ((s[i] & 0x7F7F7F7Fu) + 0x01010101u) & s[i] & 0x80808080u;
-    return hit != 0;
   }
   // `left` groups of the row exist from here on
   __device__ __forceinline__ void load(const uint8_t* src, const uint8_t* zsrc, int left, bool wide) {
@@ -271,6 +277,45 @@ __device__ __forceinline__ int sort_routes(const Params& p, int most, int* s_cou
   return chunks;
 }
 
+// The same for at most 32 routes, a lane each of one warp; chunks in the order of their
+// first routes.
+template <typename T, int WARPS>
+__device__ __forceinline__ int sort_few_routes(const Params& p, int most, uint16_t* s_route,
+                                               Chunk* s_chunk, int* s_part) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid < 32) {
+    const int64_t id = lane >= p.routes ? -1
+                       : p.ids64        ? static_cast<const int64_t*>(p.ids)[lane]
+                                        : (int64_t) static_cast<const int32_t*>(p.ids)[lane];
+    const int e = id >= 0 && id < p.E ? (int)id : -1;
+    if (id >= p.E) set_status(p.status, MOE_DEV_BAD_EXPERT);
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+    const int rank = __popc(same & lanemask_lt()), count = __popc(same);
+    const bool leads = e >= 0 && rank % most == 0;
+    const uint32_t leaders = __ballot_sync(0xFFFFFFFFu, leads);
+    // routes in the order of the experts' first ones: behind all routes of those before
+    int first = 0;
+    for (uint32_t m = __ballot_sync(0xFFFFFFFFu, e >= 0 && rank == 0); m != 0; m &= m - 1) {
+      const int l = __ffs(m) - 1, n = __shfl_sync(0xFFFFFFFFu, count, l);
+      if (l < __ffs(same) - 1) first += n;
+    }
+    if (e >= 0) s_route[first + rank] = (uint16_t)lane;
+    if (leads)
+      s_chunk[__popc(leaders & lanemask_lt())] =
+          Chunk{(int16_t)e, (int16_t)(first + rank), (int16_t)min(most, count - rank)};
+    const uint32_t without = __ballot_sync(0xFFFFFFFFu, lane < p.routes && e < 0);
+    if (lane == 0) s_part[0] = __popc(leaders), s_part[1] = (int)without;
+  }
+  __syncthreads();
+  for (uint32_t m = (uint32_t)s_part[1]; m != 0; m &= m - 1) {
+    const int r = __ffs(m) - 1;
+    if ((unsigned)r % gridDim.x != blockIdx.x) continue;
+    T* out = static_cast<T*>(p.out) + r * p.out_stride;
+    for (int64_t n = tid; n < p.n_out; n += WARPS * 32) out[n] = from_f32<T>(0.0f);
+  }
+  return s_part[0];
+}
+
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -281,25 +326,25 @@ __host__ __device__ constexpr int64_t x_pitch(int64_t K) {
   return (K + BLOCK_K - 1) / BLOCK_K * (BLOCK_K * 2) + 64;
 }
 
-constexpr int ring_bytes(int nt) { return warps_of(nt) * stages_of(nt) * STAGE; }
+constexpr int ring_bytes(int nt, int stages) { return warps_of(nt) * stages * STAGE; }
 constexpr int red_bytes(int nt) { return 2 * warps_of(nt) * 32 * 16 * nt; }
 constexpr int route_bytes(bool experts) {
   return experts ? 2 * MAX_EXPERTS * 4 + MAX_ROUTES * (2 + 6) + 64 : 0;
 }
-constexpr int fixed_bytes(int nt, bool experts) {
-  return ring_bytes(nt) + red_bytes(nt) + route_bytes(experts) + 8 * nt * 4 + warps_of(nt) * 4;
+constexpr int fixed_bytes(int nt, bool experts) {  // beside the ring and x
+  return red_bytes(nt) + route_bytes(experts) + 8 * nt * 4 + warps_of(nt) * 4;
 }
 
 template <typename T, Format F, int SPG, int NT, bool EXPERTS>
 __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
   using C = Codes<F>;
   using S = Scales<T, F, SPG>;
-  constexpr int WARPS = warps_of(NT), STAGES = stages_of(NT), COLS = 8 * NT;
+  constexpr int WARPS = warps_of(NT), COLS = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
-  float4* red = reinterpret_cast<float4*>(smem + ring_bytes(NT));
-  uint8_t* routing = smem + ring_bytes(NT) + red_bytes(NT);
+  float4* red = reinterpret_cast<float4*>(smem + ring_bytes(NT, p.stages));
+  uint8_t* routing = reinterpret_cast<uint8_t*>(red) + red_bytes(NT);
   float* s_power = reinterpret_cast<float*>(routing + route_bytes(EXPERTS));  // [COLS]
   uint32_t* s_amax = reinterpret_cast<uint32_t*>(s_power + COLS);             // [WARPS]
   uint8_t* s_x = reinterpret_cast<uint8_t*>(s_amax + WARPS);
@@ -315,52 +360,63 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
     int* s_part = s_first + MAX_EXPERTS;
     s_route = reinterpret_cast<uint16_t*>(s_part + 16);
     s_chunk = reinterpret_cast<Chunk*>(s_route + MAX_ROUTES);
-    chunks = sort_routes<T, WARPS>(p, p.most, s_count, s_first, s_route, s_chunk, s_part);
+    chunks = p.routes <= 32
+                 ? sort_few_routes<T, WARPS>(p, p.most, s_route, s_chunk, s_part)
+                 : sort_routes<T, WARPS>(p, p.most, s_count, s_first, s_route, s_chunk, s_part);
   }
   const bool gated = p.act != MOE_ACT_NONE;
   const int tile_out = gated ? ROWS / 2 : ROWS;
   const int tiles = (int)((p.n_out + tile_out - 1) / tile_out);
-  const int64_t units = (int64_t)chunks * tiles;
+  const int units = chunks * tiles;
   const int blocks = (int)((p.K + BLOCK_K - 1) / BLOCK_K);
   const int pitch = (int)(p.K / 2);  // bytes of a row
   const int xp = (int)x_pitch(p.K);
-  const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+  const int even = units / (int)gridDim.x, odd = units % (int)gridDim.x, cta = (int)blockIdx.x;
+  const int u0 = even * cta + min(cta, odd), u1 = u0 + even + (cta < odd);
   if (u0 == u1) return;
 
-  // The CTA's units lie in one or a few chunks, one after another.  A chunk's are dealt out
-  // to teams of p.team warps, a unit's blocks to the team's warps.
-  const int teams = WARPS / p.team, team = warp / p.team, member = warp % p.team;
-  const int chunk0 = (int)(u0 / tiles), chunk1 = (int)((u1 - 1) / tiles);
-  auto tile_begin = [&](int chunk) { return chunk == chunk0 ? (int)(u0 - (int64_t)chunk * tiles) : 0; };
-  auto tile_end = [&](int chunk) { return chunk == chunk1 ? (int)(u1 - (int64_t)chunk * tiles) : tiles; };
-  struct Place {
-    int chunk, tile;
+  // The CTA's units lie in one or a few chunks, one after another; the blocks of each are
+  // dealt out to the warps in runs.
+  const int chunk0 = u0 / tiles, chunk1 = (u1 - 1) / tiles;
+  struct Run {
+    int chunk, tile, kb, left;  // next block, blocks left of the run
   };
-  auto settle = [&](Place& q) {  // on to the next chunk that has a unit for this team
-    while (q.chunk <= chunk1 && q.tile >= tile_end(q.chunk)) {
-      ++q.chunk;
-      q.tile = team;
-      if (q.chunk <= chunk1) q.tile += tile_begin(q.chunk);
+  // Run of warp w in a chunk.
+  auto run_of = [&](int chunk, int w) {
+    const int t0 = chunk == chunk0 ? u0 - chunk * tiles : 0;
+    const int t1 = chunk == chunk1 ? u1 - chunk * tiles : tiles;
+    const uint32_t n = (uint32_t)((t1 - t0) * blocks);
+    const uint32_t begin = n * w / WARPS, end = n * (w + 1) / WARPS;
+    return Run{chunk, t0 + (int)(begin / blocks), (int)(begin % blocks), (int)(end - begin)};
+  };
+  auto settle = [&](Run& q) {  // on to a chunk in which this warp has a block
+    while (q.left == 0 && q.chunk < chunk1) q = run_of(q.chunk + 1, warp);
+  };
+  // One block on; whether its rows are others (or there is none).
+  auto step = [&](Run& q) {
+    ++q.kb;
+    if (--q.left == 0) {
+      settle(q);
+      return true;
     }
+    if (q.kb < blocks) return false;
+    q.kb = 0;
+    ++q.tile;
+    return true;
   };
-  auto next_unit = [&](Place& q) {
-    q.tile += teams;
-    settle(q);
-  };
-  Place unit{chunk0, tile_begin(chunk0) + team};
-  settle(unit);
   // Row r of a unit as a row of all matrices; past the last one the last, whose results are
   // computed again and not stored.
-  auto row_of = [&](const Place& q, int r) -> int64_t {
+  auto row_of = [&](const Run& q, int r) -> int64_t {
     const int64_t base = EXPERTS ? (int64_t)s_chunk[q.chunk].expert * p.N : 0;
     const int64_t n = (int64_t)q.tile * tile_out + (gated ? r & 7 : r);
     return base + min(n, p.n_out - 1) + (gated && r >= 8 ? p.n_out : 0);
   };
 
-  // Copies run STAGES - 1 blocks ahead, scales one.
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * STAGES * STAGE;
-  Place ahead = unit;
-  int ahead_kb = member;
+  // Copies run p.stages - 1 blocks ahead, scales one.
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * p.stages * STAGE;
+  Run ahead = run_of(chunk0, warp);
+  settle(ahead);
+  Run scaled = ahead;
   const uint8_t* from[4];  // this lane's 16 bytes of four rows
   auto aim = [&] {
 #pragma unroll
@@ -372,48 +428,42 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) at_piece[i] = ((lane & 7) ^ (((lane >> 3) + 4 * i) & 7)) << 4;
   auto fetch = [&](int stage) {
-    if (ahead.chunk <= chunk1) {
-      const int byte = ahead_kb * 128;
+    if (ahead.left > 0) {
+      const int byte = ahead.kb * 128;
       if (byte + (lane & 7) * 16 < pitch) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           copy16(to + stage * STAGE + i * 512 + at_piece[i & 1], from[i] + byte);
       }
-      ahead_kb += p.team;
-      if (ahead_kb >= blocks) {
-        ahead_kb = member;
-        next_unit(ahead);
-        if (ahead.chunk <= chunk1) aim();
-      }
+      if (step(ahead) && ahead.left > 0) aim();
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  if (ahead.chunk <= chunk1) aim();
-#pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) fetch(s);
+  if (ahead.left > 0) aim();
+  for (int s = 0; s < p.stages - 1; ++s) fetch(s);
 
   const int groups = (int)(p.K / (32 * SPG));
   S sc[2], sc_next[2];
   int64_t scales_at[2];  // this lane's rows of the unit, in groups
-  auto aim_scales = [&](const Place& q) {
+  auto aim_scales = [&] {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) scales_at[r] = row_of(q, g + 8 * r) * groups;
+    for (int r = 0; r < 2; ++r) scales_at[r] = row_of(scaled, g + 8 * r) * groups;
   };
-  auto fetch_scales = [&](int kb) {
-    const int j = kb * S::COUNT;
+  auto fetch_scales = [&] {
+    if (scaled.left == 0) return;
+    const int j = scaled.kb * S::COUNT;
 #pragma unroll
     for (int r = 0; r < 2; ++r)
       sc_next[r].load(static_cast<const uint8_t*>(p.scales) + (scales_at[r] + j) * S::ITEM,
                       p.zeros + (scales_at[r] + j), groups - j, p.wide_scales);
+    if (step(scaled) && scaled.left > 0) aim_scales();
   };
-  if (unit.chunk <= chunk1) {
-    aim_scales(unit);
-    fetch_scales(member);
-  }
+  if (scaled.left > 0) aim_scales();
+  fetch_scales();
 
   // a lane's row of two 32-code pieces for ldmatrix
   const uint32_t lane_row = (lane & 15) * 128, lane_piece = ((lane >> 4) ^ (lane & 7)) << 4;
-  int stage = 0, buf = 0, turn = 0;
+  int stage = 0;
   for (int chunk = chunk0; chunk <= chunk1; ++chunk) {
     int first = chunk * p.most, count = (int)min((int64_t)p.most, p.T - first);
     if constexpr (EXPERTS) first = s_chunk[chunk].first, count = s_chunk[chunk].count;
@@ -425,7 +475,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
 
     // The chunk's rows of x: copied as they are, then brought to fp16 in place, each piece
     // by the thread that copied it.  A row has as many warps as there are for each.
-    __syncthreads();  // the last chunk's are no longer read
+    if (chunk > chunk0) __syncthreads();  // the last chunk's are no longer read
     int per = WARPS;
     while (per > 1 && per * count > WARPS) per >>= 1;
     const int pieces = blocks * (BLOCK_K / 8), real = (int)(p.K / 8);
@@ -435,15 +485,26 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
       if (col < count) {
         const uint4* src = reinterpret_cast<const uint4*>(row_of_x(col));
         uint4* dst = reinterpret_cast<uint4*>(s_x + col * xp);
-        for (int i = lane0; i < pieces; i += per * 32) {
-          const uint4 v = i < real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-          dst[i] = v;
-          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        constexpr int U = 4;  // pieces in flight
+        for (int i0 = lane0; i0 < pieces; i0 += U * per * 32) {
+          uint4 v[U];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {  // the largest finite value, by its bits
-            const uint32_t m = (u[e / 2] >> (16 * (e & 1))) & 0x7FFFu;
-            constexpr uint32_t INF = std::is_same<T, __nv_bfloat16>::value ? 0x7F80u : 0x7C00u;
-            most = max(most, m < INF ? m : 0u);
+          for (int k = 0; k < U; ++k) {
+            const int i = i0 + k * per * 32;
+            v[k] = i < real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            const int i = i0 + k * per * 32;
+            if (i >= pieces) break;
+            dst[i] = v[k];
+            const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {  // the largest finite value, by its bits
+              const uint32_t m = (u[e / 2] >> (16 * (e & 1))) & 0x7FFFu;
+              constexpr uint32_t INF = std::is_same<T, __nv_bfloat16>::value ? 0x7F80u : 0x7C00u;
+              most = max(most, m < INF ? m : 0u);
+            }
           }
         }
       }
@@ -483,31 +544,58 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
       }
     }
 
-    for (; unit.chunk == chunk; next_unit(unit), buf ^= 1) {
+    // Stores a unit's outputs from its lanes' sums.
+    auto store = [&](int tile, const float4 (&sums)[NT]) {
+      const int64_t n0 = (int64_t)tile * tile_out;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const float v[4] = {sums[t].x * C::UNIT, sums[t].y * C::UNIT, sums[t].z * C::UNIT,
+                            sums[t].w * C::UNIT};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int col = t * 8 + 2 * c + e;
+          if (col >= count) continue;
+          int row = first + col;
+          if constexpr (EXPERTS) row = s_route[row];
+          T* out = static_cast<T*>(p.out) + row * p.out_stride + n0 + g;
+          if (gated) {
+            if (n0 + g < p.n_out) *out = from_f32<T>(act_value(p.act, v[e]) * v[2 + e]);
+          } else {
+            if (n0 + g < p.n_out) out[0] = from_f32<T>(v[e]);
+            if (n0 + g + 8 < p.n_out) out[8] = from_f32<T>(v[2 + e]);
+          }
+        }
+      }
+    };
+
+    // The sums of a unit that other warps have blocks of: where this warp has its first
+    // block in place 1, else in place 0, [warp][place][NT][lane].
+    auto place = [&](int w, int which) { return red + (w * 2 + which) * (32 * NT) + lane; };
+    Run run = run_of(chunk, warp);
+    int begun = 0;  // blocks of this warp in the unit of place 1
+    while (run.left > 0) {
+      const int kb0 = run.kb, kb1 = min(blocks, run.kb + run.left);
       float acc[NT][4];
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[t][e] = 0.0f;
 
-      for (int kb = member; kb < blocks; kb += p.team) {
+      for (int kb = kb0; kb < kb1; ++kb) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) sc[r] = sc_next[r];
-        if (kb + p.team < blocks) {
-          fetch_scales(kb + p.team);
-        } else {
-          Place q = unit;
-          next_unit(q);
-          if (q.chunk <= chunk1) {
-            aim_scales(q);
-            fetch_scales(member);
-          }
-        }
-        fetch(stage == 0 ? STAGES - 1 : stage - 1);
-        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+        fetch_scales();
+        fetch(stage == 0 ? p.stages - 1 : stage - 1);
+        if (p.stages == 6)
+          asm volatile("cp.async.wait_group 5;" ::: "memory");
+        else if (p.stages == 4)
+          asm volatile("cp.async.wait_group 3;" ::: "memory");
+        else
+          asm volatile("cp.async.wait_group 2;" ::: "memory");
         __syncwarp();
         const uint32_t base = ring + stage * STAGE + lane_row;
         float part[NT][4];
+        float2 s0, s1;
 #pragma unroll
         for (int s = 0; s < 8; s += 2) {
           uint32_t w[4];  // words of rows g and g + 8 of 32 codes, then of the next 32
@@ -517,12 +605,6 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int j = (s + i) / SPG;
-            if ((s + i) % SPG == 0) {
-#pragma unroll
-              for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) part[t][e] = 0.0f;
-            }
             uint32_t d0[4], d1[4];
             C::pairs(w[2 * i], C::offset(sc[0].zero(j)), d0);
             C::pairs(w[2 * i + 1], C::offset(sc[1].zero(j)), d1);
@@ -531,74 +613,55 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
               const uint4 v = *reinterpret_cast<const uint4*>(xr[t] + kb * (BLOCK_K * 2) + (s + i) * 64);
-              mma_tile(part[t], a0, v.x, v.y);
-              mma_tile(part[t], a1, v.z, v.w);
+              mma_tile(part[t], a0, v.x, v.y, (s + i) % SPG == 0);
+              mma_tile(part[t], a1, v.z, v.w, false);
             }
             if ((s + i) % SPG == SPG - 1) {
-              const float s0 = sc[0].scale(j), s1 = sc[1].scale(j);
+              if (j % 2 == 0) s0 = sc[0].scales(j / 2), s1 = sc[1].scales(j / 2);
+              const float f0 = j % 2 == 0 ? s0.x : s0.y, f1 = j % 2 == 0 ? s1.x : s1.y;
 #pragma unroll
               for (int t = 0; t < NT; ++t) {
-                acc[t][0] = fmaf(s0 * power[t][0], part[t][0], acc[t][0]);
-                acc[t][1] = fmaf(s0 * power[t][1], part[t][1], acc[t][1]);
-                acc[t][2] = fmaf(s1 * power[t][0], part[t][2], acc[t][2]);
-                acc[t][3] = fmaf(s1 * power[t][1], part[t][3], acc[t][3]);
+                acc[t][0] = fmaf(f0 * power[t][0], part[t][0], acc[t][0]);
+                acc[t][1] = fmaf(f0 * power[t][1], part[t][1], acc[t][1]);
+                acc[t][2] = fmaf(f1 * power[t][0], part[t][2], acc[t][2]);
+                acc[t][3] = fmaf(f1 * power[t][1], part[t][3], acc[t][3]);
               }
             }
           }
         }
-        if constexpr (F == E2M1) {
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-            if (sc[r].broken()) {
-#pragma unroll
-              for (int t = 0; t < NT; ++t)
-                acc[t][2 * r] = acc[t][2 * r + 1] = __uint_as_float(0x7FC00000u);
-            }
-        }
         __syncwarp();  // the stage is free
-        if (++stage == STAGES) stage = 0;
+        if (++stage == p.stages) stage = 0;
       }
 
-      if (p.team > 1) {  // join the team's sums in one of its warps, in turn
-        float4* sums = red + (buf * WARPS + team * p.team) * (32 * NT) + lane;
+      float4 sums[NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-          sums[(member * NT + t) * 32] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
-        asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(p.team * 32) : "memory");
-        const bool mine = turn == member;
-        if (++turn == p.team) turn = 0;
-        if (!mine) continue;
+      for (int t = 0; t < NT; ++t) sums[t] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+      if (kb1 - kb0 == blocks) {
+        store(run.tile, sums);
+      } else {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) place(warp, kb0 == 0)[t * 32] = sums[t];
+        if (kb0 == 0) begun = kb1;
+      }
+      run.left -= kb1 - kb0;
+      if (run.left > 0) run.kb = 0, ++run.tile;
+    }
+    __syncthreads();
+    if (begun > 0) {  // the rest of the unit is with the next warps
+      float4 sums[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) sums[t] = place(warp, 1)[t * 32];
+      for (int w = warp + 1; begun < blocks; ++w) {
+        const int more = run_of(chunk, w).left;
+        if (more == 0) continue;
+        begun += more;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          float4 v = sums[t * 32];
-          for (int m = 1; m < p.team; ++m) {
-            const float4 o = sums[(m * NT + t) * 32];
-            v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-          }
-          acc[t][0] = v.x, acc[t][1] = v.y, acc[t][2] = v.z, acc[t][3] = v.w;
+          const float4 o = place(w, 0)[t * 32];
+          sums[t].x += o.x, sums[t].y += o.y, sums[t].z += o.z, sums[t].w += o.w;
         }
       }
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[t][e] *= C::UNIT;
-      const int64_t n0 = (int64_t)unit.tile * tile_out;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int col = t * 8 + 2 * c + e;
-          if (col >= count) continue;
-          int row = first + col;
-          if constexpr (EXPERTS) row = s_route[row];
-          T* out = static_cast<T*>(p.out) + row * p.out_stride + n0 + g;
-          if (gated) {
-            if (n0 + g < p.n_out) *out = from_f32<T>(act_value(p.act, acc[t][e]) * acc[t][2 + e]);
-          } else {
-            if (n0 + g < p.n_out) out[0] = from_f32<T>(acc[t][e]);
-            if (n0 + g + 8 < p.n_out) out[8] = from_f32<T>(acc[t][2 + e]);
-          }
-        }
+      store(run.tile, sums);
     }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -615,7 +678,8 @@ constexpr int kW4Smem = 232448 - 1024;
 
 // Rows of x that a block has room for.
 static int w4_room(int nt, bool experts, int64_t K) {
-  const int64_t n = (kW4Smem - w4::fixed_bytes(nt, experts)) / w4::x_pitch(K);
+  const int64_t n = (kW4Smem - w4::fixed_bytes(nt, experts) - w4::ring_bytes(nt, w4::MIN_STAGES)) /
+                    w4::x_pitch(K);
   return (int)(n < 8 * nt ? n : 8 * nt);
 }
 
@@ -625,25 +689,21 @@ static moe_status_t launch_w4(w4::Params p, cudaStream_t s) {
   moe_status_t st = allow_smem<kernel>(kW4Smem);
   if (st != MOE_OK) return st;
   const int room = w4_room(NT, EXPERTS, p.K);
-  // with experts a chunk has no more rows than there are; the likely number of chunks is one
-  // an expert of a short batch
   const int64_t rows = EXPERTS ? p.routes : p.T;
   const int64_t passes = (rows + room - 1) / room;
   p.most = EXPERTS ? (int)(rows < room ? rows : room) : (int)((rows + passes - 1) / passes);
   const int tile = p.act == MOE_ACT_NONE ? w4::ROWS : w4::ROWS / 2;
   const int64_t tiles = (p.n_out + tile - 1) / tile;
   const int64_t chunks = EXPERTS ? p.routes : passes;
-  const int64_t likely = EXPERTS && p.E < chunks ? p.E : chunks;
-  const int64_t ctas = num_sms(), blocks = (p.K + w4::BLOCK_K - 1) / w4::BLOCK_K;
-  // Two blocks a warp at least, one where a CTA has but one unit.
-  constexpr int WARPS = w4::warps_of(NT);
-  const int64_t share = tiles * likely <= ctas ? 1 : 2;
-  p.team = 1;
-  while (p.team < WARPS && p.team * 2 * share <= blocks) p.team *= 2;
+  const int64_t ctas = num_sms();
   const int64_t units = tiles * chunks;
-  const size_t smem = (size_t)w4::fixed_bytes(NT, EXPERTS) + (size_t)(p.most * w4::x_pitch(p.K));
-  return launched(launch_pdl(kernel, dim3((unsigned)(units < ctas ? units : ctas)), dim3(WARPS * 32),
-                             smem, s, p),
+  int64_t smem = w4::fixed_bytes(NT, EXPERTS) + p.most * w4::x_pitch(p.K);
+  p.stages = smem + w4::ring_bytes(NT, 6) <= kW4Smem   ? 6
+             : smem + w4::ring_bytes(NT, 4) <= kW4Smem ? 4
+                                                       : w4::MIN_STAGES;
+  smem += w4::ring_bytes(NT, p.stages);
+  return launched(launch_pdl(kernel, dim3((unsigned)(units < ctas ? units : ctas)), dim3(w4::warps_of(NT) * 32),
+                             (size_t)smem, s, p),
                   "4-bit products");
 }
 
@@ -712,8 +772,8 @@ moe_status_t moe_w4_linear(const moe_w4_linear_args_t* a, void* stream) {
                      w4::MAX_EXPERTS);
   if (!experts && T > w4::MAX_ROUTES)
     return set_error(MOE_ERR_UNSUPPORTED, "at most %d rows", w4::MAX_ROUTES);
-  if (K > 32768 || N >= ((int64_t)1 << 28))
-    return set_error(MOE_ERR_UNSUPPORTED, "in_features above 32768 or too many rows of a matrix");
+  if (K > 32768 || N >= ((int64_t)1 << 20))
+    return set_error(MOE_ERR_UNSUPPORTED, "in_features above 32768 or 2^20 rows of a matrix");
   if (!a->x || !a->weight || !a->scales || !a->out)
     return set_error(MOE_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
   if ((T > 1 && a->x_stride0 < K) || (rows > 1 && a->out_stride0 < n_out))
