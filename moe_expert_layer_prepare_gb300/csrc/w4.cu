@@ -33,12 +33,14 @@ namespace w4 {
 
 constexpr int ROWS = 16;           // of a unit
 constexpr int BLOCK_K = 256;       // codes of a row in a stage: 128 bytes
-constexpr int STAGE = ROWS * 128;  // bytes
+// Bytes of a stage: the rows' codes, 16 bytes of scales and 8 zero points a row.
+constexpr int STAGE_SCALES = ROWS * 128, STAGE_ZEROS = STAGE_SCALES + ROWS * 16;
+constexpr int STAGE = STAGE_ZEROS + ROWS * 8;
 constexpr int MAX_ROUTES = 1024, MAX_EXPERTS = 1024;
 // Columns take registers: fewer warps.
 constexpr int warps_of(int nt) { return nt == 1 ? 16 : 8; }
-// Stages of a warp's ring, as x leaves room.
-constexpr int MIN_STAGES = 3;
+// Stages of a warp's ring, as x leaves room: 64 KB and more are on their way to an SM.
+constexpr int MIN_STAGES = 3, MAX_STAGES = 4;
 
 struct Params {
   int64_t T, K, N;  // N: rows of a matrix
@@ -53,8 +55,11 @@ struct Params {
   int ids64;
   int act;
   int most;          // rows of a chunk
-  int stages;        // of a warp's ring: 3, 4 or 6
-  bool wide_scales;  // a block's scales of a row may be read at once
+  int stages;        // of a warp's ring
+  int tiles;         // units of a chunk
+  int blocks;        // K blocks of a unit, and 2^32 / blocks rounded up
+  uint32_t blocks_inverse;
+  bool wide_scales, wide_zeros;  // a block's of a row may be copied at once
   void* out;
   int64_t out_stride;
   uint32_t* status;
@@ -130,15 +135,31 @@ __device__ __forceinline__ void mma_tile(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The scales of a K block of a row: 8 / SPG of T, or exponents; and zero points.
+// The scales of a K block of a row, 8 / SPG of T or exponents, and its zero points.
 template <typename T, Format F, int SPG>
 struct Scales {
   static constexpr int COUNT = 8 / SPG;
   static constexpr int ITEM = F == E2M1 ? 1 : 2;
-  static constexpr int WORDS = (COUNT * ITEM + 3) / 4;
-  static constexpr int ZWORDS = F == INT4_ZEROS ? (COUNT + 3) / 4 : 1;
-  uint32_t s[WORDS], z[ZWORDS];
+  static constexpr int BYTES = COUNT * ITEM;
+  uint32_t s[BYTES / 4], z[2];
 
+  // from the row's places in a stage; of two zero points a word holds two blocks'
+  __device__ __forceinline__ void read(const uint8_t* stage, int row, bool odd) {
+    const uint8_t* at = stage + STAGE_SCALES + row * 16;
+    if constexpr (BYTES == 16) {
+      const uint4 v = *reinterpret_cast<const uint4*>(at);
+      s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
+    } else if constexpr (BYTES == 8) {
+      const uint2 v = *reinterpret_cast<const uint2*>(at);
+      s[0] = v.x, s[1] = v.y;
+    } else {
+      s[0] = *reinterpret_cast<const uint32_t*>(at);
+    }
+    if constexpr (F == INT4_ZEROS) {
+      const uint2 v = *reinterpret_cast<const uint2*>(stage + STAGE_ZEROS + row * 8);
+      z[0] = COUNT == 2 && odd ? v.x >> 16 : v.x, z[1] = v.y;
+    }
+  }
   // scales 2 i and 2 i + 1
   __device__ __forceinline__ float2 scales(int i) const {
     if constexpr (F == E2M1) {
@@ -154,45 +175,54 @@ struct Scales {
   __device__ __forceinline__ uint32_t zero(int j) const {
     return F == INT4_ZEROS ? (z[j / 4] >> (8 * (j % 4))) & 15u : 8u;
   }
-  // `left` groups of the row exist from here on
-  __device__ __forceinline__ void load(const uint8_t* src, const uint8_t* zsrc, int left, bool wide) {
-    if (wide) {
-      if constexpr (COUNT * ITEM == 16) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
-        s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
-      } else if constexpr (COUNT * ITEM == 8) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
-        s[0] = v.x, s[1] = v.y;
-      } else {
-        s[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
-      }
-      if constexpr (F == INT4_ZEROS) {
-        if constexpr (COUNT == 8) {
-          const uint2 v = __ldg(reinterpret_cast<const uint2*>(zsrc));
-          z[0] = v.x, z[1] = v.y;
-        } else if constexpr (COUNT == 4) {
-          z[0] = __ldg(reinterpret_cast<const uint32_t*>(zsrc));
-        } else {
-          z[0] = __ldg(reinterpret_cast<const uint16_t*>(zsrc));
-        }
-      }
-      return;
-    }
+};
+
+template <int BYTES>
+__device__ __forceinline__ void copy_small(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Copies the scales of a block of a row to its place in a stage, `at` in groups; `left`
+// groups exist from there on.
+template <typename T, Format F, int SPG>
+__device__ __forceinline__ void fetch_scales(const Params& p, uint8_t* stage, int row, int64_t at,
+                                             int left) {
+  using S = Scales<T, F, SPG>;
+  const uint8_t* src = static_cast<const uint8_t*>(p.scales) + at * S::ITEM;
+  uint8_t* dst = stage + STAGE_SCALES + row * 16;
+  if (p.wide_scales) {
+    copy_small<S::BYTES>((uint32_t)__cvta_generic_to_shared(dst), src);
+  } else {  // the others are zero: no group may be without a number
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i) s[i] = 0;
-#pragma unroll
-    for (int i = 0; i < ZWORDS; ++i) z[i] = 0;
-#pragma unroll
-    for (int j = 0; j < COUNT; ++j) {
-      if (j >= left) break;
+    for (int j = 0; j < S::COUNT; ++j) {
       if constexpr (F == E2M1)
-        s[j / 4] |= (uint32_t)__ldg(src + j) << (8 * (j % 4));
+        dst[j] = j < left ? __ldg(src + j) : 0;
       else
-        s[j / 2] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(src) + j) << (16 * (j % 2));
-      if constexpr (F == INT4_ZEROS) z[j / 4] |= (uint32_t)__ldg(zsrc + j) << (8 * (j % 4));
+        reinterpret_cast<uint16_t*>(dst)[j] = j < left ? __ldg(reinterpret_cast<const uint16_t*>(src) + j) : 0;
     }
   }
-};
+}
+template <typename T, Format F, int SPG>
+__device__ __forceinline__ void fetch_zeros(const Params& p, uint8_t* stage, int row, int64_t at,
+                                            int left) {
+  constexpr int COUNT = 8 / SPG;
+  const uint8_t* src = p.zeros + at;
+  uint8_t* dst = stage + STAGE_ZEROS + row * 8;
+  if (p.wide_zeros) {
+    if constexpr (COUNT == 2) src = p.zeros + (at & ~int64_t(3));  // these two and two others
+    copy_small<COUNT == 8 ? 8 : 4>((uint32_t)__cvta_generic_to_shared(dst), src);
+  } else {
+#pragma unroll
+    for (int j = 0; j < COUNT; ++j) {
+      const uint8_t v = j < left ? __ldg(src + j) : 0;
+      dst[j] = v;
+      if (COUNT == 2) dst[j + 2] = v;
+    }
+  }
+}
 
 // Routes by expert: s_route in the order of the experts, chunks of at most `most`.  Routes
 // without an expert get zeros in out.  All threads of the block call it.
@@ -316,10 +346,6 @@ __device__ __forceinline__ int sort_few_routes(const Params& p, int most, uint16
   return s_part[0];
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
 // Bytes of a row of x in shared memory: zeros up to a whole block, and 64 bytes so that two
 // rows' neighbouring 64 bytes lie in different banks.
 __host__ __device__ constexpr int64_t x_pitch(int64_t K) {
@@ -328,11 +354,12 @@ __host__ __device__ constexpr int64_t x_pitch(int64_t K) {
 
 constexpr int ring_bytes(int nt, int stages) { return warps_of(nt) * stages * STAGE; }
 constexpr int red_bytes(int nt) { return 2 * warps_of(nt) * 32 * 16 * nt; }
-constexpr int route_bytes(bool experts) {
-  return experts ? 2 * MAX_EXPERTS * 4 + MAX_ROUTES * (2 + 6) + 64 : 0;
+// s_part, then of each route its place and perhaps a chunk, then two words an expert
+__host__ __device__ constexpr int route_bytes(int routes) {
+  return routes == 0 ? 0 : 64 + (routes + 1) / 2 * 16 + (routes <= 32 ? 0 : 2 * MAX_EXPERTS * 4);
 }
-constexpr int fixed_bytes(int nt, bool experts) {  // beside the ring and x
-  return red_bytes(nt) + route_bytes(experts) + 8 * nt * 4 + warps_of(nt) * 4;
+constexpr int fixed_bytes(int nt, int routes) {  // beside the ring and x
+  return red_bytes(nt) + route_bytes(routes) + 8 * nt * 4 + warps_of(nt) * 4;
 }
 
 template <typename T, Format F, int SPG, int NT, bool EXPERTS>
@@ -343,10 +370,11 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
+  const int routes = EXPERTS ? p.routes : 0;
   float4* red = reinterpret_cast<float4*>(smem + ring_bytes(NT, p.stages));
   uint8_t* routing = reinterpret_cast<uint8_t*>(red) + red_bytes(NT);
-  float* s_power = reinterpret_cast<float*>(routing + route_bytes(EXPERTS));  // [COLS]
-  uint32_t* s_amax = reinterpret_cast<uint32_t*>(s_power + COLS);             // [WARPS]
+  float* s_power = reinterpret_cast<float*>(routing + route_bytes(routes));  // [COLS]
+  uint32_t* s_amax = reinterpret_cast<uint32_t*>(s_power + COLS);            // [WARPS]
   uint8_t* s_x = reinterpret_cast<uint8_t*>(s_amax + WARPS);
   pdl_wait();
   pdl_launch_dependents();
@@ -355,20 +383,19 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
   uint16_t* s_route = nullptr;
   int chunks = (int)((p.T + p.most - 1) / p.most);
   if constexpr (EXPERTS) {
-    int* s_count = reinterpret_cast<int*>(routing);
-    int* s_first = s_count + MAX_EXPERTS;
-    int* s_part = s_first + MAX_EXPERTS;
+    int* s_part = reinterpret_cast<int*>(routing);
     s_route = reinterpret_cast<uint16_t*>(s_part + 16);
-    s_chunk = reinterpret_cast<Chunk*>(s_route + MAX_ROUTES);
-    chunks = p.routes <= 32
-                 ? sort_few_routes<T, WARPS>(p, p.most, s_route, s_chunk, s_part)
-                 : sort_routes<T, WARPS>(p, p.most, s_count, s_first, s_route, s_chunk, s_part);
+    s_chunk = reinterpret_cast<Chunk*>(s_route + (routes + 1) / 2 * 2);
+    if (routes <= 32) {
+      chunks = sort_few_routes<T, WARPS>(p, p.most, s_route, s_chunk, s_part);
+    } else {
+      int* s_count = reinterpret_cast<int*>(routing + route_bytes(routes)) - 2 * MAX_EXPERTS;
+      chunks = sort_routes<T, WARPS>(p, p.most, s_count, s_count + MAX_EXPERTS, s_route, s_chunk, s_part);
+    }
   }
   const bool gated = p.act != MOE_ACT_NONE;
   const int tile_out = gated ? ROWS / 2 : ROWS;
-  const int tiles = (int)((p.n_out + tile_out - 1) / tile_out);
-  const int units = chunks * tiles;
-  const int blocks = (int)((p.K + BLOCK_K - 1) / BLOCK_K);
+  const int tiles = p.tiles, units = chunks * tiles, blocks = p.blocks;
   const int pitch = (int)(p.K / 2);  // bytes of a row
   const int xp = (int)x_pitch(p.K);
   const int even = units / (int)gridDim.x, odd = units % (int)gridDim.x, cta = (int)blockIdx.x;
@@ -387,7 +414,9 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
     const int t1 = chunk == chunk1 ? u1 - chunk * tiles : tiles;
     const uint32_t n = (uint32_t)((t1 - t0) * blocks);
     const uint32_t begin = n * w / WARPS, end = n * (w + 1) / WARPS;
-    return Run{chunk, t0 + (int)(begin / blocks), (int)(begin % blocks), (int)(end - begin)};
+    // begin / blocks: begin is below 2^24 and blocks at most 2^7
+    const int tile = blocks == 1 ? (int)begin : (int)__umulhi(begin, p.blocks_inverse);
+    return Run{chunk, t0 + tile, (int)begin - tile * blocks, (int)(end - begin)};
   };
   auto settle = [&](Run& q) {  // on to a chunk in which this warp has a block
     while (q.left == 0 && q.chunk < chunk1) q = run_of(q.chunk + 1, warp);
@@ -412,16 +441,54 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
     return base + min(n, p.n_out - 1) + (gated && r >= 8 ? p.n_out : 0);
   };
 
-  // Copies run p.stages - 1 blocks ahead, scales one.
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * p.stages * STAGE;
+  auto row_of_x = [&](int first, int col) {
+    int row = first + col;
+    if constexpr (EXPERTS) row = s_route[row] / p.top_k;
+    return static_cast<const T*>(p.x) + row * p.x_stride;
+  };
+  auto chunk_rows = [&](int chunk, int& first, int& count) {
+    first = chunk * p.most, count = (int)min((int64_t)p.most, p.T - first);
+    if constexpr (EXPERTS) first = s_chunk[chunk].first, count = s_chunk[chunk].count;
+  };
+  // A chunk's rows of x come as they are, each with the warps that there are for one, and
+  // are brought to fp16 in place, each piece by the thread that copied it.
+  const int pieces = blocks * (BLOCK_K / 8), real = (int)(p.K / 8);
+  auto warps_a_row = [&](int count) {
+    int per = WARPS;
+    while (per > 1 && per * count > WARPS) per >>= 1;
+    return per;
+  };
+  auto copy_x = [&](int chunk) {
+    int first, count;
+    chunk_rows(chunk, first, count);
+    const int per = warps_a_row(count), lane0 = (warp % per) * 32 + lane;
+    for (int col = warp / per; col < count; col += WARPS / per) {
+      const T* src = row_of_x(first, col);
+      uint4* dst = reinterpret_cast<uint4*>(s_x + col * xp);
+      for (int i = lane0; i < pieces; i += per * 32) {
+        if (i < real)
+          copy16((uint32_t)__cvta_generic_to_shared(dst + i), src + i * 8);
+        else
+          dst[i] = make_uint4(0, 0, 0, 0);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  copy_x(chunk0);  // before the weights, behind which it would queue
+
+  // Weights and scales p.stages - 1 blocks ahead.
+  uint8_t* const ring_at = smem + warp * p.stages * STAGE;
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(ring_at);
+  const int groups = (int)(p.K / (32 * SPG));
   Run ahead = run_of(chunk0, warp);
   settle(ahead);
-  Run scaled = ahead;
   const uint8_t* from[4];  // this lane's 16 bytes of four rows
+  int64_t scales_at = 0;   // this lane's row of scales (lanes 0 to 15) or zero points, in groups
   auto aim = [&] {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       from[i] = p.w + row_of(ahead, i * 4 + (lane >> 3)) * pitch + (lane & 7) * 16;
+    scales_at = row_of(ahead, lane & 15) * groups;
   };
   const uint32_t to = ring + (lane >> 3) * 128;
   uint32_t at_piece[2];  // rows r and r + 4 differ in the permutation
@@ -429,102 +496,78 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
   for (int i = 0; i < 2; ++i) at_piece[i] = ((lane & 7) ^ (((lane >> 3) + 4 * i) & 7)) << 4;
   auto fetch = [&](int stage) {
     if (ahead.left > 0) {
-      const int byte = ahead.kb * 128;
+      const int byte = ahead.kb * 128, group = ahead.kb * S::COUNT;
       if (byte + (lane & 7) * 16 < pitch) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           copy16(to + stage * STAGE + i * 512 + at_piece[i & 1], from[i] + byte);
       }
+      if (lane < 16)
+        fetch_scales<T, F, SPG>(p, ring_at + stage * STAGE, lane, scales_at + group, groups - group);
+      else if constexpr (F == INT4_ZEROS)
+        fetch_zeros<T, F, SPG>(p, ring_at + stage * STAGE, lane - 16, scales_at + group, groups - group);
       if (step(ahead) && ahead.left > 0) aim();
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  // all but the newest p.stages - 1 groups of copies are there
+  auto arrived = [&] {
+    if (p.stages == MAX_STAGES)
+      asm volatile("cp.async.wait_group %0;" ::"n"(MAX_STAGES - 1) : "memory");
+    else
+      asm volatile("cp.async.wait_group %0;" ::"n"(MIN_STAGES - 1) : "memory");
+  };
   if (ahead.left > 0) aim();
   for (int s = 0; s < p.stages - 1; ++s) fetch(s);
-
-  const int groups = (int)(p.K / (32 * SPG));
-  S sc[2], sc_next[2];
-  int64_t scales_at[2];  // this lane's rows of the unit, in groups
-  auto aim_scales = [&] {
-#pragma unroll
-    for (int r = 0; r < 2; ++r) scales_at[r] = row_of(scaled, g + 8 * r) * groups;
-  };
-  auto fetch_scales = [&] {
-    if (scaled.left == 0) return;
-    const int j = scaled.kb * S::COUNT;
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-      sc_next[r].load(static_cast<const uint8_t*>(p.scales) + (scales_at[r] + j) * S::ITEM,
-                      p.zeros + (scales_at[r] + j), groups - j, p.wide_scales);
-    if (step(scaled) && scaled.left > 0) aim_scales();
-  };
-  if (scaled.left > 0) aim_scales();
-  fetch_scales();
 
   // a lane's row of two 32-code pieces for ldmatrix
   const uint32_t lane_row = (lane & 15) * 128, lane_piece = ((lane >> 4) ^ (lane & 7)) << 4;
   int stage = 0;
   for (int chunk = chunk0; chunk <= chunk1; ++chunk) {
-    int first = chunk * p.most, count = (int)min((int64_t)p.most, p.T - first);
-    if constexpr (EXPERTS) first = s_chunk[chunk].first, count = s_chunk[chunk].count;
-    auto row_of_x = [&](int col) {
-      int row = first + col;
-      if constexpr (EXPERTS) row = s_route[row] / p.top_k;
-      return static_cast<const T*>(p.x) + row * p.x_stride;
-    };
-
-    // The chunk's rows of x: copied as they are, then brought to fp16 in place, each piece
-    // by the thread that copied it.  A row has as many warps as there are for each.
-    if (chunk > chunk0) __syncthreads();  // the last chunk's are no longer read
-    int per = WARPS;
-    while (per > 1 && per * count > WARPS) per >>= 1;
-    const int pieces = blocks * (BLOCK_K / 8), real = (int)(p.K / 8);
+    int first, count;
+    chunk_rows(chunk, first, count);
+    if (chunk > chunk0) {
+      __syncthreads();  // the last chunk's rows are no longer read
+      copy_x(chunk);
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    } else {
+      arrived();
+    }
+    const int per = warps_a_row(count), lane0 = (warp % per) * 32 + lane;
     for (int col0 = 0; col0 < count; col0 += WARPS / per) {
-      const int col = col0 + warp / per, lane0 = (warp % per) * 32 + lane;
+      const int col = col0 + warp / per;
+      uint4* row = reinterpret_cast<uint4*>(s_x + col * xp);
       uint32_t most = 0;
-      if (col < count) {
-        const uint4* src = reinterpret_cast<const uint4*>(row_of_x(col));
-        uint4* dst = reinterpret_cast<uint4*>(s_x + col * xp);
-        constexpr int U = 4;  // pieces in flight
-        for (int i0 = lane0; i0 < pieces; i0 += U * per * 32) {
-          uint4 v[U];
+      if (col < count)
+        for (int i = lane0; i < pieces; i += per * 32) {
+          const uint4 v = row[i];
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int k = 0; k < U; ++k) {
-            const int i = i0 + k * per * 32;
-            v[k] = i < real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int k = 0; k < U; ++k) {
-            const int i = i0 + k * per * 32;
-            if (i >= pieces) break;
-            dst[i] = v[k];
-            const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {  // the largest finite value, by its bits
-              const uint32_t m = (u[e / 2] >> (16 * (e & 1))) & 0x7FFFu;
-              constexpr uint32_t INF = std::is_same<T, __nv_bfloat16>::value ? 0x7F80u : 0x7C00u;
-              most = max(most, m < INF ? m : 0u);
-            }
+          for (int e = 0; e < 8; ++e) {  // the largest finite value, by its bits
+            const uint32_t m = (u[e / 2] >> (16 * (e & 1))) & 0x7FFFu;
+            constexpr uint32_t INF = std::is_same<T, __nv_bfloat16>::value ? 0x7F80u : 0x7C00u;
+            most = max(most, m < INF ? m : 0u);
           }
         }
-      }
       most = __reduce_max_sync(0xFFFFFFFFu, most);
-      if (lane == 0) s_amax[warp] = most;
-      __syncthreads();
+      if (per > 1) {
+        if (lane == 0) s_amax[warp] = most;
+        __syncthreads();
+      }
       if (col < count) {
-        for (int w = warp / per * per; w < (warp / per + 1) * per; ++w) most = max(most, s_amax[w]);
+        if (per > 1)
+          for (int w = warp / per * per; w < (warp / per + 1) * per; ++w) most = max(most, s_amax[w]);
         const T big = *reinterpret_cast<const T*>(&most);
         // 2^(14 - e) of a largest value in [2^e, 2^(e + 1)); of the smallest ones 2^100
         const int e = max((int)(__float_as_uint(to_f32(big)) >> 23) - 127, -86);
         const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-        uint4* dst = reinterpret_cast<uint4*>(s_x + col * xp);
         for (int i = lane0; i < pieces; i += per * 32) {
-          const uint4 v = dst[i];
+          const uint4 v = row[i];
           const float2 f0 = unpack2<T>(v.x), f1 = unpack2<T>(v.y), f2 = unpack2<T>(v.z),
                        f3 = unpack2<T>(v.w);
           const float f[8] = {f0.x * up, f0.y * up, f1.x * up, f1.y * up,
                               f2.x * up, f2.y * up, f3.x * up, f3.y * up};
-          dst[i] = C::order(f);
+          row[i] = C::order(f);
         }
         if (lane0 == 0) s_power[col] = __uint_as_float((uint32_t)(127 - 14 + e) << 23) * C::UNIT;
       }
@@ -568,6 +611,11 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
       }
     };
 
+    // Place in its word of this lane's rows' first zero point, where a block has two.
+    auto odd_row = [&](const Run& q, int r) {
+      return F == INT4_ZEROS && SPG == 4 && p.wide_scales ? (int)(row_of(q, g + 8 * r) * groups) & 2 : 0;
+    };
+
     // The sums of a unit that other warps have blocks of: where this warp has its first
     // block in place 1, else in place 0, [warp][place][NT][lane].
     auto place = [&](int w, int which) { return red + (w * 2 + which) * (32 * NT) + lane; };
@@ -575,6 +623,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
     int begun = 0;  // blocks of this warp in the unit of place 1
     while (run.left > 0) {
       const int kb0 = run.kb, kb1 = min(blocks, run.kb + run.left);
+      const int odd0[2] = {odd_row(run, 0), odd_row(run, 1)};
       float acc[NT][4];
 #pragma unroll
       for (int t = 0; t < NT; ++t)
@@ -582,17 +631,12 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
         for (int e = 0; e < 4; ++e) acc[t][e] = 0.0f;
 
       for (int kb = kb0; kb < kb1; ++kb) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) sc[r] = sc_next[r];
-        fetch_scales();
         fetch(stage == 0 ? p.stages - 1 : stage - 1);
-        if (p.stages == 6)
-          asm volatile("cp.async.wait_group 5;" ::: "memory");
-        else if (p.stages == 4)
-          asm volatile("cp.async.wait_group 3;" ::: "memory");
-        else
-          asm volatile("cp.async.wait_group 2;" ::: "memory");
+        arrived();
         __syncwarp();
+        S sc[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) sc[r].read(ring_at + stage * STAGE, g + 8 * r, (odd0[r] + 2 * kb) & 2);
         const uint32_t base = ring + stage * STAGE + lane_row;
         float part[NT][4];
         float2 s0, s1;
@@ -677,8 +721,8 @@ namespace w4 = moe::w4;
 constexpr int kW4Smem = 232448 - 1024;
 
 // Rows of x that a block has room for.
-static int w4_room(int nt, bool experts, int64_t K) {
-  const int64_t n = (kW4Smem - w4::fixed_bytes(nt, experts) - w4::ring_bytes(nt, w4::MIN_STAGES)) /
+static int w4_room(int nt, int routes, int64_t K) {
+  const int64_t n = (kW4Smem - w4::fixed_bytes(nt, routes) - w4::ring_bytes(nt, w4::MIN_STAGES)) /
                     w4::x_pitch(K);
   return (int)(n < 8 * nt ? n : 8 * nt);
 }
@@ -688,7 +732,7 @@ static moe_status_t launch_w4(w4::Params p, cudaStream_t s) {
   constexpr auto kernel = w4::w4_kernel<T, F, SPG, NT, EXPERTS>;
   moe_status_t st = allow_smem<kernel>(kW4Smem);
   if (st != MOE_OK) return st;
-  const int room = w4_room(NT, EXPERTS, p.K);
+  const int room = w4_room(NT, EXPERTS ? p.routes : 0, p.K);
   const int64_t rows = EXPERTS ? p.routes : p.T;
   const int64_t passes = (rows + room - 1) / room;
   p.most = EXPERTS ? (int)(rows < room ? rows : room) : (int)((rows + passes - 1) / passes);
@@ -697,10 +741,11 @@ static moe_status_t launch_w4(w4::Params p, cudaStream_t s) {
   const int64_t chunks = EXPERTS ? p.routes : passes;
   const int64_t ctas = num_sms();
   const int64_t units = tiles * chunks;
-  int64_t smem = w4::fixed_bytes(NT, EXPERTS) + p.most * w4::x_pitch(p.K);
-  p.stages = smem + w4::ring_bytes(NT, 6) <= kW4Smem   ? 6
-             : smem + w4::ring_bytes(NT, 4) <= kW4Smem ? 4
-                                                       : w4::MIN_STAGES;
+  p.tiles = (int)tiles;
+  p.blocks = (int)((p.K + w4::BLOCK_K - 1) / w4::BLOCK_K);
+  p.blocks_inverse = (uint32_t)(((uint64_t)1 << 32) / p.blocks + 1);  // of 1 it is not used
+  int64_t smem = w4::fixed_bytes(NT, EXPERTS ? p.routes : 0) + p.most * w4::x_pitch(p.K);
+  p.stages = smem + w4::ring_bytes(NT, w4::MAX_STAGES) <= kW4Smem ? w4::MAX_STAGES : w4::MIN_STAGES;
   smem += w4::ring_bytes(NT, p.stages);
   return launched(launch_pdl(kernel, dim3((unsigned)(units < ctas ? units : ctas)), dim3(w4::warps_of(NT) * 32),
                              (size_t)smem, s, p),
@@ -715,7 +760,7 @@ static moe_status_t run_w4(const w4::Params& p, cudaStream_t s) {
     return launch_w4<T, F, SPG, 2, true>(p, s);
   }
   // as few passes over the matrix as there can be, and then as few columns of zeros
-  const int64_t one = w4_room(1, false, p.K), two = w4_room(2, false, p.K);
+  const int64_t one = w4_room(1, 0, p.K), two = w4_room(2, 0, p.K);
   if ((p.T + one - 1) / one <= (p.T + two - 1) / two) return launch_w4<T, F, SPG, 1, false>(p, s);
   return launch_w4<T, F, SPG, 2, false>(p, s);
 }
@@ -798,6 +843,8 @@ moe_status_t moe_w4_linear(const moe_w4_linear_args_t* a, void* stream) {
   p.act = a->activation;
   p.wide_scales = K % w4::BLOCK_K == 0 && rows_aligned16(a->scales, 0, 1, 1) &&
                   (a->zeros == nullptr || (reinterpret_cast<uintptr_t>(a->zeros) & 7u) == 0);
+  // of two zero points a block a word is read, which the end of the tensor has to hold
+  p.wide_zeros = p.wide_scales && (G != 128 || (experts ? E : 1) * N * (K / G) % 4 == 0);
   p.out = a->out;
   p.out_stride = a->out_stride0;
   p.status = a->device_status;
