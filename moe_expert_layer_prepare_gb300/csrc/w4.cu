@@ -54,7 +54,7 @@ struct Params {
   const void* ids;       // nullable: one matrix for all rows
   int ids64;
   int act;
-  int most;          // rows of a chunk
+  int most, room;    // rows of a chunk, and in shared memory
   int stages;        // of a warp's ring
   int tiles;         // units of a chunk
   int blocks;        // K blocks of a unit, and 2^32 / blocks rounded up
@@ -321,18 +321,16 @@ __device__ __forceinline__ int sort_few_routes(const Params& p, int most, uint16
     if (id >= p.E) set_status(p.status, MOE_DEV_BAD_EXPERT);
     const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
     const int rank = __popc(same & lanemask_lt()), count = __popc(same);
-    const bool leads = e >= 0 && rank % most == 0;
-    const uint32_t leaders = __ballot_sync(0xFFFFFFFFu, leads);
-    // routes in the order of the experts' first ones: behind all routes of those before
-    int first = 0;
+    const uint32_t leaders = __ballot_sync(0xFFFFFFFFu, e >= 0 && rank % most == 0);
+    // experts in the order of their first routes: behind all routes and chunks of those before
+    int first = 0, chunk = rank / most;
     for (uint32_t m = __ballot_sync(0xFFFFFFFFu, e >= 0 && rank == 0); m != 0; m &= m - 1) {
       const int l = __ffs(m) - 1, n = __shfl_sync(0xFFFFFFFFu, count, l);
-      if (l < __ffs(same) - 1) first += n;
+      if (l < __ffs(same) - 1) first += n, chunk += (n + most - 1) / most;
     }
     if (e >= 0) s_route[first + rank] = (uint16_t)lane;
-    if (leads)
-      s_chunk[__popc(leaders & lanemask_lt())] =
-          Chunk{(int16_t)e, (int16_t)(first + rank), (int16_t)min(most, count - rank)};
+    if (e >= 0 && rank % most == 0)
+      s_chunk[chunk] = Chunk{(int16_t)e, (int16_t)(first + rank), (int16_t)min(most, count - rank)};
     const uint32_t without = __ballot_sync(0xFFFFFFFFu, lane < p.routes && e < 0);
     if (lane == 0) s_part[0] = __popc(leaders), s_part[1] = (int)without;
   }
@@ -358,23 +356,24 @@ constexpr int red_bytes(int nt) { return 2 * warps_of(nt) * 32 * 16 * nt; }
 __host__ __device__ constexpr int route_bytes(int routes) {
   return routes == 0 ? 0 : 64 + (routes + 1) / 2 * 16 + (routes <= 32 ? 0 : 2 * MAX_EXPERTS * 4);
 }
+constexpr int MAX_ROOM = 16;  // rows of x in shared memory
 constexpr int fixed_bytes(int nt, int routes) {  // beside the ring and x
-  return red_bytes(nt) + route_bytes(routes) + 8 * nt * 4 + warps_of(nt) * 4;
+  return red_bytes(nt) + route_bytes(routes) + MAX_ROOM * 4 + warps_of(nt) * 4;
 }
 
 template <typename T, Format F, int SPG, int NT, bool EXPERTS>
 __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
   using C = Codes<F>;
   using S = Scales<T, F, SPG>;
-  constexpr int WARPS = warps_of(NT), COLS = 8 * NT;
+  constexpr int WARPS = warps_of(NT);
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
   const int routes = EXPERTS ? p.routes : 0;
   float4* red = reinterpret_cast<float4*>(smem + ring_bytes(NT, p.stages));
   uint8_t* routing = reinterpret_cast<uint8_t*>(red) + red_bytes(NT);
-  float* s_power = reinterpret_cast<float*>(routing + route_bytes(routes));  // [COLS]
-  uint32_t* s_amax = reinterpret_cast<uint32_t*>(s_power + COLS);            // [WARPS]
+  float* s_power = reinterpret_cast<float*>(routing + route_bytes(routes));  // [MAX_ROOM]
+  uint32_t* s_amax = reinterpret_cast<uint32_t*>(s_power + MAX_ROOM);       // [WARPS]
   uint8_t* s_x = reinterpret_cast<uint8_t*>(s_amax + WARPS);
   pdl_wait();
   pdl_launch_dependents();
@@ -402,24 +401,43 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
   const int u0 = even * cta + min(cta, odd), u1 = u0 + even + (cta < odd);
   if (u0 == u1) return;
 
-  // The CTA's units lie in one or a few chunks, one after another; the blocks of each are
-  // dealt out to the warps in runs.
-  const int chunk0 = u0 / tiles, chunk1 = (u1 - 1) / tiles;
+  // The CTA's units lie in one or a few chunks.  As many chunks as there is room for the
+  // rows of are a batch: their blocks are dealt out to the warps in runs.
+  const int chunk1 = (u1 - 1) / tiles;
+  auto chunk_rows = [&](int chunk, int& first, int& count) {
+    first = chunk * p.most, count = (int)min((int64_t)p.most, p.T - first);
+    if constexpr (EXPERTS) first = s_chunk[chunk].first, count = s_chunk[chunk].count;
+  };
+  struct Batch {
+    int chunk0, chunk1, u0, u1;  // chunks and units, those behind the last
+  };
+  auto batch_from = [&](int chunk) {
+    Batch q{chunk, chunk, max(u0, chunk * tiles), 0};
+    for (int rows = 0; q.chunk1 <= chunk1; ++q.chunk1) {
+      int first, count;
+      chunk_rows(q.chunk1, first, count);
+      rows += count;
+      if (rows > p.room) break;
+    }
+    q.u1 = min(u1, q.chunk1 * tiles);
+    return q;
+  };
   struct Run {
     int chunk, tile, kb, left;  // next block, blocks left of the run
+    int after;                  // first chunk of the next batch
   };
-  // Run of warp w in a chunk.
-  auto run_of = [&](int chunk, int w) {
-    const int t0 = chunk == chunk0 ? u0 - chunk * tiles : 0;
-    const int t1 = chunk == chunk1 ? u1 - chunk * tiles : tiles;
-    const uint32_t n = (uint32_t)((t1 - t0) * blocks);
-    const uint32_t begin = n * w / WARPS, end = n * (w + 1) / WARPS;
+  // Begin of warp w's run in a batch, in its blocks.
+  auto run_begin = [&](const Batch& q, int w) { return (uint32_t)((q.u1 - q.u0) * blocks) * w / WARPS; };
+  auto run_of = [&](const Batch& q) {
+    const uint32_t begin = run_begin(q, warp), end = run_begin(q, warp + 1);
     // begin / blocks: begin is below 2^24 and blocks at most 2^7
-    const int tile = blocks == 1 ? (int)begin : (int)__umulhi(begin, p.blocks_inverse);
-    return Run{chunk, t0 + tile, (int)begin - tile * blocks, (int)(end - begin)};
+    const int unit = blocks == 1 ? (int)begin : (int)__umulhi(begin, p.blocks_inverse);
+    Run r{q.chunk0, q.u0 - q.chunk0 * tiles + unit, (int)begin - unit * blocks, (int)(end - begin), q.chunk1};
+    while (r.tile >= tiles) r.tile -= tiles, ++r.chunk;
+    return r;
   };
-  auto settle = [&](Run& q) {  // on to a chunk in which this warp has a block
-    while (q.left == 0 && q.chunk < chunk1) q = run_of(q.chunk + 1, warp);
+  auto settle = [&](Run& q) {  // on to a batch in which this warp has a block
+    while (q.left == 0 && q.after <= chunk1) q = run_of(batch_from(q.after));
   };
   // One block on; whether its rows are others (or there is none).
   auto step = [&](Run& q) {
@@ -430,7 +448,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
     }
     if (q.kb < blocks) return false;
     q.kb = 0;
-    ++q.tile;
+    if (++q.tile == tiles) q.tile = 0, ++q.chunk;
     return true;
   };
   // Row r of a unit as a row of all matrices; past the last one the last, whose results are
@@ -441,16 +459,18 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
     return base + min(n, p.n_out - 1) + (gated && r >= 8 ? p.n_out : 0);
   };
 
-  auto row_of_x = [&](int first, int col) {
-    int row = first + col;
+  // Rows of a batch in the order of its chunks: with experts they are neighbours in s_route.
+  auto batch_rows = [&](const Batch& q, int& first, int& count) {
+    int f, n;
+    chunk_rows(q.chunk0, first, n);
+    chunk_rows(q.chunk1 - 1, f, n);
+    count = f + n - first;
+  };
+  auto row_of_x = [&](int row) {
     if constexpr (EXPERTS) row = s_route[row] / p.top_k;
     return static_cast<const T*>(p.x) + row * p.x_stride;
   };
-  auto chunk_rows = [&](int chunk, int& first, int& count) {
-    first = chunk * p.most, count = (int)min((int64_t)p.most, p.T - first);
-    if constexpr (EXPERTS) first = s_chunk[chunk].first, count = s_chunk[chunk].count;
-  };
-  // A chunk's rows of x come as they are, each with the warps that there are for one, and
+  // A batch's rows of x come as they are, each with the warps that there are for one, and
   // are brought to fp16 in place, each piece by the thread that copied it.
   const int pieces = blocks * (BLOCK_K / 8), real = (int)(p.K / 8);
   auto warps_a_row = [&](int count) {
@@ -458,12 +478,12 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
     while (per > 1 && per * count > WARPS) per >>= 1;
     return per;
   };
-  auto copy_x = [&](int chunk) {
+  auto copy_x = [&](const Batch& q) {
     int first, count;
-    chunk_rows(chunk, first, count);
+    batch_rows(q, first, count);
     const int per = warps_a_row(count), lane0 = (warp % per) * 32 + lane;
     for (int col = warp / per; col < count; col += WARPS / per) {
-      const T* src = row_of_x(first, col);
+      const T* src = row_of_x(first + col);
       uint4* dst = reinterpret_cast<uint4*>(s_x + col * xp);
       for (int i = lane0; i < pieces; i += per * 32) {
         if (i < real)
@@ -474,13 +494,14 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  copy_x(chunk0);  // before the weights, behind which it would queue
+  Batch batch = batch_from(u0 / tiles);
+  copy_x(batch);  // before the weights, behind which it would queue
 
   // Weights and scales p.stages - 1 blocks ahead.
   uint8_t* const ring_at = smem + warp * p.stages * STAGE;
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(ring_at);
   const int groups = (int)(p.K / (32 * SPG));
-  Run ahead = run_of(chunk0, warp);
+  Run ahead = run_of(batch);
   settle(ahead);
   const uint8_t* from[4];  // this lane's 16 bytes of four rows
   int64_t scales_at = 0;   // this lane's row of scales (lanes 0 to 15) or zero points, in groups
@@ -523,22 +544,24 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
   // a lane's row of two 32-code pieces for ldmatrix
   const uint32_t lane_row = (lane & 15) * 128, lane_piece = ((lane >> 4) ^ (lane & 7)) << 4;
   int stage = 0;
-  for (int chunk = chunk0; chunk <= chunk1; ++chunk) {
-    int first, count;
-    chunk_rows(chunk, first, count);
-    if (chunk > chunk0) {
-      __syncthreads();  // the last chunk's rows are no longer read
-      copy_x(chunk);
+  for (bool again = false;; again = true) {
+    if (again) {
+      if (batch.chunk1 > chunk1) break;
+      batch = batch_from(batch.chunk1);
+      __syncthreads();  // the last batch's rows are no longer read
+      copy_x(batch);
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     } else {
       arrived();
     }
-    const int per = warps_a_row(count), lane0 = (warp % per) * 32 + lane;
-    for (int col0 = 0; col0 < count; col0 += WARPS / per) {
+    int batch_first, rows;
+    batch_rows(batch, batch_first, rows);
+    const int per = warps_a_row(rows), lane0 = (warp % per) * 32 + lane;
+    for (int col0 = 0; col0 < rows; col0 += WARPS / per) {
       const int col = col0 + warp / per;
       uint4* row = reinterpret_cast<uint4*>(s_x + col * xp);
       uint32_t most = 0;
-      if (col < count)
+      if (col < rows)
         for (int i = lane0; i < pieces; i += per * 32) {
           const uint4 v = row[i];
           const uint32_t u[4] = {v.x, v.y, v.z, v.w};
@@ -554,7 +577,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
         if (lane == 0) s_amax[warp] = most;
         __syncthreads();
       }
-      if (col < count) {
+      if (col < rows) {
         if (per > 1)
           for (int w = warp / per * per; w < (warp / per + 1) * per; ++w) most = max(most, s_amax[w]);
         const T big = *reinterpret_cast<const T*>(&most);
@@ -573,19 +596,26 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
       }
       __syncthreads();
     }
+    int first = 0, count = 0, chunk = -1;  // of the unit at work
     const uint8_t* xr[NT];
     float power[NT][2];
+    auto take_chunk = [&](int next) {
+      if (next == chunk) return;
+      chunk = next;
+      chunk_rows(chunk, first, count);
+      const int row0 = first - batch_first;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      // columns without a row take the first one's; they are not stored
-      const int col = t * 8 + g;
-      xr[t] = s_x + (col < count ? col : 0) * xp + c * 16;
+      for (int t = 0; t < NT; ++t) {
+        // columns without a row take the first one's; they are not stored
+        const int col = t * 8 + g;
+        xr[t] = s_x + (row0 + (col < count ? col : 0)) * xp + c * 16;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int of = t * 8 + 2 * c + e;
-        power[t][e] = s_power[of < count ? of : 0];
+        for (int e = 0; e < 2; ++e) {
+          const int of = t * 8 + 2 * c + e;
+          power[t][e] = s_power[row0 + (of < count ? of : 0)];
+        }
       }
-    }
+    };
 
     // Stores a unit's outputs from its lanes' sums.
     auto store = [&](int tile, const float4 (&sums)[NT]) {
@@ -619,9 +649,10 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
     // The sums of a unit that other warps have blocks of: where this warp has its first
     // block in place 1, else in place 0, [warp][place][NT][lane].
     auto place = [&](int w, int which) { return red + (w * 2 + which) * (32 * NT) + lane; };
-    Run run = run_of(chunk, warp);
-    int begun = 0;  // blocks of this warp in the unit of place 1
+    Run run = run_of(batch);
+    bool begun = false;  // whether this warp has a unit in place 1
     while (run.left > 0) {
+      take_chunk(run.chunk);
       const int kb0 = run.kb, kb1 = min(blocks, run.kb + run.left);
       const int odd0[2] = {odd_row(run, 0), odd_row(run, 1)};
       float acc[NT][4];
@@ -685,25 +716,35 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
       } else {
 #pragma unroll
         for (int t = 0; t < NT; ++t) place(warp, kb0 == 0)[t * 32] = sums[t];
-        if (kb0 == 0) begun = kb1;
+        begun = kb0 == 0;
       }
       run.left -= kb1 - kb0;
-      if (run.left > 0) run.kb = 0, ++run.tile;
+      if (run.left > 0) {
+        run.kb = 0;
+        if (++run.tile == tiles) run.tile = 0, ++run.chunk;
+      }
     }
     __syncthreads();
-    if (begun > 0) {  // the rest of the unit is with the next warps
+    if (begun) {  // the rest of the unit is with the next warps, up to the one that ends it
+      const uint32_t end = (uint32_t)(run.chunk * tiles + run.tile + 1 - batch.u0) * blocks;
       float4 sums[NT];
 #pragma unroll
       for (int t = 0; t < NT; ++t) sums[t] = place(warp, 1)[t * 32];
-      for (int w = warp + 1; begun < blocks; ++w) {
-        const int more = run_of(chunk, w).left;
-        if (more == 0) continue;
-        begun += more;
+      for (int w0 = warp + 1; w0 < WARPS && run_begin(batch, w0) < end; w0 += 4) {
+        float4 o[4][NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const float4 o = place(w, 0)[t * 32];
-          sums[t].x += o.x, sums[t].y += o.y, sums[t].z += o.z, sums[t].w += o.w;
+        for (int k = 0; k < 4; ++k) {
+          const int w = w0 + k;
+          const bool has = w < WARPS && run_begin(batch, w) < end && run_begin(batch, w) < run_begin(batch, w + 1);
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            o[k][t] = has ? place(w, 0)[t * 32] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            sums[t].x += o[k][t].x, sums[t].y += o[k][t].y, sums[t].z += o[k][t].z, sums[t].w += o[k][t].w;
       }
       store(run.tile, sums);
     }
@@ -724,7 +765,7 @@ constexpr int kW4Smem = 232448 - 1024;
 static int w4_room(int nt, int routes, int64_t K) {
   const int64_t n = (kW4Smem - w4::fixed_bytes(nt, routes) - w4::ring_bytes(nt, w4::MIN_STAGES)) /
                     w4::x_pitch(K);
-  return (int)(n < 8 * nt ? n : 8 * nt);
+  return (int)(n < w4::MAX_ROOM ? n : w4::MAX_ROOM);
 }
 
 template <typename T, w4::Format F, int SPG, int NT, bool EXPERTS>
@@ -732,7 +773,8 @@ static moe_status_t launch_w4(w4::Params p, cudaStream_t s) {
   constexpr auto kernel = w4::w4_kernel<T, F, SPG, NT, EXPERTS>;
   moe_status_t st = allow_smem<kernel>(kW4Smem);
   if (st != MOE_OK) return st;
-  const int room = w4_room(NT, EXPERTS ? p.routes : 0, p.K);
+  p.room = w4_room(NT, EXPERTS ? p.routes : 0, p.K);
+  const int room = p.room < 8 * NT ? p.room : 8 * NT;
   const int64_t rows = EXPERTS ? p.routes : p.T;
   const int64_t passes = (rows + room - 1) / room;
   p.most = EXPERTS ? (int)(rows < room ? rows : room) : (int)((rows + passes - 1) / passes);
@@ -744,7 +786,10 @@ static moe_status_t launch_w4(w4::Params p, cudaStream_t s) {
   p.tiles = (int)tiles;
   p.blocks = (int)((p.K + w4::BLOCK_K - 1) / w4::BLOCK_K);
   p.blocks_inverse = (uint32_t)(((uint64_t)1 << 32) / p.blocks + 1);  // of 1 it is not used
-  int64_t smem = w4::fixed_bytes(NT, EXPERTS ? p.routes : 0) + p.most * w4::x_pitch(p.K);
+  // a CTA's units lie in few chunks where there are many units
+  const int64_t likely = (EXPERTS && p.E < chunks ? p.E : chunks) / ctas + 2;
+  if (p.room > p.most * likely) p.room = (int)(p.most * likely);
+  int64_t smem = w4::fixed_bytes(NT, EXPERTS ? p.routes : 0) + p.room * w4::x_pitch(p.K);
   p.stages = smem + w4::ring_bytes(NT, w4::MAX_STAGES) <= kW4Smem ? w4::MAX_STAGES : w4::MIN_STAGES;
   smem += w4::ring_bytes(NT, p.stages);
   return launched(launch_pdl(kernel, dim3((unsigned)(units < ctas ? units : ctas)), dim3(w4::warps_of(NT) * 32),
@@ -760,7 +805,7 @@ static moe_status_t run_w4(const w4::Params& p, cudaStream_t s) {
     return launch_w4<T, F, SPG, 2, true>(p, s);
   }
   // as few passes over the matrix as there can be, and then as few columns of zeros
-  const int64_t one = w4_room(1, 0, p.K), two = w4_room(2, 0, p.K);
+  const int64_t one = w4_room(1, 0, p.K) < 8 ? w4_room(1, 0, p.K) : 8, two = w4_room(2, 0, p.K);
   if ((p.T + one - 1) / one <= (p.T + two - 1) / two) return launch_w4<T, F, SPG, 1, false>(p, s);
   return launch_w4<T, F, SPG, 2, false>(p, s);
 }
