@@ -32,15 +32,13 @@ namespace moe {
 namespace w4 {
 
 constexpr int ROWS = 16;           // of a unit
-constexpr int BLOCK_K = 256;       // codes of a row in a stage: 128 bytes
-// Bytes of a stage: the rows' codes, 16 bytes of scales and 8 zero points a row.
-constexpr int STAGE_SCALES = ROWS * 128, STAGE_ZEROS = STAGE_SCALES + ROWS * 16;
-constexpr int STAGE = STAGE_ZEROS + ROWS * 8;
+constexpr int BLOCK_K = 512;       // codes of a row in a stage: 256 bytes, as two of 128
+// Bytes of a stage: the rows' codes, 32 bytes of scales and 16 zero points a row.
+constexpr int HALF_STAGE = ROWS * 128;
+constexpr int STAGE_SCALES = 2 * HALF_STAGE, STAGE_ZEROS = STAGE_SCALES + ROWS * 32;
+constexpr int STAGE = STAGE_ZEROS + ROWS * 16;
+constexpr int STAGES = 2;  // of a warp's ring: 64 KB are on their way to an SM
 constexpr int MAX_ROUTES = 1024, MAX_EXPERTS = 1024;
-// Columns take registers: fewer warps.
-constexpr int warps_of(int nt) { return nt == 1 ? 16 : 8; }
-// Stages of a warp's ring, as x leaves room: 64 KB and more are on their way to an SM.
-constexpr int MIN_STAGES = 3, MAX_STAGES = 4;
 
 struct Params {
   int64_t T, K, N;  // N: rows of a matrix
@@ -55,11 +53,10 @@ struct Params {
   int ids64;
   int act;
   int most, room;    // rows of a chunk, and in shared memory
-  int stages;        // of a warp's ring
   int tiles;         // units of a chunk
   int blocks;        // K blocks of a unit, and 2^32 / blocks rounded up
   uint32_t blocks_inverse;
-  bool wide_scales, wide_zeros;  // a block's of a row may be copied at once
+  int scale_unit, zero_unit;  // see copy_groups
   void* out;
   int64_t out_stride;
   uint32_t* status;
@@ -135,7 +132,7 @@ __device__ __forceinline__ void mma_tile(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The scales of a K block of a row, 8 / SPG of T or exponents, and its zero points.
+// The scales of half a K block of a row, 8 / SPG of T or exponents, and its zero points.
 template <typename T, Format F, int SPG>
 struct Scales {
   static constexpr int COUNT = 8 / SPG;
@@ -143,9 +140,9 @@ struct Scales {
   static constexpr int BYTES = COUNT * ITEM;
   uint32_t s[BYTES / 4], z[2];
 
-  // from the row's places in a stage; of two zero points a word holds two blocks'
-  __device__ __forceinline__ void read(const uint8_t* stage, int row, bool odd) {
-    const uint8_t* at = stage + STAGE_SCALES + row * 16;
+  // of the half `h` of a row in a stage
+  __device__ __forceinline__ void read(const uint8_t* stage, int row, int h) {
+    const uint8_t* at = stage + STAGE_SCALES + row * 32 + h * BYTES;
     if constexpr (BYTES == 16) {
       const uint4 v = *reinterpret_cast<const uint4*>(at);
       s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
@@ -156,8 +153,15 @@ struct Scales {
       s[0] = *reinterpret_cast<const uint32_t*>(at);
     }
     if constexpr (F == INT4_ZEROS) {
-      const uint2 v = *reinterpret_cast<const uint2*>(stage + STAGE_ZEROS + row * 8);
-      z[0] = COUNT == 2 && odd ? v.x >> 16 : v.x, z[1] = v.y;
+      const uint8_t* zat = stage + STAGE_ZEROS + row * 16 + h * COUNT;
+      if constexpr (COUNT == 8) {
+        const uint2 v = *reinterpret_cast<const uint2*>(zat);
+        z[0] = v.x, z[1] = v.y;
+      } else if constexpr (COUNT == 4) {
+        z[0] = *reinterpret_cast<const uint32_t*>(zat);
+      } else {
+        z[0] = *reinterpret_cast<const uint16_t*>(zat);
+      }
     }
   }
   // scales 2 i and 2 i + 1
@@ -178,48 +182,40 @@ struct Scales {
 };
 
 template <int BYTES>
-__device__ __forceinline__ void copy_small(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
-}
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 
-// Copies the scales of a block of a row to its place in a stage, `at` in groups; `left`
-// groups exist from there on.
-template <typename T, Format F, int SPG>
-__device__ __forceinline__ void fetch_scales(const Params& p, uint8_t* stage, int row, int64_t at,
-                                             int left) {
-  using S = Scales<T, F, SPG>;
-  const uint8_t* src = static_cast<const uint8_t*>(p.scales) + at * S::ITEM;
-  uint8_t* dst = stage + STAGE_SCALES + row * 16;
-  if (p.wide_scales) {
-    copy_small<S::BYTES>((uint32_t)__cvta_generic_to_shared(dst), src);
-  } else {  // the others are zero: no group may be without a number
-#pragma unroll
-    for (int j = 0; j < S::COUNT; ++j) {
-      if constexpr (F == E2M1)
-        dst[j] = j < left ? __ldg(src + j) : 0;
-      else
-        reinterpret_cast<uint16_t*>(dst)[j] = j < left ? __ldg(reinterpret_cast<const uint16_t*>(src) + j) : 0;
+// Copies BYTES of a row's scales or zero points, of which `left` exist, with zeros behind the
+// last: every group needs a number.  Rows start on multiples of `unit` bytes: 16 (or all of
+// BYTES), 4, or less.
+template <int BYTES, int ITEM>
+__device__ __forceinline__ void copy_groups(uint8_t* dst, const uint8_t* src, int left, int unit) {
+  const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
+  if (unit == 16 && left >= BYTES) {
+    if constexpr (BYTES == 32) {
+      copy_async<16>(to, src);
+      copy_async<16>(to + 16, src + 16);
+    } else {
+      copy_async<BYTES>(to, src);
     }
-  }
-}
-template <typename T, Format F, int SPG>
-__device__ __forceinline__ void fetch_zeros(const Params& p, uint8_t* stage, int row, int64_t at,
-                                            int left) {
-  constexpr int COUNT = 8 / SPG;
-  const uint8_t* src = p.zeros + at;
-  uint8_t* dst = stage + STAGE_ZEROS + row * 8;
-  if (p.wide_zeros) {
-    if constexpr (COUNT == 2) src = p.zeros + (at & ~int64_t(3));  // these two and two others
-    copy_small<COUNT == 8 ? 8 : 4>((uint32_t)__cvta_generic_to_shared(dst), src);
-  } else {
+  } else if (unit >= 4) {
 #pragma unroll
-    for (int j = 0; j < COUNT; ++j) {
-      const uint8_t v = j < left ? __ldg(src + j) : 0;
-      dst[j] = v;
-      if (COUNT == 2) dst[j + 2] = v;
+    for (int j = 0; j < BYTES; j += 4) {
+      if (j < left)
+        copy_async<4>(to + j, src + j);
+      else
+        *reinterpret_cast<uint32_t*>(dst + j) = 0;
+    }
+  } else {
+    for (int j = 0; j < BYTES; j += ITEM) {
+      if constexpr (ITEM == 2)
+        *reinterpret_cast<uint16_t*>(dst + j) = j < left ? __ldg(reinterpret_cast<const uint16_t*>(src + j)) : 0;
+      else
+        dst[j] = j < left ? __ldg(src + j) : 0;
     }
   }
 }
@@ -350,28 +346,27 @@ __host__ __device__ constexpr int64_t x_pitch(int64_t K) {
   return (K + BLOCK_K - 1) / BLOCK_K * (BLOCK_K * 2) + 64;
 }
 
-constexpr int ring_bytes(int nt, int stages) { return warps_of(nt) * stages * STAGE; }
-constexpr int red_bytes(int nt) { return 2 * warps_of(nt) * 32 * 16 * nt; }
+constexpr int ring_bytes(int warps) { return warps * STAGES * STAGE; }
+constexpr int red_bytes(int nt, int warps) { return 2 * warps * 32 * 16 * nt; }
 // s_part, then of each route its place and perhaps a chunk, then two words an expert
 __host__ __device__ constexpr int route_bytes(int routes) {
   return routes == 0 ? 0 : 64 + (routes + 1) / 2 * 16 + (routes <= 32 ? 0 : 2 * MAX_EXPERTS * 4);
 }
 constexpr int MAX_ROOM = 16;  // rows of x in shared memory
-constexpr int fixed_bytes(int nt, int routes) {  // beside the ring and x
-  return red_bytes(nt) + route_bytes(routes) + MAX_ROOM * 4 + warps_of(nt) * 4;
+constexpr int fixed_bytes(int nt, int warps, int routes) {  // beside x
+  return ring_bytes(warps) + red_bytes(nt, warps) + route_bytes(routes) + MAX_ROOM * 4 + warps * 4;
 }
 
-template <typename T, Format F, int SPG, int NT, bool EXPERTS>
-__global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
+template <typename T, Format F, int SPG, int NT, int WARPS, bool EXPERTS>
+__global__ void __launch_bounds__(WARPS * 32, 1) w4_kernel(Params p) {
   using C = Codes<F>;
   using S = Scales<T, F, SPG>;
-  constexpr int WARPS = warps_of(NT);
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
   const int routes = EXPERTS ? p.routes : 0;
-  float4* red = reinterpret_cast<float4*>(smem + ring_bytes(NT, p.stages));
-  uint8_t* routing = reinterpret_cast<uint8_t*>(red) + red_bytes(NT);
+  float4* red = reinterpret_cast<float4*>(smem + ring_bytes(WARPS));
+  uint8_t* routing = reinterpret_cast<uint8_t*>(red) + red_bytes(NT, WARPS);
   float* s_power = reinterpret_cast<float*>(routing + route_bytes(routes));  // [MAX_ROOM]
   uint32_t* s_amax = reinterpret_cast<uint32_t*>(s_power + MAX_ROOM);       // [WARPS]
   uint8_t* s_x = reinterpret_cast<uint8_t*>(s_amax + WARPS);
@@ -487,7 +482,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
       uint4* dst = reinterpret_cast<uint4*>(s_x + col * xp);
       for (int i = lane0; i < pieces; i += per * 32) {
         if (i < real)
-          copy16((uint32_t)__cvta_generic_to_shared(dst + i), src + i * 8);
+          copy_async<16>((uint32_t)__cvta_generic_to_shared(dst + i), src + i * 8);
         else
           dst[i] = make_uint4(0, 0, 0, 0);
       }
@@ -497,8 +492,8 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
   Batch batch = batch_from(u0 / tiles);
   copy_x(batch);  // before the weights, behind which it would queue
 
-  // Weights and scales p.stages - 1 blocks ahead.
-  uint8_t* const ring_at = smem + warp * p.stages * STAGE;
+  // Weights and scales one block ahead.
+  uint8_t* const ring_at = smem + warp * STAGES * STAGE;
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(ring_at);
   const int groups = (int)(p.K / (32 * SPG));
   Run ahead = run_of(batch);
@@ -514,32 +509,33 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
   const uint32_t to = ring + (lane >> 3) * 128;
   uint32_t at_piece[2];  // rows r and r + 4 differ in the permutation
 #pragma unroll
-  for (int i = 0; i < 2; ++i) at_piece[i] = ((lane & 7) ^ (((lane >> 3) + 4 * i) & 7)) << 4;
+  for (int i = 0; i < 2; ++i) at_piece[i] = to + (((lane & 7) ^ (((lane >> 3) + 4 * i) & 7)) << 4);
   auto fetch = [&](int stage) {
     if (ahead.left > 0) {
-      const int byte = ahead.kb * 128, group = ahead.kb * S::COUNT;
-      if (byte + (lane & 7) * 16 < pitch) {
+      const int byte = ahead.kb * (BLOCK_K / 2), group = ahead.kb * (2 * S::COUNT);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          copy16(to + stage * STAGE + i * 512 + at_piece[i & 1], from[i] + byte);
-      }
+      for (int h = 0; h < 2; ++h)
+        if (byte + h * 128 + (lane & 7) * 16 < pitch) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            copy_async<16>(at_piece[i & 1] + stage * STAGE + h * HALF_STAGE + i * 512, from[i] + byte + h * 128);
+        }
+      uint8_t* to_groups = ring_at + stage * STAGE;
       if (lane < 16)
-        fetch_scales<T, F, SPG>(p, ring_at + stage * STAGE, lane, scales_at + group, groups - group);
+        copy_groups<2 * S::BYTES, S::ITEM>(to_groups + STAGE_SCALES + lane * 32,
+                                           static_cast<const uint8_t*>(p.scales) + (scales_at + group) * S::ITEM,
+                                           (groups - group) * S::ITEM, p.scale_unit);
       else if constexpr (F == INT4_ZEROS)
-        fetch_zeros<T, F, SPG>(p, ring_at + stage * STAGE, lane - 16, scales_at + group, groups - group);
+        copy_groups<2 * S::COUNT, 1>(to_groups + STAGE_ZEROS + (lane - 16) * 16,
+                                     p.zeros + (scales_at + group), groups - group, p.zero_unit);
       if (step(ahead) && ahead.left > 0) aim();
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  // all but the newest p.stages - 1 groups of copies are there
-  auto arrived = [&] {
-    if (p.stages == MAX_STAGES)
-      asm volatile("cp.async.wait_group %0;" ::"n"(MAX_STAGES - 1) : "memory");
-    else
-      asm volatile("cp.async.wait_group %0;" ::"n"(MIN_STAGES - 1) : "memory");
-  };
+  // all but the newest group of copies are there
+  auto arrived = [&] { asm volatile("cp.async.wait_group 1;" ::: "memory"); };
   if (ahead.left > 0) aim();
-  for (int s = 0; s < p.stages - 1; ++s) fetch(s);
+  fetch(0);
 
   // a lane's row of two 32-code pieces for ldmatrix
   const uint32_t lane_row = (lane & 15) * 128, lane_piece = ((lane >> 4) ^ (lane & 7)) << 4;
@@ -598,7 +594,7 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
     }
     int first = 0, count = 0, chunk = -1;  // of the unit at work
     const uint8_t* xr[NT];
-    float power[NT][2];
+    float2 power[NT];
     auto take_chunk = [&](int next) {
       if (next == chunk) return;
       chunk = next;
@@ -609,11 +605,9 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
         // columns without a row take the first one's; they are not stored
         const int col = t * 8 + g;
         xr[t] = s_x + (row0 + (col < count ? col : 0)) * xp + c * 16;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int of = t * 8 + 2 * c + e;
-          power[t][e] = s_power[row0 + (of < count ? of : 0)];
-        }
+        const int of = t * 8 + 2 * c;
+        power[t] = make_float2(s_power[row0 + (of < count ? of : 0)],
+                               s_power[row0 + (of + 1 < count ? of + 1 : 0)]);
       }
     };
 
@@ -641,11 +635,6 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
       }
     };
 
-    // Place in its word of this lane's rows' first zero point, where a block has two.
-    auto odd_row = [&](const Run& q, int r) {
-      return F == INT4_ZEROS && SPG == 4 && p.wide_scales ? (int)(row_of(q, g + 8 * r) * groups) & 2 : 0;
-    };
-
     // The sums of a unit that other warps have blocks of: where this warp has its first
     // block in place 1, else in place 0, [warp][place][NT][lane].
     auto place = [&](int w, int which) { return red + (w * 2 + which) * (32 * NT) + lane; };
@@ -654,63 +643,62 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1) w4_kernel(Params p) {
     while (run.left > 0) {
       take_chunk(run.chunk);
       const int kb0 = run.kb, kb1 = min(blocks, run.kb + run.left);
-      const int odd0[2] = {odd_row(run, 0), odd_row(run, 1)};
-      float acc[NT][4];
+      float2 acc[NT][2];
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[t][e] = 0.0f;
+      for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = both(0.0f);
 
       for (int kb = kb0; kb < kb1; ++kb) {
-        fetch(stage == 0 ? p.stages - 1 : stage - 1);
+        fetch(stage ^ 1);
         arrived();
         __syncwarp();
-        S sc[2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) sc[r].read(ring_at + stage * STAGE, g + 8 * r, (odd0[r] + 2 * kb) & 2);
-        const uint32_t base = ring + stage * STAGE + lane_row;
-        float part[NT][4];
-        float2 s0, s1;
+        for (int h = 0; h < 2; ++h) {
+          S sc[2];
 #pragma unroll
-        for (int s = 0; s < 8; s += 2) {
-          uint32_t w[4];  // words of rows g and g + 8 of 32 codes, then of the next 32
-          asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                       : "r"(base + (lane_piece ^ (s << 4))));
+          for (int r = 0; r < 2; ++r) sc[r].read(ring_at + stage * STAGE, g + 8 * r, h);
+          const uint32_t base = ring + stage * STAGE + h * HALF_STAGE + lane_row;
+          float part[NT][4];
+          float2 s0, s1;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int j = (s + i) / SPG;
-            uint32_t d0[4], d1[4];
-            C::pairs(w[2 * i], C::offset(sc[0].zero(j)), d0);
-            C::pairs(w[2 * i + 1], C::offset(sc[1].zero(j)), d1);
-            const uint32_t a0[4] = {d0[0], d1[0], d0[1], d1[1]};
-            const uint32_t a1[4] = {d0[2], d1[2], d0[3], d1[3]};
+          for (int s = 0; s < 8; s += 2) {
+            uint32_t w[4];  // words of rows g and g + 8 of 32 codes, then of the next 32
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(base + (lane_piece ^ (s << 4))));
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              const uint4 v = *reinterpret_cast<const uint4*>(xr[t] + kb * (BLOCK_K * 2) + (s + i) * 64);
-              mma_tile(part[t], a0, v.x, v.y, (s + i) % SPG == 0);
-              mma_tile(part[t], a1, v.z, v.w, false);
-            }
-            if ((s + i) % SPG == SPG - 1) {
-              if (j % 2 == 0) s0 = sc[0].scales(j / 2), s1 = sc[1].scales(j / 2);
-              const float f0 = j % 2 == 0 ? s0.x : s0.y, f1 = j % 2 == 0 ? s1.x : s1.y;
+            for (int i = 0; i < 2; ++i) {
+              const int j = (s + i) / SPG;
+              uint32_t d0[4], d1[4];
+              C::pairs(w[2 * i], C::offset(sc[0].zero(j)), d0);
+              C::pairs(w[2 * i + 1], C::offset(sc[1].zero(j)), d1);
+              const uint32_t a0[4] = {d0[0], d1[0], d0[1], d1[1]};
+              const uint32_t a1[4] = {d0[2], d1[2], d0[3], d1[3]};
 #pragma unroll
               for (int t = 0; t < NT; ++t) {
-                acc[t][0] = fmaf(f0 * power[t][0], part[t][0], acc[t][0]);
-                acc[t][1] = fmaf(f0 * power[t][1], part[t][1], acc[t][1]);
-                acc[t][2] = fmaf(f1 * power[t][0], part[t][2], acc[t][2]);
-                acc[t][3] = fmaf(f1 * power[t][1], part[t][3], acc[t][3]);
+                const uint4 v = *reinterpret_cast<const uint4*>(xr[t] + kb * (BLOCK_K * 2) +
+                                                                (h * 8 + s + i) * 64);
+                mma_tile(part[t], a0, v.x, v.y, (s + i) % SPG == 0);
+                mma_tile(part[t], a1, v.z, v.w, false);
+              }
+              if ((s + i) % SPG == SPG - 1) {
+                if (j % 2 == 0) s0 = sc[0].scales(j / 2), s1 = sc[1].scales(j / 2);
+                const float2 f0 = both(j % 2 == 0 ? s0.x : s0.y), f1 = both(j % 2 == 0 ? s1.x : s1.y);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                  acc[t][0] = fma2(mul2(f0, power[t]), make_float2(part[t][0], part[t][1]), acc[t][0]);
+                  acc[t][1] = fma2(mul2(f1, power[t]), make_float2(part[t][2], part[t][3]), acc[t][1]);
+                }
               }
             }
           }
         }
         __syncwarp();  // the stage is free
-        if (++stage == p.stages) stage = 0;
+        stage ^= 1;
       }
 
       float4 sums[NT];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) sums[t] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+      for (int t = 0; t < NT; ++t) sums[t] = make_float4(acc[t][0].x, acc[t][0].y, acc[t][1].x, acc[t][1].y);
       if (kb1 - kb0 == blocks) {
         store(run.tile, sums);
       } else {
@@ -761,66 +749,71 @@ namespace w4 = moe::w4;
 
 constexpr int kW4Smem = 232448 - 1024;
 
-// Rows of x that a block has room for.
-static int w4_room(int nt, int routes, int64_t K) {
-  const int64_t n = (kW4Smem - w4::fixed_bytes(nt, routes) - w4::ring_bytes(nt, w4::MIN_STAGES)) /
-                    w4::x_pitch(K);
+// Rows of x that a CTA has room for.
+static int w4_room(int nt, int warps, int routes, int64_t K) {
+  const int64_t n = (kW4Smem - w4::fixed_bytes(nt, warps, routes)) / w4::x_pitch(K);
   return (int)(n < w4::MAX_ROOM ? n : w4::MAX_ROOM);
 }
 
-template <typename T, w4::Format F, int SPG, int NT, bool EXPERTS>
+template <typename T, w4::Format F, int SPG, int NT, int WARPS, bool EXPERTS>
 static moe_status_t launch_w4(w4::Params p, cudaStream_t s) {
-  constexpr auto kernel = w4::w4_kernel<T, F, SPG, NT, EXPERTS>;
+  constexpr auto kernel = w4::w4_kernel<T, F, SPG, NT, WARPS, EXPERTS>;
   moe_status_t st = allow_smem<kernel>(kW4Smem);
   if (st != MOE_OK) return st;
-  p.room = w4_room(NT, EXPERTS ? p.routes : 0, p.K);
+  const int routes = EXPERTS ? p.routes : 0;
+  const int64_t rows = EXPERTS ? p.routes : p.T, ctas = num_sms();
+  p.room = w4_room(NT, WARPS, routes, p.K);
   const int room = p.room < 8 * NT ? p.room : 8 * NT;
-  const int64_t rows = EXPERTS ? p.routes : p.T;
   const int64_t passes = (rows + room - 1) / room;
   p.most = EXPERTS ? (int)(rows < room ? rows : room) : (int)((rows + passes - 1) / passes);
   const int tile = p.act == MOE_ACT_NONE ? w4::ROWS : w4::ROWS / 2;
   const int64_t tiles = (p.n_out + tile - 1) / tile;
-  const int64_t chunks = EXPERTS ? p.routes : passes;
-  const int64_t ctas = num_sms();
-  const int64_t units = tiles * chunks;
+  const int64_t chunks = EXPERTS ? p.routes : passes, units = tiles * chunks;
   p.tiles = (int)tiles;
   p.blocks = (int)((p.K + w4::BLOCK_K - 1) / w4::BLOCK_K);
   p.blocks_inverse = (uint32_t)(((uint64_t)1 << 32) / p.blocks + 1);  // of 1 it is not used
   // a CTA's units lie in few chunks where there are many units
   const int64_t likely = (EXPERTS && p.E < chunks ? p.E : chunks) / ctas + 2;
   if (p.room > p.most * likely) p.room = (int)(p.most * likely);
-  int64_t smem = w4::fixed_bytes(NT, EXPERTS ? p.routes : 0) + p.room * w4::x_pitch(p.K);
-  p.stages = smem + w4::ring_bytes(NT, w4::MAX_STAGES) <= kW4Smem ? w4::MAX_STAGES : w4::MIN_STAGES;
-  smem += w4::ring_bytes(NT, p.stages);
-  return launched(launch_pdl(kernel, dim3((unsigned)(units < ctas ? units : ctas)), dim3(w4::warps_of(NT) * 32),
+  const int64_t smem = w4::fixed_bytes(NT, WARPS, routes) + p.room * w4::x_pitch(p.K);
+  return launched(launch_pdl(kernel, dim3((unsigned)(units < ctas ? units : ctas)), dim3(WARPS * 32),
                              (size_t)smem, s, p),
                   "4-bit products");
 }
 
-template <typename T, w4::Format F, int SPG>
+// Sixteen warps keep the SM's pipes busy; eight leave room for more rows of x, so that the
+// weights pass fewer times.
+template <typename T, w4::Format F, int SPG, bool EXPERTS>
 static moe_status_t run_w4(const w4::Params& p, cudaStream_t s) {
-  if (p.ids != nullptr) {
-    // most experts of a short batch have one or two of its routes
-    if (p.routes <= 8 * p.E) return launch_w4<T, F, SPG, 1, true>(p, s);
-    return launch_w4<T, F, SPG, 2, true>(p, s);
-  }
-  // as few passes over the matrix as there can be, and then as few columns of zeros
-  const int64_t one = w4_room(1, 0, p.K) < 8 ? w4_room(1, 0, p.K) : 8, two = w4_room(2, 0, p.K);
-  if ((p.T + one - 1) / one <= (p.T + two - 1) / two) return launch_w4<T, F, SPG, 1, false>(p, s);
-  return launch_w4<T, F, SPG, 2, false>(p, s);
+  const int routes = EXPERTS ? p.routes : 0;
+  // rows of a matrix: of a short batch's experts most have one or two
+  const int64_t rows = EXPERTS ? (p.routes + p.E - 1) / p.E * 2 : p.T;
+  auto passes = [&](int nt, int warps) {
+    const int64_t n = w4_room(nt, warps, routes, p.K), m = n < 8 * nt ? n : 8 * nt;
+    return (rows + m - 1) / m;
+  };
+  if (passes(1, 16) <= passes(1, 8) && passes(1, 16) <= passes(2, 8))
+    return launch_w4<T, F, SPG, 1, 16, EXPERTS>(p, s);
+  if (passes(1, 8) <= passes(2, 8)) return launch_w4<T, F, SPG, 1, 8, EXPERTS>(p, s);
+  return launch_w4<T, F, SPG, 2, 8, EXPERTS>(p, s);
 }
 
 template <typename T>
 static moe_status_t run_w4_format(const w4::Params& p, int format, int64_t group, cudaStream_t s) {
-  if (format == MOE_W4_E2M1) return run_w4<T, w4::E2M1, 1>(p, s);
-  if (p.zeros != nullptr) {
-    if (group == 32) return run_w4<T, w4::INT4_ZEROS, 1>(p, s);
-    if (group == 64) return run_w4<T, w4::INT4_ZEROS, 2>(p, s);
-    return run_w4<T, w4::INT4_ZEROS, 4>(p, s);
-  }
-  if (group == 32) return run_w4<T, w4::INT4, 1>(p, s);
-  if (group == 64) return run_w4<T, w4::INT4, 2>(p, s);
-  return run_w4<T, w4::INT4, 4>(p, s);
+  auto run = [&](auto f, auto spg) {
+    constexpr w4::Format F = decltype(f)::value;
+    constexpr int SPG = decltype(spg)::value;
+    return p.ids != nullptr ? run_w4<T, F, SPG, true>(p, s) : run_w4<T, F, SPG, false>(p, s);
+  };
+  auto groups = [&](auto f) {
+    if (group == 32) return run(f, std::integral_constant<int, 1>{});
+    if (group == 64) return run(f, std::integral_constant<int, 2>{});
+    return run(f, std::integral_constant<int, 4>{});
+  };
+  if (format == MOE_W4_E2M1)
+    return run(std::integral_constant<w4::Format, w4::E2M1>{}, std::integral_constant<int, 1>{});
+  if (p.zeros != nullptr) return groups(std::integral_constant<w4::Format, w4::INT4_ZEROS>{});
+  return groups(std::integral_constant<w4::Format, w4::INT4>{});
 }
 
 }  // namespace moe_host
@@ -886,10 +879,13 @@ moe_status_t moe_w4_linear(const moe_w4_linear_args_t* a, void* stream) {
   p.ids = a->topk_ids;
   p.ids64 = a->topk_ids_dtype == MOE_IDS_INT64;
   p.act = a->activation;
-  p.wide_scales = K % w4::BLOCK_K == 0 && rows_aligned16(a->scales, 0, 1, 1) &&
-                  (a->zeros == nullptr || (reinterpret_cast<uintptr_t>(a->zeros) & 7u) == 0);
-  // of two zero points a block a word is read, which the end of the tensor has to hold
-  p.wide_zeros = p.wide_scales && (G != 128 || (experts ? E : 1) * N * (K / G) % 4 == 0);
+  auto unit = [&](const void* base, int64_t item) {
+    const uint64_t row = (uint64_t)(K / G * item), block = (uint64_t)(w4::BLOCK_K / G * item);
+    const uint64_t bits = row | reinterpret_cast<uintptr_t>(base);
+    return bits % (block < 16 ? block : 16) == 0 ? 16 : (bits % 4 == 0 ? 4 : 1);
+  };
+  p.scale_unit = unit(a->scales, a->format == MOE_W4_E2M1 ? 1 : 2);
+  p.zero_unit = unit(a->zeros, 1);
   p.out = a->out;
   p.out_stride = a->out_stride0;
   p.status = a->device_status;
