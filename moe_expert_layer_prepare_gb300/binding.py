@@ -623,12 +623,13 @@ def _flat(name, t, shape, dtype):
     return t.data_ptr()
 
 
-def _here(**tensors):
+def _here(*tensors):
     """Every tensor on the current device, whose stream a call goes to."""
     dev = _current_device()
-    for name, t in tensors.items():
+    for t in tensors:
         if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name}: on {t.device}, and the current device is cuda:{dev}")
+            raise ValueError(f"a tensor {list(t.shape)} is on {t.device}, and the current device is "
+                             f"cuda:{dev}")
 
 
 def _code(name, dtype, table=_DTYPE):
@@ -863,7 +864,7 @@ def moe_norm_quant(x, weight, q, q_sf, z=None, x_out=None, y=None, rstd=None, we
     dt, wdt, sdt = x.dtype, weight.dtype, q_sf.dtype
     G = (K + 127) // 128
     mode = MOE_SF_FP32 if sdt is _FP32 else MOE_SF_UE8M0_PACKED
-    _here(x=x, weight=weight, q=q, q_sf=q_sf, z=z, x_out=x_out, y=y, rstd=rstd)
+    _here(x, weight, q, q_sf, z, x_out, y, rstd)
     _call("moe_norm_quant", NormQuantArgs.pack(
         T, K, _code("x", dt), _code("weight", wdt), x.data_ptr(), _rows("x", x, shape, dt),
         _at(z), _rows("z", z, shape, dt), _flat("weight", weight, (K,), wdt), weight_offset, eps,
@@ -886,7 +887,7 @@ def moe_gated_linear(x, weight, out, activation=MOE_ACT_SILU, gate_up=None, devi
     if rows % 2:
         raise ValueError(f"weight: {rows} rows are not as many gate rows as up rows")
     N = rows // 2
-    _here(x=x, weight=weight, out=out, gate_up=gate_up, device_status=device_status)
+    _here(x, weight, out, gate_up, device_status)
     _call("moe_gated_linear", GatedLinearArgs.pack(
         T, K, N, _code("x", dt), activation, x.data_ptr(), _rows("x", x, shape, dt),
         _flat("weight", weight, (rows, K), dt), out.data_ptr(), _rows("out", out, (T, N), dt),
@@ -909,8 +910,7 @@ def moe_gated_linear_backward(d_out, x, weight, gate_up, d_x=None, d_weight=None
     if rows % 2:
         raise ValueError(f"weight: {rows} rows are not as many gate rows as up rows")
     N = rows // 2
-    _here(d_out=d_out, x=x, weight=weight, gate_up=gate_up, d_x=d_x, d_weight=d_weight,
-          workspace=workspace, device_status=device_status)
+    _here(d_out, x, weight, gate_up, d_x, d_weight, workspace, device_status)
     _call("moe_gated_linear_backward", GatedLinearBackwardArgs.pack(
         T, K, N, _code("x", dt), activation, d_out.data_ptr(), _rows("d_out", d_out, (T, N), dt),
         x.data_ptr(), _rows("x", x, shape, dt), _flat("weight", weight, (rows, K), dt),
@@ -945,8 +945,7 @@ def moe_w4_linear(x, weight, scales, out, zeros=None, topk_ids=None, activation=
     if sdt is not torch.uint8 and sdt is not dt:
         raise ValueError(f"scales: want {dt} or torch.uint8 exponents, got {sdt}")
     lead, rows = tuple(ws[:-1]), T * k if E else T
-    _here(x=x, weight=weight, scales=scales, out=out, zeros=zeros, topk_ids=topk_ids,
-          device_status=device_status)
+    _here(x, weight, scales, out, zeros, topk_ids, device_status)
     n_out = N if activation == MOE_ACT_NONE else N // 2
     _call("moe_w4_linear", W4LinearArgs.pack(
         T, K, N, E, k, K // groups, _code("x", dt),

@@ -124,6 +124,58 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// VEC weights of a pack as they lie in shared memory, in their own type; fp32 ones
+// four a plane, so that neighbouring threads read neighbouring 16 bytes.
+template <int VEC>
+__device__ __forceinline__ void read_weights(const uint8_t* s, int dtype, int c, int packs,
+                                             float2 (&w)[VEC / 2]) {
+  if (dtype == MOE_DTYPE_FP32) {
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i) {
+      const float4 v = *reinterpret_cast<const float4*>(s + ((size_t)i * packs + c) * 16);
+      w[2 * i] = make_float2(v.x, v.y), w[2 * i + 1] = make_float2(v.z, v.w);
+    }
+    return;
+  }
+  uint32_t u[VEC / 2];
+  if constexpr (VEC == 8) {
+    const uint4 v = *reinterpret_cast<const uint4*>(s + (size_t)c * 16);
+    u[0] = v.x, u[1] = v.y, u[2] = v.z, u[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(s + (size_t)c * 8);
+    u[0] = v.x, u[1] = v.y;
+  }
+  if (dtype == MOE_DTYPE_BF16) {
+#pragma unroll
+    for (int q = 0; q < VEC / 2; ++q) w[q] = unpack2<__nv_bfloat16>(u[q]);
+  } else {
+#pragma unroll
+    for (int q = 0; q < VEC / 2; ++q) w[q] = unpack2<__half>(u[q]);
+  }
+}
+
+// Copies a thread's packs of a [K] tensor to shared memory.
+template <int VEC, int NV>
+__device__ __forceinline__ void fetch_weights(uint8_t* dst, const void* src, int dtype, int packs) {
+  const int bytes = VEC * (dtype == MOE_DTYPE_FP32 ? 4 : 2);  // of a pack: 8, 16 or 32
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = threadIdx.x + i * blockDim.x;
+    if (c >= packs) break;
+    const size_t o = (size_t)c * bytes;
+    const uint8_t* g = static_cast<const uint8_t*>(src) + o;
+    if (bytes == 8) {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(
+                       (uint32_t)__cvta_generic_to_shared(dst + o)),
+                   "l"(g)
+                   : "memory");
+    } else {
+      copy16(dst + (size_t)c * 16, g);
+      if (bytes == 32) copy16(dst + (size_t)(packs + c) * 16, g + 16);
+    }
+  }
+}
+
 }  // namespace moe
 
 namespace moe_host {

@@ -55,30 +55,66 @@ __device__ __forceinline__ void store_scale(const NormQuantParams& p, int64_t t,
   }
 }
 
-// Rows of 16-byte packs, NV a thread.
-template <typename T, int NV, bool FP32>
-__global__ void __launch_bounds__(512) norm_quant_rows_kernel(NormQuantParams p) {
+// Rows of 16-byte packs, NV a thread: a block takes every gridDim.x-th row and has the next
+// one's x and z on their way to shared memory while it works; the weights come there once.
+// Each thread reads only packs that it copied.  With one STAGE the next row is copied over
+// this one as soon as x' is in registers, with two from the row's start.
+template <typename T, int NV, int STAGES, bool FP32>
+__global__ void __launch_bounds__(512, NV <= 2 ? (STAGES == 1 ? 3 : 2) : 1)
+    norm_quant_rows_kernel(NormQuantParams p) {
   constexpr int VEC = 16 / sizeof(T), H = VEC / 2, LANES = kGroup / VEC;
   using P = Pack<T, VEC>;
+  extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float part[2][32];
   const int tid = threadIdx.x, threads = blockDim.x;
-  const int packs = (int)(p.K / VEC);
+  const int packs = (int)(p.K / VEC), w_dtype = p.w_dtype;
   const float inv_k = 1.0f / (float)p.K;
+  P* stage0 = reinterpret_cast<P*>(smem);
+  const int stage_packs = (1 + (p.z != nullptr)) * packs;
+  uint8_t* s_w = smem + (size_t)STAGES * stage_packs * 16;
   pdl_wait();
   pdl_launch_dependents();
+  auto fetch = [&](int64_t t, int s) {
+    if (t < p.T) {
+      P* dst = stage0 + s * stage_packs;
+      const T* x = static_cast<const T*>(p.x) + t * p.x_stride;
+      const T* z = static_cast<const T*>(p.z) + t * p.z_stride;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = tid + i * threads;
+        if (c >= packs) break;
+        copy16(dst + c, x + c * VEC);
+        if (p.z != nullptr) copy16(dst + packs + c, z + c * VEC);
+      }
+    }
+  };
+  fetch(blockIdx.x, 0);
+  fetch_weights<VEC, NV>(s_w, p.w, w_dtype, packs);
+  copies_commit();
+  const float2 offset = both(p.offset);
   int it = 0;
   for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, it ^= 1) {
+    if (STAGES == 2) {
+      fetch(t + gridDim.x, it ^ 1);
+      copies_commit();
+    }
+    copies_wait<STAGES - 1>();
+    const P* st = STAGES == 2 ? stage0 + it * stage_packs : stage0;
     float2 v[NV][H];
     float2 ss = both(0.0f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = tid + i * threads;
-      P x = zero_pack<T, VEC>();
-      if (c < packs) x = load_pack<T, VEC>(static_cast<const T*>(p.x) + t * p.x_stride + c * VEC);
+      if (c >= packs) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) v[i][h] = both(0.0f);
+        continue;
+      }
+      const P x = st[c];
 #pragma unroll
       for (int h = 0; h < H; ++h) v[i][h] = x.get2(h);
-      if (p.z != nullptr && c < packs) {
-        const P z = load_pack<T, VEC>(static_cast<const T*>(p.z) + t * p.z_stride + c * VEC);
+      if (p.z != nullptr) {
+        const P z = st[packs + c];
         P o;
 #pragma unroll
         for (int h = 0; h < H; ++h) {
@@ -90,6 +126,10 @@ __global__ void __launch_bounds__(512) norm_quant_rows_kernel(NormQuantParams p)
 #pragma unroll
       for (int h = 0; h < H; ++h) ss = fma2(v[i][h], v[i][h], ss);
     }
+    if (STAGES == 1) {
+      fetch(t + gridDim.x, 0);
+      copies_commit();
+    }
     const float r = rsqrtf(fmaf(block_sum(ss.x + ss.y, part[it]), inv_k, p.eps));
     if (tid == 0 && p.rstd != nullptr) p.rstd[t] = r;
 #pragma unroll
@@ -97,15 +137,15 @@ __global__ void __launch_bounds__(512) norm_quant_rows_kernel(NormQuantParams p)
       const int c = tid + i * threads;
       const bool live = c < packs;
       if (i * threads + (tid & ~31) >= packs) break;  // the same in a whole warp
-      float w[VEC];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) w[e] = 0.0f;
-      if (live) load_weights<VEC>(p.w, p.w_dtype, (int64_t)c * VEC, p.offset, w);
       float amax = 0.0f;
+      if (live) {
+        float2 w[H];
+        read_weights<VEC>(s_w, w_dtype, c, packs, w);
 #pragma unroll
-      for (int h = 0; h < H; ++h) {
-        v[i][h] = mul2(mul2(v[i][h], both(r)), make_float2(w[2 * h], w[2 * h + 1]));
-        amax = fmaxf(amax, fmaxf(fabsf(v[i][h].x), fabsf(v[i][h].y)));
+        for (int h = 0; h < H; ++h) {
+          v[i][h] = mul2(mul2(v[i][h], both(r)), add2(w[h], offset));
+          amax = fmaxf(amax, fmaxf(fabsf(v[i][h].x), fabsf(v[i][h].y)));
+        }
       }
 #pragma unroll
       for (int o = LANES / 2; o > 0; o >>= 1)
@@ -132,6 +172,7 @@ __global__ void __launch_bounds__(512) norm_quant_rows_kernel(NormQuantParams p)
         *reinterpret_cast<uint32_t*>(dst) = q[0];
     }
   }
+  copies_wait<0>();
 }
 
 // Any other rows: a warp has a group, four columns a lane, in a second pass over the
@@ -192,11 +233,17 @@ namespace moe_host {
 
 using moe::NormQuantParams;
 
-template <auto Kernel>
-static moe_status_t launch_norm_quant(const NormQuantParams& p, int threads, cudaStream_t s) {
-  const int64_t cap =
-      (int64_t)num_sms() * resident_blocks(reinterpret_cast<const void*>(Kernel), threads);
-  return launched(launch_pdl(Kernel, dim3((unsigned)(p.T < cap ? p.T : cap)), dim3(threads), 0, s, p),
+static size_t quant_rows_smem(const NormQuantParams& p, size_t elem, int stages) {
+  return (size_t)p.K * (stages * (1 + (p.z != nullptr)) * elem + dtype_size(p.w_dtype));
+}
+
+template <typename E, int NV, int STAGES, bool FP32>
+static moe_status_t launch_quant_rows(const NormQuantParams& p, int threads, cudaStream_t s) {
+  constexpr auto kernel = moe::norm_quant_rows_kernel<E, NV, STAGES, FP32>;
+  const size_t smem = quant_rows_smem(p, sizeof(E), STAGES);
+  const int64_t cap = (int64_t)num_sms() * resident_with<kernel>(threads, smem);
+  if (cap == 0) return set_error(MOE_ERR_CUDA, "norm quant: no resident block");
+  return launched(launch_pdl(kernel, dim3((unsigned)(p.T < cap ? p.T : cap)), dim3(threads), smem, s, p),
                   "norm quant");
 }
 
@@ -212,19 +259,24 @@ static moe_status_t run_norm_quant(const NormQuantParams& p, cudaStream_t s) {
   w.weights(p.w);
   w.ok = w.ok && reinterpret_cast<uintptr_t>(p.q) % V == 0 && (p.T <= 1 || p.q_stride % V == 0);
   if (!w.ok) {
+    constexpr auto kernel = moe::norm_quant_kernel<E, FP32>;
     const int64_t groups = (p.K + moe::kGroup - 1) / moe::kGroup;
-    return launch_norm_quant<moe::norm_quant_kernel<E, FP32>>(
-        p, (int)(groups < 16 ? groups : 16) * 32, s);
+    const int threads = (int)(groups < 16 ? groups : 16) * 32;
+    const int64_t cap =
+        (int64_t)num_sms() * resident_blocks(reinterpret_cast<const void*>(kernel), threads);
+    return launched(launch_pdl(kernel, dim3((unsigned)(p.T < cap ? p.T : cap)), dim3(threads), 0, s, p),
+                    "norm quant");
   }
   const int64_t packs = p.K / V;
   auto threads = [&](int nv) { return (int)(((packs + nv - 1) / nv + 31) / 32 * 32); };
-  if (packs <= 512)
-    return launch_norm_quant<moe::norm_quant_rows_kernel<E, 1, FP32>>(p, threads(1), s);
-  if (packs <= 1024)
-    return launch_norm_quant<moe::norm_quant_rows_kernel<E, 2, FP32>>(p, threads(2), s);
-  if (packs <= 2048)
-    return launch_norm_quant<moe::norm_quant_rows_kernel<E, 4, FP32>>(p, threads(4), s);
-  return launch_norm_quant<moe::norm_quant_rows_kernel<E, 8, FP32>>(p, threads(8), s);
+  const bool two = quant_rows_smem(p, sizeof(E), 2) <= kMaxBlockSmem;
+  if (packs <= 512) return launch_quant_rows<E, 1, 2, FP32>(p, threads(1), s);
+  if (packs <= 1024) return launch_quant_rows<E, 2, 1, FP32>(p, threads(2), s);
+  if (packs <= 2048) return launch_quant_rows<E, 4, 2, FP32>(p, threads(4), s);
+  if constexpr (sizeof(E) == 4)
+    return two ? launch_quant_rows<E, 8, 2, FP32>(p, threads(8), s)
+               : launch_quant_rows<E, 8, 1, FP32>(p, threads(8), s);
+  return set_error(MOE_ERR_UNSUPPORTED, "hidden_size too large");
 }
 
 }  // namespace moe_host
