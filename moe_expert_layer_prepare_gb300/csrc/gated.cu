@@ -38,28 +38,47 @@ struct Params {
   int64_t gate_up_stride;
   bool out_wide, gate_up_wide;  // rows that start on 16 bytes
   float* partials;              // pieces of tiles; nullptr: no tile is cut
+  int half;                     // outputs of a tile of the forward
   int pairs, splits;
   uint32_t* status;
 };
 
-// 16 values to neighbouring columns of a row, of which `left` exist.
+// 16 values a lane to neighbouring columns of its row, the warp's rows from `first` on, of
+// which `rows` and `left` exist.  Rows that do not start on 16 bytes, and a last tile's columns,
+// go through shared memory, so that a store covers two rows' 32 bytes and not two of 32 rows
+// (1031 tokens, 2056 -> 1403, with gate_up: 73 us by single stores).
+constexpr int STORE_PITCH = 18;
 template <typename T>
-__device__ __forceinline__ void store16(T* p, const float (&v)[16], int64_t left, bool wide) {
-  if (wide && left >= 16) {
-    uint32_t w[8];
+__device__ __forceinline__ void store16(T* first, int64_t stride, int64_t rows, const float (&v)[16],
+                                        int64_t left, bool wide, T* buf) {
+  const int lane = threadIdx.x & 31;
+  uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = pack2<T>(make_float2(v[2 * i], v[2 * i + 1]));
+  for (int i = 0; i < 8; ++i) w[i] = pack2<T>(make_float2(v[2 * i], v[2 * i + 1]));
+  if (wide && left >= 16) {
+    if (lane >= rows) return;
+    T* p = first + lane * stride;
     st_v4(p, make_uint4(w[0], w[1], w[2], w[3]));
     st_v4(p + 8, make_uint4(w[4], w[5], w[6], w[7]));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < left) p[i] = from_f32<T>(v[i]);
+    return;
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) reinterpret_cast<uint32_t*>(buf + lane * STORE_PITCH)[i] = w[i];
+  __syncwarp();
+  const int c = lane & 15;
+  if (c < left)
+#pragma unroll
+    for (int r = 0; r < 32; r += 2) {
+      const int row = r + (lane >> 4);
+      if (row < rows) first[row * stride + c] = buf[row * STORE_PITCH + c];
+    }
+  __syncwarp();
 }
 
 // ------------------------------------------------------------- few tokens
-constexpr int SPLIT_TOKENS = 512;
+// At 128 tokens this path takes 16 us (7168 -> 2048) and the pairs 33; at 512 36 us and two
+// pairs a tile 25, into 14336 features 175 and 82.
+constexpr int SPLIT_TOKENS = 128;
 constexpr int SM_ROWS = 128;     // of a tile: 64 gate rows of W, 64 up rows
 constexpr int SM_FEATURES = 64;  // outputs of a tile
 constexpr int SM_A_BYTES = SM_ROWS * 128;
@@ -67,6 +86,30 @@ constexpr int SM_THREADS = 256;
 constexpr int SM_MAX_STAGES = 5;
 constexpr int sm_stages(int nt) { return nt <= 32 ? 5 : 4; }
 constexpr int sm_smem(int nt) { return 1024 + sm_stages(nt) * (SM_A_BYTES + nt * 128) + 256; }
+
+// Four neighbouring outputs of a token, of which some may not exist.
+template <typename T>
+__device__ __forceinline__ void store4(const Params& p, int64_t t, int64_t n, float4 g, float4 u) {
+  const float gv[4] = {g.x, g.y, g.z, g.w}, uv[4] = {u.x, u.y, u.z, u.w};
+  float o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = act_value(p.act, gv[e]) * uv[e];
+  auto put = [&](T* dst, const float (&v)[4], bool wide) {
+    if (wide && n + 4 <= p.N) {
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(pack2<T>(make_float2(v[0], v[1])), pack2<T>(make_float2(v[2], v[3])));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < p.N) dst[e] = from_f32<T>(v[e]);
+    }
+  };
+  put(static_cast<T*>(p.out) + t * p.out_stride + n, o, p.out_wide);
+  if (p.gate_up == nullptr) return;
+  T* gu = static_cast<T*>(p.gate_up) + t * p.gate_up_stride + n;
+  put(gu, gv, p.gate_up_wide);
+  put(gu + p.N, uv, p.gate_up_wide);
+}
 
 // Stores the CTA's share of the tile's tokens from the cluster's sums in rank order.
 template <typename T, int SPLITS>
@@ -91,16 +134,7 @@ __device__ __forceinline__ void join_tokens(const Params& p, const float* sums, 
       g[0].x += g[r].x, g[0].y += g[r].y, g[0].z += g[r].z, g[0].w += g[r].w;
       u[0].x += u[r].x, u[0].y += u[r].y, u[0].z += u[r].z, u[0].w += u[r].w;
     }
-    const float gv[4] = {g[0].x, g[0].y, g[0].z, g[0].w};
-    const float uv[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
-    T* out = static_cast<T*>(p.out) + t * p.out_stride + n;
-    T* gu = static_cast<T*>(p.gate_up) + t * p.gate_up_stride + n;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (n + e >= p.N) break;
-      out[e] = from_f32<T>(act_value(p.act, gv[e]) * uv[e]);
-      if (p.gate_up != nullptr) gu[e] = from_f32<T>(gv[e]), gu[p.N + e] = from_f32<T>(uv[e]);
-    }
+    store4<T>(p, t, n, g[0], u[0]);
   }
 }
 
@@ -268,8 +302,10 @@ constexpr int HALF = 128;  // of them one CTA's operands
 constexpr int STAGES = 6;
 constexpr int OPERAND = HALF * 128;  // bytes of one CTA's A or B in a stage
 constexpr int STAGE_BYTES = 2 * OPERAND;
-constexpr int THREADS = 192;
-constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + 256;
+constexpr int EPI_WARPS = 8;  // two for each 32 rows of the accumulator
+constexpr int THREADS = (2 + EPI_WARPS) * 32;
+constexpr int STORE_BYTES = 32 * STORE_PITCH * 2;  // of a warp
+constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + 256 + EPI_WARPS * STORE_BYTES;
 constexpr int MIN_SLABS = 8;                    // of a piece of a tile
 constexpr int64_t PIECE = (int64_t)TILE * TILE;  // its sums
 
@@ -277,12 +313,12 @@ constexpr int64_t PIECE = (int64_t)TILE * TILE;  // its sums
 // that would leave pairs idle cut along k, so that each pair has a piece.
 struct Work {
   int m_tiles, n_tiles, units, slabs, full, parts, items, per;
-  __host__ __device__ Work(Mode mode, int64_t T, int64_t K, int64_t N, int pairs, bool cut) {
+  __host__ __device__ Work(Mode mode, int64_t T, int64_t K, int64_t N, int pairs, bool cut, int half) {
     const int64_t m = mode == D_W ? 2 * N : T, n = mode == FORWARD ? 2 * N : K;
     const int64_t k = mode == FORWARD ? K : (mode == D_X ? 2 * N : T);
     m_tiles = (int)((m + TILE - 1) / TILE);
-    // a tile of the forward has HALF gate rows and as many up rows
-    n_tiles = mode == FORWARD ? (int)((N + HALF - 1) / HALF) : (int)((n + TILE - 1) / TILE);
+    // a tile of the forward has `half` gate rows and as many up rows
+    n_tiles = mode == FORWARD ? (int)((N + half - 1) / half) : (int)((n + TILE - 1) / TILE);
     units = m_tiles * n_tiles;
     slabs = (int)((k + 63) / 64);
     const int rest = units % pairs;
@@ -315,7 +351,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                       const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmB2) {
   constexpr bool A_MN = MODE == D_W, B_MN = MODE != FORWARD;
-  constexpr uint32_t IDESC = f16_idesc(std::is_same<T, __nv_bfloat16>::value, TILE, TILE) |
+  constexpr uint32_t IDESC_FULL = f16_idesc(std::is_same<T, __nv_bfloat16>::value, TILE, TILE) |
                              (A_MN ? IDESC_A_MN : 0u) | (B_MN ? IDESC_B_MN : 0u);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -337,7 +373,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull0 + 8 * b, 1);
-      mbar_init(tempty0 + 8 * b, 2 * 4);
+      mbar_init(tempty0 + 8 * b, 2 * EPI_WARPS);
     }
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -361,7 +397,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   pdl_wait();
   pdl_launch_dependents();
 
-  const Work work(MODE, p.T, p.K, p.N, p.pairs, p.partials != nullptr);
+  const Work work(MODE, p.T, p.K, p.N, p.pairs, p.partials != nullptr, p.half);
   const int first = (int)(blockIdx.x >> 1), stride = (int)(gridDim.x >> 1);
 
   if (warp == 0) {
@@ -369,10 +405,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     int stage = 0;
     uint32_t phase = 0, issued = 0, issued_phase = 0;
     bool ok = true;
+    const uint32_t bytes = MODE == FORWARD ? 2 * (OPERAND + p.half * 128) : 2 * STAGE_BYTES;
     for (int i = first; ok && i < work.items; i += stride) {
       const Item item = work_item(work, i);
       const int m0 = item.unit / work.n_tiles * TILE + (int)rank * HALF;
-      const int n0 = item.unit % work.n_tiles * (MODE == FORWARD ? HALF : TILE) +
+      const int n0 = item.unit % work.n_tiles * (MODE == FORWARD ? p.half : TILE) +
                      (MODE == FORWARD ? 0 : (int)rank * HALF);
       for (int kb = item.kb0; kb < item.kb1; ++kb) {
 #ifdef MOE_TEST_WITHHOLD_STAGE
@@ -386,7 +423,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t bar = cluster_address(full0 + 8 * stage, 0);
         const uint32_t s = smem_u32(smem + stage * STAGE_BYTES);
         if (elect_one()) {
-          if (rank == 0) mbar_expect_tx(full0 + 8 * stage, 2 * STAGE_BYTES);
+          if (rank == 0) mbar_expect_tx(full0 + 8 * stage, bytes);
           if (A_MN) {
             tma_load_2d_pair(s, &tmA, m0, kb * 64, bar);
             tma_load_2d_pair(s + MN_BOX, &tmA, m0 + 64, kb * 64, bar);
@@ -415,6 +452,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------- MMA (the first CTA's)
+    const uint32_t idesc = MODE == FORWARD ? IDESC_FULL - ((uint32_t)((HALF - p.half) >> 2) << 17) : IDESC_FULL;
     constexpr uint32_t A_STEP = A_MN ? 128 : 2, B_STEP = B_MN ? 128 : 2;  // 16 of k, in 16 bytes
     int stage = 0, ab = 0;
     uint32_t phase = 0, aphase = 0;
@@ -433,7 +471,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_f16_pair(d, ad + A_STEP * k, bd + B_STEP * k, IDESC, kb > item.kb0 || k > 0);
+            mma_f16_pair(d, ad + A_STEP * k, bd + B_STEP * k, idesc, kb > item.kb0 || k > 0);
           mma_commit_pair(empty0 + 8 * stage);
         }
         __syncwarp();
@@ -446,25 +484,27 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else {
     // -------------------------------------------------------------- epilogue
-    const int row = (int)rank * HALF + (warp & 3) * 32 + lane;  // of the tile
+    const int row0 = (int)rank * HALF + (warp & 3) * 32;  // of the tile, this warp's first
     const int64_t rows = MODE == D_W ? 2 * p.N : p.T;
+    const int part_of = (warp - 2) >> 2;  // which half of the columns
+    T* buf = reinterpret_cast<T*>(smem + STAGES * STAGE_BYTES + 256 + (warp - 2) * STORE_BYTES);
     int ab = 0;
     uint32_t aphase = 0;
     for (int i = first; i < work.items; i += stride) {
       const Item item = work_item(work, i);
-      const int64_t m = (int64_t)(item.unit / work.n_tiles) * TILE + row;
+      const int64_t m = (int64_t)(item.unit / work.n_tiles) * TILE + row0, rows_left = rows - m;
       if (!warp_wait(tfull0 + 8 * ab, aphase, abort_flag, p.status) || *abort_flag != 0) break;
       fence_after();
       const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(ab * TILE);
       if constexpr (MODE == FORWARD) {
-        const int64_t n0 = (int64_t)(item.unit % work.n_tiles) * HALF;
+        const int64_t n0 = (int64_t)(item.unit % work.n_tiles) * p.half;
         T* out = static_cast<T*>(p.out) + m * p.out_stride + n0;
         T* gu = static_cast<T*>(p.gate_up) + m * p.gate_up_stride + n0;
 #pragma unroll 1
-        for (int c = 0; c < HALF; c += 16) {
+        for (int c = part_of * 16; c < p.half; c += EPI_WARPS * 4) {
           uint32_t vg[16], vu[16];
           tmem_ld16(lanes + c, vg);
-          tmem_ld16(lanes + HALF + c, vu);
+          tmem_ld16(lanes + p.half + c, vu);
           tmem_wait16(vg);
           tmem_wait16(vu);
           float o[16], g[16], u[16];
@@ -473,20 +513,20 @@ __global__ void __launch_bounds__(THREADS, 1)
             g[j] = __uint_as_float(vg[j]), u[j] = __uint_as_float(vu[j]);
             o[j] = act_value(p.act, g[j]) * u[j];
           }
-          if (m >= rows) continue;
           const int64_t left = p.N - n0 - c;
-          store16<T>(out + c, o, left, p.out_wide);
+          if (rows_left <= 0 || left <= 0) continue;
+          store16<T>(out + c, p.out_stride, rows_left, o, left, p.out_wide, buf);
           if (p.gate_up != nullptr) {
-            store16<T>(gu + c, g, left, p.gate_up_wide);
-            store16<T>(gu + p.N + c, u, left, p.gate_up_wide);
+            store16<T>(gu + c, p.gate_up_stride, rows_left, g, left, p.gate_up_wide, buf);
+            store16<T>(gu + p.N + c, p.gate_up_stride, rows_left, u, left, p.gate_up_wide, buf);
           }
         }
       } else {
         const int64_t n0 = (int64_t)(item.unit % work.n_tiles) * TILE;
         T* out = static_cast<T*>(p.out) + m * p.out_stride + n0;
-        float* part = p.partials + item.piece * PIECE + row * TILE;
+        float* part = p.partials + item.piece * PIECE + (row0 + lane) * TILE;
 #pragma unroll 1
-        for (int c = 0; c < TILE; c += 16) {
+        for (int c = part_of * 16; c < TILE; c += EPI_WARPS * 4) {
           uint32_t v[16];
           tmem_ld16(lanes + c, v);
           tmem_wait16(v);
@@ -499,7 +539,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           float f[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]);
-          if (m < rows) store16<T>(out + c, f, p.K - n0 - c, p.out_wide);
+          const int64_t left = p.K - n0 - c;
+          if (rows_left > 0 && left > 0)
+            store16<T>(out + c, p.out_stride, rows_left, f, left, p.out_wide, buf);
         }
       }
       fence_before();
@@ -519,6 +561,177 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
+// One tile of the forward for a cluster of `splits` pairs, each with a share of the K slabs:
+// where there are fewer tiles than pairs.  A CTA's sums go to its own shared memory, the
+// ring's, and each of the CTAs that have the same rows finishes a share of the outputs from
+// all of theirs in the order of the pairs.
+constexpr int SUM_PITCH = TILE + 4;  // floats: lanes' rows lie in different banks
+static_assert(HALF * SUM_PITCH * 4 <= STAGES * STAGE_BYTES, "the sums fit the ring");
+
+template <typename T, int SPLITS>
+__global__ void __launch_bounds__(THREADS, 1)
+    gated_cluster_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tmX,
+                         const __grid_constant__ CUtensorMap tmG,
+                         const __grid_constant__ CUtensorMap tmU) {
+  constexpr uint32_t IDESC = f16_idesc(std::is_same<T, __nv_bfloat16>::value, TILE, TILE);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES);
+  // full[STAGES], empty[STAGES], done
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 1);
+  int* s_abort = reinterpret_cast<int*>(tmem_holder + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort_flag = s_abort;
+  const uint32_t cta = cluster_rank(), rank = cta & 1, leader = cta & ~1u;
+  const int share = (int)(cta >> 1);
+  const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + STAGES);
+  const uint32_t done_bar = smem_u32(bars + 2 * STAGES);
+  if (tid == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    mbar_init(done_bar, 1);
+    *s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_async_smem();
+    prefetch_map(&tmX);
+    prefetch_map(&tmG);
+    prefetch_map(&tmU);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_holder)),
+                 "r"(TILE)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  cluster_sync();  // the pair's barriers are set up
+  fence_after();
+  const uint32_t tmem = *tmem_holder;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  const int n_tiles = (int)((p.N + HALF - 1) / HALF), unit = (int)blockIdx.x / (2 * SPLITS);
+  const int m0 = unit / n_tiles * TILE + (int)rank * HALF, n0 = unit % n_tiles * HALF;
+  const int slabs = (int)((p.K + 63) / 64), per = (slabs + SPLITS - 1) / SPLITS;
+  const int kb0 = share * per, kb1 = min(slabs, kb0 + per);  // every share has slabs
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA
+    int stage = 0;
+    uint32_t phase = 0, issued = 0, issued_phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+#ifdef MOE_TEST_WITHHOLD_STAGE
+      if (blockIdx.x < 2 && kb > kb0) break;  // as above: the first pair stops here
+#endif
+      if (!warp_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag, p.status)) break;
+      const uint32_t bar = cluster_address(full0 + 8 * stage, leader);
+      const uint32_t s = smem_u32(smem + stage * STAGE_BYTES);
+      if (elect_one()) {
+        if (rank == 0) mbar_expect_tx(full0 + 8 * stage, 2 * STAGE_BYTES);
+        tma_load_2d_pair(s, &tmX, kb * 64, m0, bar);
+        tma_load_2d_pair(s + OPERAND, rank == 0 ? &tmG : &tmU, kb * 64, n0, bar);
+      }
+      __syncwarp();
+      issued |= 1u << stage;
+      issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+      if (++stage == STAGES) stage = 0, phase ^= 1u;
+    }
+    if (rank == 0)  // both CTAs' copies have landed before either goes on
+      for (int s = 0; s < STAGES; ++s)
+        if (issued & (1u << s)) {
+          volatile int never = 0;
+          mbar_wait(full0 + 8 * s, (issued_phase >> s) & 1u, &never, p.status);
+        }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------- MMA (the pair's first CTA's)
+    int stage = 0;
+    uint32_t phase = 0, accumulate = 0;
+    for (int kb = kb0; kb < kb1 && rank == 0; ++kb) {
+      if (!warp_wait(full0 + 8 * stage, phase, abort_flag, p.status)) break;
+      fence_after();
+      const uint32_t s = smem_u32(smem + stage * STAGE_BYTES);
+      const uint64_t ad = sw128_desc(s), bd = sw128_desc(s + OPERAND);
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_f16_pair(tmem, ad + 2 * k, bd + 2 * k, IDESC, accumulate | (k > 0));
+        mma_commit_pair(empty0 + 8 * stage, leader);
+      }
+      __syncwarp();
+      accumulate = 1;
+      if (++stage == STAGES) stage = 0, phase ^= 1u;
+    }
+    if (rank == 0) {  // done also when a wait ran out; the sums are then not whole
+      if (elect_one()) mma_commit_pair(done_bar, leader);
+      __syncwarp();
+    }
+    volatile int never = 0;
+    mbar_wait(done_bar, 0, &never, p.status);  // no MMA is left that reads or writes
+    __syncwarp();
+  } else if (warp_wait(done_bar, 0, abort_flag, p.status)) {
+    // ------------------------------------------------------------------ sums
+    fence_after();
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    float* red = reinterpret_cast<float*>(smem) + row * SUM_PITCH;  // the ring is no longer in use
+#pragma unroll 1
+    for (int c = ((warp - 2) >> 2) * 16; c < TILE; c += EPI_WARPS * 4) {
+      uint32_t v[16];
+      tmem_ld16(lanes + c, v);
+      tmem_wait16(v);
+#pragma unroll
+      for (int j = 0; j < 16; j += 4)
+        *reinterpret_cast<uint4*>(red + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+    }
+    fence_before();
+  }
+  __syncwarp();
+  cluster_sync();
+  bool whole = true;  // no CTA of the cluster gave up
+  for (int r = 0; r < 2 * SPLITS; ++r) {
+    int gave_up;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                 : "=r"(gave_up)
+                 : "r"(cluster_address(smem_u32(s_abort), r))
+                 : "memory");
+    whole = whole && gave_up == 0;
+  }
+  constexpr int LANES = HALF / SPLITS / 4;  // of a row's share of outputs, four a lane
+  const uint32_t sums = smem_u32(smem);
+  for (int i = tid; whole && i < HALF * LANES; i += THREADS) {
+    const int row = i / LANES, c = share * (HALF / SPLITS) + i % LANES * 4;
+    const int64_t t = m0 + row, n = n0 + c;
+    if (t >= p.T || n >= p.N) continue;
+    float4 g[SPLITS], u[SPLITS];
+    const uint32_t at = sums + (uint32_t)(row * SUM_PITCH + c) * 4;
+#pragma unroll
+    for (int r = 0; r < SPLITS; ++r) {
+      g[r] = ld_cluster4(at, 2 * r + rank);
+      u[r] = ld_cluster4(at + HALF * 4, 2 * r + rank);
+    }
+#pragma unroll
+    for (int r = 1; r < SPLITS; ++r) {
+      g[0].x += g[r].x, g[0].y += g[r].y, g[0].z += g[r].z, g[0].w += g[r].w;
+      u[0].x += u[r].x, u[0].y += u[r].y, u[0].z += u[r].z, u[0].w += u[r].w;
+    }
+    store4<T>(p, t, n, g[0], u[0]);
+  }
+  __syncwarp();
+  fence_before();
+  cluster_sync();  // no CTA leaves while its sums are read
+  if (warp == 1) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TILE)
+                 : "memory");
+  }
+}
+
 // Sums the pieces of the tiles that were cut, in their order, and stores them: a block
 // JOIN_ROWS rows of a tile, a thread four columns of two of them.
 constexpr int JOIN_ROWS = 8;
@@ -527,7 +740,7 @@ template <typename T, Mode MODE>
 __global__ void __launch_bounds__(256) gated_join_kernel(Params p) {
   pdl_wait();
   pdl_launch_dependents();
-  const Work work(MODE, p.T, p.K, p.N, p.pairs, true);
+  const Work work(MODE, p.T, p.K, p.N, p.pairs, true, HALF);
   const int u = work.full + blockIdx.y;
   const int64_t rows = MODE == D_W ? 2 * p.N : p.T;
   const int f = (threadIdx.x & 63) * 4;
@@ -569,28 +782,42 @@ struct SlopeParams {
 
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) gated_slope_kernel(SlopeParams p) {
+  constexpr int U = VEC == 1 ? 4 : 1;  // packs in flight
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t packs = (p.N + VEC - 1) / VEC, total = packs * p.T;
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    const int64_t t = i / packs, n = (i - t * packs) * VEC;
-    const T* gu = static_cast<const T*>(p.gate_up) + t * p.gate_up_stride + n;
-    float g[VEC], u[VEC], d[VEC];
-    load_pack<T, VEC>(gu).get(g);
-    load_pack<T, VEC>(gu + p.N).get(u);
-    load_pack<T, VEC>(static_cast<const T*>(p.d_out) + t * p.d_out_stride + n).get(d);
+  const int N = (int)p.N;
+  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+    const T* gu = static_cast<const T*>(p.gate_up) + t * p.gate_up_stride;
+    const T* d_out = static_cast<const T*>(p.d_out) + t * p.d_out_stride;
+    T* dst = static_cast<T*>(p.d_gate_up) + t * p.d_stride;
+    for (int n0 = threadIdx.x * VEC; n0 < N; n0 += U * 256 * VEC) {
+      Pack<T, VEC> pg[U], pu[U], pd[U];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const float2 a = act_slope(p.act, g[e]);
-      g[e] = d[e] * u[e] * a.y;
-      u[e] = d[e] * a.x;
+      for (int k = 0; k < U; ++k) {
+        const int n = min(n0 + k * 256 * VEC, N - VEC);
+        pg[k] = load_pack<T, VEC>(gu + n);
+        pu[k] = load_pack<T, VEC>(gu + N + n);
+        pd[k] = load_pack<T, VEC>(d_out + n);
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int n = n0 + k * 256 * VEC;
+        if (n >= N) break;
+        float g[VEC], u[VEC], d[VEC];
+        pg[k].get(g), pu[k].get(u), pd[k].get(d);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float2 a = act_slope(p.act, g[e]);
+          g[e] = d[e] * u[e] * a.y;
+          u[e] = d[e] * a.x;
+        }
+        Pack<T, VEC> o;
+        o.set(g);
+        store_pack<T, VEC>(dst + n, o);
+        o.set(u);
+        store_pack<T, VEC>(dst + N + n, o);
+      }
     }
-    T* dst = static_cast<T*>(p.d_gate_up) + t * p.d_stride + n;
-    Pack<T, VEC> o;
-    o.set(g);
-    store_pack<T, VEC>(dst, o);
-    o.set(u);
-    store_pack<T, VEC>(dst + p.N, o);
   }
 }
 
@@ -644,7 +871,7 @@ static moe_status_t launch_gated_pair(const gated::Params& p, const CUtensorMap&
   static_assert(gated::SMEM <= kMaxSmem, "shared memory of one CTA");
   moe_status_t st = allow_smem<kernel>(gated::SMEM);
   if (st != MOE_OK) return st;
-  const gated::Work work(MODE, p.T, p.K, p.N, p.pairs, p.partials != nullptr);
+  const gated::Work work(MODE, p.T, p.K, p.N, p.pairs, p.partials != nullptr, p.half);
   const int pairs = work.items < p.pairs ? work.items : p.pairs;
   st = launched(launch_cluster(kernel, dim3((unsigned)(2 * pairs)), gated::THREADS, 2,
                                (size_t)gated::SMEM, s, p, a, b, b2),
@@ -658,6 +885,31 @@ static moe_status_t launch_gated_pair(const gated::Params& p, const CUtensorMap&
   return st;
 }
 
+template <typename T, int SPLITS>
+static moe_status_t launch_gated_cluster(const gated::Params& p, int units, const CUtensorMap& x,
+                                         const CUtensorMap& g, const CUtensorMap& u, cudaStream_t s) {
+  constexpr auto kernel = gated::gated_cluster_kernel<T, SPLITS>;
+  moe_status_t st = allow_smem<kernel>(gated::SMEM);
+  if (st != MOE_OK) return st;
+  return launched(launch_cluster(kernel, dim3((unsigned)(units * 2 * SPLITS)), gated::THREADS,
+                                 2 * SPLITS, (size_t)gated::SMEM, s, p, x, g, u),
+                  "gated projection");
+}
+
+// Outputs of a forward tile: narrower ones where they leave fewer pairs idle in the last
+// round (4096 tokens, 7168 -> 2048: 3.4 rounds of 128, exactly 4 of 112).  A tile costs its
+// columns and, as x is read for fewer of them, some more.
+static int best_half(const gated::Params& p) {
+  int best = gated::HALF;
+  int64_t least = INT64_MAX;
+  for (int half = gated::HALF; half >= 64; half -= 16) {
+    const gated::Work w(gated::FORWARD, p.T, p.K, p.N, p.pairs, false, half);
+    const int64_t cost = (int64_t)((w.units + p.pairs - 1) / p.pairs) * (half + 24);
+    if (cost < least) best = half, least = cost;
+  }
+  return best;
+}
+
 template <typename T>
 static moe_status_t launch_gated(const moe_gated_linear_args_t* a, gated::Params p, cudaStream_t s) {
   const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -665,12 +917,19 @@ static moe_status_t launch_gated(const moe_gated_linear_args_t* a, gated::Params
   const T* up = static_cast<const T*>(a->weight) + p.N * p.K;
   const bool split = p.T <= gated::SPLIT_TOKENS;
   const SplitPlan q = split_plan(p.T, p.K, p.N);
-  const int rows = split ? gated::SM_FEATURES : gated::HALF;
+  // Two pairs a tile where there are few.
+  const gated::Work whole(gated::FORWARD, p.T, p.K, p.N, p.pairs, false, gated::HALF);
+  const bool shared = !split && whole.units * 2 <= p.pairs && whole.slabs >= 8;
+  if (!split && !shared) p.half = best_half(p);
+  const int rows = split ? gated::SM_FEATURES : p.half;
   CUtensorMap g, u, x;
   if (!make_map16(&g, bf16, a->weight, p.N, p.K, p.K, rows) ||
       !make_map16(&u, bf16, up, p.N, p.K, p.K, rows) ||
       !make_map16(&x, bf16, a->x, p.T, p.K, x_stride, split ? q.nt : gated::HALF))
     return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the gated projection");
+  // (Four, in clusters of eight CTAs, of which not sixteen fit the GPU at once: 256 tokens of
+  // 7168 -> 2048 34 us, two 23.)
+  if (shared) return launch_gated_cluster<T, 2>(p, whole.units, x, g, u, s);
   if (!split) return launch_gated_pair<T, gated::FORWARD>(p, x, g, u, s);
   p.splits = q.splits;
   switch (q.nt) {
@@ -704,9 +963,8 @@ static moe_status_t launch_gated_backward(const moe_gated_linear_backward_args_t
   sp.d_stride = ds;
   const bool wide = p.N % 8 == 0 && rows_aligned16(a->d_out, a->d_out_stride0, 2, p.T) &&
                     rows_aligned16(a->gate_up, a->gate_up_stride0, 2, p.T);
-  const int64_t blocks = (p.T * ((p.N + (wide ? 7 : 0)) / (wide ? 8 : 1)) + 255) / 256;
   const int64_t cap = 8 * (int64_t)num_sms();
-  const dim3 grid((unsigned)(blocks < cap ? blocks : cap));
+  const dim3 grid((unsigned)(p.T < cap ? p.T : cap));
   moe_status_t st = launched(wide ? launch_pdl(gated::gated_slope_kernel<T, 8>, grid, dim3(256), 0, s, sp)
                                   : launch_pdl(gated::gated_slope_kernel<T, 1>, grid, dim3(256), 0, s, sp),
                              "gated slope");
@@ -791,6 +1049,7 @@ moe_status_t moe_gated_linear(const moe_gated_linear_args_t* a, void* stream) {
   p.gate_up_stride = a->gate_up_stride0;
   p.gate_up_wide = N % 8 == 0 && rows_aligned16(a->gate_up, a->gate_up_stride0, 2, T);
   p.pairs = num_sms() / 2;
+  p.half = gated::HALF;
   p.splits = 1;
   p.status = a->device_status;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -846,6 +1105,7 @@ moe_status_t moe_gated_linear_backward(const moe_gated_linear_backward_args_t* a
   p.N = N;
   p.act = a->activation;
   p.pairs = num_sms() / 2;
+  p.half = gated::HALF;
   p.splits = 1;
   p.status = a->device_status;
   return a->dtype == MOE_DTYPE_BF16 ? launch_gated_backward<__nv_bfloat16>(a, p, s)

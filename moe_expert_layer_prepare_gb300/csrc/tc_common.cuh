@@ -165,12 +165,13 @@ __device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t adesc, ui
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Arrives on the barrier at this address in both CTAs when the MMAs are done.
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+// Arrives on the barrier at this address in both CTAs of the pair whose first has rank
+// `leader` in the cluster when the MMAs are done.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint32_t leader = 0) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
       " [%0], %1;" ::"r"(bar),
-      "h"((uint16_t)3)
+      "h"((uint16_t)(3u << leader))
       : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {

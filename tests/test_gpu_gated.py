@@ -305,3 +305,13 @@ def test_wait_timeout_sets_status_and_context_survives(T):
     again, gu = check_forward(x, w, "silu")
     assert torch.equal(again, out)
     check_backward(d, x, w, gu, "silu")
+
+
+@pytest.mark.parametrize("T,N", [(1024, 2048), (700, 3000), (1300, 2100), (600, 2600), (2000, 1100), (513, 4000),
+                                 (1500, 1700), (600, 3700), (513, 3300), (129, 70), (256, 2048), (512, 1990)])
+def test_tiles_of_every_width(T, N):
+    """Batches for which the forward's tiles are 64 to 128 outputs wide, whole or shared by two pairs
+    of CTAs, with a last tile that is not full."""
+    x, w, _ = problem(T, 520, N, "bf16")
+    check_forward(x, w, "silu")
+    check_forward(x, w, "gelu_tanh", layout="strided")
