@@ -31,13 +31,17 @@
 namespace moe {
 namespace w4 {
 
-constexpr int ROWS = 16;           // of a unit
-constexpr int BLOCK_K = 512;       // codes of a row in a stage: 256 bytes, as two of 128
-// Bytes of a stage: the rows' codes, 32 bytes of scales and 16 zero points a row.
-constexpr int HALF_STAGE = ROWS * 128;
-constexpr int STAGE_SCALES = 2 * HALF_STAGE, STAGE_ZEROS = STAGE_SCALES + ROWS * 32;
-constexpr int STAGE = STAGE_ZEROS + ROWS * 16;
-constexpr int STAGES = 2;  // of a warp's ring: 64 KB are on their way to an SM
+constexpr int ROWS = 16;   // of a unit, an MMA tile
+constexpr int WARPS = 16;  // they fill the register file
+// A warp's block: 512 codes of the 16 rows, in a stage two parts of 16 rows by 128 bytes; or
+// 256, one part, where the rows of x take the room.  A part's scales and zero points (16 and
+// 8 bytes a row) stand behind the codes.  64 or 32 KB are on their way to an SM.
+constexpr int PART = ROWS * 128;
+constexpr int STAGES = 2;
+constexpr int block_k(int parts) { return 256 * parts; }
+constexpr int scales_at(int parts) { return parts * PART; }
+constexpr int zeros_at(int parts) { return scales_at(parts) + parts * ROWS * 16; }
+constexpr int stage_bytes(int parts) { return zeros_at(parts) + parts * ROWS * 8; }
 constexpr int MAX_ROUTES = 1024, MAX_EXPERTS = 1024;
 
 struct Params {
@@ -71,11 +75,6 @@ enum Format { INT4 = 0, INT4_ZEROS = 1, E2M1 = 2 };
 // The eight codes of a word as fp16 numbers in pairs.
 template <Format F>
 struct Codes {
-  // What a pair has too much, of codes at bits 0 and 16, and of those at 4 and 20: the zero
-  // point, a subnormal number too.
-  static __device__ __forceinline__ uint2 offset(uint32_t zero) {
-    return make_uint2(zero * 0x00010001u, zero * 0x00100010u);
-  }
   // pair i: codes i and i + 4, times 2^-24 (i even) or 2^-20
   static __device__ __forceinline__ void pairs(uint32_t w, uint2 off, uint32_t (&d)[4]) {
     const uint32_t v[4] = {w & 0x000F000Fu, w & 0x00F000F0u, (w >> 8) & 0x000F000Fu,
@@ -92,17 +91,15 @@ struct Codes {
   // half at the end
   static constexpr float UNIT = 0x1p12f;
   // x's eight values in the same order; those that meet codes times 2^-20 are 2^-4 as large
-  static __device__ __forceinline__ uint4 order(const float (&f)[8]) {
-    return make_uint4(pack2<__half>(make_float2(f[0], f[4])),
-                      pack2<__half>(make_float2(f[1] * 0.0625f, f[5] * 0.0625f)),
-                      pack2<__half>(make_float2(f[2], f[6])),
-                      pack2<__half>(make_float2(f[3] * 0.0625f, f[7] * 0.0625f)));
+  static __device__ __forceinline__ uint4 order(float2 a, float2 b, float2 c, float2 d, float up) {
+    const float odd = up * 0.0625f;
+    return make_uint4(pack2<__half>(make_float2(a.x * up, c.x * up)), pack2<__half>(make_float2(a.y * odd, c.y * odd)),
+                      pack2<__half>(make_float2(b.x * up, d.x * up)), pack2<__half>(make_float2(b.y * odd, d.y * odd)));
   }
 };
 // e2m1: neighbouring codes a pair.
 template <>
 struct Codes<E2M1> {
-  static __device__ __forceinline__ uint2 offset(uint32_t) { return make_uint2(0, 0); }
   static __device__ __forceinline__ void pairs(uint32_t w, uint2, uint32_t (&d)[4]) {
     asm("{ .reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %4;"
         " cvt.rn.f16x2.e2m1x2 %0, a; cvt.rn.f16x2.e2m1x2 %1, b;"
@@ -111,9 +108,9 @@ struct Codes<E2M1> {
         : "r"(w));
   }
   static constexpr float UNIT = 1.0f;
-  static __device__ __forceinline__ uint4 order(const float (&f)[8]) {
-    return make_uint4(pack2<__half>(make_float2(f[0], f[1])), pack2<__half>(make_float2(f[2], f[3])),
-                      pack2<__half>(make_float2(f[4], f[5])), pack2<__half>(make_float2(f[6], f[7])));
+  static __device__ __forceinline__ uint4 order(float2 a, float2 b, float2 c, float2 d, float up) {
+    return make_uint4(pack2<__half>(make_float2(a.x * up, a.y * up)), pack2<__half>(make_float2(b.x * up, b.y * up)),
+                      pack2<__half>(make_float2(c.x * up, c.y * up)), pack2<__half>(make_float2(d.x * up, d.y * up)));
   }
 };
 
@@ -132,7 +129,7 @@ __device__ __forceinline__ void mma_tile(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The scales of half a K block of a row, 8 / SPG of T or exponents, and its zero points.
+// The scales of 256 codes of a row, 8 / SPG of T or exponents, and its zero points.
 template <typename T, Format F, int SPG>
 struct Scales {
   static constexpr int COUNT = 8 / SPG;
@@ -140,9 +137,8 @@ struct Scales {
   static constexpr int BYTES = COUNT * ITEM;
   uint32_t s[BYTES / 4], z[2];
 
-  // of the half `h` of a row in a stage
-  __device__ __forceinline__ void read(const uint8_t* stage, int row, int h) {
-    const uint8_t* at = stage + STAGE_SCALES + row * 32 + h * BYTES;
+  // from where a row's stand in a stage
+  __device__ __forceinline__ void read(const uint8_t* at, const uint8_t* zat) {
     if constexpr (BYTES == 16) {
       const uint4 v = *reinterpret_cast<const uint4*>(at);
       s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
@@ -153,14 +149,13 @@ struct Scales {
       s[0] = *reinterpret_cast<const uint32_t*>(at);
     }
     if constexpr (F == INT4_ZEROS) {
-      const uint8_t* zat = stage + STAGE_ZEROS + row * 16 + h * COUNT;
       if constexpr (COUNT == 8) {
         const uint2 v = *reinterpret_cast<const uint2*>(zat);
-        z[0] = v.x, z[1] = v.y;
+        z[0] = v.x & 0x0F0F0F0Fu, z[1] = v.y & 0x0F0F0F0Fu;
       } else if constexpr (COUNT == 4) {
-        z[0] = *reinterpret_cast<const uint32_t*>(zat);
+        z[0] = *reinterpret_cast<const uint32_t*>(zat) & 0x0F0F0F0Fu;
       } else {
-        z[0] = *reinterpret_cast<const uint16_t*>(zat);
+        z[0] = *reinterpret_cast<const uint16_t*>(zat) & 0x0F0Fu;
       }
     }
   }
@@ -176,8 +171,12 @@ struct Scales {
     }
     return unpack2<T>(s[i]);
   }
-  __device__ __forceinline__ uint32_t zero(int j) const {
-    return F == INT4_ZEROS ? (z[j / 4] >> (8 * (j % 4))) & 15u : 8u;
+  // What a pair of codes of group j has too much, at bits 0 and 16 and at bits 4 and 20: the
+  // zero point, a subnormal number like the codes.
+  __device__ __forceinline__ uint2 offset(int j) const {
+    if constexpr (F != INT4_ZEROS) return make_uint2(0x00080008u, 0x00800080u);
+    const uint32_t o = __byte_perm(z[j / 4], 0, (j % 4) * 0x0101 + 0x4040);
+    return make_uint2(o, o << 4);
   }
 };
 
@@ -222,7 +221,7 @@ __device__ __forceinline__ void copy_groups(uint8_t* dst, const uint8_t* src, in
 
 // Routes by expert: s_route in the order of the experts, chunks of at most `most`.  Routes
 // without an expert get zeros in out.  All threads of the block call it.
-template <typename T, int WARPS>
+template <typename T>
 __device__ __forceinline__ int sort_routes(const Params& p, int most, int* s_count, int* s_first,
                                            uint16_t* s_route, Chunk* s_chunk, int* s_part) {
   constexpr int THREADS = WARPS * 32;
@@ -305,7 +304,7 @@ __device__ __forceinline__ int sort_routes(const Params& p, int most, int* s_cou
 
 // The same for at most 32 routes, a lane each of one warp; chunks in the order of their
 // first routes.
-template <typename T, int WARPS>
+template <typename T>
 __device__ __forceinline__ int sort_few_routes(const Params& p, int most, uint16_t* s_route,
                                                Chunk* s_chunk, int* s_part) {
   const int tid = threadIdx.x, lane = tid & 31;
@@ -343,30 +342,31 @@ __device__ __forceinline__ int sort_few_routes(const Params& p, int most, uint16
 // Bytes of a row of x in shared memory: zeros up to a whole block, and 64 bytes so that two
 // rows' neighbouring 64 bytes lie in different banks.
 __host__ __device__ constexpr int64_t x_pitch(int64_t K) {
-  return (K + BLOCK_K - 1) / BLOCK_K * (BLOCK_K * 2) + 64;
+  return (K + 511) / 512 * 1024 + 64;
 }
 
-constexpr int ring_bytes(int warps) { return warps * STAGES * STAGE; }
-constexpr int red_bytes(int nt, int warps) { return 2 * warps * 32 * 16 * nt; }
+constexpr int ring_bytes(int parts) { return WARPS * STAGES * stage_bytes(parts); }
+constexpr int red_bytes(int nt) { return WARPS * 32 * 16 * nt; }
 // s_part, then of each route its place and perhaps a chunk, then two words an expert
 __host__ __device__ constexpr int route_bytes(int routes) {
   return routes == 0 ? 0 : 64 + (routes + 1) / 2 * 16 + (routes <= 32 ? 0 : 2 * MAX_EXPERTS * 4);
 }
 constexpr int MAX_ROOM = 16;  // rows of x in shared memory
-constexpr int fixed_bytes(int nt, int warps, int routes) {  // beside x
-  return ring_bytes(warps) + red_bytes(nt, warps) + route_bytes(routes) + MAX_ROOM * 4 + warps * 4;
+constexpr int fixed_bytes(int nt, int parts, int routes) {  // beside x
+  return ring_bytes(parts) + red_bytes(nt) + route_bytes(routes) + MAX_ROOM * 4 + WARPS * 4;
 }
 
-template <typename T, Format F, int SPG, int NT, int WARPS, bool EXPERTS>
+template <typename T, Format F, int SPG, int NT, int PARTS, bool EXPERTS>
 __global__ void __launch_bounds__(WARPS * 32, 1) w4_kernel(Params p) {
   using C = Codes<F>;
   using S = Scales<T, F, SPG>;
+  constexpr int BLOCK_K = block_k(PARTS), STAGE = stage_bytes(PARTS);
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
   const int routes = EXPERTS ? p.routes : 0;
-  float4* red = reinterpret_cast<float4*>(smem + ring_bytes(WARPS));
-  uint8_t* routing = reinterpret_cast<uint8_t*>(red) + red_bytes(NT, WARPS);
+  float4* red = reinterpret_cast<float4*>(smem + ring_bytes(PARTS));
+  uint8_t* routing = reinterpret_cast<uint8_t*>(red) + red_bytes(NT);
   float* s_power = reinterpret_cast<float*>(routing + route_bytes(routes));  // [MAX_ROOM]
   uint32_t* s_amax = reinterpret_cast<uint32_t*>(s_power + MAX_ROOM);       // [WARPS]
   uint8_t* s_x = reinterpret_cast<uint8_t*>(s_amax + WARPS);
@@ -381,14 +381,14 @@ __global__ void __launch_bounds__(WARPS * 32, 1) w4_kernel(Params p) {
     s_route = reinterpret_cast<uint16_t*>(s_part + 16);
     s_chunk = reinterpret_cast<Chunk*>(s_route + (routes + 1) / 2 * 2);
     if (routes <= 32) {
-      chunks = sort_few_routes<T, WARPS>(p, p.most, s_route, s_chunk, s_part);
+      chunks = sort_few_routes<T>(p, p.most, s_route, s_chunk, s_part);
     } else {
       int* s_count = reinterpret_cast<int*>(routing + route_bytes(routes)) - 2 * MAX_EXPERTS;
-      chunks = sort_routes<T, WARPS>(p, p.most, s_count, s_count + MAX_EXPERTS, s_route, s_chunk, s_part);
+      chunks = sort_routes<T>(p, p.most, s_count, s_count + MAX_EXPERTS, s_route, s_chunk, s_part);
     }
   }
   const bool gated = p.act != MOE_ACT_NONE;
-  const int tile_out = gated ? ROWS / 2 : ROWS;
+  const int tile_out = gated ? ROWS / 2 : ROWS;  // outputs of a unit
   const int tiles = p.tiles, units = chunks * tiles, blocks = p.blocks;
   const int pitch = (int)(p.K / 2);  // bytes of a row
   const int xp = (int)x_pitch(p.K);
@@ -499,35 +499,39 @@ __global__ void __launch_bounds__(WARPS * 32, 1) w4_kernel(Params p) {
   Run ahead = run_of(batch);
   settle(ahead);
   const uint8_t* from[4];  // this lane's 16 bytes of four rows
-  int64_t scales_at = 0;   // this lane's row of scales (lanes 0 to 15) or zero points, in groups
+  int64_t groups_at = 0;   // this lane's row of scales (lanes 0 to 15) or zero points, in groups
   auto aim = [&] {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       from[i] = p.w + row_of(ahead, i * 4 + (lane >> 3)) * pitch + (lane & 7) * 16;
-    scales_at = row_of(ahead, lane & 15) * groups;
+    groups_at = row_of(ahead, lane & 15) * groups;
   };
   const uint32_t to = ring + (lane >> 3) * 128;
   uint32_t at_piece[2];  // rows r and r + 4 differ in the permutation
 #pragma unroll
   for (int i = 0; i < 2; ++i) at_piece[i] = to + (((lane & 7) ^ (((lane >> 3) + 4 * i) & 7)) << 4);
+  // Of two zero points a block a word is copied, of a pair of blocks.
+  constexpr bool ZERO_PAIRS = PARTS == 1 && S::COUNT == 2;
   auto fetch = [&](int stage) {
     if (ahead.left > 0) {
-      const int byte = ahead.kb * (BLOCK_K / 2), group = ahead.kb * (2 * S::COUNT);
+      const int byte = ahead.kb * (BLOCK_K / 2), group = ahead.kb * (PARTS * S::COUNT);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < PARTS; ++h)
         if (byte + h * 128 + (lane & 7) * 16 < pitch) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            copy_async<16>(at_piece[i & 1] + stage * STAGE + h * HALF_STAGE + i * 512, from[i] + byte + h * 128);
+            copy_async<16>(at_piece[i & 1] + stage * STAGE + h * PART + i * 512, from[i] + byte + h * 128);
         }
       uint8_t* to_groups = ring_at + stage * STAGE;
-      if (lane < 16)
-        copy_groups<2 * S::BYTES, S::ITEM>(to_groups + STAGE_SCALES + lane * 32,
-                                           static_cast<const uint8_t*>(p.scales) + (scales_at + group) * S::ITEM,
-                                           (groups - group) * S::ITEM, p.scale_unit);
-      else if constexpr (F == INT4_ZEROS)
-        copy_groups<2 * S::COUNT, 1>(to_groups + STAGE_ZEROS + (lane - 16) * 16,
-                                     p.zeros + (scales_at + group), groups - group, p.zero_unit);
+      if (lane < 16) {
+        copy_groups<PARTS * S::BYTES, S::ITEM>(to_groups + scales_at(PARTS) + lane * (PARTS * 16),
+                                               static_cast<const uint8_t*>(p.scales) + (groups_at + group) * S::ITEM,
+                                               (groups - group) * S::ITEM, p.scale_unit);
+      } else if constexpr (F == INT4_ZEROS) {
+        const int first = ZERO_PAIRS ? group & ~3 : group;
+        copy_groups<ZERO_PAIRS ? 4 : PARTS * S::COUNT, 1>(to_groups + zeros_at(PARTS) + (lane - 16) * (PARTS * 8),
+                                                          p.zeros + (groups_at + first), groups - first, p.zero_unit);
+      }
       if (step(ahead) && ahead.left > 0) aim();
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -556,19 +560,30 @@ __global__ void __launch_bounds__(WARPS * 32, 1) w4_kernel(Params p) {
     for (int col0 = 0; col0 < rows; col0 += WARPS / per) {
       const int col = col0 + warp / per;
       uint4* row = reinterpret_cast<uint4*>(s_x + col * xp);
-      uint32_t most = 0;
-      if (col < rows)
+      // the row's largest value, by its bits; where it is not a finite one, the largest that is
+      constexpr uint32_t INF = std::is_same<T, __nv_bfloat16>::value ? 0x7F80u : 0x7C00u;
+      uint32_t two = 0;
+      if (col < rows) {
+#pragma unroll 4
+        for (int i = lane0; i < pieces; i += per * 32) {
+          const uint4 v = row[i];
+          two = __vmaxu2(__vmaxu2(two, __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu)),
+                         __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+        }
+      }
+      uint32_t most = __reduce_max_sync(0xFFFFFFFFu, max(two & 0xFFFFu, two >> 16));
+      if (most >= INF) {
+        most = 0;
         for (int i = lane0; i < pieces; i += per * 32) {
           const uint4 v = row[i];
           const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {  // the largest finite value, by its bits
+          for (int e = 0; e < 8; ++e) {
             const uint32_t m = (u[e / 2] >> (16 * (e & 1))) & 0x7FFFu;
-            constexpr uint32_t INF = std::is_same<T, __nv_bfloat16>::value ? 0x7F80u : 0x7C00u;
             most = max(most, m < INF ? m : 0u);
           }
         }
-      most = __reduce_max_sync(0xFFFFFFFFu, most);
+        most = __reduce_max_sync(0xFFFFFFFFu, most);
+      }
       if (per > 1) {
         if (lane == 0) s_amax[warp] = most;
         __syncthreads();
@@ -580,13 +595,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1) w4_kernel(Params p) {
         // 2^(14 - e) of a largest value in [2^e, 2^(e + 1)); of the smallest ones 2^100
         const int e = max((int)(__float_as_uint(to_f32(big)) >> 23) - 127, -86);
         const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+#pragma unroll 4
         for (int i = lane0; i < pieces; i += per * 32) {
           const uint4 v = row[i];
-          const float2 f0 = unpack2<T>(v.x), f1 = unpack2<T>(v.y), f2 = unpack2<T>(v.z),
-                       f3 = unpack2<T>(v.w);
-          const float f[8] = {f0.x * up, f0.y * up, f1.x * up, f1.y * up,
-                              f2.x * up, f2.y * up, f3.x * up, f3.y * up};
-          row[i] = C::order(f);
+          row[i] = C::order(unpack2<T>(v.x), unpack2<T>(v.y), unpack2<T>(v.z), unpack2<T>(v.w), up);
         }
         if (lane0 == 0) s_power[col] = __uint_as_float((uint32_t)(127 - 14 + e) << 23) * C::UNIT;
       }
@@ -635,11 +647,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1) w4_kernel(Params p) {
       }
     };
 
-    // The sums of a unit that other warps have blocks of: where this warp has its first
-    // block in place 1, else in place 0, [warp][place][NT][lane].
-    auto place = [&](int w, int which) { return red + (w * 2 + which) * (32 * NT) + lane; };
+    // The sums of a unit that another warp began, [warp][NT][lane]; the one that began it
+    // keeps its own and adds them.
+    auto place = [&](int w) { return red + w * (32 * NT) + lane; };
+    float4 tail[NT];
     Run run = run_of(batch);
-    bool begun = false;  // whether this warp has a unit in place 1
+    bool begun = false;  // whether this warp has begun a unit that others go on with
     while (run.left > 0) {
       take_chunk(run.chunk);
       const int kb0 = run.kb, kb1 = min(blocks, run.kb + run.left);
@@ -651,12 +664,17 @@ __global__ void __launch_bounds__(WARPS * 32, 1) w4_kernel(Params p) {
         fetch(stage ^ 1);
         arrived();
         __syncwarp();
+        const uint8_t* at = ring_at + stage * STAGE;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < PARTS; ++h) {
           S sc[2];
 #pragma unroll
-          for (int r = 0; r < 2; ++r) sc[r].read(ring_at + stage * STAGE, g + 8 * r, h);
-          const uint32_t base = ring + stage * STAGE + h * HALF_STAGE + lane_row;
+          for (int r = 0; r < 2; ++r) {
+            const int row = g + 8 * r;
+            sc[r].read(at + scales_at(PARTS) + row * (PARTS * 16) + h * S::BYTES,
+                       at + zeros_at(PARTS) + row * (PARTS * 8) + (ZERO_PAIRS ? (kb & 1) * 2 : h * S::COUNT));
+          }
+          const uint32_t base = ring + stage * STAGE + h * PART + lane_row;
           float part[NT][4];
           float2 s0, s1;
 #pragma unroll
@@ -669,8 +687,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) w4_kernel(Params p) {
             for (int i = 0; i < 2; ++i) {
               const int j = (s + i) / SPG;
               uint32_t d0[4], d1[4];
-              C::pairs(w[2 * i], C::offset(sc[0].zero(j)), d0);
-              C::pairs(w[2 * i + 1], C::offset(sc[1].zero(j)), d1);
+              C::pairs(w[2 * i], sc[0].offset(j), d0);
+              C::pairs(w[2 * i + 1], sc[1].offset(j), d1);
               const uint32_t a0[4] = {d0[0], d1[0], d0[1], d1[1]};
               const uint32_t a1[4] = {d0[2], d1[2], d0[3], d1[3]};
 #pragma unroll
@@ -703,7 +721,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1) w4_kernel(Params p) {
         store(run.tile, sums);
       } else {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) place(warp, kb0 == 0)[t * 32] = sums[t];
+        for (int t = 0; t < NT; ++t) {
+          if (kb0 > 0)
+            place(warp)[t * 32] = sums[t];
+          else
+            tail[t] = sums[t];
+        }
         begun = kb0 == 0;
       }
       run.left -= kb1 - kb0;
@@ -715,9 +738,6 @@ __global__ void __launch_bounds__(WARPS * 32, 1) w4_kernel(Params p) {
     __syncthreads();
     if (begun) {  // the rest of the unit is with the next warps, up to the one that ends it
       const uint32_t end = (uint32_t)(run.chunk * tiles + run.tile + 1 - batch.u0) * blocks;
-      float4 sums[NT];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) sums[t] = place(warp, 1)[t * 32];
       for (int w0 = warp + 1; w0 < WARPS && run_begin(batch, w0) < end; w0 += 4) {
         float4 o[4][NT];
 #pragma unroll
@@ -726,15 +746,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1) w4_kernel(Params p) {
           const bool has = w < WARPS && run_begin(batch, w) < end && run_begin(batch, w) < run_begin(batch, w + 1);
 #pragma unroll
           for (int t = 0; t < NT; ++t)
-            o[k][t] = has ? place(w, 0)[t * 32] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            o[k][t] = has ? place(w)[t * 32] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
           for (int t = 0; t < NT; ++t)
-            sums[t].x += o[k][t].x, sums[t].y += o[k][t].y, sums[t].z += o[k][t].z, sums[t].w += o[k][t].w;
+            tail[t].x += o[k][t].x, tail[t].y += o[k][t].y, tail[t].z += o[k][t].z, tail[t].w += o[k][t].w;
       }
-      store(run.tile, sums);
+      store(run.tile, tail);
     }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -750,19 +770,19 @@ namespace w4 = moe::w4;
 constexpr int kW4Smem = 232448 - 1024;
 
 // Rows of x that a CTA has room for.
-static int w4_room(int nt, int warps, int routes, int64_t K) {
-  const int64_t n = (kW4Smem - w4::fixed_bytes(nt, warps, routes)) / w4::x_pitch(K);
+static int w4_room(int nt, int parts, int routes, int64_t K) {
+  const int64_t n = (kW4Smem - w4::fixed_bytes(nt, parts, routes)) / w4::x_pitch(K);
   return (int)(n < w4::MAX_ROOM ? n : w4::MAX_ROOM);
 }
 
-template <typename T, w4::Format F, int SPG, int NT, int WARPS, bool EXPERTS>
+template <typename T, w4::Format F, int SPG, int NT, int PARTS, bool EXPERTS>
 static moe_status_t launch_w4(w4::Params p, cudaStream_t s) {
-  constexpr auto kernel = w4::w4_kernel<T, F, SPG, NT, WARPS, EXPERTS>;
+  constexpr auto kernel = w4::w4_kernel<T, F, SPG, NT, PARTS, EXPERTS>;
   moe_status_t st = allow_smem<kernel>(kW4Smem);
   if (st != MOE_OK) return st;
   const int routes = EXPERTS ? p.routes : 0;
   const int64_t rows = EXPERTS ? p.routes : p.T, ctas = num_sms();
-  p.room = w4_room(NT, WARPS, routes, p.K);
+  p.room = w4_room(NT, PARTS, routes, p.K);
   const int room = p.room < 8 * NT ? p.room : 8 * NT;
   const int64_t passes = (rows + room - 1) / room;
   p.most = EXPERTS ? (int)(rows < room ? rows : room) : (int)((rows + passes - 1) / passes);
@@ -770,32 +790,32 @@ static moe_status_t launch_w4(w4::Params p, cudaStream_t s) {
   const int64_t tiles = (p.n_out + tile - 1) / tile;
   const int64_t chunks = EXPERTS ? p.routes : passes, units = tiles * chunks;
   p.tiles = (int)tiles;
-  p.blocks = (int)((p.K + w4::BLOCK_K - 1) / w4::BLOCK_K);
+  p.blocks = (int)((p.K + w4::block_k(PARTS) - 1) / w4::block_k(PARTS));
   p.blocks_inverse = (uint32_t)(((uint64_t)1 << 32) / p.blocks + 1);  // of 1 it is not used
   // a CTA's units lie in few chunks where there are many units
   const int64_t likely = (EXPERTS && p.E < chunks ? p.E : chunks) / ctas + 2;
   if (p.room > p.most * likely) p.room = (int)(p.most * likely);
-  const int64_t smem = w4::fixed_bytes(NT, WARPS, routes) + p.room * w4::x_pitch(p.K);
-  return launched(launch_pdl(kernel, dim3((unsigned)(units < ctas ? units : ctas)), dim3(WARPS * 32),
+  const int64_t smem = w4::fixed_bytes(NT, PARTS, routes) + p.room * w4::x_pitch(p.K);
+  return launched(launch_pdl(kernel, dim3((unsigned)(units < ctas ? units : ctas)), dim3(w4::WARPS * 32),
                              (size_t)smem, s, p),
                   "4-bit products");
 }
 
-// Sixteen warps keep the SM's pipes busy; eight leave room for more rows of x, so that the
-// weights pass fewer times.
+// Blocks of two parts cost less beside the codes; of one they leave room for more rows of x,
+// so that the weights pass fewer times.
 template <typename T, w4::Format F, int SPG, bool EXPERTS>
 static moe_status_t run_w4(const w4::Params& p, cudaStream_t s) {
   const int routes = EXPERTS ? p.routes : 0;
   // rows of a matrix: of a short batch's experts most have one or two
   const int64_t rows = EXPERTS ? (p.routes + p.E - 1) / p.E * 2 : p.T;
-  auto passes = [&](int nt, int warps) {
-    const int64_t n = w4_room(nt, warps, routes, p.K), m = n < 8 * nt ? n : 8 * nt;
+  auto passes = [&](int nt, int parts) {
+    const int64_t n = w4_room(nt, parts, routes, p.K), m = n < 8 * nt ? n : 8 * nt;
     return (rows + m - 1) / m;
   };
-  if (passes(1, 16) <= passes(1, 8) && passes(1, 16) <= passes(2, 8))
-    return launch_w4<T, F, SPG, 1, 16, EXPERTS>(p, s);
-  if (passes(1, 8) <= passes(2, 8)) return launch_w4<T, F, SPG, 1, 8, EXPERTS>(p, s);
-  return launch_w4<T, F, SPG, 2, 8, EXPERTS>(p, s);
+  if (passes(1, 2) <= passes(1, 1) && passes(1, 2) <= passes(2, 1))
+    return launch_w4<T, F, SPG, 1, 2, EXPERTS>(p, s);
+  if (passes(1, 1) <= passes(2, 1)) return launch_w4<T, F, SPG, 1, 1, EXPERTS>(p, s);
+  return launch_w4<T, F, SPG, 2, 1, EXPERTS>(p, s);
 }
 
 template <typename T>
@@ -880,7 +900,7 @@ moe_status_t moe_w4_linear(const moe_w4_linear_args_t* a, void* stream) {
   p.ids64 = a->topk_ids_dtype == MOE_IDS_INT64;
   p.act = a->activation;
   auto unit = [&](const void* base, int64_t item) {
-    const uint64_t row = (uint64_t)(K / G * item), block = (uint64_t)(w4::BLOCK_K / G * item);
+    const uint64_t row = (uint64_t)(K / G * item), block = (uint64_t)(512 / G * item);
     const uint64_t bits = row | reinterpret_cast<uintptr_t>(base);
     return bits % (block < 16 ? block : 16) == 0 ? 16 : (bits % 4 == 0 ? 4 : 1);
   };

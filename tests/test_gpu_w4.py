@@ -287,3 +287,19 @@ def test_refusals():
     long = torch.zeros(1025, 256, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(B.MoeError):
         B.moe_w4_linear(long, w, s, torch.empty(1025, 32, dtype=torch.bfloat16, device="cuda"))
+
+
+@pytest.mark.parametrize("fmt,G,zeros", FORMATS)
+@pytest.mark.parametrize("T,K,N", [(5, 16384, 34), (7, 8192, 66), (16, 4096, 98), (12, 7168, 40), (20, 2304, 70),
+                                   (9, 6400, 33), (2, 32768, 17)])
+def test_rows_that_fill_shared_memory(T, K, N, fmt, G, zeros):
+    """Batches whose rows leave room for fewer warps, or for some of the rows only."""
+    p, values = problem(T, K, N, "bf16", fmt, G, zeros)
+    check(p, values, "silu" if N % 2 == 0 else "none")
+
+
+@pytest.mark.parametrize("fmt,G,zeros", [("int4", 128, True), ("e2m1", 32, False)])
+@pytest.mark.parametrize("T,K,k,E", [(40, 7168, 2, 3), (12, 8192, 8, 9), (6, 16384, 2, 5)])
+def test_experts_with_more_rows_than_there_is_room_for(T, K, k, E, fmt, G, zeros):
+    p, values = problem(T, K, 48, "bf16", fmt, G, zeros, E, k, pad=0.05)
+    check(p, values, "gelu_tanh")
