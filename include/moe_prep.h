@@ -867,15 +867,16 @@ size_t moe_gated_linear_workspace_size(int64_t num_tokens, int64_t in_features,
 /*                   needs it.                                               */
 /* activation MOE_ACT_NONE: out has N columns.  Else rows [0, N/2) are a gate,  */
 /* rows [N/2, N) up, and out = act(gate) * up has N/2 columns.                 */
-/* A group's sum is in fp32 of products of the codes with x to 22 bits below    */
-/* the row's largest value and more; the scale multiplies it there; out is     */
-/* rounded once.  A row of x, non-finite values too, reaches its own     */
-/* rows of out alone.  x [T, K] and out: inner stride 1, row strides of their   */
-/* own; weight, scales and zeros contiguous; bf16 or fp16.                     */
-/* Errors: K % G, an odd N with an activation -> SHAPE; G other than 32, 64,    */
-/* 128 (E2M1: 32), zeros with E2M1, more than 1024 rows of out (routes), E >    */
-/* 1024, K > 32768, N >= 2^20, fp32 -> UNSUPPORTED; x, weight or x's rows    */
-/* -> ALIGNMENT.                                                              */
+/* A group's sum is in fp32, of exact products; the scale multiplies it there;*/
+/* out is rounded once.  x enters as it is down to 2^-31 (fp16: 2^-28) of its */
+/* row's largest finite value, and off by at most 2^-40 (2^-36) of that below.*/
+/* A row of x, non-finite values too, reaches its own rows of out alone.  x   */
+/* [T, K] and out: inner stride 1, row strides of their own; weight, scales and*/
+/* zeros contiguous; bf16 or fp16.                                            */
+/* Errors: K % G, an odd N with an activation -> SHAPE; G other than 32, 64,  */
+/* 128 (E2M1: 32), zeros with E2M1, more than 1024 rows of out (routes), E >  */
+/* 1024, K > 32768, N >= 2^20, fp32 -> UNSUPPORTED; x, weight or x's rows not */
+/* on 16-byte boundaries -> ALIGNMENT.                                        */
 /* ------------------------------------------------------------------------ */
 typedef struct moe_w4_linear_args {
   int64_t num_tokens, in_features, matrix_rows; /* T, K, N */

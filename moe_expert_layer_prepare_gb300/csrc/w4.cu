@@ -87,9 +87,7 @@ struct Codes {
       d[i] = *reinterpret_cast<const uint32_t*>(&n);
     }
   }
-  // what makes up for the 2^-24: half of it with a row's power, which goes up to 2^113, and
-  // half at the end
-  static constexpr float UNIT = 0x1p12f;
+  static constexpr int UNIT = 24;  // the codes are 2^-24 as large as they should be
   // x's eight values in the same order; those that meet codes times 2^-20 are 2^-4 as large
   static __device__ __forceinline__ uint4 order(float2 a, float2 b, float2 c, float2 d, float up) {
     const float odd = up * 0.0625f;
@@ -107,7 +105,7 @@ struct Codes<E2M1> {
         : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
         : "r"(w));
   }
-  static constexpr float UNIT = 1.0f;
+  static constexpr int UNIT = 0;
   static __device__ __forceinline__ uint4 order(float2 a, float2 b, float2 c, float2 d, float up) {
     return make_uint4(pack2<__half>(make_float2(a.x * up, a.y * up)), pack2<__half>(make_float2(b.x * up, b.y * up)),
                       pack2<__half>(make_float2(c.x * up, c.y * up)), pack2<__half>(make_float2(d.x * up, d.y * up)));
@@ -353,7 +351,7 @@ __host__ __device__ constexpr int route_bytes(int routes) {
 }
 constexpr int MAX_ROOM = 16;  // rows of x in shared memory
 constexpr int fixed_bytes(int nt, int parts, int routes) {  // beside x
-  return ring_bytes(parts) + red_bytes(nt) + route_bytes(routes) + MAX_ROOM * 4 + WARPS * 4;
+  return ring_bytes(parts) + red_bytes(nt) + route_bytes(routes) + 2 * MAX_ROOM * 4 + WARPS * 4;
 }
 
 template <typename T, Format F, int SPG, int NT, int PARTS, bool EXPERTS>
@@ -368,7 +366,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) w4_kernel(Params p) {
   float4* red = reinterpret_cast<float4*>(smem + ring_bytes(PARTS));
   uint8_t* routing = reinterpret_cast<uint8_t*>(red) + red_bytes(NT);
   float* s_power = reinterpret_cast<float*>(routing + route_bytes(routes));  // [MAX_ROOM]
-  uint32_t* s_amax = reinterpret_cast<uint32_t*>(s_power + MAX_ROOM);       // [WARPS]
+  float* s_rest = s_power + MAX_ROOM;                                         // [MAX_ROOM]
+  uint32_t* s_amax = reinterpret_cast<uint32_t*>(s_rest + MAX_ROOM);         // [WARPS]
   uint8_t* s_x = reinterpret_cast<uint8_t*>(s_amax + WARPS);
   pdl_wait();
   pdl_launch_dependents();
@@ -592,15 +591,19 @@ __global__ void __launch_bounds__(WARPS * 32, 1) w4_kernel(Params p) {
         if (per > 1)
           for (int w = warp / per * per; w < (warp / per + 1) * per; ++w) most = max(most, s_amax[w]);
         const T big = *reinterpret_cast<const T*>(&most);
-        // 2^(14 - e) of a largest value in [2^e, 2^(e + 1)); of the smallest ones 2^100
-        const int e = max((int)(__float_as_uint(to_f32(big)) >> 23) - 127, -86);
+        // 2^(14 - e) of a largest value in [2^e, 2^(e + 1)); of those below 2^-112 2^126
+        const int e = max((int)(__float_as_uint(to_f32(big)) >> 23) - 127, -112);
         const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
 #pragma unroll 4
         for (int i = lane0; i < pieces; i += per * 32) {
           const uint4 v = row[i];
           row[i] = C::order(unpack2<T>(v.x), unpack2<T>(v.y), unpack2<T>(v.z), unpack2<T>(v.w), up);
         }
-        if (lane0 == 0) s_power[col] = __uint_as_float((uint32_t)(127 - 14 + e) << 23) * C::UNIT;
+        if (lane0 == 0) {  // what makes up for it: with the scales up to 2^100, the rest at the end
+          const int back = e - 14 + C::UNIT, with = min(back, 100);
+          s_power[col] = __uint_as_float((uint32_t)(127 + with) << 23);
+          s_rest[col] = __uint_as_float((uint32_t)(127 + back - with) << 23);
+        }
       }
       __syncthreads();
     }
@@ -628,20 +631,20 @@ __global__ void __launch_bounds__(WARPS * 32, 1) w4_kernel(Params p) {
       const int64_t n0 = (int64_t)tile * tile_out;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const float v[4] = {sums[t].x * C::UNIT, sums[t].y * C::UNIT, sums[t].z * C::UNIT,
-                            sums[t].w * C::UNIT};
+        const float v[4] = {sums[t].x, sums[t].y, sums[t].z, sums[t].w};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int col = t * 8 + 2 * c + e;
           if (col >= count) continue;
           int row = first + col;
+          const float rest = s_rest[row - batch_first], low = v[e] * rest, high = v[2 + e] * rest;
           if constexpr (EXPERTS) row = s_route[row];
           T* out = static_cast<T*>(p.out) + row * p.out_stride + n0 + g;
           if (gated) {
-            if (n0 + g < p.n_out) *out = from_f32<T>(act_value(p.act, v[e]) * v[2 + e]);
+            if (n0 + g < p.n_out) *out = from_f32<T>(act_value(p.act, low) * high);
           } else {
-            if (n0 + g < p.n_out) out[0] = from_f32<T>(v[e]);
-            if (n0 + g + 8 < p.n_out) out[8] = from_f32<T>(v[2 + e]);
+            if (n0 + g < p.n_out) out[0] = from_f32<T>(low);
+            if (n0 + g + 8 < p.n_out) out[8] = from_f32<T>(high);
           }
         }
       }

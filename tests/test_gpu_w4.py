@@ -303,3 +303,30 @@ def test_rows_that_fill_shared_memory(T, K, N, fmt, G, zeros):
 def test_experts_with_more_rows_than_there_is_room_for(T, K, k, E, fmt, G, zeros):
     p, values = problem(T, K, 48, "bf16", fmt, G, zeros, E, k, pad=0.05)
     check(p, values, "gelu_tanh")
+
+
+@pytest.mark.parametrize("fmt", ["int4", "e2m1"])
+@pytest.mark.parametrize("size", [2.0 ** -130, 2.0 ** -118, 2.0 ** -90, 2.0 ** -40, 2.0 ** 40, 2.0 ** 100, 2.0 ** 117])
+def test_rows_of_any_size(fmt, size):
+    """bf16 rows near the ends of their exponents: as exact as others."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    w, s, _, values = matrices((40,), 512, fmt, 32, torch.bfloat16, False, g, whole=True)
+    x = torch.randint(-4, 5, (3, 512), generator=g, device="cuda").double()
+    x[1] *= size
+    p = dict(x=x.to(torch.bfloat16), weight=w, scales=s, zeros=None, topk_ids=None)
+    assert torch.equal(p["x"].double(), x)
+    assert torch.equal(run(p), (x @ values.t()).to(torch.float32).to(torch.bfloat16))
+
+
+def test_a_huge_value_with_zero_weight_changes_nothing():
+    g = torch.Generator(device="cuda").manual_seed(8)
+    w, s, _, values = matrices((24,), 256, "int4", 64, torch.bfloat16, False, g)
+    w[:, 50] = 0x88  # columns 100 and 101: code 8 is zero
+    s = (s.float() * 64).to(torch.bfloat16)
+    values = (torch.stack([w & 15, w >> 4], -1).view(24, 4, 64).double() - 8) * s.double()[..., None]
+    x = torch.randn(2, 256, generator=g, device="cuda").to(torch.bfloat16)
+    clean = run(dict(x=x, weight=w, scales=s, zeros=None, topk_ids=None))
+    x[0, 100] = 3e38
+    out = run(dict(x=x, weight=w, scales=s, zeros=None, topk_ids=None))
+    # the others are below 2^-31 of the row's largest value: some 2^-40 of it is all that is left
+    assert bool(out[0].isfinite().all()) and torch.equal(out[1], clean[1])
