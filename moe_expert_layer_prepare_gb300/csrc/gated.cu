@@ -36,7 +36,7 @@ struct Params {
   int64_t out_stride;
   void* gate_up;  // nullable
   int64_t gate_up_stride;
-  bool out_wide, gate_up_wide;  // rows that start on 16 bytes
+  int out_wide, gate_up_wide;  // rows start on 32 bytes (2), 16 (1), or not (0)
   float* partials;              // pieces of tiles; nullptr: no tile is cut
   int half;                     // outputs of a tile of the forward
   int pairs, splits;
@@ -46,18 +46,21 @@ struct Params {
 // 16 values a lane to neighbouring columns of its row, the warp's rows from `first` on, of
 // which `rows` and `left` exist.  Rows that do not start on 16 bytes, and a last tile's columns,
 // go through shared memory, so that a store covers two rows' 32 bytes and not two of 32 rows
-// (1031 tokens, 2056 -> 1403, with gate_up: 73 us by single stores).
+// (1031 tokens, 2056 -> 1403, with gate_up: 73 us by single stores).  Of the others a lane stores
+// whole sectors where it can: d_weight [28672, 4096] of 9 tokens, all stores, takes 73 us, by 16
+// bytes 101, and by lines of 128 bytes of four rows through shared memory 81.
 constexpr int STORE_PITCH = 18;
 template <typename T>
 __device__ __forceinline__ void store16(T* first, int64_t stride, int64_t rows, const float (&v)[16],
-                                        int64_t left, bool wide, T* buf) {
+                                        int64_t left, int wide, T* buf) {
   const int lane = threadIdx.x & 31;
   uint32_t w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = pack2<T>(make_float2(v[2 * i], v[2 * i + 1]));
-  if (wide && left >= 16) {
+  if (wide > 0 && left >= 16) {
     if (lane >= rows) return;
     T* p = first + lane * stride;
+    if (wide == 2) return st_v8(p, w);
     st_v4(p, make_uint4(w[0], w[1], w[2], w[3]));
     st_v4(p + 8, make_uint4(w[4], w[5], w[6], w[7]));
     return;
@@ -94,8 +97,8 @@ __device__ __forceinline__ void store4(const Params& p, int64_t t, int64_t n, fl
   float o[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) o[e] = act_value(p.act, gv[e]) * uv[e];
-  auto put = [&](T* dst, const float (&v)[4], bool wide) {
-    if (wide && n + 4 <= p.N) {
+  auto put = [&](T* dst, const float (&v)[4], int wide) {
+    if (wide > 0 && n + 4 <= p.N) {
       *reinterpret_cast<uint2*>(dst) =
           make_uint2(pack2<T>(make_float2(v[0], v[1])), pack2<T>(make_float2(v[2], v[3])));
     } else {
@@ -532,8 +535,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           tmem_wait16(v);
           if (item.piece >= 0) {
 #pragma unroll
-            for (int j = 0; j < 16; j += 4)
-              st_v4(part + c + j, make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]));
+            for (int j = 0; j < 16; j += 8) {
+              const uint32_t w[8] = {v[j],     v[j + 1], v[j + 2], v[j + 3],
+                                     v[j + 4], v[j + 5], v[j + 6], v[j + 7]};
+              st_v8(part + c + j, w);
+            }
             continue;
           }
           float f[16];
@@ -790,7 +796,7 @@ __global__ void __launch_bounds__(256) gated_slope_kernel(SlopeParams p) {
     const T* gu = static_cast<const T*>(p.gate_up) + t * p.gate_up_stride;
     const T* d_out = static_cast<const T*>(p.d_out) + t * p.d_out_stride;
     T* dst = static_cast<T*>(p.d_gate_up) + t * p.d_stride;
-    for (int n0 = threadIdx.x * VEC; n0 < N; n0 += U * 256 * VEC) {
+    for (int n0 = (blockIdx.y * U * 256 + threadIdx.x) * VEC; n0 < N; n0 += gridDim.y * U * 256 * VEC) {
       Pack<T, VEC> pg[U], pu[U], pd[U];
 #pragma unroll
       for (int k = 0; k < U; ++k) {
@@ -827,6 +833,12 @@ __global__ void __launch_bounds__(256) gated_slope_kernel(SlopeParams p) {
 namespace moe_host {
 
 namespace gated = moe::gated;
+
+// 2 where rows of 16-bit values start on 32 bytes, 1 on 16, else 0.
+static int row_width(const void* p, int64_t stride0, int64_t rows) {
+  const uint64_t bits = reinterpret_cast<uintptr_t>(p) | (rows > 1 ? (uint64_t)stride0 * 2 : 0);
+  return bits % 32 == 0 ? 2 : (bits % 16 == 0 ? 1 : 0);
+}
 
 // Smallest tile that holds the batch; a cluster shares a tile's K while tiles leave CTA
 // slots empty.
@@ -964,12 +976,17 @@ static moe_status_t launch_gated_backward(const moe_gated_linear_backward_args_t
   const bool wide = p.N % 8 == 0 && rows_aligned16(a->d_out, a->d_out_stride0, 2, p.T) &&
                     rows_aligned16(a->gate_up, a->gate_up_stride0, 2, p.T);
   const int64_t cap = 8 * (int64_t)num_sms();
-  const dim3 grid((unsigned)(p.T < cap ? p.T : cap));
+  // a row a block, of few rows its parts
+  const int64_t parts = (p.N + (wide ? 2048 : 1024) - 1) / (wide ? 2048 : 1024);
+  const int64_t spread = cap / p.T < 1 ? 1 : cap / p.T;
+  const dim3 grid((unsigned)(p.T < cap ? p.T : cap), (unsigned)(parts < spread ? parts : spread));
   moe_status_t st = launched(wide ? launch_pdl(gated::gated_slope_kernel<T, 8>, grid, dim3(256), 0, s, sp)
                                   : launch_pdl(gated::gated_slope_kernel<T, 1>, grid, dim3(256), 0, s, sp),
                              "gated slope");
   if (st != MOE_OK) return st;
-  p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + d_gate_up_bytes(p.T, p.N));
+  // on 32 bytes, as sums are stored
+  p.partials = reinterpret_cast<float*>(
+      (reinterpret_cast<uintptr_t>(a->workspace) + d_gate_up_bytes(p.T, p.N) + 31) & ~(uintptr_t)31);
   CUtensorMap ma, mb;
   if (a->d_x != nullptr) {
     if (!make_map16(&ma, bf16, a->workspace, p.T, 2 * p.N, ds, gated::HALF) ||
@@ -977,7 +994,7 @@ static moe_status_t launch_gated_backward(const moe_gated_linear_backward_args_t
       return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for d_x");
     p.out = a->d_x;
     p.out_stride = a->d_x_stride0;
-    p.out_wide = rows_aligned16(a->d_x, a->d_x_stride0, 2, p.T);
+    p.out_wide = row_width(a->d_x, a->d_x_stride0, p.T);
     st = launch_gated_pair<T, gated::D_X>(p, ma, mb, mb, s);
     if (st != MOE_OK) return st;
   }
@@ -988,7 +1005,7 @@ static moe_status_t launch_gated_backward(const moe_gated_linear_backward_args_t
       return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for d_weight");
     p.out = a->d_weight;
     p.out_stride = p.K;
-    p.out_wide = rows_aligned16(a->d_weight, p.K, 2, 2 * p.N);
+    p.out_wide = row_width(a->d_weight, p.K, 2 * p.N);
     st = launch_gated_pair<T, gated::D_W>(p, ma, mb, mb, s);
   }
   return st;
@@ -1044,10 +1061,13 @@ moe_status_t moe_gated_linear(const moe_gated_linear_args_t* a, void* stream) {
   p.act = a->activation;
   p.out = a->out;
   p.out_stride = a->out_stride0;
-  p.out_wide = rows_aligned16(a->out, a->out_stride0, 2, T);
+  p.out_wide = row_width(a->out, a->out_stride0, T);
   p.gate_up = a->gate_up;
   p.gate_up_stride = a->gate_up_stride0;
-  p.gate_up_wide = N % 8 == 0 && rows_aligned16(a->gate_up, a->gate_up_stride0, 2, T);
+  {  // both halves of a row
+    const int width = row_width(a->gate_up, a->gate_up_stride0, T);
+    p.gate_up_wide = N % 16 == 0 ? width : (N % 8 == 0 && width > 0);
+  }
   p.pairs = num_sms() / 2;
   p.half = gated::HALF;
   p.splits = 1;
@@ -1060,7 +1080,7 @@ moe_status_t moe_gated_linear(const moe_gated_linear_args_t* a, void* stream) {
 size_t moe_gated_linear_workspace_size(int64_t num_tokens, int64_t in_features,
                                        int64_t out_features) {
   if (num_tokens <= 0 || in_features <= 0 || out_features <= 0) return 0;
-  return (size_t)(d_gate_up_bytes(num_tokens, out_features) +
+  return (size_t)(d_gate_up_bytes(num_tokens, out_features) + 32 +
                   (int64_t)(num_sms() / 2) * gated::PIECE * 4);
 }
 

@@ -315,3 +315,20 @@ def test_tiles_of_every_width(T, N):
     x, w, _ = problem(T, 520, N, "bf16")
     check_forward(x, w, "silu")
     check_forward(x, w, "gelu_tanh", layout="strided")
+
+
+@pytest.mark.parametrize("T,K,N", [(1, 512, 5000), (3, 1024, 3001), (9, 4096, 700), (700, 1000, 300)])
+def test_gradients_of_few_tokens_and_a_workspace_on_16_bytes(T, K, N):
+    """Wide blocks of few tokens; tiles cut along k keep their sums in a workspace that starts on 16
+    bytes and on no more; results on 16 bytes too."""
+    x, w, d = problem(T, K, N, "bf16")
+    gate_up = (x.float() @ w.float().t()).to(x.dtype)
+    want = check_backward(d, x, w, gate_up, "silu")
+    need = B.gated_linear_workspace_size(T, K, N)
+    ws = torch.empty(need + 256, dtype=torch.uint8, device="cuda")
+    ws = ws[(16 - ws.data_ptr()) % 32:][:need]
+    assert ws.data_ptr() % 32 == 16
+    d_x = torch.empty(T * K + 8, dtype=x.dtype, device="cuda")[8:].view(T, K)
+    d_w = torch.empty(2 * N * K + 8, dtype=x.dtype, device="cuda")[8:].view(2 * N, K)
+    B.moe_gated_linear_backward(d, x, w, gate_up, d_x=d_x, d_weight=d_w, workspace=ws)
+    assert torch.equal(d_x, want[0]) and torch.equal(d_w, want[1])
