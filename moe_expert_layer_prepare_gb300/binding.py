@@ -2,8 +2,9 @@
 
 The functions keep the C names: ``moe_prepare_inputs``, ``moe_batched_experts``,
 ``moe_topk_reduce``; around them ``moe_route``, ``moe_sort_routes``, ``moe_permute``,
-``moe_unpermute``, ``moe_block_norm``, ``moe_lora_linear`` and their gradients.  Tensors are PyTorch CUDA tensors; only their data
-pointers, shapes and strides cross the boundary.  Every step of the path runs
+``moe_unpermute``, ``moe_block_norm``, ``moe_lora_linear``, ``moe_norm_quant``,
+``moe_gated_linear``, ``moe_w4_linear`` and their gradients.  Tensors are PyTorch CUDA tensors; only
+their data pointers, shapes and strides cross the boundary.  Every step of the path runs
 in the library's kernels; if the library is missing this module raises.
 """
 from __future__ import annotations

@@ -6,15 +6,24 @@
 //   forward   m tokens, n features, k the columns of x;
 //   d_x       m tokens, n the columns of x, k the rows of W;
 //   d_W       m the rows of W, n the columns of x, k tokens.
-// An operand that has k along its rows of memory is read as it lies (the MMA takes either
-// order), so nothing is transposed.  The forward's tile takes as many gate rows as up rows
+// Operands are read as they lie in memory, k along their rows or across them (the MMA takes
+// either), so nothing is transposed.  The forward's tile takes as many gate rows as up rows
 // of W, so that one thread has both values of an output and the activation costs no pass.
 //
 //   Few tokens (gated_split_kernel): W is streamed, so HBM bounds it.  Features are the
 //   rows of the accumulator (64 gate, 64 up), tokens its columns, and with few tiles the
 //   K slabs are dealt out to the CTAs of a cluster.
 //   Many (gated_pair_kernel): the tensor cores bound it.  CTA pairs keep 256 x 256 tiles
-//   and two accumulators, one in use while the other is written out.
+//   and two accumulators, one in use while the other is written out.  Where the forward
+//   has fewer tiles than half of the pairs, two pairs share one (gated_cluster_kernel).
+//
+// d_g and d_u are a pass of their own over d_out and gate_up (12 us of the 4096 tokens
+// below, at HBM's rate), rounded to the tensors' type as the MMA takes them: d_x and d_W are
+// then off by 1.2 times what their own rounding makes.
+//
+// Measured, 7168 -> 2048 bf16: one token 12.4 us (59 MB, 4.7 TB/s), 512 tokens 24 us, 4096
+// tokens 129 us (1.86 PFLOP/s) and their gradients 292 (1.65), 8192 tokens 250 (1.92); 64
+// tokens 4096 -> 14336 39 us (6.0 TB/s).
 #include <mutex>
 #include <type_traits>
 
