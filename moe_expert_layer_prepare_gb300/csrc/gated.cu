@@ -88,8 +88,10 @@ __device__ __forceinline__ void store16(T* first, int64_t stride, int64_t rows, 
 }
 
 // ------------------------------------------------------------- few tokens
-// At 128 tokens this path takes 16 us (7168 -> 2048) and the pairs 33; at 512 36 us and two
-// pairs a tile 25, into 14336 features 175 and 82.
+// At 128 tokens this path takes 16 us (7168 -> 2048) and two pairs a tile 22; at 512 36 us and
+// 25, into 14336 features 175 and 82. From 65 tokens on, where more than every second pair has a
+// tile of its own, the pairs are faster: 128 tokens, 7168 -> 4872 33 us against 39, -> 14336 71
+// against 87. They lose where K is small and a second round is short (1024 -> 9600 11.8, 10.9).
 constexpr int SPLIT_TOKENS = 128;
 constexpr int SM_ROWS = 128;     // of a tile: 64 gate rows of W, 64 up rows
 constexpr int SM_FEATURES = 64;  // outputs of a tile
@@ -936,10 +938,10 @@ static moe_status_t launch_gated(const moe_gated_linear_args_t* a, gated::Params
   const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
   const int64_t x_stride = p.T > 1 ? a->x_stride0 : p.K;
   const T* up = static_cast<const T*>(a->weight) + p.N * p.K;
-  const bool split = p.T <= gated::SPLIT_TOKENS;
+  const gated::Work whole(gated::FORWARD, p.T, p.K, p.N, p.pairs, false, gated::HALF);
+  const bool split = p.T <= 64 || (p.T <= gated::SPLIT_TOKENS && whole.units * 2 <= p.pairs);
   const SplitPlan q = split_plan(p.T, p.K, p.N);
   // Two pairs a tile where there are few.
-  const gated::Work whole(gated::FORWARD, p.T, p.K, p.N, p.pairs, false, gated::HALF);
   const bool shared = !split && whole.units * 2 <= p.pairs && whole.slabs >= 8;
   if (!split && !shared) p.half = best_half(p);
   const int rows = split ? gated::SM_FEATURES : p.half;

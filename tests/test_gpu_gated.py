@@ -332,3 +332,11 @@ def test_gradients_of_few_tokens_and_a_workspace_on_16_bytes(T, K, N):
     d_w = torch.empty(2 * N * K + 8, dtype=x.dtype, device="cuda")[8:].view(2 * N, K)
     B.moe_gated_linear_backward(d, x, w, gate_up, d_x=d_x, d_weight=d_w, workspace=ws)
     assert torch.equal(d_x, want[0]) and torch.equal(d_w, want[1])
+
+
+@pytest.mark.parametrize("T", [64, 65, 100, 128, 129])
+def test_wide_blocks_around_the_kernels_limits(T):
+    """Around as many features as give every second pair of CTAs a tile, and every one."""
+    for N in (4800, 4900, 9600, 9800):
+        x, w, _ = problem(T, 136, N, "fp16")
+        check_forward(x, w, "gelu_tanh")
