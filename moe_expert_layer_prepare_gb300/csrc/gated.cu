@@ -15,7 +15,7 @@
 //   K slabs are dealt out to the CTAs of a cluster.
 //   Many (gated_pair_kernel): the tensor cores bound it.  CTA pairs keep 256 x 256 tiles
 //   and two accumulators, one in use while the other is written out.  Where the forward
-//   has fewer tiles than half of the pairs, two pairs share one (gated_cluster_kernel).
+//   has few tiles and a long K, two pairs share a tile (gated_cluster_kernel).
 //
 // d_g and d_u are a pass of their own over d_out and gate_up (12 us of the 4096 tokens
 // below, at HBM's rate), rounded to the tensors' type as the MMA takes them: d_x and d_W are
@@ -908,6 +908,39 @@ static moe_status_t launch_gated_pair(const gated::Params& p, const CUtensorMap&
   return st;
 }
 
+// How many tiles' clusters the GPU runs at once (36 of four CTAs: some of its partitions' SMs
+// are left over).
+template <typename T, int SPLITS>
+static int clusters_at_once() {
+  constexpr auto kernel = gated::gated_cluster_kernel<T, SPLITS>;
+  static std::mutex mu;
+  static int known[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (allow_smem<kernel>(gated::SMEM) != MOE_OK) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (known[dev] == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(num_sms() / (2 * SPLITS) * (2 * SPLITS)));
+    cfg.blockDim = dim3(gated::THREADS);
+    cfg.dynamicSmemBytes = gated::SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2 * SPLITS;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    known[dev] = n;
+  }
+  return known[dev];
+}
+
 template <typename T, int SPLITS>
 static moe_status_t launch_gated_cluster(const gated::Params& p, int units, const CUtensorMap& x,
                                          const CUtensorMap& g, const CUtensorMap& u, cudaStream_t s) {
@@ -941,8 +974,11 @@ static moe_status_t launch_gated(const moe_gated_linear_args_t* a, gated::Params
   const gated::Work whole(gated::FORWARD, p.T, p.K, p.N, p.pairs, false, gated::HALF);
   const bool split = p.T <= 64 || (p.T <= gated::SPLIT_TOKENS && whole.units * 2 <= p.pairs);
   const SplitPlan q = split_plan(p.T, p.K, p.N);
-  // Two pairs a tile where there are few.
-  const bool shared = !split && whole.units * 2 <= p.pairs && whole.slabs >= 8;
+  // Two pairs a tile where all the clusters run at once (256 tokens, 7168 -> 4608 29.3 us and
+  // alone 31.6; with two clusters more 49 and 32) and the K that a second pair takes over is
+  // worth the sums' exchange (256 tokens -> 2048 features of 1024 8.6 us, alone 7.1; of 4096
+  // 15.7 and 17.5, -> 4096 19.0 and 19.2).
+  const bool shared = !split && whole.slabs >= 56 && whole.units <= clusters_at_once<T, 2>();
   if (!split && !shared) p.half = best_half(p);
   const int rows = split ? gated::SM_FEATURES : p.half;
   CUtensorMap g, u, x;

@@ -340,3 +340,14 @@ def test_wide_blocks_around_the_kernels_limits(T):
     for N in (4800, 4900, 9600, 9800):
         x, w, _ = problem(T, 136, N, "fp16")
         check_forward(x, w, "gelu_tanh")
+
+
+@pytest.mark.parametrize("T,K,N", [(129, 3528, 384), (256, 3592, 601), (300, 4104, 203),
+                                   (256, 3592, 4608), (256, 3592, 4736), (385, 3520, 264)])
+@pytest.mark.parametrize("layout", ["plain", "strided"])
+def test_two_pairs_a_tile_and_the_tiles_alone(T, K, N, layout):
+    """K and tiles around what two pairs share, an odd number of slabs, odd rows."""
+    x, w, _ = problem(T, K, N, "bf16", layout=layout)
+    out, _ = check_forward(x, w, "silu", layout=layout)
+    alone, _ = check_forward(x, w, "silu", layout=layout, keep=False)
+    assert torch.equal(out, alone)
