@@ -851,35 +851,73 @@ static int row_width(const void* p, int64_t stride0, int64_t rows) {
   return bits % 32 == 0 ? 2 : (bits % 16 == 0 ? 1 : 0);
 }
 
-// Smallest tile that holds the batch; a cluster shares a tile's K while tiles leave CTA
-// slots empty.
-struct SplitPlan {
-  int nt, splits;
-};
-static SplitPlan split_plan(int64_t T, int64_t K, int64_t N) {
-  SplitPlan q{};
-  const int64_t sms = num_sms();
-  q.nt = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 ? 64 : 128));
-  const int64_t tiles =
-      (N + gated::SM_FEATURES - 1) / gated::SM_FEATURES * ((T + q.nt - 1) / q.nt);
-  const int64_t slots = q.nt <= 64 ? 2 * sms : sms;
-  const int64_t slabs = (K + 63) / 64;
-  q.splits = 1;
-  while (q.splits < 8 && tiles * q.splits * 2 <= slots) {
-    const int64_t per = (slabs + 2 * q.splits - 1) / (2 * q.splits);
-    if (per < 4 || per * (2 * q.splits - 1) >= slabs) break;  // every share has slabs
-    q.splits *= 2;
+// How many clusters of 2, 4 or 8 CTAs, each on an SM of its own, the GPU runs at once.  Of four
+// it is 36, not 38, of eight 15: some of the chip's partitions leave SMs over.
+static int clusters_at_once(int ctas) {
+  constexpr auto kernel = gated::gated_cluster_kernel<__nv_bfloat16, 2>;
+  static_assert(2 * gated::SMEM > kMaxSmem, "one CTA an SM");
+  static std::mutex mu;
+  static int known[64][9] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (allow_smem<kernel>(gated::SMEM) != MOE_OK) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (known[dev][ctas] == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(gated::THREADS);
+    cfg.dynamicSmemBytes = (size_t)gated::SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    known[dev][ctas] = n;
   }
-  return q;
+  return known[dev][ctas];
+}
+
+// A cluster shares a tile's K while all the clusters run at once.  Up to 64 tokens two CTAs fit
+// an SM: then a cluster of eight takes four SMs and two of four share them.  (Measured: of 37
+// and 38 tiles in eighths, of 75 and 76 in quarters some wait; one token of 7168 -> 2432 18.8
+// us, in quarters 14.2; -> 4864 30.6, in halves 24.8.  73 and 74 in quarters would still fit,
+// 64 tokens -> 4672 25.4 against 26.8.  128 tokens -> 1024, an SM each: eighths 20.9, quarters
+// 13.8.)  The sums' exchange grows with the tokens: for 17 or more a share on a second CTA of
+// an SM has to be eight slabs (64 tokens, 2048 -> 2048 7.3 us, with four 8.5; 32 tokens 6.6
+// and 7.3; but one token, 2048 -> 1024, 4.7 and 4.4).
+template <int NT>
+static int splits_of(int64_t K, int64_t N) {
+  const int64_t tiles = (N + gated::SM_FEATURES - 1) / gated::SM_FEATURES;
+  const int64_t slabs = (K + 63) / 64;
+  int splits = 1;
+  while (splits < 8) {
+    const int more = 2 * splits;
+    const int64_t per = (slabs + more - 1) / more;
+    if (per < 4 || per * (more - 1) >= slabs) break;  // every share has slabs
+    const bool two = NT <= 64 && per >= (NT <= 16 ? 4 : 8);
+    const int64_t fit = !two ? clusters_at_once(more)
+                             : (more == 2 ? num_sms() : clusters_at_once(4) * 8 / more);
+    if (tiles > fit) break;
+    splits = more;
+  }
+  return splits;
 }
 
 template <typename T, int NT>
-static moe_status_t launch_gated_split(const gated::Params& p, const CUtensorMap& g,
-                                       const CUtensorMap& u, const CUtensorMap& x, cudaStream_t s) {
+static moe_status_t launch_gated_split(gated::Params p, const CUtensorMap& g, const CUtensorMap& u,
+                                       const CUtensorMap& x, cudaStream_t s) {
   constexpr auto kernel = gated::gated_split_kernel<T, NT>;
   static_assert(gated::sm_smem(NT) <= kMaxSmem, "shared memory of one CTA");
   moe_status_t st = allow_smem<kernel>(gated::sm_smem(NT));
   if (st != MOE_OK) return st;
+  p.splits = splits_of<NT>(p.K, p.N);
   const dim3 grid((unsigned)((p.N + gated::SM_FEATURES - 1) / gated::SM_FEATURES * p.splits),
                   (unsigned)((p.T + NT - 1) / NT));
   return launched(launch_cluster(kernel, grid, gated::SM_THREADS, p.splits,
@@ -906,39 +944,6 @@ static moe_status_t launch_gated_pair(const gated::Params& p, const CUtensorMap&
                              dim3(256), 0, s, p),
                   "gated projection join");
   return st;
-}
-
-// How many tiles' clusters the GPU runs at once (36 of four CTAs: some of its partitions' SMs
-// are left over).
-template <typename T, int SPLITS>
-static int clusters_at_once() {
-  constexpr auto kernel = gated::gated_cluster_kernel<T, SPLITS>;
-  static std::mutex mu;
-  static int known[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  if (allow_smem<kernel>(gated::SMEM) != MOE_OK) return 0;
-  std::lock_guard<std::mutex> lock(mu);
-  if (known[dev] == 0) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(num_sms() / (2 * SPLITS) * (2 * SPLITS)));
-    cfg.blockDim = dim3(gated::THREADS);
-    cfg.dynamicSmemBytes = gated::SMEM;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2 * SPLITS;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
-      cudaGetLastError();
-      return 0;
-    }
-    known[dev] = n;
-  }
-  return known[dev];
 }
 
 template <typename T, int SPLITS>
@@ -973,25 +978,25 @@ static moe_status_t launch_gated(const moe_gated_linear_args_t* a, gated::Params
   const T* up = static_cast<const T*>(a->weight) + p.N * p.K;
   const gated::Work whole(gated::FORWARD, p.T, p.K, p.N, p.pairs, false, gated::HALF);
   const bool split = p.T <= 64 || (p.T <= gated::SPLIT_TOKENS && whole.units * 2 <= p.pairs);
-  const SplitPlan q = split_plan(p.T, p.K, p.N);
+  // smallest tile that holds the batch
+  const int nt = p.T <= 16 ? 16 : (p.T <= 32 ? 32 : (p.T <= 64 ? 64 : 128));
   // Two pairs a tile where all the clusters run at once (256 tokens, 7168 -> 4608 29.3 us and
   // alone 31.6; with two clusters more 49 and 32) and the K that a second pair takes over is
   // worth the sums' exchange (256 tokens -> 2048 features of 1024 8.6 us, alone 7.1; of 4096
   // 15.7 and 17.5, -> 4096 19.0 and 19.2).
-  const bool shared = !split && whole.slabs >= 56 && whole.units <= clusters_at_once<T, 2>();
+  const bool shared = !split && whole.slabs >= 56 && whole.units <= clusters_at_once(4);
   if (!split && !shared) p.half = best_half(p);
   const int rows = split ? gated::SM_FEATURES : p.half;
   CUtensorMap g, u, x;
   if (!make_map16(&g, bf16, a->weight, p.N, p.K, p.K, rows) ||
       !make_map16(&u, bf16, up, p.N, p.K, p.K, rows) ||
-      !make_map16(&x, bf16, a->x, p.T, p.K, x_stride, split ? q.nt : gated::HALF))
+      !make_map16(&x, bf16, a->x, p.T, p.K, x_stride, split ? nt : gated::HALF))
     return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the gated projection");
   // (Four, in clusters of eight CTAs, of which not sixteen fit the GPU at once: 256 tokens of
   // 7168 -> 2048 34 us, two 23.)
   if (shared) return launch_gated_cluster<T, 2>(p, whole.units, x, g, u, s);
   if (!split) return launch_gated_pair<T, gated::FORWARD>(p, x, g, u, s);
-  p.splits = q.splits;
-  switch (q.nt) {
+  switch (nt) {
     case 16: return launch_gated_split<T, 16>(p, g, u, x, s);
     case 32: return launch_gated_split<T, 32>(p, g, u, x, s);
     case 64: return launch_gated_split<T, 64>(p, g, u, x, s);

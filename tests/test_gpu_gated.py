@@ -351,3 +351,10 @@ def test_two_pairs_a_tile_and_the_tiles_alone(T, K, N, layout):
     out, _ = check_forward(x, w, "silu", layout=layout)
     alone, _ = check_forward(x, w, "silu", layout=layout, keep=False)
     assert torch.equal(out, alone)
+
+
+@pytest.mark.parametrize("T", [1, 32, 64, 128])
+@pytest.mark.parametrize("N", [1024, 1160, 1216, 2304, 2432, 2500, 4736, 4864])
+def test_shares_of_k_around_the_clusters_that_run_at_once(T, N):
+    x, w, _ = problem(T, 2056, N, "bf16")
+    check_forward(x, w, "silu")
