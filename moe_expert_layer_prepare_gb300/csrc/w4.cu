@@ -430,7 +430,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) w4_kernel(Params p) {
   auto run_begin = [&](const Batch& q, int w) { return (uint32_t)((q.u1 - q.u0) * blocks) * w / WARPS; };
   auto run_of = [&](const Batch& q) {
     const uint32_t begin = run_begin(q, warp), end = run_begin(q, warp + 1);
-    // begin / blocks: begin is below 2^24 and blocks at most 2^7
+    // begin / blocks, exact as begin * blocks is below 2^32: blocks are at most 2^7, and a batch
+    // has 2^16 tiles a row of x at most and as many rows as shared memory holds (3 of 2^7 blocks)
     const int unit = blocks == 1 ? (int)begin : (int)__umulhi(begin, p.blocks_inverse);
     Run r{q.chunk0, q.u0 - q.chunk0 * tiles + unit, (int)begin - unit * blocks, (int)(end - begin), q.chunk1};
     while (r.tile >= tiles) r.tile -= tiles, ++r.chunk;
@@ -874,6 +875,9 @@ moe_status_t moe_w4_linear(const moe_w4_linear_args_t* a, void* stream) {
     return set_error(MOE_ERR_INVALID_ARGUMENT, "bad topk_ids_dtype %d", a->topk_ids_dtype);
   const bool gated = a->activation != MOE_ACT_NONE;
   if (gated && N % 2 != 0) return set_error(MOE_ERR_SHAPE, "as many gate rows as up rows are needed");
+  if (experts && a->top_k > 0 && T > INT64_MAX / a->top_k)
+    return set_error(MOE_ERR_UNSUPPORTED, "at most %d routes to %d experts", w4::MAX_ROUTES,
+                     w4::MAX_EXPERTS);
   const int64_t rows = experts ? T * a->top_k : T, n_out = gated ? N / 2 : N;
   if (rows == 0 || N == 0) return MOE_OK;
   if (K < 1 || K % G != 0)

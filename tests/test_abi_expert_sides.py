@@ -134,3 +134,13 @@ def test_w4_linear(lib):  # noqa: F811
     assert call(x_stride0=257) == ALIGNMENT
     assert call(x=FAKE + 2) == ALIGNMENT
     assert call(weight=FAKE + 8) == ALIGNMENT
+
+
+def test_w4_linear_counts_routes_without_wrapping(lib):  # noqa: F811
+    """tokens * top_k that would wrap to none, and to a few."""
+    for T, k in ((1 << 40, 1 << 40), ((1 << 62) + 1, 4)):
+        args = fill(B.W4LinearArgs, num_tokens=T, in_features=256, matrix_rows=32, num_experts=4,
+                    top_k=k, group_size=64, dtype=B.MOE_DTYPE_BF16, format=B.MOE_W4_INT4,
+                    activation=B.MOE_ACT_NONE, x_stride0=256, topk_ids_dtype=B.MOE_IDS_INT32,
+                    out_stride0=31)
+        assert lib.moe_w4_linear(ctypes.byref(args), None) == UNSUPPORTED
