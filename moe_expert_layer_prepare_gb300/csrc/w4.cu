@@ -48,7 +48,7 @@ constexpr int block_k(int parts) { return 256 * parts; }
 constexpr int scales_at(int parts) { return parts * PART; }
 constexpr int zeros_at(int parts) { return scales_at(parts) + parts * ROWS * 16; }
 constexpr int stage_bytes(int parts) { return zeros_at(parts) + parts * ROWS * 8; }
-constexpr int MAX_ROUTES = 1024, MAX_EXPERTS = 1024;
+constexpr int MAX_ROUTES = 1024, MAX_EXPERTS = 1024, MAX_K = 32768;
 
 struct Params {
   int64_t T, K, N;  // N: rows of a matrix
@@ -779,11 +779,14 @@ namespace w4 = moe::w4;
 
 constexpr int kW4Smem = 232448 - 1024;
 
-// Rows of x that a CTA has room for.
-static int w4_room(int nt, int parts, int routes, int64_t K) {
+// Rows of x that a CTA has room for: always one beside blocks of one part; beside those of two
+// perhaps none, where rows are long and routes many (1024 routes and K above 25,088, 33 routes
+// and K above 29,184).
+constexpr int w4_room(int nt, int parts, int routes, int64_t K) {
   const int64_t n = (kW4Smem - w4::fixed_bytes(nt, parts, routes)) / w4::x_pitch(K);
   return (int)(n < w4::MAX_ROOM ? n : w4::MAX_ROOM);
 }
+static_assert(w4_room(2, 1, w4::MAX_ROUTES, w4::MAX_K) >= 1, "a row of x has room");
 
 template <typename T, w4::Format F, int SPG, int NT, int PARTS, bool EXPERTS>
 static moe_status_t launch_w4(w4::Params p, cudaStream_t s) {
@@ -820,7 +823,7 @@ static moe_status_t run_w4(const w4::Params& p, cudaStream_t s) {
   const int64_t rows = EXPERTS ? (p.routes + p.E - 1) / p.E * 2 : p.T;
   auto passes = [&](int nt, int parts) {
     const int64_t n = w4_room(nt, parts, routes, p.K), m = n < 8 * nt ? n : 8 * nt;
-    return (rows + m - 1) / m;
+    return m < 1 ? INT64_MAX : (rows + m - 1) / m;
   };
   if (passes(1, 2) <= passes(1, 1) && passes(1, 2) <= passes(2, 1))
     return launch_w4<T, F, SPG, 1, 2, EXPERTS>(p, s);
@@ -888,8 +891,8 @@ moe_status_t moe_w4_linear(const moe_w4_linear_args_t* a, void* stream) {
                      w4::MAX_EXPERTS);
   if (!experts && T > w4::MAX_ROUTES)
     return set_error(MOE_ERR_UNSUPPORTED, "at most %d rows", w4::MAX_ROUTES);
-  if (K > 32768 || N >= ((int64_t)1 << 20))
-    return set_error(MOE_ERR_UNSUPPORTED, "in_features above 32768 or 2^20 rows of a matrix");
+  if (K > w4::MAX_K || N >= ((int64_t)1 << 20))
+    return set_error(MOE_ERR_UNSUPPORTED, "in_features above %d or 2^20 rows of a matrix", w4::MAX_K);
   if (!a->x || !a->weight || !a->scales || !a->out)
     return set_error(MOE_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
   if ((T > 1 && a->x_stride0 < K) || (rows > 1 && a->out_stride0 < n_out))

@@ -1,6 +1,9 @@
 """Host-side refusals of the norm with an 8-bit output, the gated projection and the products with
 4-bit weights (no GPU: every call below returns before its first CUDA call)."""
 import ctypes
+import os
+import subprocess
+import sys
 
 from moe_expert_layer_prepare_gb300 import binding as B
 from tests.test_abi_block import (ALIGNMENT, FAKE, INVALID, OK, SHAPE, UNSUPPORTED, WORKSPACE,  # noqa: F401
@@ -144,3 +147,34 @@ def test_w4_linear_counts_routes_without_wrapping(lib):  # noqa: F811
                     activation=B.MOE_ACT_NONE, x_stride0=256, topk_ids_dtype=B.MOE_IDS_INT32,
                     out_stride0=31)
         assert lib.moe_w4_linear(ctypes.byref(args), None) == UNSUPPORTED
+
+
+# Every length of the rows above 24,000 with every count of routes, with no GPU in sight: a call that
+# the checks let pass ends at its first CUDA call, before its pointers are read.
+SWEEP = """
+import ctypes
+from moe_expert_layer_prepare_gb300 import binding as B
+from tests.test_abi_block import fill
+lib, calls = B.load(), 0
+for fmt, G in ((B.MOE_W4_INT4, 32), (B.MOE_W4_INT4, 64), (B.MOE_W4_INT4, 128), (B.MOE_W4_E2M1, 32)):
+    for routes, k in ((1, 1), (32, 1), (33, 1), (64, 8), (216, 8), (512, 8), (1024, 1), (1024, 8)):
+        for K in range(24064, 32769, 128):
+            zeros = 0x10000 if calls % 2 and fmt == B.MOE_W4_INT4 else None
+            a = fill(B.W4LinearArgs, num_tokens=routes // k, in_features=K, matrix_rows=7168,
+                     num_experts=(3, 256)[calls // 2 % 2], top_k=k, group_size=G, dtype=1 + calls // 4 % 2,
+                     format=fmt, activation=(B.MOE_ACT_NONE, B.MOE_ACT_SILU)[calls // 8 % 2],
+                     zeros=zeros, x_stride0=K, topk_ids_dtype=B.MOE_IDS_INT32, out_stride0=7168)
+            st = lib.moe_w4_linear(ctypes.byref(a), None)
+            assert st == 6, (st, fmt, G, routes, K, lib.moe_last_error())
+            calls += 1
+print(calls)
+"""
+
+
+def test_w4_linear_has_a_form_for_long_rows_of_many_routes(lib):  # noqa: F811
+    """In a process of its own, which an integer division by zero would end."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", SWEEP], cwd=root, capture_output=True, text=True,
+                       env=dict(os.environ, CUDA_VISIBLE_DEVICES="", PYTHONPATH=root))
+    assert r.returncode == 0, (r.returncode, r.stderr[-2000:])
+    assert int(r.stdout) == 4 * 8 * 69

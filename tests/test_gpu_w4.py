@@ -330,3 +330,24 @@ def test_a_huge_value_with_zero_weight_changes_nothing():
     out = run(dict(x=x, weight=w, scales=s, zeros=None, topk_ids=None))
     # the others are below 2^-31 of the row's largest value: some 2^-40 of it is all that is left
     assert bool(out[0].isfinite().all()) and torch.equal(out[1], clean[1])
+
+
+@pytest.mark.parametrize("fmt,G,zeros", [("int4", 32, False), ("int4", 128, True), ("e2m1", 32, False)])
+@pytest.mark.parametrize("T,K,E,k", [(33, 29312, 4, 1), (8, 28672, 5, 8), (64, 32768, 3, 1), (64, 28672, 6, 8),
+                                     (128, 25600, 3, 8), (1024, 32768, 2, 1)])
+def test_long_rows_of_many_routes(T, K, E, k, fmt, G, zeros):
+    """Rows beside which the longer blocks have no room, and some beside which they have.  Whole
+    numbers, so that every sum is exact in fp32: far below 2^24 of their unit, 1/16 or 1/4."""
+    g = torch.Generator(device="cuda").manual_seed(T + K + G)
+    w, s, z, values = matrices((E, 18), K, fmt, G, torch.bfloat16, zeros, g, whole=True)
+    x = torch.randint(-4, 5, (T, K), generator=g, device="cuda").to(torch.bfloat16)
+    ids = torch.randint(-1, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    p = dict(x=x, weight=w, scales=s, zeros=z, topk_ids=ids)
+    each = torch.einsum("tk,enk->ten", x.double(), values)
+    ref = each.gather(1, ids.clamp_min(0).long()[:, :, None].expand(T, k, 18))
+    ref = ref.masked_fill(ids[:, :, None] < 0, 0.0).view(T * k, 18)
+    assert ref.abs().max() < 2 ** 17
+    assert torch.equal(run(p), ref.to(torch.bfloat16))
+    # gate and up are exact, so the activation and one rounding are all
+    want, tol = bound("silu", ref * 2.0 ** -10, torch.zeros_like(ref), torch.bfloat16)
+    assert_within(run(dict(p, x=x * 2.0 ** -10), "silu"), want, tol, "gated")
