@@ -351,3 +351,50 @@ def test_long_rows_of_many_routes(T, K, E, k, fmt, G, zeros):
     # gate and up are exact, so the activation and one rounding are all
     want, tol = bound("silu", ref * 2.0 ** -10, torch.zeros_like(ref), torch.bfloat16)
     assert_within(run(dict(p, x=x * 2.0 ** -10), "silu"), want, tol, "gated")
+
+
+@pytest.mark.parametrize("fmt,G,zeros", FORMATS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_small_values_beside_a_large_one_keep_their_bits(dtype, fmt, G, zeros):
+    """One value with all its significant bits, down to 2^-31 (fp16 2^-28) of the row's largest, whose
+    weight is zero, in each of 32 columns behind it: the product alone is left, rounded once."""
+    g = torch.Generator(device="cuda").manual_seed(G)
+    w, s, z, _ = matrices((48,), 512, fmt, G, DTYPES[dtype], zeros, g)
+    zero = (z[:, :1] & 15) if zeros else 8 if fmt == "int4" else 0
+    w[:, :1] = (w[:, :1] & 0xF0) | zero  # column 0
+    q = torch.stack([w & 15, w >> 4], -1).view(48, 512)[:, :33]
+    if fmt == "e2m1":
+        values = E2M1.cuda()[q.long()] * torch.exp2(s[:, 0:2].double() - 127).repeat_interleave(32, 1)[:, :33]
+    else:
+        z0 = (z & 15).double().repeat_interleave(G, 1)[:, :33] if zeros else 8.0
+        values = (q.double() - z0) * s.double().repeat_interleave(G, 1)[:, :33]
+    assert bool((values[:, 0] == 0).all())
+    large, bits, below = (1.0, 8, 31) if dtype == "bf16" else (2.0 ** 15, 11, 28)
+    smallest = torch.exp2(torch.arange(below - 10, below + 1, device="cuda", dtype=torch.float64).neg()) * large
+    x = torch.zeros(11, 32, 512, dtype=torch.float64, device="cuda")
+    x[:, :, 0] = large
+    col = torch.arange(32, device="cuda")
+    x[:, col, col + 1] = smallest[:, None] * (2 - 2.0 ** (1 - bits))
+    x = x.view(11 * 32, 512)
+    p = dict(x=x.to(DTYPES[dtype]), weight=w, scales=s, zeros=z, topk_ids=None)
+    assert torch.equal(p["x"].double(), x)
+    out = run(p)
+    want = x[:, :33] @ values.t()  # one product and zeros
+    assert torch.equal(out, want.float().to(out.dtype))
+
+
+@pytest.mark.parametrize("fmt,G,zeros", FORMATS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_a_large_value_of_zero_weight(dtype, fmt, G, zeros):
+    """Rows of which a value with zero weight is far the largest: the others are as exact as ever
+    to 2^-31 (fp16 2^-28) of it, and below off by at most 2^-39 of it each."""
+    p, values = problem(3, 512, 40, dtype, fmt, G, zeros)
+    codes = torch.stack([p["weight"] & 15, p["weight"] >> 4], -1).view(40, 512)
+    codes[:, 100] = (p["zeros"][:, 100 // G] & 15) if zeros else 8 if fmt == "int4" else 0
+    p["weight"] = codes[:, 0::2] | codes[:, 1::2] << 4
+    values[:, 100] = 0
+    large = [2.0 ** 8, 2.0 ** 14, 2.0 ** 15] if dtype == "fp16" else [2.0 ** 12, 2.0 ** 60, 3e38]
+    p["x"][:, 100] = torch.tensor(large, device="cuda").to(p["x"].dtype)
+    ref, tol = expect(p, values)
+    most = p["x"][:, 100:101].double()
+    assert_within(run(p), ref, rounded(ref, p["x"].dtype, tol + 2.0 ** -39 * most * values.abs().sum(1)), "out")
