@@ -67,6 +67,8 @@ class MoeBlock:
     expert's gate, up and activation are one call, with one rounding where three calls have four.
     With an FP8 shared expert the norm gives its input in 8 bits too; the block then has no
     post_norm (None) and no residual scale.
+    status (int32 [1]): the MOE_DEV_* bits of all of the block's calls, its experts' among them; one
+    word with experts.status.
     T is the most tokens of a call.  The logits are the router's projection in bf16, as the
     projection rounds its output, and the experts are taken by them; moe_route takes fp32 logits
     too, from a caller who computes them."""
@@ -93,7 +95,7 @@ class MoeBlock:
         self.logits, self.gate_up = empty(T, E), empty(T, 2 * Ns)
         self.ids = empty(T, top_k, dtype=torch.int32)
         self.topk_weights = empty(T, top_k, dtype=torch.float32)
-        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.status = self.experts.status
         ad = w["adapters"]
         if self.shared8 and (ad is not None or w["post_norm"] is not None):
             raise ValueError("an FP8 shared expert goes without adapters and without post_norm")

@@ -196,3 +196,21 @@ def test_the_gradient_passes_straight_through_the_8_bit_norm(ex):  # noqa: F811
     xd, wd = (x.double() + z.double()).requires_grad_(True), w.double().requires_grad_(True)
     (xd * torch.rsqrt(xd.square().mean(1, keepdim=True) + 1e-6) * wd * d.double()).sum().backward()
     assert rel(d_x, xd.grad) < 3e-3 and rel(d_z, xd.grad) < 3e-3 and rel(d_w, wd.grad) < 3e-3
+
+
+def test_the_blocks_status_has_its_experts_too(ex):  # noqa: F811
+    """A router that knows more experts than there are, and experts with too little room: the block's
+    word tells of both."""
+    from moe_expert_layer_prepare_gb300.block import FourBitExperts
+    x = torch.randn(20, 512, device="cuda").to(torch.bfloat16)
+    b = ex.make_light_block(20, 512, 256, 16, 4, 384, seed=3)
+    few = FourBitExperts(20, 4, {n: v[:3] for n, v in b.experts.weights.items()})
+    short = MoeBlock(20, 512, 256, 16, 4, 20, b.weights, experts=few)
+    short.forward(x)
+    assert int(short.status.item()) == B.MOE_DEV_BAD_EXPERT
+    b.forward(x)
+    assert int(b.status.item()) == 0
+    w = dict(ex.make_block(20, 512, 256, 16, 4, 384, 2, 16, seed=5).weights, adapters=None)
+    full = MoeBlock(20, 512, 256, 16, 4, 1, w)
+    full.forward(x)
+    assert int(full.status.item()) == B.MOE_DEV_CAPACITY
