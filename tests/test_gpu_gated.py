@@ -358,3 +358,34 @@ def test_two_pairs_a_tile_and_the_tiles_alone(T, K, N, layout):
 def test_shares_of_k_around_the_clusters_that_run_at_once(T, N):
     x, w, _ = problem(T, 2056, N, "bf16")
     check_forward(x, w, "silu")
+
+
+@pytest.mark.parametrize("keep", [False, True])
+def test_a_tile_of_two_pairs_that_gave_up_is_not_stored(keep):
+    """As test_wait_timeout_sets_status_and_context_survives, where two pairs share a tile: the first
+    pair withholds a stage, so no CTA of its cluster stores; the other tile is whole."""
+    from moe_expert_layer_prepare_gb300 import build
+    test_lib = B.configure(ctypes.CDLL(build.build_test_variant("timeout")))
+    T, K, N = 256, 4096, 256
+    x, w, _ = problem(T, K, N, "bf16")
+    out, gate_up = check_forward(x, w, "silu")
+    got, gu = torch.full_like(out, 7.0), torch.full_like(gate_up, 7.0)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    regular = B._lib
+    t0 = time.perf_counter()
+    try:
+        B._lib = test_lib
+        B.moe_gated_linear(x, w, got, gate_up=gu if keep else None, device_status=status)
+        torch.cuda.synchronize()
+    finally:
+        B._lib = regular
+    assert time.perf_counter() - t0 < 5.0
+    assert int(status.item()) == B.MOE_DEV_TIMEOUT
+    assert bool((got[:, :128] == 7).all()) and torch.equal(got[:, 128:], out[:, 128:])
+    if keep:
+        for at in (0, N):
+            assert bool((gu[:, at:at + 128] == 7).all())
+            assert torch.equal(gu[:, at + 128:at + N], gate_up[:, at + 128:at + N])
+    again, _ = check_forward(x, w, "silu")
+    assert torch.equal(again, out)
