@@ -870,6 +870,7 @@ size_t moe_gated_linear_workspace_size(int64_t num_tokens, int64_t in_features,
 /* A group's sum is in fp32, of exact products; the scale multiplies it there;*/
 /* out is rounded once.  x enters as it is down to 2^-31 (fp16: 2^-28) of its */
 /* row's largest finite value, and off by at most 2^-39 of that below.        */
+/* (Scales below 2^-96 need not keep all that: the sums are subnormal.)       */
 /* A matrix passes once for as many of its rows of x as a CTA has room for:   */
 /* 16 at most to K = 4096, 9 at 7168, 8 at 8192, 5 at 14336, 4 at 16384, 2     */
 /* above 24064; with routes in the hundreds one or two fewer.                 */

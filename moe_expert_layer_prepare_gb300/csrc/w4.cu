@@ -607,10 +607,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1) w4_kernel(Params p) {
           const uint4 v = row[i];
           row[i] = C::order(unpack2<T>(v.x), unpack2<T>(v.y), unpack2<T>(v.z), unpack2<T>(v.w), up);
         }
-        if (lane0 == 0) {  // what makes up for it: with the scales up to 2^100, the rest at the end
-          const int back = e - 14 + C::UNIT, with = min(back, 100);
-          s_power[col] = __uint_as_float((uint32_t)(127 + with) << 23);
-          s_rest[col] = __uint_as_float((uint32_t)(127 + back - with) << 23);
+        if (lane0 == 0) {
+          // What makes up for it: with the scales, which stay finite, where it is below one, else at the
+          // end and in two steps.  So only an output that is not finite overflows.
+          const int back = e - 14 + C::UNIT, late = (max(back, 0) + 1) / 2;
+          s_power[col] = __uint_as_float((uint32_t)(127 + back - 2 * late) << 23);
+          s_rest[col] = __uint_as_float((uint32_t)(127 + late) << 23);
         }
       }
       __syncthreads();
@@ -645,7 +647,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) w4_kernel(Params p) {
           const int col = t * 8 + 2 * c + e;
           if (col >= count) continue;
           int row = first + col;
-          const float rest = s_rest[row - batch_first], low = v[e] * rest, high = v[2 + e] * rest;
+          const float rest = s_rest[row - batch_first];
+          const float low = v[e] * rest * rest, high = v[2 + e] * rest * rest;
           if constexpr (EXPERTS) row = s_route[row];
           T* out = static_cast<T*>(p.out) + row * p.out_stride + n0 + g;
           if (gated) {

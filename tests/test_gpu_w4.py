@@ -398,3 +398,28 @@ def test_a_large_value_of_zero_weight(dtype, fmt, G, zeros):
     ref, tol = expect(p, values)
     most = p["x"][:, 100:101].double()
     assert_within(run(p), ref, rounded(ref, p["x"].dtype, tol + 2.0 ** -39 * most * values.abs().sum(1)), "out")
+
+
+@pytest.mark.parametrize("fmt", ["int4", "e2m1"])
+def test_scales_and_rows_of_any_size_together(fmt):
+    """bf16 rows and scales whose product is finite, however large either is; a group of zeros under
+    the largest scale is zero.  One product a column: exact."""
+    codes = torch.arange(16, device="cuda", dtype=torch.uint8)
+    w = (codes[:, None] * 17).expand(16, 32).contiguous()  # two groups
+    w[:, 16:] = 0x88 if fmt == "int4" else 0
+    value = codes.double() - 8 if fmt == "int4" else E2M1.cuda()
+    out = torch.empty(1, 16, dtype=torch.bfloat16, device="cuda")
+    for ex in (-126, -100, -60, -20, 0, 20, 60, 100, 120):
+        x = torch.zeros(1, 64, dtype=torch.bfloat16, device="cuda")
+        x[0, 5], x[0, 40] = 2.0 ** ex, 2.0 ** ex
+        for es in (-120, -100, -40, 0, 40, 100, 122, 124):
+            if not -120 <= ex + es <= 124:
+                continue
+            if fmt == "int4":
+                s = torch.full((16, 2), 2.0 ** es, device="cuda").to(torch.bfloat16)
+                s[:, 1] = 2.0 ** 127
+            else:
+                s = torch.full((16, 2), es + 127, dtype=torch.uint8, device="cuda")
+                s[:, 1] = 254
+            B.moe_w4_linear(x, w, s, out)
+            assert torch.equal(out[0], (value * 2.0 ** (ex + es)).float().to(torch.bfloat16)), (ex, es)
