@@ -930,7 +930,8 @@ def moe_w4_linear(x, weight, scales, out, zeros=None, topk_ids=None, activation=
     for e2m1 codes (2^(s - 127), G = 32); G is 32, 64 or 128.
     topk_ids: int32 or int64 [T, k]; out: [T, N], with topk_ids [T * k, N], a row a route (zeros
     where the id is none of an expert).  With an activation the first half of a matrix's rows is a
-    gate, the second up, and out has N / 2 columns, act(gate) * up.  See include/moe_prep.h."""
+    gate, the second up, and out has N / 2 columns, act(gate) * up.  Up to 1024 rows of out, read
+    again by the weights' passes for every 16 of a matrix or fewer, by K.  See include/moe_prep.h."""
     T, K = shape = x.shape
     dt, ws, sdt = x.dtype, weight.shape, scales.dtype
     E, k, idt = 0, 0, _INT32

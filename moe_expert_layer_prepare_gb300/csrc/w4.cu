@@ -3,9 +3,9 @@
 // of one matrix, or of the matrix of each row's expert; with an activation the first half
 // of the rows n is a gate and y = act(gate) up.
 //
-// The codes are the bytes that count, each read once for up to 8 NT rows, so HBM is the
-// bound as long as a code costs few instructions: an SM does 64 integer operations a
-// clock and HBM gives it 46 codes.  Codes become fp16 numbers without rounding: an integer
+// The codes are the bytes that count, each read once for as many rows as there is room for, 8 NT
+// at most (16 at K = 4096, 9 at 7168, 5 at 14336), so HBM is the bound as long as a code costs
+// few instructions: an SM does 64 integer operations a clock and HBM gives it 46 codes.  Codes become fp16 numbers without rounding: an integer
 // by a mask alone, its bits being those of a subnormal number, q 2^-24 or q 2^-20, and the
 // zero point taken off it; e2m1 by the conversion instruction.  So x is brought to fp16 too,
 // each row times a power of two that puts its largest value in [2^14, 2^15): a bf16 value
@@ -23,10 +23,10 @@
 // The k of a tile may come in any order that both operands share: lane c of four takes the
 // codes 8 c .. 8 c + 7 of 32, one word, and the same of x.
 //
-// Measured: one token 7168 -> 4096, integers of groups of 128, 6.9 us (15 MB: launch, x and
+// Measured: one token 7168 -> 4096, integers of groups of 128, 7.0 us (15 MB: launch, x and
 // the join are 5 of them); through the gate and up rows, 7168 -> 2 x 2048, of eight e2m1
-// experts 26 us (123 MB, 4.8 TB/s, bound by issue slots); 128 routes 2048 -> 7168 132 us (818
-// MB, 6.2 TB/s); 16 tokens 4096 -> 2 x 14336 with zero points 27 us (64 MB: the second eight
+// experts 27 us (123 MB, 4.6 TB/s, bound by issue slots); 128 routes 2048 -> 7168 135 us (818
+// MB, 6.1 TB/s); 16 tokens 4096 -> 2 x 14336 with zero points 28 us (64 MB: the second eight
 // columns take 6 of them, the zero points 5).
 #include <mutex>
 #include <type_traits>
