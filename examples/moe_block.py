@@ -4,8 +4,8 @@
 
 Serving: a batch of requests, each with its own adapter, goes through two blocks (norm, router,
 FP8 experts beside a shared expert with low-rank adapters, ``moe_expert_layer_prepare_gb300.block``).
-The same with little more than half the bytes of weights: experts with 4-bit weights and an FP8 shared expert, whose
-input the norm gives in 8 bits.
+The same with little more than half the bytes of weights: experts with 4-bit weights and an FP8
+shared expert, whose input the norm gives in 8 bits.
 Training: a router and the scales of simple experts learn a teacher's output; every gradient but
 the experts' own comes from the library (norm, unpermute, permute, router).  A gated feed-forward
 block learns another's, with the gradients of the norm and of the gated projection.

@@ -3,16 +3,17 @@
 // of one matrix, or of the matrix of each row's expert; with an activation the first half
 // of the rows n is a gate and y = act(gate) up.
 //
-// The codes are the bytes that count, each read once for as many rows as there is room for, 8 NT
-// at most (16 at K = 4096, 9 at 7168, 5 at 14336), so HBM is the bound as long as a code costs
-// few instructions: an SM does 64 integer operations a clock and HBM gives it 46 codes.  Codes become fp16 numbers without rounding: an integer
-// by a mask alone, its bits being those of a subnormal number, q 2^-24 or q 2^-20, and the
-// zero point taken off it; e2m1 by the conversion instruction.  So x is brought to fp16 too,
-// each row times a power of two that puts its largest value in [2^14, 2^15): a bf16 value
-// keeps all its bits down to 2^-31 of that, an fp16 value to 2^-28, and what is smaller is off
-// by half a step of 2^-24 at most, 2^-39 of the largest, far below the error of the fp32 sums.
-// The products of a group are summed by mma.sync tiles in fp32; its scale times the row's power
-// multiplies the group's sum.
+// The codes are the bytes that count, each read once for as many rows as there is room for,
+// 8 NT at most (16 at K = 4096, 9 at 7168, 5 at 14336), so HBM is the bound as long as a
+// code costs few instructions: an SM does 64 integer operations a clock and HBM gives it 46
+// codes. Codes become fp16 numbers without rounding: an integer by a mask alone, its bits
+// being those of a subnormal number, q 2^-24 or q 2^-20, and the zero point taken off it;
+// e2m1 by the conversion instruction. So x is brought to fp16 too, each row times a power of
+// two that puts its largest value in [2^14, 2^15): a bf16 value keeps all its bits down to
+// 2^-31 of that, an fp16 value to 2^-28, and what is smaller is off by half a step of 2^-24
+// at most, 2^-39 of the largest, far below the error of the fp32 sums. The products of a
+// group are summed by mma.sync tiles in fp32; its scale times the row's power multiplies the
+// group's sum.
 //
 // A unit is 16 rows of a matrix (gated: 8 gate rows and their 8 up rows, so that one lane
 // has both values of an output) by all of K for up to 8 NT rows of x, which a CTA keeps
